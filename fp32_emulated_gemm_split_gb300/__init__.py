@@ -374,3 +374,19 @@ def emu_shutdown() -> None:
 
 def emu_version() -> int:
     return int(lib().emu_version())
+
+
+# --------------------- the operators of a transformer block (emu_layers.h) --
+
+_LAYERS = ("emu_gated_pack", "emu_gated", "emu_gated_bwd", "emu_lora_pack", "emu_lora", "emu_qk_norm_rope",
+           "emu_qk_norm_rope_bwd", "GatedWeights", "LoraWeights")
+
+
+def __getattr__(name):
+    # on first use: that module needs torch, which this one imports as late as it can
+    if name in _LAYERS:
+        from . import layers
+        for n in _LAYERS:
+            globals()[n] = getattr(layers, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

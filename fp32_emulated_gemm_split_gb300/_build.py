@@ -20,8 +20,9 @@ BUILD_DIR = os.path.join(CSRC, "_build")
 LIB_NAME = f"libemusgemm.{platform.machine()}.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
-SOURCES = ["emu_sgemm.cu", "split.cu", "gemm_kblock.cu", "gemm_simt.cu", "noalloc.cu", "chooser.cu"]
-HEADERS = ["emu_device.cuh", "emu_internal.h", "schedule.h"]
+SOURCES = ["emu_sgemm.cu", "split.cu", "gemm_kblock.cu", "gemm_simt.cu", "noalloc.cu", "chooser.cu",
+           "gated.cu", "lora.cu", "qk_norm.cu"]
+HEADERS = ["emu_device.cuh", "emu_host.h", "emu_internal.h", "gated.cuh", "schedule.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
@@ -44,7 +45,7 @@ def _stale(target: str, deps) -> bool:
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
-    headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "emu_sgemm.h")]
+    headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, h) for h in ("emu_sgemm.h", "emu_layers.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -14,6 +14,7 @@ namespace emu {
 // public emu_status_t).
 enum : int {
     kDevErrTimeout = -5,
+    kDevErrValue = -1,       // an index or position on the device is out of range
 };
 
 // Tensor-core GEMM variants (the values of the public emu_mode_t):
@@ -68,7 +69,23 @@ struct TcGemmParams {
     // reads them through the transpose bits of its instruction descriptor,
     // so no transposed split is needed.
     int a_mn, b_mn;
+    // Gated feed-forward (kEpiGated): B's pieces hold the gate's rows from
+    // row 0 and the up projection's from row up_row, N is one projection's
+    // width, C = act(gate) * up.  G, U (or null): where the two products go
+    // as well (row stride ldg; tma_gu: their tensor maps are valid).
+    int up_row, act, tma_gu;
+    float *G, *U;
+    int64_t ldg;
 };
+
+// Epilogues of the tensor-core GEMM kernel.
+enum : int {
+    kEpiPlain = 0,       // C = alpha * acc + beta * C
+    kEpiGated = 1,       // C = act(gate) * up (TcGemmParams)
+};
+
+// Activations of the gated feed-forward (the values of the public emu_act_t).
+enum : int { kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid = 4 };
 
 // Launchers (return the launch status; nothing is synchronised).
 cudaError_t launch_split_bf16x3(const float* X, int64_t rows, int64_t cols, int64_t ld, int trans,
@@ -102,6 +119,13 @@ cudaError_t launch_gemm_kblock(int mode, int bn, int fused, const CUtensorMap& m
 // Clusters of the GEMM variant that can be resident at once on a GPU with
 // `sms` SMs (at most sms / 2); the persistent grid uses this many.
 int gemm_kblock_clusters(int mode, int bn, int fused, int sms);
+// The same kernel with the gated epilogue (BF16x9, two-pass, 256-wide tiles:
+// 128 columns of each projection); mapH, mapG, mapU: the outputs' maps.
+cudaError_t launch_gemm_gated(const CUtensorMap& mapA, const CUtensorMap& mapB,
+                              const CUtensorMap& mapH, const CUtensorMap& mapG,
+                              const CUtensorMap& mapU, const TcGemmParams& p, int sms,
+                              cudaStream_t stream);
+int gemm_gated_clusters(int sms);
 cudaError_t launch_gemm_simt(int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
                              const float* A, int64_t lda, const float* B, int64_t ldb, float beta,
                              float* C, int64_t ldc, cudaStream_t stream);

@@ -9,7 +9,7 @@
 #include <vector>
 
 #include "emu_device.cuh"
-#include "emu_sgemm.h"
+#include "emu_host.h"
 
 namespace emu {
 
@@ -20,33 +20,10 @@ static_assert(kModeBf16x9 == int(EMU_MODE_BF16X9) && kModeTf32x3 == int(EMU_MODE
                   kModeTf32 == int(EMU_MODE_TF32) && kModeTf32x3Oy == int(EMU_MODE_TF32X3_OY),
               "kernel variants follow emu_mode_t");
 
+std::mutex g_mu;
+
 namespace {
 
-constexpr int kMaxDevices = 64;
-constexpr int kHostChunksMax = 8;        // row chunks of emu_sgemm_host's copy/compute pipeline
-
-struct DeviceState {
-    int checked = 0;           // 0 unknown, 1 supported, -1 unsupported
-    int sms = 0;
-    int* err = nullptr;        // device address of g_emu_error
-    void* ws = nullptr;        // workspace for the split pieces
-    size_t ws_bytes = 0;
-    void* stage = nullptr;     // device staging for emu_sgemm_host
-    size_t stage_bytes = 0;
-    // emu_sgemm_host's pipeline: host->device and device->host copy streams
-    // and per-chunk events (created on first use, kept until exit)
-    cudaStream_t s_in = nullptr, s_out = nullptr;
-    cudaEvent_t ev_in[kHostChunksMax] = {}, ev_done[kHostChunksMax] = {};
-    cudaEvent_t ev_panel = nullptr;      // each column panel of op(B) landed
-    // the GEMM's stream-K tail: one slot of partial sums per cluster (grown on
-    // demand), flags (zeroed once) and the epoch that marks this call's flags
-    void* part = nullptr;
-    size_t part_bytes = 0;
-    unsigned* flags = nullptr;
-    unsigned epoch = 0;
-};
-
-std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 int g_path = -1;               // -1: not yet read from the environment
 int g_strategy = -1;           // same
@@ -93,6 +70,8 @@ struct ProfScope {
 
 cudaError_t g_last_cuda_error = cudaSuccess;
 
+}  // namespace
+
 emu_status_t from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return EMU_OK;
     g_last_cuda_error = e;
@@ -103,6 +82,8 @@ emu_status_t from_cuda(cudaError_t e) {
         return EMU_ERR_LAUNCH;
     return EMU_ERR_CUDA;
 }
+
+namespace {
 
 // Tile width of the K-block kernel on the two-pass path: 128 when N <= 128
 // (a 256-wide tile would compute at least half zeros), else 256.
@@ -123,8 +104,9 @@ int read_path_env() {
     return EMU_PATH_AUTO;
 }
 
-// Current device state, checking the architecture once.
-emu_status_t current_device(DeviceState** out, int* dev_out = nullptr) {
+}  // namespace
+
+emu_status_t current_device(DeviceState** out, int* dev_out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return EMU_ERR_CUDA;
     DeviceState& d = g_dev[dev];
@@ -164,6 +146,8 @@ emu_status_t ensure_buffer(void** buf, size_t* have, size_t need) {
     return EMU_OK;
 }
 
+namespace {
+
 // cuTensorMapEncodeTiled, fetched from the driver through the runtime so the
 // library needs no link-time dependency on libcuda.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -186,13 +170,11 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Tensor map over `planes` row-major planes of rows x cols elements (row
-// stride ld elements, plane stride plane_rows*ld, plane_rows 0 meaning
-// rows), box of box_cols x box_rows, 128-byte swizzle, zero fill outside the
-// matrix.
+}  // namespace
+
 emu_status_t make_plane_map(CUtensorMap* map, const void* base, bool fp32, int64_t rows,
                             int64_t cols, int64_t ld, int planes, int box_cols, int box_rows,
-                            int64_t plane_rows = 0) {
+                            int64_t plane_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return EMU_ERR_CUDA;
     const int esize = fp32 ? 4 : 2;
@@ -207,6 +189,8 @@ emu_status_t make_plane_map(CUtensorMap* map, const void* base, bool fp32, int64
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? EMU_OK : EMU_ERR_CUDA;
 }
+
+namespace {
 
 // 4-D map over M- or N-major pieces: `planes` planes of K rows x ld
 // elements (ld a multiple of 64; planes plane_rows rows apart, 0: K), each
@@ -235,14 +219,8 @@ emu_status_t make_plane_map_mn(CUtensorMap* map, const void* base, int64_t cols,
     return r == CUDA_SUCCESS ? EMU_OK : EMU_ERR_CUDA;
 }
 
-// 2-D map over C for the bulk tensor stores of the GEMM epilogue (any beta;
-// with beta != 0 the epilogue reads C itself first): box of 16 columns x 32
-// rows, 64-byte swizzle.  The map covers the first N & ~3 columns only: a
-// bulk store clips a box at the edge of the map in whole 16-byte units
-// (measured on GB300: with N = 4k + 1..3 it wrote zeros up to column 4k + 3,
-// past C), so the epilogue stores the last N % 4 columns of each row itself.
-// Returns false (and the kernel stores C directly) when C's rows are not
-// 16-byte aligned or C is narrower than 4 columns.
+}  // namespace
+
 bool make_c_map(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
     if ((ldc % 4) != 0 || (reinterpret_cast<uintptr_t>(C) & 15) != 0 || N < 4) return false;
     EncodeTiledFn enc = encode_fn();
@@ -256,23 +234,17 @@ bool make_c_map(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Plan the tail of the persistent GEMM (schedule.h) for the clusters of
-// this GEMM variant that can be resident at once, and give it its
-// workspace: one slot of bm x bn FP32 sums and 2 x 16 flags per cluster
-// sharing the tail.  Sets p.tail_*, p.part_ws, p.flags and p.epoch.
 constexpr int kFlagsBytes = 64 << 10;
 
-emu_status_t plan_tail(TcGemmParams& p, int mode, int bm, int bn, int fused, DeviceState* d) {
+emu_status_t plan_tail(TcGemmParams& p, int clusters, int fix2, int bm, int bn, DeviceState* d) {
     const int tiles = p.tiles_m * p.tiles_n;
-    const int clusters = gemm_kblock_clusters(mode, bn, fused, d->sms);
     p.tail_tiles = 0;
     p.tail_clusters = 0;
     p.part_ws = nullptr;
     p.flags = nullptr;
     p.epoch = 0;
     int tail_tiles = 0, tail_clusters = 0;
-    sched_plan_tail(tiles, p.num_kb, clusters, handover_half_blocks(mode), &tail_tiles,
-                    &tail_clusters);
+    sched_plan_tail(tiles, p.num_kb, clusters, fix2, &tail_tiles, &tail_clusters);
     if (tail_tiles == 0) return EMU_OK;
     if ((size_t)tail_clusters * 2 * 16 * sizeof(unsigned) > (size_t)kFlagsBytes) return EMU_OK;
     const size_t need = (size_t)tail_clusters * bm * bn * sizeof(float);
@@ -293,6 +265,8 @@ emu_status_t plan_tail(TcGemmParams& p, int mode, int bm, int bn, int fused, Dev
     p.epoch = ++d->epoch == 0 ? ++d->epoch : d->epoch;   // never 0 (the flags' initial value)
     return EMU_OK;
 }
+
+namespace {
 
 // a * b + c, or false when it does not fit in 62 bits (no allocation that
 // large can succeed; the check keeps every later size product from wrapping).
@@ -344,19 +318,6 @@ struct BPieces {
     int64_t ld = 0;
 };
 
-// Where one operand's pieces are: planes starting at p, ld elements per
-// row, plane_rows rows apart (0: the planes' own row count).  mn = 0:
-// K-major, a row per row of op(A) (or of op(B)^T), K elements long.  mn = 1
-// (two-pass BF16 modes): M- or N-major, a row per K index, M (or N) elements
-// long, ld a multiple of 64 (mn_ld) -- what a row-wise split writes from A
-// stored K x M or B stored K x N.
-struct PieceSet {
-    const void* p;
-    int64_t ld;
-    int64_t plane_rows;
-    int mn;
-};
-
 // Whether a two-pass call keeps an operand's pieces M- or N-major: an
 // operand stored with K as its row index (A with transA, B without transB),
 // whose split is then a row-wise one instead of a transposed one (about
@@ -379,19 +340,8 @@ inline bool mn_pieces(int mode, bool k_is_row, int64_t K, int64_t extent) {
     return mode == kModeBf16x9 || (mode == kModeBf16x3 && K >= 4 * extent);
 }
 
-// Row length of M- or N-major pieces: whole 64-element chunks (the tensor
-// copies read them a chunk at a time).
-inline int64_t mn_ld(int64_t cols) { return (cols + 63) / 64 * 64; }
+}  // namespace
 
-// Bytes of one operand's pieces: `rows` rows of op(A) (or of op(B)^T) over K.
-inline size_t piece_bytes(int mode, bool mn, int64_t rows, int64_t K) {
-    const size_t per = (size_t)mode_pieces(mode) * mode_piece_bytes(mode);
-    return mn ? per * (size_t)K * mn_ld(rows) : per * (size_t)rows * plane_ld(K);
-}
-
-// The tensor-core GEMM on pieces already in device memory (op(A)'s and
-// op(B)^T's, as PieceSet says).  Launched as a programmatic dependent of the
-// split ahead of it in the stream.
 emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int64_t M, int64_t N,
                             int64_t K, float alpha, float beta, float* C, int64_t ldc,
                             DeviceState* d, cudaStream_t stream) {
@@ -425,11 +375,13 @@ emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int6
     p.a_mn = a.mn; p.b_mn = b.mn;
     CUtensorMap mapC = mapB;                 // placeholder when C is stored directly
     p.tma_store = make_c_map(&mapC, C, M, N, ldc) ? 1 : 0;
-    st = plan_tail(p, mode, 256, bn, 0, d);
+    st = plan_tail(p, gemm_kblock_clusters(mode, bn, 0, d->sms), handover_half_blocks(mode), 256, bn, d);
     if (st != EMU_OK) return st;
     ProfScope ps(1, stream);
     return from_cuda(launch_gemm_kblock(mode, bn, 0, mapA, mapB, mapC, p, d->sms, stream, true));
 }
+
+namespace {
 
 emu_status_t run_two_pass(int mode, int transA, int transB, int64_t M, int64_t N, int64_t K,
                           float alpha, const float* A, int64_t lda, const float* B, int64_t ldb,
@@ -520,7 +472,7 @@ emu_status_t run_fused_tmem(int transB, int64_t M, int64_t N, int64_t K, float a
     p.alpha = alpha; p.beta = beta; p.C = C; p.ldc = ldc;
     CUtensorMap mapC = mapB;
     p.tma_store = make_c_map(&mapC, C, M, N, ldc) ? 1 : 0;
-    st = plan_tail(p, kModeBf16x9, 256, bn, 1, d);
+    st = plan_tail(p, gemm_kblock_clusters(kModeBf16x9, bn, 1, d->sms), handover_half_blocks(kModeBf16x9), 256, bn, d);
     if (st != EMU_OK) return st;
     {
         ProfScope ps(2, stream);
@@ -577,7 +529,7 @@ emu_status_t run_fused_smem(int mode, int transB, int64_t M, int64_t N, int64_t 
     p.A32 = A; p.lda = lda;
     CUtensorMap mapC = mapB;
     p.tma_store = make_c_map(&mapC, C, M, N, ldc) ? 1 : 0;
-    st = plan_tail(p, mode, 256, bn, 3, d);
+    st = plan_tail(p, gemm_kblock_clusters(mode, bn, 3, d->sms), handover_half_blocks(mode), 256, bn, d);
     if (st != EMU_OK) return st;
     {
         ProfScope ps(2, stream);

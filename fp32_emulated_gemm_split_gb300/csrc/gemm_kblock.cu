@@ -79,6 +79,7 @@
 #include <mutex>
 
 #include "emu_device.cuh"
+#include "gated.cuh"
 #include "schedule.h"
 
 namespace emu {
@@ -281,11 +282,20 @@ __device__ __forceinline__ bool bar_and(int id, int nthreads, bool v) {
 }
 constexpr int kSplitBarrier = 1;                      // named barrier of the split warps
 
-template <int MODE, int BN, int FUSED>
+// Further tensor maps of an epilogue: none, or the gated one's G and U.
+template <int EPI>
+struct EpiMaps {};
+template <>
+struct EpiMaps<kEpiGated> {
+    CUtensorMap g, u;
+};
+
+template <int MODE, int BN, int FUSED, int EPI>
 __global__ void __launch_bounds__(threads_k<FUSED>(), 1)
 gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
                    const __grid_constant__ CUtensorMap mapB,
-                   const __grid_constant__ CUtensorMap mapC, const TcGemmParams p) {
+                   const __grid_constant__ CUtensorMap mapC,
+                   const __grid_constant__ EpiMaps<EPI> maps, const TcGemmParams p) {
     using Cfg = KCfg<MODE, BN, FUSED>;
     using R = Roles<FUSED>;
     constexpr int S = Cfg::stages, P = Cfg::pieces, kAccCols = Cfg::acc_cols;
@@ -402,7 +412,9 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
                 int tm, tn;
                 tile_pos(w.tile, p.tiles_m, p.tiles_n, tm, tn);
                 const int arow = tm * kBM + int(rank) * kHalfRows;
-                const int brow = tn * BN + int(rank) * Cfg::b_rows;
+                // gated: this CTA's half of the tile is one projection's rows
+                const int brow = EPI == kEpiGated ? tn * (BN / 2) + int(rank) * p.up_row
+                                                  : tn * BN + int(rank) * Cfg::b_rows;
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++kbg) {
                     const uint32_t s = kbg % S, ph = (kbg / S) & 1;
                     if (Cfg::TM) {
@@ -786,7 +798,14 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
 #pragma unroll
                     for (int g = 0; g < kAccCols / 16; ++g) {
                         uint32_t r[16];
-                        tmem_ld_32x32b_x16(col0 + 16 * g, r);
+                        // gated: a thread's sums are kAccCols / 2 columns of the
+                        // gate (the tile's left half) and the same of the up
+                        // projection (its right half)
+                        constexpr int HC = kAccCols / 2;
+                        const uint32_t off = EPI != kEpiGated ? 16 * g
+                                             : 16 * g < HC    ? 16 * g - h * HC
+                                                              : BN / 2 + 16 * g - HC - h * HC;
+                        tmem_ld_32x32b_x16(col0 + off, r);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) acc[16 * g + j] += __uint_as_float(r[j]);
@@ -866,6 +885,12 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
             tile_pos(tile, p.tiles_m, p.tiles_n, tm, tn);
             const int row0 = tm * kBM + int(rank) * kHalfRows + q * 32;
             const int row = row0 + lane;
+            if constexpr (EPI == kEpiGated) {
+                gated_epilogue<kAccCols>(acc, p, mapC, maps.g, maps.u, row0, lane,
+                                         tn * (BN / 2) + h * (kAccCols / 2),
+                                         smem_u32(cstage + (warp - R::acc0) * 2048 * Cfg::c_bufs));
+                continue;
+            }
             const int col_base = tn * BN + h * kAccCols;
             if (p.tma_store) {
                 // Stage 32 rows x 16 columns at a time in this warp's 2 KB
@@ -991,7 +1016,7 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
             }
         }
         if (!ok) *abort_flag = 1;
-        if (p.tma_store && lane == 0) bulk_wait_all();        // C written before exit
+        if ((p.tma_store || p.tma_gu) && lane == 0) bulk_wait_all();   // C written before exit
     }
 
     __syncwarp();
@@ -1016,7 +1041,7 @@ struct VariantState {
     int clusters[kMaxDevices] = {};
 };
 
-template <int MODE, int BN, int FUSED>
+template <int MODE, int BN, int FUSED, int EPI = kEpiPlain>
 VariantState& variant_state() {
     static VariantState st;
     return st;
@@ -1028,37 +1053,37 @@ int current_device_index() {
     return dev;
 }
 
-template <int MODE, int BN, int FUSED>
+template <int MODE, int BN, int FUSED, int EPI = kEpiPlain>
 cudaError_t set_smem_attr_locked(VariantState& st, int dev) {
     using Cfg = KCfg<MODE, BN, FUSED>;
     if (dev >= 0 && st.attr[dev]) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(gemm_kblock_kernel<MODE, BN, FUSED>,
+    cudaError_t e = cudaFuncSetAttribute(gemm_kblock_kernel<MODE, BN, FUSED, EPI>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::smem);
     if (e == cudaSuccess && dev >= 0) st.attr[dev] = true;
     return e;
 }
 
-template <int MODE, int BN, int FUSED>
+template <int MODE, int BN, int FUSED, int EPI = kEpiPlain>
 cudaError_t set_smem_attr() {
-    VariantState& st = variant_state<MODE, BN, FUSED>();
+    VariantState& st = variant_state<MODE, BN, FUSED, EPI>();
     std::lock_guard<std::mutex> lock(st.mu);
-    return set_smem_attr_locked<MODE, BN, FUSED>(st, current_device_index());
+    return set_smem_attr_locked<MODE, BN, FUSED, EPI>(st, current_device_index());
 }
 
 // Clusters of this kernel that can be resident at once (at most sms / 2).
 // The persistent grid never exceeds it, so every cluster runs concurrently:
 // the owner of a stream-K tail tile waits for the clusters that hold the
 // tile's later K ranges, which must not be queued behind it.
-template <int MODE, int BN, int FUSED>
+template <int MODE, int BN, int FUSED, int EPI = kEpiPlain>
 int max_clusters_t(int sms) {
     using Cfg = KCfg<MODE, BN, FUSED>;
-    VariantState& st = variant_state<MODE, BN, FUSED>();
+    VariantState& st = variant_state<MODE, BN, FUSED, EPI>();
     std::lock_guard<std::mutex> lock(st.mu);
     const int dev = current_device_index();
     int n = dev >= 0 ? st.clusters[dev] : 0;
     if (n <= 0) {
         n = sms / 2;
-        if (set_smem_attr_locked<MODE, BN, FUSED>(st, dev) == cudaSuccess) {
+        if (set_smem_attr_locked<MODE, BN, FUSED, EPI>(st, dev) == cudaSuccess) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(2 * (sms / 2));
             cfg.blockDim = dim3(threads_k<FUSED>());
@@ -1071,7 +1096,7 @@ int max_clusters_t(int sms) {
             cfg.attrs = at;
             cfg.numAttrs = 1;
             int m = 0;
-            if (cudaOccupancyMaxActiveClusters(&m, gemm_kblock_kernel<MODE, BN, FUSED>, &cfg) ==
+            if (cudaOccupancyMaxActiveClusters(&m, gemm_kblock_kernel<MODE, BN, FUSED, EPI>, &cfg) ==
                     cudaSuccess && m > 0)
                 n = m;
             else
@@ -1082,12 +1107,12 @@ int max_clusters_t(int sms) {
     return n < sms / 2 ? n : sms / 2;
 }
 
-template <int MODE, int BN, int FUSED>
+template <int MODE, int BN, int FUSED, int EPI = kEpiPlain>
 cudaError_t launch_kblock_t(const CUtensorMap& mapA, const CUtensorMap& mapB,
                             const CUtensorMap& mapC, const TcGemmParams& p, int clusters,
-                            cudaStream_t stream, bool pdl) {
+                            cudaStream_t stream, bool pdl, const EpiMaps<EPI>& maps = {}) {
     using Cfg = KCfg<MODE, BN, FUSED>;
-    cudaError_t e = set_smem_attr<MODE, BN, FUSED>();
+    cudaError_t e = set_smem_attr<MODE, BN, FUSED, EPI>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters);
@@ -1103,10 +1128,41 @@ cudaError_t launch_kblock_t(const CUtensorMap& mapA, const CUtensorMap& mapB,
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_kblock_kernel<MODE, BN, FUSED>, mapA, mapB, mapC, p);
+    return cudaLaunchKernelEx(&cfg, gemm_kblock_kernel<MODE, BN, FUSED, EPI>, mapA, mapB, mapC, maps, p);
+}
+
+// Clusters that a launch runs with `resident` of them resident at once.  A
+// stream-K tail is used only as planned for that many: whole tiles fill
+// complete rounds of all of them and every cluster sharing the tail runs at
+// once (an owner waits for the others).
+int grid_clusters(TcGemmParams& q, int resident) {
+    const int tiles = q.tiles_m * q.tiles_n;
+    const int first = tiles - q.tail_tiles;
+    const bool split_ok = q.tail_tiles > 0 && q.tail_tiles <= tiles && q.part_ws && q.flags &&
+                          q.tail_clusters >= 1 && q.tail_clusters <= resident &&
+                          q.num_kb >= 2 && first % resident == 0;
+    if (!split_ok) {                         // whole tiles only
+        q.tail_tiles = 0;
+        q.tail_clusters = 0;
+    }
+    return sched_grid_clusters(tiles, q.tail_tiles, q.tail_clusters, resident);
 }
 
 }  // namespace
+
+int gemm_gated_clusters(int sms) { return max_clusters_t<kModeBf16x9, 256, 0, kEpiGated>(sms); }
+
+cudaError_t launch_gemm_gated(const CUtensorMap& mapA, const CUtensorMap& mapB,
+                              const CUtensorMap& mapH, const CUtensorMap& mapG,
+                              const CUtensorMap& mapU, const TcGemmParams& p, int sms,
+                              cudaStream_t stream) {
+    if (p.tiles_m * p.tiles_n == 0) return cudaSuccess;
+    TcGemmParams q = p;
+    const int clusters = grid_clusters(q, gemm_gated_clusters(sms));
+    const cudaError_t e = launch_kblock_t<kModeBf16x9, 256, 0, kEpiGated>(
+        mapA, mapB, mapH, q, clusters, stream, true, EpiMaps<kEpiGated>{mapG, mapU});
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 int gemm_kblock_clusters(int mode, int bn, int fused, int sms) {
     if (fused == 3 && mode == kModeTf32x3)
@@ -1133,22 +1189,9 @@ int gemm_kblock_clusters(int mode, int bn, int fused, int sms) {
 cudaError_t launch_gemm_kblock(int mode, int bn, int fused, const CUtensorMap& mapA,
                                const CUtensorMap& mapB, const CUtensorMap& mapC,
                                const TcGemmParams& p, int sms, cudaStream_t stream, bool pdl) {
-    const int tiles = p.tiles_m * p.tiles_n;
-    if (tiles == 0) return cudaSuccess;
+    if (p.tiles_m * p.tiles_n == 0) return cudaSuccess;
     TcGemmParams q = p;
-    const int resident = gemm_kblock_clusters(mode, bn, fused, sms);
-    // A stream-K tail is used only as planned for this many resident
-    // clusters: whole tiles fill complete rounds of all of them and every
-    // cluster sharing the tail runs at once (an owner waits for the others).
-    const int first = tiles - q.tail_tiles;
-    const bool split_ok = q.tail_tiles > 0 && q.tail_tiles <= tiles && q.part_ws && q.flags &&
-                          q.tail_clusters >= 1 && q.tail_clusters <= resident &&
-                          q.num_kb >= 2 && first % resident == 0;
-    if (!split_ok) {                         // whole tiles only
-        q.tail_tiles = 0;
-        q.tail_clusters = 0;
-    }
-    const int clusters = sched_grid_clusters(tiles, q.tail_tiles, q.tail_clusters, resident);
+    const int clusters = grid_clusters(q, gemm_kblock_clusters(mode, bn, fused, sms));
     cudaError_t e;
     if (fused == 3) {
         if ((mode != kModeBf16x9 && mode != kModeTf32x3) || !q.A32) return cudaErrorInvalidValue;
