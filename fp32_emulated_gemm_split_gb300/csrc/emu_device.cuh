@@ -196,6 +196,16 @@ __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// Named barrier `id` over `nthreads` threads that also ANDs a predicate: every
+// participating warp reaches it once per use, whatever its predicate, so a
+// warp whose wait gave up still meets the others and all leave together.
+__device__ __forceinline__ bool bar_and(int id, int nthreads, bool v) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n"
+                 " bar.red.and.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(r) : "r"(uint32_t(v)), "r"(id), "r"(nthreads) : "memory");
+    return r != 0;
+}
 // ------------------------------------------------- CTA pairs (clusters of 2) --
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -292,6 +302,28 @@ __device__ __forceinline__ void mma_cta2_ta_scaled(uint32_t d, uint32_t a, uint6
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "n"(SHIFT) : "memory");
 }
 
+// One CTA's own MMAs (cta_group::1), A in tensor memory: D = A*B (+ D), and
+// D = A*B + 2^-SHIFT D.
+__device__ __forceinline__ void mma_cta1_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+template <int SHIFT>
+__device__ __forceinline__ void mma_cta1_ta_scaled(uint32_t d, uint32_t a, uint64_t b,
+                                                   uint32_t idesc) {
+    static_assert(SHIFT >= 1 && SHIFT <= 15, "scale-input-d takes 0..15");
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %4;\n}\n"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "n"(SHIFT) : "memory");
+}
+// Arrive on this CTA's barrier once its MMAs issued so far have completed.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(bar) : "memory");
+}
+
 // Store 8 consecutive 32-bit columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile(
@@ -377,6 +409,39 @@ __device__ __forceinline__ void split_bf16x3_pair(float a, float b, uint32_t& p0
     const float sa2 = __fmul_rn(__fsub_rn(sa1, __uint_as_float(p1 << 16)), 256.0f);
     const float sb2 = __fmul_rn(__fsub_rn(sb1, __uint_as_float(p1 & 0xFFFF0000u)), 256.0f);
     p2 = cvt_bf16x2(sb2, sa2);
+}
+
+// The same for two finite values, with the packed FP32 operations: each
+// residual x - h is exact, as is its scaling.
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
+    return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void split_finite_pair(float a, float b, uint32_t& p0, uint32_t& p1,
+                                                  uint32_t& p2) {
+    constexpr uint64_t kMinus1 = 0xBF800000BF800000ull, k256 = 0x4380000043800000ull;
+    p0 = cvt_bf16x2(b, a);
+    const uint64_t s1 = mul_f32x2(fma_f32x2(pack_f32x2(p0 << 16, p0 & 0xFFFF0000u), kMinus1,
+                                            pack_f32x2(__float_as_uint(a), __float_as_uint(b))), k256);
+    p1 = cvt_bf16x2(__uint_as_float(uint32_t(s1 >> 32)), __uint_as_float(uint32_t(s1)));
+    const uint64_t s2 = mul_f32x2(fma_f32x2(pack_f32x2(p1 << 16, p1 & 0xFFFF0000u), kMinus1, s1), k256);
+    p2 = cvt_bf16x2(__uint_as_float(uint32_t(s2 >> 32)), __uint_as_float(uint32_t(s2)));
+}
+
+// max(m, |x|), NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float m, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(m)), "f"(fabsf(x)));
+    return r;
 }
 
 // Nearest TF32 (10 explicit mantissa bits, ties to even) kept in an FP32

@@ -101,4 +101,17 @@ emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int6
                             int64_t K, float alpha, float beta, float* C, int64_t ldc,
                             DeviceState* d, cudaStream_t stream);
 
+// Few rows of X against FP32 weights (gemm_few.cu): whether the weights can be streamed (16-byte
+// aligned rows, at most kFewRows rows of X), and the GEMM on X's pieces at
+// `xp` (M rows of ldp).  W2 NULL: Y = alpha X W^T + beta Y, W N x K; else the
+// gated form over N columns.  p carries the outputs (C, ldc, alpha, beta, act,
+// G, U, ldg).  Launched as a programmatic dependent of the split of X, which
+// must itself have been launched as an ordinary kernel: the weights are read
+// before that split has ended.
+constexpr int64_t kFewRows = 128;
+bool few_rows_ok(int64_t M, const float* W, int64_t ldw);
+emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
+                           int64_t N, int64_t K, const void* xp, int64_t ldp, TcGemmParams p,
+                           DeviceState* d, cudaStream_t stream);
+
 }  // namespace emu

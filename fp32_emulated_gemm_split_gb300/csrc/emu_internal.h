@@ -126,6 +126,17 @@ cudaError_t launch_gemm_gated(const CUtensorMap& mapA, const CUtensorMap& mapB,
                               const CUtensorMap& mapU, const TcGemmParams& p, int sms,
                               cudaStream_t stream);
 int gemm_gated_clusters(int sms);
+// Few rows of X (gemm_few.cu): FP32 weights streamed and split on chip, X's
+// pieces as the narrow operand (bn 16, 32, 64 or 128 rows of it), the result
+// stored transposed: element (weight row m < p.M, X row n < p.N) at
+// C[n * ldc + m].  mapA: an FP32 map of the weights, box 32 x 128; gated (mapA2
+// not null): maps of the two weights, box 32 x 64; mapB: X's pieces, box 64 x
+// bn.  p.tiles_m: tiles of 128 weight rows (gated: 64 of each weight).
+cudaError_t launch_gemm_few(int bn, const CUtensorMap& mapA, const CUtensorMap* mapA2,
+                            const CUtensorMap& mapB, const TcGemmParams& p, int sms,
+                            cudaStream_t stream);
+// CTAs of that kernel resident at once.
+int gemm_few_ctas(bool gated, int bn, int sms);
 cudaError_t launch_gemm_simt(int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
                              const float* A, int64_t lda, const float* B, int64_t ldb, float beta,
                              float* C, int64_t ldc, cudaStream_t stream);

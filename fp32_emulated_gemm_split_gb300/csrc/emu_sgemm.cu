@@ -381,6 +381,37 @@ emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int6
     return from_cuda(launch_gemm_kblock(mode, bn, 0, mapA, mapB, mapC, p, d->sms, stream, true));
 }
 
+bool few_rows_ok(int64_t M, const float* W, int64_t ldw) {
+    return M <= kFewRows && W && ldw % 4 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
+}
+
+// What handing one part's sums over costs in half K blocks: about 2 us
+// against the 0.7 us in which a CTA streams a K block of FP32 weights (32 KB)
+// at its share of the HBM's rate.
+constexpr int kFewRowsHandover = 6;
+
+emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
+                           int64_t N, int64_t K, const void* xp, int64_t ldp, TcGemmParams p,
+                           DeviceState* d, cudaStream_t stream) {
+    // the narrowest tile that holds the rows: the tensor core's time and the
+    // pieces' traffic grow with it
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    CUtensorMap mapA, mapA2, mapB;
+    emu_status_t st = make_plane_map(&mapA, W, true, N, K, ldw, 1, 32, W2 ? 64 : 128);
+    if (st == EMU_OK && W2) st = make_plane_map(&mapA2, W2, true, N, K, ldw2, 1, 32, 64);
+    if (st == EMU_OK) st = make_plane_map(&mapB, xp, false, M, K, ldp, 3, 64, bn);
+    if (st != EMU_OK) return st;
+    p.err = d->err;
+    p.M = (int)N; p.N = (int)M; p.K = (int)K;
+    p.num_kb = (int)((K + 63) / 64);
+    const int rows = W2 ? 64 : 128;              // of each weight per tile
+    p.tiles_m = (int)((N + rows - 1) / rows);
+    p.tiles_n = 1;
+    st = plan_tail(p, gemm_few_ctas(W2 != nullptr, bn, d->sms), kFewRowsHandover, 128, bn, d);
+    if (st != EMU_OK) return st;
+    return from_cuda(launch_gemm_few(bn, mapA, W2 ? &mapA2 : nullptr, mapB, p, d->sms, stream));
+}
+
 namespace {
 
 emu_status_t run_two_pass(int mode, int transA, int transB, int64_t M, int64_t N, int64_t K,

@@ -5,7 +5,11 @@
 // Forward: X is split into its BF16 pieces, and one GEMM over the packed
 // pieces of both weights forms 128 columns of each projection per 256-wide
 // tile, so that a thread of the epilogue holds matching columns of both and
-// writes their gated product (gemm_kblock.cu, kEpiGated).
+// writes their gated product (gemm_kblock.cu, kEpiGated).  Few rows of X
+// leave that GEMM bound by the weights' bytes with most of its 256-row tiles
+// empty: there the FP32 weights themselves are streamed (4 bytes a value
+// instead of the pieces' 6) and split on chip, with X's pieces as the narrow
+// operand (gemm_few.cu).
 //
 // Backward: dG = dH U act'(G), dU = dH act(G), then dX = [dG dU] [Wg; Wu] and
 // [dWg; dWu] = [dG dU]^T X.  Both products read [dG dU] split into BF16
@@ -39,7 +43,8 @@ inline int64_t gated_rows(int64_t F) { return (F + 31) / 32 * 32; }
 // elements (dG from column 0, dU from column Fp, zeros in the gaps F..Fp-1).
 // A thread takes 8 columns of one row: six 16-byte loads, six 16-byte stores
 // (24 bytes read or written per element pair: bound by HBM).
-__global__ void __launch_bounds__(256) gated_grad_split(int act, int64_t M, int64_t F, int64_t Fp,
+template <int ACT>
+__global__ void __launch_bounds__(256) gated_grad_split(int64_t M, int64_t F, int64_t Fp,
                                                         const float* __restrict__ dH, int64_t lddh,
                                                         const float* __restrict__ G,
                                                         const float* __restrict__ U, int64_t ldg,
@@ -68,7 +73,7 @@ __global__ void __launch_bounds__(256) gated_grad_split(int act, int64_t M, int6
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float2 a = gated_act_grad(act, g[j]);
+            const float2 a = gated_act_grad<ACT>(g[j]);
             g[j] = d[j] * u[j] * a.y;                    // dG
             u[j] = d[j] * a.x;                           // dU
         }
@@ -110,6 +115,7 @@ bool small_enough(int64_t M, int64_t F, int64_t K) {
 }
 
 emu_status_t gated_forward(int act, int64_t M, int64_t F, int64_t K, const float* X, int64_t ldx,
+                           const float* Wg, int64_t ldwg, const float* Wu, int64_t ldwu,
                            const void* Wp, int64_t ldwp, float* H, int64_t ldh, float* G, float* U,
                            int64_t ldg, DeviceState* d, cudaStream_t stream) {
     const int64_t ldp = plane_ld(K), Fp = gated_rows(F);
@@ -117,21 +123,23 @@ emu_status_t gated_forward(int act, int64_t M, int64_t F, int64_t K, const float
     if (st != EMU_OK) return st;
     cudaError_t e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);
     if (e != cudaSuccess) return from_cuda(e);
+    TcGemmParams p = {};
+    p.act = act;
+    p.C = H; p.ldc = ldh;
+    p.G = G; p.U = U; p.ldg = ldg;
+    if (few_rows_ok(M, Wg, ldwg) && few_rows_ok(M, Wu, ldwu))
+        return gemm_few_rows(Wg, ldwg, Wu, ldwu, M, F, K, d->ws, ldp, p, d, stream);
     CUtensorMap mapA, mapB;
     st = make_plane_map(&mapA, d->ws, false, M, K, ldp, 3, 64, 128);
     if (st != EMU_OK) return st;
     st = make_plane_map(&mapB, Wp, false, 2 * Fp, K, ldwp, 3, 64, 128);
     if (st != EMU_OK) return st;
-    TcGemmParams p = {};
     p.err = d->err;
     p.M = (int)M; p.N = (int)F; p.K = (int)K;
     p.num_kb = (int)((K + 63) / 64);
     p.tiles_m = (int)((M + 255) / 256);
     p.tiles_n = (int)((F + 127) / 128);
-    p.C = H; p.ldc = ldh;
-    p.act = act;
     p.up_row = (int)Fp;
-    p.G = G; p.U = U; p.ldg = ldg;
     CUtensorMap mapH = mapB, mapG = mapB, mapU = mapB;   // placeholders where stored directly
     p.tma_store = make_c_map(&mapH, H, M, F, ldh) ? 1 : 0;
     if (G)
@@ -201,7 +209,7 @@ emu_status_t emu_gated(int act, int64_t M, int64_t F, int64_t K, const float* X,
         if (e == cudaSuccess && U) e = launch_scale(M, F, 0.0f, U, ldg, stream);
         return from_cuda(e);
     }
-    return gated_forward(act, M, F, K, X, ldx, Wp, ldwp, H, ldh, G, U, ldg, d, stream);
+    return gated_forward(act, M, F, K, X, ldx, Wg, ldwg, Wu, ldwu, Wp, ldwp, H, ldh, G, U, ldg, d, stream);
 }
 
 emu_status_t emu_gated_bwd(int act, int64_t M, int64_t F, int64_t K, const float* dH, int64_t lddh,
@@ -239,8 +247,10 @@ emu_status_t emu_gated_bwd(int act, int64_t M, int64_t F, int64_t K, const float
     uint8_t* xp = static_cast<uint8_t*>(d->ws) + gu_bytes;
     const bool vec = aligned16(dH) && aligned16(G) && aligned16(U) && lddh % 4 == 0 && ldg % 4 == 0;
     const int64_t want = (M * (Fp / 8) + 255) / 256, most = (int64_t)d->sms * 16;
-    gated_grad_split<<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(
-        act, M, F, Fp, dH, lddh, G, U, ldg, vec, gu);
+    with_act(act, [&](auto a) {
+        gated_grad_split<decltype(a)::value><<<(unsigned)(want < most ? want : most), 256, 0, stream>>>(
+            M, F, Fp, dH, lddh, G, U, ldg, vec, gu);
+    });
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return from_cuda(e);
     if (dW) {                                            // independent: may run beside it

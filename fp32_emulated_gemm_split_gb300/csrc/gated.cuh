@@ -16,7 +16,7 @@ constexpr float kGeluCubic = 0.044715f;
 // s = 1 / (1 + e^-g) and c = 1 - s, each without cancellation: with
 // t = e^-|g| <= 1 the larger of the two is 1 / (1 + t), the smaller t / (1 + t).
 __device__ __forceinline__ void sigmoid_pair(float g, float& s, float& c) {
-    const float t = expf(-fabsf(g)), r = 1.0f / (1.0f + t), tr = t * r;
+    const float t = expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + t), tr = t * r;
     s = g < 0.0f ? tr : r;
     c = g < 0.0f ? r : tr;
 }
@@ -29,36 +29,56 @@ __device__ __forceinline__ void sigmoid_pair(float g, float& s, float& c) {
 //   relu       max(g, 0), NaN kept;   sigmoid  s(g)
 // (the forms with erfc and s keep their accuracy for negative g, where 1 +
 // erf and 1 + tanh cancel)
-__device__ __forceinline__ float gated_act(int act, float g) {
-    switch (act) {
-        case kActSilu: return g / (1.0f + expf(-g));
-        case kActGelu: return 0.5f * g * erfcf(-g * kSqrtHalf);
-        case kActGeluTanh:
-            return g / (1.0f + expf(-2.0f * kSqrt2OverPi * fmaf(kGeluCubic * g * g, g, g)));
-        case kActRelu: return g < 0.0f ? 0.0f : g;
-        default: return 1.0f / (1.0f + expf(-g));
-    }
+// (g / d is __fdividef's: 2 ulp; d = 1 + e^x reaches its limit of 2^126 only
+// where the quotient is below 1e-36, and is 0 there)
+template <int ACT>
+__device__ __forceinline__ float gated_act(float g) {
+    if constexpr (ACT == kActSilu) return __fdividef(g, 1.0f + expf(-g));
+    if constexpr (ACT == kActGelu) return 0.5f * g * erfcf(-g * kSqrtHalf);
+    if constexpr (ACT == kActGeluTanh)
+        return __fdividef(g, 1.0f + expf(-2.0f * kSqrt2OverPi * fmaf(kGeluCubic * g * g, g, g)));
+    if constexpr (ACT == kActRelu) return g < 0.0f ? 0.0f : g;
+    return __fdividef(1.0f, 1.0f + expf(-g));
 }
 
 // act(g) and act'(g).
-__device__ __forceinline__ float2 gated_act_grad(int act, float g) {
+template <int ACT>
+__device__ __forceinline__ float2 gated_act_grad(float g) {
     float s, c;
+    if constexpr (ACT == kActSilu) {
+        sigmoid_pair(g, s, c);
+        return make_float2(g * s, s * fmaf(g, c, 1.0f));
+    }
+    if constexpr (ACT == kActGelu) {
+        s = 0.5f * erfcf(-g * kSqrtHalf);
+        return make_float2(g * s, fmaf(g * kInvSqrt2Pi, expf(-0.5f * g * g), s));
+    }
+    if constexpr (ACT == kActGeluTanh) {
+        sigmoid_pair(2.0f * kSqrt2OverPi * fmaf(kGeluCubic * g * g, g, g), s, c);
+        const float dz = kSqrt2OverPi * fmaf(3.0f * kGeluCubic * g, g, 1.0f);
+        return make_float2(g * s, s * fmaf(2.0f * g * c, dz, 1.0f));
+    }
+    if constexpr (ACT == kActRelu) return make_float2(g < 0.0f ? 0.0f : g, g > 0.0f ? 1.0f : 0.0f);
+    sigmoid_pair(g, s, c);
+    return make_float2(s, s * c);
+}
+
+// f(activation as a compile-time constant): the choice is made once around a
+// whole loop.  Made per element it put the code of all five beside every one
+// of an unrolled loop's elements, and the epilogues waited for instructions
+// (22 us of a 78 us kernel at 24 x 4096 x (2 x 8192)).
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int act, F&& f) {
     switch (act) {
-        case kActSilu:
-            sigmoid_pair(g, s, c);
-            return make_float2(g * s, s * fmaf(g, c, 1.0f));
-        case kActGelu:
-            s = 0.5f * erfcf(-g * kSqrtHalf);
-            return make_float2(g * s, fmaf(g * kInvSqrt2Pi, expf(-0.5f * g * g), s));
-        case kActGeluTanh: {
-            sigmoid_pair(2.0f * kSqrt2OverPi * fmaf(kGeluCubic * g * g, g, g), s, c);
-            const float dz = kSqrt2OverPi * fmaf(3.0f * kGeluCubic * g, g, 1.0f);
-            return make_float2(g * s, s * fmaf(2.0f * g * c, dz, 1.0f));
-        }
-        case kActRelu: return make_float2(g < 0.0f ? 0.0f : g, g > 0.0f ? 1.0f : 0.0f);
-        default:
-            sigmoid_pair(g, s, c);
-            return make_float2(s, s * c);
+        case kActSilu: f(Const<kActSilu>{}); break;
+        case kActGelu: f(Const<kActGelu>{}); break;
+        case kActGeluTanh: f(Const<kActGeluTanh>{}); break;
+        case kActRelu: f(Const<kActRelu>{}); break;
+        default: f(Const<kActSigmoid>{}); break;
     }
 }
 
@@ -113,9 +133,11 @@ __device__ __forceinline__ void gated_epilogue(const float (&acc)[C], const TcGe
         const int gc = col0 + 16 * ch;
         if (gc >= p.N) break;                            // warp-uniform
         float h[16];
+        with_act(p.act, [&](auto a) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            h[j] = gated_act(p.act, acc[16 * ch + j]) * acc[C / 2 + 16 * ch + j];
+            for (int j = 0; j < 16; ++j)
+                h[j] = gated_act<decltype(a)::value>(acc[16 * ch + j]) * acc[C / 2 + 16 * ch + j];
+        });
         store_chunk16(h, mapH, p.tma_store, p.C, p.ldc, p.M, p.N, row0, gc, lane, stage);
         if (p.G) {
 #pragma unroll
@@ -126,6 +148,45 @@ __device__ __forceinline__ void gated_epilogue(const float (&acc)[C], const TcGe
             store_chunk16(h, mapU, p.tma_gu, p.U, p.ldg, p.M, p.N, row0, gc, lane, stage);
         }
     }
+}
+
+// Few rows of X (gemm_few.cu): acc[j] is element (weight row m, X row col0 + j),
+// stored at C[(col0 + j) * ldc + m]: a warp writes 32 neighbouring values of
+// each row of C.
+template <int C>
+__device__ __forceinline__ void few_epilogue(const float (&acc)[C], const TcGemmParams& p, int m,
+                                              int col0) {
+    if (m >= p.M) return;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        if (col0 + j < p.N) {
+            float* c = p.C + (int64_t)(col0 + j) * p.ldc + m;
+            float v = p.alpha * acc[j];
+            if (p.beta != 0.0f) v = fmaf(p.beta, *c, v);
+            *c = v;
+        }
+    }
+}
+
+// Gated: the tile's sums are in shared memory, row j of X's 128 at ex + 128 j,
+// the gate's 64 columns from f0, then the up projection's.  Thread t of n
+// takes every n-th element: a warp writes 32 neighbouring values of H.
+__device__ __forceinline__ void few_gated_epilogue(const TcGemmParams& p, const float* ex, int f0,
+                                                   int t, int n) {
+    with_act(p.act, [&](auto a) {
+#pragma unroll 2
+        for (int e = t; e < 64 * p.N; e += n) {
+            const int j = e >> 6, f = e & 63;
+            const float g = ex[j * 128 + f], u = ex[j * 128 + 64 + f];
+            if (f0 + f < p.M) {
+                p.C[(int64_t)j * p.ldc + f0 + f] = gated_act<decltype(a)::value>(g) * u;
+                if (p.G) {
+                    p.G[(int64_t)j * p.ldg + f0 + f] = g;
+                    p.U[(int64_t)j * p.ldg + f0 + f] = u;
+                }
+            }
+        }
+    });
 }
 
 }  // namespace emu

@@ -1,0 +1,527 @@
+// gemm_few.cu -- the emulated GEMM for few rows of X: Y = X W^T with at most
+// 128 rows, where what counts is reading W once.  Used by the gated
+// feed-forward and the projection with adapters (include/emu_layers.h).
+//
+// The method is BF16x9 (gemm_kblock.cu), with the operands' roles swapped: W
+// is the tensor core's A operand, 128 rows of it per tile, read as FP32 (4
+// bytes a value; its three pieces would be 6) and split on chip into tensor
+// memory; X's pieces, which a split kernel has written, are the narrow B
+// operand.  For each 64-element K block a TMA producer fetches 128 x 64 FP32
+// values of W into a ring of staging buffers (two 128-byte-swizzled boxes),
+// split warps turn them into pieces in tensor memory, and the MMAs' partial of
+// that block is added to FP32 registers with round to nearest.
+//
+// Stacked form (BN <= 32): an MMA with its A operand in tensor memory takes
+// 44 cycles however few columns it has up to 64 (measured; 48 at 96 columns,
+// 64 at 128, then in proportion), so the nine products one by one would be
+// bound by instructions.  The three pieces of X side by side are one operand of 3 BN columns: piece i of W
+// times all of them is one MMA per K step, and column group j collects
+//     a0 b_j + 2^-8 (a1 b_j + 2^-8 a2 b_j),
+// largest i first with the scaling between; the accumulator warps add the
+// groups times 2^-8j.  At BN = 64 and 128 the nine products run band by band.
+//
+// Bound by HBM: every value of W is read once.  One CTA per SM, each on its
+// own (no clusters: with CTA pairs the hand-offs between producer, split, MMA
+// and accumulators crossed SMs and took longer than the work between them:
+// 94 us against 39.5 us of HBM time at 24 x 4096 x (2 x 8192)).
+//
+// Work: tiles of 128 rows (gated: 64 rows of each weight), dealt to the CTAs
+// with the tail's K blocks shared evenly (schedule.h); a CTA that holds a
+// later part of a tile leaves its FP32 sums in global memory for the owner.
+//
+// Programmatic launch: W is read before the split of X, the kernel ahead, has
+// ended; only X's pieces and the output wait for it.
+#include <mutex>
+
+#include "emu_device.cuh"
+#include "gated.cuh"
+#include "schedule.h"
+
+namespace emu {
+namespace {
+
+constexpr int kBox = 128 * 128;                       // 128 rows x 32 floats
+constexpr int kABuf = 2 * kBox;                       // one K block of FP32 W
+constexpr int kPieceCols = 32;                        // tensor-memory columns of a piece's K block
+constexpr int kSmemMax = 232448;
+
+template <int BN, bool GATED>
+struct Cfg {
+    static constexpr bool stacked = BN <= 32;
+    static constexpr int d_cols = stacked ? 3 * BN : BN;
+    // The K blocks are dealt in turn to `lanes` pipelines that share nothing
+    // but the producers and the accumulator warps: each has its own FP32
+    // buffers, group of eight split warps, MMA issuer, stages of W's and X's
+    // pieces and partial, so that every barrier is waited for in the order of
+    // its phases.
+    // One group's latencies overlap with the other's arithmetic, and one
+    // issuing thread would need about 2100 cycles for a block's waits, MMAs and
+    // commits beside the busy split warps (the stream 1400).  At BN = 128 the
+    // nine products take 2300 cycles of the tensor core either way.
+    static constexpr int lanes = BN == 128 ? 1 : 2;
+    // tensor memory: partials, then W's pieces (96 columns per K block), both
+    // per pipeline
+    static constexpr int partials = BN == 128 ? 2 : 1;
+    static constexpr int a_stages = BN == 32 ? 1 : 2;
+    static constexpr int a_base = lanes * partials * d_cols;
+    static_assert(a_base + lanes * a_stages * 3 * kPieceCols <= 512, "tensor memory overflow");
+    // shared memory: FP32 buffers (as many as fit: the stream's bytes in
+    // flight), stages of X's pieces, the gated hand-over
+    static constexpr int a_bufs = BN == 16 ? 3 : 2;                          // per pipeline
+    static constexpr int b_tile = BN * kTcBKBytes;
+    static constexpr int b_stages = BN <= 32 ? 2 : BN == 64 ? 1 : 2;    // per pipeline
+    static constexpr int ex_bytes = GATED ? 128 * BN * 4 : 0;
+    static constexpr int smem = lanes * a_bufs * kABuf + lanes * b_stages * 3 * b_tile + ex_bytes + 2048;
+    static_assert(smem <= kSmemMax, "shared memory overflow");
+    // warps: 0 TMA of W and tensor-memory allocation, 1 TMA of X's pieces, 2
+    // (and 3) MMA, then the accumulators, four per column group, and the split
+    // warps
+    static constexpr int acc_warps = BN <= 32 ? 4 : 8;
+    static constexpr int acc_cols = BN / (acc_warps / 4);
+    static constexpr int acc0 = 4, split0 = acc0 + acc_warps;
+    static constexpr int threads = 32 * (split0 + 8 * lanes);
+};
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned* a) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+    return v;
+}
+
+// 32 elements of row r of one swizzled 128 x 32 FP32 box, the three pieces'
+// 16 columns each at `col` (piece i at col + 32 i).  The 32 lanes read the
+// same 16-byte chunk of 32 rows, which the swizzle spreads over the banks.
+// One test per 16 elements keeps infinities and NaNs off the packed path.
+__device__ __forceinline__ void split_to_tmem(const uint8_t* box, uint32_t col, int r) {
+    const uint8_t* row = box + r * 128;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float x[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(row + (((4 * half + c) ^ (r & 7)) << 4));
+            x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+        }
+        float m = max_abs_nan(x[0], x[1]);
+#pragma unroll
+        for (int j = 2; j < 16; ++j) m = max_abs_nan(m, x[j]);
+        uint32_t w0[8], w1[8], w2[8];
+        if (m < __uint_as_float(0x7F800000u)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split_finite_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) split_bf16x3_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
+        }
+        __syncwarp();
+        tmem_st_32x32b_x8(col + 8 * half, w0);
+        tmem_st_32x32b_x8(col + 8 * half + 32, w1);
+        tmem_st_32x32b_x8(col + 8 * half + 64, w2);
+    }
+}
+
+// The gated form's second weight.
+template <bool GATED>
+struct Second {};
+template <>
+struct Second<true> {
+    CUtensorMap map;
+};
+
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(Cfg<BN, GATED>::threads, 1)
+gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ Second<GATED> second,
+                const __grid_constant__ CUtensorMap mapB, const TcGemmParams p) {
+    using C = Cfg<BN, GATED>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    uint8_t* bst = smem + C::lanes * C::a_bufs * kABuf;              // X's pieces
+    float* ex = reinterpret_cast<float*>(bst + C::lanes * C::b_stages * 3 * C::b_tile);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ex) + C::ex_bytes);
+    // FP32 buffer full / free, X's stage full / free, W's pieces ready / free,
+    // partial full / free
+    constexpr int L = C::lanes, NF = L * C::a_bufs, NB = L * C::b_stages, NA = L * C::a_stages, ND = L * C::partials;
+    const uint32_t afull0 = smem_u32(bars), afree0 = afull0 + 8 * NF;
+    const uint32_t bfull0 = afree0 + 8 * NF, bfree0 = bfull0 + 8 * NB;
+    const uint32_t pready0 = bfree0 + 8 * NB, pfree0 = pready0 + 8 * NA;
+    const uint32_t dfull0 = pfree0 + 8 * NA, dfree0 = dfull0 + 8 * ND;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * (NF + NB + NA + ND));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const TileSchedule sch = {p.tiles_m, p.num_kb, p.tail_tiles, p.tail_clusters, int(gridDim.x)};
+    const int nunits = sched_units(sch, cta);
+    uint32_t blocks = 0;                                  // K blocks of all units
+    for (int i = 0; i < nunits; ++i) {
+        const Unit u = sched_unit(sch, cta, i);
+        blocks += uint32_t(u.kb1 - u.kb0);
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NF; ++i) {
+            mbar_init(afull0 + 8 * i, 1);
+            mbar_init(afree0 + 8 * i, 8);                 // the warps of a split group
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(bfull0 + 8 * i, 1);
+            mbar_init(bfree0 + 8 * i, 1);
+        }
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(pready0 + 8 * i, 8);
+            mbar_init(pfree0 + 8 * i, 1);
+        }
+        for (int i = 0; i < ND; ++i) {
+            mbar_init(dfull0 + 8 * i, 1);
+            mbar_init(dfree0 + 8 * i, C::acc_warps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&mapA);
+            tma_prefetch_desc(&mapB);
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    // Block g runs in pipeline g % L as its block n = g / L, in the stage
+    // n % count of that pipeline's rings (slot() of them all), whose barriers
+    // are then in phase n / count.
+    auto slot_of = [](uint32_t g, int count) { return (g % L) * count + (g / L) % count; };
+    auto phase_of = [](uint32_t g, int count) { return (g / L / count) & 1; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------ stream of W
+            uint32_t g = 0;
+            bool ok = true;
+            for (int i = 0; i < nunits && ok; ++i) {
+                const Unit w = sched_unit(sch, cta, i);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++g) {
+                    const uint32_t f = slot_of(g, C::a_bufs);
+                    if (!mbar_wait(afree0 + 8 * f, phase_of(g, C::a_bufs) ^ 1, p.err, kDevErrTimeout) || *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(smem + f * kABuf), bar = afull0 + 8 * f;
+                    mbar_arrive_expect_tx(bar, kABuf);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int k = kb * 64 + 32 * x;
+                        if constexpr (GATED) {
+                            tma_load_3d(dst + x * kBox, &mapA, bar, k, w.tile * 64, 0);
+                            tma_load_3d(dst + x * kBox + kBox / 2, &second.map, bar, k, w.tile * 64, 0);
+                        } else {
+                            tma_load_3d(dst + x * kBox, &mapA, bar, k, w.tile * 128, 0);
+                        }
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------------ X's pieces
+            griddep_wait();                               // the split ahead has written them
+            uint32_t g = 0;
+            bool ok = true;
+            for (int i = 0; i < nunits && ok; ++i) {
+                const Unit w = sched_unit(sch, cta, i);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++g) {
+                    const uint32_t s = slot_of(g, C::b_stages);
+                    if (!mbar_wait(bfree0 + 8 * s, phase_of(g, C::b_stages) ^ 1, p.err, kDevErrTimeout) || *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = smem_u32(bst + s * 3 * C::b_tile), bar = bfull0 + 8 * s;
+                    mbar_arrive_expect_tx(bar, 3 * C::b_tile);
+#pragma unroll
+                    for (int pc = 0; pc < 3; ++pc)
+                        tma_load_3d(st + pc * C::b_tile, &mapB, bar, kb * 64, 0, pc);
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp < C::acc0) {
+        if (lane == 0 && warp - 2 < L) {
+            // ----------------------------------------------------- MMA issuers
+            const uint32_t idesc = make_idesc(1u, 128, C::d_cols);
+            for (uint32_t g = warp - 2; g < blocks; g += L) {
+                const uint32_t s = slot_of(g, C::b_stages), t = slot_of(g, C::a_stages);
+                const uint32_t b = slot_of(g, C::partials);
+                if (!mbar_wait(dfree0 + 8 * b, phase_of(g, C::partials) ^ 1, p.err, kDevErrTimeout) ||
+                    !mbar_wait(bfull0 + 8 * s, phase_of(g, C::b_stages), p.err, kDevErrTimeout) ||
+                    !mbar_wait(pready0 + 8 * t, phase_of(g, C::a_stages), p.err, kDevErrTimeout) ||
+                    *abort_flag) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + b * C::d_cols;
+                const uint32_t a = tmem + C::a_base + t * 3 * kPieceCols;
+                const uint32_t st = smem_u32(bst + s * 3 * C::b_tile);
+                // piece i of W times the operand at `tile`: four K = 16 steps;
+                // shift: times 2^-8 what the accumulator holds before them
+                auto run = [&](int i, uint32_t tile, bool first, bool shift) {
+                    const uint64_t desc = make_sw128_kmajor_desc(tile);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k == 0 && shift)
+                            mma_cta1_ta_scaled<8>(d, a + kPieceCols * i, desc, idesc);
+                        else
+                            mma_cta1_ta(d, a + kPieceCols * i + 8 * k, desc + 2 * k, idesc,
+                                        (k == 0 && first) ? 0u : 1u);
+                    }
+                };
+                if constexpr (C::stacked) {
+                    run(2, st, true, false);
+                    run(1, st, false, true);
+                    run(0, st, false, true);
+                } else {
+                    const uint32_t b0 = st, b1 = st + C::b_tile, b2 = st + 2 * C::b_tile;
+                    run(2, b2, true, false);              // band 4
+                    run(1, b2, false, true);              // band 3
+                    run(2, b1, false, false);
+                    run(0, b2, false, true);              // band 2
+                    run(1, b1, false, false);
+                    run(2, b0, false, false);
+                    run(0, b1, false, true);              // band 1
+                    run(1, b0, false, false);
+                    run(0, b0, false, true);              // band 0
+                }
+                tc_commit(pfree0 + 8 * t);
+                tc_commit(dfull0 + 8 * b);
+                tc_commit(bfree0 + 8 * s);
+            }
+        }
+    } else if (warp >= C::split0) {
+        // ---------------------------------------------------------- split warps
+        const int w = warp - C::split0, group = w >> 3;
+        const int khalf = (w >> 2) & 1;                   // 32-element half of the 64
+        const int r = 32 * (warp & 3) + lane;             // row: this warp's TMEM lanes
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        for (uint32_t g = group; g < blocks; g += L) {
+            const uint32_t f = slot_of(g, C::a_bufs), t = slot_of(g, C::a_stages);
+            if (!mbar_wait(afull0 + 8 * f, phase_of(g, C::a_bufs), p.err, kDevErrTimeout) ||
+                !mbar_wait(pfree0 + 8 * t, phase_of(g, C::a_stages) ^ 1, p.err, kDevErrTimeout) ||
+                *abort_flag) {
+                *abort_flag = 1;
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            split_to_tmem(smem + f * kABuf + khalf * kBox,
+                          (tmem + C::a_base + t * 3 * kPieceCols + 16 * khalf) | lanes, r);
+            tmem_st_wait();
+            tc_fence_before();                            // tensor-memory stores -> the MMA
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(pready0 + 8 * t);
+                mbar_arrive(afree0 + 8 * f);
+            }
+        }
+    } else if (warp >= C::acc0) {
+        // ---------------------------------------------------- accumulator warps
+        constexpr int AC = C::acc_cols;
+        const int q = warp & 3, h = (warp - C::acc0) >> 2, aw = warp - C::acc0;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        auto slot = [&](int c) { return c * C::acc_warps + aw; };
+        uint32_t g = 0;
+        bool ok = true;
+        for (int i = 0; i < nunits; ++i) {
+            const Unit w = sched_unit(sch, cta, i);
+            float acc[AC];
+#pragma unroll
+            for (int j = 0; j < AC; ++j) acc[j] = 0.0f;
+            for (int kb = w.kb0; kb < w.kb1 && ok; ++kb, ++g) {
+                const uint32_t b = slot_of(g, C::partials);
+                if (!mbar_wait(dfull0 + 8 * b, phase_of(g, C::partials), p.err, kDevErrTimeout)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t col = (tmem + b * C::d_cols + h * AC) | lanes;
+#pragma unroll
+                for (int c = 0; c < AC; c += 8) {
+                    uint32_t r0[8], r1[8], r2[8];
+                    tmem_ld_32x32b_x8(col + c, r0);
+                    if constexpr (C::stacked) {
+                        tmem_ld_32x32b_x8(col + BN + c, r1);
+                        tmem_ld_32x32b_x8(col + 2 * BN + c, r2);
+                    }
+                    tmem_ld_wait();
+                    if (c + 8 == AC) {
+                        // all read: the buffer is free before the sums are formed
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(dfree0 + 8 * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v = __uint_as_float(r0[j]);
+                        if constexpr (C::stacked)
+                            v += fmaf(__uint_as_float(r2[j]), 0x1p-16f, __uint_as_float(r1[j]) * 0x1p-8f);
+                        acc[c + j] += v;
+                    }
+                }
+            }
+            if (!GATED && (!ok || *abort_flag)) break;
+            if (w.publish >= 0) {
+                // a later part of a split tile: leave the sums for the owner
+                if (!ok) continue;                        // (gated: on to the next meeting)
+                float4* dst = reinterpret_cast<float4*>(p.part_ws) + (size_t)slot(cta) * (AC / 4 * 32) + lane;
+#pragma unroll
+                for (int j = 0; j < AC / 4; ++j)
+                    __stcg(dst + j * 32, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
+                asm volatile("fence.acq_rel.gpu;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    asm volatile("st.release.gpu.global.u32 [%0], %1;"
+                                 :: "l"(p.flags + slot(cta)), "r"(p.epoch) : "memory");
+                continue;
+            }
+            // the owner adds the later parts in K order (bounded waits: those
+            // CTAs leave theirs before they wait for anything)
+            for (int o = 1; o <= w.others && ok; ++o) {
+                unsigned* flag = p.flags + slot(cta + o);
+                const uint64_t t0 = global_timer_ns();
+                while (load_acquire(flag) != p.epoch) {
+                    __nanosleep(64);
+                    if (global_timer_ns() - t0 > EMU_WAIT_LIMIT_NS) {
+                        record_error(p.err, kDevErrTimeout);
+                        ok = false;
+                        break;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const float4* src = reinterpret_cast<const float4*>(p.part_ws) +
+                                    (size_t)slot(cta + o) * (AC / 4 * 32) + lane;
+#pragma unroll
+                for (int j = 0; j < AC / 4; ++j) {
+                    const float4 v = __ldcg(src + j * 32);
+                    acc[4 * j] += v.x;
+                    acc[4 * j + 1] += v.y;
+                    acc[4 * j + 2] += v.z;
+                    acc[4 * j + 3] += v.w;
+                }
+                // consumed: cleared, so that a replay of this launch waits afresh
+                __syncwarp();
+                if (lane == 0) *const_cast<volatile unsigned*>(flag) = 0u;
+            }
+            const int col0 = h * AC;                      // rows of X
+            if constexpr (GATED) {
+                // rows 0..63 of the tile are the gate's, 64..127 the same rows
+                // of the up projection: their sums meet in shared memory.  Every warp reaches the first barrier of a
+                // tile, whether its waits held or not, and they leave together.
+                // It also keeps the next tile's sums out until these are read.
+                ok = bar_and(1, C::acc_warps * 32, ok && !*abort_flag);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                float* mine = ex + h * AC * 128 + q * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < AC; ++j) mine[j * 128] = acc[j];
+                bar_and(1, C::acc_warps * 32, true);
+                few_gated_epilogue(p, ex, w.tile * 64, aw * 32 + lane, C::acc_warps * 32);
+            } else {
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                few_epilogue<AC>(acc, p, w.tile * 128 + q * 32 + lane, col0);
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     :: "r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// The dynamic shared-memory limit, raised once per device and variant.
+constexpr int kMaxDev = 64;
+template <int BN, bool GATED>
+cudaError_t raise_smem() {
+    static std::mutex mu;
+    static bool done[kMaxDev] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < kMaxDev && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(gemm_few_kernel<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<BN, GATED>::smem);
+    if (e == cudaSuccess && dev < kMaxDev) done[dev] = true;
+    return e;
+}
+
+template <int BN, bool GATED>
+cudaError_t launch_few(const CUtensorMap& mapA, const Second<GATED>& second, const CUtensorMap& mapB,
+                       const TcGemmParams& q, int ctas, cudaStream_t stream) {
+    cudaError_t e = raise_smem<BN, GATED>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(Cfg<BN, GATED>::threads);
+    cfg.dynamicSmemBytes = Cfg<BN, GATED>::smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm_few_kernel<BN, GATED>, mapA, second, mapB, q);
+}
+
+template <bool GATED>
+cudaError_t launch_bn(int bn, const CUtensorMap& mapA, const Second<GATED>& second,
+                      const CUtensorMap& mapB, const TcGemmParams& q, int ctas, cudaStream_t stream) {
+    switch (bn) {
+        case 16: return launch_few<16, GATED>(mapA, second, mapB, q, ctas, stream);
+        case 32: return launch_few<32, GATED>(mapA, second, mapB, q, ctas, stream);
+        case 64: return launch_few<64, GATED>(mapA, second, mapB, q, ctas, stream);
+        case 128: return launch_few<128, GATED>(mapA, second, mapB, q, ctas, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+// One CTA per SM: each takes nearly all of an SM's shared memory and all of
+// its tensor memory.
+int gemm_few_ctas(bool, int, int sms) { return sms; }
+
+cudaError_t launch_gemm_few(int bn, const CUtensorMap& mapA, const CUtensorMap* mapA2,
+                            const CUtensorMap& mapB, const TcGemmParams& p, int sms,
+                            cudaStream_t stream) {
+    if (p.tiles_m == 0 || p.num_kb == 0) return cudaSuccess;
+    TcGemmParams q = p;
+    const int resident = gemm_few_ctas(mapA2 != nullptr, bn, sms);
+    const bool split = q.tail_tiles > 0 && q.tail_tiles <= q.tiles_m && q.part_ws && q.flags &&
+                       q.tail_clusters >= 1 && q.tail_clusters <= resident &&
+                       (q.tiles_m - q.tail_tiles) % resident == 0;
+    if (!split) q.tail_tiles = q.tail_clusters = 0;
+    const int ctas = sched_grid_clusters(q.tiles_m, q.tail_tiles, q.tail_clusters, resident);
+    const cudaError_t e = mapA2 ? launch_bn<true>(bn, mapA, Second<true>{*mapA2}, mapB, q, ctas, stream)
+                                : launch_bn<false>(bn, mapA, Second<false>{}, mapB, q, ctas, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace emu

@@ -270,16 +270,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
                  :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Named barrier `id` over `nthreads` threads that also ANDs a predicate: every
-// participating warp reaches it once per use, whatever its predicate, so a
-// warp whose wait gave up still meets the others and all leave together.
-__device__ __forceinline__ bool bar_and(int id, int nthreads, bool v) {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n"
-                 " bar.red.and.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(r) : "r"(uint32_t(v)), "r"(id), "r"(nthreads) : "memory");
-    return r != 0;
-}
 constexpr int kSplitBarrier = 1;                      // named barrier of the split warps
 
 // Further tensor maps of an epilogue: none, or the gated one's G and U.

@@ -200,6 +200,12 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
     if (e != cudaSuccess || K == 0) return from_cuda(e);
     e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);
     if (e != cudaSuccess) return from_cuda(e);
+    if (few_rows_ok(M, W, ldw)) {
+        TcGemmParams q = {};
+        q.alpha = q.beta = 1.0f;
+        q.C = Y; q.ldc = ldy;
+        return gemm_few_rows(W, ldw, nullptr, 0, M, N, K, d->ws, ldp, q, d, stream);
+    }
     return gemm_on_pieces(kModeBf16x9, PieceSet{d->ws, ldp, 0, 0}, PieceSet{Wp, ldwp, 0, 0}, M, N, K,
                           1.0f, 1.0f, Y, ldy, d, stream);
 }
