@@ -30,7 +30,10 @@
 // later part of a tile leaves its FP32 sums in global memory for the owner.
 //
 // Programmatic launch: W is read before the split of X, the kernel ahead, has
-// ended; only X's pieces and the output wait for it.
+// ended; only X's pieces and the output wait for it.  (X's rows split in this
+// kernel too, by a warp per pipeline, would save that launch, but beside the
+// busy split warps such a warp took twice the time of the stream: 24 x 4096 x
+// (2 x 8192) 146 us against 61.)
 #include <mutex>
 
 #include "emu_device.cuh"
@@ -76,7 +79,7 @@ struct Cfg {
     // warps: 0 TMA of W and tensor-memory allocation, 1 TMA of X's pieces, 2
     // (and 3) MMA, then the accumulators, four per column group, and the split
     // warps
-    static constexpr int acc_warps = BN <= 32 ? 4 : 8;
+    static constexpr int acc_warps = BN == 16 ? 4 : 8;
     static constexpr int acc_cols = BN / (acc_warps / 4);
     static constexpr int acc0 = 4, split0 = acc0 + acc_warps;
     static constexpr int threads = 32 * (split0 + 8 * lanes);
@@ -337,6 +340,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         auto slot = [&](int c) { return c * C::acc_warps + aw; };
         uint32_t g = 0;
         bool ok = true;
+        griddep_wait();                                   // the kernel ahead may still read or write C
         for (int i = 0; i < nunits; ++i) {
             const Unit w = sched_unit(sch, cta, i);
             float acc[AC];
