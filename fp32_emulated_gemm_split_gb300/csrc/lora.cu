@@ -3,13 +3,15 @@
 //
 // Three steps: S[t] = A_i X[t] for every token with an adapter (down), Y[t] =
 // bias + scale_i B_i S[t] (up), and the shared projection added to it by the
-// emulated GEMM (beta = 1).  The adapters' steps group the tokens by adapter as
-// they go: a block takes one adapter and one window of tokens, scans the
-// window's indices, and works on the tokens of its own in order, so an
-// adapter's rows are read once for all of them and no sorted copy of the tokens
-// is made.  K is cut into slices so that few tokens, too, fill the GPU; the up
-// step adds the slices in order.  Every output element is one fixed sum: where
-// a token stands in the batch cannot change its result.
+// emulated GEMM (beta = 1).  K is cut into slices so that few tokens, too, fill
+// the GPU; the up step adds the slices in order.
+//
+// Up to kFewTokens tokens a block takes four neighbouring tokens and one after
+// another the adapters among them: an adapter's rows come from L2 again for
+// every four tokens, and no grouping has to run first.  Beyond that one block
+// groups the tokens by adapter (lora_group) into tiles of up to 64, and the
+// steps' blocks take a tile each.  Every output element is one fixed sum, so
+// neither the order of the tokens in the batch nor that of a tile changes it.
 //
 // Both steps are FP32 on the CUDA cores, in packed pairs (fma.rn.f32x2: twice
 // the rate of single FMAs).  They are 2 R (K + N) of a token's 2 N K operations,
@@ -34,110 +36,147 @@ struct LoraParams {
     float* Y;
     int64_t ldy;
     int* err;
+    // the grouping (many tokens): the tokens by adapter, and its tiles
+    int32_t* order;
+    int4* tiles;             // adapter (== adapters: none), first place in order, tokens
+    int32_t* ntiles;
 };
 
-constexpr int kWindow = 2048;                // tokens scanned by a block
+constexpr int64_t kFewTokens = 256;          // up to here: no grouping
+constexpr int kTileTok = 64;                 // tokens of a tile
+constexpr int kMaxAdapters = 8191;           // lora_group counts them in shared memory
 
-// The tokens of window `win` whose adapter is `a` (a == adapters: those
-// without one), in order, as offsets in the window; returns how many.  Called
-// by all T threads of a block.
-template <int T>
-__device__ __forceinline__ int tokens_of(const LoraParams& p, int a, int64_t win, uint16_t* list) {
-    __shared__ int warp_n[T / 32];
-    constexpr int kPer = kWindow / T;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t0 = win * kWindow;
-    const int in = p.M - t0 < kWindow ? int(p.M - t0) : kWindow;
-    // thread i looks at tokens i kPer .. i kPer + kPer - 1
-    unsigned mine = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = threadIdx.x * kPer + j;
-        if (i < in) {
-            const int32_t v = p.index ? p.index[t0 + i] : -1;
-            const bool none = v < 0 || v >= p.adapters;
-            if (a == p.adapters ? none : v == a) mine |= 1u << j;
-            if (a == p.adapters && none && v != -1) record_error(p.err, kDevErrValue);
-        }
-    }
-    const int n = __popc(mine);
-    int upto = n;                            // of this warp's lanes, this one included
+// The adapter of token t, `adapters` for none.
+__device__ __forceinline__ int adapter_of(const LoraParams& p, int64_t t) {
+    const int32_t v = p.index ? p.index[t] : -1;
+    if (v >= 0 && v < p.adapters) return v;
+    if (v != -1) record_error(p.err, kDevErrValue);
+    return p.adapters;
+}
+
+// Sum of v over the block's threads before this one (1024 threads).
+__device__ __forceinline__ int block_before(int v, int* warp_sum, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int upto = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
     }
-    if (lane == 31) warp_n[warp] = upto;
+    if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
-    int at = upto - n, total = 0;
-    for (int w = 0; w < T / 32; ++w) {
-        if (w < warp) at += warp_n[w];
-        total += warp_n[w];
+    int before = upto - v, all = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
     }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-        if (mine >> j & 1) list[at++] = (uint16_t)(threadIdx.x * kPer + j);
     __syncthreads();
-    return total;
+    *total = all;
+    return before;
+}
+
+// Groups the tokens by adapter and cuts the groups into tiles.  One block; the
+// tokens are counted and placed with shared-memory atomics (their order inside
+// a group is not fixed and does not matter).
+__global__ void __launch_bounds__(1024) lora_group(const LoraParams p) {
+    __shared__ int count[kMaxAdapters + 1];  // tokens, then the next free place
+    __shared__ int warp_sum[32];
+    const int groups = p.adapters + 1, tid = threadIdx.x;
+    for (int a = tid; a < groups; a += 1024) count[a] = 0;
+    __syncthreads();
+    for (int64_t t = tid; t < p.M; t += 1024) atomicAdd(&count[adapter_of(p, t)], 1);
+    __syncthreads();
+    const int per = (groups + 1023) / 1024;
+    int tokens = 0, tiles = 0;
+    for (int a = tid * per; a < min(groups, (tid + 1) * per); ++a) {
+        tokens += count[a];
+        tiles += (count[a] + kTileTok - 1) / kTileTok;
+    }
+    int all, all_tiles;
+    int at = block_before(tokens, warp_sum, &all);
+    int tile = block_before(tiles, warp_sum, &all_tiles);
+    for (int a = tid * per; a < min(groups, (tid + 1) * per); ++a) {
+        const int n = count[a];
+        for (int i = 0; i < n; i += kTileTok) p.tiles[tile++] = make_int4(a, at + i, min(kTileTok, n - i), 0);
+        count[a] = at;
+        at += n;
+    }
+    if (tid == 0) *p.ntiles = all_tiles;
+    __syncthreads();
+    for (int64_t t = tid; t < p.M; t += 1024) p.order[atomicAdd(&count[adapter_of(p, t)], 1)] = (int32_t)t;
 }
 
 // ------------------------------------------------------------- down, dots --
 //
-// Few tokens: S[t][r] over one slice of K.  A warp takes two rows of A and
-// four tokens at a time, its lanes stride over the slice (V neighbouring
-// values each).  Bound by the latency of reading A's rows once.
+// Few tokens: S[t][r] over one slice of K.  A block takes four neighbouring
+// tokens, a warp two rows of A (the block 16 of them), its lanes stride over
+// the slice (V neighbouring values each).  Bound by the latency of reading A's
+// rows once.
 constexpr int kDotWarps = 8, kDotTok = 4, kDotRows = 2;
 
 template <int V>
 __global__ void __launch_bounds__(kDotWarps * 32) lora_down_dots(const LoraParams p) {
-    __shared__ uint16_t list[kWindow];
-    const int a = blockIdx.x;
-    const int64_t win = blockIdx.y;
-    const int n = tokens_of<kDotWarps * 32>(p, a, win, list);
+    const int64_t t0 = (int64_t)blockIdx.x * kDotTok;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t k0 = blockIdx.z * p.slice, k1 = min(p.K, k0 + p.slice);
-    float* S = p.S + blockIdx.z * p.M * p.R;
-    for (int i0 = 0; i0 < n; i0 += kDotTok) {
-        const float* row[kDotTok];
+    const int slice = blockIdx.z;
+    const int64_t k0 = slice * p.slice, k1 = min(p.K, k0 + p.slice);
+    float* S = p.S + slice * p.M * p.R;
+    const int r = (blockIdx.y * kDotWarps + warp) * kDotRows;
+    if (r >= p.R) return;
+    int own[kDotTok];
+    const float* row[kDotTok];
 #pragma unroll
-        for (int j = 0; j < kDotTok; ++j)    // past the end: the first token again, not stored
-            row[j] = p.X + (win * kWindow + list[i0 + j < n ? i0 + j : i0]) * p.ldx;
-        for (int r = warp * kDotRows; r < p.R; r += kDotWarps * kDotRows) {
-            const float* ar = p.A + ((int64_t)a * p.R + r) * p.K;
-            const float* ar1 = r + 1 < p.R ? ar + p.K : ar;
-            float acc[kDotRows][kDotTok] = {};
+    for (int j = 0; j < kDotTok; ++j) {      // past the end: the first token again, not stored
+        const int64_t t = t0 + j < p.M ? t0 + j : t0;
+        own[j] = t0 + j < p.M ? adapter_of(p, t) : p.adapters;
+        row[j] = p.X + t * p.ldx;
+    }
+    for (unsigned left = (1u << kDotTok) - 1; left != 0;) {
+        // the first token left, and those with the same adapter
+        int a = p.adapters;
+#pragma unroll
+        for (int j = kDotTok - 1; j >= 0; --j)
+            if (left >> j & 1) a = own[j];
+        unsigned now = 0;
+#pragma unroll
+        for (int j = 0; j < kDotTok; ++j)
+            if (own[j] == a) now |= 1u << j;
+        left &= ~now;
+        if (a == p.adapters) continue;
+        const float* ar = p.A + ((int64_t)a * p.R + r) * p.K;
+        const float* ar1 = r + 1 < p.R ? ar + p.K : ar;
+        float acc[kDotRows][kDotTok] = {};
 #pragma unroll 2
-            for (int64_t k = k0 + lane * V; k < k1; k += 32 * V) {
-                float w[kDotRows][V], x[V];
-                if constexpr (V == 4) {
-                    *reinterpret_cast<float4*>(w[0]) = *reinterpret_cast<const float4*>(ar + k);
-                    *reinterpret_cast<float4*>(w[1]) = *reinterpret_cast<const float4*>(ar1 + k);
-                } else {
-                    w[0][0] = ar[k];
-                    w[1][0] = ar1[k];
-                }
-#pragma unroll
-                for (int j = 0; j < kDotTok; ++j) {
-                    if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(row[j] + k);
-                    else x[0] = row[j][k];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        acc[0][j] = fmaf(w[0][v], x[v], acc[0][j]);
-                        acc[1][j] = fmaf(w[1][v], x[v], acc[1][j]);
-                    }
-                }
+        for (int64_t k = k0 + lane * V; k < k1; k += 32 * V) {
+            float w[kDotRows][V], x[V];
+            if constexpr (V == 4) {
+                *reinterpret_cast<float4*>(w[0]) = *reinterpret_cast<const float4*>(ar + k);
+                *reinterpret_cast<float4*>(w[1]) = *reinterpret_cast<const float4*>(ar1 + k);
+            } else {
+                w[0][0] = ar[k];
+                w[1][0] = ar1[k];
             }
 #pragma unroll
-            for (int q = 0; q < kDotRows; ++q)
+            for (int j = 0; j < kDotTok; ++j) {
+                if (!(now >> j & 1)) continue;       // the block's own, uniform
+                if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(row[j] + k);
+                else x[0] = row[j][k];
 #pragma unroll
-                for (int j = 0; j < kDotTok; ++j) {
-                    float v = acc[q][j];
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane == 0 && i0 + j < n && r + q < p.R)
-                        S[(win * kWindow + list[i0 + j]) * p.R + r + q] = v;
+                for (int v = 0; v < V; ++v) {
+                    acc[0][j] = fmaf(w[0][v], x[v], acc[0][j]);
+                    acc[1][j] = fmaf(w[1][v], x[v], acc[1][j]);
                 }
+            }
         }
+#pragma unroll
+        for (int q = 0; q < kDotRows; ++q)
+#pragma unroll
+            for (int j = 0; j < kDotTok; ++j) {
+                float v = acc[q][j];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0 && (now >> j & 1) && r + q < p.R) S[(t0 + j) * p.R + r + q] = v;
+            }
     }
 }
 
@@ -145,14 +184,14 @@ __global__ void __launch_bounds__(kDotWarps * 32) lora_down_dots(const LoraParam
 //
 // Many tokens: tiles of 64 tokens x 16 rows of A per warp, over one slice of
 // K.  The block stages 64 values of K of its 64 tokens and of 16 G rows of A at
-// a time in shared memory (two buffers, filled by cp.async); its 8 warps are G
+// a time in shared memory (kTileStages buffers, filled by cp.async); its 8 warps are G
 // groups of 16 rows times 8 / G parts of each stage.  A lane owns 8 tokens x 4
 // rows, each sum as a pair over even and odd k, which is how 16-byte loads
 // along K leave the operands; rows are padded by four values, so the eight
 // token groups of a load fall into different banks.  Bound by shared-memory
 // loads: 12 of them per 64 packed FMAs.
-constexpr int kTileTok = 64, kTileK = 64, kTileRow = kTileK + 4, kTileWarps = 8;
-constexpr int kTileGroups = 4;               // z blocks that share a window's tiles
+constexpr int kTileK = 64, kTileRow = kTileK + 4, kTileWarps = 8;
+constexpr int kTileStages = 4;
 
 __device__ __forceinline__ void cp_async16(float* dst, const float* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -162,27 +201,32 @@ __device__ __forceinline__ void cp_async4(float* dst, const float* src, bool in)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
                  :: "r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-constexpr int tile_smem(int G) { return 2 * (kTileTok + 16 * G) * kTileRow * 4; }
+constexpr int tile_smem(int G) { return kTileStages * (kTileTok + 16 * G) * kTileRow * 4; }
 
 template <int V, int G>
 __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraParams p) {
-    extern __shared__ __align__(16) float stage[];   // [2][64 + 16 G][kTileRow]
-    __shared__ uint16_t list[kWindow];
+    extern __shared__ __align__(16) float stage[];   // [kTileStages][64 + 16 G][kTileRow]
     constexpr int kRows = kTileTok + 16 * G, kParts = kTileWarps / G;
-    const int a = blockIdx.x;
-    const int64_t win = blockIdx.y;
-    const int n = tokens_of<kTileWarps * 32>(p, a, win, list);
+    if ((int)blockIdx.x >= *p.ntiles) return;
+    const int4 tile = p.tiles[blockIdx.x];
+    const int a = tile.x, n = tile.z;
+    if (a == p.adapters) return;
+    const int32_t* list = p.order + tile.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = warp % G, part = warp / G;
     const int tg = lane & 7, rg = lane >> 3;         // tokens tg + 8 i, rows rg + 4 j
-    const int slice = blockIdx.z / kTileGroups;
+    const int slice = blockIdx.y;
     const int64_t k0 = slice * p.slice, k1 = min(p.K, k0 + p.slice);
     const int steps = int((k1 - k0 + kTileK - 1) / kTileK);
     float* S = p.S + slice * p.M * p.R;
-    for (int i0 = (blockIdx.z % kTileGroups) * kTileTok; i0 < n; i0 += kTileGroups * kTileTok) {
+    {
         for (int r0 = 0; r0 < p.R; r0 += 16 * G) {
             auto fill = [&](int st) {
-                float* dst = stage + (st & 1) * kRows * kTileRow;
+                if (st >= steps) {                       // (an empty group keeps the count)
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    return;
+                }
+                float* dst = stage + (st % kTileStages) * kRows * kTileRow;
                 const int64_t k = k0 + (int64_t)st * kTileK;
                 constexpr int per = kTileK / V;      // copies per row
                 for (int e = tid; e < kRows * per; e += kTileWarps * 32) {
@@ -190,8 +234,8 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
                     const float* src;
                     bool in;
                     if (row < kTileTok) {
-                        in = i0 + row < n;
-                        src = p.X + (win * kWindow + list[in ? i0 + row : 0]) * p.ldx;
+                        in = row < n;
+                        src = p.X + (int64_t)list[in ? row : 0] * p.ldx;
                     } else {
                         const int r = r0 + row - kTileTok;
                         in = r < p.R;
@@ -204,17 +248,13 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
             uint64_t acc[8][4] = {};
-            fill(0);
+            for (int st = 0; st < kTileStages - 1; ++st) fill(st);
             for (int st = 0; st < steps; ++st) {
-                if (st + 1 < steps) {
-                    fill(st + 1);
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                } else {
-                    asm volatile("cp.async.wait_group 0;" ::: "memory");
-                }
-                __syncthreads();
-                const float* xs = stage + (st & 1) * kRows * kTileRow + tg * kTileRow;
-                const float* as = stage + (st & 1) * kRows * kTileRow + (kTileTok + 16 * group + rg) * kTileRow;
+                asm volatile("cp.async.wait_group %0;" :: "n"(kTileStages - 2) : "memory");
+                __syncthreads();                     // stage st is here, st - 1 is free again
+                fill(st + kTileStages - 1);
+                const float* xs = stage + (st % kTileStages) * kRows * kTileRow + tg * kTileRow;
+                const float* as = stage + (st % kTileStages) * kRows * kTileRow + (kTileTok + 16 * group + rg) * kTileRow;
 #pragma unroll
                 for (int c = 4 * part; c < kTileK; c += 4 * kParts) {
                     ulonglong2 av[4];
@@ -230,8 +270,9 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
                         }
                     }
                 }
-                __syncthreads();                     // the buffer is filled again
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
             // the parts of K meet in shared memory, added in order
             float* sum = stage;                      // [part][group][64 tokens][16 rows]
 #pragma unroll
@@ -247,7 +288,7 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
 #pragma unroll
                 for (int q = 0; q < kParts; ++q)
                     v += sum[((q * G + r / 16) * kTileTok + t) * 16 + r % 16];
-                if (i0 + t < n && r0 + r < p.R) S[(win * kWindow + list[i0 + t]) * p.R + r0 + r] = v;
+                if (t < n && r0 + r < p.R) S[(int64_t)list[t] * p.R + r0 + r] = v;
             }
             __syncthreads();
         }
@@ -257,90 +298,124 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
 // --------------------------------------------------------------------- up --
 //
 // Y[t][n] = bias[n] + scale sum_r B[n][r] S[t][r]: a thread takes C columns,
-// kUpThreads apart (a warp writes 128 neighbouring bytes), keeps kUpRank
-// values of each one's row of B in registers and walks up to kUpTok of the
-// window's tokens of its adapter, whose S the block has put in shared memory
-// (times the scale, the slices of K added in order); higher ranks take more
-// passes, which add to Y.  Bound by the writes of Y.
-constexpr int kUpThreads = 128, kUpRank = 16, kUpTok = 64, kUpGroups = 4;
+// kUpThreads apart (a warp writes 128 neighbouring bytes), keeps RK values of
+// each one's row of B in registers (loaded V at a time, as pairs of
+// neighbouring ranks) and walks its tokens, whose S the block has put in shared
+// memory (times the scale, the slices of K added in order); higher ranks take
+// more passes, which add to Y.  Bound by the writes of Y, for few tokens by the
+// latency of reading B.
+constexpr int kUpThreads = 128;
 
-template <int C>
-__global__ void __launch_bounds__(kUpThreads) lora_up(const LoraParams p) {
-    __shared__ uint16_t list[kWindow];
-    __shared__ __align__(16) float s[kUpTok][kUpRank];
-    const int a = blockIdx.x;
-    const int64_t win = blockIdx.y;
-    const int cnt = tokens_of<kUpThreads>(p, a, win, list);
-    const int64_t n0 = (int64_t)(blockIdx.z / kUpGroups) * (C * kUpThreads) + threadIdx.x;
+// Tokens list[0..nt) (or t0, t0 + 1, .. where list is null) of adapter a.
+template <int C, int RK, int V>
+__device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int32_t* list, int64_t t0,
+                                          int nt, int64_t n0, float (*s)[RK]) {
     const int R = a == p.adapters ? 0 : p.R;
     const float scale = R > 0 && p.scale ? p.scale[a] : 1.0f;
-    float bias[C];
+    int r0 = 0;
+    do {
+        uint64_t w[C][RK / 2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t n = n0 + c * kUpThreads;
-        bias[c] = p.bias && n < p.N ? p.bias[n] : 0.0f;
-    }
-    for (int i0 = (blockIdx.z % kUpGroups) * kUpTok; i0 < cnt; i0 += kUpGroups * kUpTok) {
-        const int nt = min(kUpTok, cnt - i0);
-        int r0 = 0;
-        do {
-            for (int e = threadIdx.x; e < nt * kUpRank; e += kUpThreads) {
-                const int t = e / kUpRank, r = r0 + e % kUpRank;
-                float v = 0.0f;
-                if (r < R) {
-                    const float* src = p.S + (win * kWindow + list[i0 + t]) * p.R + r;
-                    for (int q = 0; q < p.slices; ++q) v += src[q * p.M * p.R];
-                }
-                s[t][e % kUpRank] = scale * v;
-            }
-            float w[C][kUpRank];
+        for (int c = 0; c < C; ++c) {
+            const int64_t n = n0 + c * kUpThreads;
+            const float* b = p.B + ((int64_t)a * p.N + n) * p.R + r0;
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int64_t n = n0 + c * kUpThreads;
-                const float* b = p.B + ((int64_t)a * p.N + n) * p.R + r0;
-#pragma unroll
-                for (int r = 0; r < kUpRank; ++r) w[c][r] = n < p.N && r0 + r < R ? b[r] : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll 2
-            for (int t = 0; t < nt; ++t) {
-                float* y = p.Y + (win * kWindow + list[i0 + t]) * p.ldy + n0;
-                float v[C];
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    v[c] = r0 == 0 ? bias[c] : n0 + c * kUpThreads < p.N ? y[c * kUpThreads] : 0.0f;
-#pragma unroll
-                for (int r = 0; r < kUpRank; r += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(&s[t][r]);
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        v[c] = fmaf(w[c][r], x.x, v[c]);
-                        v[c] = fmaf(w[c][r + 1], x.y, v[c]);
-                        v[c] = fmaf(w[c][r + 2], x.z, v[c]);
-                        v[c] = fmaf(w[c][r + 3], x.w, v[c]);
+            for (int r = 0; r < RK; r += V) {
+                float x[V] = {};
+                if (n < p.N && r0 + r < R) {
+                    if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(b + r);
+                    else {
+                        x[0] = b[r];
+                        if (r0 + r + 1 < R) x[1] = b[r + 1];
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (n0 + c * kUpThreads < p.N) y[c * kUpThreads] = v[c];
+                for (int v = 0; v < V; v += 2)
+                    w[c][(r + v) / 2] = pack_f32x2(__float_as_uint(x[v]), __float_as_uint(x[v + 1]));
             }
-            __syncthreads();
-            r0 += kUpRank;
-        } while (r0 < R);
+        }
+        for (int e = threadIdx.x; e < nt * RK; e += kUpThreads) {
+            const int t = e / RK, r = r0 + e % RK;
+            float v = 0.0f;
+            if (r < R) {
+                const float* src = p.S + (list ? list[t] : t0 + t) * p.R + r;
+                for (int q = 0; q < p.slices; ++q) v += src[q * p.M * p.R];
+            }
+            s[t][e % RK] = scale * v;
+        }
+        float bias[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t n = n0 + c * kUpThreads;
+            bias[c] = p.bias && n < p.N ? p.bias[n] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < nt; ++t) {
+            float* y = p.Y + (list ? list[t] : t0 + t) * p.ldy + n0;
+            uint64_t v[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                v[c] = pack_f32x2(__float_as_uint(r0 == 0 ? bias[c]
+                                                  : n0 + c * kUpThreads < p.N ? y[c * kUpThreads] : 0.0f), 0u);
+#pragma unroll
+            for (int r = 0; r < RK; r += 4) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&s[t][r]);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    v[c] = fma_f32x2(w[c][r / 2], x.x, v[c]);
+                    v[c] = fma_f32x2(w[c][r / 2 + 1], x.y, v[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (n0 + c * kUpThreads < p.N)
+                    y[c * kUpThreads] = __uint_as_float(uint32_t(v[c])) + __uint_as_float(uint32_t(v[c] >> 32));
+        }
+        __syncthreads();
+        r0 += RK;
+    } while (r0 < R);
+}
+
+// Few tokens: four neighbouring ones per block, runs of one adapter together.
+template <int V>
+__global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
+    __shared__ __align__(16) float s[kDotTok][32];
+    const int64_t t0 = (int64_t)blockIdx.x * kDotTok, end = min(p.M, t0 + kDotTok);
+    const int64_t n0 = (int64_t)blockIdx.y * kUpThreads + threadIdx.x;
+    for (int64_t t = t0; t < end;) {
+        const int a = adapter_of(p, t);
+        int nt = 1;
+        while (t + nt < end && adapter_of(p, t + nt) == a) ++nt;
+        up_tokens<1, 32, V>(p, a, nullptr, t, nt, n0, s);
+        t += nt;
     }
 }
 
-// Up to this many tokens take the dots: a tile's 64 tokens would mostly be
-// empty, and what counts is reading each adapter's rows from many SMs at once.
-constexpr int64_t kDotTokens = 256;
+// Many tokens: a tile per block.
+template <int V>
+__global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p) {
+    __shared__ __align__(16) float s[kTileTok][16];
+    if ((int)blockIdx.x >= *p.ntiles) return;
+    const int4 tile = p.tiles[blockIdx.x];
+    up_tokens<4, 16, V>(p, tile.x, p.order + tile.y, 0, tile.z,
+                        (int64_t)blockIdx.y * (4 * kUpThreads) + threadIdx.x, s);
+}
+
+// Tiles that the grouping makes at most.
+int64_t max_tiles(int64_t M, int64_t adapters) {
+    return M / kTileTok + (M < adapters + 1 ? M : adapters + 1);
+}
 
 template <int V>
-cudaError_t launch_down(const LoraParams& p, unsigned windows, cudaStream_t stream) {
-    if (p.M <= kDotTokens) {
-        lora_down_dots<V><<<dim3(p.adapters, windows, p.slices), kDotWarps * 32, 0, stream>>>(p);
+cudaError_t launch_down(const LoraParams& p, cudaStream_t stream) {
+    if (p.M <= kFewTokens) {
+        const unsigned rows = (p.R + kDotWarps * kDotRows - 1) / (kDotWarps * kDotRows);
+        lora_down_dots<V><<<dim3((unsigned)((p.M + kDotTok - 1) / kDotTok), rows, p.slices),
+                            kDotWarps * 32, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    const dim3 grid(p.adapters, windows, p.slices * kTileGroups);
+    const dim3 grid((unsigned)max_tiles(p.M, p.adapters), p.slices);
     // rows of A per stage: as the rank needs, at most 64
     auto go = [&](auto kern, int smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -353,11 +428,12 @@ cudaError_t launch_down(const LoraParams& p, unsigned windows, cudaStream_t stre
     return go(lora_down_tiles<V, 4>, tile_smem(4));
 }
 
-// Slices of K: enough blocks for every SM to have two, slices of at least 256
-// values, at most 16 (the up step reads each).
-int64_t slices_of(int64_t M, int64_t K, int64_t adapters, int sms) {
-    const int64_t tiles = M <= kDotTokens ? (M < adapters ? M : adapters) : (M + kTileTok - 1) / kTileTok;
-    int64_t n = (2 * sms + tiles - 1) / tiles;
+// Slices of K: enough blocks for every SM to have two (of the dots, which are
+// bound by latency, four), slices of at least 256 values, at most 16 (the up
+// step reads each).
+int64_t slices_of(int64_t M, int64_t K, int64_t R, int sms) {
+    const int64_t blocks = M <= kFewTokens ? (M + kDotTok - 1) / kDotTok * ((R + 15) / 16) : M / kTileTok;
+    int64_t n = ((M <= kFewTokens ? 4 : 2) * sms + blocks - 1) / blocks;
     n = n > 16 ? 16 : n;
     const int64_t most = (K + 255) / 256;
     return n < most ? n : most;
@@ -377,8 +453,8 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
                                  int64_t ldy, emu_stream_t stream_) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (M < 0 || N < 0 || K < 0 || R < 0 || adapters < 0) return EMU_ERR_INVALID_VALUE;
-    if (M > 32768 * (int64_t)kWindow || N > 65535 / kUpGroups * (int64_t)kUpThreads || K > INT32_MAX - 64 ||
-        R > 65536 || adapters > (1 << 20))
+    if (M > INT32_MAX || N > 65535 * (int64_t)kUpThreads || K > INT32_MAX - 64 || R > 65536 ||
+        adapters > kMaxAdapters)
         return EMU_ERR_INVALID_VALUE;
     if (ldx < 1 || ldx < K || ldy < 1 || ldy < N || (W && (ldw < 1 || ldw < K)))
         return EMU_ERR_INVALID_VALUE;
@@ -394,9 +470,15 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
     emu_status_t st = current_device(&d);
     if (st != EMU_OK) return st;
     const int64_t ldp = plane_ld(K);
-    const int64_t slices = adapted ? slices_of(M, K, adapters, d->sms) : 0;
-    const size_t xp_bytes = ((size_t)6 * M * ldp + 1023) / 1024 * 1024;
-    st = ensure_buffer(&d->ws, &d->ws_bytes, xp_bytes + (adapted ? (size_t)slices * M * R * 4 : 0));
+    const int64_t slices = adapted ? slices_of(M, K, R, d->sms) : 0;
+    // workspace: X's pieces, S's slices, and the grouping
+    const bool few = M <= kFewTokens;
+    auto up16 = [](size_t b) { return (b + 1023) / 1024 * 1024; };
+    const size_t xp_bytes = up16((size_t)6 * M * ldp);
+    const size_t s_bytes = up16((size_t)slices * M * R * 4);
+    const size_t o_bytes = few ? 0 : up16((size_t)M * 4);
+    const size_t t_bytes = few ? 0 : (size_t)max_tiles(M, adapters) * sizeof(int4) + 16;
+    st = ensure_buffer(&d->ws, &d->ws_bytes, xp_bytes + s_bytes + o_bytes + t_bytes);
     if (st != EMU_OK) return st;
     LoraParams p = {};
     p.M = M; p.N = N; p.K = K;
@@ -404,23 +486,36 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
     p.adapters = adapted ? (int)adapters : 0;
     p.X = X; p.ldx = ldx; p.A = A; p.B = B; p.scale = scale; p.bias = bias;
     p.index = adapted ? index : nullptr;
-    p.S = reinterpret_cast<float*>(static_cast<uint8_t*>(d->ws) + xp_bytes);
+    uint8_t* ws = static_cast<uint8_t*>(d->ws) + xp_bytes;
+    p.S = reinterpret_cast<float*>(ws);
+    p.order = reinterpret_cast<int32_t*>(ws + s_bytes);
+    p.ntiles = reinterpret_cast<int32_t*>(ws + s_bytes + o_bytes);
+    p.tiles = reinterpret_cast<int4*>(ws + s_bytes + o_bytes + 16);
     p.Y = Y; p.ldy = ldy; p.err = d->err;
-    const unsigned windows = (unsigned)((M + kWindow - 1) / kWindow);
     cudaError_t e = cudaSuccess;
+    if (!few) {
+        lora_group<<<1, 1024, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return from_cuda(e);
+    }
     if (adapted) {
         p.slices = (int)slices;
         p.slice = ((K + slices - 1) / slices + 63) / 64 * 64;
-        e = K % 4 == 0 && ldx % 4 == 0 && aligned16(X) && aligned16(A) ? launch_down<4>(p, windows, stream)
-                                                                      : launch_down<1>(p, windows, stream);
+        e = K % 4 == 0 && ldx % 4 == 0 && aligned16(X) && aligned16(A) ? launch_down<4>(p, stream)
+                                                                      : launch_down<1>(p, stream);
         if (e != cudaSuccess) return from_cuda(e);
     }
-    // columns per thread: four where there are tokens to share them
-    const int cols = M <= kDotTokens ? 1 : 4;
-    const dim3 up((unsigned)p.adapters + 1, windows,
-                  (unsigned)((N + cols * kUpThreads - 1) / (cols * kUpThreads)) * kUpGroups);
-    if (cols == 1) lora_up<1><<<up, kUpThreads, 0, stream>>>(p);
-    else lora_up<4><<<up, kUpThreads, 0, stream>>>(p);
+    const bool wide = R % 4 == 0 && aligned16(B);
+    if (few) {
+        const dim3 grid((unsigned)((M + kDotTok - 1) / kDotTok), (unsigned)((N + kUpThreads - 1) / kUpThreads));
+        if (wide) lora_up_few<4><<<grid, kUpThreads, 0, stream>>>(p);
+        else lora_up_few<2><<<grid, kUpThreads, 0, stream>>>(p);
+    } else {
+        const dim3 grid((unsigned)max_tiles(M, p.adapters),
+                        (unsigned)((N + 4 * kUpThreads - 1) / (4 * kUpThreads)));
+        if (wide) lora_up_tiles<4><<<grid, kUpThreads, 0, stream>>>(p);
+        else lora_up_tiles<2><<<grid, kUpThreads, 0, stream>>>(p);
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess || K == 0) return from_cuda(e);
     e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);

@@ -111,7 +111,7 @@ emu_status_t emu_gated_bwd(int act, int64_t M, int64_t F, int64_t K, const float
  *                of N rows x ldwp, ldwp >= K and a multiple of 8.
  *  W, ldw        W itself or NULL, as in emu_gated.
  *  bias          N values or NULL.
- *  R, adapters   rank and number of adapters (an adapter of a lower rank has
+ *  R, adapters   rank and number of adapters, at most 8191 (an adapter of a lower rank has
  *                zeros in its last rows of A, columns of B); R == 0 or
  *                adapters == 0 runs the projection alone.
  *  A, B          adapters x R x K and adapters x N x R, contiguous.
