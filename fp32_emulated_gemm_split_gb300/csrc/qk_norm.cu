@@ -431,12 +431,13 @@ using namespace emu;
 extern "C" {
 
 emu_status_t emu_qk_norm_rope(int dtype, int64_t T, int64_t D, int64_t rot, int interleaved,
-                              float eps, emu_heads_t q, emu_heads_t k, const float* wq,
+                              float eps, const emu_heads_t* heads, const float* wq,
                               const float* wk, const float* cos, const float* sin,
-                              int64_t table_rows, const int32_t* positions, emu_heads_t q_out,
-                              emu_heads_t k_out, emu_stream_t stream) {
-    emu_status_t st = check_qk(dtype, T, D, rot, interleaved, eps, q, k, q_out, k_out, cos, sin,
-                               table_rows, positions);
+                              int64_t table_rows, const int32_t* positions, emu_stream_t stream) {
+    if (!heads) return EMU_ERR_INVALID_VALUE;
+    const emu_heads_t &q = heads[0], &k = heads[1];
+    emu_status_t st = check_qk(dtype, T, D, rot, interleaved, eps, q, k, heads[2], heads[3], cos,
+                               sin, table_rows, positions);
     if (st != EMU_OK) return st;
     if (T == 0 || q.heads + k.heads == 0) return EMU_OK;
     std::lock_guard<std::mutex> lock(g_mu);
@@ -444,8 +445,8 @@ emu_status_t emu_qk_norm_rope(int dtype, int64_t T, int64_t D, int64_t rot, int 
     st = current_device(&d);
     if (st != EMU_OK) return st;
     QkParams p = {};
-    p.side[0] = make_side(q, q_out, wq, nullptr);
-    p.side[1] = make_side(k, k_out, wk, nullptr);
+    p.side[0] = make_side(q, heads[2], wq, nullptr);
+    p.side[1] = make_side(k, heads[3], wk, nullptr);
     p.T = T; p.D = (int)D; p.rot = (int)rot; p.eps = eps;
     p.cos = cos; p.sin = sin; p.table_rows = table_rows; p.positions = positions;
     p.err = d->err;
@@ -455,16 +456,18 @@ emu_status_t emu_qk_norm_rope(int dtype, int64_t T, int64_t D, int64_t rot, int 
 }
 
 emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, int interleaved,
-                                  float eps, emu_heads_t dq_out, emu_heads_t dk_out, emu_heads_t q,
-                                  emu_heads_t k, const float* wq, const float* wk,
-                                  const float* cos, const float* sin, int64_t table_rows,
-                                  const int32_t* positions, emu_heads_t dq, emu_heads_t dk,
-                                  float* dwq, float* dwk, emu_stream_t stream_) {
+                                  float eps, const emu_heads_t* heads, const float* wq,
+                                  const float* wk, const float* cos, const float* sin,
+                                  int64_t table_rows, const int32_t* positions, float* dwq,
+                                  float* dwk, emu_stream_t stream_) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    emu_status_t st = check_qk(dtype, T, D, rot, interleaved, eps, q, k, dq, dk, cos, sin,
-                               table_rows, positions);
+    if (!heads) return EMU_ERR_INVALID_VALUE;
+    const emu_heads_t &q = heads[0], &k = heads[1];
+    emu_status_t st = check_qk(dtype, T, D, rot, interleaved, eps, q, k, heads[2], heads[3], cos,
+                               sin, table_rows, positions);
     if (st != EMU_OK) return st;
-    if (!heads_ok(dq_out, T) || !heads_ok(dk_out, T) || dq_out.heads != q.heads || dk_out.heads != k.heads)
+    if (!heads_ok(heads[4], T) || !heads_ok(heads[5], T) || heads[4].heads != q.heads ||
+        heads[5].heads != k.heads)
         return EMU_ERR_INVALID_VALUE;
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState* d = nullptr;
@@ -474,8 +477,8 @@ emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, 
     st = ensure_buffer(&d->ws, &d->ws_bytes, (size_t)max_blocks * 2 * D * sizeof(float));
     if (st != EMU_OK) return st;
     QkParams p = {};
-    p.side[0] = make_side(q, dq, wq, &dq_out);
-    p.side[1] = make_side(k, dk, wk, &dk_out);
+    p.side[0] = make_side(q, heads[2], wq, &heads[4]);
+    p.side[1] = make_side(k, heads[3], wk, &heads[5]);
     p.T = T; p.D = (int)D; p.rot = (int)rot; p.eps = eps;
     p.cos = cos; p.sin = sin; p.table_rows = table_rows; p.positions = positions;
     p.partial = static_cast<float*>(d->ws);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -18,12 +19,9 @@ from . import _check, _i64, _int, _f32, _vp, _stored, emu_split_b, lib
 
 ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_F32 = torch.float32
 
 _ready = None
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("heads", _i64), ("token_stride", _i64), ("head_stride", _i64)]
 
 
 def _L():
@@ -39,10 +37,9 @@ def _L():
                                     _i64, _vp, _i64, _vp, _i64, _vp]
         L.emu_lora.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
                                _vp, _vp, _vp, _vp, _vp, _i64, _vp]
-        qk = [_int, _i64, _i64, _i64, _int, _f32]
-        tables = [_vp, _vp, _vp, _vp, _i64, _vp]
-        L.emu_qk_norm_rope.argtypes = qk + [_Heads] * 2 + tables + [_Heads] * 2 + [_vp]
-        L.emu_qk_norm_rope_bwd.argtypes = qk + [_Heads] * 4 + tables + [_Heads] * 2 + [_vp] * 3
+        qk = [_int, _i64, _i64, _i64, _int, _f32, ctypes.c_char_p, _vp, _vp, _vp, _vp, _i64, _vp]
+        L.emu_qk_norm_rope.argtypes = qk + [_vp]
+        L.emu_qk_norm_rope_bwd.argtypes = qk + [_vp, _vp, _vp]
         for f in (L.emu_gated_pack, L.emu_gated, L.emu_gated_bwd, L.emu_lora, L.emu_qk_norm_rope,
                   L.emu_qk_norm_rope_bwd):
             f.restype = _int
@@ -50,49 +47,72 @@ def _L():
     return _ready
 
 
+# A call for a few tokens takes the GPU 10 to 30 us, so the wrappers count:
+# each tensor's shape and strides are read once and compared as tuples, and the
+# stream's handle comes without making a Stream object.
+
+_NONE = contextlib.nullcontext()
+
+
 def _on(stream):
     """Outputs and work of a call belong to `stream` (None: the current one)."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NONE if stream is None else torch.cuda.stream(stream)
 
 
-def _handle():
-    return torch.cuda.current_stream().cuda_stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _here(*tensors):
+def _handle(dev):
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _device(X, *tensors):
+    """The index of the current device, which holds every tensor of the call."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+    for t in (X, *tensors):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"expected tensors on the current CUDA device (cuda:{dev}), got {t.device}")
+    return dev
 
 
 def _rows(X, name, rows=None, cols=None):
     """Row stride of a 2-D float32 matrix with unit stride along its rows."""
-    if X.dtype != torch.float32:
+    if X.dtype is not _F32:
         raise TypeError(f"{name} must be float32, got {X.dtype}")
-    if X.dim() != 2 or (rows is not None and X.size(0) != rows) or (cols is not None and X.size(1) != cols):
+    shape = X.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name} must be {'M' if rows is None else rows} x {'K' if cols is None else cols}, "
-                         f"got {tuple(X.shape)}")
-    if X.size(1) > 1 and X.stride(1) != 1:
+                         f"got {tuple(shape)}")
+    ld, unit = X.stride()
+    r, c = shape
+    if unit != 1 and c > 1:
         raise ValueError(f"{name} needs unit stride along its rows")
-    ld = X.stride(0) if X.size(0) > 1 else X.size(1)
-    if ld < X.size(1):
+    if r <= 1:
+        return c if c > 0 else 1
+    if ld < c:
         raise ValueError(f"{name}'s rows overlap")
-    return max(ld, 1)
+    return ld if ld > 0 else 1
 
 
 def _vector(x, name, n):
     if x is None:
         return None
-    if x.dtype != torch.float32 or x.dim() != 1 or x.numel() != n or (n > 1 and x.stride(0) != 1):
+    if x.dtype is not _F32 or x.shape != (n,) or (n > 1 and x.stride(0) != 1):
         raise ValueError(f"{name} must be {n} contiguous float32 values")
     return x.data_ptr()
 
 
+def _indices(x, name, n):
+    if x is None or x.dtype is not torch.int32 or x.shape != (n,) or (n > 1 and x.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous int32 values")
+    return x.data_ptr()
+
+
 def _act(act):
-    if act not in ACT:
+    a = ACT.get(act)
+    if a is None:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACT)}")
-    return ACT[act]
+    return a
 
 
 # ----------------------------------------------------- gated feed-forward --
@@ -102,12 +122,15 @@ class GatedWeights:
     pieces (``emu_gated_pack``).  The pieces hold the values that the weights
     had then: pack again after changing them."""
 
-    __slots__ = ("Wg", "Wu", "pieces", "F", "K", "ldg", "ldu", "ldp", "rows")
+    __slots__ = ("Wg", "Wu", "pieces", "F", "K", "rows", "device", "_weights", "_pieces")
 
     def __init__(self, Wg, Wu, pieces, ldg, ldu, rows):
-        self.Wg, self.Wu, self.pieces = Wg, Wu, pieces
+        self.Wg, self.Wu, self.pieces, self.rows = Wg, Wu, pieces, rows
         self.F, self.K = Wg.shape
-        self.ldg, self.ldu, self.ldp, self.rows = ldg, ldu, pieces.size(2), rows
+        self.device = Wg.get_device()
+        # the entry points' arguments (the tensors above keep the memory)
+        self._weights = (Wg.data_ptr(), ldg, Wu.data_ptr(), ldu)
+        self._pieces = (pieces.data_ptr(), pieces.size(2))
 
 
 def emu_gated_pack(Wg, Wu, stream=None) -> GatedWeights:
@@ -116,12 +139,12 @@ def emu_gated_pack(Wg, Wu, stream=None) -> GatedWeights:
     ldg = _rows(Wg, "Wg")
     F, K = Wg.shape
     ldu = _rows(Wu, "Wu", F, K)
-    _here(Wg, Wu)
+    dev = _device(Wg, Wu)
     rows = _L().emu_gated_rows(F)
     with _on(stream):
         P = torch.empty((3, 2 * rows, max((K + 63) // 64 * 64, 64)), dtype=torch.int16, device=Wg.device)
         _check(_L().emu_gated_pack(F, K, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, P.data_ptr(), P.size(2),
-                                   _handle()), "emu_gated_pack")
+                                   _handle(dev)), "emu_gated_pack")
     return GatedWeights(Wg, Wu, P, ldg, ldu, rows)
 
 
@@ -129,23 +152,25 @@ def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None, stream=None)
     """H = act(X Wg^T) * (X Wu^T), or (H, G, U) with save=True: the two
     products as well, for ``emu_gated_bwd``."""
     a = _act(act)
-    ldx = _rows(X, "X", cols=w.K)
-    M = X.size(0)
-    _here(X, w.Wg, out)
+    F, K = w.F, w.K
+    ldx = _rows(X, "X", None, K)
+    M = X.shape[0]
+    dev = _device(X, w.Wg, out)
     with _on(stream):
-        H = torch.empty((M, w.F), dtype=torch.float32, device=X.device) if out is None else out
-        ldh = _rows(H, "out", M, w.F)
-        G = U = None
+        if out is None:
+            H, ldh = torch.empty((M, F), dtype=_F32, device=X.device), F if F > 0 else 1
+        else:
+            H, ldh = out, _rows(out, "out", M, F)
+        G = U = pG = pU = None
         ldg = 0
         if save:
             # rows of whole 16-byte groups, so that they can be stored and read as such
-            ldg = max((w.F + 3) // 4 * 4, 4)
-            GU = torch.empty((2, M, ldg), dtype=torch.float32, device=X.device)
-            G, U = GU[0, :, :w.F], GU[1, :, :w.F]
-        _check(_L().emu_gated(a, M, w.F, w.K, X.data_ptr(), ldx, w.Wg.data_ptr(), w.ldg, w.Wu.data_ptr(),
-                              w.ldu, w.pieces.data_ptr(), w.ldp, H.data_ptr(), ldh,
-                              G.data_ptr() if save else None, U.data_ptr() if save else None, ldg,
-                              _handle()), "emu_gated")
+            ldg = max((F + 3) // 4 * 4, 4)
+            GU = torch.empty((2, M, ldg), dtype=_F32, device=X.device)
+            G, U = GU[0, :, :F], GU[1, :, :F]
+            pG, pU = G.data_ptr(), U.data_ptr()
+        _check(_L().emu_gated(a, M, F, K, X.data_ptr(), ldx, *w._weights, *w._pieces, H.data_ptr(), ldh,
+                              pG, pU, ldg, _handle(dev)), "emu_gated")
     return (H, G, U) if save else H
 
 
@@ -158,14 +183,14 @@ def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_d
     ldg = _rows(G, "G", M, F)
     if _rows(U, "U", M, F) != ldg:
         raise ValueError("G and U need the same row stride")
-    _here(dH, X, G, U, w.Wg)
+    dev = _device(dH, X, G, U, w.Wg)
     with _on(stream):
-        dX = torch.empty((M, K), dtype=torch.float32, device=X.device) if need_dx else None
-        dW = torch.empty((2 * w.rows, K), dtype=torch.float32, device=X.device) if need_dw else None
-        _check(_L().emu_gated_bwd(a, M, F, K, dH.data_ptr(), lddh, X.data_ptr(), ldx,
-                                  w.pieces.data_ptr(), w.ldp, G.data_ptr(), U.data_ptr(), ldg,
+        dX = torch.empty((M, K), dtype=_F32, device=X.device) if need_dx else None
+        dW = torch.empty((2 * w.rows, K), dtype=_F32, device=X.device) if need_dw else None
+        _check(_L().emu_gated_bwd(a, M, F, K, dH.data_ptr(), lddh, X.data_ptr(), ldx, *w._pieces,
+                                  G.data_ptr(), U.data_ptr(), ldg,
                                   dX.data_ptr() if need_dx else None, max(K, 1),
-                                  dW.data_ptr() if need_dw else None, max(K, 1), _handle()),
+                                  dW.data_ptr() if need_dw else None, max(K, 1), _handle(dev)),
                "emu_gated_bwd")
     return dX, dW[:F] if need_dw else None, dW[w.rows:w.rows + F] if need_dw else None
 
@@ -176,12 +201,14 @@ class LoraWeights:
     """The weight (N x K) and bias of a shared projection with the weight's
     pieces (``emu_lora_pack``); pack again after changing the weight."""
 
-    __slots__ = ("W", "bias", "pieces", "N", "K", "ldw", "ldp")
+    __slots__ = ("W", "bias", "pieces", "N", "K", "_weight")
 
     def __init__(self, W, bias, pieces, ldw):
-        self.W, self.bias, self.pieces, self.ldw = W, bias, pieces, ldw
+        self.W, self.bias, self.pieces = W, bias, pieces
         self.N, self.K = W.shape
-        self.ldp = pieces.size(2)
+        # the entry point's arguments (the tensors above keep the memory)
+        self._weight = (W.data_ptr(), ldw, pieces.data_ptr(), pieces.size(2),
+                        None if bias is None else bias.data_ptr())
 
 
 def emu_lora_pack(W, bias=None, stream=None) -> LoraWeights:
@@ -190,7 +217,7 @@ def emu_lora_pack(W, bias=None, stream=None) -> LoraWeights:
     bias = None if bias is None else bias.detach()
     ldw = _rows(W, "W")
     _vector(bias, "bias", W.size(0))
-    _here(W, bias)
+    _device(W, bias)
     with _on(stream):
         P = emu_split_b(W, transB=True)
     return LoraWeights(W, bias, P, ldw)
@@ -200,67 +227,77 @@ def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None, stream=None):
     """Y = X W^T + bias + scale_i (X A_i^T) B_i^T with i = index[row] (-1: no
     adapter); A is adapters x R x K, B adapters x N x R, scale `adapters`
     values, index int32."""
-    ldx = _rows(X, "X", cols=w.K)
-    M = X.size(0)
-    if A.dtype != torch.float32 or B.dtype != torch.float32:
+    N, K = w.N, w.K
+    ldx = _rows(X, "X", None, K)
+    M = X.shape[0]
+    if A.dtype is not _F32 or B.dtype is not _F32:
         raise TypeError("A and B must be float32")
-    if A.dim() != 3 or B.dim() != 3 or A.size(2) != w.K or B.size(1) != w.N or A.size(0) != B.size(0) \
-            or A.size(1) != B.size(2):
-        raise ValueError(f"A must be adapters x R x {w.K} and B adapters x {w.N} x R, "
+    shape = A.shape
+    if len(shape) != 3 or shape[2] != K or B.shape != (shape[0], N, shape[1]):
+        raise ValueError(f"A must be adapters x R x {K} and B adapters x {N} x R, "
                          f"got {tuple(A.shape)} and {tuple(B.shape)}")
     if not A.is_contiguous() or not B.is_contiguous():
         raise ValueError("A and B must be contiguous")
-    n, R = A.size(0), A.size(1)
-    if index.dtype != torch.int32 or index.dim() != 1 or index.numel() != M or (M > 1 and index.stride(0) != 1):
-        raise ValueError(f"index must be {M} contiguous int32 values")
+    n, R = shape[0], shape[1]
+    ip = _indices(index, "index", M)
     sp = _vector(scale, "scale", n)
-    _here(X, w.W, A, B, index, scale, out)
+    dev = _device(X, w.W, A, B, index, scale, out)
     with _on(stream):
-        Y = torch.empty((M, w.N), dtype=torch.float32, device=X.device) if out is None else out
-        ldy = _rows(Y, "out", M, w.N)
-        _check(_L().emu_lora(M, w.N, w.K, X.data_ptr(), ldx, w.W.data_ptr(), w.ldw, w.pieces.data_ptr(),
-                             w.ldp, None if w.bias is None else w.bias.data_ptr(), R, n, A.data_ptr(),
-                             B.data_ptr(), sp, index.data_ptr(), Y.data_ptr(), ldy, _handle()), "emu_lora")
+        if out is None:
+            Y, ldy = torch.empty((M, N), dtype=_F32, device=X.device), N if N > 0 else 1
+        else:
+            Y, ldy = out, _rows(out, "out", M, N)
+        _check(_L().emu_lora(M, N, K, X.data_ptr(), ldx, *w._weight, R, n, A.data_ptr(), B.data_ptr(), sp, ip,
+                             Y.data_ptr(), ldy, _handle(dev)), "emu_lora")
     return Y
 
 
 # --------------------------------- norm and rotation of queries and keys --
 
-def _heads(x, name, like=None):
-    if x.dim() != 3 or (like is not None and x.shape != like.shape):
+_4_heads, _6_heads = struct.Struct("4q4q4q4q"), struct.Struct("4q4q4q4q4q4q")      # emu_heads_t each
+
+
+def _heads(x, name, shape=None):
+    """The emu_heads_t of a tokens x heads x D tensor."""
+    sh = x.shape
+    if len(sh) != 3 or (shape is not None and sh != shape):
         raise ValueError(f"{name} must be tokens x heads x D"
-                         + (f" = {tuple(like.shape)}" if like is not None else "") + f", got {tuple(x.shape)}")
-    if x.size(2) > 1 and x.stride(2) != 1:
+                         + (f" = {tuple(shape)}" if shape is not None else "") + f", got {tuple(sh)}")
+    st, sh_, unit = x.stride()
+    if unit != 1 and sh[2] > 1:
         raise ValueError(f"{name} needs unit stride along the values of a head")
-    return _Heads(x.data_ptr(), x.size(1), x.stride(0), x.stride(1))
+    return x.data_ptr(), sh[1], st, sh_
 
 
-def _qk_args(q, k, wq, wk, cos, sin, positions, rest):
-    if q.dtype not in DTYPE:
+def _qk_args(q, k, wq, wk, cos, sin, positions):
+    """Checks of both directions: (dtype, T, D, rot), q and k as emu_heads_t,
+    and the weights' and tables' arguments."""
+    dt = DTYPE.get(q.dtype)
+    if dt is None:
         raise TypeError(f"q and k must be float32, bfloat16 or float16, got {q.dtype}")
-    for t in (k, *rest):
-        if t.dtype != q.dtype:
-            raise TypeError(f"expected tensors of one type, got {q.dtype} and {t.dtype}")
+    if k.dtype is not q.dtype:
+        raise TypeError(f"expected tensors of one type, got {q.dtype} and {k.dtype}")
     hq, hk = _heads(q, "q"), _heads(k, "k")
     T, _, D = q.shape
-    if k.size(0) != T or k.size(2) != D:
+    if k.shape[0] != T or k.shape[2] != D:
         raise ValueError(f"q and k differ in tokens or head size: {tuple(q.shape)}, {tuple(k.shape)}")
+    pq, pk = _vector(wq, "wq", D), _vector(wk, "wk", D)
     if cos is None:
         if sin is not None:
             raise ValueError("cos and sin go together")
-        rot, rows, tables = 0, 0, (None, None, 0, None)
-    else:
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
-            raise TypeError("cos and sin must be float32")
-        if cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
-            raise ValueError("cos and sin must be contiguous matrices of one shape, positions x rot/2")
-        rows, rot = cos.size(0), 2 * cos.size(1)
-        if positions is None or positions.dtype != torch.int32 or positions.dim() != 1 \
-                or positions.numel() != T or (T > 1 and positions.stride(0) != 1):
-            raise ValueError(f"positions must be {T} contiguous int32 values")
-        tables = (cos.data_ptr(), sin.data_ptr(), rows, positions.data_ptr())
-    _here(q, k, wq, wk, cos, sin, positions, *rest)
-    return T, D, rot, hq, hk, (_vector(wq, "wq", D), _vector(wk, "wk", D)) + tables
+        return (dt, T, D, 0), hq, hk, (pq, pk, None, None, 0, None)
+    if cos.dtype is not _F32 or sin.dtype is not _F32:
+        raise TypeError("cos and sin must be float32")
+    shape = cos.shape
+    if len(shape) != 2 or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous matrices of one shape, positions x rot/2")
+    return (dt, T, D, 2 * shape[1]), hq, hk, (pq, pk, cos.data_ptr(), sin.data_ptr(), shape[0],
+                                              _indices(positions, "positions", T))
+
+
+def _same_type(q, a, b):
+    if a.dtype is not q.dtype or b.dtype is not q.dtype:
+        raise TypeError(f"expected tensors of one type, got {q.dtype}, {a.dtype} and {b.dtype}")
 
 
 def emu_qk_norm_rope(q, k, wq, wk, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, out=None,
@@ -269,12 +306,18 @@ def emu_qk_norm_rope(q, k, wq, wk, cos=None, sin=None, positions=None, eps=1e-6,
     strides) times wq / wk (None: ones), and the rotation of its first
     2 * cos.size(1) values by the tables' row positions[token]; returns
     (q', k').  out=(q, k) writes in place."""
-    T, D, rot, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions, out or ())
+    size, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions)
     with _on(stream):
-        qo, ko = out if out is not None else (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                                              torch.empty(k.shape, dtype=k.dtype, device=k.device))
-        _check(_L().emu_qk_norm_rope(DTYPE[q.dtype], T, D, rot, int(interleaved), eps, hq, hk, *tables,
-                                     _heads(qo, "out[0]", q), _heads(ko, "out[1]", k), _handle()),
+        if out is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            dev = _device(q, k, wq, wk, cos, sin, positions)
+        else:
+            qo, ko = out
+            _same_type(q, qo, ko)
+            dev = _device(q, k, wq, wk, cos, sin, positions, qo, ko)
+        heads = _4_heads.pack(*hq, *hk, *_heads(qo, "out[0]", q.shape), *_heads(ko, "out[1]", k.shape))
+        _check(_L().emu_qk_norm_rope(*size, 1 if interleaved else 0, eps, heads, *tables, _handle(dev)),
                "emu_qk_norm_rope")
     return qo, ko
 
@@ -283,14 +326,19 @@ def emu_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos=None, sin=None, posit
                          interleaved=False, stream=None):
     """(dq, dk, dwq, dwk) from the gradients of ``emu_qk_norm_rope``'s outputs
     and its inputs; dwq / dwk are None where wq / wk are."""
-    T, D, rot, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions, (dq_out, dk_out))
+    size, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions)
+    _same_type(q, dq_out, dk_out)
+    dev = _device(q, k, wq, wk, cos, sin, positions, dq_out, dk_out)
+    D = size[2]
     with _on(stream):
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
-        _check(_L().emu_qk_norm_rope_bwd(
-            DTYPE[q.dtype], T, D, rot, int(interleaved), eps, _heads(dq_out, "dq_out", q),
-            _heads(dk_out, "dk_out", k), hq, hk, *tables, _heads(dq, "dq"), _heads(dk, "dk"),
-            dw[0].data_ptr() if wq is not None else None, dw[1].data_ptr() if wk is not None else None,
-            _handle()), "emu_qk_norm_rope_bwd")
-    return dq, dk, dw[0] if wq is not None else None, dw[1] if wk is not None else None
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        dw = torch.empty((2, D), dtype=_F32, device=q.device)
+        dwq, dwk = (dw[0] if wq is not None else None), (dw[1] if wk is not None else None)
+        heads = _6_heads.pack(*hq, *hk, *_heads(dq, "dq"), *_heads(dk, "dk"),
+                              *_heads(dq_out, "dq_out", q.shape), *_heads(dk_out, "dk_out", k.shape))
+        _check(_L().emu_qk_norm_rope_bwd(*size, 1 if interleaved else 0, eps, heads, *tables,
+                                         None if dwq is None else dwq.data_ptr(),
+                                         None if dwk is None else dwk.data_ptr(), _handle(dev)),
+               "emu_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk

@@ -152,36 +152,35 @@ typedef struct {
 /*
  * emu_qk_norm_rope
  *
+ *  heads         four of them: q, k, and the outputs q', k'.  Either side may
+ *                have 0 heads.  An output may be its input (same data and
+ *                strides), otherwise it may not overlap one.
  *  dtype         type of q, k and the outputs (an emu_dtype_t)
  *  T, D, rot     tokens, values of a head (1..512), rotated values (even,
  *                0..D).  T == 0 is a no-op.
- *  q, k          either may have 0 heads
  *  wq, wk        D values each (FP32), or NULL for ones
  *  cos, sin      table_rows x rot/2 (FP32, contiguous); rot == 0 reads neither
  *  positions     T values in [0, table_rows); another value gives NaN in that
- *                token's rotated values and records EMU_ERR_INVALID_VALUE in
- *                the device's error word
- *  q_out, k_out  outputs; q_out may be q and k_out k (same data and strides),
- *                otherwise an output may not overlap an input.
+ *                token's rotated values (in the backward pass, in all its
+ *                gradients) and records EMU_ERR_INVALID_VALUE in the device's
+ *                error word
  */
 emu_status_t emu_qk_norm_rope(int dtype, int64_t T, int64_t D, int64_t rot, int interleaved,
-                              float eps, emu_heads_t q, emu_heads_t k, const float* wq,
+                              float eps, const emu_heads_t* heads, const float* wq,
                               const float* wk, const float* cos, const float* sin,
-                              int64_t table_rows, const int32_t* positions, emu_heads_t q_out,
-                              emu_heads_t k_out, emu_stream_t stream);
+                              int64_t table_rows, const int32_t* positions, emu_stream_t stream);
 
 /*
- * emu_qk_norm_rope_bwd -- from the gradients dq_out, dk_out of the outputs
- * and the forward's inputs: dq, dk (the inputs' type) and dwq, dwk (D FP32
- * values each, or NULL).  The weights' gradients are summed over tokens and
- * heads in a fixed order: the same inputs give the same bits.
+ * emu_qk_norm_rope_bwd -- heads: six, q and k as the forward had them, the
+ * gradients dq, dk to write, and the gradients dq', dk' of the outputs.  dwq,
+ * dwk: D FP32 values each, or NULL, summed over tokens and heads in a fixed
+ * order: the same inputs give the same bits.
  */
 emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, int interleaved,
-                                  float eps, emu_heads_t dq_out, emu_heads_t dk_out, emu_heads_t q,
-                                  emu_heads_t k, const float* wq, const float* wk,
-                                  const float* cos, const float* sin, int64_t table_rows,
-                                  const int32_t* positions, emu_heads_t dq, emu_heads_t dk,
-                                  float* dwq, float* dwk, emu_stream_t stream);
+                                  float eps, const emu_heads_t* heads, const float* wq,
+                                  const float* wk, const float* cos, const float* sin,
+                                  int64_t table_rows, const int32_t* positions, float* dwq,
+                                  float* dwk, emu_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,8 @@
 """include/emu_layers.h without a GPU: every bad argument is refused on the
 host before anything is launched, and empty calls do nothing.  The pointers
 are never dereferenced."""
+import struct
+
 import pytest
 
 from fp32_emulated_gemm_split_gb300 import _build
@@ -80,9 +82,8 @@ def test_lora_refuses(layers, kw):
 
 def _qk(L, m, dtype=0, T=3, D=64, rot=64, pairs=0, eps=1e-6, q=(P, 4, 256, 64), k=(P, 2, 128, 64), cos=P, sin=P,
         rows=100, pos=P, qo=(P, 4, 256, 64), ko=(P, 2, 128, 64)):
-    H = m._Heads
-    return L.emu_qk_norm_rope(dtype, T, D, rot, pairs, eps, H(*q), H(*k), None, None, cos, sin, rows, pos, H(*qo),
-                              H(*ko), None)
+    heads = b"".join(struct.pack("4q", h[0] or 0, *h[1:]) for h in (q, k, qo, ko))
+    return L.emu_qk_norm_rope(dtype, T, D, rot, pairs, eps, heads, None, None, cos, sin, rows, pos, None)
 
 
 @pytest.mark.parametrize("kw", [
