@@ -88,26 +88,33 @@ struct Chunk {
     }
 };
 
-// The chunk's 2 V values as x[i] (first elements) and x[V + i] (second).
-// Rotated neighbouring pairs lie as a0 b0 a1 b1 ..: two vectors in a row.
+// The chunk as it lies in memory, and its 2 V values as x[i] (first elements)
+// and x[V + i] (second).  Rotated neighbouring pairs lie as a0 b0 a1 b1 ..: two
+// vectors in a row.
+template <typename T, int V>
+struct Raw {
+    Vec<T, V> a, b;
+};
 template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ void load_chunk(const T* head, const Chunk<V, PAIRS>& ck, float (&x)[2 * V]) {
-    Vec<T, V> a = {}, b = {};
-    if (ck.has_a) a = *reinterpret_cast<const Vec<T, V>*>(head + ck.a);
-    if (ck.has_b) b = *reinterpret_cast<const Vec<T, V>*>(head + ck.b);
+__device__ __forceinline__ Raw<T, V> load_chunk(const T* head, const Chunk<V, PAIRS>& ck, bool in) {
+    Raw<T, V> r = {};
+    if (in && ck.has_a) r.a = *reinterpret_cast<const Vec<T, V>*>(head + ck.a);
+    if (in && ck.has_b) r.b = *reinterpret_cast<const Vec<T, V>*>(head + ck.b);
+    return r;
+}
+template <typename T, int V, bool PAIRS>
+__device__ __forceinline__ void unpack_chunk(const Raw<T, V>& r, const Chunk<V, PAIRS>& ck, float (&x)[2 * V]) {
     if (PAIRS && ck.rotated) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float e0 = to_f32(2 * i < V ? a.v[(2 * i) % V] : b.v[(2 * i) % V]);
-            const float e1 = to_f32(2 * i + 1 < V ? a.v[(2 * i + 1) % V] : b.v[(2 * i + 1) % V]);
-            x[i] = e0;
-            x[V + i] = e1;
+            x[i] = to_f32(2 * i < V ? r.a.v[(2 * i) % V] : r.b.v[(2 * i) % V]);
+            x[V + i] = to_f32(2 * i + 1 < V ? r.a.v[(2 * i + 1) % V] : r.b.v[(2 * i + 1) % V]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = to_f32(a.v[i]);
-            x[V + i] = to_f32(b.v[i]);
+            x[i] = to_f32(r.a.v[i]);
+            x[V + i] = to_f32(r.b.v[i]);
         }
     }
 }
@@ -188,109 +195,120 @@ __device__ __forceinline__ void load_weight(const float* w, const Chunk<V, PAIRS
 
 constexpr int kWarps = 8;                    // per block
 
-// V pairs per chunk, NC chunks per lane.
-template <typename T, int V, int NC, bool PAIRS, bool BWD>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkParams p) {
+// V pairs per chunk, NC chunks per lane, U rounds of heads read ahead of
+// their arithmetic (HBM's latency: each round is 32 bytes per lane and tensor).
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int U>
+__global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_kernel(const QkParams p) {
     extern __shared__ float dw_sum[];                            // backward: [warp][2][D]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / p.lanes, pos_in = lane % p.lanes;   // head of the warp's group, lane in it
     const int at_once = 32 / p.lanes;
-    float dw[BWD ? 2 : 1][BWD ? NC : 1][BWD ? 2 * V : 1];
-    if constexpr (BWD)
-        for (int s = 0; s < 2; ++s)
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i) dw[s][n][i] = 0.0f;
     const int64_t items = p.T * p.segments;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
-         it += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = it / p.segments;
-        const int seg = int(it - t * p.segments);
-        const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
-        const bool pos_ok = pos >= 0 && pos < p.table_rows;
-        if (!pos_ok && p.rot > 0 && lane == 0) record_error(p.err, kDevErrValue);
-        float cs[NC][V], sn[NC][V];
+    const float inv_d = 1.0f / p.D;
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) {
+        const Heads& hd = p.side[s];
+        float w[NC][2 * V], dw[BWD ? NC : 1][BWD ? 2 * V : 1];
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
-            load_turn<V, PAIRS>(p, pos, pos_ok, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), cs[n], sn[n]);
+        for (int n = 0; n < NC; ++n) {
+            load_weight<V, PAIRS>(hd.w, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), w[n]);
+            if constexpr (BWD)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const Heads& hd = p.side[s];
-            float w[NC][2 * V];
+                for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
+        }
+        const int per = (hd.heads + p.segments - 1) / p.segments;
+        for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
+             it += (int64_t)gridDim.x * kWarps) {
+            const int64_t t = it / p.segments;
+            const int seg = int(it - t * p.segments);
+            const int h_end = min(hd.heads, (seg + 1) * per);
+            if (seg * per >= h_end) continue;
+            const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
+            const bool pos_ok = pos >= 0 && pos < p.table_rows;
+            if (!pos_ok && p.rot > 0 && lane == 0) record_error(p.err, kDevErrValue);
+            float cs[NC][V], sn[NC][V];
 #pragma unroll
             for (int n = 0; n < NC; ++n)
-                load_weight<V, PAIRS>(hd.w, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), w[n]);
-            const int per = (hd.heads + p.segments - 1) / p.segments;
-            const int h1 = min(hd.heads, (seg + 1) * per);
+                load_turn<V, PAIRS>(p, pos, pos_ok, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), cs[n], sn[n]);
+            const T* in = static_cast<const T*>(hd.in) + t * hd.in_t;
+            const T* dy = static_cast<const T*>(hd.dy) + t * hd.dy_t;
+            T* out = static_cast<T*>(hd.out) + t * hd.out_t;
             // every lane of the warp runs every round (the sums are shuffles)
-            for (int h0 = seg * per; h0 < h1; h0 += at_once) {
-                const int h = h0 + sub;
-                const bool in = h < h1;
-                float x[NC][2 * V], d[BWD ? NC : 1][BWD ? 2 * V : 1];
-                float ss = 0.0f, sd = 0.0f;
+            for (int h0 = seg * per; h0 < h_end; h0 += U * at_once) {
+                Raw<T, V> rx[U][NC], rd[BWD ? U : 1][BWD ? NC : 1];
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
+                for (int u = 0; u < U; ++u) {
+                    const int h = h0 + u * at_once + sub;
 #pragma unroll
-                    for (int i = 0; i < 2 * V; ++i) x[n][i] = 0.0f;
-                    if (in) load_chunk<T, V, PAIRS>(static_cast<const T*>(hd.in) + t * hd.in_t + h * hd.in_h, ck, x[n]);
-#pragma unroll
-                    for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
-                    if constexpr (BWD) {
-#pragma unroll
-                        for (int i = 0; i < 2 * V; ++i) d[n][i] = 0.0f;
-                        if (in) load_chunk<T, V, PAIRS>(static_cast<const T*>(hd.dy) + t * hd.dy_t + h * hd.dy_h, ck, d[n]);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {            // turned back
-                            const float a = d[n][i], b = d[n][V + i];
-                            d[n][i] = fmaf(a, cs[n][i], b * sn[n][i]);
-                            d[n][V + i] = fmaf(b, cs[n][i], -(a * sn[n][i]));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2 * V; ++i) sd = fmaf(d[n][i] * w[n][i], x[n][i], sd);
+                    for (int n = 0; n < NC; ++n) {
+                        const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
+                        rx[u][n] = load_chunk<T, V, PAIRS>(in + h * hd.in_h, ck, h < h_end);
+                        if constexpr (BWD) rd[u][n] = load_chunk<T, V, PAIRS>(dy + h * hd.dy_h, ck, h < h_end);
                     }
                 }
-                ss = lanes_sum(ss, p.lanes);
-                const float r = rsqrtf(ss / p.D + p.eps);
-                if constexpr (BWD) {
-                    sd = lanes_sum(sd, p.lanes);
-                    const float m = r * r * (sd / p.D);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = h0 + u * at_once + sub;
+                    float x[NC][2 * V], d[BWD ? NC : 1][BWD ? 2 * V : 1];
+                    float ss = 0.0f, sd = 0.0f;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
                         const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
+                        unpack_chunk<T, V, PAIRS>(rx[u][n], ck, x[n]);
 #pragma unroll
-                        for (int i = 0; i < 2 * V; ++i) {
-                            if (in) dw[s][n][i] = fmaf(d[n][i], x[n][i] * r, dw[s][n][i]);
-                            d[n][i] = r * fmaf(d[n][i], w[n][i], -(x[n][i] * m));
+                        for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
+                        if constexpr (BWD) {
+                            unpack_chunk<T, V, PAIRS>(rd[u][n], ck, d[n]);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {        // turned back
+                                const float a = d[n][i], b = d[n][V + i];
+                                d[n][i] = fmaf(a, cs[n][i], b * sn[n][i]);
+                                d[n][V + i] = fmaf(b, cs[n][i], -(a * sn[n][i]));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2 * V; ++i) sd = fmaf(d[n][i] * w[n][i], x[n][i], sd);
                         }
-                        if (in) store_chunk<T, V, PAIRS>(static_cast<T*>(hd.out) + t * hd.out_t + h * hd.out_h, ck, d[n]);
                     }
-                } else {
+                    ss = lanes_sum(ss, p.lanes);
+                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+                    if constexpr (BWD) {
+                        sd = lanes_sum(sd, p.lanes);
+                        const float m = r * r * (sd * inv_d);
+                        const bool live = h < h_end;
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
+                        for (int n = 0; n < NC; ++n) {
+                            const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float a = x[n][i] * r * w[n][i], b = x[n][V + i] * r * w[n][V + i];
-                            x[n][i] = fmaf(a, cs[n][i], -(b * sn[n][i]));
-                            x[n][V + i] = fmaf(b, cs[n][i], a * sn[n][i]);
+                            for (int i = 0; i < 2 * V; ++i) {
+                                if (live) dw[n][i] = fmaf(d[n][i], x[n][i] * r, dw[n][i]);
+                                d[n][i] = r * fmaf(d[n][i], w[n][i], -(x[n][i] * m));
+                            }
+                            if (live) store_chunk<T, V, PAIRS>(out + h * hd.out_h, ck, d[n]);
                         }
-                        if (in) store_chunk<T, V, PAIRS>(static_cast<T*>(hd.out) + t * hd.out_t + h * hd.out_h, ck, x[n]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) {
+                            const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const float a = x[n][i] * r * w[n][i], b = x[n][V + i] * r * w[n][V + i];
+                                x[n][i] = fmaf(a, cs[n][i], -(b * sn[n][i]));
+                                x[n][V + i] = fmaf(b, cs[n][i], a * sn[n][i]);
+                            }
+                            if (h < h_end) store_chunk<T, V, PAIRS>(out + h * hd.out_h, ck, x[n]);
+                        }
                     }
                 }
             }
         }
-    }
-    if constexpr (BWD) {
-        // over the warp's heads, then over the block's warps, in order
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
+        if constexpr (BWD) {
+            // over the warp's heads
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
                 const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
 #pragma unroll
                 for (int i = 0; i < 2 * V; ++i) {
-                    float v = dw[s][n][i];
+                    float v = dw[n][i];
                     for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     const bool second = i >= V;
                     if (sub == 0 && (second ? ck.has_b : ck.has_a)) {
@@ -300,6 +318,10 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkParams p) 
                     }
                 }
             }
+        }
+    }
+    if constexpr (BWD) {
+        // over the block's warps, in order
         __syncthreads();
         for (int e = threadIdx.x; e < 2 * p.D; e += blockDim.x) {
             float v = 0.0f;
@@ -309,33 +331,34 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkParams p) 
     }
 }
 
-// dwq and dwk: the blocks' rows added in order, 32 columns per block, the
-// rows dealt to its warps and the warps' sums added in order.
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_dw(const float* partial, int blocks, int D,
-                                                          float* dwq, float* dwk) {
-    __shared__ float part[kWarps][32];
+// dwq and dwk: 32 columns per block, the first kernel's rows dealt to its 32
+// warps and the warps' sums added in order.
+__global__ void __launch_bounds__(1024) qk_norm_dw(const float* __restrict__ partial, int blocks, int D,
+                                                   float* dwq, float* dwk) {
+    __shared__ float part[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (e < 2 * D)
-        for (int b = warp; b < blocks; b += kWarps) v += partial[(int64_t)b * 2 * D + e];
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += 32) v += partial[(int64_t)b * 2 * D + e];
     part[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && e < 2 * D) {
         v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part[w][lane];
+        for (int w = 0; w < 32; ++w) v += part[w][lane];
         float* dw = e < D ? dwq : dwk;
         if (dw) dw[e < D ? e : e - D] = v;
     }
 }
 
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 2;
 
-template <typename T, int V, int NC, bool PAIRS, bool BWD>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int U>
 cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
     const size_t smem = BWD ? (size_t)kWarps * 2 * p.D * sizeof(float) : 0;
-    qk_norm_kernel<T, V, NC, PAIRS, BWD><<<blocks, kWarps * 32, smem, stream>>>(p);
+    qk_norm_kernel<T, V, NC, PAIRS, BWD, U><<<blocks, kWarps * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -366,12 +389,13 @@ cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t s
     while (p.segments * 2 <= rounds && p.T * p.segments < (int64_t)max_blocks * kWarps) p.segments *= 2;
     const int64_t want = (p.T * p.segments + kWarps - 1) / kWarps;
     *blocks = (int)(want < max_blocks ? want : max_blocks);
+    constexpr int U = BWD ? 2 : 4;
     if (wide) {
-        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD>(p, *blocks, stream);
-        return launch_one<T, V, 2, PAIRS, BWD>(p, *blocks, stream);
+        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, U>(p, *blocks, stream);
+        return launch_one<T, V, 2, PAIRS, BWD, U / 2>(p, *blocks, stream);
     }
-    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD>(p, *blocks, stream);
-    return launch_one<T, 1, 8, PAIRS, BWD>(p, *blocks, stream);
+    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, U>(p, *blocks, stream);
+    return launch_one<T, 1, 8, PAIRS, BWD, 1>(p, *blocks, stream);
 }
 
 template <bool BWD>
@@ -488,7 +512,7 @@ emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, 
     if (T > 0 && q.heads + k.heads > 0)
         e = launch_any<true>(dtype, interleaved != 0, p, max_blocks, &blocks, stream);
     if (e == cudaSuccess && (dwq || dwk)) {
-        qk_norm_dw<<<(unsigned)((2 * D + 31) / 32), kWarps * 32, 0, stream>>>(p.partial, blocks,
+        qk_norm_dw<<<(unsigned)((2 * D + 31) / 32), 1024, 0, stream>>>(p.partial, blocks,
                                                                              (int)D, dwq, dwk);
         e = cudaGetLastError();
     }
