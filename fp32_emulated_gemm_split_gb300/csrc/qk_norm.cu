@@ -8,11 +8,11 @@
 // reads x and dy and writes dx.  Everything else stays in registers, so the
 // layout is made for that: the values of a head are taken as D/2 pairs, the
 // rotated ones (j, j + rot/2) or (2j, 2j + 1), the rest (rot + j, rot + rest/2
-// + j); a lane holds V neighbouring pairs (two 16-byte loads for V = 16 bytes
-// of the type), so a rotation needs no other lane, and D/2/V lanes (rounded
-// up to a power of two, at most a warp) hold a head.  A warp takes one token
-// and a range of its heads, 32 / lanes of them at a time: its cosines, sines
-// and weights are read once and kept in registers.
+// + j); a lane holds V neighbouring pairs (two loads of V values), so a
+// rotation needs no other lane, and D/2/V lanes (rounded up to a power of two,
+// at most a warp) hold a head.  A warp walks a range of
+// heads, 32 / lanes of them at a time: the weights, and a token's cosines and
+// sines, are read once and kept in registers.
 //
 // The weights' gradients are summed per lane over the tokens of its warp,
 // then over the block in shared memory, and one row per block goes to the
@@ -40,7 +40,6 @@ struct QkParams {
     Heads side[2];           // queries, keys
     int64_t T;
     int D, rot, lanes;       // lanes per head, a power of two
-    int segments;            // ranges of heads that a token is cut into
     float eps;
     const float *cos, *sin;
     int64_t table_rows;
@@ -63,6 +62,31 @@ struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
 
+// Packed pairs of FP32 values (half the instructions), and the 16-bit pairs
+// of a 32-bit word as such: one or two instructions per pair.
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+    return pack_f32x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+template <typename T> __device__ __forceinline__ uint64_t widen(uint32_t w);
+template <> __device__ __forceinline__ uint64_t widen<__nv_bfloat16>(uint32_t w) {
+    return pack_f32x2(w << 16, w & 0xFFFF0000u);
+}
+template <> __device__ __forceinline__ uint64_t widen<__half>(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pk(f.x, f.y);
+}
+template <typename T> __device__ __forceinline__ uint32_t narrow(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t narrow<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t narrow<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Where the pair chunk of lane position c (pairs c V .. c V + V - 1) lies:
 // first and second elements' offsets in the head, and whether they exist.
 // An odd rest (V = 1 only) leaves the last pair without a second element.
@@ -70,6 +94,7 @@ template <int V, bool PAIRS>
 struct Chunk {
     int a, b, j;             // offsets of the first elements; rotary index
     bool rotated, has_a, has_b;
+    Chunk() = default;
     __device__ __forceinline__ Chunk(int c, int D, int rot) {
         const int p = c * V, half = rot / 2, rest = D - rot, q = p - half;
         rotated = p < half;
@@ -88,68 +113,149 @@ struct Chunk {
     }
 };
 
-// The chunk as it lies in memory, and its 2 V values as x[i] (first elements)
-// and x[V + i] (second).  Rotated neighbouring pairs lie as a0 b0 a1 b1 ..: two
-// vectors in a row.
+// A lane's chunks as they lie in memory: NC pairs of vectors.
 template <typename T, int V>
 struct Raw {
     Vec<T, V> a, b;
 };
-template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ Raw<T, V> load_chunk(const T* head, const Chunk<V, PAIRS>& ck, bool in) {
-    Raw<T, V> r = {};
-    if (in && ck.has_a) r.a = *reinterpret_cast<const Vec<T, V>*>(head + ck.a);
-    if (in && ck.has_b) r.b = *reinterpret_cast<const Vec<T, V>*>(head + ck.b);
-    return r;
-}
-template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ void unpack_chunk(const Raw<T, V>& r, const Chunk<V, PAIRS>& ck, float (&x)[2 * V]) {
-    if (PAIRS && ck.rotated) {
+template <typename T, int V, int NC, bool PAIRS>
+__device__ __forceinline__ void load_chunks(const T* head, const Chunk<V, PAIRS> (&ck)[NC], bool in,
+                                            Raw<T, V> (&r)[NC]) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = to_f32(2 * i < V ? r.a.v[(2 * i) % V] : r.b.v[(2 * i) % V]);
-            x[V + i] = to_f32(2 * i + 1 < V ? r.a.v[(2 * i + 1) % V] : r.b.v[(2 * i + 1) % V]);
+    for (int n = 0; n < NC; ++n) {
+        r[n] = {};
+        if (in && ck[n].has_a) r[n].a = *reinterpret_cast<const Vec<T, V>*>(head + ck[n].a);
+        if (in && ck[n].has_b) r[n].b = *reinterpret_cast<const Vec<T, V>*>(head + ck[n].b);
+    }
+}
+
+// The same by asynchronous copies into this thread's own slots of shared
+// memory (zeros where there is nothing), and back: a thread reads only what it
+// copied itself, so its own wait for the copies is all the order needed.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
+                     :: "r"(dst), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
+}
+template <typename T, int V, int NC, bool PAIRS, bool FULL>
+__device__ __forceinline__ void copy_chunks(const T* head, const Chunk<V, PAIRS> (&ck)[NC], bool in,
+                                            uint32_t slot, uint32_t step) {
+    constexpr int B = sizeof(T) * V;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        const bool a = FULL || (in && ck[n].has_a), b = FULL || (in && ck[n].has_b);
+        copy_async<B>(slot + 2 * n * step, a ? head + ck[n].a : head, a);
+        copy_async<B>(slot + (2 * n + 1) * step, b ? head + ck[n].b : head, b);
+    }
+}
+template <typename T, int V, int NC>
+__device__ __forceinline__ void read_chunks(const uint8_t* slot, uint32_t step, Raw<T, V> (&r)[NC]) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        r[n].a = *reinterpret_cast<const Vec<T, V>*>(slot + 2 * n * step);
+        r[n].b = *reinterpret_cast<const Vec<T, V>*>(slot + (2 * n + 1) * step);
+    }
+}
+
+// Their values: first elements a[], second b[], as packed pairs.  Rotated
+// neighbouring pairs lie as a0 b0 a1 b1 ..: two vectors in a row.
+template <typename T, int V, int NC, bool PAIRS>
+__device__ __forceinline__ void unpack(const Raw<T, V> (&r)[NC], const Chunk<V, PAIRS> (&ck)[NC],
+                                       uint64_t (&a)[NC * V / 2], uint64_t (&b)[NC * V / 2]) {
+    if constexpr (V == 1) {                          // (neighbouring pairs: a and b are what they are)
+#pragma unroll
+        for (int n = 0; n < NC; n += 2) {
+            a[n / 2] = pk(to_f32(r[n].a.v[0]), to_f32(r[n + 1].a.v[0]));
+            b[n / 2] = pk(to_f32(r[n].b.v[0]), to_f32(r[n + 1].b.v[0]));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            x[i] = to_f32(r.a.v[i]);
-            x[V + i] = to_f32(r.b.v[i]);
+        for (int n = 0; n < NC; ++n) {
+            uint64_t lo[V / 2], hi[V / 2];           // pairs of the first and of the second vector
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    lo[i] = pk(r[n].a.v[2 * i], r[n].a.v[2 * i + 1]);
+                    hi[i] = pk(r[n].b.v[2 * i], r[n].b.v[2 * i + 1]);
+                } else {
+                    lo[i] = widen<T>(reinterpret_cast<const uint32_t*>(r[n].a.v)[i]);
+                    hi[i] = widen<T>(reinterpret_cast<const uint32_t*>(r[n].b.v)[i]);
+                }
+            }
+            uint64_t* an = a + n * (V / 2);
+            uint64_t* bn = b + n * (V / 2);
+            if (PAIRS && ck[n].rotated) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {    // pairs 2 i and 2 i + 1 of the 2 V values in a row
+                    const uint64_t p0 = 2 * i < V / 2 ? lo[(2 * i) % (V / 2)] : hi[(2 * i) % (V / 2)];
+                    const uint64_t p1 = 2 * i + 1 < V / 2 ? lo[(2 * i + 1) % (V / 2)] : hi[(2 * i + 1) % (V / 2)];
+                    an[i] = pk(lo_of(p0), lo_of(p1));
+                    bn[i] = pk(hi_of(p0), hi_of(p1));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    an[i] = lo[i];
+                    bn[i] = hi[i];
+                }
+            }
         }
     }
 }
 
-template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ void store_chunk(T* head, const Chunk<V, PAIRS>& ck, const float (&y)[2 * V]) {
-    Vec<T, V> a, b;
-    if (PAIRS && ck.rotated) {
+template <typename T, int V, int NC, bool PAIRS, bool FULL>
+__device__ __forceinline__ void store_chunks(T* head, const Chunk<V, PAIRS> (&ck)[NC],
+                                             const uint64_t (&a)[NC * V / 2], const uint64_t (&b)[NC * V / 2]) {
+    if constexpr (V == 1) {
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) {
-            const T v = from_f32<T>(y[(e & 1) * V + e / 2]);
-            if (e < V) a.v[e % V] = v;
-            else b.v[e % V] = v;
+        for (int n = 0; n < NC; ++n) {
+            if (ck[n].has_a) head[ck[n].a] = from_f32<T>(n & 1 ? hi_of(a[n / 2]) : lo_of(a[n / 2]));
+            if (ck[n].has_b) head[ck[n].b] = from_f32<T>(n & 1 ? hi_of(b[n / 2]) : lo_of(b[n / 2]));
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            a.v[i] = from_f32<T>(y[i]);
-            b.v[i] = from_f32<T>(y[V + i]);
+        for (int n = 0; n < NC; ++n) {
+            const uint64_t* an = a + n * (V / 2);
+            const uint64_t* bn = b + n * (V / 2);
+            uint64_t lo[V / 2], hi[V / 2];
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                lo[i] = an[i];
+                hi[i] = bn[i];
+            }
+            if (PAIRS && ck[n].rotated) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const uint64_t p0 = pk(lo_of(an[i]), lo_of(bn[i])), p1 = pk(hi_of(an[i]), hi_of(bn[i]));
+                    (2 * i < V / 2 ? lo : hi)[(2 * i) % (V / 2)] = p0;
+                    (2 * i + 1 < V / 2 ? lo : hi)[(2 * i + 1) % (V / 2)] = p1;
+                }
+            }
+            Raw<T, V> r;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    r.a.v[2 * i] = lo_of(lo[i]); r.a.v[2 * i + 1] = hi_of(lo[i]);
+                    r.b.v[2 * i] = lo_of(hi[i]); r.b.v[2 * i + 1] = hi_of(hi[i]);
+                } else {
+                    reinterpret_cast<uint32_t*>(r.a.v)[i] = narrow<T>(lo_of(lo[i]), hi_of(lo[i]));
+                    reinterpret_cast<uint32_t*>(r.b.v)[i] = narrow<T>(lo_of(hi[i]), hi_of(hi[i]));
+                }
+            }
+            if (FULL || ck[n].has_a) *reinterpret_cast<Vec<T, V>*>(head + ck[n].a) = r.a;
+            if (FULL || ck[n].has_b) *reinterpret_cast<Vec<T, V>*>(head + ck[n].b) = r.b;
         }
     }
-    if (ck.has_a) *reinterpret_cast<Vec<T, V>*>(head + ck.a) = a;
-    if (ck.has_b) *reinterpret_cast<Vec<T, V>*>(head + ck.b) = b;
-}
-
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 
 // Cosines and sines of a chunk at position `pos` (NaN out of the table; 1, 0
 // where nothing is rotated).
 template <int V, bool PAIRS>
 __device__ __forceinline__ void load_turn(const QkParams& p, int64_t pos, bool pos_ok,
-                                          const Chunk<V, PAIRS>& ck, float (&cs)[V], float (&sn)[V]) {
+                                          const Chunk<V, PAIRS>& ck, float* cs, float* sn) {
     const float bad = __uint_as_float(0x7FC00000u);
     Vec<float, V> c, s;
 #pragma unroll
@@ -180,142 +286,219 @@ __device__ __forceinline__ void load_turn(const QkParams& p, int64_t pos, bool p
 }
 
 template <int V, bool PAIRS>
-__device__ __forceinline__ void load_weight(const float* w, const Chunk<V, PAIRS>& ck, float (&x)[2 * V]) {
+__device__ __forceinline__ void load_weight(const float* w, const Chunk<V, PAIRS>& ck, float* wa, float* wb) {
 #pragma unroll
-    for (int i = 0; i < 2 * V; ++i) x[i] = 1.0f;
-    if (w && ck.has_a)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[i] = w[PAIRS && ck.rotated ? ck.a + 2 * i : ck.a + i];
-    if (w && ck.has_b)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            x[V + i] = w[PAIRS && ck.rotated ? ck.a + 2 * i + 1 : ck.b + i];
+    for (int i = 0; i < V; ++i) {
+        wa[i] = w && ck.has_a ? w[PAIRS && ck.rotated ? ck.a + 2 * i : ck.a + i] : 1.0f;
+        wb[i] = w && ck.has_b ? w[PAIRS && ck.rotated ? ck.a + 2 * i + 1 : ck.b + i] : 1.0f;
+    }
 }
 
+// Rounds of heads in flight per warp: shared memory holds them, so that HBM's
+// latency is covered by bytes on the way and not by registers.
 constexpr int kWarps = 8;                    // per block
+template <int BYTES, int NC, bool BWD>
+struct Ring {
+    static constexpr bool used = BYTES >= 4;         // (cp.async copies 4, 8 or 16 bytes)
+    static constexpr int per_round = (BWD ? 4 : 2) * NC;             // copies per lane
+    static constexpr int depth = NC > 1 ? (BWD ? 2 : 3) : BWD ? 4 : 6;
+    static constexpr int bytes = used ? depth * per_round * BYTES * kWarps * 32 : 0;
+};
 
-// V pairs per chunk, NC chunks per lane, U rounds of heads read ahead of
-// their arithmetic (HBM's latency: each round is 32 bytes per lane and tensor).
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int U>
-__global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_kernel(const QkParams p) {
-    extern __shared__ float dw_sum[];                            // backward: [warp][2][D]
+// V pairs per chunk, NC chunks per lane.  The rounds of heads (32 / lanes at a
+// time) of all tokens are shared evenly by the warps in consecutive ranges,
+// first those of one side and then of the other.
+//
+// Forward, with the weights folded into the cosines and sines once per token:
+//   y_a = r (a (w_a c) - b (w_b s)),  y_b = r (b (w_b c) + a (w_a s)).
+//
+// FULL: every lane has both of its chunks in every round (the head's chunks
+// are the lanes of a group, and whole rounds make up both sides): no guards.
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];              // the rings; backward: then [warp][2][D]
+    constexpr int E = NC * V, H = E / 2;                         // pairs a lane holds, packed
+    static_assert(E % 2 == 0, "pairs of values");
+    constexpr int B = sizeof(T) * V;
+    using R = Ring<B, NC, BWD>;
+    constexpr uint32_t kStep = kWarps * 32 * B;                  // from one copy's slots to the next
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / p.lanes, pos_in = lane % p.lanes;   // head of the warp's group, lane in it
     const int at_once = 32 / p.lanes;
-    const int64_t items = p.T * p.segments;
+    const int64_t self = (int64_t)blockIdx.x * kWarps + warp, warps = (int64_t)gridDim.x * kWarps;
     const float inv_d = 1.0f / p.D;
+    uint8_t* mine = smem + threadIdx.x * B;
+    float* dw_sum = reinterpret_cast<float*>(smem + R::bytes);
+    Chunk<V, PAIRS> ck[NC];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) ck[n] = Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
         const Heads& hd = p.side[s];
-        float w[NC][2 * V], dw[BWD ? NC : 1][BWD ? 2 * V : 1];
+        // this warp's range of the T x per_token rounds
+        const int per_token = (hd.heads + at_once - 1) / at_once;
+        const int64_t all = p.T * per_token;
+        const int64_t begin = self * all / warps;
+        int left = int((self + 1) * all / warps - begin);
+        float wa[E], wb[E];
+        uint64_t dwa[BWD ? H : 1], dwb[BWD ? H : 1];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            load_weight<V, PAIRS>(hd.w, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), w[n]);
-            if constexpr (BWD)
+        for (int n = 0; n < NC; ++n) load_weight<V, PAIRS>(hd.w, ck[n], wa + n * V, wb + n * V);
+        if constexpr (BWD)
 #pragma unroll
-                for (int i = 0; i < 2 * V; ++i) dw[n][i] = 0.0f;
-        }
-        const int per = (hd.heads + p.segments - 1) / p.segments;
-        for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
-             it += (int64_t)gridDim.x * kWarps) {
-            const int64_t t = it / p.segments;
-            const int seg = int(it - t * p.segments);
-            const int h_end = min(hd.heads, (seg + 1) * per);
-            if (seg * per >= h_end) continue;
-            const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
-            const bool pos_ok = pos >= 0 && pos < p.table_rows;
-            if (!pos_ok && p.rot > 0 && lane == 0) record_error(p.err, kDevErrValue);
-            float cs[NC][V], sn[NC][V];
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-                load_turn<V, PAIRS>(p, pos, pos_ok, Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot), cs[n], sn[n]);
-            const T* in = static_cast<const T*>(hd.in) + t * hd.in_t;
-            const T* dy = static_cast<const T*>(hd.dy) + t * hd.dy_t;
-            T* out = static_cast<T*>(hd.out) + t * hd.out_t;
-            // every lane of the warp runs every round (the sums are shuffles)
-            for (int h0 = seg * per; h0 < h_end; h0 += U * at_once) {
-                Raw<T, V> rx[U][NC], rd[BWD ? U : 1][BWD ? NC : 1];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * at_once + sub;
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
-                        rx[u][n] = load_chunk<T, V, PAIRS>(in + h * hd.in_h, ck, h < h_end);
-                        if constexpr (BWD) rd[u][n] = load_chunk<T, V, PAIRS>(dy + h * hd.dy_h, ck, h < h_end);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int h = h0 + u * at_once + sub;
-                    float x[NC][2 * V], d[BWD ? NC : 1][BWD ? 2 * V : 1];
-                    float ss = 0.0f, sd = 0.0f;
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
-                        unpack_chunk<T, V, PAIRS>(rx[u][n], ck, x[n]);
-#pragma unroll
-                        for (int i = 0; i < 2 * V; ++i) ss = fmaf(x[n][i], x[n][i], ss);
-                        if constexpr (BWD) {
-                            unpack_chunk<T, V, PAIRS>(rd[u][n], ck, d[n]);
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {        // turned back
-                                const float a = d[n][i], b = d[n][V + i];
-                                d[n][i] = fmaf(a, cs[n][i], b * sn[n][i]);
-                                d[n][V + i] = fmaf(b, cs[n][i], -(a * sn[n][i]));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 2 * V; ++i) sd = fmaf(d[n][i] * w[n][i], x[n][i], sd);
-                        }
-                    }
-                    ss = lanes_sum(ss, p.lanes);
-                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-                    if constexpr (BWD) {
-                        sd = lanes_sum(sd, p.lanes);
-                        const float m = r * r * (sd * inv_d);
-                        const bool live = h < h_end;
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) {
-                            const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
-#pragma unroll
-                            for (int i = 0; i < 2 * V; ++i) {
-                                if (live) dw[n][i] = fmaf(d[n][i], x[n][i] * r, dw[n][i]);
-                                d[n][i] = r * fmaf(d[n][i], w[n][i], -(x[n][i] * m));
-                            }
-                            if (live) store_chunk<T, V, PAIRS>(out + h * hd.out_h, ck, d[n]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) {
-                            const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const float a = x[n][i] * r * w[n][i], b = x[n][V + i] * r * w[n][V + i];
-                                x[n][i] = fmaf(a, cs[n][i], -(b * sn[n][i]));
-                                x[n][V + i] = fmaf(b, cs[n][i], a * sn[n][i]);
-                            }
-                            if (h < h_end) store_chunk<T, V, PAIRS>(out + h * hd.out_h, ck, x[n]);
-                        }
-                    }
+            for (int e = 0; e < H; ++e) dwa[e] = dwb[e] = 0;
+        int t = per_token > 0 ? int(begin / per_token) : 0;
+        int round = per_token > 0 ? int(begin - (int64_t)t * per_token) : 0;
+        // the copies' own walk over the rounds, R::depth ahead
+        int to_copy = left, copy_at = round, filled = 0;
+        const int64_t step_in = at_once * hd.in_h, step_dy = at_once * hd.dy_h;
+        const int64_t wrap_in = hd.in_t - per_token * step_in, wrap_dy = hd.dy_t - per_token * step_dy;
+        const T* copy_in = static_cast<const T*>(hd.in) + t * hd.in_t + round * step_in + sub * hd.in_h;
+        const T* copy_dy = static_cast<const T*>(hd.dy) + t * hd.dy_t + round * step_dy + sub * hd.dy_h;
+        auto copy_round = [&]() {
+            if (to_copy > 0) {
+                --to_copy;
+                // (a head past the end: any address in range, nothing is read)
+                const bool in = FULL || copy_at * at_once + sub < hd.heads;
+                const uint32_t slot = smem_u32(mine) + filled * (R::per_round * kStep);
+                copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_in : static_cast<const T*>(hd.in), ck, in, slot, kStep);
+                if constexpr (BWD)
+                    copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_dy : static_cast<const T*>(hd.dy), ck, in,
+                                                       slot + 2 * NC * kStep, kStep);
+                filled = filled + 1 == R::depth ? 0 : filled + 1;
+                copy_in += step_in;
+                if (BWD) copy_dy += step_dy;
+                if (++copy_at == per_token) {                    // the next token
+                    copy_at = 0;
+                    copy_in += wrap_in;
+                    if (BWD) copy_dy += wrap_dy;
                 }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if constexpr (R::used)
+            for (int i = 0; i < R::depth; ++i) copy_round();
+        int read = 0;
+        // position, cosines and sines are read one token ahead
+        auto pos_of = [&](int tok) { return p.rot > 0 && tok < p.T ? p.positions[tok] : 0; };
+        float c[E], sn[E];
+        auto turn_of = [&](int pos) {
+            const bool ok = pos >= 0 && pos < p.table_rows;
+            if (!ok && p.rot > 0 && lane == 0) record_error(p.err, kDevErrValue);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) load_turn<V, PAIRS>(p, pos, ok, ck[n], c + n * V, sn + n * V);
+        };
+        int next_pos = 0;
+        if (left > 0) {
+            turn_of(pos_of(t));
+            next_pos = pos_of(t + 1);
         }
+        while (left > 0) {
+            const int here = min(left, per_token - round);       // rounds of this token
+            left -= here;
+            uint64_t ac[H], bc[H], as[H], nbs[H];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                if constexpr (BWD) {
+                    ac[e / 2] = pk(c[e], c[e + 1]);
+                    as[e / 2] = pk(sn[e], sn[e + 1]);
+                    nbs[e / 2] = pk(-sn[e], -sn[e + 1]);
+                } else {
+                    ac[e / 2] = pk(wa[e] * c[e], wa[e + 1] * c[e + 1]);
+                    as[e / 2] = pk(wa[e] * sn[e], wa[e + 1] * sn[e + 1]);
+                    bc[e / 2] = pk(wb[e] * c[e], wb[e + 1] * c[e + 1]);
+                    nbs[e / 2] = pk(-wb[e] * sn[e], -wb[e + 1] * sn[e + 1]);
+                }
+            }
+            if (left > 0) {
+                turn_of(next_pos);
+                next_pos = pos_of(t + 2);
+            }
+            T* out = static_cast<T*>(hd.out) + t * hd.out_t + (round * at_once + sub) * hd.out_h;
+            const int64_t step_out = at_once * hd.out_h;
+            // every lane of the warp runs every round (the sums are shuffles)
+            for (int i = 0; i < here; ++i, out += step_out) {
+                const int h = (round + i) * at_once + sub, h_end = hd.heads;
+                Raw<T, V> rx[NC], rd[NC];
+                if constexpr (R::used) {
+                    asm volatile("cp.async.wait_group %0;" :: "n"(R::depth - 1) : "memory");
+                    const uint8_t* slot = mine + read * (R::per_round * kStep);
+                    read_chunks<T, V, NC>(slot, kStep, rx);
+                    if constexpr (BWD) read_chunks<T, V, NC>(slot + 2 * NC * kStep, kStep, rd);
+                    read = read + 1 == R::depth ? 0 : read + 1;
+                    copy_round();                                // into the slots just read
+                } else {
+                    load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.in) + t * hd.in_t + h * hd.in_h, ck,
+                                                 h < h_end, rx);
+                    if constexpr (BWD)
+                        load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.dy) + t * hd.dy_t + h * hd.dy_h, ck,
+                                                     h < h_end, rd);
+                }
+                uint64_t xa[H], xb[H], q = 0;
+                unpack<T, V, NC, PAIRS>(rx, ck, xa, xb);
+#pragma unroll
+                for (int e = 0; e < H; ++e) q = fma_f32x2(xb[e], xb[e], fma_f32x2(xa[e], xa[e], q));
+                float ss = lo_of(q) + hi_of(q);
+                if constexpr (BWD) {
+                    // dn, the output's gradient turned back; its sum with w x
+                    uint64_t da[H], db[H], z = 0;
+                    unpack<T, V, NC, PAIRS>(rd, ck, da, db);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        const uint64_t ga = fma_f32x2(db[e], as[e], mul_f32x2(da[e], ac[e]));
+                        db[e] = fma_f32x2(da[e], nbs[e], mul_f32x2(db[e], ac[e]));
+                        da[e] = ga;
+                        z = fma_f32x2(mul_f32x2(da[e], pk(wa[2 * e], wa[2 * e + 1])), xa[e], z);
+                        z = fma_f32x2(mul_f32x2(db[e], pk(wb[2 * e], wb[2 * e + 1])), xb[e], z);
+                    }
+                    float sd = lo_of(z) + hi_of(z);
+                    for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+                        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        sd += __shfl_xor_sync(0xffffffffu, sd, o);
+                    }
+                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps)), m = sd * inv_d * r * r;
+                    const uint64_t rr = pk(r, r), nm = pk(-m, -m);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {                // r (dn w - x m)
+                        dwa[e] = fma_f32x2(da[e], mul_f32x2(xa[e], rr), dwa[e]);
+                        dwb[e] = fma_f32x2(db[e], mul_f32x2(xb[e], rr), dwb[e]);
+                        xa[e] = mul_f32x2(rr, fma_f32x2(xa[e], nm, mul_f32x2(da[e], pk(wa[2 * e], wa[2 * e + 1]))));
+                        xb[e] = mul_f32x2(rr, fma_f32x2(xb[e], nm, mul_f32x2(db[e], pk(wb[2 * e], wb[2 * e + 1]))));
+                    }
+                } else {
+                    for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+                    const uint64_t rr = pk(r, r);
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        const uint64_t ya = mul_f32x2(rr, fma_f32x2(xb[e], nbs[e], mul_f32x2(xa[e], ac[e])));
+                        xb[e] = mul_f32x2(rr, fma_f32x2(xa[e], as[e], mul_f32x2(xb[e], bc[e])));
+                        xa[e] = ya;
+                    }
+                }
+                if (FULL || h < h_end) store_chunks<T, V, NC, PAIRS, FULL>(out, ck, xa, xb);
+            }
+            round = 0;
+            ++t;
+        }
+        if constexpr (R::used) asm volatile("cp.async.wait_group 0;" ::: "memory");
         if constexpr (BWD) {
-            // over the warp's heads
+            // over the warp's heads (lanes without a head read zeros and added zeros)
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-                const Chunk<V, PAIRS> ck(pos_in + n * p.lanes, p.D, p.rot);
 #pragma unroll
-                for (int i = 0; i < 2 * V; ++i) {
-                    float v = dw[n][i];
-                    for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    const bool second = i >= V;
-                    if (sub == 0 && (second ? ck.has_b : ck.has_a)) {
-                        const int e = PAIRS && ck.rotated ? ck.a + 2 * (i % V) + (second ? 1 : 0)
-                                                          : (second ? ck.b + i - V : ck.a + i);
-                        dw_sum[(warp * 2 + s) * p.D + e] = v;
+                for (int i = 0; i < V; ++i) {
+                    const int e = n * V + i;
+                    float va = e & 1 ? hi_of(dwa[e / 2]) : lo_of(dwa[e / 2]);
+                    float vb = e & 1 ? hi_of(dwb[e / 2]) : lo_of(dwb[e / 2]);
+                    for (int o = p.lanes; o < 32; o <<= 1) {
+                        va += __shfl_xor_sync(0xffffffffu, va, o);
+                        vb += __shfl_xor_sync(0xffffffffu, vb, o);
                     }
+                    float* to = dw_sum + (warp * 2 + s) * p.D;
+                    const bool row = PAIRS && ck[n].rotated;
+                    if (sub == 0 && ck[n].has_a) to[row ? ck[n].a + 2 * i : ck[n].a + i] = va;
+                    if (sub == 0 && ck[n].has_b) to[row ? ck[n].a + 2 * i + 1 : ck[n].b + i] = vb;
                 }
             }
         }
@@ -353,24 +536,35 @@ __global__ void __launch_bounds__(1024) qk_norm_dw(const float* __restrict__ par
     }
 }
 
+template <bool BWD>
 constexpr int kBlocksPerSm = 2;
 
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int U>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL>
 cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
-    const size_t smem = BWD ? (size_t)kWarps * 2 * p.D * sizeof(float) : 0;
-    qk_norm_kernel<T, V, NC, PAIRS, BWD, U><<<blocks, kWarps * 32, smem, stream>>>(p);
+    const int smem = Ring<sizeof(T) * V, NC, BWD>::bytes + (BWD ? kWarps * 2 * p.D * (int)sizeof(float) : 0);
+    auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL>;
+    if (smem > 48 << 10) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<blocks, kWarps * 32, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
-// The widest chunk that the head's layout allows: V pairs per lane position
+// The widest chunk that the head's layout allows: four pairs per lane position
 // where both parts of the head are whole chunks and every row starts on a
-// boundary of V elements (and the tables on 16 bytes); one pair otherwise.
+// boundary of four elements (and the tables on 16 bytes); one pair otherwise.
+// Measured, forward / backward, us: bfloat16, 16384 tokens x 40 heads x 128, 62 /
+// 91 with four pairs, 67 / 112 with eight (whose cosines, sines and weights
+// alone take 64 registers); float32, 8192 x 24 x 128, 39 / 56.  Two blocks per
+// SM: 62 / 91; three 64 / 107; four 68 / 107.  (Bytes at the HBM's rate: 49 /
+// 74, 30 / 45.)  Before the rings the loads waited in registers: 89 us forward.
 template <typename T, bool PAIRS, bool BWD>
 cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 4;
     bool wide = p.rot % (2 * V) == 0 && (p.D - p.rot) % (2 * V) == 0;
     auto whole = [&](const void* q, int64_t ts, int64_t hs) {
-        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ts % V == 0 && hs % V == 0;
+        return reinterpret_cast<uintptr_t>(q) % (V * sizeof(T)) == 0 && ts % V == 0 && hs % V == 0;
     };
     for (const Heads& h : p.side)
         if (h.heads > 0)
@@ -383,19 +577,20 @@ cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t s
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes < chunks) p.lanes *= 2;
     const int nc = (chunks + p.lanes - 1) / p.lanes;
-    // few tokens: cut each one's heads into ranges until the warps fill the GPU
-    const int rounds = (p.side[0].heads * p.lanes + 31) / 32 + (p.side[1].heads * p.lanes + 31) / 32;
-    p.segments = 1;
-    while (p.segments * 2 <= rounds && p.T * p.segments < (int64_t)max_blocks * kWarps) p.segments *= 2;
-    const int64_t want = (p.T * p.segments + kWarps - 1) / kWarps;
+    // a warp per round until they fill the GPU
+    const int at_once = 32 / p.lanes;
+    const int most = p.side[0].heads > p.side[1].heads ? p.side[0].heads : p.side[1].heads;
+    const int64_t want = (p.T * ((most + at_once - 1) / at_once) + kWarps - 1) / kWarps;
     *blocks = (int)(want < max_blocks ? want : max_blocks);
-    constexpr int U = BWD ? 2 : 4;
+    constexpr int BPS = kBlocksPerSm<BWD>;
     if (wide) {
-        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, U>(p, *blocks, stream);
-        return launch_one<T, V, 2, PAIRS, BWD, U / 2>(p, *blocks, stream);
+        const bool full = chunks == p.lanes && p.side[0].heads % at_once == 0 && p.side[1].heads % at_once == 0;
+        if (nc == 1 && full) return launch_one<T, V, 1, PAIRS, BWD, BPS, true>(p, *blocks, stream);
+        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, BPS, false>(p, *blocks, stream);
+        return launch_one<T, V, 2, PAIRS, BWD, 1, false>(p, *blocks, stream);
     }
-    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, U>(p, *blocks, stream);
-    return launch_one<T, 1, 8, PAIRS, BWD, 1>(p, *blocks, stream);
+    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, BPS, false>(p, *blocks, stream);
+    return launch_one<T, 1, 8, PAIRS, BWD, 1, false>(p, *blocks, stream);
 }
 
 template <bool BWD>
@@ -427,7 +622,7 @@ emu_status_t check_qk(int dtype, int64_t T, int64_t D, int64_t rot, int interlea
                       int64_t table_rows, const int32_t* positions) {
     if (dtype < EMU_F32 || dtype > EMU_F16 || (interleaved != 0 && interleaved != 1))
         return EMU_ERR_INVALID_VALUE;
-    if (T < 0 || T > INT32_MAX || D < 1 || D > 512 || rot < 0 || rot > D || rot % 2 != 0 || !(eps >= 0.0f))
+    if (T < 0 || T > INT32_MAX / 64 || D < 1 || D > 512 || rot < 0 || rot > D || rot % 2 != 0 || !(eps >= 0.0f))
         return EMU_ERR_INVALID_VALUE;
     if (!heads_ok(q, T) || !heads_ok(k, T) || !heads_ok(qo, T) || !heads_ok(ko, T) ||
         qo.heads != q.heads || ko.heads != k.heads)
@@ -475,7 +670,7 @@ emu_status_t emu_qk_norm_rope(int dtype, int64_t T, int64_t D, int64_t rot, int 
     p.cos = cos; p.sin = sin; p.table_rows = table_rows; p.positions = positions;
     p.err = d->err;
     int blocks = 0;
-    return from_cuda(launch_any<false>(dtype, interleaved != 0, p, d->sms * kBlocksPerSm, &blocks,
+    return from_cuda(launch_any<false>(dtype, interleaved != 0, p, d->sms * kBlocksPerSm<false>, &blocks,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -497,7 +692,7 @@ emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, 
     DeviceState* d = nullptr;
     st = current_device(&d);
     if (st != EMU_OK) return st;
-    const int max_blocks = d->sms * kBlocksPerSm;
+    const int max_blocks = d->sms * kBlocksPerSm<true>;
     st = ensure_buffer(&d->ws, &d->ws_bytes, (size_t)max_blocks * 2 * D * sizeof(float));
     if (st != EMU_OK) return st;
     QkParams p = {};

@@ -156,7 +156,7 @@ typedef struct {
  *                have 0 heads.  An output may be its input (same data and
  *                strides), otherwise it may not overlap one.
  *  dtype         type of q, k and the outputs (an emu_dtype_t)
- *  T, D, rot     tokens, values of a head (1..512), rotated values (even,
+ *  T, D, rot     tokens (at most 2^25 - 1), values of a head (1..512), rotated values (even,
  *                0..D).  T == 0 is a no-op.
  *  wq, wk        D values each (FP32), or NULL for ones
  *  cos, sin      table_rows x rot/2 (FP32, contiguous); rot == 0 reads neither
