@@ -108,7 +108,7 @@ emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int6
 // G, U, ldg).  Launched as a programmatic dependent of the split of X, which
 // must itself have been launched as an ordinary kernel: the weights are read
 // before that split has ended.
-constexpr int64_t kFewRows = 128;
+constexpr int64_t kFewRows = 160;
 bool few_rows_ok(int64_t M, const float* W, int64_t ldw);
 emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
                            int64_t N, int64_t K, const void* xp, int64_t ldp, TcGemmParams p,

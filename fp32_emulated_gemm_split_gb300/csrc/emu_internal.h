@@ -127,7 +127,7 @@ cudaError_t launch_gemm_gated(const CUtensorMap& mapA, const CUtensorMap& mapB,
                               cudaStream_t stream);
 int gemm_gated_clusters(int sms);
 // Few rows of X (gemm_few.cu): FP32 weights streamed and split on chip, X's
-// pieces as the narrow operand (bn 16, 32, 64 or 128 rows of it), the result
+// pieces as the narrow operand (bn 16, 32, 64, 128 or 160 rows of it), the result
 // stored transposed: element (weight row m < p.M, X row n < p.N) at
 // C[n * ldc + m].  mapA: an FP32 map of the weights, box 32 x 128; gated (mapA2
 // not null): maps of the two weights, box 32 x 64; mapB: X's pieces, box 64 x

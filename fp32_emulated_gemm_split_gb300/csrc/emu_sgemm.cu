@@ -395,7 +395,7 @@ emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t
                            DeviceState* d, cudaStream_t stream) {
     // the narrowest tile that holds the rows: the tensor core's time and the
     // pieces' traffic grow with it
-    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 160;
     CUtensorMap mapA, mapA2, mapB;
     emu_status_t st = make_plane_map(&mapA, W, true, N, K, ldw, 1, 32, W2 ? 64 : 128);
     if (st == EMU_OK && W2) st = make_plane_map(&mapA2, W2, true, N, K, ldw2, 1, 32, 64);

@@ -157,32 +157,40 @@ template <int C>
 __device__ __forceinline__ void few_epilogue(const float (&acc)[C], const TcGemmParams& p, int m,
                                               int col0) {
     if (m >= p.M) return;
+    float* c = p.C + (int64_t)col0 * p.ldc + m;
+    // eight rows' old values of C at a time, before their stores (a store
+    // between two loads would hold the second one back)
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        if (col0 + j < p.N) {
-            float* c = p.C + (int64_t)(col0 + j) * p.ldc + m;
-            float v = p.alpha * acc[j];
-            if (p.beta != 0.0f) v = fmaf(p.beta, *c, v);
-            *c = v;
+    for (int j0 = 0; j0 < C; j0 += 8) {
+        float old[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            old[j] = p.beta != 0.0f && col0 + j0 + j < p.N ? c[(int64_t)(j0 + j) * p.ldc] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = p.alpha * acc[j0 + j];
+            if (col0 + j0 + j < p.N)
+                c[(int64_t)(j0 + j) * p.ldc] = p.beta != 0.0f ? fmaf(p.beta, old[j], v) : v;
         }
     }
 }
 
-// Gated: the tile's sums are in shared memory, row j of X's 128 at ex + 128 j,
-// the gate's 64 columns from f0, then the up projection's.  Thread t of n
-// takes every n-th element: a warp writes 32 neighbouring values of H.
+// Gated: the tile's sums of `rows` rows of X from row j0 are in shared memory,
+// 128 values each, the gate's 64 columns from f0, then the up projection's.
+// Thread t of n takes every n-th element: a warp writes 32 neighbouring values
+// of H.
 __device__ __forceinline__ void few_gated_epilogue(const TcGemmParams& p, const float* ex, int f0,
-                                                   int t, int n) {
+                                                   int j0, int rows, int t, int n) {
     with_act(p.act, [&](auto a) {
 #pragma unroll 2
-        for (int e = t; e < 64 * p.N; e += n) {
+        for (int e = t; e < 64 * rows; e += n) {
             const int j = e >> 6, f = e & 63;
             const float g = ex[j * 128 + f], u = ex[j * 128 + 64 + f];
             if (f0 + f < p.M) {
-                p.C[(int64_t)j * p.ldc + f0 + f] = gated_act<decltype(a)::value>(g) * u;
+                p.C[(int64_t)(j0 + j) * p.ldc + f0 + f] = gated_act<decltype(a)::value>(g) * u;
                 if (p.G) {
-                    p.G[(int64_t)j * p.ldg + f0 + f] = g;
-                    p.U[(int64_t)j * p.ldg + f0 + f] = u;
+                    p.G[(int64_t)(j0 + j) * p.ldg + f0 + f] = g;
+                    p.U[(int64_t)(j0 + j) * p.ldg + f0 + f] = u;
                 }
             }
         }

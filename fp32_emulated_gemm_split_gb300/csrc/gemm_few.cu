@@ -1,5 +1,5 @@
 // gemm_few.cu -- the emulated GEMM for few rows of X: Y = X W^T with at most
-// 128 rows, where what counts is reading W once.  Used by the gated
+// 160 rows, where what counts is reading W once.  Used by the gated
 // feed-forward and the projection with adapters (include/emu_layers.h).
 //
 // The method is BF16x9 (gemm_kblock.cu), with the operands' roles swapped: W
@@ -18,7 +18,8 @@
 // times all of them is one MMA per K step, and column group j collects
 //     a0 b_j + 2^-8 (a1 b_j + 2^-8 a2 b_j),
 // largest i first with the scaling between; the accumulator warps add the
-// groups times 2^-8j.  At BN = 64 and 128 the nine products run band by band.
+// groups times 2^-8j.  At BN = 64, 128 and 160 the nine products run band by
+// band, over as many columns as there are rows (in 16s).
 //
 // Bound by HBM: every value of W is read once.  One CTA per SM, each on its
 // own (no clusters: with CTA pairs the hand-offs between producer, split, MMA
@@ -59,28 +60,30 @@ struct Cfg {
     // its phases.
     // One group's latencies overlap with the other's arithmetic, and one
     // issuing thread would need about 2100 cycles for a block's waits, MMAs and
-    // commits beside the busy split warps (the stream 1400).  At BN = 128 the
-    // nine products take 2300 cycles of the tensor core either way.
-    static constexpr int lanes = BN == 128 ? 1 : 2;
+    // commits beside the busy split warps (the stream 1400).  At BN = 128 and
+    // 160 the nine products take 2300 or 2900 cycles of the tensor core anyway.
+    static constexpr int lanes = BN >= 128 ? 1 : 2;
     // tensor memory: partials, then W's pieces (96 columns per K block), both
     // per pipeline
-    static constexpr int partials = BN == 128 ? 2 : 1;
+    static constexpr int partials = BN >= 128 ? 2 : 1;
     static constexpr int a_stages = BN == 32 ? 1 : 2;
     static constexpr int a_base = lanes * partials * d_cols;
     static_assert(a_base + lanes * a_stages * 3 * kPieceCols <= 512, "tensor memory overflow");
     // shared memory: FP32 buffers (as many as fit: the stream's bytes in
     // flight), stages of X's pieces, the gated hand-over
-    static constexpr int a_bufs = BN == 16 ? 3 : 2;                          // per pipeline
+    static constexpr int a_bufs = BN == 16 || BN == 128 ? 3 : 2;                          // per pipeline
     static constexpr int b_tile = BN * kTcBKBytes;
     static constexpr int b_stages = BN <= 32 ? 2 : BN == 64 ? 1 : 2;    // per pipeline
-    static constexpr int ex_bytes = GATED ? 128 * BN * 4 : 0;
+    // (the gated hand-over in `passes` of BN / passes rows of X)
+    static constexpr int acc_warps = BN == 16 ? 4 : BN == 160 ? 16 : 8;
+    static constexpr int acc_cols = BN / (acc_warps / 4);
+    static constexpr int passes = BN <= 64 ? 1 : acc_warps / 4;
+    static constexpr int ex_bytes = GATED ? 128 * BN / passes * 4 : 0;
     static constexpr int smem = lanes * a_bufs * kABuf + lanes * b_stages * 3 * b_tile + ex_bytes + 2048;
     static_assert(smem <= kSmemMax, "shared memory overflow");
     // warps: 0 TMA of W and tensor-memory allocation, 1 TMA of X's pieces, 2
     // (and 3) MMA, then the accumulators, four per column group, and the split
     // warps
-    static constexpr int acc_warps = BN == 16 ? 4 : 8;
-    static constexpr int acc_cols = BN / (acc_warps / 4);
     static constexpr int acc0 = 4, split0 = acc0 + acc_warps;
     static constexpr int threads = 32 * (split0 + 8 * lanes);
 };
@@ -257,7 +260,8 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     } else if (warp < C::acc0) {
         if (lane == 0 && warp - 2 < L) {
             // ----------------------------------------------------- MMA issuers
-            const uint32_t idesc = make_idesc(1u, 128, C::d_cols);
+            // (not stacked: as many columns as there are rows of X, in 16s)
+            const uint32_t idesc = make_idesc(1u, 128, C::stacked ? C::d_cols : (p.N + 15) / 16 * 16);
             for (uint32_t g = warp - 2; g < blocks; g += L) {
                 const uint32_t s = slot_of(g, C::b_stages), t = slot_of(g, C::a_stages);
                 const uint32_t b = slot_of(g, C::partials);
@@ -395,33 +399,47 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                 continue;
             }
             // the owner adds the later parts in K order (bounded waits: those
-            // CTAs leave theirs before they wait for anything)
-            for (int o = 1; o <= w.others && ok; ++o) {
-                unsigned* flag = p.flags + slot(cta + o);
+            // CTAs leave theirs before they wait for anything).  The lanes look
+            // at a flag each, then the parts are read four at a time where registers
+            // allow it: flag and part after another took 0.7 us each.
+            for (int o0 = 1; o0 <= w.others && ok; o0 += 32) {
+                const int n = min(32, w.others - o0 + 1);
+                unsigned* flag = p.flags + slot(cta + o0 + lane);
                 const uint64_t t0 = global_timer_ns();
-                while (load_acquire(flag) != p.epoch) {
-                    __nanosleep(64);
-                    if (global_timer_ns() - t0 > EMU_WAIT_LIMIT_NS) {
-                        record_error(p.err, kDevErrTimeout);
+                while (!__all_sync(0xffffffffu, lane >= n || load_acquire(flag) == p.epoch)) {
+                    __nanosleep(32);
+                    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > EMU_WAIT_LIMIT_NS)) {
+                        if (lane == 0) record_error(p.err, kDevErrTimeout);
                         ok = false;
                         break;
                     }
                 }
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const float4* src = reinterpret_cast<const float4*>(p.part_ws) +
-                                    (size_t)slot(cta + o) * (AC / 4 * 32) + lane;
+                constexpr int kBatch = AC <= 16 ? 4 : 1;
+                for (int o = 0; o < n; o += kBatch) {
+                    float4 v[kBatch][AC / 4];
 #pragma unroll
-                for (int j = 0; j < AC / 4; ++j) {
-                    const float4 v = __ldcg(src + j * 32);
-                    acc[4 * j] += v.x;
-                    acc[4 * j + 1] += v.y;
-                    acc[4 * j + 2] += v.z;
-                    acc[4 * j + 3] += v.w;
+                    for (int i = 0; i < kBatch; ++i) {
+                        const float4* src = reinterpret_cast<const float4*>(p.part_ws) +
+                                            (size_t)slot(cta + o0 + min(o + i, n - 1)) * (AC / 4 * 32) + lane;
+#pragma unroll
+                        for (int j = 0; j < AC / 4; ++j) v[i][j] = __ldcg(src + j * 32);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        if (o + i >= n) break;
+#pragma unroll
+                        for (int j = 0; j < AC / 4; ++j) {
+                            acc[4 * j] += v[i][j].x;
+                            acc[4 * j + 1] += v[i][j].y;
+                            acc[4 * j + 2] += v[i][j].z;
+                            acc[4 * j + 3] += v[i][j].w;
+                        }
+                    }
                 }
                 // consumed: cleared, so that a replay of this launch waits afresh
                 __syncwarp();
-                if (lane == 0) *const_cast<volatile unsigned*>(flag) = 0u;
+                if (lane < n) *const_cast<volatile unsigned*>(flag) = 0u;
             }
             const int col0 = h * AC;                      // rows of X
             if constexpr (GATED) {
@@ -434,11 +452,18 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                     *abort_flag = 1;
                     break;
                 }
-                float* mine = ex + h * AC * 128 + q * 32 + lane;
+                constexpr int kRows = BN / C::passes;
+                for (int pass = 0; pass < C::passes; ++pass) {
+                    if (C::passes == 1 || h == pass) {
+                        float* mine = ex + (C::passes == 1 ? h * AC * 128 : 0) + q * 32 + lane;
 #pragma unroll
-                for (int j = 0; j < AC; ++j) mine[j * 128] = acc[j];
-                bar_and(1, C::acc_warps * 32, true);
-                few_gated_epilogue(p, ex, w.tile * 64, aw * 32 + lane, C::acc_warps * 32);
+                        for (int j = 0; j < AC; ++j) mine[j * 128] = acc[j];
+                    }
+                    bar_and(1, C::acc_warps * 32, true);
+                    few_gated_epilogue(p, ex, w.tile * 64, pass * kRows, min(kRows, p.N - pass * kRows),
+                                       aw * 32 + lane, C::acc_warps * 32);
+                    if (pass + 1 < C::passes) bar_and(1, C::acc_warps * 32, true);
+                }
             } else {
                 if (!ok) {
                     *abort_flag = 1;
@@ -502,6 +527,7 @@ cudaError_t launch_bn(int bn, const CUtensorMap& mapA, const Second<GATED>& seco
         case 32: return launch_few<32, GATED>(mapA, second, mapB, q, ctas, stream);
         case 64: return launch_few<64, GATED>(mapA, second, mapB, q, ctas, stream);
         case 128: return launch_few<128, GATED>(mapA, second, mapB, q, ctas, stream);
+        case 160: return launch_few<160, GATED>(mapA, second, mapB, q, ctas, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(1024) lora_group(const LoraParams p) {
     __shared__ int count[kMaxAdapters + 1];  // tokens, then the next free place
     __shared__ int warp_sum[32];
     const int groups = p.adapters + 1, tid = threadIdx.x;
+    griddep_launch_dependents();
     for (int a = tid; a < groups; a += 1024) count[a] = 0;
     __syncthreads();
     for (int64_t t = tid; t < p.M; t += 1024) atomicAdd(&count[adapter_of(p, t)], 1);
@@ -104,48 +105,52 @@ __global__ void __launch_bounds__(1024) lora_group(const LoraParams p) {
     if (tid == 0) *p.ntiles = all_tiles;
     __syncthreads();
     for (int64_t t = tid; t < p.M; t += 1024) p.order[atomicAdd(&count[adapter_of(p, t)], 1)] = (int32_t)t;
+    griddep_wait();                          // complete only after the split ahead, which may run beside it
 }
 
 // ------------------------------------------------------------- down, dots --
 //
-// Few tokens: S[t][r] over one slice of K.  A block takes four neighbouring
+// Few tokens: S[t][r] over one slice of K.  A block takes TOK neighbouring
 // tokens, a warp two rows of A (the block 16 of them), its lanes stride over
 // the slice (V neighbouring values each).  Bound by the latency of reading A's
 // rows once.
-constexpr int kDotWarps = 8, kDotTok = 4, kDotRows = 2;
+constexpr int kDotWarps = 8, kDotRows = 2;
+constexpr int kDotTok = 4;                   // tokens per block, 1 up to kSingleTokens of them
+constexpr int64_t kSingleTokens = 64;
 
-template <int V>
+template <int V, int TOK>
 __global__ void __launch_bounds__(kDotWarps * 32) lora_down_dots(const LoraParams p) {
-    const int64_t t0 = (int64_t)blockIdx.x * kDotTok;
+    griddep_launch_dependents();
+    const int64_t t0 = (int64_t)blockIdx.x * TOK;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = blockIdx.z;
     const int64_t k0 = slice * p.slice, k1 = min(p.K, k0 + p.slice);
     float* S = p.S + slice * p.M * p.R;
     const int r = (blockIdx.y * kDotWarps + warp) * kDotRows;
     if (r >= p.R) return;
-    int own[kDotTok];
-    const float* row[kDotTok];
+    int own[TOK];
+    const float* row[TOK];
 #pragma unroll
-    for (int j = 0; j < kDotTok; ++j) {      // past the end: the first token again, not stored
+    for (int j = 0; j < TOK; ++j) {      // past the end: the first token again, not stored
         const int64_t t = t0 + j < p.M ? t0 + j : t0;
         own[j] = t0 + j < p.M ? adapter_of(p, t) : p.adapters;
         row[j] = p.X + t * p.ldx;
     }
-    for (unsigned left = (1u << kDotTok) - 1; left != 0;) {
+    for (unsigned left = (1u << TOK) - 1; left != 0;) {
         // the first token left, and those with the same adapter
         int a = p.adapters;
 #pragma unroll
-        for (int j = kDotTok - 1; j >= 0; --j)
+        for (int j = TOK - 1; j >= 0; --j)
             if (left >> j & 1) a = own[j];
         unsigned now = 0;
 #pragma unroll
-        for (int j = 0; j < kDotTok; ++j)
+        for (int j = 0; j < TOK; ++j)
             if (own[j] == a) now |= 1u << j;
         left &= ~now;
         if (a == p.adapters) continue;
         const float* ar = p.A + ((int64_t)a * p.R + r) * p.K;
         const float* ar1 = r + 1 < p.R ? ar + p.K : ar;
-        float acc[kDotRows][kDotTok] = {};
+        float acc[kDotRows][TOK] = {};
 #pragma unroll 2
         for (int64_t k = k0 + lane * V; k < k1; k += 32 * V) {
             float w[kDotRows][V], x[V];
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) lora_down_dots(const LoraParam
                 w[1][0] = ar1[k];
             }
 #pragma unroll
-            for (int j = 0; j < kDotTok; ++j) {
+            for (int j = 0; j < TOK; ++j) {
                 if (!(now >> j & 1)) continue;       // the block's own, uniform
                 if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(row[j] + k);
                 else x[0] = row[j][k];
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) lora_down_dots(const LoraParam
 #pragma unroll
         for (int q = 0; q < kDotRows; ++q)
 #pragma unroll
-            for (int j = 0; j < kDotTok; ++j) {
+            for (int j = 0; j < TOK; ++j) {
                 float v = acc[q][j];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -207,6 +212,8 @@ template <int V, int G>
 __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraParams p) {
     extern __shared__ __align__(16) float stage[];   // [kTileStages][64 + 16 G][kTileRow]
     constexpr int kRows = kTileTok + 16 * G, kParts = kTileWarps / G;
+    griddep_launch_dependents();
+    griddep_wait();                                  // the grouping
     if ((int)blockIdx.x >= *p.ntiles) return;
     const int4 tile = p.tiles[blockIdx.x];
     const int a = tile.x, n = tile.z;
@@ -299,49 +306,62 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
 //
 // Y[t][n] = bias[n] + scale sum_r B[n][r] S[t][r]: a thread takes C columns,
 // kUpThreads apart (a warp writes 128 neighbouring bytes), keeps RK values of
-// each one's row of B in registers (loaded V at a time, as pairs of
-// neighbouring ranks) and walks its tokens, whose S the block has put in shared
+// each one's row of B in registers (as pairs of neighbouring ranks) and walks
+// its tokens, whose S the block has put in shared
 // memory (times the scale, the slices of K added in order); higher ranks take
 // more passes, which add to Y.  Bound by the writes of Y, for few tokens by the
 // latency of reading B.
 constexpr int kUpThreads = 128;
 
-// Tokens list[0..nt) (or t0, t0 + 1, .. where list is null) of adapter a.
+// The block's rows of B (C kUpThreads columns of Y, RK ranks) pass through
+// shared memory, `bs`: read straight into registers, a warp's 16-byte loads each
+// touched 32 lines.  Rows are padded by four values: a thread reads its own.
+template <int C, int RK>
+constexpr int up_smem() { return C * kUpThreads * (RK + 4); }
+
+// Tokens list[0..nt) (or t0, t0 + 1, .. where list is null) of adapter a;
+// the block's columns are n0 - threadIdx.x + 0 .. C kUpThreads - 1.
 template <int C, int RK, int V>
 __device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int32_t* list, int64_t t0,
-                                          int nt, int64_t n0, float (*s)[RK]) {
+                                          int nt, int64_t n0, float (*s)[RK], float* bs) {
     const int R = a == p.adapters ? 0 : p.R;
     const float scale = R > 0 && p.scale ? p.scale[a] : 1.0f;
     int r0 = 0;
     do {
-        uint64_t w[C][RK / 2];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int64_t n = n0 + c * kUpThreads;
-            const float* b = p.B + ((int64_t)a * p.N + n) * p.R + r0;
-#pragma unroll
-            for (int r = 0; r < RK; r += V) {
-                float x[V] = {};
-                if (n < p.N && r0 + r < R) {
-                    if constexpr (V == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(b + r);
-                    else {
-                        x[0] = b[r];
-                        if (r0 + r + 1 < R) x[1] = b[r + 1];
-                    }
+        if (R > 0) {
+            const int64_t first = n0 - threadIdx.x;
+            for (int e = threadIdx.x; e < C * kUpThreads * (RK / V); e += kUpThreads) {
+                const int row = e / (RK / V), r = (e % (RK / V)) * V;
+                const bool in = first + row < p.N && r0 + r < R;
+                const float* src = p.B + ((int64_t)a * p.N + (in ? first + row : 0)) * p.R + (in ? r0 + r : 0);
+                float* dst = bs + row * (RK + 4) + r;
+                if constexpr (V == 4) cp_async16(dst, src, in);
+                else {
+                    cp_async4(dst, src, in);
+                    cp_async4(dst + 1, in && r0 + r + 1 < R ? src + 1 : src, in && r0 + r + 1 < R);
                 }
-#pragma unroll
-                for (int v = 0; v < V; v += 2)
-                    w[c][(r + v) / 2] = pack_f32x2(__float_as_uint(x[v]), __float_as_uint(x[v + 1]));
             }
         }
-        for (int e = threadIdx.x; e < nt * RK; e += kUpThreads) {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        griddep_wait();                      // S (B and the indices are the caller's)
+        for (int e = threadIdx.x * V; e < nt * RK; e += kUpThreads * V) {
             const int t = e / RK, r = r0 + e % RK;
-            float v = 0.0f;
+            float v[V] = {};
             if (r < R) {
                 const float* src = p.S + (list ? list[t] : t0 + t) * p.R + r;
-                for (int q = 0; q < p.slices; ++q) v += src[q * p.M * p.R];
+#pragma unroll 4
+                for (int q = 0; q < p.slices; ++q, src += p.M * p.R) {
+                    if constexpr (V == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                    } else {
+                        v[0] += src[0];
+                        if (r + 1 < R) v[1] += src[1];
+                    }
+                }
             }
-            s[t][e % RK] = scale * v;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[t][e % RK + i] = scale * v[i];
         }
         float bias[C];
 #pragma unroll
@@ -349,8 +369,21 @@ __device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int3
             const int64_t n = n0 + c * kUpThreads;
             bias[c] = p.bias && n < p.N ? p.bias[n] : 0.0f;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-#pragma unroll 2
+        // the columns' values of B, as pairs of neighbouring ranks
+        uint64_t w[C][RK / 2] = {};
+        if (R > 0)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int r = 0; r < RK; r += 4) {
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(
+                        bs + (threadIdx.x + c * kUpThreads) * (RK + 4) + r);
+                    w[c][r / 2] = x.x;
+                    w[c][r / 2 + 1] = x.y;
+                }
+#pragma unroll 4
         for (int t = 0; t < nt; ++t) {
             float* y = p.Y + (list ? list[t] : t0 + t) * p.ldy + n0;
             uint64_t v[C];
@@ -377,17 +410,19 @@ __device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int3
     } while (r0 < R);
 }
 
-// Few tokens: four neighbouring ones per block, runs of one adapter together.
-template <int V>
+// Few tokens: TOK neighbouring ones per block, runs of one adapter together.
+template <int V, int TOK>
 __global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
-    __shared__ __align__(16) float s[kDotTok][32];
-    const int64_t t0 = (int64_t)blockIdx.x * kDotTok, end = min(p.M, t0 + kDotTok);
+    __shared__ __align__(16) float s[TOK][32];
+    __shared__ __align__(16) float bs[up_smem<1, 32>()];
+    griddep_launch_dependents();
+    const int64_t t0 = (int64_t)blockIdx.x * TOK, end = min(p.M, t0 + TOK);
     const int64_t n0 = (int64_t)blockIdx.y * kUpThreads + threadIdx.x;
     for (int64_t t = t0; t < end;) {
         const int a = adapter_of(p, t);
         int nt = 1;
         while (t + nt < end && adapter_of(p, t + nt) == a) ++nt;
-        up_tokens<1, 32, V>(p, a, nullptr, t, nt, n0, s);
+        up_tokens<1, 32, V>(p, a, nullptr, t, nt, n0, s, bs);
         t += nt;
     }
 }
@@ -396,10 +431,13 @@ __global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
 template <int V>
 __global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p) {
     __shared__ __align__(16) float s[kTileTok][16];
+    __shared__ __align__(16) float bs[up_smem<2, 16>()];
+    griddep_launch_dependents();
+    griddep_wait();                          // the grouping and S
     if ((int)blockIdx.x >= *p.ntiles) return;
     const int4 tile = p.tiles[blockIdx.x];
-    up_tokens<4, 16, V>(p, tile.x, p.order + tile.y, 0, tile.z,
-                        (int64_t)blockIdx.y * (4 * kUpThreads) + threadIdx.x, s);
+    up_tokens<2, 16, V>(p, tile.x, p.order + tile.y, 0, tile.z,
+                        (int64_t)blockIdx.y * (2 * kUpThreads) + threadIdx.x, s, bs);
 }
 
 // Tiles that the grouping makes at most.
@@ -407,12 +445,33 @@ int64_t max_tiles(int64_t M, int64_t adapters) {
     return M / kTileTok + (M < adapters + 1 ? M : adapters + 1);
 }
 
+// Launch as a programmatic dependent of the kernel ahead in the stream (pdl):
+// this call's own, whose results the kernel waits for itself.
+template <typename Kern>
+cudaError_t launch_after(Kern kern, dim3 grid, int threads, int smem, bool pdl, const LoraParams& p,
+                         cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int V>
 cudaError_t launch_down(const LoraParams& p, cudaStream_t stream) {
     if (p.M <= kFewTokens) {
         const unsigned rows = (p.R + kDotWarps * kDotRows - 1) / (kDotWarps * kDotRows);
-        lora_down_dots<V><<<dim3((unsigned)((p.M + kDotTok - 1) / kDotTok), rows, p.slices),
-                            kDotWarps * 32, 0, stream>>>(p);
+        if (p.M <= kSingleTokens)
+            lora_down_dots<V, 1><<<dim3((unsigned)p.M, rows, p.slices), kDotWarps * 32, 0, stream>>>(p);
+        else
+            lora_down_dots<V, kDotTok><<<dim3((unsigned)((p.M + kDotTok - 1) / kDotTok), rows, p.slices),
+                                         kDotWarps * 32, 0, stream>>>(p);
         return cudaGetLastError();
     }
     const dim3 grid((unsigned)max_tiles(p.M, p.adapters), p.slices);
@@ -420,20 +479,22 @@ cudaError_t launch_down(const LoraParams& p, cudaStream_t stream) {
     auto go = [&](auto kern, int smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, kTileWarps * 32, smem, stream>>>(p);
-        return cudaGetLastError();
+        return launch_after(kern, grid, kTileWarps * 32, smem, true, p, stream);
     };
     if (p.R <= 16) return go(lora_down_tiles<V, 1>, tile_smem(1));
     if (p.R <= 32) return go(lora_down_tiles<V, 2>, tile_smem(2));
     return go(lora_down_tiles<V, 4>, tile_smem(4));
 }
 
-// Slices of K: enough blocks for every SM to have two (of the dots, which are
-// bound by latency, four), slices of at least 256 values, at most 16 (the up
-// step reads each).
+// Slices of K: enough for four blocks per SM (of the dots, which are bound by
+// latency; of the tiles, two of which run at a time, so that an uneven last
+// round costs little), at least 256 values each, at most 16 (the up step reads
+// each).
 int64_t slices_of(int64_t M, int64_t K, int64_t R, int sms) {
-    const int64_t blocks = M <= kFewTokens ? (M + kDotTok - 1) / kDotTok * ((R + 15) / 16) : M / kTileTok;
-    int64_t n = ((M <= kFewTokens ? 4 : 2) * sms + blocks - 1) / blocks;
+    const int64_t blocks = M <= kSingleTokens ? M * ((R + 15) / 16)
+                           : M <= kFewTokens  ? (M + kDotTok - 1) / kDotTok * ((R + 15) / 16)
+                                              : M / kTileTok;
+    int64_t n = (4 * sms + blocks - 1) / blocks;
     n = n > 16 ? 16 : n;
     const int64_t most = (K + 255) / 256;
     return n < most ? n : most;
@@ -492,10 +553,13 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
     p.ntiles = reinterpret_cast<int32_t*>(ws + s_bytes + o_bytes);
     p.tiles = reinterpret_cast<int4*>(ws + s_bytes + o_bytes + 16);
     p.Y = Y; p.ldy = ldy; p.err = d->err;
+    // The order, each step launched as a programmatic dependent of the one
+    // before: X's pieces and the grouping, side by side; the adapters' steps; the
+    // GEMM.  For few tokens the dots come first, the pieces are made beside them.
     cudaError_t e = cudaSuccess;
     if (!few) {
-        lora_group<<<1, 1024, 0, stream>>>(p);
-        e = cudaGetLastError();
+        if (K > 0) e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);
+        if (e == cudaSuccess) e = launch_after(lora_group, dim3(1), 1024, 0, K > 0, p, stream);
         if (e != cudaSuccess) return from_cuda(e);
     }
     if (adapted) {
@@ -506,21 +570,27 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
         if (e != cudaSuccess) return from_cuda(e);
     }
     const bool wide = R % 4 == 0 && aligned16(B);
+    const bool streamed = few_rows_ok(M, W, ldw);
+    if (few && K > 0) {
+        e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream, adapted);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
+    const bool after = adapted || !few || K > 0;
     if (few) {
-        const dim3 grid((unsigned)((M + kDotTok - 1) / kDotTok), (unsigned)((N + kUpThreads - 1) / kUpThreads));
-        if (wide) lora_up_few<4><<<grid, kUpThreads, 0, stream>>>(p);
-        else lora_up_few<2><<<grid, kUpThreads, 0, stream>>>(p);
+        auto go = [&](auto kern, int tok) {
+            const dim3 grid((unsigned)((M + tok - 1) / tok), (unsigned)((N + kUpThreads - 1) / kUpThreads));
+            return launch_after(kern, grid, kUpThreads, 0, after, p, stream);
+        };
+        e = M <= kSingleTokens ? (wide ? go(lora_up_few<4, 1>, 1) : go(lora_up_few<2, 1>, 1))
+                               : (wide ? go(lora_up_few<4, kDotTok>, kDotTok) : go(lora_up_few<2, kDotTok>, kDotTok));
     } else {
         const dim3 grid((unsigned)max_tiles(M, p.adapters),
-                        (unsigned)((N + 4 * kUpThreads - 1) / (4 * kUpThreads)));
-        if (wide) lora_up_tiles<4><<<grid, kUpThreads, 0, stream>>>(p);
-        else lora_up_tiles<2><<<grid, kUpThreads, 0, stream>>>(p);
+                        (unsigned)((N + 2 * kUpThreads - 1) / (2 * kUpThreads)));
+        e = wide ? launch_after(lora_up_tiles<4>, grid, kUpThreads, 0, after, p, stream)
+                 : launch_after(lora_up_tiles<2>, grid, kUpThreads, 0, after, p, stream);
     }
-    e = cudaGetLastError();
     if (e != cudaSuccess || K == 0) return from_cuda(e);
-    e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);
-    if (e != cudaSuccess) return from_cuda(e);
-    if (few_rows_ok(M, W, ldw)) {
+    if (streamed) {
         TcGemmParams q = {};
         q.alpha = q.beta = 1.0f;
         q.C = Y; q.ldc = ldy;
