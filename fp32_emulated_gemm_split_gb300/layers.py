@@ -119,18 +119,22 @@ def _act(act):
 
 class GatedWeights:
     """The gate and up weights of a gated feed-forward with their packed
-    pieces (``emu_gated_pack``).  The pieces hold the values that the weights
-    had then: pack again after changing them."""
+    pieces (``emu_gated_pack``).  The kernels read one or the other, so a
+    weight changed in place since then is refused: pack again."""
 
-    __slots__ = ("Wg", "Wu", "pieces", "F", "K", "rows", "device", "_weights", "_pieces")
+    __slots__ = ("Wg", "Wu", "pieces", "F", "K", "rows", "_weights", "_pieces", "_versions")
 
     def __init__(self, Wg, Wu, pieces, ldg, ldu, rows):
         self.Wg, self.Wu, self.pieces, self.rows = Wg, Wu, pieces, rows
         self.F, self.K = Wg.shape
-        self.device = Wg.get_device()
+        self._versions = Wg._version, Wu._version
         # the entry points' arguments (the tensors above keep the memory)
         self._weights = (Wg.data_ptr(), ldg, Wu.data_ptr(), ldu)
         self._pieces = (pieces.data_ptr(), pieces.size(2))
+
+    def check(self):
+        if (self.Wg._version, self.Wu._version) != self._versions:
+            raise ValueError("a weight was changed in place since emu_gated_pack: pack again")
 
 
 def emu_gated_pack(Wg, Wu, stream=None) -> GatedWeights:
@@ -152,6 +156,7 @@ def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None, stream=None)
     """H = act(X Wg^T) * (X Wu^T), or (H, G, U) with save=True: the two
     products as well, for ``emu_gated_bwd``."""
     a = _act(act)
+    w.check()
     F, K = w.F, w.K
     ldx = _rows(X, "X", None, K)
     M = X.shape[0]
@@ -178,6 +183,7 @@ def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_d
     """(dX, dWg, dWu) from the gradient dH of H and what ``emu_gated`` saved;
     None in the place of a gradient that is not needed."""
     a = _act(act)
+    w.check()
     M, F, K = X.size(0), w.F, w.K
     ldx, lddh = _rows(X, "X", cols=K), _rows(dH, "dH", M, F)
     ldg = _rows(G, "G", M, F)
@@ -199,13 +205,15 @@ def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_d
 
 class LoraWeights:
     """The weight (N x K) and bias of a shared projection with the weight's
-    pieces (``emu_lora_pack``); pack again after changing the weight."""
+    pieces (``emu_lora_pack``).  The kernels read one or the other, so a weight
+    changed in place since then is refused: pack again."""
 
-    __slots__ = ("W", "bias", "pieces", "N", "K", "_weight")
+    __slots__ = ("W", "bias", "pieces", "N", "K", "_weight", "_version")
 
     def __init__(self, W, bias, pieces, ldw):
         self.W, self.bias, self.pieces = W, bias, pieces
         self.N, self.K = W.shape
+        self._version = W._version
         # the entry point's arguments (the tensors above keep the memory)
         self._weight = (W.data_ptr(), ldw, pieces.data_ptr(), pieces.size(2),
                         None if bias is None else bias.data_ptr())
@@ -227,6 +235,8 @@ def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None, stream=None):
     """Y = X W^T + bias + scale_i (X A_i^T) B_i^T with i = index[row] (-1: no
     adapter); A is adapters x R x K, B adapters x N x R, scale `adapters`
     values, index int32."""
+    if w.W._version != w._version:
+        raise ValueError("the weight was changed in place since emu_lora_pack: pack again")
     N, K = w.N, w.K
     ldx = _rows(X, "X", None, K)
     M = X.shape[0]

@@ -2,6 +2,8 @@
 every element within the bound that the number of roundings gives
 (layer_ref.py), over row counts from one up, odd widths, strides, each
 activation; the gradients against the formula and against differences."""
+import gc
+
 import pytest
 
 import layer_ref as ref
@@ -17,7 +19,8 @@ REL = 1.5e-6
 
 @pytest.fixture(scope="module")
 def emu():
-    return emu_module()
+    yield emu_module()
+    gc.collect()                                     # tensors that graphs and tracebacks still hold
 
 
 def _make(M, K, F, seed, pad=0, offset=0):

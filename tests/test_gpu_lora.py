@@ -1,5 +1,7 @@
 """The adapters of many requests beside a shared projection, on the GPU,
 against their definition in 64 bits."""
+import gc
+
 import pytest
 
 import layer_ref as ref
@@ -12,7 +14,8 @@ REL = 1.5e-6
 
 @pytest.fixture(scope="module")
 def emu():
-    return emu_module()
+    yield emu_module()
+    gc.collect()                                     # tensors that graphs and tracebacks still hold
 
 
 def _make(M, K, N, R, n, seed, order="random", bias=True, scale=True):

@@ -1,5 +1,7 @@
 """Norm and rotation of query and key heads on the GPU, forward and backward,
 against the definition in 64 bits."""
+import gc
+
 import pytest
 
 import layer_ref as ref
@@ -10,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.fixture(scope="module")
 def emu():
-    return emu_module()
+    yield emu_module()
+    gc.collect()                                     # tensors that graphs and tracebacks still hold
 
 
 def _make(T, Hq, Hk, D, rot, dtype, seed, rows=400):
