@@ -53,39 +53,40 @@ template <int BN, bool GATED>
 struct Cfg {
     static constexpr bool stacked = BN <= 32;
     static constexpr int d_cols = stacked ? 3 * BN : BN;
-    // The K blocks are dealt in turn to `lanes` pipelines that share nothing
-    // but the producers and the accumulator warps: each has its own FP32
-    // buffers, group of eight split warps, MMA issuer, stages of W's and X's
-    // pieces and partial, so that every barrier is waited for in the order of
-    // its phases.
-    // One group's latencies overlap with the other's arithmetic, and one
-    // issuing thread would need about 2100 cycles for a block's waits, MMAs and
-    // commits beside the busy split warps (the stream 1400).  At BN = 128 and
-    // 160 the nine products take 2300 or 2900 cycles of the tensor core anyway.
-    static constexpr int lanes = BN >= 128 ? 1 : 2;
-    // tensor memory: partials, then W's pieces (96 columns per K block), both
-    // per pipeline
-    static constexpr int partials = BN >= 128 ? 2 : 1;
-    static constexpr int a_stages = BN == 32 ? 1 : 2;
-    static constexpr int a_base = lanes * partials * d_cols;
-    static_assert(a_base + lanes * a_stages * 3 * kPieceCols <= 512, "tensor memory overflow");
+    // All split warps work on one K block after another, each of them on its
+    // own (there is no barrier among them), into a ring of stages in tensor
+    // memory.  Two threads issue the MMAs, of the even and of the odd blocks
+    // (one would need about 2100 cycles for a block's waits, MMAs and commits
+    // beside the busy split warps, the stream 1400); the rings that they wait on
+    // have even counts, so each has stages of its own and meets every barrier's
+    // phases in order.  At BN = 128 and 160 the nine products take 2300 or 2900
+    // cycles of the tensor core anyway: one issuer, and half the split warps.
+    static constexpr int issuers = BN >= 128 ? 1 : 2;
+    static constexpr int split_warps = BN >= 128 ? 8 : 16;
+    // tensor memory: partials, then W's pieces (96 columns per K block)
+    static constexpr int partials = 2;
+    static constexpr int a_stages = BN == 16 || BN == 64 ? 4 : 2;
+    static_assert(a_stages % issuers == 0 && partials % issuers == 0, "an issuer's own stages");
+    static constexpr int a_base = partials * d_cols;
+    static_assert(a_base + a_stages * 3 * kPieceCols <= 512, "tensor memory overflow");
     // shared memory: FP32 buffers (as many as fit: the stream's bytes in
     // flight), stages of X's pieces, the gated hand-over
-    static constexpr int a_bufs = BN == 16 || BN == 128 ? 3 : 2;                          // per pipeline
+    static constexpr int a_bufs = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 3 : 2;
     static constexpr int b_tile = BN * kTcBKBytes;
-    static constexpr int b_stages = BN <= 32 ? 2 : BN == 64 ? 1 : 2;    // per pipeline
+    static constexpr int b_stages = BN <= 32 ? 4 : 2;
+    static_assert(b_stages % issuers == 0, "an issuer's own stages");
     // (the gated hand-over in `passes` of BN / passes rows of X)
     static constexpr int acc_warps = BN == 16 ? 4 : BN == 160 ? 16 : 8;
     static constexpr int acc_cols = BN / (acc_warps / 4);
     static constexpr int passes = BN <= 64 ? 1 : acc_warps / 4;
     static constexpr int ex_bytes = GATED ? 128 * BN / passes * 4 : 0;
-    static constexpr int smem = lanes * a_bufs * kABuf + lanes * b_stages * 3 * b_tile + ex_bytes + 2048;
+    static constexpr int smem = a_bufs * kABuf + b_stages * 3 * b_tile + ex_bytes + 2048;
     static_assert(smem <= kSmemMax, "shared memory overflow");
     // warps: 0 TMA of W and tensor-memory allocation, 1 TMA of X's pieces, 2
     // (and 3) MMA, then the accumulators, four per column group, and the split
     // warps
     static constexpr int acc0 = 4, split0 = acc0 + acc_warps;
-    static constexpr int threads = 32 * (split0 + 8 * lanes);
+    static constexpr int threads = 32 * (split0 + split_warps);
 };
 
 __device__ __forceinline__ unsigned load_acquire(const unsigned* a) {
@@ -94,36 +95,34 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* a) {
     return v;
 }
 
-// 32 elements of row r of one swizzled 128 x 32 FP32 box, the three pieces'
-// 16 columns each at `col` (piece i at col + 32 i).  The 32 lanes read the
-// same 16-byte chunk of 32 rows, which the swizzle spreads over the banks.
-// One test per 16 elements keeps infinities and NaNs off the packed path.
-__device__ __forceinline__ void split_to_tmem(const uint8_t* box, uint32_t col, int r) {
-    const uint8_t* row = box + r * 128;
+// 16 elements (quarter kq of the K block's 64) of row r of the two swizzled 128
+// x 32 FP32 boxes at `box`, the three pieces' 8 columns each at `col` (piece i
+// at col + 32 i).  The 32 lanes read the same 16-byte chunk of 32 rows, which
+// the swizzle spreads over the banks.  One test per 16 elements keeps
+// infinities and NaNs off the packed path.
+__device__ __forceinline__ void split_to_tmem(const uint8_t* box, uint32_t col, int r, int kq) {
+    const uint8_t* row = box + (kq >> 1) * kBox + r * 128;
+    float x[16];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float x[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(row + (((4 * half + c) ^ (r & 7)) << 4));
-            x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
-        }
-        float m = max_abs_nan(x[0], x[1]);
-#pragma unroll
-        for (int j = 2; j < 16; ++j) m = max_abs_nan(m, x[j]);
-        uint32_t w0[8], w1[8], w2[8];
-        if (m < __uint_as_float(0x7F800000u)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) split_finite_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) split_bf16x3_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
-        }
-        __syncwarp();
-        tmem_st_32x32b_x8(col + 8 * half, w0);
-        tmem_st_32x32b_x8(col + 8 * half + 32, w1);
-        tmem_st_32x32b_x8(col + 8 * half + 64, w2);
+    for (int c = 0; c < 4; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(row + (((4 * (kq & 1) + c) ^ (r & 7)) << 4));
+        x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
     }
+    float m = max_abs_nan(x[0], x[1]);
+#pragma unroll
+    for (int j = 2; j < 16; ++j) m = max_abs_nan(m, x[j]);
+    uint32_t w0[8], w1[8], w2[8];
+    if (m < __uint_as_float(0x7F800000u)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split_finite_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split_bf16x3_pair(x[2 * j], x[2 * j + 1], w0[j], w1[j], w2[j]);
+    }
+    __syncwarp();
+    tmem_st_32x32b_x8(col, w0);
+    tmem_st_32x32b_x8(col + 32, w1);
+    tmem_st_32x32b_x8(col + 64, w2);
 }
 
 // The gated form's second weight.
@@ -142,12 +141,12 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    uint8_t* bst = smem + C::lanes * C::a_bufs * kABuf;              // X's pieces
-    float* ex = reinterpret_cast<float*>(bst + C::lanes * C::b_stages * 3 * C::b_tile);
+    uint8_t* bst = smem + C::a_bufs * kABuf;              // X's pieces
+    float* ex = reinterpret_cast<float*>(bst + C::b_stages * 3 * C::b_tile);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ex) + C::ex_bytes);
     // FP32 buffer full / free, X's stage full / free, W's pieces ready / free,
     // partial full / free
-    constexpr int L = C::lanes, NF = L * C::a_bufs, NB = L * C::b_stages, NA = L * C::a_stages, ND = L * C::partials;
+    constexpr int NF = C::a_bufs, NB = C::b_stages, NA = C::a_stages, ND = C::partials;
     const uint32_t afull0 = smem_u32(bars), afree0 = afull0 + 8 * NF;
     const uint32_t bfull0 = afree0 + 8 * NF, bfree0 = bfull0 + 8 * NB;
     const uint32_t pready0 = bfree0 + 8 * NB, pfree0 = pready0 + 8 * NA;
@@ -167,14 +166,14 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int i = 0; i < NF; ++i) {
             mbar_init(afull0 + 8 * i, 1);
-            mbar_init(afree0 + 8 * i, 8);                 // the warps of a split group
+            mbar_init(afree0 + 8 * i, C::split_warps);
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(bfull0 + 8 * i, 1);
             mbar_init(bfree0 + 8 * i, 1);
         }
         for (int i = 0; i < NA; ++i) {
-            mbar_init(pready0 + 8 * i, 8);
+            mbar_init(pready0 + 8 * i, C::split_warps);
             mbar_init(pfree0 + 8 * i, 1);
         }
         for (int i = 0; i < ND; ++i) {
@@ -199,11 +198,9 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_launch_dependents();
-    // Block g runs in pipeline g % L as its block n = g / L, in the stage
-    // n % count of that pipeline's rings (slot() of them all), whose barriers
-    // are then in phase n / count.
-    auto slot_of = [](uint32_t g, int count) { return (g % L) * count + (g / L) % count; };
-    auto phase_of = [](uint32_t g, int count) { return (g / L / count) & 1; };
+    // Block g's place in a ring of `count`, and the phase of its barriers there.
+    auto slot_of = [](uint32_t g, int count) { return g % count; };
+    auto phase_of = [](uint32_t g, int count) { return (g / count) & 1; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -258,11 +255,11 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             if (!ok) *abort_flag = 1;
         }
     } else if (warp < C::acc0) {
-        if (lane == 0 && warp - 2 < L) {
+        if (lane == 0 && warp - 2 < C::issuers) {
             // ----------------------------------------------------- MMA issuers
             // (not stacked: as many columns as there are rows of X, in 16s)
             const uint32_t idesc = make_idesc(1u, 128, C::stacked ? C::d_cols : (p.N + 15) / 16 * 16);
-            for (uint32_t g = warp - 2; g < blocks; g += L) {
+            for (uint32_t g = warp - 2; g < blocks; g += C::issuers) {
                 const uint32_t s = slot_of(g, C::b_stages), t = slot_of(g, C::a_stages);
                 const uint32_t b = slot_of(g, C::partials);
                 if (!mbar_wait(dfree0 + 8 * b, phase_of(g, C::partials) ^ 1, p.err, kDevErrTimeout) ||
@@ -312,11 +309,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         }
     } else if (warp >= C::split0) {
         // ---------------------------------------------------------- split warps
-        const int w = warp - C::split0, group = w >> 3;
-        const int khalf = (w >> 2) & 1;                   // 32-element half of the 64
+        const int w = warp - C::split0;
         const int r = 32 * (warp & 3) + lane;             // row: this warp's TMEM lanes
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        for (uint32_t g = group; g < blocks; g += L) {
+        for (uint32_t g = 0; g < blocks; ++g) {
             const uint32_t f = slot_of(g, C::a_bufs), t = slot_of(g, C::a_stages);
             if (!mbar_wait(afull0 + 8 * f, phase_of(g, C::a_bufs), p.err, kDevErrTimeout) ||
                 !mbar_wait(pfree0 + 8 * t, phase_of(g, C::a_stages) ^ 1, p.err, kDevErrTimeout) ||
@@ -326,8 +322,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             }
             __syncwarp();
             tc_fence_after();
-            split_to_tmem(smem + f * kABuf + khalf * kBox,
-                          (tmem + C::a_base + t * 3 * kPieceCols + 16 * khalf) | lanes, r);
+            const uint32_t col = (tmem + C::a_base + t * 3 * kPieceCols) | lanes;
+#pragma unroll
+            for (int kq = w >> 2; kq < 4; kq += C::split_warps / 4)
+                split_to_tmem(smem + f * kABuf, col + 8 * kq, r, kq);
             tmem_st_wait();
             tc_fence_before();                            // tensor-memory stores -> the MMA
             __syncwarp();
