@@ -110,8 +110,17 @@ emu_status_t gemm_on_pieces(int mode, const PieceSet& a, const PieceSet& b, int6
 // before that split has ended.
 constexpr int64_t kFewRows = 160;
 bool few_rows_ok(int64_t M, const float* W, int64_t ldw);
+// plane_rows: rows from one plane of X's pieces to the next (0: M).
 emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
-                           int64_t N, int64_t K, const void* xp, int64_t ldp, TcGemmParams p,
-                           DeviceState* d, cudaStream_t stream);
+                           int64_t N, int64_t K, const void* xp, int64_t ldp, int64_t plane_rows,
+                           TcGemmParams p, DeviceState* d, cudaStream_t stream);
+
+// The last M % 256 rows of M > 256, where they are few enough that streaming
+// the FP32 weights for them costs less than one more row of 256-row tiles,
+// mostly empty (0: run all rows in tiles).  Per F K weights (two of F x K): a
+// row of tiles takes 3.8e-6 us, the stream 1.3e-6 us up to 32 rows, 2.4e-6 up
+// to 64 and as much as the tiles at 128, and about 6 us to start (measured at
+// 2048 x 8192: 65 us, 28, 46, 65).
+inline int64_t ragged_rows(int64_t M) { return M > 256 && M % 256 <= 64 ? M % 256 : 0; }
 
 }  // namespace emu

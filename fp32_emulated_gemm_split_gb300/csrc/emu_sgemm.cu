@@ -391,15 +391,15 @@ bool few_rows_ok(int64_t M, const float* W, int64_t ldw) {
 constexpr int kFewRowsHandover = 6;
 
 emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
-                           int64_t N, int64_t K, const void* xp, int64_t ldp, TcGemmParams p,
-                           DeviceState* d, cudaStream_t stream) {
+                           int64_t N, int64_t K, const void* xp, int64_t ldp, int64_t plane_rows,
+                           TcGemmParams p, DeviceState* d, cudaStream_t stream) {
     // the narrowest tile that holds the rows: the tensor core's time and the
     // pieces' traffic grow with it
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 160;
     CUtensorMap mapA, mapA2, mapB;
     emu_status_t st = make_plane_map(&mapA, W, true, N, K, ldw, 1, 32, W2 ? 64 : 128);
     if (st == EMU_OK && W2) st = make_plane_map(&mapA2, W2, true, N, K, ldw2, 1, 32, 64);
-    if (st == EMU_OK) st = make_plane_map(&mapB, xp, false, M, K, ldp, 3, 64, bn);
+    if (st == EMU_OK) st = make_plane_map(&mapB, xp, false, M, K, ldp, 3, 64, bn, plane_rows);
     if (st != EMU_OK) return st;
     p.err = d->err;
     p.M = (int)N; p.N = (int)M; p.K = (int)K;

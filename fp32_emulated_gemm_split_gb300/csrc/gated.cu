@@ -123,27 +123,39 @@ emu_status_t gated_forward(int act, int64_t M, int64_t F, int64_t K, const float
     if (st != EMU_OK) return st;
     cudaError_t e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream);
     if (e != cudaSuccess) return from_cuda(e);
+    // rows that stream the FP32 weights: all of them, or what whole tiles leave
+    const int64_t few = !few_rows_ok(1, Wg, ldwg) || !few_rows_ok(1, Wu, ldwu) ? 0
+                        : M <= kFewRows                                        ? M
+                                                                               : ragged_rows(M);
+    const int64_t rows = M - few;
     TcGemmParams p = {};
     p.act = act;
+    if (few > 0) {
+        p.C = H + rows * ldh; p.ldc = ldh;
+        if (G) {
+            p.G = G + rows * ldg; p.U = U + rows * ldg; p.ldg = ldg;
+        }
+        st = gemm_few_rows(Wg, ldwg, Wu, ldwu, few, F, K, static_cast<uint16_t*>(d->ws) + rows * ldp, ldp,
+                           M, p, d, stream);
+        if (st != EMU_OK || rows == 0) return st;
+    }
     p.C = H; p.ldc = ldh;
     p.G = G; p.U = U; p.ldg = ldg;
-    if (few_rows_ok(M, Wg, ldwg) && few_rows_ok(M, Wu, ldwu))
-        return gemm_few_rows(Wg, ldwg, Wu, ldwu, M, F, K, d->ws, ldp, p, d, stream);
     CUtensorMap mapA, mapB;
-    st = make_plane_map(&mapA, d->ws, false, M, K, ldp, 3, 64, 128);
+    st = make_plane_map(&mapA, d->ws, false, rows, K, ldp, 3, 64, 128, M);
     if (st != EMU_OK) return st;
     st = make_plane_map(&mapB, Wp, false, 2 * Fp, K, ldwp, 3, 64, 128);
     if (st != EMU_OK) return st;
     p.err = d->err;
-    p.M = (int)M; p.N = (int)F; p.K = (int)K;
+    p.M = (int)rows; p.N = (int)F; p.K = (int)K;
     p.num_kb = (int)((K + 63) / 64);
-    p.tiles_m = (int)((M + 255) / 256);
+    p.tiles_m = (int)((rows + 255) / 256);
     p.tiles_n = (int)((F + 127) / 128);
     p.up_row = (int)Fp;
     CUtensorMap mapH = mapB, mapG = mapB, mapU = mapB;   // placeholders where stored directly
-    p.tma_store = make_c_map(&mapH, H, M, F, ldh) ? 1 : 0;
+    p.tma_store = make_c_map(&mapH, H, rows, F, ldh) ? 1 : 0;
     if (G)
-        p.tma_gu = make_c_map(&mapG, G, M, F, ldg) && make_c_map(&mapU, U, M, F, ldg) ? 1 : 0;
+        p.tma_gu = make_c_map(&mapG, G, rows, F, ldg) && make_c_map(&mapU, U, rows, F, ldg) ? 1 : 0;
     st = plan_tail(p, gemm_gated_clusters(d->sms), handover_half_blocks(kModeBf16x9), 256, 256, d);
     if (st != EMU_OK) return st;
     return from_cuda(launch_gemm_gated(mapA, mapB, mapH, mapG, mapU, p, d->sms, stream));

@@ -570,7 +570,6 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
         if (e != cudaSuccess) return from_cuda(e);
     }
     const bool wide = R % 4 == 0 && aligned16(B);
-    const bool streamed = few_rows_ok(M, W, ldw);
     if (few && K > 0) {
         e = launch_split_pieces(kModeBf16x9, X, M, K, ldx, 0, d->ws, ldp, stream, adapted);
         if (e != cudaSuccess) return from_cuda(e);
@@ -590,12 +589,17 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
                  : launch_after(lora_up_tiles<2>, grid, kUpThreads, 0, after, p, stream);
     }
     if (e != cudaSuccess || K == 0) return from_cuda(e);
-    if (streamed) {
+    // rows that stream the FP32 weight: all of them, or what whole tiles leave
+    const int64_t stream_rows = !few_rows_ok(1, W, ldw) ? 0 : M <= kFewRows ? M : ragged_rows(M);
+    const int64_t rows = M - stream_rows;
+    if (stream_rows > 0) {
         TcGemmParams q = {};
         q.alpha = q.beta = 1.0f;
-        q.C = Y; q.ldc = ldy;
-        return gemm_few_rows(W, ldw, nullptr, 0, M, N, K, d->ws, ldp, q, d, stream);
+        q.C = Y + rows * ldy; q.ldc = ldy;
+        st = gemm_few_rows(W, ldw, nullptr, 0, stream_rows, N, K,
+                           static_cast<uint16_t*>(d->ws) + rows * ldp, ldp, M, q, d, stream);
+        if (st != EMU_OK || rows == 0) return st;
     }
-    return gemm_on_pieces(kModeBf16x9, PieceSet{d->ws, ldp, 0, 0}, PieceSet{Wp, ldwp, 0, 0}, M, N, K,
+    return gemm_on_pieces(kModeBf16x9, PieceSet{d->ws, ldp, M, 0}, PieceSet{Wp, ldwp, 0, 0}, rows, N, K,
                           1.0f, 1.0f, Y, ldy, d, stream);
 }
