@@ -297,16 +297,17 @@ __device__ __forceinline__ void load_weight(const float* w, const Chunk<V, PAIRS
 // Rounds of heads in flight per warp: shared memory holds them, so that HBM's
 // latency is covered by bytes on the way and not by registers.
 constexpr int kWarps = 8;                    // per block
-template <int BYTES, int NC, bool BWD>
+template <int BYTES, int NC, bool BWD, int HU>
 struct Ring {
     static constexpr bool used = BYTES >= 4;         // (cp.async copies 4, 8 or 16 bytes)
-    static constexpr int per_round = (BWD ? 4 : 2) * NC;             // copies per lane
-    static constexpr int depth = NC > 1 ? (BWD ? 2 : 3) : BWD ? 4 : 6;
+    static constexpr int per_head = (BWD ? 4 : 2) * NC;              // copies per lane
+    static constexpr int per_round = per_head * HU;
+    static constexpr int depth = 3;
     static constexpr int bytes = used ? depth * per_round * BYTES * kWarps * 32 : 0;
 };
 
-// V pairs per chunk, NC chunks per lane.  The rounds of heads (32 / lanes at a
-// time) of all tokens are shared evenly by the warps in consecutive ranges,
+// V pairs per chunk, NC chunks per lane and head, HU heads per lane and round.
+// The rounds of heads (32 / lanes times HU at a time) of all tokens are shared evenly by the warps in consecutive ranges,
 // first those of one side and then of the other.
 //
 // Forward, with the weights folded into the cosines and sines once per token:
@@ -314,17 +315,17 @@ struct Ring {
 //
 // FULL: every lane has both of its chunks in every round (the head's chunks
 // are the lanes of a group, and whole rounds make up both sides): no guards.
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
 __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParams p) {
     extern __shared__ __align__(16) uint8_t smem[];              // the rings; backward: then [warp][2][D]
     constexpr int E = NC * V, H = E / 2;                         // pairs a lane holds, packed
     static_assert(E % 2 == 0, "pairs of values");
     constexpr int B = sizeof(T) * V;
-    using R = Ring<B, NC, BWD>;
+    using R = Ring<B, NC, BWD, HU>;
     constexpr uint32_t kStep = kWarps * 32 * B;                  // from one copy's slots to the next
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / p.lanes, pos_in = lane % p.lanes;   // head of the warp's group, lane in it
-    const int at_once = 32 / p.lanes;
+    const int groups = 32 / p.lanes, at_once = groups * HU;      // heads of a warp's round: u groups + sub
     const int64_t self = (int64_t)blockIdx.x * kWarps + warp, warps = (int64_t)gridDim.x * kWarps;
     const float inv_d = 1.0f / p.D;
     uint8_t* mine = smem + threadIdx.x * B;
@@ -358,13 +359,18 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
         auto copy_round = [&]() {
             if (to_copy > 0) {
                 --to_copy;
-                // (a head past the end: any address in range, nothing is read)
-                const bool in = FULL || copy_at * at_once + sub < hd.heads;
                 const uint32_t slot = smem_u32(mine) + filled * (R::per_round * kStep);
-                copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_in : static_cast<const T*>(hd.in), ck, in, slot, kStep);
-                if constexpr (BWD)
-                    copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_dy : static_cast<const T*>(hd.dy), ck, in,
-                                                       slot + 2 * NC * kStep, kStep);
+#pragma unroll
+                for (int u = 0; u < HU; ++u) {
+                    // (a head past the end: any address in range, nothing is read)
+                    const bool in = FULL || copy_at * at_once + u * groups + sub < hd.heads;
+                    copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_in + u * groups * hd.in_h : static_cast<const T*>(hd.in),
+                                                       ck, in, slot + u * R::per_head * kStep, kStep);
+                    if constexpr (BWD)
+                        copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_dy + u * groups * hd.dy_h
+                                                              : static_cast<const T*>(hd.dy),
+                                                           ck, in, slot + (u * R::per_head + 2 * NC) * kStep, kStep);
+                }
                 filled = filled + 1 == R::depth ? 0 : filled + 1;
                 copy_in += step_in;
                 if (BWD) copy_dy += step_dy;
@@ -418,65 +424,85 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
             const int64_t step_out = at_once * hd.out_h;
             // every lane of the warp runs every round (the sums are shuffles)
             for (int i = 0; i < here; ++i, out += step_out) {
-                const int h = (round + i) * at_once + sub, h_end = hd.heads;
-                Raw<T, V> rx[NC], rd[NC];
+                Raw<T, V> rx[HU][NC], rd[HU][NC];
+                auto live = [&](int u) { return FULL || (round + i) * at_once + u * groups + sub < hd.heads; };
                 if constexpr (R::used) {
                     asm volatile("cp.async.wait_group %0;" :: "n"(R::depth - 1) : "memory");
                     const uint8_t* slot = mine + read * (R::per_round * kStep);
-                    read_chunks<T, V, NC>(slot, kStep, rx);
-                    if constexpr (BWD) read_chunks<T, V, NC>(slot + 2 * NC * kStep, kStep, rd);
+#pragma unroll
+                    for (int u = 0; u < HU; ++u) {
+                        read_chunks<T, V, NC>(slot + u * R::per_head * kStep, kStep, rx[u]);
+                        if constexpr (BWD) read_chunks<T, V, NC>(slot + (u * R::per_head + 2 * NC) * kStep, kStep, rd[u]);
+                    }
                     read = read + 1 == R::depth ? 0 : read + 1;
                     copy_round();                                // into the slots just read
                 } else {
-                    load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.in) + t * hd.in_t + h * hd.in_h, ck,
-                                                 h < h_end, rx);
-                    if constexpr (BWD)
-                        load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.dy) + t * hd.dy_t + h * hd.dy_h, ck,
-                                                     h < h_end, rd);
+#pragma unroll
+                    for (int u = 0; u < HU; ++u) {
+                        const int64_t h = (round + i) * at_once + u * groups + sub;
+                        load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.in) + t * hd.in_t + h * hd.in_h, ck,
+                                                     live(u), rx[u]);
+                        if constexpr (BWD)
+                            load_chunks<T, V, NC, PAIRS>(static_cast<const T*>(hd.dy) + t * hd.dy_t + h * hd.dy_h, ck,
+                                                         live(u), rd[u]);
+                    }
                 }
-                uint64_t xa[H], xb[H], q = 0;
-                unpack<T, V, NC, PAIRS>(rx, ck, xa, xb);
+                uint64_t xa[HU][H], xb[HU][H], da[BWD ? HU : 1][H], db[BWD ? HU : 1][H];
+                float ss[HU], sd[HU];
 #pragma unroll
-                for (int e = 0; e < H; ++e) q = fma_f32x2(xb[e], xb[e], fma_f32x2(xa[e], xa[e], q));
-                float ss = lo_of(q) + hi_of(q);
-                if constexpr (BWD) {
-                    // dn, the output's gradient turned back; its sum with w x
-                    uint64_t da[H], db[H], z = 0;
-                    unpack<T, V, NC, PAIRS>(rd, ck, da, db);
+                for (int u = 0; u < HU; ++u) {
+                    uint64_t q = 0;
+                    unpack<T, V, NC, PAIRS>(rx[u], ck, xa[u], xb[u]);
 #pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        const uint64_t ga = fma_f32x2(db[e], as[e], mul_f32x2(da[e], ac[e]));
-                        db[e] = fma_f32x2(da[e], nbs[e], mul_f32x2(db[e], ac[e]));
-                        da[e] = ga;
-                        z = fma_f32x2(mul_f32x2(da[e], pk(wa[2 * e], wa[2 * e + 1])), xa[e], z);
-                        z = fma_f32x2(mul_f32x2(db[e], pk(wb[2 * e], wb[2 * e + 1])), xb[e], z);
-                    }
-                    float sd = lo_of(z) + hi_of(z);
-                    for (int o = p.lanes >> 1; o > 0; o >>= 1) {
-                        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                        sd += __shfl_xor_sync(0xffffffffu, sd, o);
-                    }
-                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps)), m = sd * inv_d * r * r;
-                    const uint64_t rr = pk(r, r), nm = pk(-m, -m);
+                    for (int e = 0; e < H; ++e) q = fma_f32x2(xb[u][e], xb[u][e], fma_f32x2(xa[u][e], xa[u][e], q));
+                    ss[u] = lo_of(q) + hi_of(q);
+                    if constexpr (BWD) {
+                        // dn, the output's gradient turned back; its sum with w x
+                        uint64_t z = 0;
+                        unpack<T, V, NC, PAIRS>(rd[u], ck, da[u], db[u]);
 #pragma unroll
-                    for (int e = 0; e < H; ++e) {                // r (dn w - x m)
-                        dwa[e] = fma_f32x2(da[e], mul_f32x2(xa[e], rr), dwa[e]);
-                        dwb[e] = fma_f32x2(db[e], mul_f32x2(xb[e], rr), dwb[e]);
-                        xa[e] = mul_f32x2(rr, fma_f32x2(xa[e], nm, mul_f32x2(da[e], pk(wa[2 * e], wa[2 * e + 1]))));
-                        xb[e] = mul_f32x2(rr, fma_f32x2(xb[e], nm, mul_f32x2(db[e], pk(wb[2 * e], wb[2 * e + 1]))));
+                        for (int e = 0; e < H; ++e) {
+                            const uint64_t ga = fma_f32x2(db[u][e], as[e], mul_f32x2(da[u][e], ac[e]));
+                            db[u][e] = fma_f32x2(da[u][e], nbs[e], mul_f32x2(db[u][e], ac[e]));
+                            da[u][e] = ga;
+                            z = fma_f32x2(mul_f32x2(ga, pk(wa[2 * e], wa[2 * e + 1])), xa[u][e], z);
+                            z = fma_f32x2(mul_f32x2(db[u][e], pk(wb[2 * e], wb[2 * e + 1])), xb[u][e], z);
+                        }
+                        sd[u] = lo_of(z) + hi_of(z);
                     }
-                } else {
-                    for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+                }
+                for (int o = p.lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+                    for (int u = 0; u < HU; ++u) {
+                        ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+                        if constexpr (BWD) sd[u] += __shfl_xor_sync(0xffffffffu, sd[u], o);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < HU; ++u) {
+                    const float r = rsqrtf(fmaf(ss[u], inv_d, p.eps));
                     const uint64_t rr = pk(r, r);
+                    if constexpr (BWD) {
+                        const float m = sd[u] * inv_d * r * r;
+                        const uint64_t nm = pk(-m, -m);
 #pragma unroll
-                    for (int e = 0; e < H; ++e) {
-                        const uint64_t ya = mul_f32x2(rr, fma_f32x2(xb[e], nbs[e], mul_f32x2(xa[e], ac[e])));
-                        xb[e] = mul_f32x2(rr, fma_f32x2(xa[e], as[e], mul_f32x2(xb[e], bc[e])));
-                        xa[e] = ya;
+                        for (int e = 0; e < H; ++e) {            // r (dn w - x m)
+                            const uint64_t a = xa[u][e], b = xb[u][e];
+                            dwa[e] = fma_f32x2(da[u][e], mul_f32x2(a, rr), dwa[e]);
+                            dwb[e] = fma_f32x2(db[u][e], mul_f32x2(b, rr), dwb[e]);
+                            xa[u][e] = mul_f32x2(rr, fma_f32x2(a, nm, mul_f32x2(da[u][e], pk(wa[2 * e], wa[2 * e + 1]))));
+                            xb[u][e] = mul_f32x2(rr, fma_f32x2(b, nm, mul_f32x2(db[u][e], pk(wb[2 * e], wb[2 * e + 1]))));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < H; ++e) {
+                            const uint64_t a = xa[u][e], b = xb[u][e];
+                            xa[u][e] = mul_f32x2(rr, fma_f32x2(b, nbs[e], mul_f32x2(a, ac[e])));
+                            xb[u][e] = mul_f32x2(rr, fma_f32x2(a, as[e], mul_f32x2(b, bc[e])));
+                        }
                     }
+                    if (live(u)) store_chunks<T, V, NC, PAIRS, FULL>(out + u * groups * hd.out_h, ck, xa[u], xb[u]);
                 }
-                if (FULL || h < h_end) store_chunks<T, V, NC, PAIRS, FULL>(out, ck, xa, xb);
             }
             round = 0;
             ++t;
@@ -538,11 +564,13 @@ __global__ void __launch_bounds__(1024) qk_norm_dw(const float* __restrict__ par
 
 template <bool BWD>
 constexpr int kBlocksPerSm = 2;
+template <typename T, bool BWD>
+constexpr int kHeadsPerLane = sizeof(T) == 2 && !BWD ? 2 : 1;
 
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
 cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
-    const int smem = Ring<sizeof(T) * V, NC, BWD>::bytes + (BWD ? kWarps * 2 * p.D * (int)sizeof(float) : 0);
-    auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL>;
+    const int smem = Ring<sizeof(T) * V, NC, BWD, HU>::bytes + (BWD ? kWarps * 2 * p.D * (int)sizeof(float) : 0);
+    auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL, HU>;
     if (smem > 48 << 10) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -557,8 +585,10 @@ cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
 // Measured, forward / backward, us: bfloat16, 16384 tokens x 40 heads x 128, 62 /
 // 91 with four pairs, 67 / 112 with eight (whose cosines, sines and weights
 // alone take 64 registers); float32, 8192 x 24 x 128, 39 / 56.  Two blocks per
-// SM: 62 / 91; three 64 / 107; four 68 / 107.  (Bytes at the HBM's rate: 49 /
-// 74, 30 / 45.)  Before the rings the loads waited in registers: 89 us forward.
+// SM: 62 / 91; three 64 / 107; four 68 / 107.  Two heads per lane and round in
+// the 16-bit forward pass: float16, 12001 x 28 x 96, 42 -> 38.  (Bytes at the
+// HBM's rate: 49 / 74, 30 / 45, 19 / 29.)  Before the rings the loads waited in
+// registers: 89 us forward.
 template <typename T, bool PAIRS, bool BWD>
 cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t stream) {
     constexpr int V = 4;
@@ -578,19 +608,19 @@ cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t s
     while (p.lanes < 32 && p.lanes < chunks) p.lanes *= 2;
     const int nc = (chunks + p.lanes - 1) / p.lanes;
     // a warp per round until they fill the GPU
-    const int at_once = 32 / p.lanes;
+    constexpr int BPS = kBlocksPerSm<BWD>, HU = kHeadsPerLane<T, BWD>;
+    const int at_once = 32 / p.lanes * (wide && nc == 1 ? HU : 1);
     const int most = p.side[0].heads > p.side[1].heads ? p.side[0].heads : p.side[1].heads;
     const int64_t want = (p.T * ((most + at_once - 1) / at_once) + kWarps - 1) / kWarps;
     *blocks = (int)(want < max_blocks ? want : max_blocks);
-    constexpr int BPS = kBlocksPerSm<BWD>;
     if (wide) {
         const bool full = chunks == p.lanes && p.side[0].heads % at_once == 0 && p.side[1].heads % at_once == 0;
-        if (nc == 1 && full) return launch_one<T, V, 1, PAIRS, BWD, BPS, true>(p, *blocks, stream);
-        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, BPS, false>(p, *blocks, stream);
-        return launch_one<T, V, 2, PAIRS, BWD, 1, false>(p, *blocks, stream);
+        if (nc == 1 && full) return launch_one<T, V, 1, PAIRS, BWD, BPS, true, HU>(p, *blocks, stream);
+        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, BPS, false, HU>(p, *blocks, stream);
+        return launch_one<T, V, 2, PAIRS, BWD, 1, false, 1>(p, *blocks, stream);
     }
-    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, BPS, false>(p, *blocks, stream);
-    return launch_one<T, 1, 8, PAIRS, BWD, 1, false>(p, *blocks, stream);
+    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, BPS, false, 1>(p, *blocks, stream);
+    return launch_one<T, 1, 8, PAIRS, BWD, 1, false, 1>(p, *blocks, stream);
 }
 
 template <bool BWD>
