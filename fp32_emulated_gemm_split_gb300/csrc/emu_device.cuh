@@ -343,6 +343,46 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
                  ".multicast::cluster.b64 [%0], %1;" :: "r"(bar), "h"((uint16_t)3) : "memory");
 }
 
+// ---------------------------------------------- stores to unaligned rows --
+
+// out = v + beta out for 32 rows x 16 columns (lane = row, v[0..15]) whose tile
+// starts at (row0, gc0), for rows that are not 16-byte aligned: turned in the
+// warp's 2 KB staging buffer (64-byte swizzle: conflict-free both ways), so that
+// 16 lanes read and write 16 neighbouring values of a row.  Lane by lane, each
+// its own row, such an epilogue took longer than the products (5120 x 322 x 704:
+// 175 us).
+__device__ __forceinline__ void store_unaligned16(const float (&v)[16], float beta, float* out,
+                                                  int64_t ld, int M, int N, int row0, int gc0,
+                                                  int lane, uint32_t stage) {
+    __syncwarp();                                        // the buffer has been read
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t a = stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(a), "f"(v[4 * c]), "f"(v[4 * c + 1]), "f"(v[4 * c + 2]), "f"(v[4 * c + 3])
+                     : "memory");
+    }
+    __syncwarp();
+    const int c = lane & 15;
+    float* dst = out + (int64_t)(row0 + (lane >> 4)) * ld + gc0 + c;
+    const bool in = gc0 + c < N;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 4, dst += 8 * ld) {
+        float old[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            old[i] = beta != 0.0f && in && row0 + 2 * (i0 + i) + (lane >> 4) < M ? dst[2 * i * ld] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 2 * (i0 + i) + (lane >> 4);
+            float x;
+            const uint32_t a = stage + r * 64 + (((c >> 2) ^ ((r >> 1) & 3)) << 4) + (c & 3) * 4;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+            if (in && row0 + r < M) dst[2 * i * ld] = beta != 0.0f ? fmaf(beta, old[i], x) : x;
+        }
+    }
+}
+
 // ------------------------------------------------------------- the split --
 
 // Nearest BF16 (ties to even) of a finite FP32 value; a value whose nearest

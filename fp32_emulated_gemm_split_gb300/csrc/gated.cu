@@ -186,9 +186,9 @@ emu_status_t emu_gated_pack(int64_t F, int64_t K, const float* Wg, int64_t ldwg,
     uint16_t* P = static_cast<uint16_t*>(Wp);
     cudaError_t e = cudaSuccess;
     // the gaps' rows meet zeros of [dG dU] in dX's product: they hold zeros too
-    for (int pc = 0; pc < 3 && Fp > F; ++pc)
-        for (int half = 0; half < 2 && e == cudaSuccess; ++half)
-            e = cudaMemsetAsync(P + ((pc * 2 + half) * Fp + F) * ldwp, 0, (Fp - F) * ldwp * 2, stream);
+    // (six of them, behind every F rows of the planes' halves)
+    if (Fp > F)
+        e = cudaMemset2DAsync(P + F * ldwp, Fp * ldwp * 2, 0, (Fp - F) * ldwp * 2, 6, stream);
     if (e == cudaSuccess)
         e = launch_split_pieces(kModeBf16x9, Wg, F, K, ldwg, 0, P, ldwp, stream, false, 2 * Fp);
     if (e == cudaSuccess)                                // may run beside the gate's split

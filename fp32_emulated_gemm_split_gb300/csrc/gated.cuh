@@ -86,13 +86,17 @@ __host__ __device__ __forceinline__ void with_act(int act, F&& f) {
 // starts at (row0, gc0): through the warp's 2 KB staging buffer and one bulk
 // tensor store where the output's rows are 16-byte aligned (64-byte swizzle;
 // the map ends at column N & ~3, so a lane stores its row's last N % 4
-// columns itself), element by element otherwise.
+// columns itself), turned in that buffer otherwise.
 __device__ __forceinline__ void store_chunk16(const float (&v)[16], const CUtensorMap& map,
                                               bool tma, float* out, int64_t ld, int M, int N,
                                               int row0, int gc0, int lane, uint32_t stage) {
+    if (!tma) {
+        store_unaligned16(v, 0.0f, out, ld, M, N, row0, gc0, lane, stage);
+        return;
+    }
     const int row = row0 + lane;
     const int n4 = N & ~3;
-    if (tma) {
+    {
         if (lane == 0) bulk_wait_read_n<0>();            // the buffer is free again
         __syncwarp();
 #pragma unroll
@@ -114,7 +118,7 @@ __device__ __forceinline__ void store_chunk16(const float (&v)[16], const CUtens
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const int c = gc0 + j;
-            if (c < N && (!tma || c >= n4)) dst[c] = v[j];
+            if (c < N && c >= n4) dst[c] = v[j];
         }
     }
 }

@@ -973,9 +973,9 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
                         }
                     }
                 }
-            } else if (row < p.M && col_base < p.N) {
-                float* crow = p.C + (int64_t)row * p.ldc + col_base;
-                if (vec && col_base + kAccCols <= p.N) {
+            } else if (vec && col_base + kAccCols <= p.N) {
+                if (row < p.M) {
+                    float* crow = p.C + (int64_t)row * p.ldc + col_base;
 #pragma unroll
                     for (int v4 = 0; v4 < kAccCols / 4; ++v4) {
                         float4 v;
@@ -993,15 +993,16 @@ gemm_kblock_kernel(const __grid_constant__ CUtensorMap mapA,
                         }
                         *dst = v;
                     }
-                } else {
+                }
+            } else if (row0 < p.M) {
+                const uint32_t cst = smem_u32(cstage + (warp - R::acc0) * 2048 * Cfg::c_bufs);
 #pragma unroll
-                    for (int j = 0; j < kAccCols; ++j) {
-                        if (col_base + j < p.N) {
-                            float v = p.alpha * acc[j];
-                            if (p.beta != 0.0f) v = fmaf(p.beta, crow[j], v);
-                            crow[j] = v;
-                        }
-                    }
+                for (int ch = 0; ch < kAccCols / 16; ++ch) {
+                    if (col_base + 16 * ch >= p.N) break;              // warp-uniform
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = p.alpha * acc[16 * ch + j];
+                    store_unaligned16(v, p.beta, p.C, p.ldc, p.M, p.N, row0, col_base + 16 * ch, lane, cst);
                 }
             }
         }

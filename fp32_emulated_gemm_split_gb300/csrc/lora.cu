@@ -427,16 +427,19 @@ __global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
     }
 }
 
-// Many tokens: a tile per block.
-template <int V>
-__global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p) {
-    __shared__ __align__(16) float s[kTileTok][16];
-    __shared__ __align__(16) float bs[up_smem<2, 16>()];
+// Many tokens: `part` tokens of a tile per block (z picks them), RK ranks per
+// pass: as the rank needs, 32 where it is more than 16.
+template <int V, int RK>
+__global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p, int part) {
+    __shared__ __align__(16) float s[kTileTok][RK];
+    __shared__ __align__(16) float bs[up_smem<2, RK>()];
     griddep_launch_dependents();
     griddep_wait();                          // the grouping and S
     if ((int)blockIdx.x >= *p.ntiles) return;
     const int4 tile = p.tiles[blockIdx.x];
-    up_tokens<2, 16, V>(p, tile.x, p.order + tile.y, 0, tile.z,
+    const int first = blockIdx.z * part;
+    if (first >= tile.z) return;
+    up_tokens<2, RK, V>(p, tile.x, p.order + tile.y + first, 0, min(part, tile.z - first),
                         (int64_t)blockIdx.y * (2 * kUpThreads) + threadIdx.x, s, bs);
 }
 
@@ -447,9 +450,9 @@ int64_t max_tiles(int64_t M, int64_t adapters) {
 
 // Launch as a programmatic dependent of the kernel ahead in the stream (pdl):
 // this call's own, whose results the kernel waits for itself.
-template <typename Kern>
+template <typename Kern, typename... More>
 cudaError_t launch_after(Kern kern, dim3 grid, int threads, int smem, bool pdl, const LoraParams& p,
-                         cudaStream_t stream) {
+                         cudaStream_t stream, More... more) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -460,7 +463,7 @@ cudaError_t launch_after(Kern kern, dim3 grid, int threads, int smem, bool pdl, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p, more...);
 }
 
 template <int V>
@@ -583,10 +586,15 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
         e = M <= kSingleTokens ? (wide ? go(lora_up_few<4, 1>, 1) : go(lora_up_few<2, 1>, 1))
                                : (wide ? go(lora_up_few<4, kDotTok>, kDotTok) : go(lora_up_few<2, kDotTok>, kDotTok));
     } else {
-        const dim3 grid((unsigned)max_tiles(M, p.adapters),
-                        (unsigned)((N + 2 * kUpThreads - 1) / (2 * kUpThreads)));
-        e = wide ? launch_after(lora_up_tiles<4>, grid, kUpThreads, 0, after, p, stream)
-                 : launch_after(lora_up_tiles<2>, grid, kUpThreads, 0, after, p, stream);
+        const unsigned tiles = (unsigned)max_tiles(M, p.adapters);
+        const unsigned cols = (unsigned)((N + 2 * kUpThreads - 1) / (2 * kUpThreads));
+        // a tile's tokens go to four blocks where the tiles are too few to fill
+        // the GPU (341 tokens, 632 columns, rank 64: 27 blocks took 84 us)
+        const int part = (int64_t)tiles * cols < 8 * d->sms ? kTileTok / 4 : kTileTok;
+        const dim3 grid(tiles, cols, kTileTok / part);
+        auto go = [&](auto kern) { return launch_after(kern, grid, kUpThreads, 0, after, p, stream, part); };
+        e = p.R > 16 ? (wide ? go(lora_up_tiles<4, 32>) : go(lora_up_tiles<2, 32>))
+                     : (wide ? go(lora_up_tiles<4, 16>) : go(lora_up_tiles<2, 16>));
     }
     if (e != cudaSuccess || K == 0) return from_cuda(e);
     // rows that stream the FP32 weight: all of them, or what whole tiles leave

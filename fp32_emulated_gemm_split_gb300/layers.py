@@ -171,8 +171,10 @@ def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None, stream=None)
         if save:
             # rows of whole 16-byte groups, so that they can be stored and read as such
             ldg = max((F + 3) // 4 * 4, 4)
-            GU = torch.empty((2, M, ldg), dtype=_F32, device=X.device)
-            G, U = GU[0, :, :F], GU[1, :, :F]
+            G = torch.empty((M, ldg), dtype=_F32, device=X.device)
+            U = torch.empty((M, ldg), dtype=_F32, device=X.device)
+            if ldg != F:
+                G, U = G[:, :F], U[:, :F]
             pG, pU = G.data_ptr(), U.data_ptr()
         _check(_L().emu_gated(a, M, F, K, X.data_ptr(), ldx, *w._weights, *w._pieces, H.data_ptr(), ldh,
                               pG, pU, ldg, _handle(dev)), "emu_gated")
@@ -343,8 +345,8 @@ def emu_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos=None, sin=None, posit
     with _on(stream):
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        dw = torch.empty((2, D), dtype=_F32, device=q.device)
-        dwq, dwk = (dw[0] if wq is not None else None), (dw[1] if wk is not None else None)
+        dwq = torch.empty(D, dtype=_F32, device=q.device) if wq is not None else None
+        dwk = torch.empty(D, dtype=_F32, device=q.device) if wk is not None else None
         heads = _6_heads.pack(*hq, *hk, *_heads(dq, "dq"), *_heads(dk, "dk"),
                               *_heads(dq_out, "dq_out", q.shape), *_heads(dk_out, "dk_out", k.shape))
         _check(_L().emu_qk_norm_rope_bwd(*size, 1 if interleaved else 0, eps, heads, *tables,
