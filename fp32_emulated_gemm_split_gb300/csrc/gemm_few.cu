@@ -145,13 +145,14 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     float* ex = reinterpret_cast<float*>(bst + C::b_stages * 3 * C::b_tile);
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ex) + C::ex_bytes);
     // FP32 buffer full / free, X's stage full / free, W's pieces ready / free,
-    // partial full / free
+    // partial full / free, an issuer's MMAs done (only where a wait gave up)
     constexpr int NF = C::a_bufs, NB = C::b_stages, NA = C::a_stages, ND = C::partials;
     const uint32_t afull0 = smem_u32(bars), afree0 = afull0 + 8 * NF;
     const uint32_t bfull0 = afree0 + 8 * NF, bfree0 = bfull0 + 8 * NB;
     const uint32_t pready0 = bfree0 + 8 * NB, pfree0 = pready0 + 8 * NA;
     const uint32_t dfull0 = pfree0 + 8 * NA, dfree0 = dfull0 + 8 * ND;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * (NF + NB + NA + ND));
+    const uint32_t drain0 = dfree0 + 8 * ND;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * (NF + NB + NA + ND) + C::issuers);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -180,6 +181,7 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             mbar_init(dfull0 + 8 * i, 1);
             mbar_init(dfree0 + 8 * i, C::acc_warps);
         }
+        for (int i = 0; i < C::issuers; ++i) mbar_init(drain0 + 8 * i, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -230,6 +232,9 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                 }
             }
             if (!ok) *abort_flag = 1;
+            // no copy may land after this CTA is gone (they have, unless a wait gave up)
+            for (uint32_t i = g > NF ? g - NF : 0; i < g; ++i)
+                mbar_wait(afull0 + 8 * slot_of(i, NF), phase_of(i, NF), p.err, kDevErrTimeout);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -253,6 +258,8 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                 }
             }
             if (!ok) *abort_flag = 1;
+            for (uint32_t i = g > NB ? g - NB : 0; i < g; ++i)
+                mbar_wait(bfull0 + 8 * slot_of(i, NB), phase_of(i, NB), p.err, kDevErrTimeout);
         }
     } else if (warp < C::acc0) {
         if (lane == 0 && warp - 2 < C::issuers) {
@@ -266,7 +273,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                     !mbar_wait(bfull0 + 8 * s, phase_of(g, C::b_stages), p.err, kDevErrTimeout) ||
                     !mbar_wait(pready0 + 8 * t, phase_of(g, C::a_stages), p.err, kDevErrTimeout) ||
                     *abort_flag) {
+                    // tensor memory is freed only behind the MMAs issued so far
                     *abort_flag = 1;
+                    tc_commit(drain0 + 8 * (warp - 2));
+                    mbar_wait(drain0 + 8 * (warp - 2), 0, p.err, kDevErrTimeout);
                     break;
                 }
                 tc_fence_after();

@@ -27,6 +27,8 @@
 namespace emu {
 namespace {
 
+constexpr int kMaxD = 512;                   // values of a head
+
 struct Heads {
     const void* in;
     const void* dy;          // backward: the gradient of the output
@@ -569,10 +571,18 @@ constexpr int kHeadsPerLane = sizeof(T) == 2 && !BWD ? 2 : 1;
 
 template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
 cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
-    const int smem = Ring<sizeof(T) * V, NC, BWD, HU>::bytes + (BWD ? kWarps * 2 * p.D * (int)sizeof(float) : 0);
+    constexpr int ring = Ring<sizeof(T) * V, NC, BWD, HU>::bytes, per_value = BWD ? kWarps * 2 * (int)sizeof(float) : 0;
+    const int smem = ring + per_value * p.D;
     auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL, HU>;
-    if (smem > 48 << 10) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (ring + per_value * kMaxD > 48 << 10) {
+        // the limit, raised once per device (g_mu is held)
+        static bool done[kMaxDevices] = {};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && (dev >= kMaxDevices || !done[dev])) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring + per_value * kMaxD);
+            if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
+        }
         if (e != cudaSuccess) return e;
     }
     kern<<<blocks, kWarps * 32, smem, stream>>>(p);
@@ -652,7 +662,7 @@ emu_status_t check_qk(int dtype, int64_t T, int64_t D, int64_t rot, int interlea
                       int64_t table_rows, const int32_t* positions) {
     if (dtype < EMU_F32 || dtype > EMU_F16 || (interleaved != 0 && interleaved != 1))
         return EMU_ERR_INVALID_VALUE;
-    if (T < 0 || T > INT32_MAX / 64 || D < 1 || D > 512 || rot < 0 || rot > D || rot % 2 != 0 || !(eps >= 0.0f))
+    if (T < 0 || T > INT32_MAX / 64 || D < 1 || D > kMaxD || rot < 0 || rot > D || rot % 2 != 0 || !(eps >= 0.0f))
         return EMU_ERR_INVALID_VALUE;
     if (!heads_ok(q, T) || !heads_ok(k, T) || !heads_ok(qo, T) || !heads_ok(ko, T) ||
         qo.heads != q.heads || ko.heads != k.heads)

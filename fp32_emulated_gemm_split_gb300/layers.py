@@ -9,8 +9,8 @@ Outputs are allocated where they are not given.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import struct
 
 import torch
@@ -51,12 +51,16 @@ def _L():
 # each tensor's shape and strides are read once and compared as tuples, and the
 # stream's handle comes without making a Stream object.
 
-_NONE = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Outputs and work of a call belong to `stream` (None: the current one)."""
-    return _NONE if stream is None else torch.cuda.stream(stream)
+def _on_stream(fn):
+    """Gives fn a ``stream``: its outputs and work belong to it (None: to the
+    current one)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -137,7 +141,8 @@ class GatedWeights:
             raise ValueError("a weight was changed in place since emu_gated_pack: pack again")
 
 
-def emu_gated_pack(Wg, Wu, stream=None) -> GatedWeights:
+@_on_stream
+def emu_gated_pack(Wg, Wu) -> GatedWeights:
     """The weights Wg and Wu (F x K each) ready for ``emu_gated``."""
     Wg, Wu = Wg.detach(), Wu.detach()
     ldg = _rows(Wg, "Wg")
@@ -145,14 +150,14 @@ def emu_gated_pack(Wg, Wu, stream=None) -> GatedWeights:
     ldu = _rows(Wu, "Wu", F, K)
     dev = _device(Wg, Wu)
     rows = _L().emu_gated_rows(F)
-    with _on(stream):
-        P = torch.empty((3, 2 * rows, max((K + 63) // 64 * 64, 64)), dtype=torch.int16, device=Wg.device)
-        _check(_L().emu_gated_pack(F, K, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, P.data_ptr(), P.size(2),
-                                   _handle(dev)), "emu_gated_pack")
+    P = torch.empty((3, 2 * rows, max((K + 63) // 64 * 64, 64)), dtype=torch.int16, device=Wg.device)
+    _check(_L().emu_gated_pack(F, K, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, P.data_ptr(), P.size(2),
+                               _handle(dev)), "emu_gated_pack")
     return GatedWeights(Wg, Wu, P, ldg, ldu, rows)
 
 
-def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None, stream=None):
+@_on_stream
+def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None):
     """H = act(X Wg^T) * (X Wu^T), or (H, G, U) with save=True: the two
     products as well, for ``emu_gated_bwd``."""
     a = _act(act)
@@ -161,27 +166,27 @@ def emu_gated(X, w: GatedWeights, act="silu", save=False, out=None, stream=None)
     ldx = _rows(X, "X", None, K)
     M = X.shape[0]
     dev = _device(X, w.Wg, out)
-    with _on(stream):
-        if out is None:
-            H, ldh = torch.empty((M, F), dtype=_F32, device=X.device), F if F > 0 else 1
-        else:
-            H, ldh = out, _rows(out, "out", M, F)
-        G = U = pG = pU = None
-        ldg = 0
-        if save:
-            # rows of whole 16-byte groups, so that they can be stored and read as such
-            ldg = max((F + 3) // 4 * 4, 4)
-            G = torch.empty((M, ldg), dtype=_F32, device=X.device)
-            U = torch.empty((M, ldg), dtype=_F32, device=X.device)
-            if ldg != F:
-                G, U = G[:, :F], U[:, :F]
-            pG, pU = G.data_ptr(), U.data_ptr()
-        _check(_L().emu_gated(a, M, F, K, X.data_ptr(), ldx, *w._weights, *w._pieces, H.data_ptr(), ldh,
-                              pG, pU, ldg, _handle(dev)), "emu_gated")
+    if out is None:
+        H, ldh = torch.empty((M, F), dtype=_F32, device=X.device), F if F > 0 else 1
+    else:
+        H, ldh = out, _rows(out, "out", M, F)
+    G = U = pG = pU = None
+    ldg = 0
+    if save:
+        # rows of whole 16-byte groups, so that they can be stored and read as such
+        ldg = max((F + 3) // 4 * 4, 4)
+        G = torch.empty((M, ldg), dtype=_F32, device=X.device)
+        U = torch.empty((M, ldg), dtype=_F32, device=X.device)
+        if ldg != F:
+            G, U = G[:, :F], U[:, :F]
+        pG, pU = G.data_ptr(), U.data_ptr()
+    _check(_L().emu_gated(a, M, F, K, X.data_ptr(), ldx, *w._weights, *w._pieces, H.data_ptr(), ldh,
+                          pG, pU, ldg, _handle(dev)), "emu_gated")
     return (H, G, U) if save else H
 
 
-def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_dw=True, stream=None):
+@_on_stream
+def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_dw=True):
     """(dX, dWg, dWu) from the gradient dH of H and what ``emu_gated`` saved;
     None in the place of a gradient that is not needed."""
     a = _act(act)
@@ -192,14 +197,13 @@ def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_d
     if _rows(U, "U", M, F) != ldg:
         raise ValueError("G and U need the same row stride")
     dev = _device(dH, X, G, U, w.Wg)
-    with _on(stream):
-        dX = torch.empty((M, K), dtype=_F32, device=X.device) if need_dx else None
-        dW = torch.empty((2 * w.rows, K), dtype=_F32, device=X.device) if need_dw else None
-        _check(_L().emu_gated_bwd(a, M, F, K, dH.data_ptr(), lddh, X.data_ptr(), ldx, *w._pieces,
-                                  G.data_ptr(), U.data_ptr(), ldg,
-                                  dX.data_ptr() if need_dx else None, max(K, 1),
-                                  dW.data_ptr() if need_dw else None, max(K, 1), _handle(dev)),
-               "emu_gated_bwd")
+    dX = torch.empty((M, K), dtype=_F32, device=X.device) if need_dx else None
+    dW = torch.empty((2 * w.rows, K), dtype=_F32, device=X.device) if need_dw else None
+    _check(_L().emu_gated_bwd(a, M, F, K, dH.data_ptr(), lddh, X.data_ptr(), ldx, *w._pieces,
+                              G.data_ptr(), U.data_ptr(), ldg,
+                              dX.data_ptr() if need_dx else None, max(K, 1),
+                              dW.data_ptr() if need_dw else None, max(K, 1), _handle(dev)),
+           "emu_gated_bwd")
     return dX, dW[:F] if need_dw else None, dW[w.rows:w.rows + F] if need_dw else None
 
 
@@ -221,19 +225,20 @@ class LoraWeights:
                         None if bias is None else bias.data_ptr())
 
 
-def emu_lora_pack(W, bias=None, stream=None) -> LoraWeights:
+@_on_stream
+def emu_lora_pack(W, bias=None) -> LoraWeights:
     """The projection's weight W (N x K) and bias ready for ``emu_lora``."""
     W = W.detach()
     bias = None if bias is None else bias.detach()
     ldw = _rows(W, "W")
     _vector(bias, "bias", W.size(0))
     _device(W, bias)
-    with _on(stream):
-        P = emu_split_b(W, transB=True)
+    P = emu_split_b(W, transB=True)
     return LoraWeights(W, bias, P, ldw)
 
 
-def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None, stream=None):
+@_on_stream
+def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None):
     """Y = X W^T + bias + scale_i (X A_i^T) B_i^T with i = index[row] (-1: no
     adapter); A is adapters x R x K, B adapters x N x R, scale `adapters`
     values, index int32."""
@@ -254,13 +259,12 @@ def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None, stream=None):
     ip = _indices(index, "index", M)
     sp = _vector(scale, "scale", n)
     dev = _device(X, w.W, A, B, index, scale, out)
-    with _on(stream):
-        if out is None:
-            Y, ldy = torch.empty((M, N), dtype=_F32, device=X.device), N if N > 0 else 1
-        else:
-            Y, ldy = out, _rows(out, "out", M, N)
-        _check(_L().emu_lora(M, N, K, X.data_ptr(), ldx, *w._weight, R, n, A.data_ptr(), B.data_ptr(), sp, ip,
-                             Y.data_ptr(), ldy, _handle(dev)), "emu_lora")
+    if out is None:
+        Y, ldy = torch.empty((M, N), dtype=_F32, device=X.device), N if N > 0 else 1
+    else:
+        Y, ldy = out, _rows(out, "out", M, N)
+    _check(_L().emu_lora(M, N, K, X.data_ptr(), ldx, *w._weight, R, n, A.data_ptr(), B.data_ptr(), sp, ip,
+                         Y.data_ptr(), ldy, _handle(dev)), "emu_lora")
     return Y
 
 
@@ -269,88 +273,83 @@ def emu_lora(X, w: LoraWeights, A, B, index, scale=None, out=None, stream=None):
 _4_heads, _6_heads = struct.Struct("4q4q4q4q"), struct.Struct("4q4q4q4q4q4q")      # emu_heads_t each
 
 
-def _heads(x, name, shape=None):
-    """The emu_heads_t of a tokens x heads x D tensor."""
-    sh = x.shape
-    if len(sh) != 3 or (shape is not None and sh != shape):
-        raise ValueError(f"{name} must be tokens x heads x D"
-                         + (f" = {tuple(shape)}" if shape is not None else "") + f", got {tuple(sh)}")
-    st, sh_, unit = x.stride()
-    if unit != 1 and sh[2] > 1:
+def _heads(x, name, shape, dtype):
+    """The emu_heads_t of a tokens x heads x D tensor of the given shape."""
+    if x.dtype is not dtype:
+        raise TypeError(f"expected tensors of one type, got {dtype} and {x.dtype} for {name}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must be tokens x heads x D = {tuple(shape)}, got {tuple(x.shape)}")
+    st, sh, unit = x.stride()
+    if unit != 1 and shape[2] > 1:
         raise ValueError(f"{name} needs unit stride along the values of a head")
-    return x.data_ptr(), sh[1], st, sh_
+    return x.data_ptr(), shape[1], st, sh
 
 
 def _qk_args(q, k, wq, wk, cos, sin, positions):
     """Checks of both directions: (dtype, T, D, rot), q and k as emu_heads_t,
     and the weights' and tables' arguments."""
-    dt = DTYPE.get(q.dtype)
+    kind = q.dtype
+    dt = DTYPE.get(kind)
     if dt is None:
-        raise TypeError(f"q and k must be float32, bfloat16 or float16, got {q.dtype}")
-    if k.dtype is not q.dtype:
-        raise TypeError(f"expected tensors of one type, got {q.dtype} and {k.dtype}")
-    hq, hk = _heads(q, "q"), _heads(k, "k")
-    T, _, D = q.shape
-    if k.shape[0] != T or k.shape[2] != D:
-        raise ValueError(f"q and k differ in tokens or head size: {tuple(q.shape)}, {tuple(k.shape)}")
+        raise TypeError(f"q and k must be float32, bfloat16 or float16, got {kind}")
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError(f"q and k must be tokens x heads x D with the same tokens and D, got {tuple(qs)}, {tuple(ks)}")
+    T, _, D = qs
+    hq, hk = _heads(q, "q", qs, kind), _heads(k, "k", ks, kind)
     pq, pk = _vector(wq, "wq", D), _vector(wk, "wk", D)
     if cos is None:
         if sin is not None:
             raise ValueError("cos and sin go together")
         return (dt, T, D, 0), hq, hk, (pq, pk, None, None, 0, None)
+    shape = cos.shape
     if cos.dtype is not _F32 or sin.dtype is not _F32:
         raise TypeError("cos and sin must be float32")
-    shape = cos.shape
     if len(shape) != 2 or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
         raise ValueError("cos and sin must be contiguous matrices of one shape, positions x rot/2")
     return (dt, T, D, 2 * shape[1]), hq, hk, (pq, pk, cos.data_ptr(), sin.data_ptr(), shape[0],
                                               _indices(positions, "positions", T))
 
 
-def _same_type(q, a, b):
-    if a.dtype is not q.dtype or b.dtype is not q.dtype:
-        raise TypeError(f"expected tensors of one type, got {q.dtype}, {a.dtype} and {b.dtype}")
-
-
-def emu_qk_norm_rope(q, k, wq, wk, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, out=None,
-                     stream=None):
+@_on_stream
+def emu_qk_norm_rope(q, k, wq, wk, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, out=None):
     """Norm of each head of q and k (tokens x heads x D, any token and head
     strides) times wq / wk (None: ones), and the rotation of its first
     2 * cos.size(1) values by the tables' row positions[token]; returns
     (q', k').  out=(q, k) writes in place."""
     size, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions)
-    with _on(stream):
-        if out is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            ko = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-            dev = _device(q, k, wq, wk, cos, sin, positions)
-        else:
-            qo, ko = out
-            _same_type(q, qo, ko)
-            dev = _device(q, k, wq, wk, cos, sin, positions, qo, ko)
-        heads = _4_heads.pack(*hq, *hk, *_heads(qo, "out[0]", q.shape), *_heads(ko, "out[1]", k.shape))
-        _check(_L().emu_qk_norm_rope(*size, 1 if interleaved else 0, eps, heads, *tables, _handle(dev)),
-               "emu_qk_norm_rope")
+    D = size[2]
+    if out is None:
+        dev = _device(q, k, wq, wk, cos, sin, positions)
+        kind, on = q.dtype, q.device
+        qo, ko = torch.empty(q.shape, dtype=kind, device=on), torch.empty(k.shape, dtype=kind, device=on)
+        ho, hp = (qo.data_ptr(), hq[1], hq[1] * D, D), (ko.data_ptr(), hk[1], hk[1] * D, D)
+    else:
+        qo, ko = out
+        dev = _device(q, k, wq, wk, cos, sin, positions, qo, ko)
+        ho, hp = _heads(qo, "out[0]", q.shape, q.dtype), _heads(ko, "out[1]", k.shape, q.dtype)
+    heads = _4_heads.pack(*hq, *hk, *ho, *hp)
+    _check(_L().emu_qk_norm_rope(*size, 1 if interleaved else 0, eps, heads, *tables, _handle(dev)),
+           "emu_qk_norm_rope")
     return qo, ko
 
 
+@_on_stream
 def emu_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos=None, sin=None, positions=None, eps=1e-6,
-                         interleaved=False, stream=None):
+                         interleaved=False):
     """(dq, dk, dwq, dwk) from the gradients of ``emu_qk_norm_rope``'s outputs
     and its inputs; dwq / dwk are None where wq / wk are."""
     size, hq, hk, tables = _qk_args(q, k, wq, wk, cos, sin, positions)
-    _same_type(q, dq_out, dk_out)
     dev = _device(q, k, wq, wk, cos, sin, positions, dq_out, dk_out)
-    D = size[2]
-    with _on(stream):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        dwq = torch.empty(D, dtype=_F32, device=q.device) if wq is not None else None
-        dwk = torch.empty(D, dtype=_F32, device=q.device) if wk is not None else None
-        heads = _6_heads.pack(*hq, *hk, *_heads(dq, "dq"), *_heads(dk, "dk"),
-                              *_heads(dq_out, "dq_out", q.shape), *_heads(dk_out, "dk_out", k.shape))
-        _check(_L().emu_qk_norm_rope_bwd(*size, 1 if interleaved else 0, eps, heads, *tables,
-                                         None if dwq is None else dwq.data_ptr(),
-                                         None if dwk is None else dwk.data_ptr(), _handle(dev)),
-               "emu_qk_norm_rope_bwd")
+    D, kind, on = size[2], q.dtype, q.device
+    hdq, hdk = _heads(dq_out, "dq_out", q.shape, kind), _heads(dk_out, "dk_out", k.shape, kind)
+    dq, dk = torch.empty(q.shape, dtype=kind, device=on), torch.empty(k.shape, dtype=kind, device=on)
+    dwq = torch.empty(D, dtype=_F32, device=on) if wq is not None else None
+    dwk = torch.empty(D, dtype=_F32, device=on) if wk is not None else None
+    heads = _6_heads.pack(*hq, *hk, dq.data_ptr(), hq[1], hq[1] * D, D, dk.data_ptr(), hk[1], hk[1] * D, D,
+                          *hdq, *hdk)
+    _check(_L().emu_qk_norm_rope_bwd(*size, 1 if interleaved else 0, eps, heads, *tables,
+                                     None if dwq is None else dwq.data_ptr(),
+                                     None if dwk is None else dwk.data_ptr(), _handle(dev)),
+           "emu_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk

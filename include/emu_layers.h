@@ -17,7 +17,9 @@
  * the same shape has run outside capture).  Values on the device that have
  * to be in range (adapter indices, positions) are checked by the kernels: one
  * that is not records EMU_ERR_INVALID_VALUE in the device's sticky error word
- * (emu_get_last_device_error) and reads nothing out of bounds.  The kernel
+ * (emu_get_last_device_error) and reads nothing out of bounds.  Infinities in
+ * a product's operands usually give NaN, as in emu_sgemm; they and NaN stay in
+ * the outputs that they enter.  The kernel
  * timing of emu_profile_enable counts the GEMMs that gated's backward and
  * lora run on emu_sgemm's kernel; the other kernels of this header are not
  * counted.
