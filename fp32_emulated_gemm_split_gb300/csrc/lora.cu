@@ -228,29 +228,39 @@ __global__ void __launch_bounds__(kTileWarps * 32) lora_down_tiles(const LoraPar
     float* S = p.S + slice * p.M * p.R;
     {
         for (int r0 = 0; r0 < p.R; r0 += 16 * G) {
-            auto fill = [&](int st) {
-                if (st >= steps) {                       // (an empty group keeps the count)
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    return;
+            // a thread's copies of a stage: the same rows every time, kTileK
+            // further along; their sources are worked out once
+            constexpr int per = kTileK / V, kCopies = kRows * per / (kTileWarps * 32);
+            static_assert(kRows * per % (kTileWarps * 32) == 0 && (kTileWarps * 32) % per == 0, "whole rows");
+            const int col = tid % per * V;
+            const float* src[kCopies];
+            unsigned live = 0;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int row = tid / per + i * (kTileWarps * 32 / per);
+                bool in;
+                if (row < kTileTok) {
+                    in = row < n;
+                    src[i] = p.X + (int64_t)list[in ? row : 0] * p.ldx;
+                } else {
+                    const int r = r0 + row - kTileTok;
+                    in = r < p.R;
+                    src[i] = p.A + ((int64_t)a * p.R + (in ? r : 0)) * p.K;
                 }
-                float* dst = stage + (st % kTileStages) * kRows * kTileRow;
-                const int64_t k = k0 + (int64_t)st * kTileK;
-                constexpr int per = kTileK / V;      // copies per row
-                for (int e = tid; e < kRows * per; e += kTileWarps * 32) {
-                    const int row = e / per, c = (e % per) * V;
-                    const float* src;
-                    bool in;
-                    if (row < kTileTok) {
-                        in = row < n;
-                        src = p.X + (int64_t)list[in ? row : 0] * p.ldx;
-                    } else {
-                        const int r = r0 + row - kTileTok;
-                        in = r < p.R;
-                        src = p.A + ((int64_t)a * p.R + (in ? r : 0)) * p.K;
+                if (in) live |= 1u << i;
+            }
+            auto fill = [&](int st) {
+                if (st < steps) {                    // (an empty group keeps the count)
+                    float* dst = stage + (st % kTileStages) * kRows * kTileRow + tid / per * kTileRow + col;
+                    const int64_t k = k0 + (int64_t)st * kTileK + col;
+                    const bool here = k < k1;
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        const bool in = here && (live >> i & 1);
+                        float* to = dst + i * (kTileWarps * 32 / per) * kTileRow;
+                        if constexpr (V == 4) cp_async16(to, in ? src[i] + k : src[i], in);
+                        else cp_async4(to, in ? src[i] + k : src[i], in);
                     }
-                    in = in && k + c < k1;
-                    if constexpr (V == 4) cp_async16(dst + row * kTileRow + c, src + (in ? k + c : 0), in);
-                    else cp_async4(dst + row * kTileRow + c, src + (in ? k + c : 0), in);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
@@ -320,12 +330,14 @@ template <int C, int RK>
 constexpr int up_smem() { return C * kUpThreads * (RK + 4); }
 
 // Tokens list[0..nt) (or t0, t0 + 1, .. where list is null) of adapter a;
-// the block's columns are n0 - threadIdx.x + 0 .. C kUpThreads - 1.
+// the block's columns are n0 - threadIdx.x + 0 .. C kUpThreads - 1.  place:
+// room for the tokens' rows of Y.
 template <int C, int RK, int V>
 __device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int32_t* list, int64_t t0,
-                                          int nt, int64_t n0, float (*s)[RK], float* bs) {
+                                          int nt, int64_t n0, float (*s)[RK], float* bs, int32_t* place) {
     const int R = a == p.adapters ? 0 : p.R;
     const float scale = R > 0 && p.scale ? p.scale[a] : 1.0f;
+    for (int t = threadIdx.x; t < nt; t += kUpThreads) place[t] = list ? list[t] : (int32_t)(t0 + t);
     int r0 = 0;
     do {
         if (R > 0) {
@@ -385,7 +397,7 @@ __device__ __forceinline__ void up_tokens(const LoraParams& p, int a, const int3
                 }
 #pragma unroll 4
         for (int t = 0; t < nt; ++t) {
-            float* y = p.Y + (list ? list[t] : t0 + t) * p.ldy + n0;
+            float* y = p.Y + place[t] * p.ldy + n0;
             uint64_t v[C];
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -415,6 +427,7 @@ template <int V, int TOK>
 __global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
     __shared__ __align__(16) float s[TOK][32];
     __shared__ __align__(16) float bs[up_smem<1, 32>()];
+    __shared__ int32_t place[TOK];
     griddep_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * TOK, end = min(p.M, t0 + TOK);
     const int64_t n0 = (int64_t)blockIdx.y * kUpThreads + threadIdx.x;
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(kUpThreads) lora_up_few(const LoraParams p) {
         const int a = adapter_of(p, t);
         int nt = 1;
         while (t + nt < end && adapter_of(p, t + nt) == a) ++nt;
-        up_tokens<1, 32, V>(p, a, nullptr, t, nt, n0, s, bs);
+        up_tokens<1, 32, V>(p, a, nullptr, t, nt, n0, s, bs, place);
         t += nt;
     }
 }
@@ -433,6 +446,7 @@ template <int V, int RK>
 __global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p, int part) {
     __shared__ __align__(16) float s[kTileTok][RK];
     __shared__ __align__(16) float bs[up_smem<2, RK>()];
+    __shared__ int32_t place[kTileTok];
     griddep_launch_dependents();
     griddep_wait();                          // the grouping and S
     if ((int)blockIdx.x >= *p.ntiles) return;
@@ -440,7 +454,7 @@ __global__ void __launch_bounds__(kUpThreads) lora_up_tiles(const LoraParams p, 
     const int first = blockIdx.z * part;
     if (first >= tile.z) return;
     up_tokens<2, RK, V>(p, tile.x, p.order + tile.y + first, 0, min(part, tile.z - first),
-                        (int64_t)blockIdx.y * (2 * kUpThreads) + threadIdx.x, s, bs);
+                        (int64_t)blockIdx.y * (2 * kUpThreads) + threadIdx.x, s, bs, place);
 }
 
 // Tiles that the grouping makes at most.
