@@ -36,6 +36,8 @@ struct Heads {
     int64_t in_t, in_h, dy_t, dy_h, out_t, out_h;
     const float* w;
     int heads;
+    int per_token;           // rounds of a token
+    int per_warp, one_more;  // rounds of a warp; the first one_more warps do one more
 };
 
 struct QkParams {
@@ -310,7 +312,9 @@ struct Ring {
 
 // V pairs per chunk, NC chunks per lane and head, HU heads per lane and round.
 // The rounds of heads (32 / lanes times HU at a time) of all tokens are shared evenly by the warps in consecutive ranges,
-// first those of one side and then of the other.
+// first those of one side and then of the other.  (One range over both sides, most
+// warps on one of them: 8 tokens no faster, 4099 12.0 -> 11.0, but 16384 tokens
+// 61.0 -> 62.5 and 12001 37.3 -> 39.5.)
 //
 // Forward, with the weights folded into the cosines and sines once per token:
 //   y_a = r (a (w_a c) - b (w_b s)),  y_b = r (b (w_b c) + a (w_a s)).
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / p.lanes, pos_in = lane % p.lanes;   // head of the warp's group, lane in it
     const int groups = 32 / p.lanes, at_once = groups * HU;      // heads of a warp's round: u groups + sub
-    const int64_t self = (int64_t)blockIdx.x * kWarps + warp, warps = (int64_t)gridDim.x * kWarps;
+    const int self = blockIdx.x * kWarps + warp;
     const float inv_d = 1.0f / p.D;
     uint8_t* mine = smem + threadIdx.x * B;
     float* dw_sum = reinterpret_cast<float*>(smem + R::bytes);
@@ -338,11 +342,11 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
         const Heads& hd = p.side[s];
-        // this warp's range of the T x per_token rounds
-        const int per_token = (hd.heads + at_once - 1) / at_once;
-        const int64_t all = p.T * per_token;
-        const int64_t begin = self * all / warps;
-        int left = int((self + 1) * all / warps - begin);
+        // this warp's range of the T x per_token rounds (divided on the host: the
+        // 64-bit divisions took 0.3 to 1 us of a call here)
+        const int per_token = hd.per_token;
+        const int64_t begin = (int64_t)self * hd.per_warp + min(self, hd.one_more);
+        int left = hd.per_warp + (self < hd.one_more);
         float wa[E], wb[E];
         uint64_t dwa[BWD ? H : 1], dwb[BWD ? H : 1];
 #pragma unroll
@@ -350,8 +354,8 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
         if constexpr (BWD)
 #pragma unroll
             for (int e = 0; e < H; ++e) dwa[e] = dwb[e] = 0;
-        int t = per_token > 0 ? int(begin / per_token) : 0;
-        int round = per_token > 0 ? int(begin - (int64_t)t * per_token) : 0;
+        int t = left > 0 ? begin <= UINT32_MAX ? int((uint32_t)begin / per_token) : int(begin / per_token) : 0;
+        int round = left > 0 ? int(begin - (int64_t)t * per_token) : 0;
         // the copies' own walk over the rounds, R::depth ahead
         int to_copy = left, copy_at = round, filled = 0;
         const int64_t step_in = at_once * hd.in_h, step_dy = at_once * hd.dy_h;
@@ -570,10 +574,16 @@ template <typename T, bool BWD>
 constexpr int kHeadsPerLane = sizeof(T) == 2 && !BWD ? 2 : 1;
 
 template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
-cudaError_t launch_one(const QkParams& p, int blocks, cudaStream_t stream) {
+cudaError_t launch_one(QkParams p, int blocks, cudaStream_t stream) {
     constexpr int ring = Ring<sizeof(T) * V, NC, BWD, HU>::bytes, per_value = BWD ? kWarps * 2 * (int)sizeof(float) : 0;
     const int smem = ring + per_value * p.D;
     auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL, HU>;
+    for (Heads& h : p.side) {
+        const int at_once = 32 / p.lanes * HU, warps = blocks * kWarps;
+        h.per_token = (h.heads + at_once - 1) / at_once;
+        h.per_warp = int(p.T * h.per_token / warps);
+        h.one_more = int(p.T * h.per_token % warps);
+    }
     if (ring + per_value * kMaxD > 48 << 10) {
         // the limit, raised once per device (g_mu is held)
         static bool done[kMaxDevices] = {};
