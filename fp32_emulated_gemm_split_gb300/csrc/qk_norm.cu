@@ -6,13 +6,18 @@
 //
 // Bound by HBM: the forward reads and writes each head once, the backward
 // reads x and dy and writes dx.  Everything else stays in registers, so the
-// layout is made for that: the values of a head are taken as D/2 pairs, the
-// rotated ones (j, j + rot/2) or (2j, 2j + 1), the rest (rot + j, rot + rest/2
-// + j); a lane holds V neighbouring pairs (two loads of V values), so a
-// rotation needs no other lane, and D/2/V lanes (rounded up to a power of two,
-// at most a warp) hold a head.  A warp walks a range of
-// heads, 32 / lanes of them at a time: the weights, and a token's cosines and
-// sines, are read once and kept in registers.
+// layout is made for that.  Halves: the values of a head are taken as D/2 pairs,
+// the rotated ones (j, j + rot/2), the rest (rot + j, rot + rest/2 + j); a lane
+// holds V neighbouring pairs (two loads of V values).  Neighbouring pairs (2j,
+// 2j + 1): a lane holds 2 V values in a row.  So a rotation needs no other lane,
+// and D/2/V lanes (rounded up to a power of two, at most a warp) hold a head.  A
+// warp walks a range of heads, 32 / lanes of them at a time: the weights, and a
+// token's cosines and sines, are read once and kept in registers.
+//
+// What a round costs beyond the bytes are its instructions: values stay packed
+// in pairs as they lie in memory (fma.rn.f32x2), and where the layout allows it
+// no copy or load is guarded (a lane without a chunk, or a head past the end,
+// does another's and stores nothing).
 //
 // The weights' gradients are summed per lane over the tokens of its warp,
 // then over the block in shared memory, and one row per block goes to the
@@ -91,21 +96,26 @@ template <> __device__ __forceinline__ uint32_t narrow<__half>(float lo, float h
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Where the pair chunk of lane position c (pairs c V .. c V + V - 1) lies:
-// first and second elements' offsets in the head, and whether they exist.
-// An odd rest (V = 1 only) leaves the last pair without a second element.
+// Where the chunk of lane position c (pairs c V .. c V + V - 1) lies: first and
+// second vectors' offsets in the head, and whether they exist.  An odd rest (V =
+// 1 only) leaves the last pair without a second element.
 template <int V, bool PAIRS>
 struct Chunk {
-    int a, b, j;             // offsets of the first elements; rotary index
+    int a, b, j;             // offsets of the vectors; rotary index
     bool rotated, has_a, has_b;
     Chunk() = default;
     __device__ __forceinline__ Chunk(int c, int D, int rot) {
         const int p = c * V, half = rot / 2, rest = D - rot, q = p - half;
         rotated = p < half;
         j = p;
-        if (rotated) {
-            a = PAIRS ? 2 * p : p;
-            b = PAIRS ? 2 * p + V : p + half;
+        if (PAIRS) {
+            a = 2 * p;
+            b = a + V;
+            has_a = a < D;
+            has_b = b < D;
+        } else if (rotated) {
+            a = p;
+            b = p + half;
             has_a = has_b = true;
         } else {
             const int up = (rest + 1) / 2;
@@ -117,9 +127,9 @@ struct Chunk {
     }
 };
 
-// A lane's chunks as they lie in memory: NC pairs of vectors.
+// A lane's chunk as it lies in memory: two vectors (of neighbouring pairs: in a row).
 template <typename T, int V>
-struct Raw {
+struct alignas(sizeof(T) * V >= 16 || V == 1 ? sizeof(T) * V : 2 * sizeof(T) * V) Raw {
     Vec<T, V> a, b;
 };
 template <typename T, int V, int NC, bool PAIRS>
@@ -133,9 +143,13 @@ __device__ __forceinline__ void load_chunks(const T* head, const Chunk<V, PAIRS>
     }
 }
 
+// One access for both vectors where they lie in a row and make up to 16 bytes.
+template <typename T, int V, bool PAIRS>
+constexpr bool kJoined = PAIRS && V > 1 && 2 * V * sizeof(T) <= 16;
+
 // The same by asynchronous copies into this thread's own slots of shared
-// memory (zeros where there is nothing), and back: a thread reads only what it
-// copied itself, so its own wait for the copies is all the order needed.
+// memory (GUARD: zeros where there is nothing), and back: a thread reads only
+// what it copied itself, so its own wait for the copies is all the order needed.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
     if constexpr (BYTES == 16)
@@ -144,113 +158,144 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool i
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
                      :: "r"(dst), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
 }
-template <typename T, int V, int NC, bool PAIRS, bool FULL>
+template <typename T, int V, int NC, bool PAIRS, bool GUARD>
 __device__ __forceinline__ void copy_chunks(const T* head, const Chunk<V, PAIRS> (&ck)[NC], bool in,
                                             uint32_t slot, uint32_t step) {
     constexpr int B = sizeof(T) * V;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-        const bool a = FULL || (in && ck[n].has_a), b = FULL || (in && ck[n].has_b);
-        copy_async<B>(slot + 2 * n * step, a ? head + ck[n].a : head, a);
-        copy_async<B>(slot + (2 * n + 1) * step, b ? head + ck[n].b : head, b);
+        const bool a = !GUARD || (in && ck[n].has_a), b = !GUARD || (in && ck[n].has_b);
+        if constexpr (kJoined<T, V, PAIRS>) {
+            copy_async<2 * B>(slot + n * step, a ? head + ck[n].a : head, a);
+        } else {
+            copy_async<B>(slot + 2 * n * step, a ? head + ck[n].a : head, a);
+            copy_async<B>(slot + (2 * n + 1) * step, b ? head + ck[n].b : head, b);
+        }
     }
 }
-template <typename T, int V, int NC>
+template <typename T, int V, int NC, bool PAIRS>
 __device__ __forceinline__ void read_chunks(const uint8_t* slot, uint32_t step, Raw<T, V> (&r)[NC]) {
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-        r[n].a = *reinterpret_cast<const Vec<T, V>*>(slot + 2 * n * step);
-        r[n].b = *reinterpret_cast<const Vec<T, V>*>(slot + (2 * n + 1) * step);
+        if constexpr (kJoined<T, V, PAIRS>) {
+            r[n] = *reinterpret_cast<const Raw<T, V>*>(slot + n * step);
+        } else {
+            r[n].a = *reinterpret_cast<const Vec<T, V>*>(slot + 2 * n * step);
+            r[n].b = *reinterpret_cast<const Vec<T, V>*>(slot + (2 * n + 1) * step);
+        }
     }
 }
 
-// Their values: first elements a[], second b[], as packed pairs.  Rotated
-// neighbouring pairs lie as a0 b0 a1 b1 ..: two vectors in a row.
+// A lane's NC V pairs of values, packed: for wide chunks as they lie in memory,
+// those of a chunk's first vector and then of its second; V = 1: the first
+// elements of two chunks and then their second ones (neighbouring pairs: a
+// chunk's own two).
 template <typename T, int V, int NC, bool PAIRS>
-__device__ __forceinline__ void unpack(const Raw<T, V> (&r)[NC], const Chunk<V, PAIRS> (&ck)[NC],
-                                       uint64_t (&a)[NC * V / 2], uint64_t (&b)[NC * V / 2]) {
-    if constexpr (V == 1) {                          // (neighbouring pairs: a and b are what they are)
+__device__ __forceinline__ void unpack(const Raw<T, V> (&r)[NC], uint64_t (&x)[NC * V]) {
+    if constexpr (V == 1 && PAIRS) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) x[n] = pk(to_f32(r[n].a.v[0]), to_f32(r[n].b.v[0]));
+    } else if constexpr (V == 1) {
 #pragma unroll
         for (int n = 0; n < NC; n += 2) {
-            a[n / 2] = pk(to_f32(r[n].a.v[0]), to_f32(r[n + 1].a.v[0]));
-            b[n / 2] = pk(to_f32(r[n].b.v[0]), to_f32(r[n + 1].b.v[0]));
+            x[n] = pk(to_f32(r[n].a.v[0]), to_f32(r[n + 1].a.v[0]));
+            x[n + 1] = pk(to_f32(r[n].b.v[0]), to_f32(r[n + 1].b.v[0]));
         }
     } else {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            uint64_t lo[V / 2], hi[V / 2];           // pairs of the first and of the second vector
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                if constexpr (sizeof(T) == 4) {
-                    lo[i] = pk(r[n].a.v[2 * i], r[n].a.v[2 * i + 1]);
-                    hi[i] = pk(r[n].b.v[2 * i], r[n].b.v[2 * i + 1]);
-                } else {
-                    lo[i] = widen<T>(reinterpret_cast<const uint32_t*>(r[n].a.v)[i]);
-                    hi[i] = widen<T>(reinterpret_cast<const uint32_t*>(r[n].b.v)[i]);
-                }
+            for (int i = 0; i < V; ++i) {
+                const Vec<T, V>& from = i < V / 2 ? r[n].a : r[n].b;
+                const int at = i % (V / 2);
+                if constexpr (sizeof(T) == 4) x[n * V + i] = pk(from.v[2 * at], from.v[2 * at + 1]);
+                else x[n * V + i] = widen<T>(reinterpret_cast<const uint32_t*>(from.v)[at]);
             }
-            uint64_t* an = a + n * (V / 2);
-            uint64_t* bn = b + n * (V / 2);
-            if (PAIRS && ck[n].rotated) {
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) {    // pairs 2 i and 2 i + 1 of the 2 V values in a row
-                    const uint64_t p0 = 2 * i < V / 2 ? lo[(2 * i) % (V / 2)] : hi[(2 * i) % (V / 2)];
-                    const uint64_t p1 = 2 * i + 1 < V / 2 ? lo[(2 * i + 1) % (V / 2)] : hi[(2 * i + 1) % (V / 2)];
-                    an[i] = pk(lo_of(p0), lo_of(p1));
-                    bn[i] = pk(hi_of(p0), hi_of(p1));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                    an[i] = lo[i];
-                    bn[i] = hi[i];
-                }
-            }
-        }
     }
 }
 
-template <typename T, int V, int NC, bool PAIRS, bool FULL>
-__device__ __forceinline__ void store_chunks(T* head, const Chunk<V, PAIRS> (&ck)[NC],
-                                             const uint64_t (&a)[NC * V / 2], const uint64_t (&b)[NC * V / 2]) {
+template <typename T, int V, int NC, bool PAIRS, bool GUARD>
+__device__ __forceinline__ void store_chunks(T* head, const Chunk<V, PAIRS> (&ck)[NC], const uint64_t (&x)[NC * V]) {
     if constexpr (V == 1) {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            if (ck[n].has_a) head[ck[n].a] = from_f32<T>(n & 1 ? hi_of(a[n / 2]) : lo_of(a[n / 2]));
-            if (ck[n].has_b) head[ck[n].b] = from_f32<T>(n & 1 ? hi_of(b[n / 2]) : lo_of(b[n / 2]));
+            const float a = PAIRS ? lo_of(x[n]) : n & 1 ? hi_of(x[n - 1]) : lo_of(x[n]);
+            const float b = PAIRS ? hi_of(x[n]) : n & 1 ? hi_of(x[n]) : lo_of(x[n + 1]);
+            if (ck[n].has_a) head[ck[n].a] = from_f32<T>(a);
+            if (ck[n].has_b) head[ck[n].b] = from_f32<T>(b);
         }
     } else {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            const uint64_t* an = a + n * (V / 2);
-            const uint64_t* bn = b + n * (V / 2);
-            uint64_t lo[V / 2], hi[V / 2];
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                lo[i] = an[i];
-                hi[i] = bn[i];
-            }
-            if (PAIRS && ck[n].rotated) {
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) {
-                    const uint64_t p0 = pk(lo_of(an[i]), lo_of(bn[i])), p1 = pk(hi_of(an[i]), hi_of(bn[i]));
-                    (2 * i < V / 2 ? lo : hi)[(2 * i) % (V / 2)] = p0;
-                    (2 * i + 1 < V / 2 ? lo : hi)[(2 * i + 1) % (V / 2)] = p1;
-                }
-            }
             Raw<T, V> r;
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
+            for (int i = 0; i < V; ++i) {
+                Vec<T, V>& to = i < V / 2 ? r.a : r.b;
+                const int at = i % (V / 2);
+                const uint64_t v = x[n * V + i];
                 if constexpr (sizeof(T) == 4) {
-                    r.a.v[2 * i] = lo_of(lo[i]); r.a.v[2 * i + 1] = hi_of(lo[i]);
-                    r.b.v[2 * i] = lo_of(hi[i]); r.b.v[2 * i + 1] = hi_of(hi[i]);
+                    to.v[2 * at] = lo_of(v);
+                    to.v[2 * at + 1] = hi_of(v);
                 } else {
-                    reinterpret_cast<uint32_t*>(r.a.v)[i] = narrow<T>(lo_of(lo[i]), hi_of(lo[i]));
-                    reinterpret_cast<uint32_t*>(r.b.v)[i] = narrow<T>(lo_of(hi[i]), hi_of(hi[i]));
+                    reinterpret_cast<uint32_t*>(to.v)[at] = narrow<T>(lo_of(v), hi_of(v));
                 }
             }
-            if (FULL || ck[n].has_a) *reinterpret_cast<Vec<T, V>*>(head + ck[n].a) = r.a;
-            if (FULL || ck[n].has_b) *reinterpret_cast<Vec<T, V>*>(head + ck[n].b) = r.b;
+            if constexpr (kJoined<T, V, PAIRS>) {
+                if (!GUARD || ck[n].has_a) *reinterpret_cast<Raw<T, V>*>(head + ck[n].a) = r;
+            } else {
+                if (!GUARD || ck[n].has_a) *reinterpret_cast<Vec<T, V>*>(head + ck[n].a) = r.a;
+                if (!GUARD || ck[n].has_b) *reinterpret_cast<Vec<T, V>*>(head + ck[n].b) = r.b;
+            }
+        }
+    }
+}
+
+// Turns a lane's pairs, coefficients k1 and k2:
+//   halves: first' = first k1[first] + second k2[second], second' = second k1[second] + first k2[first]
+//   neighbouring pairs: (a, b)' = (a, b) k1 + (b, a) k2
+// and makes the coefficients from a lane's cosines c and sines s (of the turn, or
+// of its reverse with -s) and weights (as pairs; null: ones).
+template <int V, int NC>
+struct Halves {                                      // the k-th first and second vector's pair
+    static constexpr int a(int k) { return V == 1 ? 2 * k : k / (V / 2) * V + k % (V / 2); }
+    static constexpr int b(int k) { return V == 1 ? 2 * k + 1 : a(k) + V / 2; }
+};
+template <int V, int NC, bool PAIRS>
+__device__ __forceinline__ void make_turn(const float* c, const float* s, float sign, const uint64_t* w,
+                                          uint64_t (&k1)[NC * V], uint64_t (&k2)[NC * V]) {
+    using H = Halves<V, NC>;
+    if constexpr (PAIRS) {
+#pragma unroll
+        for (int e = 0; e < NC * V; ++e) {
+            const float wa = w ? lo_of(w[e]) : 1.0f, wb = w ? hi_of(w[e]) : 1.0f, sn = sign * s[e];
+            k1[e] = pk(wa * c[e], wb * c[e]);
+            k2[e] = pk(-wb * sn, wa * sn);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < NC * V / 2; ++k) {
+            const uint64_t cc = pk(c[2 * k], c[2 * k + 1]), sp = pk(sign * s[2 * k], sign * s[2 * k + 1]);
+            const uint64_t sm = pk(-sign * s[2 * k], -sign * s[2 * k + 1]);
+            k1[H::a(k)] = w ? mul_f32x2(w[H::a(k)], cc) : cc;
+            k1[H::b(k)] = w ? mul_f32x2(w[H::b(k)], cc) : cc;
+            k2[H::a(k)] = w ? mul_f32x2(w[H::a(k)], sp) : sp;
+            k2[H::b(k)] = w ? mul_f32x2(w[H::b(k)], sm) : sm;
+        }
+    }
+}
+template <int V, int NC, bool PAIRS>
+__device__ __forceinline__ void turn(uint64_t (&x)[NC * V], const uint64_t (&k1)[NC * V], const uint64_t (&k2)[NC * V]) {
+    using H = Halves<V, NC>;
+    if constexpr (PAIRS) {
+#pragma unroll
+        for (int e = 0; e < NC * V; ++e)
+            x[e] = fma_f32x2(pk(hi_of(x[e]), lo_of(x[e])), k2[e], mul_f32x2(x[e], k1[e]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < NC * V / 2; ++k) {
+            const uint64_t a = x[H::a(k)], b = x[H::b(k)];
+            x[H::a(k)] = fma_f32x2(b, k2[H::b(k)], mul_f32x2(a, k1[H::a(k)]));
+            x[H::b(k)] = fma_f32x2(a, k2[H::a(k)], mul_f32x2(b, k1[H::b(k)]));
         }
     }
 }
@@ -289,25 +334,33 @@ __device__ __forceinline__ void load_turn(const QkParams& p, int64_t pos, bool p
     }
 }
 
-template <int V, bool PAIRS>
-__device__ __forceinline__ void load_weight(const float* w, const Chunk<V, PAIRS>& ck, float* wa, float* wb) {
+// The weights of a lane's chunks, as pairs like its values (ones where w is null).
+template <int V, int NC, bool PAIRS>
+__device__ __forceinline__ void load_weights(const float* w, const Chunk<V, PAIRS> (&ck)[NC], uint64_t (&out)[NC * V]) {
+    Raw<float, V> r[NC];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        wa[i] = w && ck.has_a ? w[PAIRS && ck.rotated ? ck.a + 2 * i : ck.a + i] : 1.0f;
-        wb[i] = w && ck.has_b ? w[PAIRS && ck.rotated ? ck.a + 2 * i + 1 : ck.b + i] : 1.0f;
-    }
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            r[n].a.v[i] = w && ck[n].has_a ? w[ck[n].a + i] : 1.0f;
+            r[n].b.v[i] = w && ck[n].has_b ? w[ck[n].b + i] : 1.0f;
+        }
+    unpack<float, V, NC, PAIRS>(r, out);
 }
 
 // Rounds of heads in flight per warp: shared memory holds them, so that HBM's
 // latency is covered by bytes on the way and not by registers.
 constexpr int kWarps = 8;                    // per block
-template <int BYTES, int NC, bool BWD, int HU>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int HU>
 struct Ring {
-    static constexpr bool used = BYTES >= 4;         // (cp.async copies 4, 8 or 16 bytes)
-    static constexpr int per_head = (BWD ? 4 : 2) * NC;              // copies per lane
+    static constexpr int copy = (kJoined<T, V, PAIRS> ? 2 : 1) * V * (int)sizeof(T);
+    static constexpr bool used = copy >= 4;          // (cp.async copies 4, 8 or 16 bytes)
+    static constexpr int per_tensor = (kJoined<T, V, PAIRS> ? 1 : 2) * NC;   // copies per lane and head
+    static constexpr int per_head = per_tensor * (BWD ? 2 : 1);
     static constexpr int per_round = per_head * HU;
+    static constexpr int step = kWarps * 32 * copy;  // from one copy's slots to the next
     static constexpr int depth = 3;
-    static constexpr int bytes = used ? depth * per_round * BYTES * kWarps * 32 : 0;
+    static constexpr int bytes = used ? depth * per_round * step : 0;
 };
 
 // V pairs per chunk, NC chunks per lane and head, HU heads per lane and round.
@@ -319,26 +372,33 @@ struct Ring {
 // Forward, with the weights folded into the cosines and sines once per token:
 //   y_a = r (a (w_a c) - b (w_b s)),  y_b = r (b (w_b c) + a (w_a s)).
 //
-// FULL: every lane has both of its chunks in every round (the head's chunks
-// are the lanes of a group, and whole rounds make up both sides): no guards.
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
+// LAYOUT kWhole: a head's chunks fit its lanes and whole rounds make up both
+// sides: nothing is guarded (a lane without a chunk does the last one's and
+// neither adds nor stores it).  kTail (forward): a head past the end reads the
+// first one and is not stored.  kAny: every access is guarded.
+enum { kAny, kTail, kWhole };
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, int LAYOUT, int HU>
 __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParams p) {
+    static_assert(LAYOUT == kAny || NC == 1, "one chunk per lane");
+    static_assert(!(BWD && LAYOUT == kTail), "what is read twice would count in dw");
+    constexpr bool GUARD = LAYOUT == kAny;
     extern __shared__ __align__(16) uint8_t smem[];              // the rings; backward: then [warp][2][D]
-    constexpr int E = NC * V, H = E / 2;                         // pairs a lane holds, packed
+    constexpr int E = NC * V;                                    // pairs a lane holds
     static_assert(E % 2 == 0, "pairs of values");
-    constexpr int B = sizeof(T) * V;
-    using R = Ring<B, NC, BWD, HU>;
-    constexpr uint32_t kStep = kWarps * 32 * B;                  // from one copy's slots to the next
+    using R = Ring<T, V, NC, PAIRS, BWD, HU>;
+    constexpr uint32_t kStep = R::step;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / p.lanes, pos_in = lane % p.lanes;   // head of the warp's group, lane in it
     const int groups = 32 / p.lanes, at_once = groups * HU;      // heads of a warp's round: u groups + sub
     const int self = blockIdx.x * kWarps + warp;
     const float inv_d = 1.0f / p.D;
-    uint8_t* mine = smem + threadIdx.x * B;
+    uint8_t* mine = smem + threadIdx.x * R::copy;
     float* dw_sum = reinterpret_cast<float*>(smem + R::bytes);
     Chunk<V, PAIRS> ck[NC];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) ck[n] = Chunk<V, PAIRS>(pos_in + n * p.lanes, p.D, p.rot);
+    for (int n = 0; n < NC; ++n)
+        ck[n] = Chunk<V, PAIRS>(GUARD ? pos_in + n * p.lanes : min(pos_in, p.D / (2 * V) - 1), p.D, p.rot);
+    const bool mine_counts = GUARD || pos_in < p.D / (2 * V);
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
         const Heads& hd = p.side[s];
@@ -347,13 +407,10 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
         const int per_token = hd.per_token;
         const int64_t begin = (int64_t)self * hd.per_warp + min(self, hd.one_more);
         int left = hd.per_warp + (self < hd.one_more);
-        float wa[E], wb[E];
-        uint64_t dwa[BWD ? H : 1], dwb[BWD ? H : 1];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) load_weight<V, PAIRS>(hd.w, ck[n], wa + n * V, wb + n * V);
+        uint64_t w[E], dw[BWD ? E : 1];
         if constexpr (BWD)
 #pragma unroll
-            for (int e = 0; e < H; ++e) dwa[e] = dwb[e] = 0;
+            for (int e = 0; e < E; ++e) dw[e] = 0;
         int t = left > 0 ? begin <= UINT32_MAX ? int((uint32_t)begin / per_token) : int(begin / per_token) : 0;
         int round = left > 0 ? int(begin - (int64_t)t * per_token) : 0;
         // the copies' own walk over the rounds, R::depth ahead
@@ -368,14 +425,14 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
                 const uint32_t slot = smem_u32(mine) + filled * (R::per_round * kStep);
 #pragma unroll
                 for (int u = 0; u < HU; ++u) {
-                    // (a head past the end: any address in range, nothing is read)
-                    const bool in = FULL || copy_at * at_once + u * groups + sub < hd.heads;
-                    copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_in + u * groups * hd.in_h : static_cast<const T*>(hd.in),
-                                                       ck, in, slot + u * R::per_head * kStep, kStep);
+                    // (a head past the end: any address in range)
+                    const bool in = LAYOUT == kWhole || copy_at * at_once + u * groups + sub < hd.heads;
+                    copy_chunks<T, V, NC, PAIRS, GUARD>(in ? copy_in + u * groups * hd.in_h : static_cast<const T*>(hd.in),
+                                                        ck, in, slot + u * R::per_head * kStep, kStep);
                     if constexpr (BWD)
-                        copy_chunks<T, V, NC, PAIRS, FULL>(in ? copy_dy + u * groups * hd.dy_h
-                                                              : static_cast<const T*>(hd.dy),
-                                                           ck, in, slot + (u * R::per_head + 2 * NC) * kStep, kStep);
+                        copy_chunks<T, V, NC, PAIRS, GUARD>(in ? copy_dy + u * groups * hd.dy_h
+                                                               : static_cast<const T*>(hd.dy),
+                                                            ck, in, slot + (u * R::per_head + R::per_tensor) * kStep, kStep);
                 }
                 filled = filled + 1 == R::depth ? 0 : filled + 1;
                 copy_in += step_in;
@@ -400,28 +457,16 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
 #pragma unroll
             for (int n = 0; n < NC; ++n) load_turn<V, PAIRS>(p, pos, ok, ck[n], c + n * V, sn + n * V);
         };
-        int next_pos = 0;
-        if (left > 0) {
-            turn_of(pos_of(t));
-            next_pos = pos_of(t + 1);
-        }
+        // (after the first copies, none of which waits for these)
+        const int pos = left > 0 ? pos_of(t) : 0;
+        int next_pos = left > 0 ? pos_of(t + 1) : 0;
+        load_weights<V, NC, PAIRS>(left > 0 ? hd.w : nullptr, ck, w);
+        if (left > 0) turn_of(pos);
         while (left > 0) {
             const int here = min(left, per_token - round);       // rounds of this token
             left -= here;
-            uint64_t ac[H], bc[H], as[H], nbs[H];
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                if constexpr (BWD) {
-                    ac[e / 2] = pk(c[e], c[e + 1]);
-                    as[e / 2] = pk(sn[e], sn[e + 1]);
-                    nbs[e / 2] = pk(-sn[e], -sn[e + 1]);
-                } else {
-                    ac[e / 2] = pk(wa[e] * c[e], wa[e + 1] * c[e + 1]);
-                    as[e / 2] = pk(wa[e] * sn[e], wa[e + 1] * sn[e + 1]);
-                    bc[e / 2] = pk(wb[e] * c[e], wb[e + 1] * c[e + 1]);
-                    nbs[e / 2] = pk(-wb[e] * sn[e], -wb[e + 1] * sn[e + 1]);
-                }
-            }
+            uint64_t k1[E], k2[E];
+            make_turn<V, NC, PAIRS>(c, sn, BWD ? -1.0f : 1.0f, BWD ? nullptr : w, k1, k2);
             if (left > 0) {
                 turn_of(next_pos);
                 next_pos = pos_of(t + 2);
@@ -431,14 +476,17 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
             // every lane of the warp runs every round (the sums are shuffles)
             for (int i = 0; i < here; ++i, out += step_out) {
                 Raw<T, V> rx[HU][NC], rd[HU][NC];
-                auto live = [&](int u) { return FULL || (round + i) * at_once + u * groups + sub < hd.heads; };
+                auto live = [&](int u) {
+                    return LAYOUT == kWhole || (round + i) * at_once + u * groups + sub < hd.heads;
+                };
                 if constexpr (R::used) {
                     asm volatile("cp.async.wait_group %0;" :: "n"(R::depth - 1) : "memory");
                     const uint8_t* slot = mine + read * (R::per_round * kStep);
 #pragma unroll
                     for (int u = 0; u < HU; ++u) {
-                        read_chunks<T, V, NC>(slot + u * R::per_head * kStep, kStep, rx[u]);
-                        if constexpr (BWD) read_chunks<T, V, NC>(slot + (u * R::per_head + 2 * NC) * kStep, kStep, rd[u]);
+                        read_chunks<T, V, NC, PAIRS>(slot + u * R::per_head * kStep, kStep, rx[u]);
+                        if constexpr (BWD)
+                            read_chunks<T, V, NC, PAIRS>(slot + (u * R::per_head + R::per_tensor) * kStep, kStep, rd[u]);
                     }
                     read = read + 1 == R::depth ? 0 : read + 1;
                     copy_round();                                // into the slots just read
@@ -453,28 +501,23 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
                                                          live(u), rd[u]);
                     }
                 }
-                uint64_t xa[HU][H], xb[HU][H], da[BWD ? HU : 1][H], db[BWD ? HU : 1][H];
+                uint64_t x[HU][E], dn[BWD ? HU : 1][E];
                 float ss[HU], sd[HU];
 #pragma unroll
                 for (int u = 0; u < HU; ++u) {
                     uint64_t q = 0;
-                    unpack<T, V, NC, PAIRS>(rx[u], ck, xa[u], xb[u]);
+                    unpack<T, V, NC, PAIRS>(rx[u], x[u]);
 #pragma unroll
-                    for (int e = 0; e < H; ++e) q = fma_f32x2(xb[u][e], xb[u][e], fma_f32x2(xa[u][e], xa[u][e], q));
-                    ss[u] = lo_of(q) + hi_of(q);
+                    for (int e = 0; e < E; ++e) q = fma_f32x2(x[u][e], x[u][e], q);
+                    ss[u] = mine_counts ? lo_of(q) + hi_of(q) : 0.0f;
                     if constexpr (BWD) {
                         // dn, the output's gradient turned back; its sum with w x
                         uint64_t z = 0;
-                        unpack<T, V, NC, PAIRS>(rd[u], ck, da[u], db[u]);
+                        unpack<T, V, NC, PAIRS>(rd[u], dn[u]);
+                        turn<V, NC, PAIRS>(dn[u], k1, k2);
 #pragma unroll
-                        for (int e = 0; e < H; ++e) {
-                            const uint64_t ga = fma_f32x2(db[u][e], as[e], mul_f32x2(da[u][e], ac[e]));
-                            db[u][e] = fma_f32x2(da[u][e], nbs[e], mul_f32x2(db[u][e], ac[e]));
-                            da[u][e] = ga;
-                            z = fma_f32x2(mul_f32x2(ga, pk(wa[2 * e], wa[2 * e + 1])), xa[u][e], z);
-                            z = fma_f32x2(mul_f32x2(db[u][e], pk(wb[2 * e], wb[2 * e + 1])), xb[u][e], z);
-                        }
-                        sd[u] = lo_of(z) + hi_of(z);
+                        for (int e = 0; e < E; ++e) z = fma_f32x2(mul_f32x2(dn[u][e], w[e]), x[u][e], z);
+                        sd[u] = mine_counts ? lo_of(z) + hi_of(z) : 0.0f;
                     }
                 }
                 for (int o = p.lanes >> 1; o > 0; o >>= 1) {
@@ -492,22 +535,17 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
                         const float m = sd[u] * inv_d * r * r;
                         const uint64_t nm = pk(-m, -m);
 #pragma unroll
-                        for (int e = 0; e < H; ++e) {            // r (dn w - x m)
-                            const uint64_t a = xa[u][e], b = xb[u][e];
-                            dwa[e] = fma_f32x2(da[u][e], mul_f32x2(a, rr), dwa[e]);
-                            dwb[e] = fma_f32x2(db[u][e], mul_f32x2(b, rr), dwb[e]);
-                            xa[u][e] = mul_f32x2(rr, fma_f32x2(a, nm, mul_f32x2(da[u][e], pk(wa[2 * e], wa[2 * e + 1]))));
-                            xb[u][e] = mul_f32x2(rr, fma_f32x2(b, nm, mul_f32x2(db[u][e], pk(wb[2 * e], wb[2 * e + 1]))));
+                        for (int e = 0; e < E; ++e) {            // r (dn w - x m)
+                            dw[e] = fma_f32x2(dn[u][e], mul_f32x2(x[u][e], rr), dw[e]);
+                            x[u][e] = mul_f32x2(rr, fma_f32x2(x[u][e], nm, mul_f32x2(dn[u][e], w[e])));
                         }
                     } else {
+                        turn<V, NC, PAIRS>(x[u], k1, k2);
 #pragma unroll
-                        for (int e = 0; e < H; ++e) {
-                            const uint64_t a = xa[u][e], b = xb[u][e];
-                            xa[u][e] = mul_f32x2(rr, fma_f32x2(b, nbs[e], mul_f32x2(a, ac[e])));
-                            xb[u][e] = mul_f32x2(rr, fma_f32x2(a, as[e], mul_f32x2(b, bc[e])));
-                        }
+                        for (int e = 0; e < E; ++e) x[u][e] = mul_f32x2(rr, x[u][e]);
                     }
-                    if (live(u)) store_chunks<T, V, NC, PAIRS, FULL>(out + u * groups * hd.out_h, ck, xa[u], xb[u]);
+                    if (live(u) && mine_counts)
+                        store_chunks<T, V, NC, PAIRS, GUARD>(out + u * groups * hd.out_h, ck, x[u]);
                 }
             }
             round = 0;
@@ -517,22 +555,15 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
         if constexpr (BWD) {
             // over the warp's heads (lanes without a head read zeros and added zeros)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = n * V + i;
-                    float va = e & 1 ? hi_of(dwa[e / 2]) : lo_of(dwa[e / 2]);
-                    float vb = e & 1 ? hi_of(dwb[e / 2]) : lo_of(dwb[e / 2]);
-                    for (int o = p.lanes; o < 32; o <<= 1) {
-                        va += __shfl_xor_sync(0xffffffffu, va, o);
-                        vb += __shfl_xor_sync(0xffffffffu, vb, o);
-                    }
-                    float* to = dw_sum + (warp * 2 + s) * p.D;
-                    const bool row = PAIRS && ck[n].rotated;
-                    if (sub == 0 && ck[n].has_a) to[row ? ck[n].a + 2 * i : ck[n].a + i] = va;
-                    if (sub == 0 && ck[n].has_b) to[row ? ck[n].a + 2 * i + 1 : ck[n].b + i] = vb;
+            for (int e = 0; e < E; ++e) {
+                float lo = lo_of(dw[e]), hi = hi_of(dw[e]);
+                for (int o = p.lanes; o < 32; o <<= 1) {
+                    lo += __shfl_xor_sync(0xffffffffu, lo, o);
+                    hi += __shfl_xor_sync(0xffffffffu, hi, o);
                 }
+                dw[e] = pk(lo, hi);
             }
+            if (sub == 0 && mine_counts) store_chunks<float, V, NC, PAIRS, GUARD>(dw_sum + (warp * 2 + s) * p.D, ck, dw);
         }
     }
     if constexpr (BWD) {
@@ -573,11 +604,11 @@ constexpr int kBlocksPerSm = 2;
 template <typename T, bool BWD>
 constexpr int kHeadsPerLane = sizeof(T) == 2 && !BWD ? 2 : 1;
 
-template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, bool FULL, int HU>
+template <typename T, int V, int NC, bool PAIRS, bool BWD, int BPS, int LAYOUT, int HU>
 cudaError_t launch_one(QkParams p, int blocks, cudaStream_t stream) {
-    constexpr int ring = Ring<sizeof(T) * V, NC, BWD, HU>::bytes, per_value = BWD ? kWarps * 2 * (int)sizeof(float) : 0;
+    constexpr int ring = Ring<T, V, NC, PAIRS, BWD, HU>::bytes, per_value = BWD ? kWarps * 2 * (int)sizeof(float) : 0;
     const int smem = ring + per_value * p.D;
-    auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, FULL, HU>;
+    auto kern = qk_norm_kernel<T, V, NC, PAIRS, BWD, BPS, LAYOUT, HU>;
     for (Heads& h : p.side) {
         const int at_once = 32 / p.lanes * HU, warps = blocks * kWarps;
         h.per_token = (h.heads + at_once - 1) / at_once;
@@ -606,15 +637,19 @@ cudaError_t launch_one(QkParams p, int blocks, cudaStream_t stream) {
 // 91 with four pairs, 67 / 112 with eight (whose cosines, sines and weights
 // alone take 64 registers); float32, 8192 x 24 x 128, 39 / 56.  Two blocks per
 // SM: 62 / 91; three 64 / 107; four 68 / 107.  Two heads per lane and round in
-// the 16-bit forward pass: float16, 12001 x 28 x 96, 42 -> 38.  (Bytes at the
-// HBM's rate: 49 / 74, 30 / 45, 19 / 29.)  Before the rings the loads waited in
-// registers: 89 us forward.
+// the 16-bit forward pass: float16, neighbouring pairs, 12001 x 28 x 96, 42 ->
+// 38; values packed as they lie and no guards: 37 / 62 -> 30 / 50 (a round took
+// 327 instructions, two thirds of all issue slots).  Three chunks per lane where
+// that leaves fewer lanes idle (96: 4 lanes of 3): 46 / 68, registers spilled.
+// (Bytes at the HBM's rate: 49 / 74, 30 / 45, 19 / 29.)  Before the rings the
+// loads waited in registers: 89 us forward.
 template <typename T, bool PAIRS, bool BWD>
 cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t stream) {
     constexpr int V = 4;
     bool wide = p.rot % (2 * V) == 0 && (p.D - p.rot) % (2 * V) == 0;
+    constexpr int kWide = kJoined<T, V, PAIRS> ? 2 * V : V;          // values of an access
     auto whole = [&](const void* q, int64_t ts, int64_t hs) {
-        return reinterpret_cast<uintptr_t>(q) % (V * sizeof(T)) == 0 && ts % V == 0 && hs % V == 0;
+        return reinterpret_cast<uintptr_t>(q) % (kWide * sizeof(T)) == 0 && ts % kWide == 0 && hs % kWide == 0;
     };
     for (const Heads& h : p.side)
         if (h.heads > 0)
@@ -634,13 +669,13 @@ cudaError_t launch_typed(QkParams p, int max_blocks, int* blocks, cudaStream_t s
     const int64_t want = (p.T * ((most + at_once - 1) / at_once) + kWarps - 1) / kWarps;
     *blocks = (int)(want < max_blocks ? want : max_blocks);
     if (wide) {
-        const bool full = chunks == p.lanes && p.side[0].heads % at_once == 0 && p.side[1].heads % at_once == 0;
-        if (nc == 1 && full) return launch_one<T, V, 1, PAIRS, BWD, BPS, true, HU>(p, *blocks, stream);
-        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, BPS, false, HU>(p, *blocks, stream);
-        return launch_one<T, V, 2, PAIRS, BWD, 1, false, 1>(p, *blocks, stream);
+        const bool whole_rounds = p.side[0].heads % at_once == 0 && p.side[1].heads % at_once == 0;
+        if (nc == 1 && whole_rounds) return launch_one<T, V, 1, PAIRS, BWD, BPS, kWhole, HU>(p, *blocks, stream);
+        if (nc == 1) return launch_one<T, V, 1, PAIRS, BWD, BPS, BWD ? kAny : kTail, HU>(p, *blocks, stream);
+        return launch_one<T, V, 2, PAIRS, BWD, 1, kAny, 1>(p, *blocks, stream);
     }
-    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, BPS, false, 1>(p, *blocks, stream);
-    return launch_one<T, 1, 8, PAIRS, BWD, 1, false, 1>(p, *blocks, stream);
+    if (nc <= 2) return launch_one<T, 1, 2, PAIRS, BWD, BPS, kAny, 1>(p, *blocks, stream);
+    return launch_one<T, 1, 8, PAIRS, BWD, 1, kAny, 1>(p, *blocks, stream);
 }
 
 template <bool BWD>
