@@ -302,26 +302,36 @@ __device__ __forceinline__ void mma_cta2_ta_scaled(uint32_t d, uint32_t a, uint6
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "n"(SHIFT) : "memory");
 }
 
+// One lane of a converged warp, the same one every time: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
+}
+
 // One CTA's own MMAs (cta_group::1), A in tensor memory: D = A*B (+ D), and
-// D = A*B + 2^-SHIFT D.
+// D = A*B + 2^-SHIFT D.  Called by a whole warp, issued by the lane whose
+// `leader` is set: in code that only that lane runs, the operands, which the
+// instruction wants in uniform registers, are moved there one by one.
 __device__ __forceinline__ void mma_cta1_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+                                            uint32_t accumulate, uint32_t leader) {
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 template <int SHIFT>
 __device__ __forceinline__ void mma_cta1_ta_scaled(uint32_t d, uint32_t a, uint64_t b,
-                                                   uint32_t idesc) {
+                                                   uint32_t idesc, uint32_t leader) {
     static_assert(SHIFT >= 1 && SHIFT <= 15, "scale-input-d takes 0..15");
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %4;\n}\n"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "n"(SHIFT) : "memory");
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, 1, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %4;\n}\n"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "n"(SHIFT), "r"(leader) : "memory");
 }
-// Arrive on this CTA's barrier once its MMAs issued so far have completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(bar) : "memory");
+// Arrive on this CTA's barrier once the leader's MMAs issued so far have completed.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t leader) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+                 " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+                 :: "r"(bar), "r"(leader) : "memory");
 }
 
 // Store 8 consecutive 32-bit columns of this warp's 32 TMEM lanes.

@@ -63,6 +63,7 @@ struct Cfg {
     // cycles of the tensor core anyway: one issuer, and half the split warps.
     static constexpr int issuers = BN >= 128 ? 1 : 2;
     static constexpr int split_warps = BN >= 128 ? 8 : 16;
+    static constexpr bool early = issuers == 1;          // (two stages of each ring for the one issuer)
     // tensor memory: partials, then W's pieces (96 columns per K block)
     static constexpr int partials = 2;
     static constexpr int a_stages = BN == 16 || BN == 64 ? 4 : 2;
@@ -71,9 +72,9 @@ struct Cfg {
     static_assert(a_base + a_stages * 3 * kPieceCols <= 512, "tensor memory overflow");
     // shared memory: FP32 buffers (as many as fit: the stream's bytes in
     // flight), stages of X's pieces, the gated hand-over
-    static constexpr int a_bufs = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 3 : 2;
+    static constexpr int a_bufs = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? (GATED ? 3 : 4) : BN == 128 ? 3 : 2;
     static constexpr int b_tile = BN * kTcBKBytes;
-    static constexpr int b_stages = BN <= 32 ? 4 : 2;
+    static constexpr int b_stages = BN <= 64 ? 4 : 2;
     static_assert(b_stages % issuers == 0, "an issuer's own stages");
     // (the gated hand-over in `passes` of BN / passes rows of X)
     static constexpr int acc_warps = BN == 16 ? 4 : BN == 160 ? 16 : 8;
@@ -262,20 +263,31 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                 mbar_wait(bfull0 + 8 * slot_of(i, NB), phase_of(i, NB), p.err, kDevErrTimeout);
         }
     } else if (warp < C::acc0) {
-        if (lane == 0 && warp - 2 < C::issuers) {
+        if (warp - 2 < C::issuers) {
             // ----------------------------------------------------- MMA issuers
+            const uint32_t leader = elect_one();
             // (not stacked: as many columns as there are rows of X, in 16s)
             const uint32_t idesc = make_idesc(1u, 128, C::stacked ? C::d_cols : (p.N + 15) / 16 * 16);
+            // what block g's MMAs wait for: its partial, X's pieces, W's pieces
+            auto drained = [&](uint32_t g) {
+                return mbar_wait(dfree0 + 8 * slot_of(g, C::partials), phase_of(g, C::partials) ^ 1, p.err, kDevErrTimeout);
+            };
+            auto x_ready = [&](uint32_t g) {
+                return mbar_wait(bfull0 + 8 * slot_of(g, C::b_stages), phase_of(g, C::b_stages), p.err, kDevErrTimeout);
+            };
+            auto w_ready = [&](uint32_t g) {
+                return mbar_wait(pready0 + 8 * slot_of(g, C::a_stages), phase_of(g, C::a_stages), p.err, kDevErrTimeout);
+            };
+            bool ok = true;
             for (uint32_t g = warp - 2; g < blocks; g += C::issuers) {
                 const uint32_t s = slot_of(g, C::b_stages), t = slot_of(g, C::a_stages);
                 const uint32_t b = slot_of(g, C::partials);
-                if (!mbar_wait(dfree0 + 8 * b, phase_of(g, C::partials) ^ 1, p.err, kDevErrTimeout) ||
-                    !mbar_wait(bfull0 + 8 * s, phase_of(g, C::b_stages), p.err, kDevErrTimeout) ||
-                    !mbar_wait(pready0 + 8 * t, phase_of(g, C::a_stages), p.err, kDevErrTimeout) ||
-                    *abort_flag) {
+                if (!C::early || g == 0) ok = drained(g) && x_ready(g) && w_ready(g);
+                ok = ok && !*abort_flag;
+                if (!__all_sync(0xffffffffu, ok)) {
                     // tensor memory is freed only behind the MMAs issued so far
                     *abort_flag = 1;
-                    tc_commit(drain0 + 8 * (warp - 2));
+                    tc_commit(drain0 + 8 * (warp - 2), leader);
                     mbar_wait(drain0 + 8 * (warp - 2), 0, p.err, kDevErrTimeout);
                     break;
                 }
@@ -290,10 +302,10 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (k == 0 && shift)
-                            mma_cta1_ta_scaled<8>(d, a + kPieceCols * i, desc, idesc);
+                            mma_cta1_ta_scaled<8>(d, a + kPieceCols * i, desc, idesc, leader);
                         else
                             mma_cta1_ta(d, a + kPieceCols * i + 8 * k, desc + 2 * k, idesc,
-                                        (k == 0 && first) ? 0u : 1u);
+                                        (k == 0 && first) ? 0u : 1u, leader);
                     }
                 };
                 if constexpr (C::stacked) {
@@ -308,13 +320,19 @@ gemm_few_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                     run(0, b2, false, true);              // band 2
                     run(1, b1, false, false);
                     run(2, b0, false, false);
+                    // the next block's waits, each behind MMAs that are in the queue
+                    // (none of them waits for this block's MMAs)
+                    const bool next = C::early && g + 1 < blocks;
+                    if (next) ok = ok && drained(g + 1);
                     run(0, b1, false, true);              // band 1
+                    if (next) ok = ok && x_ready(g + 1);
                     run(1, b0, false, false);
+                    if (next) ok = ok && w_ready(g + 1);
                     run(0, b0, false, true);              // band 0
                 }
-                tc_commit(pfree0 + 8 * t);
-                tc_commit(dfull0 + 8 * b);
-                tc_commit(bfree0 + 8 * s);
+                tc_commit(pfree0 + 8 * t, leader);
+                tc_commit(dfull0 + 8 * b, leader);
+                tc_commit(bfree0 + 8 * s, leader);
             }
         }
     } else if (warp >= C::split0) {
