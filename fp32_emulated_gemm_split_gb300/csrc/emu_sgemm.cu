@@ -236,15 +236,13 @@ bool make_c_map(CUtensorMap* map, float* C, int64_t M, int64_t N, int64_t ldc) {
 
 constexpr int kFlagsBytes = 64 << 10;
 
-emu_status_t plan_tail(TcGemmParams& p, int clusters, int fix2, int bm, int bn, DeviceState* d) {
-    const int tiles = p.tiles_m * p.tiles_n;
+// The workspace and flags of a tail of tail_tiles tiles (0: none).
+static emu_status_t share_tail(TcGemmParams& p, int tail_tiles, int tail_clusters, int bm, int bn, DeviceState* d) {
     p.tail_tiles = 0;
     p.tail_clusters = 0;
     p.part_ws = nullptr;
     p.flags = nullptr;
     p.epoch = 0;
-    int tail_tiles = 0, tail_clusters = 0;
-    sched_plan_tail(tiles, p.num_kb, clusters, fix2, &tail_tiles, &tail_clusters);
     if (tail_tiles == 0) return EMU_OK;
     if ((size_t)tail_clusters * 2 * 16 * sizeof(unsigned) > (size_t)kFlagsBytes) return EMU_OK;
     const size_t need = (size_t)tail_clusters * bm * bn * sizeof(float);
@@ -264,6 +262,12 @@ emu_status_t plan_tail(TcGemmParams& p, int clusters, int fix2, int bm, int bn, 
     p.flags = d->flags;
     p.epoch = ++d->epoch == 0 ? ++d->epoch : d->epoch;   // never 0 (the flags' initial value)
     return EMU_OK;
+}
+
+emu_status_t plan_tail(TcGemmParams& p, int clusters, int fix2, int bm, int bn, DeviceState* d) {
+    int tail_tiles = 0, tail_clusters = 0;
+    sched_plan_tail(p.tiles_m * p.tiles_n, p.num_kb, clusters, fix2, &tail_tiles, &tail_clusters);
+    return share_tail(p, tail_tiles, tail_clusters, bm, bn, d);
 }
 
 namespace {
@@ -385,10 +389,42 @@ bool few_rows_ok(int64_t M, const float* W, int64_t ldw) {
     return M <= kFewRows && W && ldw % 4 == 0 && (reinterpret_cast<uintptr_t>(W) & 15) == 0;
 }
 
-// What handing one part's sums over costs in half K blocks: about 2 us
-// against the 0.7 us in which a CTA streams a K block of FP32 weights (32 KB)
-// at its share of the HBM's rate.
-constexpr int kFewRowsHandover = 6;
+// How the tiles that do not fill a round of gemm_few's CTAs are shared (the
+// forms of sched_plan_tail).  Few CTAs that stream get more of the HBM each, so
+// a round costs what its bytes take at the HBM's rate, or its longest CTA at
+// the rate of one CTA (us per 32 KB K block with at most 16, 32, 64, 128, 160
+// rows: 0.64, 0.70, 0.88, 1.34, 1.60), whichever is more.  A tile in aligned
+// parts costs 3.2 us more than whole tiles (5 with more than 64 rows, whose
+// parts are larger), ranges that cross tiles 6 (9), and an owner reads four
+// parts at a time.  Measured, one row, us: 134 MB of weights in 64 tiles, 128
+// aligned parts 30.9, 152 ranges 34.0; in 128 tiles, whole 28, 152 ranges 34;
+// 120 MB in 114 tiles, whole 27.5, 152 ranges 31.3.
+static void plan_few_tail(int tiles, int num_kb, int resident, int bn, int* tail_tiles, int* tail_clusters) {
+    *tail_tiles = *tail_clusters = 0;
+    const int r = tiles % resident;
+    if (r == 0 || num_kb < 2) return;
+    const int64_t block_ns = bn <= 16 ? 640 : bn <= 32 ? 700 : bn <= 64 ? 880 : bn <= 128 ? 1340 : 1600;
+    const int64_t blocks = (int64_t)r * num_kb;
+    const double bytes_ns = blocks * 32768 / 6790.0;
+    auto cost = [&](int64_t ctas, double more) {
+        const double longest = double((blocks + ctas - 1) / ctas * block_ns);
+        const int64_t parts = (ctas + r - 1) / r;
+        return (longest > bytes_ns ? longest : bytes_ns) + more + (parts > 4 ? (parts - 4) * 250.0 : 0.0);
+    };
+    double best = cost(r, 0.0);
+    int64_t best_ctas = 0;
+    for (int64_t ctas = blocks / 2 < resident ? blocks / 2 : resident; ctas > r; --ctas) {
+        if (ctas % r == 0 && ctas / r > num_kb / 2) continue;
+        const double c = cost(ctas, ctas % r == 0 ? (bn <= 64 ? 3200.0 : 5000.0) : (bn <= 64 ? 6000.0 : 9000.0));
+        if (c < best) {
+            best = c;
+            best_ctas = ctas;
+        }
+    }
+    if (best_ctas == 0) return;
+    *tail_tiles = r;
+    *tail_clusters = (int)best_ctas;
+}
 
 emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t ldw2, int64_t M,
                            int64_t N, int64_t K, const void* xp, int64_t ldp, int64_t plane_rows,
@@ -407,7 +443,9 @@ emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t
     const int rows = W2 ? 64 : 128;              // of each weight per tile
     p.tiles_m = (int)((N + rows - 1) / rows);
     p.tiles_n = 1;
-    st = plan_tail(p, gemm_few_ctas(W2 != nullptr, bn, d->sms), kFewRowsHandover, 128, bn, d);
+    int tail_tiles = 0, tail_ctas = 0;
+    plan_few_tail(p.tiles_m, p.num_kb, gemm_few_ctas(W2 != nullptr, bn, d->sms), bn, &tail_tiles, &tail_ctas);
+    st = share_tail(p, tail_tiles, tail_ctas, 128, bn, d);
     if (st != EMU_OK) return st;
     return from_cuda(launch_gemm_few(bn, mapA, W2 ? &mapA2 : nullptr, mapB, p, d->sms, stream));
 }

@@ -34,7 +34,7 @@
 // ended; only X's pieces and the output wait for it.  (X's rows split in this
 // kernel too, by a warp per pipeline, would save that launch, but beside the
 // busy split warps such a warp took twice the time of the stream: 24 x 4096 x
-// (2 x 8192) 146 us against 61.)
+// (2 x 8192) 146 us against 61 then.)
 #include <mutex>
 
 #include "emu_device.cuh"
@@ -60,10 +60,15 @@ struct Cfg {
     // beside the busy split warps, the stream 1400); the rings that they wait on
     // have even counts, so each has stages of its own and meets every barrier's
     // phases in order.  At BN = 128 and 160 the nine products take 2300 or 2900
-    // cycles of the tensor core anyway: one issuer, and half the split warps.
+    // cycles of the tensor core anyway: one issuer, which waits for the next
+    // block while this one's last MMAs are in the queue (131 rows x 4096 x 6144:
+    // 60 us, 68 with the waits between the blocks, 62 with two issuers), and half
+    // the split warps.  The issuers' code is run by whole warps: by one lane of
+    // it, an MMA cost 70 to 80 cycles to issue, the operands' moves to uniform
+    // registers among the split warps' work (24 x 4096 x (2 x 8192): 61 -> 56 us).
     static constexpr int issuers = BN >= 128 ? 1 : 2;
     static constexpr int split_warps = BN >= 128 ? 8 : 16;
-    static constexpr bool early = issuers == 1;          // (two stages of each ring for the one issuer)
+    static constexpr bool early = issuers == 1;          // (needs two stages of each ring per issuer)
     // tensor memory: partials, then W's pieces (96 columns per K block)
     static constexpr int partials = 2;
     static constexpr int a_stages = BN == 16 || BN == 64 ? 4 : 2;
