@@ -91,6 +91,8 @@ __device__ __forceinline__ void store_chunk16(const float (&v)[16], const CUtens
                                               bool tma, float* out, int64_t ld, int M, int N,
                                               int row0, int gc0, int lane, uint32_t stage) {
     if (!tma) {
+        // (another output's bulk store may still read the buffer)
+        if (lane == 0) bulk_wait_read_n<0>();
         store_unaligned16(v, 0.0f, out, ld, M, N, row0, gc0, lane, stage);
         return;
     }
