@@ -115,12 +115,23 @@ emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t
                            int64_t N, int64_t K, const void* xp, int64_t ldp, int64_t plane_rows,
                            TcGemmParams p, DeviceState* d, cudaStream_t stream);
 
-// The last M % 256 rows of M > 256, where they are few enough that streaming
-// the FP32 weights for them costs less than one more row of 256-row tiles,
-// mostly empty (0: run all rows in tiles).  Per F K weights (two of F x K): a
-// row of tiles takes 3.8e-6 us, the stream 1.3e-6 us up to 32 rows, 2.4e-6 up
-// to 64 and as much as the tiles at 128, and about 6 us to start (measured at
-// 2048 x 8192: 65 us, 28, 46, 65).
-inline int64_t ragged_rows(int64_t M) { return M > 256 && M % 256 <= 64 ? M % 256 : 0; }
+// The last M % 256 rows of M > 256, where streaming the FP32 weights (N rows in
+// all, of K) for them costs less than one more row of 256-row tiles, mostly
+// empty (0: run all rows in tiles).  Per 128 x 64 block of the weights a row of
+// tiles takes 15.8 ns (a pair's 36 MMAs for two of them, shared by 76 pairs), the
+// stream 4.8 ns up to 32 rows, 5.8 up to 64, 8.8 up to 128 and 10.5 up to 160
+// (gemm_few's rate on 152 CTAs).  Start, end and uneven rounds take 10 to 20 us
+// of that gain.  Measured, us, in tiles alone and with the last rows streamed:
+// gated 777 x 2048 x (2 x 5504) 208 / 200, 356 x 4096 x (2 x 8192) 293 / 251, 612 x
+// 2048 x (2 x 5504) 162 / 173, 300 x 1024 x (2 x 1024) 32.5 / 47; adapters 1040 x
+// 2048 x 6144 119.5 / 118, 3117 x 1216 x 1152 94.5 / 114.
+inline int64_t ragged_rows(int64_t M, int64_t N, int64_t K) {
+    const int64_t rows = M % 256;
+    if (M <= 256 || rows == 0 || rows > kFewRows) return 0;
+    const double stream_ns = rows <= 32 ? 4.8 : rows <= 64 ? 5.8 : rows <= 128 ? 8.8 : 10.5;
+    const double gain_ns = rows <= 32 ? 10000.0 : rows <= 64 ? 15000.0 : 20000.0;
+    const double blocks = double((N + 127) / 128) * double((K + 63) / 64);
+    return blocks * (15.8 - stream_ns) > gain_ns ? rows : 0;
+}
 
 }  // namespace emu

@@ -126,7 +126,7 @@ emu_status_t gated_forward(int act, int64_t M, int64_t F, int64_t K, const float
     // rows that stream the FP32 weights: all of them, or what whole tiles leave
     const int64_t few = !few_rows_ok(1, Wg, ldwg) || !few_rows_ok(1, Wu, ldwu) ? 0
                         : M <= kFewRows                                        ? M
-                                                                               : ragged_rows(M);
+                                                                               : ragged_rows(M, 2 * F, K);
     const int64_t rows = M - few;
     TcGemmParams p = {};
     p.act = act;

@@ -612,7 +612,7 @@ extern "C" emu_status_t emu_lora(int64_t M, int64_t N, int64_t K, const float* X
     }
     if (e != cudaSuccess || K == 0) return from_cuda(e);
     // rows that stream the FP32 weight: all of them, or what whole tiles leave
-    const int64_t stream_rows = !few_rows_ok(1, W, ldw) ? 0 : M <= kFewRows ? M : ragged_rows(M);
+    const int64_t stream_rows = !few_rows_ok(1, W, ldw) ? 0 : M <= kFewRows ? M : ragged_rows(M, N, K);
     const int64_t rows = M - stream_rows;
     if (stream_rows > 0) {
         TcGemmParams q = {};
