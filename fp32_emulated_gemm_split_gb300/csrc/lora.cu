@@ -503,15 +503,15 @@ cudaError_t launch_down(const LoraParams& p, cudaStream_t stream) {
     return go(lora_down_tiles<V, 4>, tile_smem(4));
 }
 
-// Slices of K: enough for four blocks per SM (of the dots, which are bound by
-// latency; of the tiles, two of which run at a time, so that an uneven last
-// round costs little), at least 256 values each, at most 16 (the up step reads
-// each).
+// Slices of K, at least 256 values each, at most 16 (the up step reads each):
+// for the dots enough for two blocks per SM (131 tokens, 40 adapters of rank 32,
+// the whole call, us: one 83, two 78, four 84), for the tiles four, two of which
+// run at a time, so that an uneven last round costs little.
 int64_t slices_of(int64_t M, int64_t K, int64_t R, int sms) {
     const int64_t blocks = M <= kSingleTokens ? M * ((R + 15) / 16)
                            : M <= kFewTokens  ? (M + kDotTok - 1) / kDotTok * ((R + 15) / 16)
                                               : M / kTileTok;
-    int64_t n = (4 * sms + blocks - 1) / blocks;
+    int64_t n = ((M <= kFewTokens ? 2 : 4) * sms + blocks - 1) / blocks;
     n = n > 16 ? 16 : n;
     const int64_t most = (K + 255) / 256;
     return n < most ? n : most;
