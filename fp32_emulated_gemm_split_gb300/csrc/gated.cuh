@@ -90,16 +90,16 @@ __host__ __device__ __forceinline__ void with_act(int act, F&& f) {
 __device__ __forceinline__ void store_chunk16(const float (&v)[16], const CUtensorMap& map,
                                               bool tma, float* out, int64_t ld, int M, int N,
                                               int row0, int gc0, int lane, uint32_t stage) {
+    // the buffer is free again (either way: the output before may have gone by a
+    // bulk store where this one does not)
+    if (lane == 0) bulk_wait_read_n<0>();
     if (!tma) {
-        // (another output's bulk store may still read the buffer)
-        if (lane == 0) bulk_wait_read_n<0>();
         store_unaligned16(v, 0.0f, out, ld, M, N, row0, gc0, lane, stage);
         return;
     }
     const int row = row0 + lane;
     const int n4 = N & ~3;
     {
-        if (lane == 0) bulk_wait_read_n<0>();            // the buffer is free again
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
