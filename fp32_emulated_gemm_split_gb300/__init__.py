@@ -108,18 +108,27 @@ def _stream_handle(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _ld(X) -> int:
+    """Leading dimension of a matrix whose rows are contiguous.  Rows that
+    overlap (an expanded tensor) have none: the kernels would read, or write,
+    past its storage."""
+    rows, cols = X.shape
+    if rows <= 1:
+        return max(cols, 1)
+    if X.stride(0) < cols:
+        raise ValueError(f"the matrix's rows overlap ({rows} x {cols}, row stride {X.stride(0)}): make it contiguous")
+    return max(X.stride(0), 1)
+
+
 def _stored(X, trans: bool):
     """(tensor whose rows are contiguous, trans flag, leading dimension)."""
     import torch
     if X.dtype != torch.float32 or X.dim() != 2:
         raise TypeError("expected a 2-D float32 tensor")
     if X.stride(1) == 1 or X.size(1) <= 1:
-        ld = X.stride(0) if X.size(0) > 1 else max(X.size(1), 1)
-        return X, bool(trans), max(ld, X.size(1), 1)
+        return X, bool(trans), _ld(X)
     if X.stride(0) == 1:
-        Xt = X.t()
-        ld = Xt.stride(0) if Xt.size(0) > 1 else max(Xt.size(1), 1)
-        return Xt, not trans, max(ld, Xt.size(1), 1)
+        return X.t(), not trans, _ld(X.t())
     raise ValueError("matrix needs unit stride along rows or columns")
 
 
@@ -148,9 +157,9 @@ def emu_sgemm(A, B, C=None, *, transA=False, transB=False, alpha=1.0, beta=0.0,
         C = torch.empty((M, N), dtype=torch.float32, device=A.device)
     if C.dim() != 2 or C.shape != (M, N) or C.dtype != torch.float32 or (C.stride(1) != 1 and N > 1):
         raise ValueError("C must be an M x N float32 tensor with unit row stride")
-    ldc = C.stride(0) if M > 1 else max(N, 1)
+    ldc = _ld(C)
     st = lib().emu_sgemm(int(tA), int(tB), M, N, K, float(alpha), As.data_ptr(), lda,
-                         Bs.data_ptr(), ldb, float(beta), C.data_ptr(), max(ldc, N, 1),
+                         Bs.data_ptr(), ldb, float(beta), C.data_ptr(), ldc,
                          _mode(mode), _stream_handle(stream))
     _check(st, "emu_sgemm")
     return C
@@ -171,9 +180,9 @@ def emu_sgemm_noalloc(A, B, C, *, transA=False, transB=False, alpha=1.0, beta=0.
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     if C.dim() != 2 or C.shape != (M, N) or (C.stride(1) != 1 and N > 1):
         raise ValueError("C must be an M x N float32 tensor with unit row stride")
-    ldc = C.stride(0) if M > 1 else max(N, 1)
+    ldc = _ld(C)
     st = lib().emu_sgemm_noalloc(int(tA), int(tB), M, N, K, float(alpha), As.data_ptr(), lda,
-                                 Bs.data_ptr(), ldb, float(beta), C.data_ptr(), max(ldc, N, 1),
+                                 Bs.data_ptr(), ldb, float(beta), C.data_ptr(), ldc,
                                  _mode(mode), _stream_handle(stream))
     _check(st, "emu_sgemm_noalloc")
     return C
@@ -226,9 +235,9 @@ def emu_sgemm_bsplit(A, Bp, C=None, *, transA=False, alpha=1.0, beta=0.0, mode="
         C = torch.empty((M, N), dtype=torch.float32, device=A.device)
     if C.dim() != 2 or C.shape != (M, N) or C.dtype != torch.float32 or (C.stride(1) != 1 and N > 1):
         raise ValueError("C must be an M x N float32 tensor with unit row stride")
-    ldc = C.stride(0) if M > 1 else max(N, 1)
+    ldc = _ld(C)
     st = lib().emu_sgemm_bsplit(int(tA), M, N, K, float(alpha), As.data_ptr(), lda,
-                                Bp.data_ptr(), ldp, float(beta), C.data_ptr(), max(ldc, N, 1),
+                                Bp.data_ptr(), ldp, float(beta), C.data_ptr(), ldc,
                                 _mode(mode), _stream_handle(stream))
     _check(st, "emu_sgemm_bsplit")
     return C
