@@ -53,6 +53,16 @@ class _WeightPieces:
         self._cache.clear()
 
 
+def as_rows(x, cols):
+    """x flattened to rows of `cols` values that the kernels can read: copied
+    where the values of a row are apart, or rows overlap (the gradient of a sum
+    over the rows comes expanded, with a row stride of 0)."""
+    x2 = x.reshape(-1, cols)
+    if x2.stride(-1) != 1 or (x2.size(0) > 1 and x2.stride(0) < cols):
+        x2 = x2.contiguous()
+    return x2
+
+
 def _product(a, weight, out, transB, beta, mode, pieces):
     """out = a op(W) + beta out, with W's pieces from the cache when the mode
     runs on the tensor cores."""
@@ -66,9 +76,7 @@ class _EmuLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, mode, pieces):
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.stride(-1) != 1:
-            x2 = x2.contiguous()
+        x2 = as_rows(x, x.shape[-1])
         out = torch.empty((x2.shape[0], weight.shape[0]), dtype=torch.float32, device=x.device)
         if x2.shape[0] > 0:
             if bias is not None:
@@ -86,9 +94,7 @@ class _EmuLinearFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_out):
         x2, weight = ctx.saved_tensors
-        g2 = grad_out.reshape(-1, weight.shape[0])
-        if g2.stride(-1) != 1:
-            g2 = g2.contiguous()
+        g2 = as_rows(grad_out, weight.shape[0])
         gx = gw = gb = None
         if ctx.needs_input_grad[0]:
             gx = torch.empty_like(x2)

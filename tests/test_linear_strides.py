@@ -1,0 +1,39 @@
+"""EmuLinear's inputs and gradients with strides that the GEMM cannot read as
+they are, on the CPU through stand-ins that read a matrix as the kernels do."""
+import pytest
+import torch
+
+import block_fakes
+
+
+@pytest.fixture
+def linear(monkeypatch):
+    block_fakes.put_in(monkeypatch)
+    from fp32_emulated_gemm_split_gb300.linear import EmuLinear
+    torch.manual_seed(0)
+    return EmuLinear(5, 7)
+
+
+def _same(linear, x, loss):
+    """The layer's output and gradients against torch's own, in float64."""
+    params = [linear.weight, linear.bias]
+    y = linear(x)
+    got = (y, *torch.autograd.grad(loss(y), [x, *params]))
+    x64, *p64 = (t.detach().double().requires_grad_() for t in (x, *params))
+    y64 = torch.nn.functional.linear(x64, *p64)
+    for a, b in zip(got, (y64, *torch.autograd.grad(loss(y64), [x64, *p64]))):
+        assert torch.allclose(a.double(), b, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("loss", [
+    lambda y: (y.sum(0) * torch.arange(7)).sum(), lambda y: (y.mean(0) ** 2).sum(),
+    lambda y: y.sum(), lambda y: (y.sum(1) * torch.arange(6)).sum(), lambda y: (y.t().contiguous() ** 2).sum()])
+def test_expanded_gradients(linear, loss):
+    _same(linear, torch.randn(6, 5, requires_grad=True), loss)
+
+
+@pytest.mark.parametrize("x", [
+    torch.randn(5).expand(6, 5), torch.randn(6, 1).expand(6, 5), torch.randn(5, 6).t(),
+    torch.randn(20).unfold(0, 5, 3), torch.randn(6, 10)[:, ::2], torch.randn(6, 8)[:, 1:6]])
+def test_inputs_of_any_strides(linear, x):
+    _same(linear, x.detach().requires_grad_(), lambda y: (y ** 2).sum())
