@@ -21,15 +21,13 @@ import torch
 
 from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
                      emu_qk_norm_rope_bwd)
-from .linear import EmuLinear
+from .linear import EmuLinear, as_rows
 
 
 class _GatedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, up, act):
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.stride(-1) != 1:
-            x2 = x2.contiguous()
+        x2 = as_rows(x, x.shape[-1])
         w = emu_gated_pack(gate, up)
         h, g, u = emu_gated(x2, w, act=act, save=True)
         ctx.save_for_backward(x2, g, u)
@@ -39,9 +37,7 @@ class _GatedFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dh):
         x2, g, u = ctx.saved_tensors
-        dh2 = dh.reshape(-1, dh.shape[-1])
-        if dh2.stride(-1) != 1:
-            dh2 = dh2.contiguous()
+        dh2 = as_rows(dh, dh.shape[-1])
         need_w = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         dx, dg, du = emu_gated_bwd(dh2, x2, ctx.w, g, u, act=ctx.act, need_dx=ctx.needs_input_grad[0],
                                    need_dw=need_w)
@@ -79,9 +75,7 @@ class EmuGatedLinear(torch.nn.Module):
         if torch.is_grad_enabled() and (x.requires_grad or self.gate.requires_grad or self.up.requires_grad):
             return _GatedFn.apply(x, self.gate, self.up, self.activation)
         w = self._packed if self._packed is not None else emu_gated_pack(self.gate, self.up)
-        x2 = x.reshape(-1, x.shape[-1])
-        if x2.stride(-1) != 1:
-            x2 = x2.contiguous()
+        x2 = as_rows(x, x.shape[-1])
         return emu_gated(x2, w, act=self.activation).view(*x.shape[:-1], self.gate.shape[0])
 
 
