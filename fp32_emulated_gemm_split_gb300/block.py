@@ -48,8 +48,14 @@ class EmuGatedLinear(torch.nn.Module):
     """act(x Wg^T) * (x Wu^T) with FP32 parameters ``gate`` and ``up``
     (hidden x in).  A call that needs no gradients uses the weights as
     ``pack()`` laid them out, if it was called; otherwise each call lays them
-    out itself.  Weights changed since ``pack()`` are refused: call it again
-    (``train()`` drops what it made)."""
+    out itself.
+
+    ``pack()`` keeps the weights' values of its time: a copy (4 bytes a value,
+    for few rows) and the pieces (6 bytes).  A call after the parameters were
+    changed in place, replaced, or given other data is refused: call ``pack()``
+    again (``train()`` drops what it made; a copy of the module has none).  What
+    is written in place through ``parameter.data`` leaves no trace that could
+    be looked at: it takes effect with the next ``pack()``."""
 
     def __init__(self, in_features, hidden_features, activation="silu", device=None):
         super().__init__()
@@ -58,15 +64,25 @@ class EmuGatedLinear(torch.nn.Module):
         self.gate = torch.nn.Parameter(torch.randn(shape, device=device) * std)
         self.up = torch.nn.Parameter(torch.randn(shape, device=device) * std)
         self.activation = activation
-        self._packed = None
+        self._packed = self._packed_of = None
+
+    def _weights(self):
+        """What tells today's parameters from others."""
+        return [(w.data_ptr(), w._version, w.shape, w.stride(), w.device) for w in (self.gate, self.up)]
 
     def pack(self):
-        self._packed = emu_gated_pack(self.gate, self.up)
+        gate, up = self.gate.detach(), self.up.detach()
+        self._packed = emu_gated_pack(*(w.clone(memory_format=torch.contiguous_format) for w in (gate, up)))
+        # gate and up are held, so that no other tensor gets their addresses
+        self._packed_of = self._weights(), gate, up
         return self
+
+    def __getstate__(self):
+        return {**self.__dict__, "_packed": None, "_packed_of": None}
 
     def train(self, mode=True):
         if mode:
-            self._packed = None
+            self._packed = self._packed_of = None
         return super().train(mode)
 
     def forward(self, x):
@@ -74,7 +90,11 @@ class EmuGatedLinear(torch.nn.Module):
             raise TypeError("EmuGatedLinear computes FP32 in and out")
         if torch.is_grad_enabled() and (x.requires_grad or self.gate.requires_grad or self.up.requires_grad):
             return _GatedFn.apply(x, self.gate, self.up, self.activation)
-        w = self._packed if self._packed is not None else emu_gated_pack(self.gate, self.up)
+        w = self._packed
+        if w is None:
+            w = emu_gated_pack(self.gate, self.up)
+        elif self._packed_of[0] != self._weights():
+            raise ValueError("the weights were changed since pack(): call it again")
         x2 = as_rows(x, x.shape[-1])
         return emu_gated(x2, w, act=self.activation).view(*x.shape[:-1], self.gate.shape[0])
 

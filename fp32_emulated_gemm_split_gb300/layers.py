@@ -82,7 +82,10 @@ def _act(act):
 class GatedWeights:
     """The gate and up weights of a gated feed-forward with their packed
     pieces (``emu_gated_pack``).  The kernels read one or the other, so a
-    weight changed in place since then is refused: pack again."""
+    weight changed in place since then is refused: pack again.  A write that
+    leaves the tensor's version as it was (through ``.data``) cannot be seen,
+    and few rows would read the new values where many read the old: pack again
+    after it, or pack a copy."""
 
     __slots__ = ("Wg", "Wu", "pieces", "F", "K", "rows", "_args")
 
@@ -121,7 +124,8 @@ def emu_gated_bwd(dH, X, w: GatedWeights, G, U, act="silu", need_dx=True, need_d
 class LoraWeights:
     """The weight (N x K) and bias of a shared projection with the weight's
     pieces (``emu_lora_pack``).  The kernels read one or the other, so a weight
-    changed in place since then is refused: pack again."""
+    changed in place since then is refused: pack again (after a write through
+    ``.data`` as well, which cannot be seen)."""
 
     __slots__ = ("W", "bias", "pieces", "N", "K", "_args")
 

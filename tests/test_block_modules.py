@@ -40,3 +40,82 @@ def test_gated_takes_inputs_of_any_strides(block, x, grad):
         y = layer(x)
     want = _gated64(x.double(), layer.gate.double(), layer.up.double())
     assert torch.allclose(y.double(), want, rtol=1e-5, atol=1e-6)
+
+
+def _assign(layer, new):
+    layer.load_state_dict({"gate": new, "up": layer.up.detach().clone()}, assign=True)
+
+
+def _set_data(layer, new):
+    layer.gate.data = new
+
+
+def _replace(layer, new):
+    layer.gate = torch.nn.Parameter(new)
+
+
+def _in_place(layer, new):
+    with torch.no_grad():
+        layer.gate.copy_(new)
+
+
+def _load(layer, new):
+    layer.load_state_dict({"gate": new, "up": layer.up.detach().clone()})
+
+
+def _other_strides(layer, new):
+    layer.gate.data = new.t().contiguous().t()
+
+
+@pytest.mark.parametrize("change", [_assign, _set_data, _replace, _in_place, _load, _other_strides])
+def test_weights_changed_since_pack_are_refused(block, change):
+    layer = block.EmuGatedLinear(4, 6).eval().pack()
+    x = torch.randn(3, 4)
+    with torch.no_grad():
+        old = layer(x)
+        change(layer, torch.randn(6, 4))
+        with pytest.raises(ValueError, match="pack"):
+            layer(x)
+        y = layer.pack()(x)
+    assert not torch.allclose(y, old)
+    assert torch.allclose(y.double(), _gated64(x.double(), layer.gate.double(), layer.up.double()), atol=1e-6)
+
+
+def test_a_new_weight_at_the_old_address_is_refused(block):
+    """The pack holds the storage that it was made of, so no later tensor can have its address."""
+    layer = block.EmuGatedLinear(64, 64).eval().pack()
+    was = layer.gate.data_ptr()
+    for _ in range(8):
+        layer.gate = torch.nn.Parameter(torch.randn(64, 64))
+        assert layer.gate.data_ptr() != was
+    with torch.no_grad(), pytest.raises(ValueError, match="pack"):
+        layer(torch.randn(3, 64))
+
+
+def test_packed_values_are_one_set(block, monkeypatch):
+    """A write through .data bumps no version.  It reaches neither what the
+    tiles read (the pieces) nor what few rows read (the weights): both are the
+    pack's own, the values of its time."""
+    layer = block.EmuGatedLinear(4, 6).eval().pack()
+    x = torch.randn(3, 4)
+    with torch.no_grad():
+        old = layer(x)
+        layer.gate.data.mul_(2)
+        assert torch.equal(layer(x), old)
+        mine = {t.data_ptr() for t in layer._packed.tensors}
+        assert mine.isdisjoint({layer.gate.data_ptr(), layer.up.data_ptr()})
+        assert not torch.allclose(layer.pack()(x), old)
+
+
+def test_copies_of_a_packed_layer(block):
+    import copy
+    import pickle
+    layer = block.EmuGatedLinear(4, 6).eval().pack()
+    x = torch.randn(3, 4)
+    with torch.no_grad():
+        want = layer(x)
+        for other in (copy.deepcopy(layer), pickle.loads(pickle.dumps(layer))):
+            assert torch.equal(other(x), want) and other._packed is None
+            other.gate.mul_(2)
+            assert not torch.allclose(other(x), want)
+        assert torch.equal(layer(x), want)
