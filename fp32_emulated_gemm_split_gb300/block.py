@@ -9,6 +9,9 @@ as torch modules, and a small decoder block that runs them together.
                    rotation of the heads, attention, output projection; norm,
                    gated feed-forward, down projection
 
+The operators have first derivatives; a derivative of a gradient (a loss made of
+forces) raises.
+
 ``python -m fp32_emulated_gemm_split_gb300.block`` runs the block on a prompt,
 then token by token on the same sequence, and prints how far the two and a
 float64 evaluation are apart.
@@ -18,6 +21,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
                      emu_qk_norm_rope_bwd)
@@ -35,6 +39,7 @@ class _GatedFn(torch.autograd.Function):
         return h.view(*x.shape[:-1], gate.shape[0])
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         x2, g, u = ctx.saved_tensors
         dh2 = as_rows(dh, dh.shape[-1])
@@ -107,6 +112,7 @@ class _QkFn(torch.autograd.Function):
         return emu_qk_norm_rope(q, k, wq, wk, cos, sin, positions, **ctx.how)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         unit = [d if d.stride(-1) == 1 else d.contiguous() for d in (dq, dk)]
         grads = emu_qk_norm_rope_bwd(*unit, *ctx.saved_tensors, **ctx.how)

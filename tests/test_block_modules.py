@@ -119,3 +119,33 @@ def test_copies_of_a_packed_layer(block):
             other.gate.mul_(2)
             assert not torch.allclose(other(x), want)
         assert torch.equal(layer(x), want)
+
+
+def _qk_inputs():
+    q, k = torch.randn(5, 2, 8), torch.randn(5, 1, 8)
+    cos, sin = torch.randn(5, 4), torch.randn(5, 4)
+    return q, k, torch.rand(8), torch.rand(8), cos, sin, torch.arange(5, dtype=torch.int32)
+
+
+def _gated_case(block):
+    layer = block.EmuGatedLinear(4, 6)
+    return layer, torch.randn(5, 4)
+
+
+def _qk_case(block):
+    q, *rest = _qk_inputs()
+    return lambda x: block.qk_norm_rope(x, *rest)[0], q
+
+
+@pytest.mark.parametrize("case", [_gated_case, _qk_case])
+def test_a_second_derivative_is_refused(block, case):
+    """The backward passes run kernels that autograd does not see: a loss made
+    of a gradient raises, where it would be trained on a part of itself."""
+    f, x = case(block)
+    x.requires_grad_()
+    energy = f(x).sum()
+    force, = torch.autograd.grad(energy, x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (energy + force.square().sum()).backward()
+    # one derivative is as before, asked for with a graph or not
+    assert torch.equal(torch.autograd.grad(f(x).sum(), x)[0], force)
