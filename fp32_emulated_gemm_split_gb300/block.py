@@ -21,11 +21,10 @@ from __future__ import annotations
 import math
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
                      emu_qk_norm_rope_bwd)
-from .linear import EmuLinear, as_rows
+from .linear import EmuLinear, as_rows, underivable
 
 
 class _GatedFn(torch.autograd.Function):
@@ -34,19 +33,20 @@ class _GatedFn(torch.autograd.Function):
         x2 = as_rows(x, x.shape[-1])
         w = emu_gated_pack(gate, up)
         h, g, u = emu_gated(x2, w, act=act, save=True)
-        ctx.save_for_backward(x2, g, u)
-        ctx.w, ctx.act, ctx.shape = w, act, x.shape
+        ctx.save_for_backward(x, x2, g, u)
+        ctx.w, ctx.act, ctx.weights = w, act, (gate, up)
         return h.view(*x.shape[:-1], gate.shape[0])
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dh):
-        x2, g, u = ctx.saved_tensors
+        x, x2, g, u = ctx.saved_tensors
         dh2 = as_rows(dh, dh.shape[-1])
         need_w = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         dx, dg, du = emu_gated_bwd(dh2, x2, ctx.w, g, u, act=ctx.act, need_dx=ctx.needs_input_grad[0],
                                    need_dw=need_w)
-        return None if dx is None else dx.view(ctx.shape), dg, du, None
+        if dx is not None:
+            dx = dx.view(x.shape)
+        return (*underivable("EmuGatedLinear", (dx, dg, du), dh, x, *ctx.weights), None)
 
 
 class EmuGatedLinear(torch.nn.Module):
@@ -112,11 +112,11 @@ class _QkFn(torch.autograd.Function):
         return emu_qk_norm_rope(q, k, wq, wk, cos, sin, positions, **ctx.how)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dq, dk):
         unit = [d if d.stride(-1) == 1 else d.contiguous() for d in (dq, dk)]
-        grads = emu_qk_norm_rope_bwd(*unit, *ctx.saved_tensors, **ctx.how)
-        return (*grads, None, None, None, None, None)
+        saved = ctx.saved_tensors
+        grads = emu_qk_norm_rope_bwd(*unit, *saved, **ctx.how)
+        return (*underivable("qk_norm_rope", grads, dq, dk, *saved[:4]), None, None, None, None, None)
 
 
 def qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps=1e-6, interleaved=False):

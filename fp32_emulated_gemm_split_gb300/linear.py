@@ -63,6 +63,30 @@ def as_rows(x, cols):
     return x2
 
 
+class _Underivable(torch.autograd.Function):
+    """A gradient that kernels formed out of autograd's sight.  It depends on
+    `of`, so a derivative of it has terms that nothing here computes: asking for
+    one raises.  (once_differentiable sees the dependence on the incoming
+    gradient only: with a constant one, as of a sum, it lets the terms go.)"""
+
+    @staticmethod
+    def forward(ctx, what, grad, *of):
+        ctx.what = what
+        return grad.detach()
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.what} has no second derivative: a gradient through it was taken with "
+                           "create_graph=True and is differentiated again")
+
+
+def underivable(what, grads, *of):
+    """What a backward pass returns: `grads` (some None), which depend on `of`."""
+    if not torch.is_grad_enabled():                  # no create_graph
+        return tuple(grads)
+    return tuple(None if g is None else _Underivable.apply(what, g, *of) for g in grads)
+
+
 def _product(a, weight, out, transB, beta, mode, pieces):
     """out = a op(W) + beta out, with W's pieces from the cache when the mode
     runs on the tensor cores."""

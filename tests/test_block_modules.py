@@ -138,14 +138,27 @@ def _qk_case(block):
 
 
 @pytest.mark.parametrize("case", [_gated_case, _qk_case])
-def test_a_second_derivative_is_refused(block, case):
+@pytest.mark.parametrize("energy", [lambda y: y.sum(), lambda y: y.square().sum()])
+def test_a_second_derivative_is_refused(block, case, energy):
     """The backward passes run kernels that autograd does not see: a loss made
-    of a gradient raises, where it would be trained on a part of itself."""
+    of a gradient raises, where it would be trained on a part of itself (with a
+    constant incoming gradient, too: the gradient depends on x and the weights)."""
     f, x = case(block)
     x.requires_grad_()
-    energy = f(x).sum()
-    force, = torch.autograd.grad(energy, x, create_graph=True)
-    with pytest.raises(RuntimeError, match="once_differentiable"):
-        (energy + force.square().sum()).backward()
+    for wanted in (None, x):
+        e = energy(f(x))
+        force, = torch.autograd.grad(e, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            (e + force.square().sum()).backward(inputs=wanted)
     # one derivative is as before, asked for with a graph or not
-    assert torch.equal(torch.autograd.grad(f(x).sum(), x)[0], force)
+    assert torch.equal(torch.autograd.grad(energy(f(x)), x)[0], force)
+    energy(f(x)).backward(create_graph=True)
+    assert torch.equal(x.grad, force)
+
+
+def test_a_second_derivative_by_the_weights_is_refused(block):
+    layer, x = _gated_case(block)
+    x.requires_grad_()
+    force, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        torch.autograd.grad(force.square().sum(), [layer.gate])
