@@ -14,6 +14,9 @@ This module does that for both emulations:
   weight gradient  dW = dy^T x         emu_sgemm(dy, x, transA=1)
   bias gradient    db = sum of dy over the leading dimensions
 
+Of the input and weight gradients there is no derivative: a loss made of
+forces raises.
+
 Inputs of any leading shape (..., in_features) are flattened to 2-D.
 
 The weight is the same for every batch until an optimiser changes it, so
@@ -108,7 +111,7 @@ class _EmuLinearFn(torch.autograd.Function):
                 _product(x2, weight, out, True, 1.0, mode, pieces)
             else:
                 _product(x2, weight, out, True, 0.0, mode, pieces)
-        ctx.save_for_backward(x2, weight)
+        ctx.save_for_backward(x, x2, weight)
         ctx.mode = mode
         ctx.pieces = pieces
         ctx.has_bias = bias is not None
@@ -117,7 +120,7 @@ class _EmuLinearFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out):
-        x2, weight = ctx.saved_tensors
+        x, x2, weight = ctx.saved_tensors
         g2 = as_rows(grad_out, weight.shape[0])
         gx = gw = gb = None
         if ctx.needs_input_grad[0]:
@@ -135,6 +138,7 @@ class _EmuLinearFn(torch.autograd.Function):
                 gw.zero_()
         if ctx.has_bias and ctx.needs_input_grad[2]:
             gb = g2.sum(dim=0)
+        gx, gw = underivable("EmuLinear", (gx, gw), grad_out, x, weight)
         return gx, gw, gb, None, None
 
 

@@ -37,3 +37,23 @@ def test_expanded_gradients(linear, loss):
     torch.randn(20).unfold(0, 5, 3), torch.randn(6, 10)[:, ::2], torch.randn(6, 8)[:, 1:6]])
 def test_inputs_of_any_strides(linear, x):
     _same(linear, x.detach().requires_grad_(), lambda y: (y ** 2).sum())
+
+
+@pytest.mark.parametrize("energy", [lambda y: y.sum(), lambda y: y.square().sum()])
+def test_a_second_derivative_is_refused(linear, energy):
+    """A loss made of forces raises, where it would be trained on the energy alone."""
+    x = torch.randn(6, 5, requires_grad=True)
+    for wanted in (None, [x], [linear.weight]):
+        e = energy(linear(x))
+        force, = torch.autograd.grad(e, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            (e + force.square().sum()).backward(inputs=wanted)
+    assert torch.equal(torch.autograd.grad(energy(linear(x)), x)[0], force)
+
+
+def test_the_bias_gradient_can_be_differentiated(linear):
+    """It is a sum of the incoming gradient, by torch itself."""
+    x = torch.randn(6, 5)
+    g = torch.randn(6, 7, requires_grad=True)
+    db, = torch.autograd.grad(linear(x), linear.bias, g, create_graph=True)
+    assert torch.allclose(torch.autograd.grad(db.square().sum(), g)[0], (2 * db).expand(6, 7))
