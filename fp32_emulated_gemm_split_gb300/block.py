@@ -136,7 +136,8 @@ class EmuDecoderBlock(torch.nn.Module):
     the position of the first token, attends to the keys and values kept from
     earlier calls when ``keep`` is true, and adds the adapters'
     part to the first projection where ``adapters`` = (A, B, scale) and
-    ``index`` are given (no gradients then)."""
+    ``index`` are given.  That part is for serving: it has no backward pass, and
+    where a gradient would have to go through it the call raises."""
 
     def __init__(self, width, heads, kv_heads, hidden, max_positions=4096, eps=1e-6, device="cuda"):
         super().__init__()
@@ -172,6 +173,10 @@ class EmuDecoderBlock(torch.nn.Module):
             qkv = self.qkv(n)
         else:
             A, B, scale = adapters
+            if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                               for t in (n, self.qkv.weight, A, B, scale)):
+                raise RuntimeError("the adapters have no backward pass: call the block under torch.no_grad(), or "
+                                   "train without them")
             qkv = emu_lora(n, emu_lora_pack(self.qkv.weight), A, B, index, scale)
         q, k, v = qkv.view(T, -1, D).split((self.heads, self.kv_heads, self.kv_heads), 1)
         positions = torch.arange(start, start + T, device=x.device, dtype=torch.int32)

@@ -162,3 +162,33 @@ def test_a_second_derivative_by_the_weights_is_refused(block):
     force, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="no second derivative"):
         torch.autograd.grad(force.square().sum(), [layer.gate])
+
+
+def _decoder(block, **kw):
+    b = block.EmuDecoderBlock(8, 2, 1, 12, max_positions=16, device="cpu", **kw)
+    A, B = torch.randn(2, 3, 8), torch.randn(2, 16, 3)
+    return b, torch.randn(5, 8), (A, B, torch.rand(2)), torch.tensor([0, 1, -1, 1, 0], dtype=torch.int32)
+
+
+@pytest.mark.parametrize("who", ["all", "x", "norm1", "qkv.weight", "A", "B", "scale"])
+def test_adapters_where_gradients_are_wanted_are_refused(block, who):
+    """The adapters' product has no backward pass: a loss would flow past it
+    through the residual only."""
+    b, x, adapters, index = _decoder(block)
+    if who != "all":
+        b.requires_grad_(False)
+        named = dict(b.named_parameters(), x=x, **dict(zip(("A", "B", "scale"), adapters)))
+        named[who].requires_grad_()
+    with pytest.raises(RuntimeError, match="adapters.*no_grad"):
+        b(x, adapters=adapters, index=index)
+    with torch.no_grad():
+        b(x, adapters=adapters, index=index)
+
+
+def test_adapters_beside_a_part_that_is_trained(block):
+    """What comes behind the adapters can be trained: no gradient goes through them."""
+    b, x, adapters, index = _decoder(block)
+    b.requires_grad_(False)
+    b.gated.requires_grad_()
+    b(x, adapters=adapters, index=index).sum().backward()
+    assert b.gated.gate.grad is not None
