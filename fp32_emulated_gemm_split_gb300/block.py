@@ -134,10 +134,11 @@ def rotary_tables(positions, rot, base=10000.0, device=None):
 class EmuDecoderBlock(torch.nn.Module):
     """One decoder block, FP32.  ``forward(x, start)`` takes tokens x width and
     the position of the first token, attends to the keys and values kept from
-    earlier calls when ``keep`` is true, and adds the adapters'
-    part to the first projection where ``adapters`` = (A, B, scale) and
-    ``index`` are given.  That part is for serving: it has no backward pass, and
-    where a gradient would have to go through it the call raises."""
+    earlier calls, which have to stand before it, when ``keep`` is true (to its
+    own tokens otherwise), and adds the adapters' part to the first projection
+    where ``adapters`` = (A, B, scale) and ``index`` are given.  That part is for
+    serving: it has no backward pass, and where a gradient would have to go
+    through it the call raises."""
 
     def __init__(self, width, heads, kv_heads, hidden, max_positions=4096, eps=1e-6, device="cuda"):
         super().__init__()
@@ -157,17 +158,23 @@ class EmuDecoderBlock(torch.nn.Module):
     def _norm(self, x, w):
         return x * (x.square().mean(-1, keepdim=True) + self.eps).rsqrt() * w
 
-    def _attention(self, q, k, v, start):
-        """Plain causal attention; query t stands at position start + t."""
+    def _attention(self, q, k, v):
+        """Plain causal attention; the queries are the last of the keys' tokens."""
         group = self.heads // self.kv_heads
         k, v = k.repeat_interleave(group, 1), v.repeat_interleave(group, 1)
         s = torch.einsum("qhd,khd->hqk", q, k) / math.sqrt(self.dim)
-        seen = torch.arange(k.size(0), device=q.device) <= start + torch.arange(q.size(0), device=q.device)[:, None]
+        before = k.size(0) - q.size(0)
+        seen = torch.arange(k.size(0), device=q.device) <= before + torch.arange(q.size(0), device=q.device)[:, None]
         s = s.masked_fill(~seen, float("-inf"))
         return torch.einsum("hqk,khd->qhd", s.softmax(-1), v).reshape(q.size(0), -1)
 
     def forward(self, x, start=0, adapters=None, index=None, keep=False):
         T, D = x.size(0), self.dim
+        if start < 0 or start + T > self.cos.size(0):
+            raise ValueError(f"positions {start} to {start + T - 1} are not all in the tables' {self.cos.size(0)}")
+        if keep and start > 0 and (self.kept is None or self.kept[0].size(0) > start):
+            held = "none" if self.kept is None else f"{self.kept[0].size(0)} tokens"
+            raise ValueError(f"start is {start}: the tokens before it have to be kept, and no others ({held} kept)")
         n = self._norm(x, self.norm1)
         if adapters is None:
             qkv = self.qkv(n)
@@ -185,7 +192,7 @@ class EmuDecoderBlock(torch.nn.Module):
             if start > 0:
                 k, v = torch.cat((self.kept[0], k)), torch.cat((self.kept[1], v))
             self.kept = k, v
-        x = x + self.out(self._attention(q, k, v, start))
+        x = x + self.out(self._attention(q, k, v))
         return x + self.down(self.gated(self._norm(x, self.norm2)))
 
 

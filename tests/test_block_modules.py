@@ -192,3 +192,32 @@ def test_adapters_beside_a_part_that_is_trained(block):
     b.gated.requires_grad_()
     b(x, adapters=adapters, index=index).sum().backward()
     assert b.gated.gate.grad is not None
+
+
+def test_tokens_from_a_later_position_on_see_no_later_token(block):
+    """A call with a start that keeps nothing: causal among its own tokens."""
+    b, x, _, _ = _decoder(block)
+    with torch.no_grad():
+        whole = b(x, start=7)
+        for t in range(1, 5):
+            assert torch.allclose(b(x[:t], start=7), whole[:t], atol=1e-6)
+
+
+def test_start_has_to_follow_what_is_kept(block):
+    b, x, _, _ = _decoder(block)
+    with torch.no_grad():
+        with pytest.raises(ValueError, match="kept"):
+            b(x[3:], start=3, keep=True)
+        whole = b(x)
+        b(x[:3], keep=True)
+        with pytest.raises(ValueError, match="kept"):
+            b(x[3:], start=2, keep=True)
+        assert torch.allclose(b(x[3:], start=3, keep=True), whole[3:], atol=1e-6)
+        assert torch.equal(b(x, keep=True), whole)       # from the start again
+
+
+@pytest.mark.parametrize("start", [-1, 12, 16])
+def test_positions_past_the_tables_are_refused(block, start):
+    b, x, _, _ = _decoder(block)
+    with torch.no_grad(), pytest.raises(ValueError, match="positions"):
+        b(x, start=start)
