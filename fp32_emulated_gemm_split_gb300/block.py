@@ -23,7 +23,7 @@ import math
 import torch
 
 from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
-                     emu_qk_norm_rope_bwd)
+                     emu_qk_norm_rope_bwd, version_of)
 from .linear import EmuLinear, as_rows, underivable
 
 
@@ -73,7 +73,7 @@ class EmuGatedLinear(torch.nn.Module):
 
     def _weights(self):
         """What tells today's parameters from others."""
-        return [(w.data_ptr(), w._version, w.shape, w.stride(), w.device) for w in (self.gate, self.up)]
+        return [(w.data_ptr(), version_of(w), w.shape, w.stride(), w.device) for w in (self.gate, self.up)]
 
     def pack(self):
         gate, up = self.gate.detach(), self.up.detach()

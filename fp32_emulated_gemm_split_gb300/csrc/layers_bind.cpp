@@ -148,6 +148,10 @@ PyObject* tuple(PyObject* const (&items)[N]) {
     return r;
 }
 
+// The version that in-place changes of a tensor raise (-1: an inference tensor,
+// which has none).
+int64_t version_of(const at::Tensor& t) { return t.is_inference() ? -1 : (int64_t)t._version(); }
+
 // A function of exactly N positional arguments.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -178,8 +182,7 @@ struct Gated {
         Wg = tensor(PyTuple_GET_ITEM(o, 0), "Wg");
         Wu = tensor(PyTuple_GET_ITEM(o, 1), "Wu");
         pieces = tensor(PyTuple_GET_ITEM(o, 2), "pieces");
-        if ((int64_t)Wg->_version() != integer(PyTuple_GET_ITEM(o, 3)) ||
-            (int64_t)Wu->_version() != integer(PyTuple_GET_ITEM(o, 4)))
+        if (version_of(*Wg) != integer(PyTuple_GET_ITEM(o, 3)) || version_of(*Wu) != integer(PyTuple_GET_ITEM(o, 4)))
             value_error("a weight was changed in place since emu_gated_pack: pack again");
         ldg = rows_of(*Wg, "Wg");
         F = Wg->size(0);
@@ -280,7 +283,7 @@ PyObject* lora(PyObject* const* a) {   // X, (W, bias, pieces, version of W), A,
     if (!PyTuple_Check(a[1]) || PyTuple_GET_SIZE(a[1]) != 4) type_error("w must come from emu_lora_pack");
     T W = tensor(PyTuple_GET_ITEM(a[1], 0), "W"), bias = maybe(PyTuple_GET_ITEM(a[1], 1), "bias");
     T pieces = tensor(PyTuple_GET_ITEM(a[1], 2), "pieces");
-    if ((int64_t)W->_version() != integer(PyTuple_GET_ITEM(a[1], 3)))
+    if (version_of(*W) != integer(PyTuple_GET_ITEM(a[1], 3)))
         value_error("the weight was changed in place since emu_lora_pack: pack again");
     const int64_t ldw = rows_of(*W, "W"), N = W->size(0), K = W->size(1);
     const int64_t ldx = rows_of(*X, "X", -1, K), M = X->size(0);

@@ -77,6 +77,18 @@ def _act(act):
     return a
 
 
+def version_of(t):
+    """The version that in-place changes of t raise; -1 for an inference
+    tensor, which has none."""
+    return -1 if t.is_inference() else t._version
+
+
+def _kept(t):
+    """A weight as a pack keeps it: itself, or a copy where its changes could not be seen."""
+    t = t.detach()
+    return t.clone() if t.is_inference() else t
+
+
 # ----------------------------------------------------- gated feed-forward --
 
 class GatedWeights:
@@ -85,21 +97,22 @@ class GatedWeights:
     weight changed in place since then is refused: pack again.  A write that
     leaves the tensor's version as it was (through ``.data``) cannot be seen,
     and few rows would read the new values where many read the old: pack again
-    after it, or pack a copy."""
+    after it, or pack a copy.  Of inference tensors, which have no version, a
+    copy is kept."""
 
     __slots__ = ("Wg", "Wu", "pieces", "F", "K", "rows", "_args")
 
     def __init__(self, Wg, Wu, pieces):
         self.Wg, self.Wu, self.pieces, self.rows = Wg, Wu, pieces, pieces.size(1) // 2
         self.F, self.K = Wg.shape
-        self._args = Wg, Wu, pieces, Wg._version, Wu._version
+        self._args = Wg, Wu, pieces, version_of(Wg), version_of(Wu)
 
 
 def emu_gated_pack(Wg, Wu, *, stream=None) -> GatedWeights:
     """The weights Wg and Wu (F x K each) ready for ``emu_gated``."""
     if stream is not None:
         return _on(stream, emu_gated_pack, Wg, Wu)
-    Wg, Wu = Wg.detach(), Wu.detach()
+    Wg, Wu = _kept(Wg), _kept(Wu)
     return GatedWeights(Wg, Wu, _C().gated_pack(Wg, Wu))
 
 
@@ -125,21 +138,22 @@ class LoraWeights:
     """The weight (N x K) and bias of a shared projection with the weight's
     pieces (``emu_lora_pack``).  The kernels read one or the other, so a weight
     changed in place since then is refused: pack again (after a write through
-    ``.data`` as well, which cannot be seen)."""
+    ``.data`` as well, which cannot be seen).  Of an inference tensor, which has
+    no version, a copy is kept."""
 
     __slots__ = ("W", "bias", "pieces", "N", "K", "_args")
 
     def __init__(self, W, bias, pieces):
         self.W, self.bias, self.pieces = W, bias, pieces
         self.N, self.K = W.shape
-        self._args = W, bias, pieces, W._version
+        self._args = W, bias, pieces, version_of(W)
 
 
 def emu_lora_pack(W, bias=None, *, stream=None) -> LoraWeights:
     """The projection's weight W (N x K) and bias ready for ``emu_lora``."""
     if stream is not None:
         return _on(stream, emu_lora_pack, W, bias)
-    W = W.detach()
+    W = _kept(W)
     bias = None if bias is None else bias.detach()
     _C().lora_weights(W, bias)
     return LoraWeights(W, bias, emu_split_b(W, transB=True))

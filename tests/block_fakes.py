@@ -5,6 +5,7 @@ import torch
 
 import fp32_emulated_gemm_split_gb300 as emu
 import layer_ref as ref
+from fp32_emulated_gemm_split_gb300.layers import version_of
 
 
 def _matrix(X, rows=None, cols=None):
@@ -48,10 +49,10 @@ class Packed:
     def __init__(self, *tensors):
         self.tensors = [t.detach() for t in tensors]
         self.values = [_matrix(t).clone() for t in tensors]
-        self.versions = [t._version for t in self.tensors]
+        self.versions = [version_of(t) for t in self.tensors]
 
     def checked(self):
-        if self.versions != [t._version for t in self.tensors]:
+        if self.versions != [version_of(t) for t in self.tensors]:
             raise ValueError("changed in place: pack again")
         return self.values
 

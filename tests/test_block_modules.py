@@ -221,3 +221,16 @@ def test_positions_past_the_tables_are_refused(block, start):
     b, x, _, _ = _decoder(block)
     with torch.no_grad(), pytest.raises(ValueError, match="positions"):
         b(x, start=start)
+
+
+def test_gated_weights_made_in_inference_mode(block):
+    """Such tensors have no version counter."""
+    with torch.inference_mode():
+        layer = block.EmuGatedLinear(4, 6).eval()
+        x = torch.randn(3, 4)
+        want = _gated64(x.double(), layer.gate.double(), layer.up.double())
+        assert torch.allclose(layer(x).double(), want, atol=1e-6)
+        assert torch.allclose(layer.pack()(x).double(), want, atol=1e-6)
+        layer.gate = torch.nn.Parameter(torch.randn(6, 4), requires_grad=False)
+        with pytest.raises(ValueError, match="pack"):
+            layer(x)
