@@ -26,7 +26,8 @@ input-gradient products run emu_sgemm_bsplit on those pieces: no split of
 the weight per call, and in BF16x9 with 4096 rows or more and at most 256
 output columns a single kernel launch per product.  The pieces are dropped
 and made again whenever the weight's storage or version changes (an
-in-place update bumps the version).
+in-place update bumps the version; an inference tensor has none, and is split
+in every call).
 """
 from __future__ import annotations
 
@@ -44,6 +45,8 @@ class _WeightPieces:
         self._cache = {}
 
     def get(self, weight, transB, mode):
+        if weight.is_inference():                    # no version would tell of a change
+            return emu_split_b(weight, transB=transB, mode=mode)
         key = (bool(transB), mode)
         stamp = (weight.data_ptr(), weight._version, tuple(weight.shape), weight.device)
         hit = self._cache.get(key)

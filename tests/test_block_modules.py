@@ -234,3 +234,14 @@ def test_gated_weights_made_in_inference_mode(block):
         layer.gate = torch.nn.Parameter(torch.randn(6, 4), requires_grad=False)
         with pytest.raises(ValueError, match="pack"):
             layer(x)
+
+
+def test_decoder_made_in_inference_mode(block):
+    with torch.inference_mode():
+        b, x, adapters, index = _decoder(block)
+        whole = b.eval()(x, adapters=adapters, index=index)
+        b.gated.pack()
+        parts = [b(x[:3], adapters=adapters, index=index[:3], keep=True)]
+        for t in (3, 4):
+            parts.append(b(x[t:t + 1], start=t, adapters=adapters, index=index[t:t + 1], keep=True))
+        assert torch.allclose(torch.cat(parts), whole, atol=1e-6)

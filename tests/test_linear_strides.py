@@ -57,3 +57,17 @@ def test_the_bias_gradient_can_be_differentiated(linear):
     g = torch.randn(6, 7, requires_grad=True)
     db, = torch.autograd.grad(linear(x), linear.bias, g, create_graph=True)
     assert torch.allclose(torch.autograd.grad(db.square().sum(), g)[0], (2 * db).expand(6, 7))
+
+
+def test_a_weight_made_in_inference_mode(linear):
+    """It has no version that would tell of a change: its pieces are made for each call."""
+    from fp32_emulated_gemm_split_gb300.linear import EmuLinear
+    with torch.inference_mode():
+        layer, x = EmuLinear(5, 7), torch.randn(6, 5)
+        for _ in range(2):
+            want = torch.nn.functional.linear(x, layer.weight, layer.bias)
+            assert torch.allclose(layer(x), want, atol=1e-6)
+            layer.weight.mul_(2)
+    with torch.no_grad():
+        want = torch.nn.functional.linear(x, layer.weight, layer.bias)
+        assert torch.allclose(layer(x), want, atol=1e-6)
