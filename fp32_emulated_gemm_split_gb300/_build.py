@@ -4,7 +4,8 @@ Each .cu file under csrc/ is compiled by nvcc in parallel and the objects are
 linked into ``csrc/_build/libemusgemm.<machine>.so``.  The CUDA runtime is
 linked statically; the driver's tensor-map encoder is looked up at run time,
 so the library has no link-time dependency on libcuda.  The Python side of
-emu_layers.h, a CPython extension, is compiled beside it by the host compiler.
+emu_layers.h, a CPython extension, is compiled beside it by the host compiler
+where torch is installed.
 """
 from __future__ import annotations
 
@@ -26,9 +27,26 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["emu_sgemm.cu", "split.cu", "gemm_kblock.cu", "gemm_simt.cu", "noalloc.cu", "chooser.cu",
            "gated.cu", "gemm_few.cu", "lora.cu", "qk_norm.cu"]
 HEADERS = ["emu_device.cuh", "emu_host.h", "emu_internal.h", "gated.cuh", "schedule.h"]
+
+
+def _torch_version():
+    """None where there is no torch: the C library needs none."""
+    try:
+        return metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        pass
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__
+
+
 # the Python side of emu_layers.h: a CPython extension against torch's headers
+# (None where torch is missing)
 BIND_SOURCE = "layers_bind.cpp"
-BIND_PATH = os.path.join(BUILD_DIR, f"emu_layers_bind.{platform.machine()}.{metadata.version('torch')}.so")
+TORCH = _torch_version()
+BIND_PATH = TORCH and os.path.join(BUILD_DIR, f"emu_layers_bind.{platform.machine()}.{TORCH}.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
@@ -81,8 +99,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         return r
 
     cuda_jobs = len(jobs)
-    bind_tmp = BIND_PATH + f".tmp{os.getpid()}"
-    bind_stale = force or _stale(BIND_PATH, [os.path.join(CSRC, BIND_SOURCE), *headers[-2:], __file__])
+    bind_tmp = f"{BIND_PATH}.tmp{os.getpid()}"
+    bind_stale = BIND_PATH is not None and (
+        force or _stale(BIND_PATH, [os.path.join(CSRC, BIND_SOURCE), *headers[-2:], __file__]))
     if bind_stale:
         jobs.append(_bind_command(bind_tmp))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
