@@ -534,9 +534,11 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
                     if constexpr (BWD) {
                         const float m = sd[u] * inv_d * r * r;
                         const uint64_t nm = pk(-m, -m);
+                        // (a head past the end has no norm where eps is 0: 0 times infinity)
+                        const bool counts = live(u);
 #pragma unroll
                         for (int e = 0; e < E; ++e) {            // r (dn w - x m)
-                            dw[e] = fma_f32x2(dn[u][e], mul_f32x2(x[u][e], rr), dw[e]);
+                            if (counts) dw[e] = fma_f32x2(dn[u][e], mul_f32x2(x[u][e], rr), dw[e]);
                             x[u][e] = mul_f32x2(rr, fma_f32x2(x[u][e], nm, mul_f32x2(dn[u][e], w[e])));
                         }
                     } else {
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32, BPS) qk_norm_kernel(const QkParam
         }
         if constexpr (R::used) asm volatile("cp.async.wait_group 0;" ::: "memory");
         if constexpr (BWD) {
-            // over the warp's heads (lanes without a head read zeros and added zeros)
+            // over the warp's heads (lanes without a head added nothing)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float lo = lo_of(dw[e]), hi = hi_of(dw[e]);
