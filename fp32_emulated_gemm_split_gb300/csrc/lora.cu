@@ -10,8 +10,11 @@
 // another the adapters among them: an adapter's rows come from L2 again for
 // every four tokens, and no grouping has to run first.  Beyond that one block
 // groups the tokens by adapter (lora_group) into tiles of up to 64, and the
-// steps' blocks take a tile each.  Every output element is one fixed sum, so
-// neither the order of the tokens in the batch nor that of a tile changes it.
+// steps' blocks take a tile each.  Every element of the adapter's term is one
+// fixed sum, so neither the order of the tokens in the batch nor that of a tile
+// changes it.  The projection's last rounding may depend on a token's place: whole
+// tiles, tiles that share K and the last rows of a ragged batch (ragged_rows) add
+// their partial sums in different orders.
 //
 // Both steps are FP32 on the CUDA cores, in packed pairs (fma.rn.f32x2: twice
 // the rate of single FMAs).  They are 2 R (K + N) of a token's 2 N K operations,
