@@ -322,6 +322,13 @@ emu_heads_t heads_of(const at::Tensor& x, const char* name, at::IntArrayRef shap
     if (st[2] != 1 && shape[2] > 1) value_error(std::string(name) + " needs unit stride along the values of a head");
     return {x.data_ptr(), shape[1], st[0], st[1]};
 }
+// The same of an output: no two of its elements in one place.
+emu_heads_t output_heads(const at::Tensor& x, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+    const emu_heads_t h = heads_of(x, name, shape, type);
+    if ((h.token_stride == 0 && shape[0] > 1) || (h.head_stride == 0 && shape[1] > 1))
+        if (x.numel() > 0) value_error(std::string(name) + "'s elements share memory");
+    return h;
+}
 emu_heads_t dense_heads(const at::Tensor& x, int64_t heads, int64_t D) { return {x.data_ptr(), heads, heads * D, D}; }
 
 // What both directions take: q, k, wq, wk, cos, sin, positions, eps, interleaved.
@@ -373,12 +380,12 @@ PyObject* qk(PyObject* const* a) {                   // what Qk takes, q', k' (b
     const Qk x(a);
     T qo = maybe(a[9], "out[0]"), ko = maybe(a[10], "out[1]");
     if (!qo != !ko) type_error("out must be two tensors");
-    const int dev = device_of({x.q, x.k, x.wq, x.wk, x.cos, x.sin, x.positions, qo, ko});
     emu_heads_t h[4] = {x.hq, x.hk, {}, {}};
     if (qo) {
-        h[2] = heads_of(*qo, "out[0]", x.q->sizes(), x.type);
-        h[3] = heads_of(*ko, "out[1]", x.k->sizes(), x.type);
+        h[2] = output_heads(*qo, "out[0]", x.q->sizes(), x.type);
+        h[3] = output_heads(*ko, "out[1]", x.k->sizes(), x.type);
     }
+    const int dev = device_of({x.q, x.k, x.wq, x.wk, x.cos, x.sin, x.positions, qo, ko});
     at::Tensor q, k;
     emu_status_t st;
     {
