@@ -136,7 +136,7 @@ cudaError_t launch_gemm_few(int bn, const CUtensorMap& mapA, const CUtensorMap* 
                             const CUtensorMap& mapB, const TcGemmParams& p, int sms,
                             cudaStream_t stream);
 // CTAs of that kernel resident at once.
-int gemm_few_ctas(bool gated, int bn, int sms);
+int gemm_few_ctas(int sms);
 cudaError_t launch_gemm_simt(int transA, int transB, int64_t M, int64_t N, int64_t K, float alpha,
                              const float* A, int64_t lda, const float* B, int64_t ldb, float beta,
                              float* C, int64_t ldc, cudaStream_t stream);

@@ -444,7 +444,7 @@ emu_status_t gemm_few_rows(const float* W, int64_t ldw, const float* W2, int64_t
     p.tiles_m = (int)((N + rows - 1) / rows);
     p.tiles_n = 1;
     int tail_tiles = 0, tail_ctas = 0;
-    plan_few_tail(p.tiles_m, p.num_kb, gemm_few_ctas(W2 != nullptr, bn, d->sms), bn, &tail_tiles, &tail_ctas);
+    plan_few_tail(p.tiles_m, p.num_kb, gemm_few_ctas(d->sms), bn, &tail_tiles, &tail_ctas);
     st = share_tail(p, tail_tiles, tail_ctas, 128, bn, d);
     if (st != EMU_OK) return st;
     return from_cuda(launch_gemm_few(bn, mapA, W2 ? &mapA2 : nullptr, mapB, p, d->sms, stream));

@@ -567,14 +567,14 @@ cudaError_t launch_bn(int bn, const CUtensorMap& mapA, const Second<GATED>& seco
 
 // One CTA per SM: each takes nearly all of an SM's shared memory and all of
 // its tensor memory.
-int gemm_few_ctas(bool, int, int sms) { return sms; }
+int gemm_few_ctas(int sms) { return sms; }
 
 cudaError_t launch_gemm_few(int bn, const CUtensorMap& mapA, const CUtensorMap* mapA2,
                             const CUtensorMap& mapB, const TcGemmParams& p, int sms,
                             cudaStream_t stream) {
     if (p.tiles_m == 0 || p.num_kb == 0) return cudaSuccess;
     TcGemmParams q = p;
-    const int resident = gemm_few_ctas(mapA2 != nullptr, bn, sms);
+    const int resident = gemm_few_ctas(sms);
     const bool split = q.tail_tiles > 0 && q.tail_tiles <= q.tiles_m && q.part_ws && q.flags &&
                        q.tail_clusters >= 1 && q.tail_clusters <= resident &&
                        (q.tiles_m - q.tail_tiles) % resident == 0;
