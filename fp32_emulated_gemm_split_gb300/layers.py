@@ -5,7 +5,9 @@ rotation of query and key heads, each as the C entry point of its name.
 The functions check shapes, types, strides and devices, allocate the outputs
 that are not given, and enqueue the library's kernels on the current CUDA stream
 (or ``stream``, a ``torch.cuda.Stream``).  All tensors of a call are on the
-current device.  csrc/layers_bind.cpp does this in C++.
+current device; an output that is given may not overlap an input (q and k in
+place excepted).  Autograd does not see the calls: block.py has the modules with
+gradients.  csrc/layers_bind.cpp does the work in C++.
 """
 from __future__ import annotations
 
