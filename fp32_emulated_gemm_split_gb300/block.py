@@ -24,7 +24,7 @@ import torch
 
 from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
                      emu_qk_norm_rope_bwd, version_of)
-from .linear import EmuLinear, as_rows, underivable
+from .linear import EmuLinear, as_rows, readable, underivable
 
 
 class _GatedFn(torch.autograd.Function):
@@ -94,7 +94,7 @@ class EmuGatedLinear(torch.nn.Module):
         if x.dtype != torch.float32:
             raise TypeError("EmuGatedLinear computes FP32 in and out")
         if torch.is_grad_enabled() and (x.requires_grad or self.gate.requires_grad or self.up.requires_grad):
-            return _GatedFn.apply(x, self.gate, self.up, self.activation)
+            return _GatedFn.apply(readable(x), self.gate, self.up, self.activation)
         w = self._packed
         if w is None:
             w = emu_gated_pack(self.gate, self.up)

@@ -69,6 +69,12 @@ def as_rows(x, cols):
     return x2
 
 
+def readable(x):
+    """x, or where the kernels cannot read its rows as they lie a copy that
+    autograd knows of: the functions below save what they get."""
+    return x if x.is_contiguous() else as_rows(x, x.shape[-1]).view(x.shape)
+
+
 class _Underivable(torch.autograd.Function):
     """A gradient that kernels formed out of autograd's sight.  It depends on
     `of`, so a derivative of it has terms that nothing here computes: asking for
@@ -178,7 +184,7 @@ class EmuLinear(torch.nn.Module):
     def forward(self, x):
         if x.dtype != torch.float32:
             raise TypeError("EmuLinear computes FP32 in and out")
-        return _EmuLinearFn.apply(x, self.weight, self.bias, self.mode, self._pieces)
+        return _EmuLinearFn.apply(readable(x), self.weight, self.bias, self.mode, self._pieces)
 
     def extra_repr(self):
         return (f"in_features={self.in_features}, out_features={self.out_features}, "

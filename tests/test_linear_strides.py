@@ -71,3 +71,26 @@ def test_a_weight_made_in_inference_mode(linear):
     with torch.no_grad():
         want = torch.nn.functional.linear(x, layer.weight, layer.bias)
         assert torch.allclose(layer(x), want, atol=1e-6)
+
+
+@pytest.mark.parametrize("strided", [lambda: torch.randn(4, 6, 5).transpose(0, 1), lambda: torch.randn(5, 6).t(),
+                                     lambda: torch.randn(5).expand(6, 5).detach()])
+def test_a_copied_input_may_change_before_the_backward_pass(linear, monkeypatch, strided):
+    from fp32_emulated_gemm_split_gb300 import block
+    gated = block.EmuGatedLinear(5, 7)
+    for layer in (linear, gated):
+        x = strided()
+        want = [torch.autograd.grad(layer(x.contiguous()).square().sum(), p)[0] for p in layer.parameters()]
+        y = layer(x)
+        x.copy_(torch.zeros(())) if x.stride(0) else x[0].zero_()
+        for a, b in zip(torch.autograd.grad(y.square().sum(), list(layer.parameters())), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("strided", [lambda x: x.t().contiguous().t(), lambda x: x[:1].expand(6, 5),
+                                     lambda x: torch.cat((x, x), 1)[:, :5], lambda x: x])
+def test_a_second_derivative_is_refused_for_any_strides(linear, strided):
+    x = torch.randn(6, 5, requires_grad=True)
+    force, = torch.autograd.grad(linear(strided(x)).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        torch.autograd.grad(force.square().sum(), x)
