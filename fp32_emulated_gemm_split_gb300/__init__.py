@@ -388,7 +388,8 @@ def emu_version() -> int:
 # --------------------- the operators of a transformer block (emu_layers.h) --
 
 _LAYERS = ("emu_gated_pack", "emu_gated", "emu_gated_bwd", "emu_lora_pack", "emu_lora", "emu_qk_norm_rope",
-           "emu_qk_norm_rope_bwd", "GatedWeights", "LoraWeights")
+           "emu_qk_norm_rope_bwd", "GatedWeights", "LoraWeights",
+           "KvCache", "KvPlan", "emu_kv_cache", "emu_kv_tables", "emu_kv_store", "emu_kv_attention")
 
 
 def __getattr__(name):

@@ -1192,7 +1192,7 @@ emu_status_t emu_shutdown(void) {
     cudaGetDevice(&cur);
     for (int i = 0; i < kMaxDevices; ++i) {
         DeviceState& d = g_dev[i];
-        if (!d.ws && !d.stage && !d.s_in && !d.part && !d.flags) continue;
+        if (!d.ws && !d.stage && !d.s_in && !d.part && !d.flags && !d.kv_ws) continue;
         cudaSetDevice(i);
         if (d.ws) cudaFree(d.ws);
         if (d.stage) cudaFree(d.stage);
@@ -1203,6 +1203,8 @@ emu_status_t emu_shutdown(void) {
         d.part = nullptr;
         d.part_bytes = 0;
         d.flags = nullptr;
+        if (d.kv_ws) cudaFree(d.kv_ws);
+        d.kv_ws = nullptr;
         if (d.s_in) {
             cudaStreamDestroy(d.s_in);
             cudaStreamDestroy(d.s_out);

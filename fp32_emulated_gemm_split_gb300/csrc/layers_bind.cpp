@@ -31,6 +31,9 @@ struct {
     decltype(&emu_lora) lora;
     decltype(&emu_qk_norm_rope) qk;
     decltype(&emu_qk_norm_rope_bwd) qk_bwd;
+    decltype(&emu_kv_tables) kv_tables;
+    decltype(&emu_kv_store) kv_store;
+    decltype(&emu_kv_attention) kv_attention;
 } api;
 PyObject* check_status;
 
@@ -429,12 +432,147 @@ PyObject* qk_bwd(PyObject* const* a) {               // what Qk takes, dq', dk'
     return tuple({wrap(dq), wrap(dk), wrap_or_none(dwq), wrap_or_none(dwk)});
 }
 
+// ------------------------------- keys and values kept in 8 bits --
+
+// The tuple (k, v, k_scale, v_scale).
+struct Cache {
+    T k, v, ks, vs;
+    emu_kv_cache_t c;
+    explicit Cache(PyObject* o) {
+        if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4)
+            type_error("cache must be a KvCache, or a tuple (k, v, k_scale, v_scale)");
+        k = tensor(PyTuple_GET_ITEM(o, 0), "cache.k");
+        v = tensor(PyTuple_GET_ITEM(o, 1), "cache.v");
+        ks = tensor(PyTuple_GET_ITEM(o, 2), "cache.k_scale");
+        vs = tensor(PyTuple_GET_ITEM(o, 3), "cache.v_scale");
+        for (T t : {k, v})
+            if (t->scalar_type() != at::kFloat8_e4m3fn)
+                type_error(std::string("cache.k and cache.v must be float8_e4m3fn, got ") + show(t->scalar_type()));
+        const auto s = k->sizes();
+        if (s.size() != 4 || v->sizes() != s || !k->is_contiguous() || !v->is_contiguous())
+            value_error("cache.k and cache.v must be contiguous, pages x heads x page x D, got " + show(s) + " and " +
+                        show(v->sizes()));
+        for (T t : {ks, vs}) {
+            if (t->scalar_type() != at::kFloat) type_error("the cache's scales must be float32");
+            if (t->dim() != 2 || t->size(0) != s[0] || t->size(1) != s[1] || !t->is_contiguous())
+                value_error("the cache's scales must be contiguous, pages x heads = (" + std::to_string(s[0]) + ", " +
+                            std::to_string(s[1]) + "), got " + show(t->sizes()));
+        }
+        if (s[2] < 16 || s[2] > 256 || (s[2] & (s[2] - 1)))
+            value_error("a page must have 16, 32, 64, 128 or 256 rows, got " + std::to_string(s[2]));
+        if (s[3] < 16 || s[3] > 256 || s[3] % 16)
+            value_error("a head must have a multiple of 16 values, up to 256, got " + std::to_string(s[3]));
+        c = {k->data_ptr(), v->data_ptr(), f32(*ks), f32(*vs), s[0], s[1], s[2], s[3]};
+    }
+};
+
+int heads_dtype(const at::Tensor& x, const char* name) {
+    const at::ScalarType t = x.scalar_type();
+    const int d = t == at::kFloat ? EMU_F32 : t == at::kBFloat16 ? EMU_BF16 : t == at::kHalf ? EMU_F16 : -1;
+    if (d < 0) type_error(std::string(name) + " must be float32, bfloat16 or float16, got " + show(t));
+    if (x.dim() != 3) value_error(std::string(name) + " must be tokens x heads x D, got " + show(x.sizes()));
+    return d;
+}
+
+// The rows of pages of the batch's sequences.
+int32_t* table_of(T t, int64_t rows) {
+    if (t->scalar_type() != at::kInt || t->dim() != 2 || t->size(0) != rows || !t->is_contiguous())
+        value_error("table must be contiguous int32, " + std::to_string(rows) + " sequences x pages");
+    return static_cast<int32_t*>(t->data_ptr());
+}
+
+PyObject* kv_tables(PyObject* const* a) {            // kept, new, table, free, pages, page, tokens, taken
+    T kept = tensor(a[0], "kept"), fresh = tensor(a[1], "new"), table = tensor(a[2], "table");
+    T free_pages = tensor(a[3], "free"), taken = maybe(a[7], "taken");
+    const int64_t pages = integer(a[4]), page = integer(a[5]), rows = integer(a[6]);
+    const int64_t B = kept->dim() == 1 ? kept->size(0) : -1;
+    const int32_t *kp = indices(kept, "kept", B), *np = indices(fresh, "new", B);
+    int32_t* tp = table_of(table, B);
+    if (free_pages->dim() != 1) value_error("free must be a row of int32 page numbers");
+    const int32_t* fp = indices(free_pages, "free", free_pages->size(0));
+    const int32_t* gone = taken ? indices(taken, "taken", 1) : nullptr;
+    if (rows < 0 || rows >= (int64_t)1 << 25) value_error("tokens must be 0 to 2^25 - 1, got " + std::to_string(rows));
+    const int dev = device_of({kept, fresh, table, free_pages, taken});
+    // starts, lengths, taken, and from a 16-byte boundary slots and positions: one allocation
+    const int64_t head = (2 * B + 2 + 3) / 4 * 4, some = (rows + 3) / 4 * 4;
+    at::Tensor all, out[5];
+    emu_status_t st;
+    {
+        NoGil no;
+        all = empty({head + 2 * some}, at::kInt, dev);
+        out[0] = all.narrow(0, 0, B + 1);
+        out[1] = all.narrow(0, B + 1, B);
+        out[2] = all.narrow(0, head, rows);
+        out[3] = all.narrow(0, head + some, rows);
+        out[4] = all.narrow(0, 2 * B + 1, 1);
+        int32_t* p = static_cast<int32_t*>(all.data_ptr());
+        st = api.kv_tables(B, kp, np, pages, page, fp, free_pages->size(0), gone, tp, table->size(1), rows, p, p + B + 1,
+                           p + head, p + head + some, p + 2 * B + 1, stream_of(dev));
+    }
+    check(st, "emu_kv_tables");
+    return tuple({wrap(out[0]), wrap(out[1]), wrap(out[2]), wrap(out[3]), wrap(out[4])});
+}
+
+PyObject* kv_store(PyObject* const* a) {             // k, v, cache, slots
+    T k = tensor(a[0], "k"), v = tensor(a[1], "v"), slots = maybe(a[3], "slots");
+    const Cache c(a[2]);
+    const int dtype = heads_dtype(*k, "k");
+    const int64_t shape[3] = {k->size(0), c.c.heads, c.c.D};
+    const emu_heads_t hk = heads_of(*k, "k", shape, k->scalar_type()), hv = heads_of(*v, "v", shape, k->scalar_type());
+    const int32_t* sp = indices(slots, "slots", shape[0]);
+    const int dev = device_of({k, v, c.k, c.v, c.ks, c.vs, slots});
+    emu_status_t st;
+    {
+        NoGil no;
+        st = api.kv_store(dtype, shape[0], &hk, &hv, sp, &c.c, stream_of(dev));
+    }
+    check(st, "emu_kv_store");
+    return none();
+}
+
+PyObject* kv_attention(PyObject* const* a) {  // q, cache, table, starts, lengths, scale, window, max_new, out
+    T q = tensor(a[0], "q"), table = tensor(a[2], "table"), starts = maybe(a[3], "starts"),
+      lengths = tensor(a[4], "lengths"), out = maybe(a[8], "out");
+    const Cache c(a[1]);
+    const int dtype = heads_dtype(*q, "q");
+    const at::IntArrayRef shape = q->sizes();
+    if (shape[2] != c.c.D || shape[1] < 1 || shape[1] % std::max<int64_t>(c.c.heads, 1))
+        value_error("q must be tokens x a multiple of " + std::to_string(c.c.heads) + " heads x " +
+                    std::to_string(c.c.D) + ", got " + show(shape));
+    const emu_heads_t hq = heads_of(*q, "q", shape, q->scalar_type());
+    emu_heads_t ho = {};
+    if (out) ho = output_heads(*out, "out", shape, q->scalar_type());
+    const int64_t B = lengths->dim() == 1 ? lengths->size(0) : -1;
+    const int32_t *lp = indices(lengths, "lengths", B), *sp = indices(starts, "starts", B + 1);
+    const int32_t* tp = table_of(table, B);
+    const double scale = PyFloat_AsDouble(a[5]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
+    const int64_t window = integer(a[6]), max_new = integer(a[7]);
+    const int dev = device_of({q, c.k, c.v, c.ks, c.vs, table, starts, lengths, out});
+    at::Tensor y;
+    emu_status_t st;
+    {
+        NoGil no;
+        if (out) {
+            y = *out;
+        } else {
+            y = empty(shape, q->scalar_type(), dev);
+            ho = dense_heads(y, shape[1], shape[2]);
+        }
+        st = api.kv_attention(dtype, shape[0], &hq, &ho, &c.c, B, tp, table->size(1), sp, lp, (float)scale, window,
+                              max_new, stream_of(dev));
+    }
+    check(st, "emu_kv_attention");
+    return wrap(y);
+}
+
 // (function that raises for a status, the entry points' addresses in api's order)
 PyObject* bind(PyObject*, PyObject* args) {
-    static_assert(sizeof(api) == 7 * sizeof(void*), "one pointer each");
-    unsigned long long p[7];
+    static_assert(sizeof(api) == 10 * sizeof(void*), "one pointer each");
+    unsigned long long p[10];
     PyObject* f;
-    if (!PyArg_ParseTuple(args, "OKKKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6])) return nullptr;
+    if (!PyArg_ParseTuple(args, "OKKKKKKKKKK", &f, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5], &p[6], &p[7], &p[8], &p[9]))
+        return nullptr;
     auto set = [&](auto& to, int i) { to = reinterpret_cast<std::decay_t<decltype(to)>>((uintptr_t)p[i]); };
     set(api.gated_rows, 0);
     set(api.gated_pack, 1);
@@ -443,6 +581,9 @@ PyObject* bind(PyObject*, PyObject* args) {
     set(api.lora, 4);
     set(api.qk, 5);
     set(api.qk_bwd, 6);
+    set(api.kv_tables, 7);
+    set(api.kv_store, 8);
+    set(api.kv_attention, 9);
     Py_INCREF(f);
     Py_XDECREF(check_status);
     check_status = f;
@@ -464,6 +605,9 @@ PyMethodDef* methods() {
         {"lora", fast<lora, 7>(), METH_FASTCALL, nullptr},
         {"qk_norm_rope", fast<qk, 11>(), METH_FASTCALL, nullptr},
         {"qk_norm_rope_bwd", fast<qk_bwd, 11>(), METH_FASTCALL, nullptr},
+        {"kv_tables", fast<kv_tables, 8>(), METH_FASTCALL, nullptr},
+        {"kv_store", fast<kv_store, 4>(), METH_FASTCALL, nullptr},
+        {"kv_attention", fast<kv_attention, 9>(), METH_FASTCALL, nullptr},
         {nullptr, nullptr, 0, nullptr}};
     return m;
 }

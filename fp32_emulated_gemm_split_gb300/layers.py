@@ -1,6 +1,7 @@
 """Python binding of include/emu_layers.h: the gated feed-forward, the
-low-rank adapters of many requests beside a projection, and the norm and
-rotation of query and key heads, each as the C entry point of its name.
+low-rank adapters of many requests beside a projection, the norm and rotation
+of query and key heads, and the pages of keys and values kept in 8 bits with the
+attention over them, each as the C entry point of its name.
 
 The functions check shapes, types, strides and devices, allocate the outputs
 that are not given, and enqueue the library's kernels on the current CUDA stream
@@ -14,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -41,8 +43,13 @@ def _L():
         qk = [_int, _i64, _i64, _i64, _int, _f32, ctypes.c_char_p, _vp, _vp, _vp, _vp, _i64, _vp]
         L.emu_qk_norm_rope.argtypes = qk + [_vp]
         L.emu_qk_norm_rope_bwd.argtypes = qk + [_vp, _vp, _vp]
+        L.emu_kv_tables.argtypes = [_i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                    _vp, _vp]
+        L.emu_kv_store.argtypes = [_int, _i64, ctypes.c_char_p, ctypes.c_char_p, _vp, ctypes.c_char_p, _vp]
+        L.emu_kv_attention.argtypes = [_int, _i64, ctypes.c_char_p, ctypes.c_char_p, ctypes.c_char_p, _i64, _vp, _i64,
+                                       _vp, _vp, _f32, _i64, _i64, _vp]
         for f in (L.emu_gated_pack, L.emu_gated, L.emu_gated_bwd, L.emu_lora, L.emu_qk_norm_rope,
-                  L.emu_qk_norm_rope_bwd):
+                  L.emu_qk_norm_rope_bwd, L.emu_kv_tables, L.emu_kv_store, L.emu_kv_attention):
             f.restype = _int
         _ready = L
     return _ready
@@ -61,7 +68,7 @@ def _C():
         spec.loader.exec_module(module)
         module.bind(_check, *(ctypes.cast(f, _vp).value for f in (
             L.emu_gated_rows, L.emu_gated_pack, L.emu_gated, L.emu_gated_bwd, L.emu_lora, L.emu_qk_norm_rope,
-            L.emu_qk_norm_rope_bwd)))
+            L.emu_qk_norm_rope_bwd, L.emu_kv_tables, L.emu_kv_store, L.emu_kv_attention)))
         _bound = module
     return _bound
 
@@ -191,3 +198,72 @@ def emu_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, cos=None, sin=None, posit
     if stream is not None:
         return _on(stream, emu_qk_norm_rope_bwd, dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved)
     return _C().qk_norm_rope_bwd(q, k, wq, wk, cos, sin, positions, eps, interleaved, dq_out, dk_out)
+
+
+# ----------------------------------------- keys and values kept in 8 bits --
+
+class KvCache(NamedTuple):
+    """Pages of keys and values: e4m3 codes (pages x heads x page x D, contiguous)
+    and a scale for each page and head (pages x heads, float32); a value is code
+    times scale.  The functions below also take a plain tuple of the four."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+class KvPlan(NamedTuple):
+    """A step's places (``emu_kv_tables``), int32: sequence b's rows are starts[b]
+    to starts[b + 1] - 1 and it holds lengths[b] tokens with them; each row's slot
+    (-1 behind the last sequence) and position; how many free pages are given away."""
+
+    starts: torch.Tensor
+    lengths: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    taken: torch.Tensor
+
+
+def emu_kv_cache(pages, heads, D, page=64, device="cuda") -> KvCache:
+    """An empty cache of pages * page tokens: 2 * D + 8 / page bytes for each token
+    and key head.  page: 16, 32, 64, 128 or 256; D: a multiple of 16, up to 256."""
+    codes = [torch.zeros(pages, heads, page, D, device=device, dtype=torch.float8_e4m3fn) for _ in range(2)]
+    return KvCache(*codes, *(torch.zeros(pages, heads, device=device) for _ in range(2)))
+
+
+def emu_kv_tables(kept, new, table, free, pages, page, tokens, taken=None, *, stream=None) -> KvPlan:
+    """The places of a step in which sequence b, of kept[b] tokens, gets new[b]
+    more, in a cache of `pages` pages of `page` tokens.  The pages that the sequences
+    lack are written into `table` (sequences x pages, int32, in place), from
+    free[taken] on; `taken` (one int32 on the GPU, None for 0) is what the plan of
+    the step before gave.  `tokens`: the step's rows, new.sum() or more."""
+    if stream is not None:
+        return _on(stream, emu_kv_tables, kept, new, table, free, pages, page, tokens, taken)
+    return KvPlan(*_C().kv_tables(kept, new, table, free, pages, page, tokens, taken))
+
+
+def emu_kv_store(k, v, cache: KvCache, slots, *, stream=None) -> None:
+    """Keys and values (tokens x heads x D, any token and head strides; float32,
+    bfloat16 or float16) into their slots of the cache (-1: none), a page's
+    slots one after another.  A page's scale is a power of two that grows as it
+    has to; a run that writes a page's first row begins it anew."""
+    if stream is not None:
+        return _on(stream, emu_kv_store, k, v, cache, slots)
+    _C().kv_store(k, v, cache, slots)
+
+
+def emu_kv_attention(q, cache: KvCache, table, starts, lengths, scale=None, window=0, max_new=None, out=None, *,
+                     stream=None):
+    """Causal attention of the rows of q (tokens x heads x D, any token and head
+    strides), sequence b's from starts[b] to starts[b + 1], the last of its
+    lengths[b] tokens, over the cache.  scale: D ** -0.5 by default; window: how
+    many tokens a row sees at most, itself among them (0: all); max_new: rows
+    of a sequence at most, which lets a step of single tokens launch one kernel
+    only.  A row that sees nothing is zero, as are the rows behind the last
+    sequence.  out may be q."""
+    if stream is not None:
+        return _on(stream, emu_kv_attention, q, cache, table, starts, lengths, scale, window, max_new, out)
+    if scale is None:
+        scale = q.size(-1) ** -0.5
+    return _C().kv_attention(q, cache, table, starts, lengths, scale, window, max_new or 0, out)

@@ -7,6 +7,9 @@
  *                                    of many requests at once
  *   emu_qk_norm_rope, ..._bwd        norm of each query and key head with the
  *                                    position rotation, forward and backward
+ *   emu_kv_tables, emu_kv_store,     pages of keys and values kept in 8 bits:
+ *   emu_kv_attention                 which ones a batch's requests get, the
+ *                                    store into them and the attention over them
  *
  * The matrix products are emu_sgemm's BF16X9 (emu_sgemm.h): FP32 in and out,
  * at FP32 accuracy.  The conventions of emu_sgemm.h hold: row-major storage,
@@ -183,6 +186,99 @@ emu_status_t emu_qk_norm_rope_bwd(int dtype, int64_t T, int64_t D, int64_t rot, 
                                   const float* wk, const float* cos, const float* sin,
                                   int64_t table_rows, const int32_t* positions, float* dwq,
                                   float* dwk, emu_stream_t stream);
+
+/* --------------------------------------- keys and values kept in 8 bits --
+ *
+ * The keys and values of many sequences, in pages of `page` tokens.  Page p of
+ * head h holds e4m3 codes, row r's D values at k[((p heads + h) page + r) D], and
+ * one scale for them, k_scale[p heads + h] (v alike): a value is code times
+ * scale.  A row of `table` lists the pages of a sequence in the order of its
+ * tokens.  A slot is page number * page + row.
+ */
+typedef struct {
+    void *k, *v;                     /* pages x heads x page x D codes, 16-byte aligned */
+    float *k_scale, *v_scale;        /* pages x heads, positive */
+    int64_t pages, heads, page, D;   /* page: 16, 32, 64, 128 or 256; D: a multiple of 16, up to 256;
+                                        heads: up to 1024; pages * page < 2^31 */
+} emu_kv_cache_t;
+
+/*
+ * emu_kv_tables -- a step's places from the lengths of its sequences: sequence b
+ * holds kept[b] tokens and gets fresh[b] new ones.  The new tokens' rows follow
+ * each other, sequence after sequence, in the step's T rows.
+ *
+ *  free_pages    n_free page numbers that no sequence has.  The pages that sequence
+ *                b lacks (held = ceil(kept / page) <= j < ceil((kept + fresh) / page))
+ *                are taken from free_pages[*taken] on, in the order of sequences and
+ *                tokens, and written to table[b * width + j]; the row's other
+ *                entries stay.
+ *  taken         how many of free_pages were given away before, or NULL for none
+ *  starts        B + 1 values: sequence b's rows are starts[b] .. starts[b+1] - 1
+ *  lengths       B values: kept + fresh
+ *  slots         T values: the slot of each row's token, -1 behind the last sequence
+ *  positions     T values: its position, 0 behind the last sequence
+ *  taken_out     *taken and the pages given (not the same address as taken)
+ *
+ * B at most 2^20, T at most 2^25 - 1.  Each of these records EMU_ERR_INVALID_VALUE in
+ * the device's error word: a negative length, or more tokens than width pages
+ * hold (that sequence gets no rows, and length 0); more rows than T (those that
+ * do not fit are left out, of `lengths` too); free pages that run out or page
+ * numbers outside 0..pages-1 (-1 in the table, slots -1).
+ */
+emu_status_t emu_kv_tables(int64_t B, const int32_t* kept, const int32_t* fresh, int64_t pages, int64_t page,
+                           const int32_t* free_pages, int64_t n_free, const int32_t* taken, int32_t* table,
+                           int64_t width, int64_t T, int32_t* starts, int32_t* lengths, int32_t* slots,
+                           int32_t* positions, int32_t* taken_out, emu_stream_t stream);
+
+/*
+ * emu_kv_store -- T rows of keys and values (`dtype`, cache->heads heads of cache->D
+ * values each, any strides) into their slots.
+ *
+ *  slots         T values.  -1: the row is not stored.  Rows of one page have to be
+ *                neighbours in ascending slots, as emu_kv_tables gives them: where two
+ *                separate runs of one call write to one page, that page's content is
+ *                undefined.  Another value than -1 outside the cache is
+ *                not stored either and records EMU_ERR_INVALID_VALUE.
+ *
+ * A page's scale becomes the least power of two (2^-126 or more) with which its
+ * new finite values are within e4m3's 448, or stays where it is larger; rows that the
+ * page held before are then rounded again (code * old / new).  A run that writes a
+ * page's row 0 begins the page anew: what it held does not count.  Values are
+ * rounded to the nearest code, ties to even; infinities and NaN become NaN.
+ */
+emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_heads_t* v, const int32_t* slots,
+                          const emu_kv_cache_t* cache, emu_stream_t stream);
+
+/*
+ * emu_kv_attention -- softmax attention of every row over its sequence's kept tokens:
+ *     out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = e^(scale q[t, h] . k_j)
+ * where j runs over the tokens 0..position, with a window over the last `window`
+ * of them only.  Row i of sequence b has the position lengths[b] - rows + i: the
+ * rows are the sequence's last tokens, and are in the cache themselves.
+ *
+ *  q, out        T rows of the same number of heads, a multiple of cache->heads: head h
+ *                reads key head h / (heads / cache->heads).  `dtype`, any strides; out may
+ *                be q.
+ *  table, width  B rows of page numbers, as emu_kv_tables leaves them
+ *  starts        B + 1 values, ascending: sequence b has the rows starts[b] ..
+ *                starts[b+1] - 1 (none are fine); rows from starts[B] on become zero
+ *  lengths       B values
+ *  window        0: all tokens before
+ *  max_new       rows that a sequence has at most, or 0 where the caller does not
+ *                know.  It chooses kernels, not results.
+ *
+ * Scores, weights and sums are FP32-accurate for FP32 rows; for 16-bit rows the
+ * weights p are rounded to 11 bits for their product with v.  A row that sees no
+ * token is zero.  What a row does not see has no part in it, whatever it holds
+ * (NaN among it).  A length that is negative or more than width pages hold, and a
+ * page number outside the cache, give NaN in the rows that need them; `starts`
+ * out of order leaves rows of that sequence unwritten.  Each records
+ * EMU_ERR_INVALID_VALUE.
+ */
+emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t* q, const emu_heads_t* out,
+                              const emu_kv_cache_t* cache, int64_t B, const int32_t* table, int64_t width,
+                              const int32_t* starts, const int32_t* lengths, float scale, int64_t window,
+                              int64_t max_new, emu_stream_t stream);
 
 #ifdef __cplusplus
 }
