@@ -7,7 +7,7 @@
 //
 // A code is an FP16 value (4 significant bits, exponents -6..8), so one FP16 piece
 // of K and V is exact, and FP32 queries and weights p need two pieces each, hi +
-// lo (22 to 24 bits), where a product of two FP32 operands would need nine of three:
+// lo (good to 2^-23), where a product of two FP32 operands would need nine of three:
 // S = q_hi K + q_lo K, O = p_hi V + p_lo V, FP32 sums.  BF16 and FP16 queries are
 // exact in one piece (a row is scaled by a power of two so that its largest value
 // lies in 2^14..2^15; what falls below 2^-24 there is 2^-39 of the largest), and
@@ -17,13 +17,20 @@
 // bits however far the pages' scales are apart.
 //
 // Next tokens and drafts: bound by reading the cache.  The work is cut into units
-// of kUnit tokens of one sequence and key head for 16 rows (a key head's query
-// heads, of one token after another); the CTAs take equal consecutive ranges of all
-// units.  A range's first and last segment may be shared with neighbours: their
-// sums go to a slot in memory and the last one to arrive adds them up in order, so
-// the result does not depend on who is last.  Within a CTA each warp takes every
-// kWarps-th tile of 16 tokens (always inside one page) through a ring of its own,
-// filled by asynchronous copies: no barrier but at a segment's end.
+// of tokens of one sequence and key head for a segment of 8 NR rows (a key head's
+// query heads, of one token after another); the CTAs take equal consecutive ranges
+// of all units.  A range's first and last segment may be shared with neighbours:
+// their sums go to a slot in memory and the last one to arrive adds them up in
+// order (in groups first), so the result does not depend on who is last.  Within a
+// CTA each warp takes every kWarps-th step of ST tokens through a ring of its own,
+// filled by tensor copies: no barrier but at a segment's end.
+//
+// The rows are the MMA's N, so that 8 of them fill it: S^T = K Q^T, O^T = V^T P^T,
+// codes as the A operand, straight from their bytes.  The order of the values in a
+// product's sum, of the rows of O^T and of the tokens is free, and chosen so that
+// a lane reads 16 bytes at a time and no two lanes of a phase the same banks:
+// token t(g) = (g >> 1) + 4 (g & 1) is row g of S^T, piece (g >> 1) + 4 (g & 1) of 16
+// values of V belongs to rows g and g + 8 of O^T.
 #include "emu_device.cuh"
 #include "emu_host.h"
 #include "emu_layers.h"
@@ -33,10 +40,9 @@ namespace emu {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16;                            // tokens of a warp's step
-constexpr int kUnit = kTile * kWarps;
-constexpr int kRows = 16;                            // rows of a segment
-constexpr int kKvCtasPerSm = 3;
+constexpr int kGroup = 32;                           // parts that are added up at once, at most
+constexpr int kKvCtasPerSm = 4;                      // at most
+constexpr int kKvRows = 16;                          // rows of a segment, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
@@ -50,8 +56,11 @@ struct AttnParams {
     const int32_t *table, *starts, *lengths;
     float scale;
     int wide;                                        // rows of q on 16 bytes
-    float* partial;                                  // [2 ctas][kRows][D + 4]
-    unsigned* arrived;                               // [ctas], zero between calls
+    int depth, side;                                 // stages of a warp's ring, bytes of a stage's keys (or values)
+    int copy_tokens;                                 // tokens of one tensor copy
+    float* partial;                                  // [2 max ctas][kKvRows][D + 4]
+    unsigned* arrived;                               // [3][max ctas], zero between calls
+    int max_ctas;
     int* err;
 };
 
@@ -69,17 +78,21 @@ __device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
     if (s.len < 0 || s.len > (int64_t)p.width << p.page_log) s.len = -1;
     return s;
 }
-// Tiles start on 16 tokens; the first one that any row of the sequence sees.
-__device__ __forceinline__ int first_tile_token(const AttnParams& p, const Seq& s) {
+// Steps start on multiples of ST tokens; the first one that any row of the sequence sees.
+template <int ST>
+__device__ __forceinline__ int first_token(const AttnParams& p, const Seq& s) {
     if (!p.window) return 0;
-    return max(0, s.len - s.n - p.window + 1) & ~(kTile - 1);
+    return max(0, s.len - s.n - p.window + 1) & ~(ST - 1);
 }
+template <int ST>
 __device__ __forceinline__ int units_of(const AttnParams& p, const Seq& s) {       // of one segment
-    return max(1, (s.len - first_tile_token(p, s) + kUnit - 1) / kUnit);
+    constexpr int unit = ST * kWarps;
+    return max(1, (s.len - first_token<ST>(p, s) + unit - 1) / unit);
 }
+template <int ST, int ROWS>
 __device__ __forceinline__ int64_t all_units(const AttnParams& p, const Seq& s) {  // of the sequence
     const int64_t rows = (int64_t)s.n * p.group;
-    return (rows + kRows - 1) / kRows * p.heads * units_of(p, s);
+    return (rows + ROWS - 1) / ROWS * p.heads * units_of<ST>(p, s);
 }
 
 __device__ __forceinline__ float exp2_of(float x) {
@@ -90,8 +103,14 @@ __device__ __forceinline__ float exp2_of(float x) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, turned.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -105,57 +124,115 @@ __device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t h) {
     return half2_bits(lo - a, hi - b);
 }
 
-// Codes in shared memory: rows of NG x 64 bytes, their 16-byte pieces c at c ^
-// f(row), so that a quarter warp's reads of K (two rows, four pieces each) and a
-// half warp's of V (four rows two apart, two pieces each) meet all banks.
-template <int NG>
-__device__ __forceinline__ uint32_t piece_at(int row, int c) {
-    const int f = NG % 2 == 0 ? (row & 1) << 2 ^ (row >> 1 & 3) << 1 : (row >> 1 & 1) << 1;
-    return row * (NG * 64) + ((c ^ f) << 4);
-}
-
-template <int NG>
-struct Ring {
-    static constexpr int side = kTile * NG * 64;     // a tile of K or of V
-    static constexpr int stage = 2 * side + 16;      // and the two scales
-    static constexpr int depth = NG <= 2 ? 4 : 3;
-    static constexpr int warp = depth * stage;
-    static constexpr int joined = kWarps * kRows * (NG * 64 + 4) * 4;              // the warps' sums
-    static constexpr int bytes = kWarps * warp > joined ? kWarps * warp : joined;
-};
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
-
 // Of four codes: the bytes that are NaN (0x7F, 0xFF), all bits set.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
 }
 
-template <typename T, int NG>
-__global__ void __launch_bounds__(kThreads) kv_decode_kernel(const AttnParams p) {
+// Where byte o of a run of codes lies in shared memory: rows of 128 bytes, their
+// 16-byte pieces swizzled by the row (the tensor copies' 128-byte swizzle).
+__device__ __forceinline__ uint32_t swizzled(uint32_t o) { return o ^ (o >> 3 & 0x70); }
+
+// D in 64s (NG) as the lanes hold the values of O^T: blocks of 128 (16 bytes per
+// lane group and token), and one of 64 (8 bytes) where NG is odd.
+template <int NG>
+struct Blocks {
+    static constexpr int whole = NG / 2, count = (NG + 1) / 2;
+    static constexpr int tiles(int b) { return b < whole ? 8 : 4; }      // MMA tiles of 16 values
+    // first of the values that lane group g has in block b
+    static __device__ __forceinline__ int first(int b, int g) {
+        return b < whole ? 128 * b + 16 * ((g >> 1) + 4 * (g & 1)) : 128 * b + 8 * g;
+    }
+};
+
+// Adds up to kGroup parts of a segment (part 0 at part[0], k at part[1] + (k - 1) step; rows of
+// D + 4: maximum, sum, reference, -, and D sums) and hands each four values to `done`, with
+// their row's maximum, sum and reference.  Called by the whole CTA; weight: [kGroup][ROWS],
+// stats: [ROWS][3] in shared memory.
+template <int ROWS, typename F>
+__device__ __forceinline__ void add_parts(const float* const (&part)[2], int64_t step, int parts, int rows, int D,
+                                          float* weight, float* stats, F&& done) {
+    const int pitch = D + 4;
+    auto at = [&](int k) { return k == 0 ? part[0] : part[1] + (k - 1) * step; };
+    for (int r = threadIdx.x >> 5; r < rows; r += kWarps) {      // a row per warp, a part per lane
+        const int k = threadIdx.x & 31;
+        const bool in = k < parts;
+        const float* f = at(k) + r * pitch;
+        const float m = in ? __ldcg(f) : -INFINITY, l = in ? __ldcg(f + 1) : 0.0f, ref = in ? __ldcg(f + 2) : -INFINITY;
+        float m_all = m, ref_all = ref;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            m_all = fmaxf(m_all, __shfl_xor_sync(0xffffffffu, m_all, o));
+            ref_all = fmaxf(ref_all, __shfl_xor_sync(0xffffffffu, ref_all, o));
+        }
+        // (a part that saw nothing has no weight; NaN stays)
+        float sum = m > -INFINITY || l != 0.0f ? l * exp2_of(m - m_all) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        weight[k * ROWS + r] = ref > -INFINITY ? exp2_of(ref - ref_all) : 1.0f;
+        if (k == 0) {
+            stats[r * 3] = m_all;
+            stats[r * 3 + 1] = sum;
+            stats[r * 3 + 2] = ref_all;
+        }
+    }
+    __syncthreads();
+    const int quads = D / 4;
+    for (int i = threadIdx.x; i < rows * quads; i += kThreads) {
+        const int r = i / quads, d = (i - r * quads) * 4;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < parts; k0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < parts) v[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + k) + r * pitch + 4 + d));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < parts) {
+                    const float x = weight[(k0 + k) * ROWS + r];
+                    o.x = fmaf(v[k].x, x, o.x);
+                    o.y = fmaf(v[k].y, x, o.y);
+                    o.z = fmaf(v[k].z, x, o.z);
+                    o.w = fmaf(v[k].w, x, o.w);
+                }
+        }
+        done(r, d, stats[r * 3], stats[r * 3 + 1], stats[r * 3 + 2], o);
+    }
+}
+
+template <typename T, int NG, int NR, int ST>
+__global__ void __launch_bounds__(kThreads, NG > 2 ? 1 : NR == 1 && (NG == 1 || sizeof(T) == 2) ? 3 : 2)
+kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     constexpr bool TWO = sizeof(T) == 4;             // two pieces of q and of p
     constexpr int PIECES = TWO ? 2 : 1;
-    using R = Ring<NG>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int ROWS = 8 * NR, SUB = ST / 16;      // rows of a segment; tiles of 16 tokens in a step
+    constexpr int UNIT = ST * kWarps;
+    constexpr int BATCH = 32 / SUB;                  // steps whose pages the lanes hold, one tile each
+    using Bl = Blocks<NG>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kWarps][4];
     __shared__ int64_t warp_sum[kWarps];
     __shared__ int64_t found_base;
     __shared__ int found_seq;
     __shared__ unsigned order;
+    __shared__ float weight[kGroup * ROWS], stats[ROWS * 3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int P = 1 << p.page_log;
-    uint8_t* const ring = smem + warp * R::warp;
+    const int P = 1 << p.page_log, D = p.D;
+    const uint32_t ring = smem_u32(smem) + warp * p.depth * 2 * p.side;
+    uint8_t* const ring_at = smem + warp * p.depth * 2 * p.side;
+    const uint32_t bar0 = smem_u32(bars[warp]);
+    if (lane == 0) {
+        for (int i = 0; i < 4; ++i) mbar_init(bar0 + 8 * i, SUB);
+        fence_mbar_init();
+    }
+    const float nan = __uint_as_float(0x7FC00000u);
 
     // all units, and where this CTA's range of them begins: a run of sequences per thread
     const int per = (p.B + kThreads - 1) / kThreads;
     int64_t mine = 0;
     for (int b = tid * per; b < min((tid + 1) * per, p.B); ++b) {
         const Seq s = seq_of(p, b);
-        mine += all_units(p, s);
+        mine += all_units<ST, ROWS>(p, s);
         if (blockIdx.x == 0 && (s.len < 0 || p.starts[b + 1] < s.start || s.start < 0 || p.starts[b + 1] > p.T))
             record_error(p.err, kDevErrValue);
     }
@@ -176,14 +253,14 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const AttnParams p)
     // rows behind the last sequence
     {
         const int used = p.B > 0 ? min(max(p.starts[p.B], 0), p.T) : 0;
-        const int values = p.heads * p.group * p.D;
+        const int values = p.heads * p.group * D;
         for (int row = used + blockIdx.x; row < p.T; row += gridDim.x)
             for (int e = tid; e < values; e += kThreads) {
-                const int h = e / p.D;
-                static_cast<T*>(p.out)[row * p.out_t + h * p.out_h + (e - h * p.D)] = kv_from<T>(0.0f);
+                const int h = e / D;
+                static_cast<T*>(p.out)[row * p.out_t + h * p.out_h + (e - h * D)] = kv_from<T>(0.0f);
             }
     }
-    // (no more of them than units: each has one at least)
+    // (no more CTAs than units: each has one at least)
     const int64_t ctas = min((int64_t)gridDim.x, all);
     if (blockIdx.x >= ctas) return;
     int64_t at = all * blockIdx.x / ctas;
@@ -192,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const AttnParams p)
     if (before <= at && at < sum) {
         int b = tid * per;
         for (;; ++b) {
-            const int64_t w = all_units(p, seq_of(p, b));
+            const int64_t w = all_units<ST, ROWS>(p, seq_of(p, b));
             if (at < before + w) break;
             before += w;
         }
@@ -202,88 +279,97 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const AttnParams p)
     __syncthreads();
     int b = found_seq;
     int64_t base = found_base;
+    int stage_in = 0, stage_out = 0;                 // next stage to fill, to read
+    uint32_t parity = 0;                             // of the stage to read, flips when the ring wraps
+    bool dead = false;                               // a wait gave up: no more copies
 
     while (at < stop) {
         Seq s = seq_of(p, b);
-        int64_t w = all_units(p, s);
+        int64_t w = all_units<ST, ROWS>(p, s);
         while (at >= base + w) {
             base += w;
             s = seq_of(p, ++b);
-            w = all_units(p, s);
+            w = all_units<ST, ROWS>(p, s);
         }
         const bool bad = s.len < 0;
         if (bad) s.len = 0;
-        const int units = units_of(p, s);
-        const int seg = (int)((at - base) / units);  // q tile * heads + head
+        const int units = units_of<ST>(p, s);
+        const int seg = (int)((at - base) / units);  // row tile * heads + head
         const int64_t seg_begin = base + (int64_t)seg * units, seg_end = seg_begin + units;
         const int u0 = (int)(at - seg_begin), u1 = (int)(min(stop, seg_end) - seg_begin);
-        const int head = seg % p.heads, row0 = seg / p.heads * kRows;
-        const int rows = min(kRows, s.n * p.group - row0);
+        const int head = seg % p.heads, row0 = seg / p.heads * ROWS;
+        const int rows = min(ROWS, s.n * p.group - row0);
         const int pos0 = s.len - s.n;                // position of the sequence's first new token
-        // tokens that some row of the segment sees
-        const int sees_end = max(0, min(s.len, pos0 + (row0 + rows - 1) / p.group + 1));
-        const int sees_begin = p.window ? max(0, pos0 + row0 / p.group - p.window + 1) : 0;
-        const int tile0 = first_tile_token(p, s) + u0 * kUnit + warp * kTile;
-        const int tiles = (u1 - u0);                 // of this warp, kUnit tokens apart
+        // tokens that some row of the segment sees; steps of this warp that have any
+        const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
+        const int sees_end = max(0, min(s.len, pos_last + 1));
+        const int sees_begin = p.window ? max(0, pos_first - p.window + 1) : 0;
+        int token0 = first_token<ST>(p, s) + u0 * UNIT + warp * ST;
+        int steps = u1 - u0;
+        if (token0 + ST <= sees_begin) {
+            const int skip = (sees_begin - token0 - ST) / UNIT + 1;
+            token0 += skip * UNIT;
+            steps -= skip;
+        }
+        steps = sees_end <= token0 ? 0 : min(steps, (sees_end - token0 + UNIT - 1) / UNIT);
         const int32_t* pages = p.table + (int64_t)b * p.width;
-        const float nan = __uint_as_float(0x7FC00000u);
 
-        // copies of the warp's tile i; page: its page as the table has it
+        // A lane has one tile of each of BATCH steps: the page (-1: bad, -2: no row sees the tile) and its scales.
         auto page_of = [&](int i) {
-            const int tok = tile0 + i * kUnit;
-            return i < tiles && tok < sees_end && tok + kTile > sees_begin ? pages[tok >> p.page_log] : 0;
+            const int tok = token0 + i * UNIT + (SUB == 2 ? (lane & 1) * 16 : 0);
+            // (where one copy brings the whole step, the step counts)
+            const int from = p.copy_tokens > 16 ? token0 + i * UNIT : tok, to = from + p.copy_tokens;
+            if (i >= steps || from >= sees_end || to <= sees_begin) return -2;
+            const int page = pages[from >> p.page_log];
+            return page >= 0 && page < p.pages ? page : -1;
         };
-        auto copy_tile = [&](int i, int page) {
-            const int tok = tile0 + i * kUnit;
-            if (i < tiles && tok < sees_end && tok + kTile > sees_begin) {
-                const uint32_t dst = smem_u32(ring) + i % R::depth * R::stage;
-                const bool ok = page >= 0 && page < p.pages;
-                const int64_t unit = (int64_t)(ok ? page : 0) * p.heads + head;
-                const int64_t from = ((unit << p.page_log) + (tok & (P - 1))) * p.D;
-#pragma unroll
-                for (int c = lane; c < kTile * NG * 4; c += 32) {
-                    const int row = c / (NG * 4), piece = c % (NG * 4);
-                    const bool in = ok && tok + row >= sees_begin && tok + row < sees_end && piece * 16 < p.D;
-                    const int64_t off = in ? from + row * p.D + piece * 16 : 0;
-                    const uint32_t to = dst + piece_at<NG>(row, piece);
-                    copy16(to, p.k + off, in);
-                    copy16(to + R::side, p.v + off, in);
-                }
-                if (lane < 2) {
-                    const uint32_t to = dst + 2 * R::side + 4 * lane;
-                    if (ok) copy4(to, (lane ? p.vs : p.ks) + unit);
-                    else {
-                        asm volatile("st.shared.f32 [%0], %1;" :: "r"(to), "f"(nan) : "memory");
-                        record_error(p.err, kDevErrValue);
-                    }
+        auto scales_of = [&](int page, float& ks, float& vs) {
+            const int64_t unit = (int64_t)max(page, 0) * p.heads + head;
+            ks = page >= 0 ? p.ks[unit] : page == -1 ? nan : 0.0f;
+            vs = page >= 0 ? p.vs[unit] : page == -1 ? nan : 0.0f;
+            if (page == -1) record_error(p.err, kDevErrValue);
+        };
+        const int my_step = lane / SUB;              // of a batch
+        int page_now = page_of(my_step), page_next = page_of(BATCH + my_step);
+        // The step's copies, by the lanes that have its tiles; each arrives once.
+        auto copy_step = [&](int i, int page) {
+            if (i < steps && my_step == i % BATCH && !dead) {
+                const uint32_t bar = bar0 + 8 * stage_in, dst = ring + stage_in * 2 * p.side;
+                const int sub = SUB == 2 ? lane & 1 : 0;
+                const bool joint = p.copy_tokens > 16;           // both tiles in one copy: this lane does one side
+                const int tok = token0 + i * UNIT + (joint ? 0 : sub * 16);
+                const int64_t first = (((int64_t)max(page, 0) * p.heads + head) << p.page_log) + (tok & (P - 1));
+                const int row = (int)(first * D >> 7);
+                const uint32_t bytes = p.copy_tokens * D;
+                const bool both = !joint || SUB == 1;
+                mbar_arrive_expect_tx(bar, page >= 0 ? (both ? 2 : 1) * bytes : 0);
+                if (page >= 0) {
+                    const uint32_t to = dst + (joint ? 0 : sub * 16 * D);
+                    if (both || sub == 0) tma_load_3d(to, &map_k, bar, 0, row, 0);
+                    if (both || sub == 1) tma_load_3d(to + p.side, &map_v, bar, 0, row, 0);
                 }
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (i < steps) stage_in = stage_in + 1 == p.depth ? 0 : stage_in + 1;
         };
-        int next_page[R::depth];
-#pragma unroll
-        for (int i = 0; i < R::depth; ++i) next_page[i] = page_of(i);
-        __syncthreads();                             // the shared memory of the segment before has been read
-#pragma unroll
-        for (int i = 0; i < R::depth - 1; ++i) copy_tile(i, next_page[i]);
-        int page_ahead = next_page[R::depth - 1];
+        for (int i = 0; i < p.depth - 1; ++i) copy_step(i, page_now);
+        float ks_now, vs_now, ks_next = 0.0f, vs_next = 0.0f;
+        scales_of(page_now, ks_now, vs_now);
 
-        // The rows g and g + 8 of the queries as FP16 pieces: of the 64 values of a
-        // group a lane holds 16 in a row, four for each K = 16 step.
-        uint32_t qa[PIECES][NG * 4][4];
-        float factor[2];                             // a row's: scores are sums times factor times s_k, base 2
-        int pos[2];
+        // The rows of the queries as FP16 pieces: of the 64 values of a group a lane
+        // holds 16 in a row, four for each K = 16 step.
+        uint32_t qb[PIECES][NR][NG * 4][2];
+        float factor[NR][2];                         // of rows 8 r + 2t, + 1: scores are sums times factor times s_k, base 2
+        int pos[NR][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = min(row0 + g + 8 * r, row0 + rows - 1), i = row / p.group;
+        for (int r = 0; r < NR; ++r) {
+            const int row = min(row0 + 8 * r + g, row0 + rows - 1), i = row / p.group;
             const T* from = static_cast<const T*>(p.q) + (s.start + i) * p.q_t + (head * p.group + row - i * p.group) * p.q_h;
-            pos[r] = pos0 + i;
             float x[NG * 16];
             float top = 0.0f;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const int d = n * 64 + t * 16;
-                if (d < p.D) {
+                if (d < D) {
                     kv_load8(from + d, p.wide, x + n * 16);
                     kv_load8(from + d + 8, p.wide, x + n * 16 + 8);
                 } else {
@@ -298,285 +384,445 @@ __global__ void __launch_bounds__(kThreads) kv_decode_kernel(const AttnParams p)
             // 2^(14 - E), top = m 2^E
             const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
             const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-            factor[r] = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (p.scale * kLog2e);
+            const float mine_factor = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (p.scale * kLog2e);
 #pragma unroll
             for (int k = 0; k < NG * 4; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {        // a0/a1: the first pair; a2/a3: the second
+                for (int h = 0; h < 2; ++h) {
                     const float lo = x[4 * k + 2 * h] * up, hi = x[4 * k + 2 * h + 1] * up;
-                    qa[0][k][r + 2 * h] = half2_bits(lo, hi);
-                    if constexpr (TWO) qa[PIECES - 1][k][r + 2 * h] = half2_rest(lo, hi, qa[0][k][r + 2 * h]);
+                    qb[0][r][k][h] = half2_bits(lo, hi);
+                    if constexpr (TWO) qb[PIECES - 1][r][k][h] = half2_rest(lo, hi, qb[0][r][k][h]);
                 }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                factor[r][e] = __shfl_sync(0xffffffffu, mine_factor, 4 * (2 * t + e));
+                pos[r][e] = pos0 + min(row0 + 8 * r + 2 * t + e, row0 + rows - 1) / p.group;
+            }
         }
 
-        float o[NG * 8][4];
+        float o[Bl::count * 8][NR][4];               // (of a block of 64: the first four tiles)
 #pragma unroll
-        for (int n = 0; n < NG * 8; ++n)
+        for (int n = 0; n < Bl::count * 8; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
-        float top[2] = {-INFINITY, -INFINITY};       // running maxima of the scores
-        float ref[2] = {-INFINITY, -INFINITY};       // and of what o is held against
-        float total[2] = {0.0f, 0.0f};               // this lane's sums of p
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][r][e] = 0.0f;
+        float top[NR][2], ref[NR][2], total[NR][2];  // running maxima of the scores, what o is held against, sums of p
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[r][e] = ref[r][e] = -INFINITY;
+                total[r][e] = 0.0f;
+            }
+        const int tau = (g >> 1) + 4 * (g & 1);      // this lane's token of S^T's rows 0..7
 
-        for (int i = 0; i < tiles; ++i) {
-            asm volatile("cp.async.wait_group %0;" :: "n"(R::depth - 2) : "memory");
-            __syncwarp();
-            copy_tile(i + R::depth - 1, page_ahead);
-            page_ahead = page_of(i + R::depth);
-            const int tok = tile0 + i * kUnit;
-            if (tok >= sees_end || tok + kTile <= sees_begin) continue;
-            const uint8_t* kt = ring + i % R::depth * R::stage;
-            const uint8_t* vt = kt + R::side;
-            const float k_scale = *reinterpret_cast<const float*>(kt + 2 * R::side);
-            const float v_scale = *reinterpret_cast<const float*>(kt + 2 * R::side + 4);
+        for (int i = 0; i < steps; ++i) {
+            const int in_batch = i % BATCH;
+            if (in_batch == 0 && i > 0) {
+                page_now = page_next;
+                ks_now = ks_next;
+                vs_now = vs_next;
+                page_next = page_of(i + BATCH + my_step);
+            }
+            if (in_batch == BATCH / 2) scales_of(page_next, ks_next, vs_next);
+            if (!dead && __any_sync(0xffffffffu, !mbar_wait(bar0 + 8 * stage_out, parity, p.err, kDevErrTimeout))) {
+                // the copies in flight may still land: once more for each
+                dead = true;
+                for (int k = 0; k < min(p.depth - 1, steps - i); ++k) {
+                    const int st = (stage_out + k) % p.depth;
+                    mbar_wait(bar0 + 8 * st, parity ^ (stage_out + k >= p.depth), p.err, kDevErrTimeout);
+                }
+            }
+            __syncwarp();                            // all lanes have read the stage that is filled now
+            const int ahead = i + p.depth - 1;
+            copy_step(ahead, ahead / BATCH == i / BATCH ? page_now : page_next);
+            const int tok = token0 + i * UNIT;
+            const uint8_t* kt = ring_at + stage_out * 2 * p.side;
+            const uint8_t* vt = kt + p.side;
+            if (++stage_out == p.depth) {
+                stage_out = 0;
+                parity ^= 1;
+            }
+            float k_scale[SUB], v_scale[SUB];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                k_scale[u] = __shfl_sync(0xffffffffu, ks_now, in_batch * SUB + u);
+                v_scale[u] = __shfl_sync(0xffffffffu, vs_now, in_batch * SUB + u);
+            }
 
-            float sc[2][4];
+            float sc[SUB][NR][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int u = 0; u < SUB; ++u) {
+                float other[NR][4];                  // a second chain of sums (TWO: of the low pieces)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[u][r][e] = other[r][e] = 0.0f;
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    const uint4 w4 = *reinterpret_cast<const uint4*>(kt + piece_at<NG>(8 * n + g, 4 * gr + t));
-                    const uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const uint32_t at0 = (16 * u + tau) * D + 64 * gr + 16 * t;
+                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                    if (64 * gr + 16 * t < D) {
+                        lo = *reinterpret_cast<const uint4*>(kt + swizzled(at0));
+                        hi = *reinterpret_cast<const uint4*>(kt + swizzled(at0 + 8 * D));
+                    }
+                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t b0 = kv_half2((uint16_t)wd[k]), b1 = kv_half2((uint16_t)(wd[k] >> 16));
-                        if constexpr (TWO) mma_f16(sc[n], qa[PIECES - 1][4 * gr + k], b0, b1);
-                        mma_f16(sc[n], qa[0][4 * gr + k], b0, b1);
+                        const uint32_t a[4] = {kv_half2((uint16_t)wl[k]), kv_half2((uint16_t)wh[k]),
+                                               kv_half2((uint16_t)(wl[k] >> 16)), kv_half2((uint16_t)(wh[k] >> 16))};
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            if constexpr (TWO) {
+                                mma_f16(other[r], a, qb[PIECES - 1][r][4 * gr + k][0], qb[PIECES - 1][r][4 * gr + k][1]);
+                                mma_f16(sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
+                            } else {
+                                mma_f16(k & 1 ? other[r] : sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
+                            }
+                        }
                     }
                 }
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[u][r][e] += other[r][e];
             }
-            // base-2 scores; what a row does not see is -infinity
-            const bool edge = tok + kTile > pos0 + row0 / p.group + 1 || tok + kTile > s.len ||
-                              (p.window && tok <= pos0 + (row0 + rows - 1) / p.group - p.window);
+            // Whether some row does not see some token of the step
+            const bool edge = tok + ST > pos_first + 1 || tok + ST > s.len || (p.window && tok <= pos_last - p.window);
+            // bounds of log2(s_v): its exponent and one
+            int v_exp[SUB];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float f = factor[r] * k_scale;
+            for (int u = 0; u < SUB; ++u) v_exp[u] = (int)((__float_as_uint(v_scale[u]) >> 23) & 0xFF) - 126;
+            uint32_t pb[PIECES][SUB][NR][2];         // P^T: rows of tokens, turned
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+            for (int r = 0; r < NR; ++r) {
+                float m0[2], f[SUB][2], fs[SUB][2];
+                uint32_t hidden = 0;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& x = sc[n][2 * r + e];
-                        x *= f;
+                for (int e = 0; e < 2; ++e) {
+                    float m[SUB];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        fs[u][e] = factor[r][e] * k_scale[u];
+                        float a = sc[u][r][e] * fs[u][e], c = sc[u][r][e + 2] * fs[u][e];
                         if (edge) {
-                            const int j = tok + 8 * n + 2 * t + e;
-                            if (j > pos[r] || j >= s.len || (p.window && j <= pos[r] - p.window)) x = -INFINITY;
+                            // what a row does not see is -infinity, and has no weight below
+                            const int j = tok + 16 * u + tau, last = min(pos[r][e], s.len - 1);
+                            const int from = p.window ? pos[r][e] - p.window : -1;
+                            if (j > last || j <= from) a = -INFINITY, hidden |= 1u << (4 * u + e);
+                            if (j + 8 > last || j + 8 <= from) c = -INFINITY, hidden |= 1u << (4 * u + 2 + e);
+                        }
+                        m[u] = fmaxf(a, c);
+                    }
+                    float m_all = m[0], over = m[0] + (float)(v_exp[0] - 14);
+                    bool apart = false;
+                    if constexpr (SUB == 2) {
+                        m_all = fmaxf(m[0], m[1]);
+                        over = fmaxf(over, m[1] + (float)(v_exp[1] - 14));
+                        apart = v_exp[0] != v_exp[1];
+                    }
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) m_all = fmaxf(m_all, __shfl_xor_sync(0xffffffffu, m_all, x));
+                    if (apart) {
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, x));
+                    } else {
+                        over = m_all + (float)(v_exp[0] - 14);
+                    }
+                    const float top_now = fmaxf(top[r][e], m_all), ref_now = fmaxf(ref[r][e], over);
+                    if (top_now > top[r][e]) total[r][e] *= exp2_of(top[r][e] - top_now);
+                    const bool up = ref_now > ref[r][e];
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float c = up ? exp2_of(ref[r][e] - ref_now) : 1.0f;
+#pragma unroll
+                        for (int n = 0; n < Bl::count * 8; ++n) {
+                            o[n][r][e] *= c;
+                            o[n][r][e + 2] *= c;
                         }
                     }
-            }
-            // a bound of log2(s_v): its exponent and one
-            const int v_exp = (int)((__float_as_uint(v_scale) >> 23) & 0xFF) - 126;
-            uint32_t pa[PIECES][4];
+                    top[r][e] = top_now;
+                    ref[r][e] = ref_now;
+                    m0[e] = top_now == -INFINITY ? 0.0f : top_now;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float m = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const float top_now = fmaxf(top[r], m), ref_now = fmaxf(ref[r], m + (float)(v_exp - 14));
-                if (top_now > top[r]) total[r] *= exp2_of(top[r] - top_now);
-                if (__any_sync(0xffffffffu, ref_now > ref[r])) {
-                    const float c = ref_now > ref[r] ? exp2_of(ref[r] - ref_now) : 1.0f;
+                    for (int u = 0; u < SUB; ++u)
+                        f[u][e] = top_now == -INFINITY ? 0.0f : v_scale[u] * exp2_of(top_now - ref_now);
+                }
 #pragma unroll
-                    for (int n = 0; n < NG * 8; ++n) {
-                        o[n][2 * r] *= c;
-                        o[n][2 * r + 1] *= c;
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float w2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            // (one rounding, at the difference's size)
+                            float x = exp2_of(fmaf(sc[u][r][e + 2 * h], fs[u][e], -m0[e]));
+                            w2[e] = x * f[u][e];
+                            if (hidden >> (4 * u + 2 * h + e) & 1) x = w2[e] = 0.0f;
+                            total[r][e] += x;
+                        }
+                        const uint32_t hi = half2_bits(w2[0], w2[1]);
+                        pb[0][u][r][h] = turned(hi);
+                        if constexpr (TWO) pb[PIECES - 1][u][r][h] = turned(half2_rest(w2[0], w2[1], hi));
                     }
-                }
-                top[r] = top_now;
-                ref[r] = ref_now;
-                const float m0 = top_now == -INFINITY ? 0.0f : top_now;
-                const float f = top_now == -INFINITY ? 0.0f : v_scale * exp2_of(top_now - ref_now);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = exp2_of(sc[n][2 * r] - m0), p1 = exp2_of(sc[n][2 * r + 1] - m0);
-                    total[r] += p0 + p1;
-                    pa[0][r + 2 * n] = half2_bits(p0 * f, p1 * f);
-                    if constexpr (TWO) pa[PIECES - 1][r + 2 * n] = half2_rest(p0 * f, p1 * f, pa[0][r + 2 * n]);
-                }
             }
-            // Values: of the 64 of a group a lane holds 8 in a row, of the four tokens 2t, 2t + 1, 2t + 8, 2t + 9.
+            // Values: of a token a lane has 16 (8) in a row of each block, of the four tokens t, t + 4, t + 8, t + 12
+            // of a tile; bytes 2j and 2j + 1 are rows g and g + 8 of the block's tile j.
             bool nan_seen = false;
+            auto clean = [&](uint32_t& w) {
+                // A NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken out here
+                // and put into those rows below.
+                const uint32_t n = nan_bytes(w);
+                nan_seen = nan_seen || n != 0;
+                w &= ~n;
+            };
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-                uint2 row[4];
+            for (int bl = 0; bl < Bl::count; ++bl) {
+                constexpr int WIDE = TWO ? 2 : 4;    // words of a token at a time (TWO: the step's own sums need the registers)
+                const int d0 = Bl::first(bl, g);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    row[k] = *reinterpret_cast<const uint2*>(
-                        vt + piece_at<NG>(2 * t + (k & 1) + 8 * (k >> 1), 4 * gr + (g >> 1)) + (g & 1) * 8);
-                    if (edge) {
-                        // A NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is
-                        // taken out here and put into those rows below.
-                        if (nan_bytes(row[k].x) | nan_bytes(row[k].y)) {
-                            nan_seen = true;
-                            row[k].x &= ~nan_bytes(row[k].x);
-                            row[k].y &= ~nan_bytes(row[k].y);
+                for (int w0 = 0; w0 < Bl::tiles(bl) / 2; w0 += WIDE) {
+                    const int words = min(WIDE, Bl::tiles(bl) / 2 - w0);
+                    float fresh[TWO ? 2 * WIDE : 1][NR][4];      // added to o in FP32, nearest
+#pragma unroll
+                    for (int j = 0; j < (TWO ? 2 * WIDE : 1); ++j)
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) fresh[j][r][e] = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t row[4][WIDE];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint8_t* from = vt + swizzled((16 * u + t + 4 * k) * D + d0 + 4 * w0);
+                            if (words == 4) *reinterpret_cast<uint4*>(row[k]) = *reinterpret_cast<const uint4*>(from);
+                            else *reinterpret_cast<uint2*>(row[k]) = *reinterpret_cast<const uint2*>(from);
+                            if (edge)
+#pragma unroll
+                                for (int x = 0; x < WIDE; ++x)
+                                    if (x < words) clean(row[k][x]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2 * WIDE; ++j) {
+                            if (j >= 2 * words) continue;
+                            const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+                            const uint32_t x = __byte_perm(row[0][j / 2], row[1][j / 2], sel);
+                            const uint32_t y = __byte_perm(row[2][j / 2], row[3][j / 2], sel);
+                            const uint32_t a[4] = {kv_half2((uint16_t)x), kv_half2((uint16_t)(x >> 16)), kv_half2((uint16_t)y),
+                                                   kv_half2((uint16_t)(y >> 16))};
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) {
+                                if constexpr (TWO) {
+                                    mma_f16(fresh[j][r], a, pb[PIECES - 1][u][r][0], pb[PIECES - 1][u][r][1]);
+                                    mma_f16(fresh[j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
+                                } else {
+                                    mma_f16(o[bl * 8 + 2 * w0 + j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
+                                }
+                            }
                         }
                     }
-                }
+                    if constexpr (TWO)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t a0 = j < 4 ? row[0].x : row[0].y, a1 = j < 4 ? row[1].x : row[1].y;
-                    const uint32_t a2 = j < 4 ? row[2].x : row[2].y, a3 = j < 4 ? row[3].x : row[3].y;
-                    const uint32_t sel = (j & 3) < 2 ? 0x5140 : 0x7362;
-                    const uint32_t lo = __byte_perm(a0, a1, sel), hi = __byte_perm(a2, a3, sel);
-                    const uint32_t b0 = kv_half2((uint16_t)(j & 1 ? lo >> 16 : lo));
-                    const uint32_t b1 = kv_half2((uint16_t)(j & 1 ? hi >> 16 : hi));
-                    if constexpr (TWO) mma_f16(o[gr * 8 + j], pa[PIECES - 1], b0, b1);
-                    mma_f16(o[gr * 8 + j], pa[0], b0, b1);
+                        for (int j = 0; j < 2 * WIDE; ++j)
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (j < 2 * words) o[bl * 8 + 2 * w0 + j][r][e] += fresh[j][r][e];
                 }
             }
             if (edge && __any_sync(0xffffffffu, nan_seen)) {
-                for (int row = 0; row < kTile; ++row) {
-                    const int j = tok + row;
+                for (int x = 0; x < ST; ++x) {
+                    const int j = tok + x;
 #pragma unroll
-                    for (int gr = 0; gr < NG; ++gr)
+                    for (int bl = 0; bl < Bl::count; ++bl)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // values 64 gr + 8 (2t + e) .. + 7
-                            const uint8_t* at8 = vt + piece_at<NG>(row, 4 * gr + t) + e * 8;
+                        for (int c = 0; c < 2 * Bl::tiles(bl); ++c)
+                            if ((vt[swizzled(x * D + Bl::first(bl, g) + c)] & 0x7F) == 0x7F) {
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                if ((at8[x] & 0x7F) == 0x7F) {
+                                for (int r = 0; r < NR; ++r)
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r)
-                                        if (j <= pos[r] && j < s.len && !(p.window && j <= pos[r] - p.window))
-                                            o[gr * 8 + x][2 * r + e] = nan;
-                                }
-                        }
+                                    for (int e = 0; e < 2; ++e)
+                                        if (j <= pos[r][e] && j < s.len && !(p.window && j <= pos[r][e] - p.window))
+                                            o[bl * 8 + c / 2][r][e + 2 * (c & 1)] = nan;
+                            }
                 }
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            total[r] += __shfl_xor_sync(0xffffffffu, total[r], 1);
-            total[r] += __shfl_xor_sync(0xffffffffu, total[r], 2);
-        }
-        __syncthreads();                             // all rings have been read
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) total[r][e] += __shfl_xor_sync(0xffffffffu, total[r][e], x);
+        __syncthreads();                             // all rings have been read, and none has copies in flight
         // the warps' sums: [warp][row][4 + D]: maximum, sum, reference, and o
         const int pitch = NG * 64 + 4;
         float* const joined = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float* to = joined + (warp * kRows + g + 8 * r) * pitch;
-            if (t == 0) {
-                to[0] = top[r];
-                to[1] = total[r];
-                to[2] = ref[r];
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float* to = joined + (warp * ROWS + 8 * r + 2 * t + e) * pitch;
+                if (g == 0) {
+                    to[0] = top[r][e];
+                    to[1] = total[r][e];
+                    to[2] = ref[r][e];
+                }
+#pragma unroll
+                for (int bl = 0; bl < Bl::count; ++bl)
+#pragma unroll
+                    for (int j = 0; j < Bl::tiles(bl); j += 2)
+                        *reinterpret_cast<float4*>(to + 4 + Bl::first(bl, g) + 2 * j) =
+                            make_float4(o[bl * 8 + j][r][e], o[bl * 8 + j][r][e + 2], o[bl * 8 + j + 1][r][e],
+                                        o[bl * 8 + j + 1][r][e + 2]);
             }
-            to += 4;
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float4*>(to + 64 * gr + 16 * t + 8 * e + 4 * h) =
-                            make_float4(o[gr * 8 + 4 * h][2 * r + e], o[gr * 8 + 4 * h + 1][2 * r + e],
-                                        o[gr * 8 + 4 * h + 2][2 * r + e], o[gr * 8 + 4 * h + 3][2 * r + e]);
-        }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;
-        // Adds `parts` of one layout up; row r, value d of each at from + part * step
-        auto finish = [&](int r, int d, float m, float l, float ref_all, float sum_o) {
+        auto finish = [&](int r, int d, float m, float l, float ref_all, float4 v) {
             const int row = row0 + r, i = row / p.group;
-            float y = l > 0.0f || l != l ? sum_o / l * exp2_of(ref_all - m) : 0.0f;
-            if (bad) y = nan;
-            static_cast<T*>(p.out)[(s.start + i) * p.out_t + (head * p.group + row - i * p.group) * p.out_h + d] = kv_from<T>(y);
+            const float f = l > 0.0f || l != l ? exp2_of(ref_all - m) / l : 0.0f;
+            float y[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+            T* to = static_cast<T*>(p.out) + (s.start + i) * p.out_t + (head * p.group + row - i * p.group) * p.out_h + d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e] = kv_from<T>(bad ? nan : y[e]);
         };
-        auto add_up = [&](const float* from, int64_t step, int parts, float& m, float& l, float& ref_all, int d, float& sum_o) {
-            m = ref_all = -INFINITY;
-            for (int k = 0; k < parts; ++k) {
-                m = fmaxf(m, from[k * step]);
-                ref_all = fmaxf(ref_all, from[k * step + 2]);
+        const int part_pitch = D + 4;
+        const int64_t slot_size = (int64_t)kKvRows * part_pitch;
+        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + (u0 == 0)) * slot_size;
+        const int quads = D / 4;
+        for (int i = tid; i < rows * quads; i += kThreads) {
+            const int r = i / quads, d = (i - r * quads) * 4;
+            const float* from = joined + r * pitch;
+            float m = -INFINITY, ref_all = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                m = fmaxf(m, from[k * ROWS * pitch]);
+                ref_all = fmaxf(ref_all, from[k * ROWS * pitch + 2]);
             }
-            l = sum_o = 0.0f;
-            for (int k = 0; k < parts; ++k) {
-                const float mk = from[k * step], rk = from[k * step + 2];
-                if (mk > -INFINITY || from[k * step + 1] != 0.0f) l += from[k * step + 1] * exp2_of(mk - m);
-                const float ok = from[k * step + 4 + d];
-                if (rk > -INFINITY || ok != 0.0f) sum_o += ok * exp2_of(rk - ref_all);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float* f = from + k * ROWS * pitch;
+                // (a warp that saw nothing has no weight; NaN stays)
+                if (f[0] > -INFINITY || f[1] != 0.0f) l += f[1] * exp2_of(f[0] - m);
+                const float x = f[2] > -INFINITY ? exp2_of(f[2] - ref_all) : 1.0f;
+                const float4 y = *reinterpret_cast<const float4*>(f + 4 + d);
+                v.x = fmaf(y.x, x, v.x);
+                v.y = fmaf(y.y, x, v.y);
+                v.z = fmaf(y.z, x, v.z);
+                v.w = fmaf(y.w, x, v.w);
             }
-        };
-        const int part_pitch = p.D + 4;
-        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + (u0 == 0)) * kRows * part_pitch;
-        for (int e = tid; e < rows * p.D; e += kThreads) {
-            const int r = e / p.D, d = e - r * p.D;
-            float m, l, ref_all, sum_o;
-            add_up(joined + r * pitch, kRows * pitch, kWarps, m, l, ref_all, d, sum_o);
             if (whole) {
-                finish(r, d, m, l, ref_all, sum_o);
+                finish(r, d, m, l, ref_all, v);
             } else {
                 float* to = slot + r * part_pitch;
-                to[4 + d] = sum_o;
-                if (d == 0) {
-                    to[0] = m;
-                    to[1] = l;
-                    to[2] = ref_all;
-                }
+                *reinterpret_cast<float4*>(to + 4 + d) = v;
+                if (d == 0) *reinterpret_cast<float4*>(to) = make_float4(m, l, ref_all, 0.0f);
             }
         }
         if (!whole) {
-            // CTAs that share the segment: c0, whose part is its range's last, to c1
-            const int64_t c0 = ((seg_begin + 1) * ctas - 1) / all, c1 = (seg_end * ctas - 1) / all;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                order = atomicAdd(p.arrived + c0, 1u);
+            // CTAs that share the segment: c0, whose part is its range's last, to c1.  c0's slot is its odd
+            // one, the others' their even one.
+            const int c0 = (int)(((seg_begin + 1) * ctas - 1) / all), c1 = (int)((seg_end * ctas - 1) / all);
+            auto slot_of = [&](int c) { return p.partial + (2 * (int64_t)c + (c == c0)) * slot_size; };
+            auto last_one = [&](unsigned* count, int of) {       // whether this CTA is the last of `of` to arrive
                 __threadfence();
-            }
-            __syncthreads();
-            if (order == (unsigned)(c1 - c0)) {
-                if (tid == 0) p.arrived[c0] = 0;
-                for (int e = tid; e < rows * p.D; e += kThreads) {
-                    const int r = e / p.D, d = e - r * p.D;
-                    // c0's slot is its odd one, the others' their even one
-                    float m = -INFINITY, ref_all = -INFINITY, l = 0.0f, sum_o = 0.0f;
-                    auto part = [&](int64_t c) { return p.partial + ((2 * c + (c == c0)) * kRows + r) * part_pitch; };
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        m = fmaxf(m, __ldcg(part(c)));
-                        ref_all = fmaxf(ref_all, __ldcg(part(c) + 2));
-                    }
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float* from = part(c);
-                        const float mk = __ldcg(from), lk = __ldcg(from + 1), rk = __ldcg(from + 2), ok = __ldcg(from + 4 + d);
-                        if (mk > -INFINITY || lk != 0.0f) l += lk * exp2_of(mk - m);
-                        if (rk > -INFINITY || ok != 0.0f) sum_o += ok * exp2_of(rk - ref_all);
-                    }
-                    finish(r, d, m, l, ref_all, sum_o);
+                __syncthreads();
+                if (tid == 0) {
+                    order = atomicAdd(count, 1u);
+                    if (order == (unsigned)(of - 1)) *count = 0; // for the next call
+                    __threadfence();
                 }
+                __syncthreads();
+                return order == (unsigned)(of - 1);
+            };
+            // groups of about the square root of their number
+            const int all_parts = c1 - c0 + 1;
+            int size = all_parts;
+            if (all_parts > 16)
+                for (size = 4; size * size < all_parts;) ++size;
+            const int groups = (all_parts + size - 1) / size;
+            const int mine_group = (int)(blockIdx.x - c0) / size, first = c0 + mine_group * size;
+            const int in_group = min(size, c1 - first + 1);
+            bool go = last_one(mine_group == 0 ? p.arrived + p.max_ctas + c0 : p.arrived + 2 * p.max_ctas + first, in_group);
+            if (go && groups > 1) {
+                float* const to = slot_of(first);
+                const float* const parts[2] = {to, slot_of(first + 1)};
+                // (a value of the first slot is read by the thread that writes it)
+                add_parts<ROWS>(parts, 2 * slot_size, in_group, rows, D, weight, stats,
+                                [&](int r, int d, float, float, float, float4 v) {
+                                    *reinterpret_cast<float4*>(to + r * part_pitch + 4 + d) = v;
+                                });
+                __syncthreads();
+                for (int r = tid; r < rows; r += kThreads)
+                    *reinterpret_cast<float4*>(to + r * part_pitch) =
+                        make_float4(stats[3 * r], stats[3 * r + 1], stats[3 * r + 2], 0.0f);
+                go = last_one(p.arrived + c0, groups);
+            }
+            if (go) {
+                const int step = groups > 1 ? size : 1;
+                const float* const parts[2] = {slot_of(c0), slot_of(c0 + step)};
+                add_parts<ROWS>(parts, step * 2 * slot_size, groups > 1 ? groups : in_group, rows, D, weight, stats, finish);
             }
         }
+        // the next segment's copies come after what was read and written here
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
         at = min(stop, seg_end);
     }
 }
 
-template <typename T, int NG>
-cudaError_t launch_decode(AttnParams p, DeviceState* d, cudaStream_t stream) {
-    auto kern = kv_decode_kernel<T, NG>;
-    static int per_sm[kMaxDevices] = {};             // (g_mu is held)
+template <typename T, int NG, int NR>
+cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
+    constexpr int ST = NG <= 2 ? 32 : 16, ROWS = 8 * NR;
+    auto kern = kv_decode_kernel<T, NG, NR, ST>;
+    // the ring: up to 64 KB a CTA, two stages at least and four at most; a lane reads the values of a token in NG
+    // whole 64s, of the last one past its end
+    p.side = ((ST - 1) * p.D + NG * 64 + 1023) / 1024 * 1024;
+    p.depth = (64 << 10) / (kWarps * 2 * p.side);
+    p.depth = p.depth < 2 ? 2 : p.depth > 4 ? 4 : p.depth;
+    p.copy_tokens = ST < c.page ? ST : (int)c.page;
+    const int ring = kWarps * p.depth * 2 * p.side, joined = kWarps * ROWS * (NG * 64 + 4) * 4;
+    const int smem = ring > joined ? ring : joined;
+    CUtensorMap map_k = {}, map_v = {};
+    if (c.pages > 0) {                               // (no page, no copy)
+        const int64_t rows = c.pages * c.heads * c.page * c.D / 128;
+        const int box = p.copy_tokens * p.D / 128;
+        if (make_plane_map(&map_k, c.k, false, rows, 64, 64, 1, 64, box) != EMU_OK ||
+            make_plane_map(&map_v, c.v, false, rows, 64, 64, 1, 64, box) != EMU_OK)
+            return cudaErrorInvalidValue;
+    }
+    // CTAs resident at once, by ring size (g_mu is held)
+    static int per_sm[kMaxDevices][17] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!per_sm[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NG>::bytes);
+    int& fit = per_sm[dev][p.D / 16];
+    if (!fit) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
         int n = 0;
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, Ring<NG>::bytes);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
         if (e != cudaSuccess) return e;
-        per_sm[dev] = n < 1 ? 1 : n > kKvCtasPerSm ? kKvCtasPerSm : n;
+        fit = n < 1 ? 1 : n > kKvCtasPerSm ? kKvCtasPerSm : n;
     }
-    kern<<<(unsigned)(d->sms * per_sm[dev]), kThreads, Ring<NG>::bytes, stream>>>(p);
+    kern<<<(unsigned)(d->sms * fit), kThreads, smem, stream>>>(p, map_k, map_v);
     return cudaGetLastError();
 }
 
+template <typename T, int NR>
+cudaError_t launch_rows(const AttnParams& p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
+    if (p.D <= 64) return launch_decode<T, 1, NR>(p, c, d, stream);
+    if (p.D <= 128) return launch_decode<T, 2, NR>(p, c, d, stream);
+    if (p.D <= 192) return launch_decode<T, 3, NR>(p, c, d, stream);
+    return launch_decode<T, 4, NR>(p, c, d, stream);
+}
+
 template <typename T>
-cudaError_t launch_typed(const AttnParams& p, DeviceState* d, cudaStream_t stream) {
-    if (p.D <= 64) return launch_decode<T, 1>(p, d, stream);
-    if (p.D <= 128) return launch_decode<T, 2>(p, d, stream);
-    if (p.D <= 192) return launch_decode<T, 3>(p, d, stream);
-    return launch_decode<T, 4>(p, d, stream);
+cudaError_t launch_typed(const AttnParams& p, const emu_kv_cache_t& c, int64_t max_rows, DeviceState* d, cudaStream_t stream) {
+    return max_rows <= 8 ? launch_rows<T, 1>(p, c, d, stream) : launch_rows<T, 2>(p, c, d, stream);
 }
 
 }  // namespace
@@ -606,10 +852,10 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     emu_status_t st = current_device(&d);
     if (st != EMU_OK) return st;
     // Made once, for the largest head and grid, so that no later call moves what a captured one reads.
+    const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
     if (!d->kv_ws) {
-        const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
-        const size_t flags = (ctas * sizeof(unsigned) + 255) / 256 * 256;
-        const size_t bytes = flags + 2 * ctas * kRows * (256 + 4) * sizeof(float);
+        const size_t flags = (3 * ctas * sizeof(unsigned) + 255) / 256 * 256;
+        const size_t bytes = flags + 2 * ctas * kKvRows * (256 + 4) * sizeof(float);
         void* ws = nullptr;
         if (cudaMalloc(&ws, bytes) != cudaSuccess) {
             cudaGetLastError();
@@ -638,12 +884,14 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     const int size = dtype == EMU_F32 ? 4 : 2;
     p.wide = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_t * size % 16 == 0 && p.q_h * size % 16 == 0;
     p.arrived = static_cast<unsigned*>(d->kv_ws);
+    p.max_ctas = (int)ctas;
     p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d->kv_ws) + d->kv_flags);
     p.err = d->err;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;
     cudaError_t e;
-    if (dtype == EMU_F32) e = launch_typed<float>(p, d, stream);
-    else if (dtype == EMU_BF16) e = launch_typed<__nv_bfloat16>(p, d, stream);
-    else e = launch_typed<__half>(p, d, stream);
+    if (dtype == EMU_F32) e = launch_typed<float>(p, *cache, max_rows, d, stream);
+    else if (dtype == EMU_BF16) e = launch_typed<__nv_bfloat16>(p, *cache, max_rows, d, stream);
+    else e = launch_typed<__half>(p, *cache, max_rows, d, stream);
     return from_cuda(e);
 }

@@ -104,6 +104,23 @@ def test_long_and_many(emu, type):
     _check(emu, _make([(37 * i) % 211 for i in range(700)], [1 + (i % 7 == 0) for i in range(700)], 4, 2, 64, 16, type))
 
 
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("D", list(range(16, 257, 16)))
+def test_many_steps(emu, type, D):
+    """Long enough that every stage of every ring is filled and read, and pages are looked up ahead."""
+    import torch
+    for P, G, window in ((16, 3, 0), (64, 9, 700)):
+        q, cache, table, starts, lengths = _make([2500 + 33 * i for i in range(30)], [1 + i % 2 for i in range(30)], 8 * G, 8,
+                                                 D, P, type, seed=D)
+        out = emu.emu_kv_attention(q, cache, table, _ints(starts), _ints(lengths), window=window)
+        for b in (0, 13, 29):                        # (the reference of all would take long)
+            rows = slice(starts[b], starts[b + 1])
+            want, bound = ref.attention(q[rows], *cache, table[b:b + 1], [0, starts[b + 1] - starts[b]], [lengths[b]],
+                                        D ** -0.5, window)
+            assert ref.within(out[rows], want, bound)
+        assert torch.isfinite(out).all() and _error(emu) == 0
+
+
 def test_rows_that_see_nothing(emu):
     """Length 0, fewer tokens than rows, rows behind the last sequence, no sequence."""
     import torch
