@@ -200,7 +200,260 @@ __device__ __forceinline__ void add_parts(const float* const (&part)[2], int64_t
     }
 }
 
-template <typename T, int NG, int NR, int ST>
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// What a warp of kv_decode_kernel holds of a segment, and a step of ST tokens of it.
+//
+// DT: the values of a head where they are known when this is compiled (a lane's places in a
+// tile are then the same in every tile, 16 DT bytes apart), or 0.
+template <typename T, int NG, int DT, int NR, int ST>
+struct Segment {
+    static constexpr bool TWO = sizeof(T) == 4;      // two pieces of q and of p
+    static constexpr int PIECES = TWO ? 2 : 1;
+    static constexpr int SUB = ST / 16;              // tiles of 16 tokens in a step
+    using Bl = Blocks<NG>;
+    static_assert(DT % 64 == 0, "whole rows of 1024 bytes from tile to tile");
+
+    uint32_t qb[PIECES][NR][NG * 4][2];              // the rows of the queries as FP16 pieces, 2^14 the largest value
+    float factor[NR][2];                             // of rows 8 r + 2t, + 1: scores are sums times factor times s_k, base 2
+    int pos[NR][2];                                  // and their positions
+    float o[Bl::count * 8][NR][4];                   // (of a block of 64: the first four tiles)
+    float top[NR][2], ref[NR][2], total[NR][2];      // running maxima of the scores, what o is held against, sums of p
+    uint32_t k_at[NG][2], v_at[Bl::count][4];        // where a lane's codes lie in a stage
+    int d_rt, len, window, side;
+
+    // EDGE: some row does not see some token of the step.
+    template <bool EDGE>
+    __device__ __forceinline__ void step(int tok, uint32_t kt, const float (&k_scale)[SUB], const float (&v_scale)[SUB]) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = DT ? DT : d_rt;
+        const int tau = (g >> 1) + 4 * (g & 1);      // this lane's token of S^T's rows 0..7
+        const float nan = __uint_as_float(0x7FC00000u);
+        float sc[SUB][NR][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            float other[NR][4];                  // a second chain of sums (TWO: of the low pieces)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[u][r][e] = other[r][e] = 0.0f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                if (DT) {
+                    lo = lds128(kt + k_at[gr][0] + u * 16 * DT);
+                    hi = lds128(kt + k_at[gr][1] + u * 16 * DT);
+                } else if (64 * gr + 16 * t < D) {
+                    lo = lds128(kt + swizzled((16 * u + tau) * D + 64 * gr + 16 * t));
+                    hi = lds128(kt + swizzled((16 * u + tau + 8) * D + 64 * gr + 16 * t));
+                }
+                const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a[4] = {kv_half2((uint16_t)wl[k]), kv_half2((uint16_t)wh[k]),
+                                           kv_half2((uint16_t)(wl[k] >> 16)), kv_half2((uint16_t)(wh[k] >> 16))};
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        if constexpr (TWO) {
+                            mma_f16(other[r], a, qb[PIECES - 1][r][4 * gr + k][0], qb[PIECES - 1][r][4 * gr + k][1]);
+                            mma_f16(sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
+                        } else {
+                            mma_f16(k & 1 ? other[r] : sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[u][r][e] += other[r][e];
+        }
+        // bounds of log2(s_v): its exponent and one
+        int v_exp[SUB];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) v_exp[u] = (int)((__float_as_uint(v_scale[u]) >> 23) & 0xFF) - 126;
+        uint32_t pb[PIECES][SUB][NR][2];         // P^T: rows of tokens, turned
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            float m0[2], f[SUB][2], fs[SUB][2];
+            uint32_t hidden = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float m[SUB];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    fs[u][e] = factor[r][e] * k_scale[u];
+                    float a = sc[u][r][e] * fs[u][e], c = sc[u][r][e + 2] * fs[u][e];
+                    if constexpr (EDGE) {
+                        // what a row does not see is -infinity, and has no weight below
+                        const int j = tok + 16 * u + tau, last = min(pos[r][e], len - 1);
+                        const int from = window ? pos[r][e] - window : -1;
+                        if (j > last || j <= from) a = -INFINITY, hidden |= 1u << (4 * u + e);
+                        if (j + 8 > last || j + 8 <= from) c = -INFINITY, hidden |= 1u << (4 * u + 2 + e);
+                    }
+                    m[u] = fmaxf(a, c);
+                }
+                float m_all = m[0], over = m[0] + (float)(v_exp[0] - 14);
+                bool apart = false;
+                if constexpr (SUB == 2) {
+                    m_all = fmaxf(m[0], m[1]);
+                    over = fmaxf(over, m[1] + (float)(v_exp[1] - 14));
+                    apart = v_exp[0] != v_exp[1];
+                }
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) m_all = fmaxf(m_all, __shfl_xor_sync(0xffffffffu, m_all, x));
+                if (apart) {
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, x));
+                } else {
+                    over = m_all + (float)(v_exp[0] - 14);
+                }
+                const float top_now = fmaxf(top[r][e], m_all), ref_now = fmaxf(ref[r][e], over);
+                if (top_now > top[r][e]) total[r][e] *= exp2_of(top[r][e] - top_now);
+                const bool up = ref_now > ref[r][e];
+                if (__any_sync(0xffffffffu, up)) {
+                    const float c = up ? exp2_of(ref[r][e] - ref_now) : 1.0f;
+#pragma unroll
+                    for (int n = 0; n < Bl::count * 8; ++n) {
+                        o[n][r][e] *= c;
+                        o[n][r][e + 2] *= c;
+                    }
+                }
+                top[r][e] = top_now;
+                ref[r][e] = ref_now;
+                m0[e] = top_now == -INFINITY ? 0.0f : top_now;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+                    f[u][e] = top_now == -INFINITY ? 0.0f : v_scale[u] * exp2_of(top_now - ref_now);
+            }
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float w2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // (one rounding, at the difference's size)
+                        float x = exp2_of(fmaf(sc[u][r][e + 2 * h], fs[u][e], -m0[e]));
+                        w2[e] = x * f[u][e];
+                        if (EDGE && (hidden >> (4 * u + 2 * h + e) & 1)) x = w2[e] = 0.0f;
+                        total[r][e] += x;
+                    }
+                    const uint32_t hi = half2_bits(w2[0], w2[1]);
+                    pb[0][u][r][h] = turned(hi);
+                    if constexpr (TWO) pb[PIECES - 1][u][r][h] = turned(half2_rest(w2[0], w2[1], hi));
+                }
+        }
+        // Values: of a token a lane has 16 (8) in a row of each block, of the four tokens t, t + 4, t + 8, t + 12
+        // of a tile; bytes 2j and 2j + 1 are rows g and g + 8 of the block's tile j.
+        bool nan_seen = false;
+        auto clean = [&](uint32_t& w) {
+            // A NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken out here
+            // and put into those rows below.
+            const uint32_t n = nan_bytes(w);
+            nan_seen = nan_seen || n != 0;
+            w &= ~n;
+        };
+#pragma unroll
+        for (int bl = 0; bl < Bl::count; ++bl) {
+            constexpr int WIDE = TWO ? 2 : 4;    // words of a token at a time (TWO: the step's own sums need the registers)
+            const int d0 = Bl::first(bl, g);
+#pragma unroll
+            for (int w0 = 0; w0 < Bl::tiles(bl) / 2; w0 += WIDE) {
+                const int words = min(WIDE, Bl::tiles(bl) / 2 - w0);
+                float fresh[TWO ? 2 * WIDE : 1][NR][4];      // added to o in FP32, nearest
+#pragma unroll
+                for (int j = 0; j < (TWO ? 2 * WIDE : 1); ++j)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) fresh[j][r][e] = 0.0f;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t row[4][WIDE];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // (4 w0 is 0 or 8: the half of a piece, which is not swizzled)
+                        const uint32_t from = kt + 4 * w0 + (DT ? v_at[bl][k] + u * 16 * DT
+                                                                 : swizzled((16 * u + t + 4 * k) * D + d0) + side);
+                        if (words == 4) {
+                            const uint4 x = lds128(from);
+                            row[k][0] = x.x;
+                            row[k][1] = x.y;
+                            row[k][WIDE - 2] = x.z;
+                            row[k][WIDE - 1] = x.w;
+                        } else {
+                            const uint2 x = lds64(from);
+                            row[k][0] = x.x;
+                            row[k][1] = x.y;
+                        }
+                        if (EDGE)
+#pragma unroll
+                            for (int x = 0; x < WIDE; ++x)
+                                if (x < words) clean(row[k][x]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2 * WIDE; ++j) {
+                        if (j >= 2 * words) continue;
+                        const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
+                        const uint32_t x = __byte_perm(row[0][j / 2], row[1][j / 2], sel);
+                        const uint32_t y = __byte_perm(row[2][j / 2], row[3][j / 2], sel);
+                        const uint32_t a[4] = {kv_half2((uint16_t)x), kv_half2((uint16_t)(x >> 16)), kv_half2((uint16_t)y),
+                                               kv_half2((uint16_t)(y >> 16))};
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            if constexpr (TWO) {
+                                mma_f16(fresh[j][r], a, pb[PIECES - 1][u][r][0], pb[PIECES - 1][u][r][1]);
+                                mma_f16(fresh[j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
+                            } else {
+                                mma_f16(o[bl * 8 + 2 * w0 + j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
+                            }
+                        }
+                    }
+                }
+                if constexpr (TWO)
+#pragma unroll
+                    for (int j = 0; j < 2 * WIDE; ++j)
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (j < 2 * words) o[bl * 8 + 2 * w0 + j][r][e] += fresh[j][r][e];
+            }
+        }
+        if (EDGE && __any_sync(0xffffffffu, nan_seen)) {
+            for (int x = 0; x < ST; ++x) {
+                const int j = tok + x;
+#pragma unroll
+                for (int bl = 0; bl < Bl::count; ++bl)
+#pragma unroll
+                    for (int c = 0; c < 2 * Bl::tiles(bl); ++c) {
+                        const uint32_t at4 = kt + side + swizzled(x * D + Bl::first(bl, g) + (c & ~3));
+                        uint32_t four;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(four) : "r"(at4) : "memory");
+                        if ((four >> 8 * (c & 3) & 0x7F) == 0x7F) {
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (j <= pos[r][e] && j < len && !(window && j <= pos[r][e] - window))
+                                        o[bl * 8 + c / 2][r][e + 2 * (c & 1)] = nan;
+                        }
+                    }
+            }
+        }
+    }
+};
+
+template <typename T, int NG, int DT, int NR, int ST>
 __global__ void __launch_bounds__(kThreads, NG > 2 ? 1 : NR == 1 && (NG == 1 || sizeof(T) == 2) ? 3 : 2)
 kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     constexpr bool TWO = sizeof(T) == 4;             // two pieces of q and of p
@@ -217,9 +470,9 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
     __shared__ unsigned order;
     __shared__ float weight[kGroup * ROWS], stats[ROWS * 3];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int P = 1 << p.page_log, D = p.D;
+    const int P = 1 << p.page_log, D = DT ? DT : p.D;
+    static_assert(DT % 64 == 0, "whole rows of 1024 bytes from tile to tile");
     const uint32_t ring = smem_u32(smem) + warp * p.depth * 2 * p.side;
-    uint8_t* const ring_at = smem + warp * p.depth * 2 * p.side;
     const uint32_t bar0 = smem_u32(bars[warp]);
     if (lane == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(bar0 + 8 * i, SUB);
@@ -329,27 +582,25 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
             vs = page >= 0 ? p.vs[unit] : page == -1 ? nan : 0.0f;
             if (page == -1) record_error(p.err, kDevErrValue);
         };
-        const int my_step = lane / SUB;              // of a batch
+        const int my_step = lane / SUB, my_sub = lane % SUB;     // of a batch, of a step
+        // where one copy brings both tiles, one lane has the keys', the other the values'
+        const bool joint = p.copy_tokens > 16;
         int page_now = page_of(my_step), page_next = page_of(BATCH + my_step);
         // The step's copies, by the lanes that have its tiles; each arrives once.
         auto copy_step = [&](int i, int page) {
-            if (i < steps && my_step == i % BATCH && !dead) {
-                const uint32_t bar = bar0 + 8 * stage_in, dst = ring + stage_in * 2 * p.side;
-                const int sub = SUB == 2 ? lane & 1 : 0;
-                const bool joint = p.copy_tokens > 16;           // both tiles in one copy: this lane does one side
-                const int tok = token0 + i * UNIT + (joint ? 0 : sub * 16);
-                const int64_t first = (((int64_t)max(page, 0) * p.heads + head) << p.page_log) + (tok & (P - 1));
-                const int row = (int)(first * D >> 7);
+            if (i >= steps) return;
+            if (my_step == i % BATCH && !dead) {
+                const uint32_t bar = bar0 + 8 * stage_in, dst = ring + stage_in * 2 * p.side + (joint ? 0 : my_sub * 16 * D);
+                const int tok = token0 + i * UNIT + (joint ? 0 : my_sub * 16);
+                const int row = (int)(((((int64_t)page * p.heads + head) << p.page_log) + (tok & (P - 1))) * D >> 7);
                 const uint32_t bytes = p.copy_tokens * D;
-                const bool both = !joint || SUB == 1;
-                mbar_arrive_expect_tx(bar, page >= 0 ? (both ? 2 : 1) * bytes : 0);
+                mbar_arrive_expect_tx(bar, page < 0 ? 0 : joint ? bytes : 2 * bytes);
                 if (page >= 0) {
-                    const uint32_t to = dst + (joint ? 0 : sub * 16 * D);
-                    if (both || sub == 0) tma_load_3d(to, &map_k, bar, 0, row, 0);
-                    if (both || sub == 1) tma_load_3d(to + p.side, &map_v, bar, 0, row, 0);
+                    if (!joint || my_sub == 0) tma_load_3d(dst, &map_k, bar, 0, row, 0);
+                    if (!joint || my_sub == 1) tma_load_3d(dst + p.side, &map_v, bar, 0, row, 0);
                 }
             }
-            if (i < steps) stage_in = stage_in + 1 == p.depth ? 0 : stage_in + 1;
+            stage_in = stage_in + 1 == p.depth ? 0 : stage_in + 1;
         };
         for (int i = 0; i < p.depth - 1; ++i) copy_step(i, page_now);
         float ks_now, vs_now, ks_next = 0.0f, vs_next = 0.0f;
@@ -357,9 +608,11 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
 
         // The rows of the queries as FP16 pieces: of the 64 values of a group a lane
         // holds 16 in a row, four for each K = 16 step.
-        uint32_t qb[PIECES][NR][NG * 4][2];
-        float factor[NR][2];                         // of rows 8 r + 2t, + 1: scores are sums times factor times s_k, base 2
-        int pos[NR][2];
+        Segment<T, NG, DT, NR, ST> sg;
+        sg.d_rt = D;
+        sg.len = s.len;
+        sg.window = p.window;
+        sg.side = p.side;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = min(row0 + 8 * r + g, row0 + rows - 1), i = row / p.group;
@@ -390,32 +643,38 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float lo = x[4 * k + 2 * h] * up, hi = x[4 * k + 2 * h + 1] * up;
-                    qb[0][r][k][h] = half2_bits(lo, hi);
-                    if constexpr (TWO) qb[PIECES - 1][r][k][h] = half2_rest(lo, hi, qb[0][r][k][h]);
+                    sg.qb[0][r][k][h] = half2_bits(lo, hi);
+                    if constexpr (TWO) sg.qb[PIECES - 1][r][k][h] = half2_rest(lo, hi, sg.qb[0][r][k][h]);
                 }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                factor[r][e] = __shfl_sync(0xffffffffu, mine_factor, 4 * (2 * t + e));
-                pos[r][e] = pos0 + min(row0 + 8 * r + 2 * t + e, row0 + rows - 1) / p.group;
+                sg.factor[r][e] = __shfl_sync(0xffffffffu, mine_factor, 4 * (2 * t + e));
+                sg.pos[r][e] = pos0 + min(row0 + 8 * r + 2 * t + e, row0 + rows - 1) / p.group;
             }
         }
 
-        float o[Bl::count * 8][NR][4];               // (of a block of 64: the first four tiles)
 #pragma unroll
         for (int n = 0; n < Bl::count * 8; ++n)
 #pragma unroll
             for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][r][e] = 0.0f;
-        float top[NR][2], ref[NR][2], total[NR][2];  // running maxima of the scores, what o is held against, sums of p
+                for (int e = 0; e < 4; ++e) sg.o[n][r][e] = 0.0f;
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                top[r][e] = ref[r][e] = -INFINITY;
-                total[r][e] = 0.0f;
+                sg.top[r][e] = sg.ref[r][e] = -INFINITY;
+                sg.total[r][e] = 0.0f;
             }
-        const int tau = (g >> 1) + 4 * (g & 1);      // this lane's token of S^T's rows 0..7
+        const int tau = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sg.k_at[gr][h] = swizzled((tau + 8 * h) * D + 64 * gr + 16 * t);
+#pragma unroll
+        for (int bl = 0; bl < Bl::count; ++bl)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sg.v_at[bl][k] = swizzled((t + 4 * k) * D + Bl::first(bl, g)) + p.side;
 
         for (int i = 0; i < steps; ++i) {
             const int in_batch = i % BATCH;
@@ -437,225 +696,30 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
             __syncwarp();                            // all lanes have read the stage that is filled now
             const int ahead = i + p.depth - 1;
             copy_step(ahead, ahead / BATCH == i / BATCH ? page_now : page_next);
-            const int tok = token0 + i * UNIT;
-            const uint8_t* kt = ring_at + stage_out * 2 * p.side;
-            const uint8_t* vt = kt + p.side;
-            if (++stage_out == p.depth) {
-                stage_out = 0;
-                parity ^= 1;
-            }
             float k_scale[SUB], v_scale[SUB];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 k_scale[u] = __shfl_sync(0xffffffffu, ks_now, in_batch * SUB + u);
                 v_scale[u] = __shfl_sync(0xffffffffu, vs_now, in_batch * SUB + u);
             }
-
-            float sc[SUB][NR][4];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                float other[NR][4];                  // a second chain of sums (TWO: of the low pieces)
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[u][r][e] = other[r][e] = 0.0f;
-#pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
-                    const uint32_t at0 = (16 * u + tau) * D + 64 * gr + 16 * t;
-                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                    if (64 * gr + 16 * t < D) {
-                        lo = *reinterpret_cast<const uint4*>(kt + swizzled(at0));
-                        hi = *reinterpret_cast<const uint4*>(kt + swizzled(at0 + 8 * D));
-                    }
-                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a[4] = {kv_half2((uint16_t)wl[k]), kv_half2((uint16_t)wh[k]),
-                                               kv_half2((uint16_t)(wl[k] >> 16)), kv_half2((uint16_t)(wh[k] >> 16))};
-#pragma unroll
-                        for (int r = 0; r < NR; ++r) {
-                            if constexpr (TWO) {
-                                mma_f16(other[r], a, qb[PIECES - 1][r][4 * gr + k][0], qb[PIECES - 1][r][4 * gr + k][1]);
-                                mma_f16(sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
-                            } else {
-                                mma_f16(k & 1 ? other[r] : sc[u][r], a, qb[0][r][4 * gr + k][0], qb[0][r][4 * gr + k][1]);
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[u][r][e] += other[r][e];
+            const int tok = token0 + i * UNIT;
+            const uint32_t kt = ring + stage_out * 2 * p.side;
+            if (++stage_out == p.depth) {
+                stage_out = 0;
+                parity ^= 1;
             }
-            // Whether some row does not see some token of the step
-            const bool edge = tok + ST > pos_first + 1 || tok + ST > s.len || (p.window && tok <= pos_last - p.window);
-            // bounds of log2(s_v): its exponent and one
-            int v_exp[SUB];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) v_exp[u] = (int)((__float_as_uint(v_scale[u]) >> 23) & 0xFF) - 126;
-            uint32_t pb[PIECES][SUB][NR][2];         // P^T: rows of tokens, turned
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float m0[2], f[SUB][2], fs[SUB][2];
-                uint32_t hidden = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float m[SUB];
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        fs[u][e] = factor[r][e] * k_scale[u];
-                        float a = sc[u][r][e] * fs[u][e], c = sc[u][r][e + 2] * fs[u][e];
-                        if (edge) {
-                            // what a row does not see is -infinity, and has no weight below
-                            const int j = tok + 16 * u + tau, last = min(pos[r][e], s.len - 1);
-                            const int from = p.window ? pos[r][e] - p.window : -1;
-                            if (j > last || j <= from) a = -INFINITY, hidden |= 1u << (4 * u + e);
-                            if (j + 8 > last || j + 8 <= from) c = -INFINITY, hidden |= 1u << (4 * u + 2 + e);
-                        }
-                        m[u] = fmaxf(a, c);
-                    }
-                    float m_all = m[0], over = m[0] + (float)(v_exp[0] - 14);
-                    bool apart = false;
-                    if constexpr (SUB == 2) {
-                        m_all = fmaxf(m[0], m[1]);
-                        over = fmaxf(over, m[1] + (float)(v_exp[1] - 14));
-                        apart = v_exp[0] != v_exp[1];
-                    }
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) m_all = fmaxf(m_all, __shfl_xor_sync(0xffffffffu, m_all, x));
-                    if (apart) {
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, x));
-                    } else {
-                        over = m_all + (float)(v_exp[0] - 14);
-                    }
-                    const float top_now = fmaxf(top[r][e], m_all), ref_now = fmaxf(ref[r][e], over);
-                    if (top_now > top[r][e]) total[r][e] *= exp2_of(top[r][e] - top_now);
-                    const bool up = ref_now > ref[r][e];
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float c = up ? exp2_of(ref[r][e] - ref_now) : 1.0f;
-#pragma unroll
-                        for (int n = 0; n < Bl::count * 8; ++n) {
-                            o[n][r][e] *= c;
-                            o[n][r][e + 2] *= c;
-                        }
-                    }
-                    top[r][e] = top_now;
-                    ref[r][e] = ref_now;
-                    m0[e] = top_now == -INFINITY ? 0.0f : top_now;
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u)
-                        f[u][e] = top_now == -INFINITY ? 0.0f : v_scale[u] * exp2_of(top_now - ref_now);
-                }
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float w2[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // (one rounding, at the difference's size)
-                            float x = exp2_of(fmaf(sc[u][r][e + 2 * h], fs[u][e], -m0[e]));
-                            w2[e] = x * f[u][e];
-                            if (hidden >> (4 * u + 2 * h + e) & 1) x = w2[e] = 0.0f;
-                            total[r][e] += x;
-                        }
-                        const uint32_t hi = half2_bits(w2[0], w2[1]);
-                        pb[0][u][r][h] = turned(hi);
-                        if constexpr (TWO) pb[PIECES - 1][u][r][h] = turned(half2_rest(w2[0], w2[1], hi));
-                    }
-            }
-            // Values: of a token a lane has 16 (8) in a row of each block, of the four tokens t, t + 4, t + 8, t + 12
-            // of a tile; bytes 2j and 2j + 1 are rows g and g + 8 of the block's tile j.
-            bool nan_seen = false;
-            auto clean = [&](uint32_t& w) {
-                // A NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken out here
-                // and put into those rows below.
-                const uint32_t n = nan_bytes(w);
-                nan_seen = nan_seen || n != 0;
-                w &= ~n;
-            };
-#pragma unroll
-            for (int bl = 0; bl < Bl::count; ++bl) {
-                constexpr int WIDE = TWO ? 2 : 4;    // words of a token at a time (TWO: the step's own sums need the registers)
-                const int d0 = Bl::first(bl, g);
-#pragma unroll
-                for (int w0 = 0; w0 < Bl::tiles(bl) / 2; w0 += WIDE) {
-                    const int words = min(WIDE, Bl::tiles(bl) / 2 - w0);
-                    float fresh[TWO ? 2 * WIDE : 1][NR][4];      // added to o in FP32, nearest
-#pragma unroll
-                    for (int j = 0; j < (TWO ? 2 * WIDE : 1); ++j)
-#pragma unroll
-                        for (int r = 0; r < NR; ++r)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) fresh[j][r][e] = 0.0f;
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        uint32_t row[4][WIDE];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint8_t* from = vt + swizzled((16 * u + t + 4 * k) * D + d0 + 4 * w0);
-                            if (words == 4) *reinterpret_cast<uint4*>(row[k]) = *reinterpret_cast<const uint4*>(from);
-                            else *reinterpret_cast<uint2*>(row[k]) = *reinterpret_cast<const uint2*>(from);
-                            if (edge)
-#pragma unroll
-                                for (int x = 0; x < WIDE; ++x)
-                                    if (x < words) clean(row[k][x]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2 * WIDE; ++j) {
-                            if (j >= 2 * words) continue;
-                            const uint32_t sel = j & 1 ? 0x7362 : 0x5140;
-                            const uint32_t x = __byte_perm(row[0][j / 2], row[1][j / 2], sel);
-                            const uint32_t y = __byte_perm(row[2][j / 2], row[3][j / 2], sel);
-                            const uint32_t a[4] = {kv_half2((uint16_t)x), kv_half2((uint16_t)(x >> 16)), kv_half2((uint16_t)y),
-                                                   kv_half2((uint16_t)(y >> 16))};
-#pragma unroll
-                            for (int r = 0; r < NR; ++r) {
-                                if constexpr (TWO) {
-                                    mma_f16(fresh[j][r], a, pb[PIECES - 1][u][r][0], pb[PIECES - 1][u][r][1]);
-                                    mma_f16(fresh[j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
-                                } else {
-                                    mma_f16(o[bl * 8 + 2 * w0 + j][r], a, pb[0][u][r][0], pb[0][u][r][1]);
-                                }
-                            }
-                        }
-                    }
-                    if constexpr (TWO)
-#pragma unroll
-                        for (int j = 0; j < 2 * WIDE; ++j)
-#pragma unroll
-                            for (int r = 0; r < NR; ++r)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (j < 2 * words) o[bl * 8 + 2 * w0 + j][r][e] += fresh[j][r][e];
-                }
-            }
-            if (edge && __any_sync(0xffffffffu, nan_seen)) {
-                for (int x = 0; x < ST; ++x) {
-                    const int j = tok + x;
-#pragma unroll
-                    for (int bl = 0; bl < Bl::count; ++bl)
-#pragma unroll
-                        for (int c = 0; c < 2 * Bl::tiles(bl); ++c)
-                            if ((vt[swizzled(x * D + Bl::first(bl, g) + c)] & 0x7F) == 0x7F) {
-#pragma unroll
-                                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e)
-                                        if (j <= pos[r][e] && j < s.len && !(p.window && j <= pos[r][e] - p.window))
-                                            o[bl * 8 + c / 2][r][e + 2 * (c & 1)] = nan;
-                            }
-                }
-            }
+            // (an edge: some row does not see some token of the step)
+            if (tok + ST > pos_first + 1 || tok + ST > s.len || (p.window && tok <= pos_last - p.window))
+                sg.template step<true>(tok, kt, k_scale, v_scale);
+            else
+                sg.template step<false>(tok, kt, k_scale, v_scale);
         }
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) total[r][e] += __shfl_xor_sync(0xffffffffu, total[r][e], x);
+                for (int x = 4; x < 32; x <<= 1) sg.total[r][e] += __shfl_xor_sync(0xffffffffu, sg.total[r][e], x);
         __syncthreads();                             // all rings have been read, and none has copies in flight
         // the warps' sums: [warp][row][4 + D]: maximum, sum, reference, and o
         const int pitch = NG * 64 + 4;
@@ -666,17 +730,17 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
             for (int e = 0; e < 2; ++e) {
                 float* to = joined + (warp * ROWS + 8 * r + 2 * t + e) * pitch;
                 if (g == 0) {
-                    to[0] = top[r][e];
-                    to[1] = total[r][e];
-                    to[2] = ref[r][e];
+                    to[0] = sg.top[r][e];
+                    to[1] = sg.total[r][e];
+                    to[2] = sg.ref[r][e];
                 }
 #pragma unroll
                 for (int bl = 0; bl < Bl::count; ++bl)
 #pragma unroll
                     for (int j = 0; j < Bl::tiles(bl); j += 2)
                         *reinterpret_cast<float4*>(to + 4 + Bl::first(bl, g) + 2 * j) =
-                            make_float4(o[bl * 8 + j][r][e], o[bl * 8 + j][r][e + 2], o[bl * 8 + j + 1][r][e],
-                                        o[bl * 8 + j + 1][r][e + 2]);
+                            make_float4(sg.o[bl * 8 + j][r][e], sg.o[bl * 8 + j][r][e + 2], sg.o[bl * 8 + j + 1][r][e],
+                                        sg.o[bl * 8 + j + 1][r][e + 2]);
             }
         __syncthreads();
         const bool whole = u0 == 0 && u1 == units;
@@ -774,10 +838,10 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
     }
 }
 
-template <typename T, int NG, int NR>
+template <typename T, int NG, int DT, int NR>
 cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
     constexpr int ST = NG <= 2 ? 32 : 16, ROWS = 8 * NR;
-    auto kern = kv_decode_kernel<T, NG, NR, ST>;
+    auto kern = kv_decode_kernel<T, NG, DT, NR, ST>;
     // the ring: up to 64 KB a CTA, two stages at least and four at most; a lane reads the values of a token in NG
     // whole 64s, of the last one past its end
     p.side = ((ST - 1) * p.D + NG * 64 + 1023) / 1024 * 1024;
@@ -814,10 +878,13 @@ cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, DeviceState* d,
 
 template <typename T, int NR>
 cudaError_t launch_rows(const AttnParams& p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
-    if (p.D <= 64) return launch_decode<T, 1, NR>(p, c, d, stream);
-    if (p.D <= 128) return launch_decode<T, 2, NR>(p, c, d, stream);
-    if (p.D <= 192) return launch_decode<T, 3, NR>(p, c, d, stream);
-    return launch_decode<T, 4, NR>(p, c, d, stream);
+    if (p.D == 64) return launch_decode<T, 1, 64, NR>(p, c, d, stream);
+    if (p.D == 128) return launch_decode<T, 2, 128, NR>(p, c, d, stream);
+    if (p.D == 256) return launch_decode<T, 4, 256, NR>(p, c, d, stream);
+    if (p.D < 64) return launch_decode<T, 1, 0, NR>(p, c, d, stream);
+    if (p.D < 128) return launch_decode<T, 2, 0, NR>(p, c, d, stream);
+    if (p.D <= 192) return launch_decode<T, 3, 0, NR>(p, c, d, stream);
+    return launch_decode<T, 4, 0, NR>(p, c, d, stream);
 }
 
 template <typename T>
