@@ -37,10 +37,9 @@ struct DeviceState {
     size_t part_bytes = 0;
     unsigned* flags = nullptr;
     unsigned epoch = 0;
-    // attention over 8-bit keys and values: flags (zero between calls) and then
-    // two slots of partial sums per CTA (made once, of a fixed size)
+    // attention over 8-bit keys and values: two slots of partial sums and a shared
+    // segment's description per CTA (made once, of a fixed size)
     void* kv_ws = nullptr;
-    size_t kv_flags = 0;
 };
 
 extern std::mutex g_mu;

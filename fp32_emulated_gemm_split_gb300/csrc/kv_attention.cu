@@ -20,9 +20,9 @@
 // of tokens of one sequence and key head for a segment of 8 NR rows (a key head's
 // query heads, of one token after another); the CTAs take equal consecutive ranges
 // of all units.  A range's first and last segment may be shared with neighbours:
-// their sums go to a slot in memory and the last one to arrive adds them up in
-// order (in groups first), so the result does not depend on who is last.  Within a
-// CTA each warp takes every kWarps-th step of ST tokens through a ring of its own,
+// their sums go to a slot in memory, and a second kernel adds them up in order.  (In
+// the first one, by the last CTA to arrive, the sums' code took registers from the
+// steps: 96 sequences 220 us, 192 without it.)  Within a CTA each warp takes every kWarps-th step of ST tokens through a ring of its own,
 // filled by tensor copies: no barrier but at a segment's end.
 //
 // The rows are the MMA's N, so that 8 of them fill it: S^T = K Q^T, O^T = V^T P^T,
@@ -40,11 +40,11 @@ namespace emu {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kGroup = 32;                           // parts that are added up at once, at most
 constexpr int kKvCtasPerSm = 4;                      // at most
 constexpr int kKvRows = 16;                          // rows of a segment, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
+struct Work;
 struct AttnParams {
     const void* q;
     void* out;
@@ -58,9 +58,8 @@ struct AttnParams {
     int wide;                                        // rows of q on 16 bytes
     int depth, side;                                 // stages of a warp's ring, bytes of a stage's keys (or values)
     int copy_tokens;                                 // tokens of one tensor copy
-    float* partial;                                  // [2 max ctas][kKvRows][D + 4]
-    unsigned* arrived;                               // [3][max ctas], zero between calls
-    int max_ctas;
+    float* partial;                                  // [2 ctas][kKvRows][D + 4]
+    Work* shared;                             // [ctas]: the segment that a CTA begins and others end (or units 0)
     int* err;
 };
 
@@ -144,61 +143,6 @@ struct Blocks {
         return b < whole ? 128 * b + 16 * ((g >> 1) + 4 * (g & 1)) : 128 * b + 8 * g;
     }
 };
-
-// Adds up to kGroup parts of a segment (part 0 at part[0], k at part[1] + (k - 1) step; rows of
-// D + 4: maximum, sum, reference, -, and D sums) and hands each four values to `done`, with
-// their row's maximum, sum and reference.  Called by the whole CTA; weight: [kGroup][ROWS],
-// stats: [ROWS][3] in shared memory.
-template <int ROWS, typename F>
-__device__ __forceinline__ void add_parts(const float* const (&part)[2], int64_t step, int parts, int rows, int D,
-                                          float* weight, float* stats, F&& done) {
-    const int pitch = D + 4;
-    auto at = [&](int k) { return k == 0 ? part[0] : part[1] + (k - 1) * step; };
-    for (int r = threadIdx.x >> 5; r < rows; r += kWarps) {      // a row per warp, a part per lane
-        const int k = threadIdx.x & 31;
-        const bool in = k < parts;
-        const float* f = at(k) + r * pitch;
-        const float m = in ? __ldcg(f) : -INFINITY, l = in ? __ldcg(f + 1) : 0.0f, ref = in ? __ldcg(f + 2) : -INFINITY;
-        float m_all = m, ref_all = ref;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            m_all = fmaxf(m_all, __shfl_xor_sync(0xffffffffu, m_all, o));
-            ref_all = fmaxf(ref_all, __shfl_xor_sync(0xffffffffu, ref_all, o));
-        }
-        // (a part that saw nothing has no weight; NaN stays)
-        float sum = m > -INFINITY || l != 0.0f ? l * exp2_of(m - m_all) : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        weight[k * ROWS + r] = ref > -INFINITY ? exp2_of(ref - ref_all) : 1.0f;
-        if (k == 0) {
-            stats[r * 3] = m_all;
-            stats[r * 3 + 1] = sum;
-            stats[r * 3 + 2] = ref_all;
-        }
-    }
-    __syncthreads();
-    const int quads = D / 4;
-    for (int i = threadIdx.x; i < rows * quads; i += kThreads) {
-        const int r = i / quads, d = (i - r * quads) * 4;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k0 = 0; k0 < parts; k0 += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k0 + k < parts) v[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + k) + r * pitch + 4 + d));
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k0 + k < parts) {
-                    const float x = weight[(k0 + k) * ROWS + r];
-                    o.x = fmaf(v[k].x, x, o.x);
-                    o.y = fmaf(v[k].y, x, o.y);
-                    o.z = fmaf(v[k].z, x, o.z);
-                    o.w = fmaf(v[k].w, x, o.w);
-                }
-        }
-        done(r, d, stats[r * 3], stats[r * 3 + 1], stats[r * 3 + 2], o);
-    }
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -453,9 +397,77 @@ struct Segment {
     }
 };
 
+// A CTA's way through the units, and the segment that it is at (in shared memory: both are
+// looked at between segments only).
+struct Work {
+    int64_t all, ctas;                               // units, CTAs that share them
+    int64_t at, stop;                                // the CTA's next unit, the end of its range
+    int64_t base;                                    // units of the sequences before `seq`
+    int64_t begin, end;                              // the segment's units
+    int seq, start, len, pos0;                       // sequence, its first row, its length, position of its first row
+    int head, row0, rows;                            // the segment's key head, first row of the sequence, rows
+    int token0, units;                               // of the CTA's part: first token, units
+    bool bad, starts, whole;                         // no length; the part has the segment's first unit, all of them
+};
+
+// Looks up the segment of unit w.at.
+template <int ST, int ROWS>
+__device__ __forceinline__ void find_segment(const AttnParams& p, Work& w) {
+    Seq s = seq_of(p, w.seq);
+    int64_t n = all_units<ST, ROWS>(p, s);
+    while (w.at >= w.base + n) {
+        w.base += n;
+        s = seq_of(p, ++w.seq);
+        n = all_units<ST, ROWS>(p, s);
+    }
+    w.bad = s.len < 0;
+    if (w.bad) s.len = 0;
+    w.start = s.start;
+    w.len = s.len;
+    w.pos0 = s.len - s.n;
+    const int units = units_of<ST>(p, s);
+    const int seg = (int)((w.at - w.base) / units);  // row tile * heads + head
+    w.begin = w.base + (int64_t)seg * units;
+    w.end = w.begin + units;
+    const int u0 = (int)(w.at - w.begin);
+    w.units = (int)(min(w.stop, w.end) - w.at);
+    w.starts = u0 == 0;
+    w.whole = w.units == units;
+    w.head = seg % p.heads;
+    w.row0 = seg / p.heads * ROWS;
+    w.rows = min(ROWS, s.n * p.group - w.row0);
+    w.token0 = first_token<ST>(p, s) + u0 * (ST * kWarps);
+}
+
+// Four values of a row from its sums, maximum m, sum of weights l, reference ref.
+template <typename T>
+__device__ __forceinline__ void write_row(const AttnParams& p, const Work& w, int r, int d, float m, float l, float ref, float4 v) {
+    const int row = w.row0 + r, i = row / p.group;
+    const float f = w.bad ? __uint_as_float(0x7FC00000u) : l > 0.0f || l != l ? exp2_of(ref - m) / l : 0.0f;
+    T* to = static_cast<T*>(p.out) + (w.start + i) * p.out_t + (w.head * p.group + row - i * p.group) * p.out_h + d;
+    to[0] = kv_from<T>(v.x * f);
+    to[1] = kv_from<T>(v.y * f);
+    to[2] = kv_from<T>(v.z * f);
+    to[3] = kv_from<T>(v.w * f);
+}
+// Part sums: v += x y.
+__device__ __forceinline__ void add_to(float4& v, float x, const float4& y) {
+    v.x = fmaf(y.x, x, v.x);
+    v.y = fmaf(y.y, x, v.y);
+    v.z = fmaf(y.z, x, v.z);
+    v.w = fmaf(y.w, x, v.w);
+}
+// What a part counts: of its weights' sum and of its o (one that saw nothing has no weight; NaN stays).
+__device__ __forceinline__ float weight_of(float m, float l, float m_all) {
+    return m > -INFINITY || l != 0.0f ? exp2_of(m - m_all) : 0.0f;
+}
+__device__ __forceinline__ float share_of(float ref, float ref_all) {
+    return ref > -INFINITY ? exp2_of(ref - ref_all) : 1.0f;
+}
+
 template <typename T, int NG, int DT, int NR, int ST>
 __global__ void __launch_bounds__(kThreads, NG > 2 ? 1 : NR == 1 && (NG == 1 || sizeof(T) == 2) ? 3 : 2)
-kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     constexpr bool TWO = sizeof(T) == 4;             // two pieces of q and of p
     constexpr int PIECES = TWO ? 2 : 1;
     constexpr int ROWS = 8 * NR, SUB = ST / 16;      // rows of a segment; tiles of 16 tokens in a step
@@ -465,10 +477,7 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][4];
     __shared__ int64_t warp_sum[kWarps];
-    __shared__ int64_t found_base;
-    __shared__ int found_seq;
-    __shared__ unsigned order;
-    __shared__ float weight[kGroup * ROWS], stats[ROWS * 3];
+    __shared__ Work work;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int P = 1 << p.page_log, D = DT ? DT : p.D;
     static_assert(DT % 64 == 0, "whole rows of 1024 bytes from tile to tile");
@@ -479,6 +488,7 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
         fence_mbar_init();
     }
     const float nan = __uint_as_float(0x7FC00000u);
+    griddep_launch_dependents();                     // (kv_join_kernel waits for this one's end)
 
     // all units, and where this CTA's range of them begins: a run of sequences per thread
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -503,69 +513,51 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
         if (w < warp) sum += warp_sum[w];
         all += warp_sum[w];
     }
-    // rows behind the last sequence
-    {
-        const int used = p.B > 0 ? min(max(p.starts[p.B], 0), p.T) : 0;
-        const int values = p.heads * p.group * D;
-        for (int row = used + blockIdx.x; row < p.T; row += gridDim.x)
-            for (int e = tid; e < values; e += kThreads) {
-                const int h = e / D;
-                static_cast<T*>(p.out)[row * p.out_t + h * p.out_h + (e - h * D)] = kv_from<T>(0.0f);
-            }
-    }
     // (no more CTAs than units: each has one at least)
     const int64_t ctas = min((int64_t)gridDim.x, all);
-    if (blockIdx.x >= ctas) return;
-    int64_t at = all * blockIdx.x / ctas;
-    const int64_t stop = all * (blockIdx.x + 1) / ctas;
-    int64_t before = sum - mine;
-    if (before <= at && at < sum) {
-        int b = tid * per;
-        for (;; ++b) {
-            const int64_t w = all_units<ST, ROWS>(p, seq_of(p, b));
-            if (at < before + w) break;
-            before += w;
-        }
-        found_seq = b;
-        found_base = before;
+    if (blockIdx.x >= ctas) {
+        if (tid == 0) p.shared[blockIdx.x].units = 0;
+        return;
     }
-    __syncthreads();
-    int b = found_seq;
-    int64_t base = found_base;
+    {
+        const int64_t at = all * blockIdx.x / ctas;
+        int64_t before = sum - mine;
+        if (before <= at && at < sum) {              // (one thread)
+            int b = tid * per;
+            for (;; ++b) {
+                const int64_t n = all_units<ST, ROWS>(p, seq_of(p, b));
+                if (at < before + n) break;
+                before += n;
+            }
+            work.all = all;
+            work.ctas = ctas;
+            work.at = at;
+            work.stop = all * (blockIdx.x + 1) / ctas;
+            work.base = before;
+            work.seq = b;
+            find_segment<ST, ROWS>(p, work);
+        }
+    }
     int stage_in = 0, stage_out = 0;                 // next stage to fill, to read
     uint32_t parity = 0;                             // of the stage to read, flips when the ring wraps
     bool dead = false;                               // a wait gave up: no more copies
 
-    while (at < stop) {
-        Seq s = seq_of(p, b);
-        int64_t w = all_units<ST, ROWS>(p, s);
-        while (at >= base + w) {
-            base += w;
-            s = seq_of(p, ++b);
-            w = all_units<ST, ROWS>(p, s);
-        }
-        const bool bad = s.len < 0;
-        if (bad) s.len = 0;
-        const int units = units_of<ST>(p, s);
-        const int seg = (int)((at - base) / units);  // row tile * heads + head
-        const int64_t seg_begin = base + (int64_t)seg * units, seg_end = seg_begin + units;
-        const int u0 = (int)(at - seg_begin), u1 = (int)(min(stop, seg_end) - seg_begin);
-        const int head = seg % p.heads, row0 = seg / p.heads * ROWS;
-        const int rows = min(ROWS, s.n * p.group - row0);
-        const int pos0 = s.len - s.n;                // position of the sequence's first new token
+    for (;;) {
+        __syncthreads();                             // the segment is known, the shared memory of the one before read
+        const int len = work.len, pos0 = work.pos0, head = work.head, row0 = work.row0, rows = work.rows, start = work.start;
         // tokens that some row of the segment sees; steps of this warp that have any
         const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
-        const int sees_end = max(0, min(s.len, pos_last + 1));
+        const int sees_end = max(0, min(len, pos_last + 1));
         const int sees_begin = p.window ? max(0, pos_first - p.window + 1) : 0;
-        int token0 = first_token<ST>(p, s) + u0 * UNIT + warp * ST;
-        int steps = u1 - u0;
+        int token0 = work.token0 + warp * ST;
+        int steps = work.units;
         if (token0 + ST <= sees_begin) {
             const int skip = (sees_begin - token0 - ST) / UNIT + 1;
             token0 += skip * UNIT;
             steps -= skip;
         }
         steps = sees_end <= token0 ? 0 : min(steps, (sees_end - token0 + UNIT - 1) / UNIT);
-        const int32_t* pages = p.table + (int64_t)b * p.width;
+        const int32_t* pages = p.table + (int64_t)work.seq * p.width;
 
         // A lane has one tile of each of BATCH steps: the page (-1: bad, -2: no row sees the tile) and its scales.
         auto page_of = [&](int i) {
@@ -610,13 +602,13 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
         // holds 16 in a row, four for each K = 16 step.
         Segment<T, NG, DT, NR, ST> sg;
         sg.d_rt = D;
-        sg.len = s.len;
+        sg.len = len;
         sg.window = p.window;
         sg.side = p.side;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = min(row0 + 8 * r + g, row0 + rows - 1), i = row / p.group;
-            const T* from = static_cast<const T*>(p.q) + (s.start + i) * p.q_t + (head * p.group + row - i * p.group) * p.q_h;
+            const T* from = static_cast<const T*>(p.q) + (start + i) * p.q_t + (head * p.group + row - i * p.group) * p.q_h;
             float x[NG * 16];
             float top = 0.0f;
 #pragma unroll
@@ -709,7 +701,7 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
                 parity ^= 1;
             }
             // (an edge: some row does not see some token of the step)
-            if (tok + ST > pos_first + 1 || tok + ST > s.len || (p.window && tok <= pos_last - p.window))
+            if (tok + ST > pos_first + 1 || tok + ST > len || (p.window && tok <= pos_last - p.window))
                 sg.template step<true>(tok, kt, k_scale, v_scale);
             else
                 sg.template step<false>(tok, kt, k_scale, v_scale);
@@ -743,19 +735,9 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
                                         sg.o[bl * 8 + j + 1][r][e + 2]);
             }
         __syncthreads();
-        const bool whole = u0 == 0 && u1 == units;
-        auto finish = [&](int r, int d, float m, float l, float ref_all, float4 v) {
-            const int row = row0 + r, i = row / p.group;
-            const float f = l > 0.0f || l != l ? exp2_of(ref_all - m) / l : 0.0f;
-            float y[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
-            T* to = static_cast<T*>(p.out) + (s.start + i) * p.out_t + (head * p.group + row - i * p.group) * p.out_h + d;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[e] = kv_from<T>(bad ? nan : y[e]);
-        };
-        const int part_pitch = D + 4;
-        const int64_t slot_size = (int64_t)kKvRows * part_pitch;
-        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + (u0 == 0)) * slot_size;
-        const int quads = D / 4;
+        // the warps' sums added up: the rows, or this CTA's part of a segment that it shares
+        const int quads = D / 4, part_pitch = D + 4;
+        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + work.starts) * (kKvRows * part_pitch);
         for (int i = tid; i < rows * quads; i += kThreads) {
             const int r = i / quads, d = (i - r * quads) * 4;
             const float* from = joined + r * pitch;
@@ -769,77 +751,152 @@ kv_decode_kernel(const AttnParams p, const __grid_constant__ CUtensorMap map_k, 
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 const float* f = from + k * ROWS * pitch;
-                // (a warp that saw nothing has no weight; NaN stays)
-                if (f[0] > -INFINITY || f[1] != 0.0f) l += f[1] * exp2_of(f[0] - m);
-                const float x = f[2] > -INFINITY ? exp2_of(f[2] - ref_all) : 1.0f;
-                const float4 y = *reinterpret_cast<const float4*>(f + 4 + d);
-                v.x = fmaf(y.x, x, v.x);
-                v.y = fmaf(y.y, x, v.y);
-                v.z = fmaf(y.z, x, v.z);
-                v.w = fmaf(y.w, x, v.w);
+                l += f[1] * weight_of(f[0], f[1], m);
+                add_to(v, share_of(f[2], ref_all), *reinterpret_cast<const float4*>(f + 4 + d));
             }
-            if (whole) {
-                finish(r, d, m, l, ref_all, v);
+            if (work.whole) {
+                write_row<T>(p, work, r, d, m, l, ref_all, v);
             } else {
                 float* to = slot + r * part_pitch;
                 *reinterpret_cast<float4*>(to + 4 + d) = v;
                 if (d == 0) *reinterpret_cast<float4*>(to) = make_float4(m, l, ref_all, 0.0f);
             }
         }
-        if (!whole) {
-            // CTAs that share the segment: c0, whose part is its range's last, to c1.  c0's slot is its odd
-            // one, the others' their even one.
-            const int c0 = (int)(((seg_begin + 1) * ctas - 1) / all), c1 = (int)((seg_end * ctas - 1) / all);
-            auto slot_of = [&](int c) { return p.partial + (2 * (int64_t)c + (c == c0)) * slot_size; };
-            auto last_one = [&](unsigned* count, int of) {       // whether this CTA is the last of `of` to arrive
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) {
-                    order = atomicAdd(count, 1u);
-                    if (order == (unsigned)(of - 1)) *count = 0; // for the next call
-                    __threadfence();
-                }
-                __syncthreads();
-                return order == (unsigned)(of - 1);
-            };
-            // groups of about the square root of their number
-            const int all_parts = c1 - c0 + 1;
-            int size = all_parts;
-            if (all_parts > 16)
-                for (size = 4; size * size < all_parts;) ++size;
-            const int groups = (all_parts + size - 1) / size;
-            const int mine_group = (int)(blockIdx.x - c0) / size, first = c0 + mine_group * size;
-            const int in_group = min(size, c1 - first + 1);
-            bool go = last_one(mine_group == 0 ? p.arrived + p.max_ctas + c0 : p.arrived + 2 * p.max_ctas + first, in_group);
-            if (go && groups > 1) {
-                float* const to = slot_of(first);
-                const float* const parts[2] = {to, slot_of(first + 1)};
-                // (a value of the first slot is read by the thread that writes it)
-                add_parts<ROWS>(parts, 2 * slot_size, in_group, rows, D, weight, stats,
-                                [&](int r, int d, float, float, float, float4 v) {
-                                    *reinterpret_cast<float4*>(to + r * part_pitch + 4 + d) = v;
-                                });
-                __syncthreads();
-                for (int r = tid; r < rows; r += kThreads)
-                    *reinterpret_cast<float4*>(to + r * part_pitch) =
-                        make_float4(stats[3 * r], stats[3 * r + 1], stats[3 * r + 2], 0.0f);
-                go = last_one(p.arrived + c0, groups);
-            }
-            if (go) {
-                const int step = groups > 1 ? size : 1;
-                const float* const parts[2] = {slot_of(c0), slot_of(c0 + step)};
-                add_parts<ROWS>(parts, step * 2 * slot_size, groups > 1 ? groups : in_group, rows, D, weight, stats, finish);
-            }
-        }
         // the next segment's copies come after what was read and written here
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
-        at = min(stop, seg_end);
+        if (work.end >= work.stop) break;
+        __syncthreads();
+        if (tid == 0) {
+            work.at = work.end;
+            find_segment<ST, ROWS>(p, work);
+        }
+    }
+    // a segment that begins here and is shared is added up by kv_join_kernel
+    if (tid == 0) {
+        if (work.whole || !work.starts) work.units = 0;
+        p.shared[blockIdx.x] = work;
+    }
+}
+
+// What parts of a segment's row add up to: a lane has four values of o, of more than 128 eight.
+struct RowSum {
+    float m, l, ref;
+    float4 v[2];
+    __device__ __forceinline__ void clear() {
+        m = ref = -INFINITY;
+        l = 0.0f;
+        v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    // Holds the sums against a maximum and a reference at least as large.
+    __device__ __forceinline__ void lift(float m_new, float ref_new) {
+        l *= weight_of(m, l, m_new);
+        const float x = share_of(ref, ref_new);
+        m = m_new;
+        ref = ref_new;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 o = v[h];
+            v[h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            add_to(v[h], x, o);
+        }
+    }
+};
+
+// Adds the parts of the segments that CTAs share up in order, and the rows behind the last
+// sequence become zero.  Block (x, y): the segment that CTA x began; where it has few parts
+// (most do: two or three), its rows kJoinWarps y on, a warp each; where it has many, its rows
+// y, y + gridDim.y and so on, the parts dealt to the warps.
+constexpr int kJoinWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ float4 sums[kJoinWarps][64];
+    __shared__ float stat[kJoinWarps][3];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D, c0 = blockIdx.x;
+    griddep_wait();
+    {
+        const int used = p.B > 0 ? min(max(p.starts[p.B], 0), p.T) : 0, values = p.heads * p.group * D;
+        for (int row = used + blockIdx.x + blockIdx.y * gridDim.x; row < p.T; row += gridDim.x * gridDim.y)
+            for (int e = tid; e < values; e += kJoinWarps * 32) {
+                const int h = e / D;
+                static_cast<T*>(p.out)[row * p.out_t + h * p.out_h + (e - h * D)] = kv_from<T>(0.0f);
+            }
+    }
+    const Work& w = p.shared[c0];
+    if (w.units == 0) return;
+    // from c0's part, its odd slot, to that of the segment's last unit; theirs are the even ones
+    const int parts = (int)((w.end * w.ctas - 1) / w.all) - c0 + 1;
+    const int pitch = D + 4, d0 = lane * 4;
+    auto add_row = [&](RowSum& s, int r, int first, int step) {
+        s.clear();
+        auto at = [&](int k) { return p.partial + ((2 * ((int64_t)c0 + k) + (k == 0)) * kKvRows + r) * pitch; };
+        for (int k0 = first; k0 < parts; k0 += 4 * step) {
+            float4 head[4], x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + i * step;
+                const float* from = at(min(k, parts - 1));
+                head[i] = *reinterpret_cast<const float4*>(from);
+                x[i] = *reinterpret_cast<const float4*>(from + 4 + min(d0, D - 4));
+                if (D > 128) y[i] = *reinterpret_cast<const float4*>(from + 4 + min(128 + d0, D - 4));
+            }
+            float m = s.m, ref = s.ref;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {            // (the last part twice changes no maximum)
+                m = fmaxf(m, head[i].x);
+                ref = fmaxf(ref, head[i].z);
+            }
+            s.lift(m, ref);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k0 + i * step < parts) {
+                    s.l += head[i].y * weight_of(head[i].x, head[i].y, m);
+                    const float share = share_of(head[i].z, ref);
+                    add_to(s.v[0], share, x[i]);
+                    if (D > 128) add_to(s.v[1], share, y[i]);
+                }
+        }
+    };
+    RowSum s;
+    if (parts <= 16) {
+        const int r = blockIdx.y * kJoinWarps + warp;
+        if (r >= w.rows) return;
+        add_row(s, r, 0, 1);
+        if (d0 < D) write_row<T>(p, w, r, d0, s.m, s.l, s.ref, s.v[0]);
+        if (128 + d0 < D) write_row<T>(p, w, r, 128 + d0, s.m, s.l, s.ref, s.v[1]);
+        return;
+    }
+    for (int r = blockIdx.y; r < w.rows; r += gridDim.y) {
+        add_row(s, r, warp, kJoinWarps);
+        if (lane == 0) {
+            stat[warp][0] = s.m;
+            stat[warp][1] = s.l;
+            stat[warp][2] = s.ref;
+        }
+        sums[warp][lane] = s.v[0];
+        sums[warp][lane + 32] = s.v[1];
+        __syncthreads();
+        if (tid * 4 < D) {
+            float m = -INFINITY, ref = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                m = fmaxf(m, stat[k][0]);
+                ref = fmaxf(ref, stat[k][2]);
+            }
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                l += stat[k][1] * weight_of(stat[k][0], stat[k][1], m);
+                add_to(o, share_of(stat[k][2], ref), sums[k][tid]);
+            }
+            write_row<T>(p, w, r, tid * 4, m, l, ref, o);
+        }
+        __syncthreads();
     }
 }
 
 template <typename T, int NG, int DT, int NR>
-cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
+cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, int64_t max_rows, DeviceState* d, cudaStream_t stream) {
     constexpr int ST = NG <= 2 ? 32 : 16, ROWS = 8 * NR;
     auto kern = kv_decode_kernel<T, NG, DT, NR, ST>;
     // the ring: up to 64 KB a CTA, two stages at least and four at most; a lane reads the values of a token in NG
@@ -872,24 +929,36 @@ cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, DeviceState* d,
         if (e != cudaSuccess) return e;
         fit = n < 1 ? 1 : n > kKvCtasPerSm ? kKvCtasPerSm : n;
     }
-    kern<<<(unsigned)(d->sms * fit), kThreads, smem, stream>>>(p, map_k, map_v);
-    return cudaGetLastError();
+    const unsigned ctas = (unsigned)(d->sms * fit);
+    kern<<<ctas, kThreads, smem, stream>>>(p, map_k, map_v);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t how = {};
+    how.gridDim = dim3(ctas, max_rows < ROWS ? (unsigned)max_rows : ROWS);
+    how.blockDim = dim3(kJoinWarps * 32);
+    how.stream = stream;
+    cudaLaunchAttribute dependent = {};
+    dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dependent.val.programmaticStreamSerializationAllowed = 1;
+    how.attrs = &dependent;
+    how.numAttrs = 1;
+    return cudaLaunchKernelEx(&how, kv_join_kernel<T>, p);
 }
 
 template <typename T, int NR>
-cudaError_t launch_rows(const AttnParams& p, const emu_kv_cache_t& c, DeviceState* d, cudaStream_t stream) {
-    if (p.D == 64) return launch_decode<T, 1, 64, NR>(p, c, d, stream);
-    if (p.D == 128) return launch_decode<T, 2, 128, NR>(p, c, d, stream);
-    if (p.D == 256) return launch_decode<T, 4, 256, NR>(p, c, d, stream);
-    if (p.D < 64) return launch_decode<T, 1, 0, NR>(p, c, d, stream);
-    if (p.D < 128) return launch_decode<T, 2, 0, NR>(p, c, d, stream);
-    if (p.D <= 192) return launch_decode<T, 3, 0, NR>(p, c, d, stream);
-    return launch_decode<T, 4, 0, NR>(p, c, d, stream);
+cudaError_t launch_rows(const AttnParams& p, const emu_kv_cache_t& c, int64_t max_rows, DeviceState* d, cudaStream_t stream) {
+    if (p.D == 64) return launch_decode<T, 1, 64, NR>(p, c, max_rows, d, stream);
+    if (p.D == 128) return launch_decode<T, 2, 128, NR>(p, c, max_rows, d, stream);
+    if (p.D == 256) return launch_decode<T, 4, 256, NR>(p, c, max_rows, d, stream);
+    if (p.D < 64) return launch_decode<T, 1, 0, NR>(p, c, max_rows, d, stream);
+    if (p.D < 128) return launch_decode<T, 2, 0, NR>(p, c, max_rows, d, stream);
+    if (p.D <= 192) return launch_decode<T, 3, 0, NR>(p, c, max_rows, d, stream);
+    return launch_decode<T, 4, 0, NR>(p, c, max_rows, d, stream);
 }
 
 template <typename T>
 cudaError_t launch_typed(const AttnParams& p, const emu_kv_cache_t& c, int64_t max_rows, DeviceState* d, cudaStream_t stream) {
-    return max_rows <= 8 ? launch_rows<T, 1>(p, c, d, stream) : launch_rows<T, 2>(p, c, d, stream);
+    return max_rows <= 8 ? launch_rows<T, 1>(p, c, max_rows, d, stream) : launch_rows<T, 2>(p, c, max_rows, d, stream);
 }
 
 }  // namespace
@@ -919,23 +988,11 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     emu_status_t st = current_device(&d);
     if (st != EMU_OK) return st;
     // Made once, for the largest head and grid, so that no later call moves what a captured one reads.
-    const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
-    if (!d->kv_ws) {
-        const size_t flags = (3 * ctas * sizeof(unsigned) + 255) / 256 * 256;
-        const size_t bytes = flags + 2 * ctas * kKvRows * (256 + 4) * sizeof(float);
-        void* ws = nullptr;
-        if (cudaMalloc(&ws, bytes) != cudaSuccess) {
-            cudaGetLastError();
-            return EMU_ERR_ALLOC;
-        }
-        cudaError_t e = cudaMemset(ws, 0, flags);
-        if (e == cudaSuccess) e = cudaDeviceSynchronize();       // whatever stream the calls are on
-        if (e != cudaSuccess) {
-            cudaFree(ws);
-            return from_cuda(e);
-        }
-        d->kv_ws = ws;
-        d->kv_flags = flags;
+    const size_t ctas = (size_t)d->sms * kKvCtasPerSm, slots = 2 * ctas * kKvRows * (256 + 4) * sizeof(float);
+    if (!d->kv_ws && cudaMalloc(&d->kv_ws, slots + ctas * sizeof(Work)) != cudaSuccess) {
+        cudaGetLastError();
+        d->kv_ws = nullptr;
+        return EMU_ERR_ALLOC;
     }
     AttnParams p = {};
     p.q = q->data; p.q_t = q->token_stride; p.q_h = q->head_stride;
@@ -950,9 +1007,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     p.scale = scale;
     const int size = dtype == EMU_F32 ? 4 : 2;
     p.wide = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_t * size % 16 == 0 && p.q_h * size % 16 == 0;
-    p.arrived = static_cast<unsigned*>(d->kv_ws);
-    p.max_ctas = (int)ctas;
-    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d->kv_ws) + d->kv_flags);
+    p.partial = static_cast<float*>(d->kv_ws);
+    p.shared = reinterpret_cast<Work*>(static_cast<uint8_t*>(d->kv_ws) + slots);
     p.err = d->err;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;
