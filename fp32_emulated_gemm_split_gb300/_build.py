@@ -25,8 +25,8 @@ LIB_NAME = f"libemusgemm.{platform.machine()}.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
 SOURCES = ["emu_sgemm.cu", "split.cu", "gemm_kblock.cu", "gemm_simt.cu", "noalloc.cu", "chooser.cu",
-           "gated.cu", "gemm_few.cu", "lora.cu", "qk_norm.cu", "kv_cache.cu", "kv_attention.cu"]
-HEADERS = ["emu_device.cuh", "emu_host.h", "emu_internal.h", "gated.cuh", "kv_cache.cuh", "schedule.h"]
+           "gated.cu", "gemm_few.cu", "lora.cu", "qk_norm.cu", "kv_cache.cu", "kv_attention.cu", "kv_prompt.cu"]
+HEADERS = ["emu_device.cuh", "emu_host.h", "emu_internal.h", "gated.cuh", "kv_cache.cuh", "kv_attention.cuh", "schedule.h"]
 
 
 def _torch_version():

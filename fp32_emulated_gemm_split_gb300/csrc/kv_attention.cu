@@ -31,52 +31,16 @@
 // a lane reads 16 bytes at a time and no two lanes of a phase the same banks:
 // token t(g) = (g >> 1) + 4 (g & 1) is row g of S^T, piece (g >> 1) + 4 (g & 1) of 16
 // values of V belongs to rows g and g + 8 of O^T.
-#include "emu_device.cuh"
-#include "emu_host.h"
-#include "emu_layers.h"
-#include "kv_cache.cuh"
+#include "kv_attention.cuh"
+
+#include <type_traits>
 
 namespace emu {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKvCtasPerSm = 4;                      // at most
-constexpr int kKvRows = 16;                          // rows of a segment, at most
-constexpr float kLog2e = 1.4426950408889634f;
 
-struct Work;
-struct AttnParams {
-    const void* q;
-    void* out;
-    int64_t q_t, q_h, out_t, out_h;
-    int T, heads, group, D, page_log, B, width, window;
-    const uint8_t *k, *v;
-    const float *ks, *vs;
-    int64_t pages;
-    const int32_t *table, *starts, *lengths;
-    float scale;
-    int wide;                                        // rows of q on 16 bytes
-    int depth, side;                                 // stages of a warp's ring, bytes of a stage's keys (or values)
-    int copy_tokens;                                 // tokens of one tensor copy
-    float* partial;                                  // [2 ctas][kKvRows][D + 4]
-    Work* shared;                             // [ctas]: the segment that a CTA begins and others end (or units 0)
-    int* err;
-};
-
-// A sequence of the batch: its rows (none where `starts` is not in order), and its
-// length, -1 where that is out of range.
-struct Seq {
-    int start, n, len;
-};
-__device__ __forceinline__ Seq seq_of(const AttnParams& p, int b) {
-    Seq s;
-    s.start = p.starts[b];
-    const int end = p.starts[b + 1];
-    s.n = s.start >= 0 && end >= s.start && end <= p.T ? end - s.start : 0;
-    s.len = p.lengths[b];
-    if (s.len < 0 || s.len > (int64_t)p.width << p.page_log) s.len = -1;
-    return s;
-}
 // Steps start on multiples of ST tokens; the first one that any row of the sequence sees.
 template <int ST>
 __device__ __forceinline__ int first_token(const AttnParams& p, const Seq& s) {
@@ -94,12 +58,6 @@ __device__ __forceinline__ int64_t all_units(const AttnParams& p, const Seq& s) 
     return (rows + ROWS - 1) / ROWS * p.heads * units_of<ST>(p, s);
 }
 
-__device__ __forceinline__ float exp2_of(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -110,22 +68,6 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// (lo, hi) minus its FP16 rounding h
-__device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t h) {
-    float a, b;
-    kv_widen<__half>(h, a, b);
-    return half2_bits(lo - a, hi - b);
-}
-
-// Of four codes: the bytes that are NaN (0x7F, 0xFF), all bits set.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return ((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
 }
 
 // Where byte o of a run of codes lies in shared memory: rows of 128 bytes, their
@@ -220,10 +162,10 @@ struct Segment {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[u][r][e] += other[r][e];
         }
-        // bounds of log2(s_v): its exponent and one
+        // bounds of log2(s_v), its exponent and one, less 14: p s_v has 14 bits above 1 in FP16
         int v_exp[SUB];
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) v_exp[u] = (int)((__float_as_uint(v_scale[u]) >> 23) & 0xFF) - 126;
+        for (int u = 0; u < SUB; ++u) v_exp[u] = scale_bound(v_scale[u]);
         uint32_t pb[PIECES][SUB][NR][2];         // P^T: rows of tokens, turned
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -245,11 +187,11 @@ struct Segment {
                     }
                     m[u] = fmaxf(a, c);
                 }
-                float m_all = m[0], over = m[0] + (float)(v_exp[0] - 14);
+                float m_all = m[0], over = m[0] + (float)v_exp[0];
                 bool apart = false;
                 if constexpr (SUB == 2) {
                     m_all = fmaxf(m[0], m[1]);
-                    over = fmaxf(over, m[1] + (float)(v_exp[1] - 14));
+                    over = fmaxf(over, m[1] + (float)v_exp[1]);
                     apart = v_exp[0] != v_exp[1];
                 }
 #pragma unroll
@@ -258,7 +200,7 @@ struct Segment {
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, x));
                 } else {
-                    over = m_all + (float)(v_exp[0] - 14);
+                    over = m_all + (float)v_exp[0];
                 }
                 const float top_now = fmaxf(top[r][e], m_all), ref_now = fmaxf(ref[r][e], over);
                 if (top_now > top[r][e]) total[r][e] *= exp2_of(top[r][e] - top_now);
@@ -397,19 +339,6 @@ struct Segment {
     }
 };
 
-// A CTA's way through the units, and the segment that it is at (in shared memory: both are
-// looked at between segments only).
-struct Work {
-    int64_t all, ctas;                               // units, CTAs that share them
-    int64_t at, stop;                                // the CTA's next unit, the end of its range
-    int64_t base;                                    // units of the sequences before `seq`
-    int64_t begin, end;                              // the segment's units
-    int seq, start, len, pos0;                       // sequence, its first row, its length, position of its first row
-    int head, row0, rows;                            // the segment's key head, first row of the sequence, rows
-    int token0, units;                               // of the CTA's part: first token, units
-    bool bad, starts, whole;                         // no length; the part has the segment's first unit, all of them
-};
-
 // Looks up the segment of unit w.at.
 template <int ST, int ROWS>
 __device__ __forceinline__ void find_segment(const AttnParams& p, Work& w) {
@@ -437,32 +366,6 @@ __device__ __forceinline__ void find_segment(const AttnParams& p, Work& w) {
     w.row0 = seg / p.heads * ROWS;
     w.rows = min(ROWS, s.n * p.group - w.row0);
     w.token0 = first_token<ST>(p, s) + u0 * (ST * kWarps);
-}
-
-// Four values of a row from its sums, maximum m, sum of weights l, reference ref.
-template <typename T>
-__device__ __forceinline__ void write_row(const AttnParams& p, const Work& w, int r, int d, float m, float l, float ref, float4 v) {
-    const int row = w.row0 + r, i = row / p.group;
-    const float f = w.bad ? __uint_as_float(0x7FC00000u) : l > 0.0f || l != l ? exp2_of(ref - m) / l : 0.0f;
-    T* to = static_cast<T*>(p.out) + (w.start + i) * p.out_t + (w.head * p.group + row - i * p.group) * p.out_h + d;
-    to[0] = kv_from<T>(v.x * f);
-    to[1] = kv_from<T>(v.y * f);
-    to[2] = kv_from<T>(v.z * f);
-    to[3] = kv_from<T>(v.w * f);
-}
-// Part sums: v += x y.
-__device__ __forceinline__ void add_to(float4& v, float x, const float4& y) {
-    v.x = fmaf(y.x, x, v.x);
-    v.y = fmaf(y.y, x, v.y);
-    v.z = fmaf(y.z, x, v.z);
-    v.w = fmaf(y.w, x, v.w);
-}
-// What a part counts: of its weights' sum and of its o (one that saw nothing has no weight; NaN stays).
-__device__ __forceinline__ float weight_of(float m, float l, float m_all) {
-    return m > -INFINITY || l != 0.0f ? exp2_of(m - m_all) : 0.0f;
-}
-__device__ __forceinline__ float share_of(float ref, float ref_all) {
-    return ref > -INFINITY ? exp2_of(ref - ref_all) : 1.0f;
 }
 
 template <typename T, int NG, int DT, int NR, int ST>
@@ -737,7 +640,7 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         __syncthreads();
         // the warps' sums added up: the rows, or this CTA's part of a segment that it shares
         const int quads = D / 4, part_pitch = D + 4;
-        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + work.starts) * (kKvRows * part_pitch);
+        float* const slot = p.partial + (2 * (int64_t)blockIdx.x + work.starts) * (p.slot_rows * part_pitch);
         for (int i = tid; i < rows * quads; i += kThreads) {
             const int r = i / quads, d = (i - r * quads) * 4;
             const float* from = joined + r * pitch;
@@ -829,7 +732,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_c
     const int pitch = D + 4, d0 = lane * 4;
     auto add_row = [&](RowSum& s, int r, int first, int step) {
         s.clear();
-        auto at = [&](int k) { return p.partial + ((2 * ((int64_t)c0 + k) + (k == 0)) * kKvRows + r) * pitch; };
+        auto at = [&](int k) { return p.partial + ((2 * ((int64_t)c0 + k) + (k == 0)) * p.slot_rows + r) * pitch; };
         for (int k0 = first; k0 < parts; k0 += 4 * step) {
             float4 head[4], x[4], y[4];
 #pragma unroll
@@ -929,20 +832,13 @@ cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, int64_t max_row
         if (e != cudaSuccess) return e;
         fit = n < 1 ? 1 : n > kKvCtasPerSm ? kKvCtasPerSm : n;
     }
+    p.slot_rows = ROWS;
     const unsigned ctas = (unsigned)(d->sms * fit);
     kern<<<ctas, kThreads, smem, stream>>>(p, map_k, map_v);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t how = {};
-    how.gridDim = dim3(ctas, max_rows < ROWS ? (unsigned)max_rows : ROWS);
-    how.blockDim = dim3(kJoinWarps * 32);
-    how.stream = stream;
-    cudaLaunchAttribute dependent = {};
-    dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    dependent.val.programmaticStreamSerializationAllowed = 1;
-    how.attrs = &dependent;
-    how.numAttrs = 1;
-    return cudaLaunchKernelEx(&how, kv_join_kernel<T>, p);
+    const int dtype = sizeof(T) == 4 ? EMU_F32 : std::is_same<T, __half>::value ? EMU_F16 : EMU_BF16;
+    return launch_join(dtype, p, ctas, max_rows < ROWS ? (unsigned)max_rows : ROWS, stream);
 }
 
 template <typename T, int NR>
@@ -957,11 +853,32 @@ cudaError_t launch_rows(const AttnParams& p, const emu_kv_cache_t& c, int64_t ma
 }
 
 template <typename T>
+cudaError_t launch_join_typed(const AttnParams& p, unsigned ctas, unsigned rows, cudaStream_t stream) {
+    cudaLaunchConfig_t how = {};
+    how.gridDim = dim3(ctas, rows);
+    how.blockDim = dim3(kJoinWarps * 32);
+    how.stream = stream;
+    cudaLaunchAttribute dependent = {};
+    dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dependent.val.programmaticStreamSerializationAllowed = 1;
+    how.attrs = &dependent;
+    how.numAttrs = 1;
+    return cudaLaunchKernelEx(&how, kv_join_kernel<T>, p);
+}
+
+template <typename T>
 cudaError_t launch_typed(const AttnParams& p, const emu_kv_cache_t& c, int64_t max_rows, DeviceState* d, cudaStream_t stream) {
     return max_rows <= 8 ? launch_rows<T, 1>(p, c, max_rows, d, stream) : launch_rows<T, 2>(p, c, max_rows, d, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_join(int dtype, const AttnParams& p, unsigned ctas, unsigned rows, cudaStream_t stream) {
+    if (dtype == EMU_F32) return launch_join_typed<float>(p, ctas, rows, stream);
+    if (dtype == EMU_BF16) return launch_join_typed<__nv_bfloat16>(p, ctas, rows, stream);
+    return launch_join_typed<__half>(p, ctas, rows, stream);
+}
+
 }  // namespace emu
 
 using namespace emu;
@@ -982,13 +899,16 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
             (T > 0 && !h->data))
             return EMU_ERR_INVALID_VALUE;
     if (T > 0 && B > 0 && (!starts || !lengths || (width > 0 && !table))) return EMU_ERR_INVALID_VALUE;
+    if (T * (q->heads / cache->heads) > INT32_MAX - 256) return EMU_ERR_INVALID_VALUE;
     if (T == 0) return EMU_OK;
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState* d = nullptr;
     emu_status_t st = current_device(&d);
     if (st != EMU_OK) return st;
     // Made once, for the largest head and grid, so that no later call moves what a captured one reads.
-    const size_t ctas = (size_t)d->sms * kKvCtasPerSm, slots = 2 * ctas * kKvRows * (256 + 4) * sizeof(float);
+    const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
+    const size_t few = 2 * ctas * 16 * (256 + 4) * sizeof(float), many = 2 * (size_t)d->sms * kKvSlotRows * (128 + 4) * sizeof(float);
+    const size_t slots = few > many ? few : many;
     if (!d->kv_ws && cudaMalloc(&d->kv_ws, slots + ctas * sizeof(Work)) != cudaSuccess) {
         cudaGetLastError();
         d->kv_ws = nullptr;
@@ -1013,7 +933,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;
     cudaError_t e;
-    if (dtype == EMU_F32) e = launch_typed<float>(p, *cache, max_rows, d, stream);
+    if (max_rows > 16 && p.D <= 128) e = launch_prompt(dtype, p, d->sms, stream);
+    else if (dtype == EMU_F32) e = launch_typed<float>(p, *cache, max_rows, d, stream);
     else if (dtype == EMU_BF16) e = launch_typed<__nv_bfloat16>(p, *cache, max_rows, d, stream);
     else e = launch_typed<__half>(p, *cache, max_rows, d, stream);
     return from_cuda(e);

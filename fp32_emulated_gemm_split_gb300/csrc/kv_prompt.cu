@@ -1,0 +1,693 @@
+// kv_prompt.cu -- the attention over 8-bit keys and values for many rows of a
+// sequence (prompts, drafts of many query heads); the mathematics is
+// kv_attention.cu's.
+//
+// A segment is 128 rows (a key head's query heads, of one token after another), a
+// unit 128 tokens of it.  Bound by the tensor cores and the exponentials, which
+// take about as long: S = Q K^T and O = P V are tcgen05 MMAs of 128 x 128 (x D),
+// S, P and O in tensor memory, P over the S that it came from.  Roles of a CTA, one per SM:
+// four warps read codes and write them as FP16 into swizzled tiles, one issues
+// MMAs, and two groups of four turn S into P, a thread a row.  The groups take the
+// units in turn and each has an O of its own, so that one's exponentials run beside
+// the other's products; their sums are joined at the segment's end, as are those of
+// CTAs that share a segment (kv_join_kernel).  The CTAs take equal consecutive
+// ranges of all units, of which a causal tile has as many as it needs.
+//
+// FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
+// taken in a pass of its own over S (0.5 operations a value); O's reference moves
+// only where p s_v would pass 2^14, so O is rarely scaled.
+#include "kv_attention.cuh"
+
+namespace emu {
+namespace {
+
+constexpr int kTile = 128;                           // rows of a segment, tokens of a unit
+constexpr int kPanel = kTile * 128;                  // 128 rows of 64 FP16 values, swizzled
+constexpr int kSoftWarps = 8, kCodeWarps = 4;
+constexpr int kThreads = (kSoftWarps + kCodeWarps + 1) * 32;
+
+// ------------------------------------------------- tiles of a sequence --
+
+// Tile i of a sequence: its units from first(i) to end(i), in the order of tiles and, within one, heads.
+struct Tiles {
+    int n, group, pos0, window, count;
+    __device__ __forceinline__ Tiles(const AttnParams& p, const Seq& s)
+        : n(s.n), group(p.group), pos0(max(s.len, 0) - s.n), window(p.window),
+          count((int)(((int64_t)s.n * p.group + kTile - 1) / kTile)) {}
+    __device__ __forceinline__ int64_t end_token(int64_t i) const {      // behind the last one that a row sees, any tile but the last
+        return (int64_t)pos0 + (kTile * (i + 1) - 1) / group + 1;
+    }
+    __device__ __forceinline__ int64_t first_token(int64_t i) const {    // negative: none before
+        return window ? (int64_t)pos0 + kTile * i / group - window + 1 : -1;
+    }
+    __device__ __forceinline__ int first(int i) const { return (int)(max(first_token(i), (int64_t)0) / kTile); }
+    __device__ __forceinline__ int end(int i) const {                    // (a tile that sees nothing has a unit: it is written)
+        const int64_t e = i == count - 1 ? (int64_t)pos0 + n : end_token(i);
+        return (int)max((e + kTile - 1) >> 7, (int64_t)1);
+    }
+    __device__ __forceinline__ int units(int i) const { return end(i) - first(i); }
+    // sum of max(low, a + k) over 0 <= k < c
+    static __device__ __forceinline__ int64_t ramp(int64_t a, int64_t c, int64_t low) {
+        const int64_t flat = min(max(low - a, (int64_t)0), c);
+        return flat * low + (c - flat) * a + (c - 1 + flat) * (c - flat) / 2;
+    }
+    // Units of the first m tiles, m < count: a tile `group` tiles on lies 128 tokens on.
+    __device__ __forceinline__ int64_t before(int64_t m) const {
+        int64_t sum = 0;
+        for (int64_t r = 0; r < min((int64_t)group, m); ++r) {
+            const int64_t c = (m - r + group - 1) / group;
+            sum += ramp((end_token(r) + kTile - 1) >> 7, c, 1);
+            if (window) sum -= ramp(first_token(r) >> 7, c, 0);
+        }
+        return sum;
+    }
+    __device__ __forceinline__ int64_t all() const { return count ? before(count - 1) + units(count - 1) : 0; }
+};
+
+// ------------------------------------------------------- tensor memory --
+
+__device__ __forceinline__ void tmem_ld_x32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+           "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+// D = A B (+ D), A and B in shared memory
+__device__ __forceinline__ void mma_cta1(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t leader) {
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t two(float x) { return pack_f32x2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// ------------------------------------------------------------- kernel --
+
+template <typename T, int NG>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ AttnParams p) {
+    constexpr bool TWO = sizeof(T) == 4;
+    constexpr int PIECES = TWO ? 2 : 1;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // q: [piece][64 values], k and v: [stage][64 values] panels
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + PIECES * NG * kPanel, v_at = k_at + 2 * NG * kPanel;
+    __shared__ __align__(8) uint64_t bars[18];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag, nan_flag;
+    __shared__ int64_t warp_sum[kThreads / 32];
+    __shared__ Work work;
+    // of a unit's tiles of 16 tokens: keys, values (four units: a group may still read its unit's while the
+    // next but one's keys are stored; five later its weights are done)
+    __shared__ float scales[4][2][8];
+    __shared__ float q_top[2][kTile];
+    __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
+    const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
+                   s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 104,
+                   c_full = k_full + 112;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D;
+    volatile int* const aborted = &abort_flag;
+    const float nan = __uint_as_float(0x7FC00000u);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full + 8 * i, kCodeWarps * 32);
+            mbar_init(k_free + 8 * i, 1);
+            mbar_init(v_full + 8 * i, kCodeWarps * 32);
+            mbar_init(v_free + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, kTile);
+        }
+        mbar_init(q_full, kSoftWarps * 32);
+        mbar_init(drained, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(c_full + 8 * i, 8);
+        abort_flag = nan_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kSoftWarps + kCodeWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+
+    // all units, and where this CTA's range of them begins: a run of sequences per thread
+    const int per = (p.B + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    for (int b = tid * per; b < min((tid + 1) * per, p.B); ++b) {
+        const Seq s = seq_of(p, b);
+        mine += Tiles(p, s).all() * p.heads;
+        if (blockIdx.x == 0 && (s.len < 0 || p.starts[b + 1] < s.start || s.start < 0 || p.starts[b + 1] > p.T))
+            record_error(p.err, kDevErrValue);
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    int64_t all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) sum += warp_sum[w];
+        all += warp_sum[w];
+    }
+    griddep_launch_dependents();                     // (kv_join_kernel waits for this one's end)
+    const int64_t ctas = min((int64_t)gridDim.x, all);
+    bool ok = true;
+
+    if (blockIdx.x < ctas) {
+        const int64_t begin = all * blockIdx.x / ctas;
+        if (sum - mine <= begin && begin < sum) {    // (one thread)
+            int64_t before = sum - mine;
+            int b = tid * per;
+            for (;; ++b) {
+                const int64_t n = Tiles(p, seq_of(p, b)).all() * p.heads;
+                if (begin < before + n) break;
+                before += n;
+            }
+            work.all = all;
+            work.ctas = ctas;
+            work.at = begin;
+            work.stop = all * (blockIdx.x + 1) / ctas;
+            work.base = before;
+            work.seq = b;
+        }
+        __syncthreads();
+        {
+            // the tile of the sequence: every thread tries some, twice where there are many
+            const Tiles ti(p, seq_of(p, work.seq));
+            const int64_t u = (work.at - work.base) / p.heads;
+            __shared__ int found;
+            int lo = 0, hi = ti.count;               // in [lo, hi)
+            while (hi - lo > 1) {
+                const int step = (hi - lo + kThreads - 1) / kThreads, i = lo + tid * step;
+                __syncthreads();
+                if (i < hi) {
+                    const int64_t from = ti.before(i), to = i + step < hi ? ti.before(i + step) : INT64_MAX;
+                    if (from <= u && u < to) found = i;
+                }
+                __syncthreads();
+                lo = found;
+                hi = min(hi, lo + step);
+            }
+            if (tid == 0) {
+                work.begin = work.base + ti.before(lo) * p.heads;            // of the tile's first head
+                const int units = ti.units(lo);
+                work.head = (int)((work.at - work.begin) / units);
+                work.begin += (int64_t)work.head * units;
+                work.row0 = lo * kTile;
+            }
+        }
+        uint32_t j = 0;                              // units of this CTA so far
+        uint32_t segments = 0;
+        for (;;) {
+            __syncthreads();
+            // ------------------------------------------------ the segment
+            if (tid == 0) {
+                const Seq s = seq_of(p, work.seq);
+                const Tiles ti(p, s);
+                const int i = work.row0 / kTile, units = ti.units(i);
+                work.bad = s.len < 0;
+                work.start = s.start;
+                work.len = max(s.len, 0);
+                work.pos0 = work.len - s.n;
+                work.end = work.begin + units;
+                work.rows = min(kTile, (int)min((int64_t)s.n * p.group - work.row0, (int64_t)kTile));
+                work.token0 = (ti.first(i) + (int)(work.at - work.begin)) * kTile;
+                work.units = (int)(min(work.stop, work.end) - work.at);
+                work.starts = work.at == work.begin;
+                work.whole = work.units == units;
+                nan_flag = 0;
+            }
+            __syncthreads();
+            const int units = work.units, token0 = work.token0, len = work.len, pos0 = work.pos0, head = work.head;
+            const int row0 = work.row0, rows = work.rows;
+            // tokens that some row of the segment sees
+            const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
+            const int sees_end = max(0, min(len, pos_last + 1));
+            const int sees_begin = p.window ? max(0, pos_first - p.window + 1) : 0;
+            // whether some row does not see some token of a unit
+            auto edge_of = [&](int tok) {
+                return tok + kTile > pos_first + 1 || tok + kTile > len || (p.window && tok <= pos_last - p.window);
+            };
+            const uint32_t j0 = j, j1 = j + units;
+            auto phase = [](uint32_t i) { return i >> 1 & 1; };
+
+            if (warp >= kSoftWarps + kCodeWarps) {
+                // ------------------------------------------------- MMAs
+                const uint32_t leader = elect_one();
+                const uint32_t idesc_s = make_idesc(0u, kTile, kTile), idesc_o = make_idesc(0u, kTile, D) | kIdescBMn;
+                ok = ok && mbar_wait(q_full, segments & 1, p.err, kDevErrTimeout);
+                auto values = [&](uint32_t i) {      // O += P V
+                    const uint32_t s = i & 1;
+                    ok = ok && mbar_wait(v_full + 8 * s, phase(i), p.err, kDevErrTimeout) &&
+                         mbar_wait(p_full + 8 * s, phase(i), p.err, kDevErrTimeout) && !*aborted;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t b = make_sw128_mn_desc(v_at + s * NG * kPanel, kPanel);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
+                        const uint32_t a = tmem + s * kTile + 32 * (k / 2) + 8 * (k % 2);
+                        if constexpr (TWO)
+                            mma_cta1_ta(tmem + 2 * kTile + s * kTile, a + 16, b + k * (2048 >> 4), idesc_o, k > 0 || i >= j0 + 2, leader);
+                        mma_cta1_ta(tmem + 2 * kTile + s * kTile, a, b + k * (2048 >> 4), idesc_o, TWO || k > 0 || i >= j0 + 2, leader);
+                    }
+                    tc_commit(v_free + 8 * s, leader);
+                };
+                for (uint32_t i = j0; i < j1 && ok; ++i) {
+                    const uint32_t s = i & 1;
+                    ok = ok && mbar_wait(k_full + 8 * s, phase(i), p.err, kDevErrTimeout) && !*aborted;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int piece = PIECES - 1; piece >= 0; --piece)
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t step = (k / 4) * kPanel + (k % 4) * 32;
+                            mma_cta1(tmem + s * kTile, make_sw128_kmajor_desc(q_at + piece * NG * kPanel + step),
+                                     make_sw128_kmajor_desc(k_at + s * NG * kPanel + step), idesc_s,
+                                     piece < PIECES - 1 || k > 0, leader);
+                        }
+                    tc_commit(k_free + 8 * s, leader);
+                    tc_commit(s_full + 8 * s, leader);
+                    if (i > j0) values(i - 1);
+                }
+                if (ok) values(j1 - 1);
+                if (!ok) *aborted = 1;
+            } else if (warp >= kSoftWarps) {
+                // ------------------------------------------------ codes
+                const int ct = tid - kSoftWarps * 32, piece = ct & 3;
+                const int32_t* pages = p.table + (int64_t)work.seq * p.width;
+                // lane L < 8 looks after tile L of 16 tokens: its page (-1: bad, -2: no row sees it)
+                auto page_of = [&](uint32_t i) {
+                    const int tok = token0 + (int)(i - j0) * kTile + 16 * (lane & 7);
+                    if (i >= j1 || tok >= sees_end || tok + 16 <= sees_begin) return -2;
+                    const int page = pages[tok >> p.page_log];
+                    return page >= 0 && page < p.pages ? page : -1;
+                };
+                uint4 raw[NG * 4];
+                auto load = [&](const uint8_t* from, uint32_t i, int page_lane) {
+                    const int tok0 = token0 + (int)(i - j0) * kTile;
+#pragma unroll
+                    for (int st = 0; st < 4; ++st) {
+                        const int in_tile = st * 32 + (ct >> 2), tok = tok0 + in_tile;
+                        const int page = __shfl_sync(0xffffffffu, page_lane, in_tile >> 4);
+                        const uint8_t* row = from + (((((int64_t)page * p.heads + head) << p.page_log) +
+                                                      (tok & ((1 << p.page_log) - 1))) * D + piece * 16);
+                        const bool in = page >= 0 && tok >= sees_begin && tok < sees_end;
+#pragma unroll
+                        for (int n = 0; n < NG; ++n)
+                            raw[n * 4 + st] = in && n * 64 + piece * 16 < D ? __ldg(reinterpret_cast<const uint4*>(row + n * 64))
+                                                                             : make_uint4(0, 0, 0, 0);
+                    }
+                };
+                auto store = [&](uint32_t to) {
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int st = 0; st < 4; ++st) {
+                            const int row = st * 32 + (ct >> 2);
+                            const uint32_t at = to + n * kPanel + row * 128, x = (row & 7) << 4;
+                            const uint32_t w[4] = {raw[n * 4 + st].x, raw[n * 4 + st].y, raw[n * 4 + st].z, raw[n * 4 + st].w};
+                            uint32_t h[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                h[2 * e] = kv_half2((uint16_t)w[e]);
+                                h[2 * e + 1] = kv_half2((uint16_t)(w[e] >> 16));
+                            }
+                            sts128(at + (piece * 32 ^ x), h[0], h[1], h[2], h[3]);
+                            sts128(at + ((piece * 32 + 16) ^ x), h[4], h[5], h[6], h[7]);
+                        }
+                };
+                // pages two units ahead, codes and scales one
+                int page = page_of(j0), page_next = page_of(j0 + 1);
+                auto scale_of = [&](int pg, const float* from) {
+                    return pg >= 0 ? __ldg(from + (int64_t)pg * p.heads + head) : pg == -1 ? nan : 0.0f;
+                };
+                float ks = scale_of(page, p.ks), vs = scale_of(page, p.vs);
+                load(p.k, j0, page);
+                for (uint32_t i = j0; i < j1 && ok; ++i) {
+                    const uint32_t s = i & 1;
+                    if (page == -1) record_error(p.err, kDevErrValue);
+                    ok = mbar_wait(k_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
+                    if (!ok) break;
+                    store(k_at + s * NG * kPanel);
+                    if (ct < 8) {
+                        scales[i & 3][0][ct] = ks;
+                        scales[i & 3][1][ct] = vs;
+                        mbar_arrive(c_full + 8 * (i & 3));
+                    }
+                    fence_async_smem();
+                    mbar_arrive(k_full + 8 * s);
+                    load(p.v, i, page);
+                    const bool edge = edge_of(token0 + (int)(i - j0) * kTile);
+                    const int page_this = page_next;
+                    ks = scale_of(page_this, p.ks);
+                    vs = scale_of(page_this, p.vs);
+                    page_next = page_of(i + 2);
+                    ok = mbar_wait(v_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
+                    if (!ok) break;
+                    if (edge) {
+                        // a NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken out
+                        // here and put into those rows at the end
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int n = 0; n < NG * 4; ++n) {
+                            uint32_t* const w[4] = {&raw[n].x, &raw[n].y, &raw[n].z, &raw[n].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t x = nan_bytes(*w[e]);
+                                *w[e] &= ~x;
+                                any |= x;
+                            }
+                        }
+                        if (any) nan_flag = 1;
+                    }
+                    store(v_at + s * NG * kPanel);
+                    fence_async_smem();
+                    mbar_arrive(v_full + 8 * s);
+                    page = page_this;
+                    if (i + 1 < j1) load(p.k, i + 1, page);
+                }
+                if (!ok) *aborted = 1;
+            } else {
+                // --------------------------------------------- scores to weights
+                const int half = warp >> 2, r = tid & (kTile - 1);       // group, row
+                const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+                // Q: this thread's row, the values of its group's part
+                const int row = row0 + min(r, rows - 1), token = row / p.group, pos = pos0 + token;
+                float factor;
+                {
+                    constexpr int MINE = NG * 32;    // values
+                    const T* from = static_cast<const T*>(p.q) + (work.start + token) * p.q_t +
+                                    (head * p.group + row - token * p.group) * p.q_h;
+                    float x[MINE];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < MINE; c += 8) {
+                        const int d = half * MINE + c;
+                        if (d < D) kv_load8(from + d, p.wide, x + c);
+                        else
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[c + e] = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[c + e]));
+                    }
+                    q_top[half][r] = top;
+                    bar_and(1, kSoftWarps * 32, true);
+                    top = fmaxf(q_top[0][r], q_top[1][r]);
+                    // 2^(14 - E), top = m 2^E; a negative scale turns q
+                    const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
+                    const float up = copysignf(__uint_as_float((uint32_t)(14 - E + 127) << 23), p.scale);
+                    factor = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (fabsf(p.scale) * kLog2e);
+#pragma unroll
+                    for (int c = 0; c < MINE; c += 8) {
+                        const int d = half * MINE + c;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = x[c + 2 * e] * up, b = x[c + 2 * e + 1] * up;
+                            hi[e] = half2_bits(a, b);
+                            lo[e] = TWO ? half2_rest(a, b, hi[e]) : 0u;
+                        }
+                        const uint32_t at = q_at + (d / 64) * kPanel + r * 128 + ((d % 64 * 2) ^ ((r & 7) << 4));
+                        sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                        if (TWO) sts128(at + NG * kPanel, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    fence_async_smem();
+                    mbar_arrive(q_full);
+                }
+
+                float m = -INFINITY, l = 0.0f, ref = -INFINITY;
+                const uint32_t s_at = (tmem + half * kTile) | lanes, o_at = (tmem + (2 + half) * kTile) | lanes;
+                bool first = true;
+                for (uint32_t i = j0 + ((j0 ^ half) & 1); i < j1 && ok; i += 2) {
+                    ok = mbar_wait(s_full + 8 * half, phase(i), p.err, kDevErrTimeout) &&
+                         mbar_wait(c_full + 8 * (i & 3), i >> 2 & 1, p.err, kDevErrTimeout) && !*aborted;
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int tok = token0 + (int)(i - j0) * kTile;
+                    const bool edge = edge_of(tok);
+                    const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
+                    const float* const ks = scales[i & 3][0];
+                    const float* const vs = scales[i & 3][1];
+                    // the largest score, and the largest with its page's bound
+                    float top = -INFINITY, over = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t sc[32];
+                        tmem_ld_x32(s_at + c, sc);
+                        tmem_ld_wait();
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (tok + c + e > last || tok + c + e <= from) sc[e] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float x = __uint_as_float(sc[16 * g]);
+#pragma unroll
+                            for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(sc[16 * g + e]));
+                            // (what no row sees has scale 0)
+                            if (x > -INFINITY) {
+                                x *= factor * ks[c / 16 + g];
+                                top = fmaxf(top, x);
+                                over = fmaxf(over, x + (float)scale_bound(vs[c / 16 + g]));
+                            }
+                        }
+                    }
+                    if (top > m) {
+                        l *= exp2_of(m - top);
+                        m = top;
+                    }
+                    // o's reference: p s_v between 2^8 and 2^14 at its largest (scale_bound is 14 below), moved where it
+                    // would pass 2^14
+                    const bool move = over > ref;
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float now = move ? over + 6.0f : ref;
+                        if (!first) {
+                            // (O is whole once the unit two before is)
+                            ok = mbar_wait(v_free + 8 * half, phase(i) ^ 1, p.err, kDevErrTimeout);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const float f = move ? exp2_of(ref - now) : 1.0f;
+                            for (int c = 0; c < D; c += 8) {
+                                uint32_t o[8];
+                                tmem_ld_32x32b_x8(o_at + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st_32x32b_x8(o_at + c, o);
+                            }
+                            tmem_st_wait();
+                        }
+                        ref = now;
+                    }
+                    first = false;
+                    const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
+                    uint64_t sums = 0;
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t sc[32], w[16], rest[16];
+                        tmem_ld_x32(s_at + c, sc);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const uint64_t k2 = two(factor * ks[c / 16 + g]), m2 = two(-m0), f2 = two(vs[c / 16 + g] * up);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const uint64_t x = fma_f32x2(pack_f32x2(sc[16 * g + e], sc[16 * g + e + 1]), k2, m2);
+                                float p0 = exp2_of(lo_of(x)), p1 = exp2_of(hi_of(x));
+                                if (edge) {
+                                    const int t0 = tok + c + 16 * g + e;
+                                    if (t0 > last || t0 <= from) p0 = 0.0f;
+                                    if (t0 + 1 > last || t0 + 1 <= from) p1 = 0.0f;
+                                }
+                                const uint64_t pp = pack_f32x2(__float_as_uint(p0), __float_as_uint(p1));
+                                sums = add_f32x2(sums, pp);
+                                const uint64_t ww = mul_f32x2(pp, f2);
+                                float w0 = lo_of(ww), w1 = hi_of(ww);
+                                if (edge) {          // (a page that is not there has no scale)
+                                    if (p0 == 0.0f) w0 = 0.0f;
+                                    if (p1 == 0.0f) w1 = 0.0f;
+                                }
+                                w[8 * g + e / 2] = half2_bits(w0, w1);
+                                if constexpr (TWO) rest[8 * g + e / 2] = half2_rest(w0, w1, w[8 * g + e / 2]);
+                            }
+                        }
+                        // over the scores just read
+                        tmem_st_x16(s_at + c, w);
+                        if constexpr (TWO) tmem_st_x16(s_at + c + 16, rest);
+                    }
+                    l += lo_of(sums) + hi_of(sums);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(p_full + 8 * half);
+                }
+                if (!ok) *aborted = 1;
+                // --------------------------------------------- the segment's end
+                row_stat[half][r][0] = m;
+                row_stat[half][r][1] = l;
+                row_stat[half][r][2] = ref;
+                // both groups' last products (a unit's two before it are done where it is)
+                const bool two_units = units > 1;
+                if (ok) ok = mbar_wait(v_free + 8 * ((j1 - 1) & 1), phase(j1 - 1), p.err, kDevErrTimeout);
+                if (ok && two_units) ok = mbar_wait(v_free + 8 * ((j1 - 2) & 1), phase(j1 - 2), p.err, kDevErrTimeout);
+                ok = bar_and(1, kSoftWarps * 32, ok);
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t s0 = j0 & 1;      // the group that had the first unit
+                    const float m_a = row_stat[s0][r][0], l_a = row_stat[s0][r][1], ref_a = row_stat[s0][r][2];
+                    float m_all = m_a, ref_all = ref_a, l_all = l_a, x_a = 1.0f, x_b = 0.0f;
+                    if (two_units) {
+                        const float m_b = row_stat[s0 ^ 1][r][0], l_b = row_stat[s0 ^ 1][r][1], ref_b = row_stat[s0 ^ 1][r][2];
+                        m_all = fmaxf(m_a, m_b);
+                        ref_all = fmaxf(ref_a, ref_b);
+                        l_all = l_a * weight_of(m_a, l_a, m_all) + l_b * weight_of(m_b, l_b, m_all);
+                        x_a = share_of(ref_a, ref_all);
+                        x_b = share_of(ref_b, ref_all);
+                    }
+                    float* const slot = p.partial + ((2 * (int64_t)blockIdx.x + work.starts) * p.slot_rows + r) * (D + 4);
+                    if (!work.whole && r < rows && half == 0)
+                        *reinterpret_cast<float4*>(slot) = make_float4(m_all, l_all, ref_all, 0.0f);
+                    const bool nan_seen = nan_flag != 0;
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+                        uint32_t a[8], b[8];
+                        tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
+                        if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
+                        tmem_ld_wait();
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            y[e] = __uint_as_float(a[e]) * x_a;
+                            if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
+                        }
+                        if (r >= rows) continue;
+                        if (nan_seen)
+                            for (int u = 0; u < units; ++u) {
+                                const int tok = token0 + u * kTile;
+                                if (!edge_of(tok)) continue;
+                                const int lo = max(tok, p.window ? pos - p.window + 1 : 0), hi = min(tok + kTile, min(pos, len - 1) + 1);
+                                for (int t = max(lo, 0); t < hi; ++t) {
+                                    const int page = p.table[(int64_t)work.seq * p.width + (t >> p.page_log)];
+                                    if (page < 0 || page >= p.pages) continue;
+                                    const uint8_t* v = p.v + (((((int64_t)page * p.heads + head) << p.page_log) +
+                                                               (t & ((1 << p.page_log) - 1))) * D + c);
+                                    for (int e = 0; e < 8; ++e)
+                                        if ((v[e] & 0x7F) == 0x7F) y[e] = nan;
+                                }
+                            }
+                        const float4 y0 = make_float4(y[0], y[1], y[2], y[3]), y1 = make_float4(y[4], y[5], y[6], y[7]);
+                        if (work.whole) {
+                            write_row<T>(p, work, r, c, m_all, l_all, ref_all, y0);
+                            write_row<T>(p, work, r, c + 4, m_all, l_all, ref_all, y1);
+                        } else {
+                            *reinterpret_cast<float4*>(slot + 4 + c) = y0;
+                            *reinterpret_cast<float4*>(slot + 8 + c) = y1;
+                        }
+                    }
+                    tc_fence_before();
+                }
+            }
+            j = j1;
+            ++segments;
+            if (__syncthreads_or(!ok) || work.end >= work.stop) break;
+            if (tid == 0) {
+                // the next head, tile or sequence
+                work.at = work.begin = work.end;
+                if (++work.head == p.heads) {
+                    work.head = 0;
+                    Seq s = seq_of(p, work.seq);
+                    if (work.row0 + (int64_t)kTile < (int64_t)s.n * p.group) {
+                        work.row0 += kTile;
+                    } else {
+                        work.row0 = 0;
+                        do s = seq_of(p, ++work.seq);
+                        while (s.n == 0);
+                    }
+                }
+            }
+        }
+        // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
+        if (warp == kSoftWarps + kCodeWarps && !ok) {
+            const uint32_t leader = elect_one();
+            tc_commit(drained, leader);
+            mbar_wait(drained, 0, p.err, kDevErrTimeout);
+        }
+    }
+    if (tid == 0) {
+        if (blockIdx.x >= ctas) work.units = 0;
+        else if (work.whole || !work.starts) work.units = 0;
+        p.shared[blockIdx.x] = work;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps + kCodeWarps)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u));
+}
+
+template <typename T, int NG>
+cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
+    constexpr int smem = ((sizeof(T) == 4 ? 2 : 1) + 4) * NG * kPanel;
+    auto kern = kv_prompt_kernel<T, NG>;
+    static bool done[kMaxDevices] = {};              // (g_mu is held)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    p.slot_rows = kTile;
+    kern<<<(unsigned)sms, kThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, 16, stream);
+}
+
+template <typename T>
+cudaError_t launch_typed(const AttnParams& p, int dtype, int sms, cudaStream_t stream) {
+    return p.D <= 64 ? launch<T, 1>(p, dtype, sms, stream) : launch<T, 2>(p, dtype, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(int dtype, const AttnParams& p, int sms, cudaStream_t stream) {
+    if (dtype == EMU_F32) return launch_typed<float>(p, dtype, sms, stream);
+    if (dtype == EMU_BF16) return launch_typed<__nv_bfloat16>(p, dtype, sms, stream);
+    return launch_typed<__half>(p, dtype, sms, stream);
+}
+
+}  // namespace emu

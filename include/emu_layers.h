@@ -257,8 +257,8 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  * rows are the sequence's last tokens, and are in the cache themselves.
  *
  *  q, out        T rows of the same number of heads, a multiple of cache->heads: head h
- *                reads key head h / (heads / cache->heads).  `dtype`, any strides; out may
- *                be q.
+ *                reads key head h / (heads / cache->heads); T times that quotient below
+ *                2^31 - 256.  `dtype`, any strides; out may be q.
  *  table, width  B rows of page numbers, as emu_kv_tables leaves them
  *  starts        B + 1 values, ascending: sequence b has the rows starts[b] ..
  *                starts[b+1] - 1 (none are fine); rows from starts[B] on become zero

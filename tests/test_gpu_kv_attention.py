@@ -112,13 +112,55 @@ def test_many_steps(emu, type, D):
     for P, G, window in ((16, 3, 0), (64, 9, 700)):
         q, cache, table, starts, lengths = _make([2500 + 33 * i for i in range(30)], [1 + i % 2 for i in range(30)], 8 * G, 8,
                                                  D, P, type, seed=D)
-        out = emu.emu_kv_attention(q, cache, table, _ints(starts), _ints(lengths), window=window)
-        for b in (0, 13, 29):                        # (the reference of all would take long)
-            rows = slice(starts[b], starts[b + 1])
-            want, bound = ref.attention(q[rows], *cache, table[b:b + 1], [0, starts[b + 1] - starts[b]], [lengths[b]],
-                                        D ** -0.5, window)
-            assert ref.within(out[rows], want, bound)
-        assert torch.isfinite(out).all() and _error(emu) == 0
+        for most in (2, None):                       # (kernels for few rows, and for many)
+            out = emu.emu_kv_attention(q, cache, table, _ints(starts), _ints(lengths), window=window, max_new=most)
+            for b in (0, 13, 29):                    # (the reference of all would take long)
+                rows = slice(starts[b], starts[b + 1])
+                want, bound = ref.attention(q[rows], *cache, table[b:b + 1], [0, starts[b + 1] - starts[b]], [lengths[b]],
+                                            D ** -0.5, window)
+                assert ref.within(out[rows], want, bound)
+            assert torch.isfinite(out).all() and _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("D", [16, 32, 48, 64, 80, 96, 112, 128])
+@pytest.mark.parametrize("window", [0, 300])
+def test_many_tiles(emu, type, D, window):
+    """Prompts of more tiles than the GPU has SMs, of different lengths: every CTA has parts of several."""
+    new = [700, 1, 0, 333, 1025, 64]
+    made = _make([0, 600, 50, 1000, 129, 3], new, 10, 2, D, 32, type, seed=D, behind=3)
+    _check(emu, made, window=window)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("n", [1, 200])
+def test_zeros(emu, type, n):
+    """Keys and values of zero, as the store leaves them (scale 2^-126), alone and beside others."""
+    import torch
+    q, cache, table, starts, lengths = _make([100, 100], [n, n], 4, 2, 64, 32, type)
+    for pages in (table[0], table[0, 1:3]):
+        k, v, ks, vs = (x.clone() for x in cache)
+        at = pages[pages >= 0].long()
+        for codes, scale in ((k, ks), (v, vs)):
+            codes.view(torch.uint8)[at] = 0
+            scale[at] = 2.0 ** -126
+        out = _check(emu, (q, (k, v, ks, vs), table, starts, lengths), max_new=n)
+        assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 40.0])
+def test_scale(emu, type, scale):
+    for kept, new in (([70, 9], [1, 1]), ([70, 9], [40, 150])):
+        _check(emu, _make(kept, new, 4, 2, 64, 32, type), scale=scale, max_new=max(new))
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_max_new_is_a_hint(emu, D):
+    """Too small a max_new changes kernels only."""
+    made = _make([300, 40], [30, 3], 6, 2, D, 16, "f32")
+    for most in (1, 2, 30, 1000):
+        _check(emu, made, max_new=most)
 
 
 def test_rows_that_see_nothing(emu):
