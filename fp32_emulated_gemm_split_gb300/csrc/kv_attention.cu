@@ -927,6 +927,7 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     p.scale = scale;
     const int size = dtype == EMU_F32 ? 4 : 2;
     p.wide = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_t * size % 16 == 0 && p.q_h * size % 16 == 0;
+    p.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.out_t * size % 16 == 0 && p.out_h * size % 16 == 0;
     p.partial = static_cast<float*>(d->kv_ws);
     p.shared = reinterpret_cast<Work*>(static_cast<uint8_t*>(d->kv_ws) + slots);
     p.err = d->err;

@@ -23,7 +23,7 @@ struct AttnParams {
     int64_t pages;
     const int32_t *table, *starts, *lengths;
     float scale;
-    int wide;                                        // rows of q on 16 bytes
+    int wide, wide_out;                              // rows of q, of out on 16 bytes
     int depth, side;                                 // stages of a warp's ring, bytes of a stage's keys (or values)
     int copy_tokens;                                 // tokens of one tensor copy
     float* partial;                                  // [2 ctas][slot_rows][D + 4]
@@ -87,11 +87,15 @@ struct Work {
     bool bad, starts, whole;                         // no length; the part has the segment's first unit, all of them
 };
 
-// Four values of a row from its sums, maximum m, sum of weights l, reference ref.
+// What a row's sums are multiplied with: maximum m, sum of weights l, reference ref.
+__device__ __forceinline__ float row_factor(bool bad, float m, float l, float ref) {
+    return bad ? __uint_as_float(0x7FC00000u) : l > 0.0f || l != l ? exp2_of(ref - m) / l : 0.0f;
+}
+// Four values of a row from its sums.
 template <typename T>
 __device__ __forceinline__ void write_row(const AttnParams& p, const Work& w, int r, int d, float m, float l, float ref, float4 v) {
     const int row = w.row0 + r, i = row / p.group;
-    const float f = w.bad ? __uint_as_float(0x7FC00000u) : l > 0.0f || l != l ? exp2_of(ref - m) / l : 0.0f;
+    const float f = row_factor(w.bad, m, l, ref);
     T* to = static_cast<T*>(p.out) + (w.start + i) * p.out_t + (w.head * p.group + row - i * p.group) * p.out_h + d;
     to[0] = kv_from<T>(v.x * f);
     to[1] = kv_from<T>(v.y * f);

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "emu_layers.h"
 
@@ -60,6 +61,26 @@ __device__ __forceinline__ void kv_load8(const T* at, bool wide, float* x) {
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = kv_f32(at[i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void kv_store8(T* at, bool wide, const float (&x)[8]) {
+    if (wide) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            T y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = kv_from<T>(x[i]);
+            uint4 w;
+            memcpy(&w, y, 16);
+            *reinterpret_cast<uint4*>(at) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at[i] = kv_from<T>(x[i]);
     }
 }
 

@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     const int page = pages[tok >> p.page_log];
                     return page >= 0 && page < p.pages ? page : -1;
                 };
-                uint4 raw[NG * 4];
-                auto load = [&](const uint8_t* from, uint32_t i, int page_lane) {
+                uint4 raw_k[NG * 4], raw_v[NG * 4];
+                auto load = [&](uint4 (&raw)[NG * 4], const uint8_t* from, uint32_t i, int page_lane) {
                     const int tok0 = token0 + (int)(i - j0) * kTile;
 #pragma unroll
                     for (int st = 0; st < 4; ++st) {
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                                                              : make_uint4(0, 0, 0, 0);
                     }
                 };
-                auto store = [&](uint32_t to) {
+                auto store = [&](const uint4 (&raw)[NG * 4], uint32_t to) {
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -343,19 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             sts128(at + ((piece * 32 + 16) ^ x), h[4], h[5], h[6], h[7]);
                         }
                 };
-                // pages two units ahead, codes and scales one
+                // pages two units ahead, codes and scales one: a unit's codes are on the way while those of the one
+                // before are written
                 int page = page_of(j0), page_next = page_of(j0 + 1);
                 auto scale_of = [&](int pg, const float* from) {
                     return pg >= 0 ? __ldg(from + (int64_t)pg * p.heads + head) : pg == -1 ? nan : 0.0f;
                 };
                 float ks = scale_of(page, p.ks), vs = scale_of(page, p.vs);
-                load(p.k, j0, page);
+                load(raw_k, p.k, j0, page);
+                load(raw_v, p.v, j0, page);
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
                     const uint32_t s = i & 1;
                     if (page == -1) record_error(p.err, kDevErrValue);
                     ok = mbar_wait(k_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
                     if (!ok) break;
-                    store(k_at + s * NG * kPanel);
+                    store(raw_k, k_at + s * NG * kPanel);
                     if (ct < 8) {
                         scales[i & 3][0][ct] = ks;
                         scales[i & 3][1][ct] = vs;
@@ -363,12 +365,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     }
                     fence_async_smem();
                     mbar_arrive(k_full + 8 * s);
-                    load(p.v, i, page);
-                    const bool edge = edge_of(token0 + (int)(i - j0) * kTile);
-                    const int page_this = page_next;
-                    ks = scale_of(page_this, p.ks);
-                    vs = scale_of(page_this, p.vs);
+                    page = page_next;
                     page_next = page_of(i + 2);
+                    if (i + 1 < j1) {
+                        load(raw_k, p.k, i + 1, page);
+                        ks = scale_of(page, p.ks);
+                        vs = scale_of(page, p.vs);
+                    }
+                    const bool edge = edge_of(token0 + (int)(i - j0) * kTile);
                     ok = mbar_wait(v_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
                     if (!ok) break;
                     if (edge) {
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         uint32_t any = 0;
 #pragma unroll
                         for (int n = 0; n < NG * 4; ++n) {
-                            uint32_t* const w[4] = {&raw[n].x, &raw[n].y, &raw[n].z, &raw[n].w};
+                            uint32_t* const w[4] = {&raw_v[n].x, &raw_v[n].y, &raw_v[n].z, &raw_v[n].w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint32_t x = nan_bytes(*w[e]);
@@ -387,11 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         }
                         if (any) nan_flag = 1;
                     }
-                    store(v_at + s * NG * kPanel);
+                    store(raw_v, v_at + s * NG * kPanel);
                     fence_async_smem();
                     mbar_arrive(v_full + 8 * s);
-                    page = page_this;
-                    if (i + 1 < j1) load(p.k, i + 1, page);
+                    if (i + 1 < j1) load(raw_v, p.v, i + 1, page);
                 }
                 if (!ok) *aborted = 1;
             } else {
@@ -458,9 +461,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
                     const float* const ks = scales[i & 3][0];
                     const float* const vs = scales[i & 3][1];
+                    if constexpr (!TWO) {
+                        // Most units: the maximum and the reference as they are, and P held back until it is known
+                        // that none of it passed FP16's range.
+                        if (!edge && !first) {
+                            uint32_t w[kTile / 2], sc[2][16];
+                            __half2 most = __float2half2_rn(0.0f);
+                            uint64_t sums = 0;
+                            const uint64_t m2 = two(-m);
+                            const float up = exp2_of(m - ref);
+                            tmem_ld_32x32b_x16(s_at, sc[0]);
+#pragma unroll
+                            for (int g = 0; g < kTile / 16; ++g) {
+                                tmem_ld_wait();
+                                if (g + 1 < kTile / 16) tmem_ld_32x32b_x16(s_at + 16 * (g + 1), sc[(g + 1) & 1]);
+                                const uint64_t k2 = two(factor * ks[g]), f2 = two(vs[g] * up);
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) {
+                                    const uint64_t x = fma_f32x2(pack_f32x2(sc[g & 1][e], sc[g & 1][e + 1]), k2, m2);
+                                    const uint64_t pp = pack_f32x2(__float_as_uint(exp2_of(lo_of(x))), __float_as_uint(exp2_of(hi_of(x))));
+                                    sums = add_f32x2(sums, pp);
+                                    const uint64_t ww = mul_f32x2(pp, f2);
+                                    const uint32_t h = half2_bits(lo_of(ww), hi_of(ww));
+                                    most = __hmax2(most, *reinterpret_cast<const __half2*>(&h));
+                                    w[8 * g + e / 2] = h;
+                                }
+                            }
+                            const float more = lo_of(sums) + hi_of(sums);
+                            const bool fits = !__hisinf(__low2half(most)) && !__hisinf(__high2half(most)) && !(more > 1e37f) &&
+                                              m > -INFINITY;
+                            if (__all_sync(0xffffffffu, fits)) {
+                                l += more;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    tmem_st_x16(s_at + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * c));
+                                tmem_st_wait();
+                                tc_fence_before();
+                                mbar_arrive(p_full + 8 * half);
+                                continue;
+                            }
+                        }
+                    }
                     // the largest score, and the largest with its page's bound
                     float top = -INFINITY, over = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kTile; c += 32) {
                         uint32_t sc[32];
                         tmem_ld_x32(s_at + c, sc);
@@ -487,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         l *= exp2_of(m - top);
                         m = top;
                     }
-                    // o's reference: p s_v between 2^8 and 2^14 at its largest (scale_bound is 14 below), moved where it
-                    // would pass 2^14
+                    // o's reference: p s_v is 2^8 (16-bit rows: 2^4) at its largest (scale_bound is 14 below), and the
+                    // reference moves where it would pass 2^14
                     const bool move = over > ref;
                     if (__any_sync(0xffffffffu, move)) {
-                        const float now = move ? over + 6.0f : ref;
+                        const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
                         if (!first) {
                             // (O is whole once the unit two before is)
                             ok = mbar_wait(v_free + 8 * half, phase(i) ^ 1, p.err, kDevErrTimeout);
@@ -501,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             }
                             tc_fence_after();
                             const float f = move ? exp2_of(ref - now) : 1.0f;
+#pragma unroll 1
                             for (int c = 0; c < D; c += 8) {
                                 uint32_t o[8];
                                 tmem_ld_32x32b_x8(o_at + c, o);
@@ -516,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     first = false;
                     const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
                     uint64_t sums = 0;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kTile; c += 32) {
                         uint32_t sc[32], w[16], rest[16];
                         tmem_ld_x32(s_at + c, sc);
@@ -581,6 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     if (!work.whole && r < rows && half == 0)
                         *reinterpret_cast<float4*>(slot) = make_float4(m_all, l_all, ref_all, 0.0f);
                     const bool nan_seen = nan_flag != 0;
+                    const float f_all = row_factor(work.bad, m_all, l_all, ref_all);
+                    T* const to = static_cast<T*>(p.out) + (work.start + token) * p.out_t +
+                                  (head * p.group + row - token * p.group) * p.out_h;
                     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
                         uint32_t a[8], b[8];
                         tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
@@ -607,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                         if ((v[e] & 0x7F) == 0x7F) y[e] = nan;
                                 }
                             }
-                        const float4 y0 = make_float4(y[0], y[1], y[2], y[3]), y1 = make_float4(y[4], y[5], y[6], y[7]);
                         if (work.whole) {
-                            write_row<T>(p, work, r, c, m_all, l_all, ref_all, y0);
-                            write_row<T>(p, work, r, c + 4, m_all, l_all, ref_all, y1);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] *= f_all;
+                            kv_store8(to + c, p.wide_out, y);
                         } else {
-                            *reinterpret_cast<float4*>(slot + 4 + c) = y0;
-                            *reinterpret_cast<float4*>(slot + 8 + c) = y1;
+                            *reinterpret_cast<float4*>(slot + 4 + c) = make_float4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<float4*>(slot + 8 + c) = make_float4(y[4], y[5], y[6], y[7]);
                         }
                     }
                     tc_fence_before();
