@@ -934,7 +934,7 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;
     cudaError_t e;
-    if (max_rows > 16 && p.D <= 128) e = launch_prompt(dtype, p, d->sms, stream);
+    if (max_rows > 16 && p.D <= 128) e = launch_prompt(dtype, p, max_rows, d->sms, stream);
     else if (dtype == EMU_F32) e = launch_typed<float>(p, *cache, max_rows, d, stream);
     else if (dtype == EMU_BF16) e = launch_typed<__nv_bfloat16>(p, *cache, max_rows, d, stream);
     else e = launch_typed<__half>(p, *cache, max_rows, d, stream);

@@ -10,7 +10,7 @@
 namespace emu {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKvSlotRows = 128;                     // rows of a segment at most
+constexpr int kKvSlotRows = 256;                     // rows of a segment at most
 
 struct Work;
 struct AttnParams {
@@ -121,6 +121,6 @@ __device__ __forceinline__ float share_of(float ref, float ref_all) {
 cudaError_t launch_join(int dtype, const AttnParams& p, unsigned ctas, unsigned rows, cudaStream_t stream);
 
 // Many rows of a sequence (kv_prompt.cu), D up to 128.
-cudaError_t launch_prompt(int dtype, const AttnParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_prompt(int dtype, const AttnParams& p, int64_t max_rows, int sms, cudaStream_t stream);
 
 }  // namespace emu

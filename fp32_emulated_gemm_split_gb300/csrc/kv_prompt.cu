@@ -2,12 +2,12 @@
 // sequence (prompts, drafts of many query heads); the mathematics is
 // kv_attention.cu's.
 //
-// A segment is 128 rows (a key head's query heads, of one token after another), a
+// A segment is 128 or 256 rows (a key head's query heads, of one token after another), a
 // unit 128 tokens of it.  Bound by the tensor cores and the exponentials, which
 // take about as long: S = Q K^T and O = P V are tcgen05 MMAs of 128 x 128 (x D),
 // S, P and O in tensor memory, P over the S that it came from.  Roles of a CTA, one per SM:
-// four warps read codes and write them as FP16 into swizzled tiles, one issues
-// MMAs, and two groups of four turn S into P, a thread a row.  The groups take the
+// one warp copies codes into a ring (bulk copies: as loads, 32 KB a unit waited for the
+// L1's misses in flight), four write them as FP16 into swizzled tiles, one issues MMAs, and two groups of four turn S into P, a thread a row.  The groups take the
 // units in turn and each has an O of its own, so that one's exponentials run beside
 // the other's products; their sums are joined at the segment's end, as are those of
 // CTAs that share a segment (kv_join_kernel).  The CTAs take equal consecutive
@@ -24,21 +24,25 @@ namespace {
 constexpr int kTile = 128;                           // rows of a segment, tokens of a unit
 constexpr int kPanel = kTile * 128;                  // 128 rows of 64 FP16 values, swizzled
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
-constexpr int kThreads = (kSoftWarps + kCodeWarps + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kHalf = kTile / 2;                     // tokens of a copied piece: keys, keys, values, values of a unit
 
 // ------------------------------------------------- tiles of a sequence --
 
 // Tile i of a sequence: its units from first(i) to end(i), in the order of tiles and, within one, heads.
+template <int ROWS>
 struct Tiles {
+    static constexpr int kSlope = ROWS / kTile;      // units that a tile `group` tiles on lies further
     int n, group, pos0, window, count;
     __device__ __forceinline__ Tiles(const AttnParams& p, const Seq& s)
         : n(s.n), group(p.group), pos0(max(s.len, 0) - s.n), window(p.window),
-          count((int)(((int64_t)s.n * p.group + kTile - 1) / kTile)) {}
+          count((int)(((int64_t)s.n * p.group + ROWS - 1) / ROWS)) {}
     __device__ __forceinline__ int64_t end_token(int64_t i) const {      // behind the last one that a row sees, any tile but the last
-        return (int64_t)pos0 + (kTile * (i + 1) - 1) / group + 1;
+        return (int64_t)pos0 + (ROWS * (i + 1) - 1) / group + 1;
     }
     __device__ __forceinline__ int64_t first_token(int64_t i) const {    // negative: none before
-        return window ? (int64_t)pos0 + kTile * i / group - window + 1 : -1;
+        return window ? (int64_t)pos0 + ROWS * i / group - window + 1 : -1;
     }
     __device__ __forceinline__ int first(int i) const { return (int)(max(first_token(i), (int64_t)0) / kTile); }
     __device__ __forceinline__ int end(int i) const {                    // (a tile that sees nothing has a unit: it is written)
@@ -46,12 +50,12 @@ struct Tiles {
         return (int)max((e + kTile - 1) >> 7, (int64_t)1);
     }
     __device__ __forceinline__ int units(int i) const { return end(i) - first(i); }
-    // sum of max(low, a + k) over 0 <= k < c
+    // sum of max(low, a + kSlope k) over 0 <= k < c
     static __device__ __forceinline__ int64_t ramp(int64_t a, int64_t c, int64_t low) {
-        const int64_t flat = min(max(low - a, (int64_t)0), c);
-        return flat * low + (c - flat) * a + (c - 1 + flat) * (c - flat) / 2;
+        const int64_t flat = min((max(low - a, (int64_t)0) + kSlope - 1) / kSlope, c);
+        return flat * low + (c - flat) * a + kSlope * (c - 1 + flat) * (c - flat) / 2;
     }
-    // Units of the first m tiles, m < count: a tile `group` tiles on lies 128 tokens on.
+    // Units of the first m tiles, m < count: a tile `group` tiles on lies ROWS tokens on.
     __device__ __forceinline__ int64_t before(int64_t m) const {
         int64_t sum = 0;
         for (int64_t r = 0; r < min((int64_t)group, m); ++r) {
@@ -102,28 +106,56 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// How a CTA's rows and shared memory are shared out.
+//
+// PAIR (16-bit rows, more than 128 of a sequence): a segment of 256 rows, a tile of 128 for
+// each group, every unit for both: half the codes per row are copied and turned.  Otherwise 128
+// rows, and the groups take units in turn (few rows; FP32 rows, whose two pieces of Q fill the place).
+template <typename T, int NG, bool PAIR>
+struct Plan {
+    static constexpr bool TWO = sizeof(T) == 4;
+    static constexpr int rows = PAIR ? 2 * kTile : kTile;
+    static constexpr int q_tiles = PAIR || TWO ? 2 : 1;          // tiles of Q, or pieces
+    static constexpr int k_stages = PAIR ? 1 : 2, v_stages = PAIR || TWO ? 1 : 2;
+    static constexpr int piece = kHalf * NG * 64;                // bytes of a piece of codes
+    static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
+    static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
+    static constexpr int bytes = tiles + slots * piece;
+};
+
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
 // ------------------------------------------------------------- kernel --
 
-template <typename T, int NG>
+template <typename T, int NG, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ AttnParams p) {
     constexpr bool TWO = sizeof(T) == 4;
     constexpr int PIECES = TWO ? 2 : 1;
+    static_assert(!(PAIR && TWO), "one piece of each tile");
+    using Pl = Plan<T, NG, PAIR>;
+    using Ti = Tiles<Pl::rows>;
+    constexpr int SLOTS = Pl::slots, KS = Pl::k_stages, VS = Pl::v_stages, kStageBytes = NG * kPanel;
     extern __shared__ __align__(1024) uint8_t smem[];
-    // q: [piece][64 values], k and v: [stage][64 values] panels
-    const uint32_t q_at = smem_u32(smem), k_at = q_at + PIECES * NG * kPanel, v_at = k_at + 2 * NG * kPanel;
-    __shared__ __align__(8) uint64_t bars[18];
+    // q: [tile or piece][64 values], k and v: [stage][64 values] panels; then the ring of codes as they are
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + Pl::q_tiles * kStageBytes, v_at = k_at + KS * kStageBytes,
+                   raw_at = v_at + VS * kStageBytes;
+    __shared__ __align__(8) uint64_t bars[24 + 2 * SLOTS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, nan_flag;
     __shared__ int64_t warp_sum[kThreads / 32];
     __shared__ Work work;
-    // of a unit's tiles of 16 tokens: keys, values (four units: a group may still read its unit's while the
-    // next but one's keys are stored; five later its weights are done)
-    __shared__ float scales[4][2][8];
+    // of a unit's tiles of 16 tokens: keys, values (eight units: a group may still read a unit's while the copies
+    // are four ahead)
+    __shared__ float scales[8][2][8];
+    __shared__ uint32_t present[SLOTS];              // of a piece's tiles of 16 tokens: those that were copied
     __shared__ float q_top[2][kTile];
     __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
     const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
                    s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 104,
-                   c_full = k_full + 112;
+                   c_full = k_full + 112, o_done = k_full + 176, raw_full = k_full + 192, raw_free = raw_full + 8 * SLOTS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D;
     volatile int* const aborted = &abort_flag;
     const float nan = __uint_as_float(0x7FC00000u);
@@ -136,14 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             mbar_init(v_free + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, kTile);
+            mbar_init(o_done + 8 * i, 1);
         }
         mbar_init(q_full, kSoftWarps * 32);
         mbar_init(drained, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(c_full + 8 * i, 8);
+        for (int i = 0; i < 8; ++i) mbar_init(c_full + 8 * i, 8);
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_free + 8 * i, kCodeWarps);
+        }
         abort_flag = nan_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kSoftWarps + kCodeWarps) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(smem_u32(&tmem_slot)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -154,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     int64_t mine = 0;
     for (int b = tid * per; b < min((tid + 1) * per, p.B); ++b) {
         const Seq s = seq_of(p, b);
-        mine += Tiles(p, s).all() * p.heads;
+        mine += Ti(p, s).all() * p.heads;
         if (blockIdx.x == 0 && (s.len < 0 || p.starts[b + 1] < s.start || s.start < 0 || p.starts[b + 1] > p.T))
             record_error(p.err, kDevErrValue);
     }
@@ -184,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             int64_t before = sum - mine;
             int b = tid * per;
             for (;; ++b) {
-                const int64_t n = Tiles(p, seq_of(p, b)).all() * p.heads;
+                const int64_t n = Ti(p, seq_of(p, b)).all() * p.heads;
                 if (begin < before + n) break;
                 before += n;
             }
@@ -198,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         __syncthreads();
         {
             // the tile of the sequence: every thread tries some, twice where there are many
-            const Tiles ti(p, seq_of(p, work.seq));
+            const Ti ti(p, seq_of(p, work.seq));
             const int64_t u = (work.at - work.base) / p.heads;
             __shared__ int found;
             int lo = 0, hi = ti.count;               // in [lo, hi)
@@ -218,24 +255,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 const int units = ti.units(lo);
                 work.head = (int)((work.at - work.begin) / units);
                 work.begin += (int64_t)work.head * units;
-                work.row0 = lo * kTile;
+                work.row0 = lo * Pl::rows;
             }
         }
-        uint32_t j = 0;                              // units of this CTA so far
+        uint32_t j = 0, second = 0, pieces = 0;      // units, those of a second tile, copied pieces of this CTA so far
         uint32_t segments = 0;
         for (;;) {
             __syncthreads();
             // ------------------------------------------------ the segment
             if (tid == 0) {
                 const Seq s = seq_of(p, work.seq);
-                const Tiles ti(p, s);
-                const int i = work.row0 / kTile, units = ti.units(i);
+                const Ti ti(p, s);
+                const int i = work.row0 / Pl::rows, units = ti.units(i);
                 work.bad = s.len < 0;
                 work.start = s.start;
                 work.len = max(s.len, 0);
                 work.pos0 = work.len - s.n;
                 work.end = work.begin + units;
-                work.rows = min(kTile, (int)min((int64_t)s.n * p.group - work.row0, (int64_t)kTile));
+                work.rows = (int)min((int64_t)s.n * p.group - work.row0, (int64_t)Pl::rows);
                 work.token0 = (ti.first(i) + (int)(work.at - work.begin)) * kTile;
                 work.units = (int)(min(work.stop, work.end) - work.at);
                 work.starts = work.at == work.begin;
@@ -249,197 +286,274 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
             const int sees_end = max(0, min(len, pos_last + 1));
             const int sees_begin = p.window ? max(0, pos_first - p.window + 1) : 0;
-            // whether some row does not see some token of a unit
-            auto edge_of = [&](int tok) {
-                return tok + kTile > pos_first + 1 || tok + kTile > len || (p.window && tok <= pos_last - p.window);
+            // whether some row (from the first's position to the last's) does not see some token of a unit
+            auto hides = [&](int tok, int pos_a, int pos_b) {
+                return tok + kTile > pos_a + 1 || tok + kTile > len || (p.window && tok <= pos_b - p.window);
             };
+            auto edge_of = [&](int tok) { return hides(tok, pos_first, pos_last); };
             const uint32_t j0 = j, j1 = j + units;
-            auto phase = [](uint32_t i) { return i >> 1 & 1; };
+            const bool both = PAIR && rows > kTile;  // (a second tile)
+            // phases: of unit i's stages of keys and values, and of its scores in group t
+            auto k_phase = [](uint32_t i) { return i / KS & 1; };
+            auto v_phase = [](uint32_t i) { return i / VS & 1; };
+            auto s_phase = [&](uint32_t i, uint32_t t) { return PAIR ? (t ? second + (i - j0) : i) & 1 : i >> 1 & 1; };
 
-            if (warp >= kSoftWarps + kCodeWarps) {
+            if (warp == kMmaWarp) {
                 // ------------------------------------------------- MMAs
                 const uint32_t leader = elect_one();
                 const uint32_t idesc_s = make_idesc(0u, kTile, kTile), idesc_o = make_idesc(0u, kTile, D) | kIdescBMn;
+                const uint64_t q_desc = make_sw128_kmajor_desc(q_at), k_desc = make_sw128_kmajor_desc(k_at),
+                               v_desc = make_sw128_mn_desc(v_at, kPanel);
+                constexpr uint32_t kStage = kStageBytes >> 4;        // a stage (a tile, a piece of Q) in descriptors
                 ok = ok && mbar_wait(q_full, segments & 1, p.err, kDevErrTimeout);
-                auto values = [&](uint32_t i) {      // O += P V
-                    const uint32_t s = i & 1;
-                    ok = ok && mbar_wait(v_full + 8 * s, phase(i), p.err, kDevErrTimeout) &&
-                         mbar_wait(p_full + 8 * s, phase(i), p.err, kDevErrTimeout) && !*aborted;
+                auto scores = [&](uint32_t i, uint32_t t, uint32_t q) {      // S = Q K^T, group t
+                    const uint64_t b = k_desc + i % KS * kStage;
+#pragma unroll
+                    for (int piece = PIECES - 1; piece >= 0; --piece)
+#pragma unroll
+                        for (int k = 0; k < NG * 4; ++k)
+                            if (k < D / 16) {
+                                const uint32_t step = (k / 4) * (kPanel >> 4) + (k % 4) * 2;
+                                mma_cta1(tmem + t * kTile, q_desc + (q + piece) * kStage + step, b + step, idesc_s,
+                                         piece < PIECES - 1 || k > 0, leader);
+                            }
+                };
+                auto values = [&](uint32_t i, uint32_t t, bool go_on, bool last) {   // O += P V; last: V's stage is free behind it
+                    ok = ok && mbar_wait(v_full + 8 * (i % VS), v_phase(i), p.err, kDevErrTimeout) &&
+                         mbar_wait(p_full + 8 * t, s_phase(i, t), p.err, kDevErrTimeout) && !*aborted;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint64_t b = make_sw128_mn_desc(v_at + s * NG * kPanel, kPanel);
+                    const uint64_t b = v_desc + i % VS * kStage;
+                    const uint32_t o = tmem + (2 + t) * kTile, a = tmem + t * kTile;
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k) {
                         // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
-                        const uint32_t a = tmem + s * kTile + 32 * (k / 2) + 8 * (k % 2);
                         if constexpr (TWO)
-                            mma_cta1_ta(tmem + 2 * kTile + s * kTile, a + 16, b + k * (2048 >> 4), idesc_o, k > 0 || i >= j0 + 2, leader);
-                        mma_cta1_ta(tmem + 2 * kTile + s * kTile, a, b + k * (2048 >> 4), idesc_o, TWO || k > 0 || i >= j0 + 2, leader);
+                            mma_cta1_ta(o, a + 16 + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, k > 0 || go_on, leader);
+                        mma_cta1_ta(o, a + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, TWO || k > 0 || go_on, leader);
                     }
-                    tc_commit(v_free + 8 * s, leader);
+                    tc_commit(o_done + 8 * t, leader);
+                    if (last) tc_commit(v_free + 8 * (i % VS), leader);
                 };
+                // (MMAs run in the order of their issue: P is read before the next S is written over it)
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
-                    const uint32_t s = i & 1;
-                    ok = ok && mbar_wait(k_full + 8 * s, phase(i), p.err, kDevErrTimeout) && !*aborted;
+                    ok = ok && mbar_wait(k_full + 8 * (i % KS), k_phase(i), p.err, kDevErrTimeout) && !*aborted;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int piece = PIECES - 1; piece >= 0; --piece)
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t step = (k / 4) * kPanel + (k % 4) * 32;
-                            mma_cta1(tmem + s * kTile, make_sw128_kmajor_desc(q_at + piece * NG * kPanel + step),
-                                     make_sw128_kmajor_desc(k_at + s * NG * kPanel + step), idesc_s,
-                                     piece < PIECES - 1 || k > 0, leader);
+                    if constexpr (PAIR) {
+                        if (i > j0) values(i - 1, 0, i - 1 > j0, !both);
+                        if (!ok) break;
+                        scores(i, 0, 0);
+                        tc_commit(s_full, leader);
+                        if (both) {
+                            if (i > j0) values(i - 1, 1, i - 1 > j0, true);
+                            if (!ok) break;
+                            scores(i, 1, 1);
+                            tc_commit(s_full + 8, leader);
                         }
-                    tc_commit(k_free + 8 * s, leader);
-                    tc_commit(s_full + 8 * s, leader);
-                    if (i > j0) values(i - 1);
+                        tc_commit(k_free, leader);
+                    } else {
+                        scores(i, i & 1, 0);
+                        tc_commit(s_full + 8 * (i & 1), leader);
+                        tc_commit(k_free + 8 * (i % KS), leader);
+                        if (i > j0) values(i - 1, (i - 1) & 1, i - 1 >= j0 + 2, true);
+                    }
                 }
-                if (ok) values(j1 - 1);
+                if (ok && PAIR) {
+                    values(j1 - 1, 0, units > 1, !both);
+                    if (ok && both) values(j1 - 1, 1, units > 1, true);
+                } else if (ok) {
+                    values(j1 - 1, (j1 - 1) & 1, units > 2, true);
+                }
                 if (!ok) *aborted = 1;
-            } else if (warp >= kSoftWarps) {
-                // ------------------------------------------------ codes
-                const int ct = tid - kSoftWarps * 32, piece = ct & 3;
+            } else if (warp == kCopyWarp) {
+                // ----------------------------------------------- copies
                 const int32_t* pages = p.table + (int64_t)work.seq * p.width;
-                // lane L < 8 looks after tile L of 16 tokens: its page (-1: bad, -2: no row sees it)
+                const int P = 1 << p.page_log, run = min(P, kHalf);          // tokens of a copy
+                // lane L < 8 looks after tile L of 16 tokens of a unit: its page (-1: bad, -2: no row sees it)
                 auto page_of = [&](uint32_t i) {
                     const int tok = token0 + (int)(i - j0) * kTile + 16 * (lane & 7);
                     if (i >= j1 || tok >= sees_end || tok + 16 <= sees_begin) return -2;
                     const int page = pages[tok >> p.page_log];
                     return page >= 0 && page < p.pages ? page : -1;
                 };
-                uint4 raw_k[NG * 4], raw_v[NG * 4];
-                auto load = [&](uint4 (&raw)[NG * 4], const uint8_t* from, uint32_t i, int page_lane) {
-                    const int tok0 = token0 + (int)(i - j0) * kTile;
+                int page_next = page_of(j0);
+                uint32_t g = pieces;
+                for (uint32_t i = j0; i < j1 && ok; ++i) {
+                    const int page = page_next, tok = token0 + (int)(i - j0) * kTile + 16 * (lane & 7);
+                    page_next = page_of(i + 1);
+                    const int64_t place = (int64_t)max(page, 0) * p.heads + head;
+                    if (page == -1) record_error(p.err, kDevErrValue);
+                    const float none = page == -1 ? nan : 0.0f;
+                    const float ks = page >= 0 ? __ldg(p.ks + place) : none, vs = page >= 0 ? __ldg(p.vs + place) : none;
+                    // A copy brings what it covers of a page, seen or not: a page of 64 tokens and more has one for
+                    // a piece, by the lane of its first tile that is seen.
+                    const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xFF;
+                    const int first = (lane & 7) & ~(run / 16 - 1);          // of the tiles of this lane's copy
+                    const uint32_t of_copy = ((1u << run / 16) - 1) << first;
+                    const bool copies = lane < 8 && (seen & of_copy) && (31 - __clz((seen & of_copy) & -(seen & of_copy))) == lane;
+                    const int from = (tok - 16 * ((lane & 7) - first)) & (P - 1);
+                    const int64_t offset = ((place << p.page_log) + from) * D;
+                    const uint32_t who = __ballot_sync(0xffffffffu, copies);
 #pragma unroll
-                    for (int st = 0; st < 4; ++st) {
-                        const int in_tile = st * 32 + (ct >> 2), tok = tok0 + in_tile;
-                        const int page = __shfl_sync(0xffffffffu, page_lane, in_tile >> 4);
-                        const uint8_t* row = from + (((((int64_t)page * p.heads + head) << p.page_log) +
-                                                      (tok & ((1 << p.page_log) - 1))) * D + piece * 16);
-                        const bool in = page >= 0 && tok >= sees_begin && tok < sees_end;
-#pragma unroll
-                        for (int n = 0; n < NG; ++n)
-                            raw[n * 4 + st] = in && n * 64 + piece * 16 < D ? __ldg(reinterpret_cast<const uint4*>(row + n * 64))
-                                                                             : make_uint4(0, 0, 0, 0);
+                    for (int piece = 0; piece < 4; ++piece, ++g) {
+                        const uint32_t slot = g % SLOTS, bar = raw_full + 8 * slot;
+                        ok = ok && mbar_wait(raw_free + 8 * slot, (g / SLOTS & 1) ^ 1, p.err, kDevErrTimeout) && !*aborted;
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint32_t mine = 0xFu << 4 * (piece & 1);
+                        if (lane == 0) {
+                            present[slot] = (seen & mine) >> 4 * (piece & 1);
+                            mbar_arrive_expect_tx(bar, __popc(who & mine) * run * D);
+                        }
+                        __syncwarp();
+                        if (copies && (1u << lane & mine))
+                            copy_bytes(raw_at + slot * Pl::piece + (first & 3) * 16 * D, (piece < 2 ? p.k : p.v) + offset,
+                                       run * D, bar);
                     }
+                    if (lane < 8) {
+                        scales[i & 7][0][lane] = ks;
+                        scales[i & 7][1][lane] = vs;
+                        mbar_arrive(c_full + 8 * (i & 7));
+                    }
+                }
+                if (!ok) {
+                    // no copy may land after this CTA is gone
+                    *aborted = 1;
+                    for (uint32_t x = g > SLOTS ? g - SLOTS : 0; x < g; ++x)
+                        mbar_wait(raw_full + 8 * (x % SLOTS), x / SLOTS & 1, p.err, kDevErrTimeout);
+                }
+            } else if (warp >= kSoftWarps) {
+                // ------------------------------------------------ codes
+                // A thread has 16 values of rows r and r + 32 of a piece (64 tokens) and panel: two rows' quarters by eight
+                // lanes, whose stores meet all banks.
+                const int ct = tid - kSoftWarps * 32, r = ct >> 2, quarter = ct & 3;
+                const uint32_t load_at = r * D + quarter * 16, store_at = r * 128 + (quarter * 32 ^ (r & 7) << 4);
+                auto halves = [&](const uint4& v, uint32_t to) {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[2 * e] = kv_half2((uint16_t)w[e]);
+                        h[2 * e + 1] = kv_half2((uint16_t)(w[e] >> 16));
+                    }
+                    sts128(to, h[0], h[1], h[2], h[3]);
+                    sts128(to ^ 16, h[4], h[5], h[6], h[7]);
                 };
-                auto store = [&](const uint4 (&raw)[NG * 4], uint32_t to) {
+                uint32_t g = pieces;
+                // A piece's codes as FP16 into rows `first`.. of a tile.
+                auto turn = [&](uint32_t to, int tok, bool clean) {
+                    const uint32_t slot = g % SLOTS;
+                    ok = ok && mbar_wait(raw_full + 8 * slot, g / SLOTS & 1, p.err, kDevErrTimeout) && !*aborted;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    const uint32_t from = raw_at + slot * Pl::piece + load_at, there = present[slot];
+                    uint4 v[NG * 2];
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
-                        for (int st = 0; st < 4; ++st) {
-                            const int row = st * 32 + (ct >> 2);
-                            const uint32_t at = to + n * kPanel + row * 128, x = (row & 7) << 4;
-                            const uint32_t w[4] = {raw[n * 4 + st].x, raw[n * 4 + st].y, raw[n * 4 + st].z, raw[n * 4 + st].w};
-                            uint32_t h[8];
+                        for (int h = 0; h < 2; ++h)
+                            if (n * 64 + quarter * 16 < D)
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(v[2 * n + h].x), "=r"(v[2 * n + h].y), "=r"(v[2 * n + h].z), "=r"(v[2 * n + h].w)
+                                             : "r"(from + n * 64 + h * 32 * D) : "memory");
+                    if (clean || there != 0xF || tok < sees_begin || tok + kHalf > sees_end) {
+                        uint32_t nans = 0;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                h[2 * e] = kv_half2((uint16_t)w[e]);
-                                h[2 * e + 1] = kv_half2((uint16_t)(w[e] >> 16));
+                        for (int n = 0; n < NG * 2; ++n) {
+                            const int row = r + 32 * (n & 1);
+                            if (!(there >> (row >> 4) & 1) || tok + row < sees_begin || tok + row >= sees_end)
+                                v[n] = make_uint4(0, 0, 0, 0);
+                            if (clean && n / 2 * 64 + quarter * 16 < D) {
+                                // a NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken
+                                // out here and put into those rows at the end
+                                uint32_t* const w[4] = {&v[n].x, &v[n].y, &v[n].z, &v[n].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t x = nan_bytes(*w[e]);
+                                    *w[e] &= ~x;
+                                    nans |= x;
+                                }
                             }
-                            sts128(at + (piece * 32 ^ x), h[0], h[1], h[2], h[3]);
-                            sts128(at + ((piece * 32 + 16) ^ x), h[4], h[5], h[6], h[7]);
                         }
+                        if (nans) nan_flag = 1;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (n * 64 + quarter * 16 < D) halves(v[2 * n + h], to + store_at + n * kPanel + h * 32 * 128);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_free + 8 * slot);
+                    ++g;
                 };
-                // pages two units ahead, codes and scales one: a unit's codes are on the way while those of the one
-                // before are written
-                int page = page_of(j0), page_next = page_of(j0 + 1);
-                auto scale_of = [&](int pg, const float* from) {
-                    return pg >= 0 ? __ldg(from + (int64_t)pg * p.heads + head) : pg == -1 ? nan : 0.0f;
-                };
-                float ks = scale_of(page, p.ks), vs = scale_of(page, p.vs);
-                load(raw_k, p.k, j0, page);
-                load(raw_v, p.v, j0, page);
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
-                    const uint32_t s = i & 1;
-                    if (page == -1) record_error(p.err, kDevErrValue);
-                    ok = mbar_wait(k_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
-                    if (!ok) break;
-                    store(raw_k, k_at + s * NG * kPanel);
-                    if (ct < 8) {
-                        scales[i & 3][0][ct] = ks;
-                        scales[i & 3][1][ct] = vs;
-                        mbar_arrive(c_full + 8 * (i & 3));
+                    const int tok = token0 + (int)(i - j0) * kTile;
+                    const bool edge = edge_of(tok);
+#pragma unroll 1
+                    for (int side = 0; side < 2 && ok; ++side) {
+                        const uint32_t s = side ? i % VS : i % KS, to = (side ? v_at : k_at) + s * kStageBytes;
+                        ok = mbar_wait((side ? v_free : k_free) + 8 * s, (side ? v_phase(i) : k_phase(i)) ^ 1, p.err, kDevErrTimeout) &&
+                             !*aborted;
+                        ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) turn(to + h * kHalf * 128, tok + h * kHalf, edge && side);
+                        if (!ok) break;
+                        fence_async_smem();
+                        mbar_arrive((side ? v_full : k_full) + 8 * s);
                     }
-                    fence_async_smem();
-                    mbar_arrive(k_full + 8 * s);
-                    page = page_next;
-                    page_next = page_of(i + 2);
-                    if (i + 1 < j1) {
-                        load(raw_k, p.k, i + 1, page);
-                        ks = scale_of(page, p.ks);
-                        vs = scale_of(page, p.vs);
-                    }
-                    const bool edge = edge_of(token0 + (int)(i - j0) * kTile);
-                    ok = mbar_wait(v_free + 8 * s, phase(i) ^ 1, p.err, kDevErrTimeout) && !*aborted;
-                    if (!ok) break;
-                    if (edge) {
-                        // a NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken out
-                        // here and put into those rows at the end
-                        uint32_t any = 0;
-#pragma unroll
-                        for (int n = 0; n < NG * 4; ++n) {
-                            uint32_t* const w[4] = {&raw_v[n].x, &raw_v[n].y, &raw_v[n].z, &raw_v[n].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t x = nan_bytes(*w[e]);
-                                *w[e] &= ~x;
-                                any |= x;
-                            }
-                        }
-                        if (any) nan_flag = 1;
-                    }
-                    store(raw_v, v_at + s * NG * kPanel);
-                    fence_async_smem();
-                    mbar_arrive(v_full + 8 * s);
-                    if (i + 1 < j1) load(raw_v, p.v, i + 1, page);
                 }
                 if (!ok) *aborted = 1;
             } else {
                 // --------------------------------------------- scores to weights
-                const int half = warp >> 2, r = tid & (kTile - 1);       // group, row
+                const int half = warp >> 2, r = tid & (kTile - 1);       // group, row of its tile
                 const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-                // Q: this thread's row, the values of its group's part
-                const int row = row0 + min(r, rows - 1), token = row / p.group, pos = pos0 + token;
+                const int tile_row = PAIR ? half * kTile : 0;    // the tile's first row of the segment
+                const bool idle = PAIR && half && !both;         // no row in the tile
+                const int row = row0 + min(tile_row + r, rows - 1), token = row / p.group, pos = pos0 + token;
+                const int pos_a = pos0 + (row0 + min(tile_row, rows - 1)) / p.group;
+                const int pos_b = pos0 + (row0 + min(tile_row + kTile, rows) - 1) / p.group;
+                // Q: this thread's row, or of one tile the values of its group's half, twice (the largest first)
                 float factor;
                 {
-                    constexpr int MINE = NG * 32;    // values
+                    constexpr int MINE = PAIR ? NG * 64 : NG * 32;
+                    const int d0 = PAIR ? 0 : half * MINE;
                     const T* from = static_cast<const T*>(p.q) + (work.start + token) * p.q_t +
                                     (head * p.group + row - token * p.group) * p.q_h;
-                    float x[MINE];
                     float top = 0.0f;
+#pragma unroll 4
+                    for (int d = d0; d < min(d0 + MINE, D); d += 8) {
+                        float x[8];
+                        kv_load8(from + d, p.wide, x);
 #pragma unroll
-                    for (int c = 0; c < MINE; c += 8) {
-                        const int d = half * MINE + c;
-                        if (d < D) kv_load8(from + d, p.wide, x + c);
-                        else
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[c + e] = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[c + e]));
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
                     }
-                    q_top[half][r] = top;
-                    bar_and(1, kSoftWarps * 32, true);
-                    top = fmaxf(q_top[0][r], q_top[1][r]);
+                    if constexpr (!PAIR) {
+                        q_top[half][r] = top;
+                        bar_and(1, kSoftWarps * 32, true);
+                        top = fmaxf(q_top[0][r], q_top[1][r]);
+                    }
                     // 2^(14 - E), top = m 2^E; a negative scale turns q
                     const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
                     const float up = copysignf(__uint_as_float((uint32_t)(14 - E + 127) << 23), p.scale);
                     factor = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (fabsf(p.scale) * kLog2e);
-#pragma unroll
-                    for (int c = 0; c < MINE; c += 8) {
-                        const int d = half * MINE + c;
+#pragma unroll 2
+                    for (int d = d0; d < min(d0 + MINE, D); d += 8) {
+                        float x[8];
+                        kv_load8(from + d, p.wide, x);
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float a = x[c + 2 * e] * up, b = x[c + 2 * e + 1] * up;
+                            const float a = x[2 * e] * up, b = x[2 * e + 1] * up;
                             hi[e] = half2_bits(a, b);
                             lo[e] = TWO ? half2_rest(a, b, hi[e]) : 0u;
                         }
-                        const uint32_t at = q_at + (d / 64) * kPanel + r * 128 + ((d % 64 * 2) ^ ((r & 7) << 4));
+                        const uint32_t at = q_at + (PAIR ? half * kStageBytes : 0) + (d / 64) * kPanel + r * 128 +
+                                            ((d % 64 * 2) ^ ((r & 7) << 4));
                         sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                        if (TWO) sts128(at + NG * kPanel, lo[0], lo[1], lo[2], lo[3]);
+                        if (TWO) sts128(at + kStageBytes, lo[0], lo[1], lo[2], lo[3]);
                     }
                     fence_async_smem();
                     mbar_arrive(q_full);
@@ -448,19 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 float m = -INFINITY, l = 0.0f, ref = -INFINITY;
                 const uint32_t s_at = (tmem + half * kTile) | lanes, o_at = (tmem + (2 + half) * kTile) | lanes;
                 bool first = true;
-                for (uint32_t i = j0 + ((j0 ^ half) & 1); i < j1 && ok; i += 2) {
-                    ok = mbar_wait(s_full + 8 * half, phase(i), p.err, kDevErrTimeout) &&
-                         mbar_wait(c_full + 8 * (i & 3), i >> 2 & 1, p.err, kDevErrTimeout) && !*aborted;
+                for (uint32_t i = PAIR ? (idle ? j1 : j0) : j0 + ((j0 ^ half) & 1); i < j1 && ok; i += PAIR ? 1 : 2) {
+                    ok = mbar_wait(s_full + 8 * half, s_phase(i, half), p.err, kDevErrTimeout) &&
+                         mbar_wait(c_full + 8 * (i & 7), i >> 3 & 1, p.err, kDevErrTimeout) && !*aborted;
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const int tok = token0 + (int)(i - j0) * kTile;
-                    const bool edge = edge_of(tok);
+                    const bool edge = hides(tok, pos_a, pos_b);
                     const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
-                    const float* const ks = scales[i & 3][0];
-                    const float* const vs = scales[i & 3][1];
+                    const float* const ks = scales[i & 7][0];
+                    const float* const vs = scales[i & 7][1];
                     if constexpr (!TWO) {
                         // Most units: the maximum and the reference as they are, and P held back until it is known
                         // that none of it passed FP16's range.
@@ -537,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     if (__any_sync(0xffffffffu, move)) {
                         const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
                         if (!first) {
-                            // (O is whole once the unit two before is)
-                            ok = mbar_wait(v_free + 8 * half, phase(i) ^ 1, p.err, kDevErrTimeout);
+                            // (O is whole once the group's unit before is)
+                            ok = mbar_wait(o_done + 8 * half, s_phase(i, half) ^ 1, p.err, kDevErrTimeout);
                             if (!__all_sync(0xffffffffu, ok)) {
                                 ok = false;
                                 break;
@@ -604,14 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 row_stat[half][r][0] = m;
                 row_stat[half][r][1] = l;
                 row_stat[half][r][2] = ref;
-                // both groups' last products (a unit's two before it are done where it is)
-                const bool two_units = units > 1;
-                if (ok) ok = mbar_wait(v_free + 8 * ((j1 - 1) & 1), phase(j1 - 1), p.err, kDevErrTimeout);
-                if (ok && two_units) ok = mbar_wait(v_free + 8 * ((j1 - 2) & 1), phase(j1 - 2), p.err, kDevErrTimeout);
+                // the last products: of this group's tile, of both groups' units
+                const bool two_units = !PAIR && units > 1;
+                if (ok && !idle) {
+                    const uint32_t t = PAIR ? half : (j1 - 1) & 1;
+                    ok = mbar_wait(o_done + 8 * t, s_phase(j1 - 1, t), p.err, kDevErrTimeout);
+                }
+                if (ok && two_units) ok = mbar_wait(o_done + 8 * ((j1 - 2) & 1), s_phase(j1 - 2, (j1 - 2) & 1), p.err, kDevErrTimeout);
                 ok = bar_and(1, kSoftWarps * 32, ok);
-                if (ok) {
+                if (ok && !idle) {
                     tc_fence_after();
-                    const uint32_t s0 = j0 & 1;      // the group that had the first unit
+                    const uint32_t s0 = PAIR ? half : j0 & 1;    // the group that had the first unit
                     const float m_a = row_stat[s0][r][0], l_a = row_stat[s0][r][1], ref_a = row_stat[s0][r][2];
                     float m_all = m_a, ref_all = ref_a, l_all = l_a, x_a = 1.0f, x_b = 0.0f;
                     if (two_units) {
@@ -622,14 +739,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         x_a = share_of(ref_a, ref_all);
                         x_b = share_of(ref_b, ref_all);
                     }
-                    float* const slot = p.partial + ((2 * (int64_t)blockIdx.x + work.starts) * p.slot_rows + r) * (D + 4);
-                    if (!work.whole && r < rows && half == 0)
+                    const bool live = tile_row + r < rows;
+                    float* const slot = p.partial + ((2 * (int64_t)blockIdx.x + work.starts) * p.slot_rows + tile_row + r) * (D + 4);
+                    if (!work.whole && live && (PAIR || half == 0))
                         *reinterpret_cast<float4*>(slot) = make_float4(m_all, l_all, ref_all, 0.0f);
                     const bool nan_seen = nan_flag != 0;
                     const float f_all = row_factor(work.bad, m_all, l_all, ref_all);
                     T* const to = static_cast<T*>(p.out) + (work.start + token) * p.out_t +
                                   (head * p.group + row - token * p.group) * p.out_h;
-                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+                    const int c_begin = PAIR ? 0 : half * (D / 2), c_end = PAIR ? D : (half + 1) * (D / 2);
+#pragma unroll 1
+                    for (int c = c_begin; c < c_end; c += 8) {
                         uint32_t a[8], b[8];
                         tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
                         if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
@@ -640,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             y[e] = __uint_as_float(a[e]) * x_a;
                             if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
                         }
-                        if (r >= rows) continue;
+                        if (!live) continue;
                         if (nan_seen)
                             for (int u = 0; u < units; ++u) {
                                 const int tok = token0 + u * kTile;
@@ -667,7 +787,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     tc_fence_before();
                 }
             }
+            if (both) second += units;
             j = j1;
+            pieces += 4 * units;
             ++segments;
             if (__syncthreads_or(!ok) || work.end >= work.stop) break;
             if (tid == 0) {
@@ -676,8 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 if (++work.head == p.heads) {
                     work.head = 0;
                     Seq s = seq_of(p, work.seq);
-                    if (work.row0 + (int64_t)kTile < (int64_t)s.n * p.group) {
-                        work.row0 += kTile;
+                    if (work.row0 + (int64_t)Pl::rows < (int64_t)s.n * p.group) {
+                        work.row0 += Pl::rows;
                     } else {
                         work.row0 = 0;
                         do s = seq_of(p, ++work.seq);
@@ -687,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
         }
         // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
-        if (warp == kSoftWarps + kCodeWarps && !ok) {
+        if (warp == kMmaWarp && !ok) {
             const uint32_t leader = elect_one();
             tc_commit(drained, leader);
             mbar_wait(drained, 0, p.err, kDevErrTimeout);
@@ -701,41 +823,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSoftWarps + kCodeWarps)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u));
 }
 
-template <typename T, int NG>
+template <typename T, int NG, bool PAIR>
 cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
-    constexpr int smem = ((sizeof(T) == 4 ? 2 : 1) + 4) * NG * kPanel;
-    auto kern = kv_prompt_kernel<T, NG>;
+    using Pl = Plan<T, NG, PAIR>;
+    auto kern = kv_prompt_kernel<T, NG, PAIR>;
     static bool done[kMaxDevices] = {};              // (g_mu is held)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!done[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::bytes);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }
-    p.slot_rows = kTile;
-    kern<<<(unsigned)sms, kThreads, smem, stream>>>(p);
+    p.slot_rows = Pl::rows;
+    kern<<<(unsigned)sms, kThreads, Pl::bytes, stream>>>(p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, 16, stream);
+    return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, Pl::rows / 8, stream);
+}
+
+template <typename T, int NG>
+cudaError_t launch_rows(const AttnParams& p, int dtype, int64_t max_rows, int sms, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2)
+        if (max_rows > kTile) return launch<T, NG, true>(p, dtype, sms, stream);
+    return launch<T, NG, false>(p, dtype, sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_typed(const AttnParams& p, int dtype, int sms, cudaStream_t stream) {
-    return p.D <= 64 ? launch<T, 1>(p, dtype, sms, stream) : launch<T, 2>(p, dtype, sms, stream);
+cudaError_t launch_typed(const AttnParams& p, int dtype, int64_t max_rows, int sms, cudaStream_t stream) {
+    return p.D <= 64 ? launch_rows<T, 1>(p, dtype, max_rows, sms, stream) : launch_rows<T, 2>(p, dtype, max_rows, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(int dtype, const AttnParams& p, int sms, cudaStream_t stream) {
-    if (dtype == EMU_F32) return launch_typed<float>(p, dtype, sms, stream);
-    if (dtype == EMU_BF16) return launch_typed<__nv_bfloat16>(p, dtype, sms, stream);
-    return launch_typed<__half>(p, dtype, sms, stream);
+cudaError_t launch_prompt(int dtype, const AttnParams& p, int64_t max_rows, int sms, cudaStream_t stream) {
+    if (dtype == EMU_F32) return launch_typed<float>(p, dtype, max_rows, sms, stream);
+    if (dtype == EMU_BF16) return launch_typed<__nv_bfloat16>(p, dtype, max_rows, sms, stream);
+    return launch_typed<__half>(p, dtype, max_rows, sms, stream);
 }
 
 }  // namespace emu
