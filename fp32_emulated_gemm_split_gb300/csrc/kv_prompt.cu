@@ -7,10 +7,12 @@
 // take about as long: S = Q K^T and O = P V are tcgen05 MMAs of 128 x 128 (x D),
 // S, P and O in tensor memory, P over the S that it came from.  Roles of a CTA, one per SM:
 // one warp copies codes into a ring (bulk copies: as loads, 32 KB a unit waited for the
-// L1's misses in flight), four write them as FP16 into swizzled tiles, one issues MMAs, and two groups of four turn S into P, a thread a row.  The groups take the
-// units in turn and each has an O of its own, so that one's exponentials run beside
-// the other's products; their sums are joined at the segment's end, as are those of
-// CTAs that share a segment (kv_join_kernel).  The CTAs take equal consecutive
+// L1's misses in flight), four write them as FP16 into swizzled tiles, and two groups of
+// four turn S into P, a thread a row, each with a warp that issues its MMAs.  Each group
+// has an O of its own (of its own rows, or of the units that it takes in turn with the
+// other), so that one's exponentials run beside the other's products; sums of the same
+// rows are joined at the segment's end, as are those of CTAs that share a segment
+// (kv_join_kernel).  The CTAs take equal consecutive
 // ranges of all units, of which a causal tile has as many as it needs.
 //
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
@@ -24,7 +26,7 @@ namespace {
 constexpr int kTile = 128;                           // rows of a segment, tokens of a unit
 constexpr int kPanel = kTile * 128;                  // 128 rows of 64 FP16 values, swizzled
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 2;    // (an issuer for each group)
 constexpr int kThreads = (kCopyWarp + 1) * 32;
 constexpr int kHalf = kTile / 2;                     // tokens of a copied piece: keys, keys, values, values of a unit
 
@@ -106,6 +108,38 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// 8 values as they lie in memory (16 or 32 bytes; wide: from a 16-byte boundary), and as FP32.
+template <typename T, int W>
+__device__ __forceinline__ void load_words(const T* from, bool wide, uint32_t (&w)[W]) {
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(from) + i);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+            w[i + 2] = v.z;
+            w[i + 3] = v.w;
+        }
+    } else {
+        T x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = from[i];
+        memcpy(w, x, sizeof(x));
+    }
+}
+template <typename T, int W>
+__device__ __forceinline__ void values_of(const uint32_t (&w)[W], float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            x[2 * i] = __uint_as_float(w[2 * i]);
+            x[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+        } else {
+            kv_widen<T>(w[i], x[2 * i], x[2 * i + 1]);
+        }
+    }
+}
+
 // How a CTA's rows and shared memory are shared out.
 //
 // PAIR (16-bit rows, more than 128 of a sequence): a segment of 256 rows, a tile of 128 for
@@ -116,7 +150,8 @@ struct Plan {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int rows = PAIR ? 2 * kTile : kTile;
     static constexpr int q_tiles = PAIR || TWO ? 2 : 1;          // tiles of Q, or pieces
-    static constexpr int k_stages = PAIR ? 1 : 2, v_stages = PAIR || TWO ? 1 : 2;
+    // (two stages of V where the groups take units in turn: each issuer then meets every phase of its own stage)
+    static constexpr int k_stages = 2, v_stages = PAIR ? 1 : 2;
     static constexpr int piece = kHalf * NG * 64;                // bytes of a piece of codes
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
     static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
@@ -151,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     // are four ahead)
     __shared__ float scales[8][2][8];
     __shared__ uint32_t present[SLOTS];              // of a piece's tiles of 16 tokens: those that were copied
-    __shared__ float q_top[2][kTile];
+    __shared__ float q_factor[2][kTile];
     __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
     const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
                    s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 104,
@@ -163,15 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full + 8 * i, kCodeWarps * 32);
-            mbar_init(k_free + 8 * i, 1);
+            mbar_init(k_free + 8 * i, PAIR ? 2 : 1);
             mbar_init(v_full + 8 * i, kCodeWarps * 32);
-            mbar_init(v_free + 8 * i, 1);
+            mbar_init(v_free + 8 * i, PAIR ? 2 : 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, kTile);
             mbar_init(o_done + 8 * i, 1);
         }
         mbar_init(q_full, kSoftWarps * 32);
-        mbar_init(drained, 1);
+        mbar_init(drained, 2);
         for (int i = 0; i < 8; ++i) mbar_init(c_full + 8 * i, 8);
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
@@ -298,74 +333,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             auto v_phase = [](uint32_t i) { return i / VS & 1; };
             auto s_phase = [&](uint32_t i, uint32_t t) { return PAIR ? (t ? second + (i - j0) : i) & 1 : i >> 1 & 1; };
 
-            if (warp == kMmaWarp) {
+            if (warp == kMmaWarp || warp == kMmaWarp + 1) {
                 // ------------------------------------------------- MMAs
+                const uint32_t t = warp - kMmaWarp;  // the group
                 const uint32_t leader = elect_one();
                 const uint32_t idesc_s = make_idesc(0u, kTile, kTile), idesc_o = make_idesc(0u, kTile, D) | kIdescBMn;
-                const uint64_t q_desc = make_sw128_kmajor_desc(q_at), k_desc = make_sw128_kmajor_desc(k_at),
-                               v_desc = make_sw128_mn_desc(v_at, kPanel);
-                constexpr uint32_t kStage = kStageBytes >> 4;        // a stage (a tile, a piece of Q) in descriptors
+                const uint64_t q_desc = make_sw128_kmajor_desc(q_at + (PAIR ? t : 0) * kStageBytes);
+                const uint64_t k_desc = make_sw128_kmajor_desc(k_at), v_desc = make_sw128_mn_desc(v_at, kPanel);
+                constexpr uint32_t kStage = kStageBytes >> 4;        // a stage (a piece of Q) in descriptors
+                const uint32_t s_at = tmem + t * kTile, o_at = tmem + (2 + t) * kTile;
+                const bool idle = PAIR && t && !both;
                 ok = ok && mbar_wait(q_full, segments & 1, p.err, kDevErrTimeout);
-                auto scores = [&](uint32_t i, uint32_t t, uint32_t q) {      // S = Q K^T, group t
-                    const uint64_t b = k_desc + i % KS * kStage;
-#pragma unroll
-                    for (int piece = PIECES - 1; piece >= 0; --piece)
-#pragma unroll
-                        for (int k = 0; k < NG * 4; ++k)
-                            if (k < D / 16) {
-                                const uint32_t step = (k / 4) * (kPanel >> 4) + (k % 4) * 2;
-                                mma_cta1(tmem + t * kTile, q_desc + (q + piece) * kStage + step, b + step, idesc_s,
-                                         piece < PIECES - 1 || k > 0, leader);
-                            }
-                };
-                auto values = [&](uint32_t i, uint32_t t, bool go_on, bool last) {   // O += P V; last: V's stage is free behind it
-                    ok = ok && mbar_wait(v_full + 8 * (i % VS), v_phase(i), p.err, kDevErrTimeout) &&
-                         mbar_wait(p_full + 8 * t, s_phase(i, t), p.err, kDevErrTimeout) && !*aborted;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t b = v_desc + i % VS * kStage;
-                    const uint32_t o = tmem + (2 + t) * kTile, a = tmem + t * kTile;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k) {
-                        // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
-                        if constexpr (TWO)
-                            mma_cta1_ta(o, a + 16 + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, k > 0 || go_on, leader);
-                        mma_cta1_ta(o, a + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, TWO || k > 0 || go_on, leader);
-                    }
-                    tc_commit(o_done + 8 * t, leader);
-                    if (last) tc_commit(v_free + 8 * (i % VS), leader);
-                };
-                // (MMAs run in the order of their issue: P is read before the next S is written over it)
-                for (uint32_t i = j0; i < j1 && ok; ++i) {
+                // (MMAs of one warp run in the order of their issue: P is read before the next S is written over it)
+                const uint32_t from = PAIR ? j0 : j0 + ((j0 ^ t) & 1);
+                for (uint32_t i = from; i < j1 && ok; i += PAIR ? 1 : 2) {
+                    // S = Q K^T
                     ok = ok && mbar_wait(k_full + 8 * (i % KS), k_phase(i), p.err, kDevErrTimeout) && !*aborted;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    if constexpr (PAIR) {
-                        if (i > j0) values(i - 1, 0, i - 1 > j0, !both);
-                        if (!ok) break;
-                        scores(i, 0, 0);
-                        tc_commit(s_full, leader);
-                        if (both) {
-                            if (i > j0) values(i - 1, 1, i - 1 > j0, true);
-                            if (!ok) break;
-                            scores(i, 1, 1);
-                            tc_commit(s_full + 8, leader);
-                        }
-                        tc_commit(k_free, leader);
-                    } else {
-                        scores(i, i & 1, 0);
-                        tc_commit(s_full + 8 * (i & 1), leader);
-                        tc_commit(k_free + 8 * (i % KS), leader);
-                        if (i > j0) values(i - 1, (i - 1) & 1, i - 1 >= j0 + 2, true);
+                    if (!idle) {
+                        const uint64_t b = k_desc + i % KS * kStage;
+#pragma unroll
+                        for (int piece = PIECES - 1; piece >= 0; --piece)
+#pragma unroll
+                            for (int k = 0; k < NG * 4; ++k)
+                                if (k < D / 16) {
+                                    const uint32_t step = (k / 4) * (kPanel >> 4) + (k % 4) * 2;
+                                    mma_cta1(s_at, q_desc + piece * kStage + step, b + step, idesc_s, piece < PIECES - 1 || k > 0, leader);
+                                }
+                        tc_commit(s_full + 8 * t, leader);
                     }
-                }
-                if (ok && PAIR) {
-                    values(j1 - 1, 0, units > 1, !both);
-                    if (ok && both) values(j1 - 1, 1, units > 1, true);
-                } else if (ok) {
-                    values(j1 - 1, (j1 - 1) & 1, units > 2, true);
+                    tc_commit(k_free + 8 * (i % KS), leader);
+                    // O += P V
+                    ok = mbar_wait(v_full + 8 * (i % VS), v_phase(i), p.err, kDevErrTimeout) &&
+                         (idle || mbar_wait(p_full + 8 * t, s_phase(i, t), p.err, kDevErrTimeout)) && !*aborted;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (!idle) {
+                        const uint64_t b = v_desc + i % VS * kStage;
+                        const bool go_on = i > from;
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k) {
+                            // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
+                            if constexpr (TWO)
+                                mma_cta1_ta(o_at, s_at + 16 + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, k > 0 || go_on, leader);
+                            mma_cta1_ta(o_at, s_at + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, TWO || k > 0 || go_on, leader);
+                        }
+                        tc_commit(o_done + 8 * t, leader);
+                    }
+                    tc_commit(v_free + 8 * (i % VS), leader);
                 }
                 if (!ok) *aborted = 1;
             } else if (warp == kCopyWarp) {
@@ -379,15 +397,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     const int page = pages[tok >> p.page_log];
                     return page >= 0 && page < p.pages ? page : -1;
                 };
-                int page_next = page_of(j0);
+                // pages two units ahead, scales one
+                int page = -2, page_next = page_of(j0), page_after = page_of(j0 + 1);
+                auto scale_of = [&](const float* from) {
+                    return page_next >= 0 ? __ldg(from + (int64_t)page_next * p.heads + head) : page_next == -1 ? nan : 0.0f;
+                };
+                float ks_next = scale_of(p.ks), vs_next = scale_of(p.vs);
                 uint32_t g = pieces;
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
-                    const int page = page_next, tok = token0 + (int)(i - j0) * kTile + 16 * (lane & 7);
-                    page_next = page_of(i + 1);
+                    const int tok = token0 + (int)(i - j0) * kTile + 16 * (lane & 7);
+                    const float ks = ks_next, vs = vs_next;
+                    page = page_next;
+                    page_next = page_after;
+                    page_after = page_of(i + 2);
+                    ks_next = scale_of(p.ks);
+                    vs_next = scale_of(p.vs);
                     const int64_t place = (int64_t)max(page, 0) * p.heads + head;
                     if (page == -1) record_error(p.err, kDevErrValue);
-                    const float none = page == -1 ? nan : 0.0f;
-                    const float ks = page >= 0 ? __ldg(p.ks + place) : none, vs = page >= 0 ? __ldg(p.vs + place) : none;
                     // A copy brings what it covers of a page, seen or not: a page of 64 tokens and more has one for
                     // a piece, by the lane of its first tile that is seen.
                     const uint32_t seen = __ballot_sync(0xffffffffu, page >= 0) & 0xFF;
@@ -443,33 +469,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     sts128(to ^ 16, h[4], h[5], h[6], h[7]);
                 };
                 uint32_t g = pieces;
-                // A piece's codes as FP16 into rows `first`.. of a tile.
+                // A unit's keys or values, two pieces, as FP16 into a tile.
                 auto turn = [&](uint32_t to, int tok, bool clean) {
-                    const uint32_t slot = g % SLOTS;
-                    ok = ok && mbar_wait(raw_full + 8 * slot, g / SLOTS & 1, p.err, kDevErrTimeout) && !*aborted;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) return;
-                    const uint32_t from = raw_at + slot * Pl::piece + load_at, there = present[slot];
-                    uint4 v[NG * 2];
+                    uint4 v[2][NG * 2];
+                    uint32_t there[2];
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t slot = (g + x) % SLOTS;
+                        ok = ok && mbar_wait(raw_full + 8 * slot, (g + x) / SLOTS & 1, p.err, kDevErrTimeout) && !*aborted;
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return;
+                        const uint32_t from = raw_at + slot * Pl::piece + load_at;
+                        there[x] = present[slot];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (n * 64 + quarter * 16 < D)
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(v[2 * n + h].x), "=r"(v[2 * n + h].y), "=r"(v[2 * n + h].z), "=r"(v[2 * n + h].w)
-                                             : "r"(from + n * 64 + h * 32 * D) : "memory");
-                    if (clean || there != 0xF || tok < sees_begin || tok + kHalf > sees_end) {
+                        for (int n = 0; n < NG; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint4& w = v[x][2 * n + h];
+                                if (n * 64 + quarter * 16 < D)
+                                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                                 : "r"(from + n * 64 + h * 32 * D) : "memory");
+                            }
+                    }
+                    if (clean || (there[0] & there[1]) != 0xF || tok < sees_begin || tok + kTile > sees_end) {
                         uint32_t nans = 0;
 #pragma unroll
-                        for (int n = 0; n < NG * 2; ++n) {
-                            const int row = r + 32 * (n & 1);
-                            if (!(there >> (row >> 4) & 1) || tok + row < sees_begin || tok + row >= sees_end)
-                                v[n] = make_uint4(0, 0, 0, 0);
-                            if (clean && n / 2 * 64 + quarter * 16 < D) {
+                        for (int n = 0; n < NG * 4; ++n) {
+                            uint4& w4 = v[n / (NG * 2)][n % (NG * 2)];
+                            const int half = n / (NG * 2), row = r + 32 * (n & 1), at = tok + half * kHalf + row;
+                            if (!(there[half] >> (row >> 4) & 1) || at < sees_begin || at >= sees_end) w4 = make_uint4(0, 0, 0, 0);
+                            if (clean && n % (NG * 2) / 2 * 64 + quarter * 16 < D) {
                                 // a NaN counts in the rows that see its token only: 0 times NaN is NaN, so it is taken
                                 // out here and put into those rows at the end
-                                uint32_t* const w[4] = {&v[n].x, &v[n].y, &v[n].z, &v[n].w};
+                                uint32_t* const w[4] = {&w4.x, &w4.y, &w4.z, &w4.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const uint32_t x = nan_bytes(*w[e]);
@@ -481,13 +513,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         if (nans) nan_flag = 1;
                     }
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (n * 64 + quarter * 16 < D) halves(v[2 * n + h], to + store_at + n * kPanel + h * 32 * 128);
+                    for (int n = 0; n < NG * 4; ++n)
+                        if (n % (NG * 2) / 2 * 64 + quarter * 16 < D)
+                            halves(v[n / (NG * 2)][n % (NG * 2)],
+                                   to + store_at + n % (NG * 2) / 2 * kPanel + (n & 1) * 32 * 128 + n / (NG * 2) * kHalf * 128);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(raw_free + 8 * slot);
-                    ++g;
+                    if (lane < 2) mbar_arrive(raw_free + 8 * ((g + lane) % SLOTS));
+                    g += 2;
                 };
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
                     const int tok = token0 + (int)(i - j0) * kTile;
@@ -498,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         ok = mbar_wait((side ? v_free : k_free) + 8 * s, (side ? v_phase(i) : k_phase(i)) ^ 1, p.err, kDevErrTimeout) &&
                              !*aborted;
                         ok = __all_sync(0xffffffffu, ok);
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) turn(to + h * kHalf * 128, tok + h * kHalf, edge && side);
+                        turn(to, tok, edge && side);
                         if (!ok) break;
                         fence_async_smem();
                         mbar_arrive((side ? v_full : k_full) + 8 * s);
@@ -515,48 +546,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 const int row = row0 + min(tile_row + r, rows - 1), token = row / p.group, pos = pos0 + token;
                 const int pos_a = pos0 + (row0 + min(tile_row, rows - 1)) / p.group;
                 const int pos_b = pos0 + (row0 + min(tile_row + kTile, rows) - 1) / p.group;
-                // Q: this thread's row, or of one tile the values of its group's half, twice (the largest first)
+                // Q: 16 lanes a row, eight values each, 16 rows at a time (all loads before the first use); a group has its
+                // tile's rows, or half of the one tile's
                 float factor;
                 {
-                    constexpr int MINE = PAIR ? NG * 64 : NG * 32;
-                    const int d0 = PAIR ? 0 : half * MINE;
-                    const T* from = static_cast<const T*>(p.q) + (work.start + token) * p.q_t +
-                                    (head * p.group + row - token * p.group) * p.q_h;
-                    float top = 0.0f;
-#pragma unroll 4
-                    for (int d = d0; d < min(d0 + MINE, D); d += 8) {
-                        float x[8];
-                        kv_load8(from + d, p.wide, x);
+                    constexpr int ROWS = PAIR ? 32 : 16;         // of a warp
+                    const int r0 = (PAIR ? 0 : half * 64) + (warp & 3) * ROWS, d = (lane & 15) * 8;
+                    const uint32_t to = q_at + (PAIR ? half * kStageBytes : 0) + (d / 64) * kPanel;
+#pragma unroll 1
+                    for (int b = 0; b < ROWS; b += 16) {
+                        constexpr int W = TWO ? 8 : 4;
+                        uint32_t raw[8][W];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-                    }
-                    if constexpr (!PAIR) {
-                        q_top[half][r] = top;
-                        bar_and(1, kSoftWarps * 32, true);
-                        top = fmaxf(q_top[0][r], q_top[1][r]);
-                    }
-                    // 2^(14 - E), top = m 2^E; a negative scale turns q
-                    const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
-                    const float up = copysignf(__uint_as_float((uint32_t)(14 - E + 127) << 23), p.scale);
-                    factor = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (fabsf(p.scale) * kLog2e);
-#pragma unroll 2
-                    for (int d = d0; d < min(d0 + MINE, D); d += 8) {
-                        float x[8];
-                        kv_load8(from + d, p.wide, x);
-                        uint32_t hi[4], lo[4];
+                        for (int n = 0; n < 8; ++n) {
+                            const int at = row0 + min(tile_row + r0 + b + 2 * n + (lane >> 4), rows - 1), i = at / p.group;
+                            const T* from = static_cast<const T*>(p.q) + (work.start + i) * p.q_t +
+                                            (head * p.group + at - i * p.group) * p.q_h + d;
+                            if (d < D) load_words(from, p.wide, raw[n]);
+                            else
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = x[2 * e] * up, b = x[2 * e + 1] * up;
-                            hi[e] = half2_bits(a, b);
-                            lo[e] = TWO ? half2_rest(a, b, hi[e]) : 0u;
+                                for (int e = 0; e < W; ++e) raw[n][e] = 0;
                         }
-                        const uint32_t at = q_at + (PAIR ? half * kStageBytes : 0) + (d / 64) * kPanel + r * 128 +
-                                            ((d % 64 * 2) ^ ((r & 7) << 4));
-                        sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                        if (TWO) sts128(at + kStageBytes, lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            const int rr = r0 + b + 2 * n + (lane >> 4);
+                            float x[8], top = 0.0f;
+                            values_of<T>(raw[n], x);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+                            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            // 2^(14 - E), top = m 2^E; a negative scale turns q
+                            const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
+                            const float up = copysignf(__uint_as_float((uint32_t)(14 - E + 127) << 23), p.scale);
+                            if ((lane & 15) == 0)
+                                q_factor[PAIR ? half : 0][rr] = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (fabsf(p.scale) * kLog2e);
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float a = x[2 * e] * up, c = x[2 * e + 1] * up;
+                                hi[e] = half2_bits(a, c);
+                                lo[e] = TWO ? half2_rest(a, c, hi[e]) : 0u;
+                            }
+                            if (d < D) {
+                                const uint32_t line = to + rr * 128 + ((d % 64 * 2) ^ ((rr & 7) << 4));
+                                sts128(line, hi[0], hi[1], hi[2], hi[3]);
+                                if (TWO) sts128(line + kStageBytes, lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        }
                     }
                     fence_async_smem();
                     mbar_arrive(q_full);
+                    bar_and(1, kSoftWarps * 32, true);
+                    factor = q_factor[PAIR ? half : 0][r];
                 }
 
                 float m = -INFINITY, l = 0.0f, ref = -INFINITY;
@@ -747,20 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     const float f_all = row_factor(work.bad, m_all, l_all, ref_all);
                     T* const to = static_cast<T*>(p.out) + (work.start + token) * p.out_t +
                                   (head * p.group + row - token * p.group) * p.out_h;
-                    const int c_begin = PAIR ? 0 : half * (D / 2), c_end = PAIR ? D : (half + 1) * (D / 2);
-#pragma unroll 1
-                    for (int c = c_begin; c < c_end; c += 8) {
-                        uint32_t a[8], b[8];
-                        tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
-                        if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
-                        tmem_ld_wait();
-                        float y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            y[e] = __uint_as_float(a[e]) * x_a;
-                            if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
-                        }
-                        if (!live) continue;
+                    // eight values of the row from column c
+                    auto put = [&](int c, float (&y)[8]) {
+                        if (!live) return;
                         if (nan_seen)
                             for (int u = 0; u < units; ++u) {
                                 const int tok = token0 + u * kTile;
@@ -782,6 +813,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         } else {
                             *reinterpret_cast<float4*>(slot + 4 + c) = make_float4(y[0], y[1], y[2], y[3]);
                             *reinterpret_cast<float4*>(slot + 8 + c) = make_float4(y[4], y[5], y[6], y[7]);
+                        }
+                    };
+                    if constexpr (PAIR) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t a[16];
+                            tmem_ld_32x32b_x16((tmem + (2 + s0) * kTile + c) | lanes, a);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(a[8 * h + e]);
+                                put(c + 8 * h, y);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+                            uint32_t a[8], b[8];
+                            tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
+                            if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
+                            tmem_ld_wait();
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                y[e] = __uint_as_float(a[e]) * x_a;
+                                if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
+                            }
+                            put(c, y);
                         }
                     }
                     tc_fence_before();
@@ -809,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
         }
         // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
-        if (warp == kMmaWarp && !ok) {
+        if ((warp == kMmaWarp || warp == kMmaWarp + 1) && !ok) {
             const uint32_t leader = elect_one();
             tc_commit(drained, leader);
             mbar_wait(drained, 0, p.err, kDevErrTimeout);
