@@ -7,6 +7,8 @@
 #include "emu_layers.h"
 #include "kv_cache.cuh"
 
+#include <type_traits>
+
 namespace emu {
 namespace {
 
@@ -151,11 +153,14 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TableParam
 // two stay exact down to the type's subnormal values.  Bound by HBM: the values
 // are read once and the codes written once.
 //
-// A unit of work is a run of new rows that follow each other in one page, for one
-// head and side; a warp does it.  The run's first token leads: the warps of the
-// others see that and leave.
-constexpr int kStoreWarps = 4;
-constexpr int kStoreKeep = 8;                        // chunks of 8 values that a lane keeps from the first look to the second
+// A unit of work is what a window of tokens has of runs of new rows that follow each
+// other in one page, for one head and side; a run's first token leads, and the
+// window that it is in does the run.  For a few tokens a window is one token and a
+// warp's (the warps of tokens that do not lead see that and leave); otherwise it is a
+// block's, whose warps share long runs and take short ones in turn.  (A warp for each
+// run: prompts of 18,000 tokens, 8 heads of 128, 86 us.)
+constexpr int kStoreWarps = 8, kStoreThreads = kStoreWarps * 32;
+constexpr int kStoreKeep = 4;                        // chunks of 8 values that a lane keeps from the first look to the second
 
 struct StoreParams {
     const void* in[2];                               // keys, values
@@ -164,10 +169,45 @@ struct StoreParams {
     float* scales[2];
     const int32_t* slots;
     int T, heads, D, page_log, window;               // window: tokens per unit
+    uint32_t per_row_inverse;                        // 2^32 / chunks of a row, rounded up
     int wide;                                        // every row of a head starts on 16 bytes
     int64_t slots_all;                               // pages * P
     int64_t units;
     int* err;
+};
+
+// 8 neighbouring values as they lie in memory.
+template <typename T>
+struct Chunk8 {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T* at, bool wide) {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(at)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        } else {
+            T x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = at[i];
+            memcpy(w, x, sizeof(x));
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[2 * i] = __uint_as_float(w[2 * i]);
+                x[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+            } else {
+                kv_widen<T>(w[i], x[2 * i], x[2 * i + 1]);
+            }
+        }
+    }
 };
 
 // The scale of values whose largest finite magnitude has these bits.
@@ -178,119 +218,175 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kStoreWarps * 32) kv_store_kernel(const StoreParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kStoreWarps + (threadIdx.x >> 5);
+// Stores the run of n rows at token t and slot `slot`: by a warp (THREADS 32), or by
+// the block (tops: shared memory for its warps' maxima).
+template <typename T, int THREADS>
+__device__ __forceinline__ void store_run(const StoreParams& p, int side, int head, int t, int slot, int n, uint32_t* tops) {
+    const int me = threadIdx.x % THREADS, P = 1 << p.page_log, per_row = p.D >> 3;
+    const int64_t in_t = side ? p.in_t[1] : p.in_t[0];
+    const T* rows = static_cast<const T*>(side ? p.in[1] : p.in[0]) + head * (side ? p.in_h[1] : p.in_h[0]) + t * in_t;
+    const int page = slot >> p.page_log, r0 = slot & (P - 1), chunks = n * per_row;
+    const int64_t unit = (int64_t)page * p.heads + head;
+    float* const scale = (side ? p.scales[1] : p.scales[0]) + unit;
+    uint8_t* const codes = (side ? p.codes[1] : p.codes[0]) + unit * P * p.D;
+    const float old = r0 > 0 ? *scale : 0.0f;
+    auto from = [&](int c) {                         // chunk c of the run
+        const int row = (int)__umulhi((uint32_t)c, p.per_row_inverse);
+        return rows + row * in_t + (c - row * per_row) * 8;
+    };
+    Chunk8<T> kept[kStoreKeep];
+    // the largest magnitude as its bits (16-bit types: of the two halves of a word at once)
+    constexpr uint32_t kMagnitude = sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    constexpr uint32_t kInfinite = sizeof(T) == 4 ? 0x7F800000u : std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t bits = 0;
+    auto look = [&](const Chunk8<T>& v) {
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i)
+            bits = sizeof(T) == 4 ? max(bits, v.w[i] & kMagnitude) : __vmaxu2(bits, v.w[i] & kMagnitude);
+    };
+    // over the warp, the block
+    auto all = [&](uint32_t x) {
+        x = __reduce_max_sync(0xffffffffu, x);
+        if constexpr (THREADS > 32) {
+            if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = x;
+            __syncthreads();                         // (all have read the old scale, too)
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) x = max(x, tops[w]);
+        }
+        return x;
+    };
+    auto each = [&](auto&& f) {                      // over the run's chunks, those kept and then the others again
+#pragma unroll
+        for (int i = 0; i < kStoreKeep; ++i)
+            if (i * THREADS + me < chunks) f(i * THREADS + me, kept[i]);
+#pragma unroll 1
+        for (int c = kStoreKeep * THREADS + me; c < chunks; c += THREADS) {
+            Chunk8<T> v;
+            v.load(from(c), p.wide);
+            f(c, v);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStoreKeep; ++i)
+        if (i * THREADS + me < chunks) kept[i].load(from(i * THREADS + me), p.wide);
+    each([&](int, const Chunk8<T>& v) { look(v); });
+    bits = all(sizeof(T) == 4 ? bits : max(bits & 0xFFFFu, bits >> 16));
+    const bool finite = bits < kInfinite;
+    uint32_t top;
+    if (finite) {
+        if constexpr (sizeof(T) == 4) top = bits;
+        else top = __float_as_uint(std::is_same<T, __half>::value ? __half2float(__ushort_as_half((unsigned short)bits))
+                                                                  : __uint_as_float(bits << 16));
+    } else {
+        // infinities and NaN do not count
+        top = 0;
+        each([&](int, const Chunk8<T>& v) {
+            float x[8];
+            v.get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+        });
+        if constexpr (THREADS > 32) __syncthreads();
+        top = all(top);
+    }
+    const float now = fmaxf(old, scale_of(top));
+    if (r0 > 0 && now > old) {
+        // the page's other rows, rounded again
+        const float ratio = old / now;
+#pragma unroll 1
+        for (int c = me; c < P * per_row; c += THREADS) {
+            const int row = (int)__umulhi((uint32_t)c, p.per_row_inverse);
+            if (row >= r0 && row < r0 + n) continue;
+            uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)c * 8);
+            const uint2 w = *at;
+            *at = make_uint2(kv_rescale(w.x, ratio), kv_rescale(w.y, ratio));
+        }
+    }
+    if constexpr (THREADS == 32) __syncwarp();
+    if (me == 0) *scale = now;
+    // a power of two's inverse is exact
+    const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0 && now >= 1.1754944e-38f && now < 8.5e37f;
+    const float inverse = exact ? 1.0f / now : 0.0f;
+    auto put = [&](int c, const float (&x)[8]) {
+        *reinterpret_cast<uint2*>(codes + ((int64_t)r0 * per_row + c) * 8) =
+            make_uint2(kv_codes(x[0], x[1], x[2], x[3]), kv_codes(x[4], x[5], x[6], x[7]));
+    };
+    if (finite && exact)
+        each([&](int c, const Chunk8<T>& v) {
+            float x[8];
+            v.get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inverse;
+            put(c, x);
+        });
+    else
+        each([&](int c, const Chunk8<T>& v) {
+            float x[8];
+            v.get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = (__float_as_uint(x[e]) & 0x7F800000u) == 0x7F800000u ? __uint_as_float(0x7FC00000u) : x[e] / now;
+            put(c, x);
+        });
+}
+
+template <typename T, bool BLOCK>
+__global__ void __launch_bounds__(kStoreThreads, sizeof(T) == 4 ? 3 : 4) kv_store_kernel(const __grid_constant__ StoreParams p) {
+    __shared__ uint32_t tops[2][kStoreWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kStoreWarps + warp;
     if (unit >= p.units) return;
     const int side = (int)(unit & 1), P = 1 << p.page_log;
     const int64_t v = unit >> 1;
     const int head = (int)(v % p.heads), t0 = (int)(v / p.heads) * p.window;
-    const int per_row = p.D >> 3;                    // chunks
-    const T* in = static_cast<const T*>(side ? p.in[1] : p.in[0]) + head * (side ? p.in_h[1] : p.in_h[0]);
-    const int64_t in_t = side ? p.in_t[1] : p.in_t[0];
-    uint8_t* const all_codes = side ? p.codes[1] : p.codes[0];
-    float* const all_scales = side ? p.scales[1] : p.scales[0];
 
-    // the window's tokens that lead a run
-    bool leads = false;
+    // Where runs begin or there are none, 32 tokens at a time from t0 on: the slots of the window and of
+    // the 64 tokens behind it are loaded at once.
+    auto slot_at = [&](int t) { return t < p.T ? p.slots[t] : -1; };
+    auto breaks = [&](int slot, int before) {
+        return __ballot_sync(0xffffffffu, slot < 0 || slot >= p.slots_all || before < 0 || before != slot - 1 || (slot & (P - 1)) == 0);
+    };
     const int t_lane = t0 + lane;
-    int slot_lane = -1;
-    if (lane < p.window && t_lane < p.T) {
-        slot_lane = p.slots[t_lane];
-        const int before = t_lane > 0 ? p.slots[t_lane - 1] : -1;
-        leads = slot_lane >= 0 && slot_lane < p.slots_all &&
-                (before < 0 || before != slot_lane - 1 || (slot_lane & (P - 1)) == 0);
-        if (slot_lane < -1 || slot_lane >= p.slots_all) record_error(p.err, kDevErrValue);
-    }
-    for (uint32_t todo = __ballot_sync(0xffffffffu, leads); todo; todo &= todo - 1) {
+    const int slot_lane = slot_at(t_lane), slot_1 = slot_at(t_lane + 32), slot_2 = slot_at(t_lane + 64);
+    const int before_0 = t_lane > 0 ? slot_at(t_lane - 1) : -1;
+    if (slot_lane < -1 || slot_lane >= p.slots_all) record_error(p.err, kDevErrValue);
+    int up = __shfl_up_sync(0xffffffffu, slot_1, 1), last = __shfl_sync(0xffffffffu, slot_lane, 31);
+    const uint32_t break_0 = breaks(slot_lane, before_0), break_1 = breaks(slot_1, lane ? up : last);
+    up = __shfl_up_sync(0xffffffffu, slot_2, 1);
+    last = __shfl_sync(0xffffffffu, slot_1, 31);
+    const uint32_t break_2 = breaks(slot_2, lane ? up : last);
+    const bool valid = slot_lane >= 0 && slot_lane < p.slots_all;
+    int turn = 0, shared = 0;
+    for (uint32_t todo = break_0 & __ballot_sync(0xffffffffu, valid && lane < p.window); todo; todo &= todo - 1) {
         const int which = __ffs(todo) - 1, t = t0 + which;
         const int slot = __shfl_sync(0xffffffffu, slot_lane, which);
-        const int page = slot >> p.page_log, r0 = slot & (P - 1);
-        int n = 1;                                   // rows of the run
-        for (int most = min(P - r0, p.T - t); n < most;) {
-            const int i = n + lane;
-            const uint32_t ends = __ballot_sync(0xffffffffu, i >= most || p.slots[t + i] != slot + i);
-            if (ends) {
-                n += __ffs(ends) - 1;
-                break;
-            }
-            n += 32;
-        }
-        const int chunks = n * per_row;
-        const T* rows = in + t * in_t;
-        float kept[kStoreKeep][8];
-        uint32_t top = 0;
-        auto look = [&](const float (&x)[8]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t a = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-                top = max(top, a < 0x7F800000u ? a : 0u);
-            }
-        };
-        auto from = [&](int c) {                     // chunk c of the run
-            const int row = c / per_row;
-            return rows + row * in_t + (c - row * per_row) * 8;
-        };
-#pragma unroll
-        for (int i = 0; i < kStoreKeep; ++i) {
-            const int c = i * 32 + lane;
-            if (c < chunks) kv_load8(from(c), p.wide, kept[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kStoreKeep; ++i)
-            if (i * 32 + lane < chunks) look(kept[i]);
-        for (int c = kStoreKeep * 32 + lane; c < chunks; c += 32) {
-            float x[8];
-            kv_load8(from(c), p.wide, x);
-            look(x);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        float* scale = all_scales + (int64_t)page * p.heads + head;
-        uint8_t* codes = all_codes + ((int64_t)page * p.heads + head) * (int64_t)P * p.D;
-        float now = scale_of(top);
-        if (r0 > 0) {
-            const float old = *scale;
-            now = fmaxf(old, now);
-            if (now > old) {
-                // the page's other rows, rounded again
-                const float ratio = old / now;
-                for (int c = lane; c < P * per_row; c += 32) {
-                    const int row = c / per_row;
-                    if (row >= r0 && row < r0 + n) continue;
-                    uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)c * 8);
-                    const uint2 w = *at;
-                    *at = make_uint2(kv_rescale(w.x, ratio), kv_rescale(w.y, ratio));
+        // the next break ends the run
+        const uint32_t rest = which == 31 ? 0u : break_0 >> (which + 1);
+        int n;
+        if (rest) n = __ffs(rest);
+        else if (break_1) n = 32 - which + __ffs(break_1) - 1;
+        else if (break_2) n = 64 - which + __ffs(break_2) - 1;
+        else {
+            n = 96 - which;                          // (pages of 128 and 256)
+            for (int most = min(P - (slot & (P - 1)), p.T - t); n < most;) {
+                const int i = n + lane;
+                const uint32_t ends = __ballot_sync(0xffffffffu, i >= most || p.slots[t + i] != slot + i);
+                if (ends) {
+                    n += __ffs(ends) - 1;
+                    break;
                 }
+                n += 32;
             }
         }
-        __syncwarp();
-        if (lane == 0) *scale = now;
-        // a power of two's inverse is exact
-        const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0 && now >= 1.1754944e-38f && now < 8.5e37f;
-        const float inverse = exact ? 1.0f / now : 0.0f;
-        auto write = [&](int c, const float (&x)[8]) {
-            uint32_t w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float z = x[4 * i + e];
-                    const bool finite = (__float_as_uint(z) & 0x7F800000u) != 0x7F800000u;
-                    y[e] = !finite ? __uint_as_float(0x7FC00000u) : exact ? z * inverse : z / now;
-                }
-                w[i] = kv_codes(y[0], y[1], y[2], y[3]);
-            }
-            *reinterpret_cast<uint2*>(codes + ((int64_t)r0 * per_row + c) * 8) = make_uint2(w[0], w[1]);
-        };
-#pragma unroll
-        for (int i = 0; i < kStoreKeep; ++i)
-            if (i * 32 + lane < chunks) write(i * 32 + lane, kept[i]);
-        for (int c = kStoreKeep * 32 + lane; c < chunks; c += 32) {
-            float x[8];
-            kv_load8(from(c), p.wide, x);
-            write(c, x);
+        if constexpr (BLOCK) {
+            // (all warps see the same runs)
+            if (n * (p.D >> 3) > kStoreKeep * 32) store_run<T, kStoreThreads>(p, side, head, t, slot, n, tops[shared++ & 1]);
+            else if (turn++ % kStoreWarps == warp) store_run<T, 32>(p, side, head, t, slot, n, nullptr);
+        } else {
+            store_run<T, 32>(p, side, head, t, slot, n, nullptr);
         }
     }
 }
@@ -380,15 +476,22 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
     p.page_log = kv_log2(cache->page);
     p.slots_all = cache->pages * cache->page;
     p.err = d->err;
-    // a token per unit until they fill the GPU's warps, up to 32
+    p.per_row_inverse = (uint32_t)(((uint64_t(1) << 32) + p.D / 8 - 1) / (p.D / 8));
+    // a warp for each of a few tokens; else a block for each window, up to 32 tokens, of which there are eight or more an SM
+    const bool block = T > 32;
     p.window = 1;
-    while (p.window < 32 && (T + p.window - 1) / p.window * cache->heads * 2 > (int64_t)d->sms * 64) p.window *= 2;
+    while (block && p.window < 32 && (T + 2 * p.window - 1) / (2 * p.window) * cache->heads * 2 >= (int64_t)d->sms * 8) p.window *= 2;
     p.units = (T + p.window - 1) / p.window * cache->heads * 2;
-    const unsigned blocks = (unsigned)((p.units + kStoreWarps - 1) / kStoreWarps);
+    const unsigned blocks = (unsigned)(block ? p.units : (p.units + kStoreWarps - 1) / kStoreWarps);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (dtype == EMU_F32) kv_store_kernel<float><<<blocks, kStoreWarps * 32, 0, stream>>>(p);
-    else if (dtype == EMU_BF16) kv_store_kernel<__nv_bfloat16><<<blocks, kStoreWarps * 32, 0, stream>>>(p);
-    else kv_store_kernel<__half><<<blocks, kStoreWarps * 32, 0, stream>>>(p);
+    auto go = [&](auto t) {
+        using V = decltype(t);
+        if (block) kv_store_kernel<V, true><<<blocks, kStoreThreads, 0, stream>>>(p);
+        else kv_store_kernel<V, false><<<blocks, kStoreThreads, 0, stream>>>(p);
+    };
+    if (dtype == EMU_F32) go(float{});
+    else if (dtype == EMU_BF16) go(__nv_bfloat16{});
+    else go(__half{});
     return from_cuda(cudaGetLastError());
 }
 

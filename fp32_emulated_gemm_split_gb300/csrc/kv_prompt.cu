@@ -150,7 +150,8 @@ struct Plan {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int rows = PAIR ? 2 * kTile : kTile;
     static constexpr int q_tiles = PAIR || TWO ? 2 : 1;          // tiles of Q, or pieces
-    // (two stages of V where the groups take units in turn: each issuer then meets every phase of its own stage)
+    // (two stages of V where the groups take units in turn: each issuer then meets every phase of its own.  One of K
+    // and two of V for a pair: 727 us for 709)
     static constexpr int k_stages = 2, v_stages = PAIR ? 1 : 2;
     static constexpr int piece = kHalf * NG * 64;                // bytes of a piece of codes
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
