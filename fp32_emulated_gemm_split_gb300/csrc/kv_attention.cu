@@ -40,6 +40,10 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKvCtasPerSm = 4;                      // at most
+// Rows of a sequence (16-bit types, heads up to 128) up to which this file's kernel runs, in segments of 16 that
+// each read the cache, all but the first from L2: 24 sequences of 3 to 7 tokens, 8 heads of 128 a key head, 80 us,
+// in kv_prompt.cu 106, and in segments of 32 (queries in shared memory, steps of 16 tokens for their registers) 102.
+constexpr int kFewKvRows = 64;
 
 // Steps start on multiples of ST tokens; the first one that any row of the sequence sees.
 template <int ST>
@@ -934,7 +938,7 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;
     cudaError_t e;
-    if (max_rows > 16 && p.D <= 128) e = launch_prompt(dtype, p, max_rows, d->sms, stream);
+    if (max_rows > (dtype == EMU_F32 ? 16 : kFewKvRows) && p.D <= 128) e = launch_prompt(dtype, p, max_rows, d->sms, stream);
     else if (dtype == EMU_F32) e = launch_typed<float>(p, *cache, max_rows, d, stream);
     else if (dtype == EMU_BF16) e = launch_typed<__nv_bfloat16>(p, *cache, max_rows, d, stream);
     else e = launch_typed<__half>(p, *cache, max_rows, d, stream);

@@ -98,6 +98,17 @@ def test_prompts(emu, type, Hq, Hk, D, P, n, kept):
 
 
 @pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("Hq,Hk,D,P,most", [(16, 2, 128, 32, 7), (24, 3, 64, 16, 4), (10, 2, 80, 64, 9), (17, 1, 32, 16, 2),
+                                            (16, 1, 256, 32, 3), (40, 1, 112, 128, 1)])
+def test_drafts(emu, type, Hq, Hk, D, P, most):
+    """A few rows of many heads: 17 to 63 of a sequence and key head."""
+    kept = [0, 3, 40, 127, 128, 300, 2000]
+    new = [1 + i % most for i in range(len(kept))]
+    _check(emu, _make(kept, new, Hq, Hk, D, P, type, seed=most, behind=2), max_new=most)
+    _check(emu, _make(kept, new, Hq, Hk, D, P, type, seed=most), max_new=most, window=35)
+
+
+@pytest.mark.parametrize("type", TYPES)
 def test_long_and_many(emu, type):
     _check(emu, _make([20011], [1], 8, 2, 128, 16, type))
     _check(emu, _make([9000, 10], [3, 4], 4, 1, 64, 128, type))
