@@ -6,24 +6,27 @@ as torch modules, and a small decoder block that runs them together.
                    backward
   EmuDecoderBlock  norm, one projection to queries, keys and values (with each
                    token's low-rank adapter where adapters are given), norm and
-                   rotation of the heads, attention, output projection; norm,
-                   gated feed-forward, down projection
+                   rotation of the heads, attention (for serving over the pages
+                   of a KvCache, many sequences at once), output projection;
+                   norm, gated feed-forward, down projection
 
 The operators have first derivatives; a derivative of a gradient (a loss made of
 forces) raises.
 
 ``python -m fp32_emulated_gemm_split_gb300.block`` runs the block on a prompt,
-then token by token on the same sequence, and prints how far the two and a
-float64 evaluation are apart.
+then token by token on the same sequence, and prints how far the two are apart;
+then on three sequences at once whose keys and values are kept in 8 bits, and
+prints how far that is from keeping them in FP32.
 """
 from __future__ import annotations
 
 import math
+from typing import NamedTuple
 
 import torch
 
-from .layers import (emu_gated, emu_gated_bwd, emu_gated_pack, emu_lora, emu_lora_pack, emu_qk_norm_rope,
-                     emu_qk_norm_rope_bwd, version_of)
+from .layers import (KvCache, KvPlan, emu_gated, emu_gated_bwd, emu_gated_pack, emu_kv_attention, emu_kv_cache, emu_kv_store,
+                     emu_kv_tables, emu_lora, emu_lora_pack, emu_qk_norm_rope, emu_qk_norm_rope_bwd, version_of)
 from .linear import EmuLinear, as_rows, readable, underivable
 
 
@@ -131,6 +134,17 @@ def rotary_tables(positions, rot, base=10000.0, device=None):
     return (at * f).cos().float(), (at * f).sin().float()
 
 
+class KvStep(NamedTuple):
+    """What a step of many sequences attends to: a block's cache, the sequences'
+    pages (``table``) and the step's places (``emu_kv_tables``); max_new as in
+    ``emu_kv_attention``.  The blocks of a model have a cache each and share the rest."""
+
+    cache: KvCache
+    table: torch.Tensor
+    plan: KvPlan
+    max_new: int | None = None
+
+
 class EmuDecoderBlock(torch.nn.Module):
     """One decoder block, FP32.  ``forward(x, start)`` takes tokens x width and
     the position of the first token, attends to the keys and values kept from
@@ -138,7 +152,13 @@ class EmuDecoderBlock(torch.nn.Module):
     own tokens otherwise), and adds the adapters' part to the first projection
     where ``adapters`` = (A, B, scale) and ``index`` are given.  That part is for
     serving: it has no backward pass, and where a gradient would have to go
-    through it the call raises."""
+    through it the call raises.
+
+    With ``kv`` (a KvStep) the rows of x are the new tokens of many sequences, in the
+    plan's order: their keys and values are rounded into the cache's pages, and each
+    attends to its own sequence's.  For serving, too; ``start`` and ``keep`` do not
+    go with it.  Rows behind the last sequence come out of a block as any others do
+    that attend to nothing."""
 
     def __init__(self, width, heads, kv_heads, hidden, max_positions=4096, eps=1e-6, device="cuda"):
         super().__init__()
@@ -168,9 +188,19 @@ class EmuDecoderBlock(torch.nn.Module):
         s = s.masked_fill(~seen, float("-inf"))
         return torch.einsum("hqk,khd->qhd", s.softmax(-1), v).reshape(q.size(0), -1)
 
-    def forward(self, x, start=0, adapters=None, index=None, keep=False):
+    def _serves(self, what, *tensors):
+        """Raises where a gradient would have to go through what has no backward pass."""
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+            raise RuntimeError(f"{what} no backward pass: call the block under torch.no_grad(), or train without them")
+
+    def forward(self, x, start=0, adapters=None, index=None, keep=False, kv=None):
         T, D = x.size(0), self.dim
-        if start < 0 or start + T > self.cos.size(0):
+        if kv is not None:
+            if start != 0 or keep:
+                raise ValueError("start and keep are one sequence's: with kv the plan has the positions, the cache the tokens")
+            if kv.plan.positions.size(0) != T:
+                raise ValueError(f"the plan has places for {kv.plan.positions.size(0)} rows, x has {T}")
+        elif start < 0 or start + T > self.cos.size(0):
             raise ValueError(f"positions {start} to {start + T - 1} are not all in the tables' {self.cos.size(0)}")
         if keep and start > 0 and (self.kept is None or self.kept[0].size(0) > start):
             held = "none" if self.kept is None else f"{self.kept[0].size(0)} tokens"
@@ -180,12 +210,16 @@ class EmuDecoderBlock(torch.nn.Module):
             qkv = self.qkv(n)
         else:
             A, B, scale = adapters
-            if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                               for t in (n, self.qkv.weight, A, B, scale)):
-                raise RuntimeError("the adapters have no backward pass: call the block under torch.no_grad(), or "
-                                   "train without them")
+            self._serves("the adapters have", n, self.qkv.weight, A, B, scale)
             qkv = emu_lora(n, emu_lora_pack(self.qkv.weight), A, B, index, scale)
         q, k, v = qkv.view(T, -1, D).split((self.heads, self.kv_heads, self.kv_heads), 1)
+        if kv is not None:
+            self._serves("keys and values in 8 bits have", qkv, self.wq, self.wk)
+            q, k = emu_qk_norm_rope(q, k, self.wq, self.wk, self.cos, self.sin, kv.plan.positions, self.eps)
+            emu_kv_store(k, v, kv.cache, kv.plan.slots)
+            y = emu_kv_attention(q, kv.cache, kv.table, kv.plan.starts, kv.plan.lengths, max_new=kv.max_new)
+            x = x + self.out(y.view(T, -1))
+            return x + self.down(self.gated(self._norm(x, self.norm2)))
         positions = torch.arange(start, start + T, device=x.device, dtype=torch.int32)
         q, k = qk_norm_rope(q, k, self.wq, self.wk, self.cos, self.sin, positions, self.eps)
         if keep:
@@ -213,6 +247,24 @@ def main():
             parts.append(block(x[t:t + 1], start=t, adapters=adapters, index=index[t:t + 1], keep=True))
     off = (torch.cat(parts) - whole).norm() / whole.norm()
     print(f"prompt of {T} and {new} single tokens against one pass: {float(off):.2e} apart")
+
+    # three sequences at once, each the first tokens of x, over pages of 8-bit keys and values
+    page, pages = 16, 32
+    cache = emu_kv_cache(pages, block.kv_heads, block.dim, page=page)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, free = torch.full((3, 8), -1, dtype=torch.int32, device="cuda"), torch.arange(pages, device="cuda", dtype=torch.int32)
+    kept, taken, prompts = ints(0, 0, 0), None, (T, 1, 37)
+    with torch.no_grad():
+        for step in range(new + 1):
+            rows = prompts if step == 0 else (1, 1, 1)
+            plan = emu_kv_tables(kept, ints(*rows), table, free, pages, page, sum(rows), taken)
+            first = prompts if step else (0, 0, 0)
+            x_new = torch.cat([x[f + max(step - 1, 0):f + max(step - 1, 0) + n] for f, n in zip(first, rows)])
+            y = block(x_new, kv=KvStep(cache, table, plan, max(rows)))
+            kept, taken = plan.lengths, plan.taken
+        want = torch.stack([block(x[:n + new])[-1] for n in prompts])
+    off = (y - want).norm() / want.norm()
+    print(f"three sequences over 8-bit keys and values, against FP32: {float(off):.2e} apart")
 
 
 if __name__ == "__main__":

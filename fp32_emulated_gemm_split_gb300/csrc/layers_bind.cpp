@@ -481,6 +481,15 @@ int32_t* table_of(T t, int64_t rows) {
     return static_cast<int32_t*>(t->data_ptr());
 }
 
+// n values of a tensor's storage from `first` on (narrow() takes 1.5 us a call, this a tenth).
+at::Tensor part_of(const at::Tensor& t, int64_t first, int64_t n) {
+    at::Tensor r = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()), t.key_set(),
+                                                            t.dtype());
+    r.unsafeGetTensorImpl()->set_storage_offset(first);
+    r.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(&n, 1));
+    return r;
+}
+
 PyObject* kv_tables(PyObject* const* a) {            // kept, new, table, free, pages, page, tokens, taken
     T kept = tensor(a[0], "kept"), fresh = tensor(a[1], "new"), table = tensor(a[2], "table");
     T free_pages = tensor(a[3], "free"), taken = maybe(a[7], "taken");
@@ -500,11 +509,11 @@ PyObject* kv_tables(PyObject* const* a) {            // kept, new, table, free, 
     {
         NoGil no;
         all = empty({head + 2 * some}, at::kInt, dev);
-        out[0] = all.narrow(0, 0, B + 1);
-        out[1] = all.narrow(0, B + 1, B);
-        out[2] = all.narrow(0, head, rows);
-        out[3] = all.narrow(0, head + some, rows);
-        out[4] = all.narrow(0, 2 * B + 1, 1);
+        out[0] = part_of(all, 0, B + 1);
+        out[1] = part_of(all, B + 1, B);
+        out[2] = part_of(all, head, rows);
+        out[3] = part_of(all, head + some, rows);
+        out[4] = part_of(all, 2 * B + 1, 1);
         int32_t* p = static_cast<int32_t*>(all.data_ptr());
         st = api.kv_tables(B, kp, np, pages, page, fp, free_pages->size(0), gone, tp, table->size(1), rows, p, p + B + 1,
                            p + head, p + head + some, p + 2 * B + 1, stream_of(dev));

@@ -120,7 +120,7 @@ def attention(q, k, v, k_scale, v_scale, table, starts, lengths, scale, window=0
         hurt = torch.einsum("nhl,lhd->nhd", seen.double().expand(p.shape), torch.isnan(V).double()) > 0
         size = torch.einsum("nhl,lhd->nhd", p * off, clean.abs()) + (p * off).sum(-1, keepdim=True) * y.abs()
         size = 1.01 * size + (L / 16 + 80) * 4 * u * torch.einsum("nhl,lhd->nhd", p, clean.abs())
-        size = size + HALF_ULP[q.dtype] * (y.abs() + size) + LEAST[q.dtype] + 1e-37
+        size = size + HALF_ULP.get(q.dtype, 0.0) * (y.abs() + size) + LEAST.get(q.dtype, 0.0) + 1e-37
         out[first:first + n] = torch.where(some, torch.where(hurt, math.nan, y), 0.0)
         bound[first:first + n] = torch.where(some, size, 0.0)
     return out, bound
