@@ -72,16 +72,6 @@ struct Tiles {
 
 // ------------------------------------------------------- tensor memory --
 
-__device__ __forceinline__ void tmem_ld_x32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr) : "memory");
-}
 __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -182,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, nan_flag;
     __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ Work work;
+    __shared__ Work work, work_next;                 // (the next segment: found while this one runs)
     // of a unit's tiles of 16 tokens: keys, values (eight units: a group may still read a unit's while the copies
     // are four ahead)
     __shared__ float scales[8][2][8];
@@ -296,26 +286,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         }
         uint32_t j = 0, second = 0, pieces = 0;      // units, those of a second tile, copied pieces of this CTA so far
         uint32_t segments = 0;
-        for (;;) {
-            __syncthreads();
-            // ------------------------------------------------ the segment
-            if (tid == 0) {
-                const Seq s = seq_of(p, work.seq);
-                const Ti ti(p, s);
-                const int i = work.row0 / Pl::rows, units = ti.units(i);
-                work.bad = s.len < 0;
-                work.start = s.start;
-                work.len = max(s.len, 0);
-                work.pos0 = work.len - s.n;
-                work.end = work.begin + units;
-                work.rows = (int)min((int64_t)s.n * p.group - work.row0, (int64_t)Pl::rows);
-                work.token0 = (ti.first(i) + (int)(work.at - work.begin)) * kTile;
-                work.units = (int)(min(work.stop, work.end) - work.at);
-                work.starts = work.at == work.begin;
-                work.whole = work.units == units;
-                nan_flag = 0;
+        // The rest of a segment's description, from its sequence, tile, head, first unit and the CTA's next unit.
+        auto describe = [&](Work& w) {
+            const Seq s = seq_of(p, w.seq);
+            const Ti ti(p, s);
+            const int i = w.row0 / Pl::rows, units = ti.units(i);
+            w.bad = s.len < 0;
+            w.start = s.start;
+            w.len = max(s.len, 0);
+            w.pos0 = w.len - s.n;
+            w.end = w.begin + units;
+            w.rows = (int)min((int64_t)s.n * p.group - w.row0, (int64_t)Pl::rows);
+            w.token0 = (ti.first(i) + (int)(w.at - w.begin)) * kTile;
+            w.units = (int)(min(w.stop, w.end) - w.at);
+            w.starts = w.at == w.begin;
+            w.whole = w.units == units;
+        };
+        // The segment behind it: the next head, tile or sequence.
+        auto advance = [&](Work& w) {
+            w.at = w.begin = w.end;
+            if (++w.head == p.heads) {
+                w.head = 0;
+                Seq s = seq_of(p, w.seq);
+                if (w.row0 + (int64_t)Pl::rows < (int64_t)s.n * p.group) {
+                    w.row0 += Pl::rows;
+                } else {
+                    w.row0 = 0;
+                    do s = seq_of(p, ++w.seq);
+                    while (s.n == 0);
+                }
             }
-            __syncthreads();
+            describe(w);
+        };
+        if (tid == 0) describe(work);
+        __syncthreads();
+        for (;;) {
             const int units = work.units, token0 = work.token0, len = work.len, pos0 = work.pos0, head = work.head;
             const int row0 = work.row0, rows = work.rows;
             // tokens that some row of the segment sees
@@ -446,6 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         mbar_arrive(c_full + 8 * (i & 7));
                     }
                 }
+                if (lane == 0 && work.end < work.stop) {
+                    Work next = work;
+                    advance(next);
+                    work_next = next;
+                }
                 if (!ok) {
                     // no copy may land after this CTA is gone
                     *aborted = 1;
@@ -551,15 +561,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 // tile's rows, or half of the one tile's
                 float factor;
                 {
-                    constexpr int ROWS = PAIR ? 32 : 16;         // of a warp
+                    constexpr int ROWS = PAIR ? 32 : 16, LOADS = 8;      // of a warp, at once (16: 709 -> 735 us)
                     const int r0 = (PAIR ? 0 : half * 64) + (warp & 3) * ROWS, d = (lane & 15) * 8;
                     const uint32_t to = q_at + (PAIR ? half * kStageBytes : 0) + (d / 64) * kPanel;
 #pragma unroll 1
-                    for (int b = 0; b < ROWS; b += 16) {
+                    for (int b = 0; b < ROWS; b += 2 * LOADS) {
                         constexpr int W = TWO ? 8 : 4;
-                        uint32_t raw[8][W];
+                        uint32_t raw[LOADS][W];
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
+                        for (int n = 0; n < LOADS; ++n) {
                             const int at = row0 + min(tile_row + r0 + b + 2 * n + (lane >> 4), rows - 1), i = at / p.group;
                             const T* from = static_cast<const T*>(p.q) + (work.start + i) * p.q_t +
                                             (head * p.group + at - i * p.group) * p.q_h + d;
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                 for (int e = 0; e < W; ++e) raw[n][e] = 0;
                         }
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
+                        for (int n = 0; n < LOADS; ++n) {
                             const int rr = r0 + b + 2 * n + (lane >> 4);
                             float x[8], top = 0.0f;
                             values_of<T>(raw[n], x);
@@ -661,29 +671,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     }
                     // the largest score, and the largest with its page's bound
                     float top = -INFINITY, over = -INFINITY;
+                    uint32_t sc[2][16];              // (16 scores on the way while those before are looked at)
+                    tmem_ld_32x32b_x16(s_at, sc[0]);
 #pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
-                        uint32_t sc[32];
-                        tmem_ld_x32(s_at + c, sc);
-                        tmem_ld_wait();
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (tok + c + e > last || tok + c + e <= from) sc[e] = 0xFF800000u;
-                        }
+                    for (int c = 0; c < kTile; c += 32)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            float x = __uint_as_float(sc[16 * g]);
+                            tmem_ld_wait();
+                            if (g == 0) tmem_ld_32x32b_x16(s_at + c + 16, sc[1]);
+                            else if (c + 32 < kTile) tmem_ld_32x32b_x16(s_at + c + 32, sc[0]);
+                            if (edge) {
 #pragma unroll
-                            for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(sc[16 * g + e]));
+                                for (int e = 0; e < 16; ++e) {
+                                    const int t = tok + c + 16 * g + e;
+                                    if (t > last || t <= from) sc[g][e] = 0xFF800000u;
+                                }
+                            }
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = fmaxf(fmaxf(__uint_as_float(sc[g][e]), __uint_as_float(sc[g][4 + e])),
+                                             fmaxf(__uint_as_float(sc[g][8 + e]), __uint_as_float(sc[g][12 + e])));
+                            float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                             // (what no row sees has scale 0)
-                            if (x > -INFINITY) {
-                                x *= factor * ks[c / 16 + g];
-                                top = fmaxf(top, x);
-                                over = fmaxf(over, x + (float)scale_bound(vs[c / 16 + g]));
+                            if (y > -INFINITY) {
+                                y *= factor * ks[c / 16 + g];
+                                top = fmaxf(top, y);
+                                over = fmaxf(over, y + (float)scale_bound(vs[c / 16 + g]));
                             }
                         }
-                    }
                     if (top > m) {
                         l *= exp2_of(m - top);
                         m = top;
@@ -718,17 +734,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     first = false;
                     const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
                     uint64_t sums = 0;
+                    tmem_ld_32x32b_x16(s_at, sc[0]);
 #pragma unroll 1
                     for (int c = 0; c < kTile; c += 32) {
-                        uint32_t sc[32], w[16], rest[16];
-                        tmem_ld_x32(s_at + c, sc);
-                        tmem_ld_wait();
+                        uint32_t w[16], rest[16];
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
+                            tmem_ld_wait();
+                            if (g == 0) tmem_ld_32x32b_x16(s_at + c + 16, sc[1]);
+                            else if (c + 32 < kTile) tmem_ld_32x32b_x16(s_at + c + 32, sc[0]);
                             const uint64_t k2 = two(factor * ks[c / 16 + g]), m2 = two(-m0), f2 = two(vs[c / 16 + g] * up);
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
-                                const uint64_t x = fma_f32x2(pack_f32x2(sc[16 * g + e], sc[16 * g + e + 1]), k2, m2);
+                                const uint64_t x = fma_f32x2(pack_f32x2(sc[g][e], sc[g][e + 1]), k2, m2);
                                 float p0 = exp2_of(lo_of(x)), p1 = exp2_of(hi_of(x));
                                 if (edge) {
                                     const int t0 = tok + c + 16 * g + e;
@@ -817,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         }
                     };
                     if constexpr (PAIR) {
+                        // (the next columns on the way while these are written: 830 us for 700, registers of the units' loop)
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t a[16];
@@ -854,21 +873,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             pieces += 4 * units;
             ++segments;
             if (__syncthreads_or(!ok) || work.end >= work.stop) break;
+            __syncthreads();                         // (all have looked)
             if (tid == 0) {
-                // the next head, tile or sequence
-                work.at = work.begin = work.end;
-                if (++work.head == p.heads) {
-                    work.head = 0;
-                    Seq s = seq_of(p, work.seq);
-                    if (work.row0 + (int64_t)Pl::rows < (int64_t)s.n * p.group) {
-                        work.row0 += Pl::rows;
-                    } else {
-                        work.row0 = 0;
-                        do s = seq_of(p, ++work.seq);
-                        while (s.n == 0);
-                    }
-                }
+                work = work_next;
+                nan_flag = 0;
             }
+            __syncthreads();
         }
         // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
         if ((warp == kMmaWarp || warp == kMmaWarp + 1) && !ok) {
