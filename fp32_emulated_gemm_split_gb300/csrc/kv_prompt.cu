@@ -27,7 +27,11 @@ constexpr int kTile = 128;                           // rows of a segment, token
 constexpr int kPanel = kTile * 128;                  // 128 rows of 64 FP16 values, swizzled
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 2;    // (an issuer for each group)
-constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kThreads = (kCopyWarp + 2) * 32;        // (the last warp fills the fourth group of warps)
+enum { kSoft, kCode, kMma, kCopy, kIdle };
+// Registers of a thread: at launch, of the groups that turn scores into weights, of the others.
+constexpr int kLaunchRegs = 128, kSoftRegs = 168, kOtherRegs = 88;
+static_assert(kSoftWarps * kSoftRegs + (kThreads / 32 - kSoftWarps) * kOtherRegs <= kThreads / 32 * kLaunchRegs, "no more than there are");
 constexpr int kHalf = kTile / 2;                     // tokens of a copied piece: keys, keys, values, values of a unit
 
 // ------------------------------------------------- tiles of a sequence --
@@ -320,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         };
         if (tid == 0) describe(work);
         __syncthreads();
-        for (;;) {
+        // One segment, as a warp of this role; whether another one follows.
+        auto segment = [&](int role) __attribute__((always_inline)) {
             const int units = work.units, token0 = work.token0, len = work.len, pos0 = work.pos0, head = work.head;
             const int row0 = work.row0, rows = work.rows;
             // tokens that some row of the segment sees
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             auto v_phase = [](uint32_t i) { return i / VS & 1; };
             auto s_phase = [&](uint32_t i, uint32_t t) { return PAIR ? (t ? second + (i - j0) : i) & 1 : i >> 1 & 1; };
 
-            if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            if (role == kMma) {
                 // ------------------------------------------------- MMAs
                 const uint32_t t = warp - kMmaWarp;  // the group
                 const uint32_t leader = elect_one();
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     tc_commit(v_free + 8 * (i % VS), leader);
                 }
                 if (!ok) *aborted = 1;
-            } else if (warp == kCopyWarp) {
+            } else if (role == kCopy) {
                 // ----------------------------------------------- copies
                 const int32_t* pages = p.table + (int64_t)work.seq * p.width;
                 const int P = 1 << p.page_log, run = min(P, kHalf);          // tokens of a copy
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     for (uint32_t x = g > SLOTS ? g - SLOTS : 0; x < g; ++x)
                         mbar_wait(raw_full + 8 * (x % SLOTS), x / SLOTS & 1, p.err, kDevErrTimeout);
                 }
-            } else if (warp >= kSoftWarps) {
+            } else if (role == kCode) {
                 // ------------------------------------------------ codes
                 // A thread has 16 values of rows r and r + 32 of a piece (64 tokens) and panel: two rows' quarters by eight
                 // lanes, whose stores meet all banks.
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     }
                 }
                 if (!ok) *aborted = 1;
-            } else {
+            } else if (role == kSoft) {
                 // --------------------------------------------- scores to weights
                 const int half = warp >> 2, r = tid & (kTile - 1);       // group, row of its tile
                 const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -872,13 +877,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             j = j1;
             pieces += 4 * units;
             ++segments;
-            if (__syncthreads_or(!ok) || work.end >= work.stop) break;
+            if (__syncthreads_or(!ok) || work.end >= work.stop) return false;
             __syncthreads();                         // (all have looked)
             if (tid == 0) {
                 work = work_next;
                 nan_flag = 0;
             }
             __syncthreads();
+            return true;
+        };
+        // (a unit's P waits in registers: with 128 for all, spilled, prompts took 700 us)
+        if (warp < kSoftWarps) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
+            while (segment(kSoft)) {}
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
+            if (warp < kMmaWarp) while (segment(kCode)) {}
+            else if (warp < kCopyWarp) while (segment(kMma)) {}
+            else if (warp == kCopyWarp) while (segment(kCopy)) {}
+            else while (segment(kIdle)) {}
         }
         // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
         if ((warp == kMmaWarp || warp == kMmaWarp + 1) && !ok) {
@@ -909,7 +926,11 @@ cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!done[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::bytes);
+        // (the warps' shares of registers add up to what the block is launched with, or they would wait for ever)
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, kern);
+        if (e == cudaSuccess && a.numRegs != kLaunchRegs) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pl::bytes);
         if (e != cudaSuccess) return e;
         done[dev] = true;
     }

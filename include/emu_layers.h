@@ -265,15 +265,16 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  *  lengths       B values
  *  window        0: all tokens before
  *  max_new       rows that a sequence has at most, or 0 where the caller does not
- *                know.  It chooses kernels, not results.
+ *                know.  It chooses kernels (whose sums are rounded differently), not
+ *                what is computed: too small a value is slow, not wrong.
  *
  * Scores, weights and sums are FP32-accurate for FP32 rows; for 16-bit rows the
  * weights p are rounded to 11 bits for their product with v.  A row that sees no
  * token is zero.  What a row does not see has no part in it, whatever it holds
  * (NaN among it).  A length that is negative or more than width pages hold, and a
  * page number outside the cache, give NaN in the rows that need them; `starts`
- * out of order leaves rows of that sequence unwritten.  Each records
- * EMU_ERR_INVALID_VALUE.
+ * out of order leaves the outputs undefined (nothing else is written).  Each
+ * records EMU_ERR_INVALID_VALUE.
  */
 emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t* q, const emu_heads_t* out,
                               const emu_kv_cache_t* cache, int64_t B, const int32_t* table, int64_t width,

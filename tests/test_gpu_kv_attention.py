@@ -244,14 +244,35 @@ def test_strides_and_in_place(emu):
     assert torch.equal(emu.emu_kv_attention(turned, cache, table, _ints(starts), _ints(lengths)), want)
 
 
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_strides_and_in_place_of_prompts(emu, type, D):
+    import torch
+    q, cache, table, starts, lengths = _make([40, 700], [150, 33], 6, 2, D, 32, type, behind=2)
+    want = _check(emu, (q, cache, table, starts, lengths))
+    for odd in (0, 1):
+        wide = torch.zeros(185, 6 * (D + 16) + odd, device="cuda", dtype=q.dtype)
+        view = wide[:, odd:odd + 6 * (D + 16)].view(185, 6, D + 16)[..., :D]
+        view.copy_(q)
+        out = torch.full_like(wide, 7.0)
+        here = out[:, odd:odd + 6 * (D + 16)].view(185, 6, D + 16)[..., :D]
+        emu.emu_kv_attention(view, cache, table, _ints(starts), _ints(lengths), out=here)
+        assert torch.equal(here, want)
+        here.fill_(7.0)
+        assert (out == 7.0).all()
+        emu.emu_kv_attention(view, cache, table, _ints(starts), _ints(lengths), out=view)
+        assert torch.equal(view, want)
+
+
 def test_same_bits_again(emu):
     import torch
     made = _make([5000, 100, 3000], [1, 4, 1], 8, 2, 128, 16, "f32")
     q, cache, table, starts, lengths = made
     args = (q, cache, table, _ints(starts), _ints(lengths))
-    first = emu.emu_kv_attention(*args)
-    for _ in range(20):
-        assert torch.equal(emu.emu_kv_attention(*args), first)
+    for most in (4, None):                           # (both kernels)
+        first = emu.emu_kv_attention(*args, max_new=most)
+        for _ in range(20):
+            assert torch.equal(emu.emu_kv_attention(*args, max_new=most), first)
 
 
 def test_bad_values_on_the_device(emu):
