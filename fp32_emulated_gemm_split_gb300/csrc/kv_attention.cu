@@ -23,7 +23,10 @@
 // their sums go to a slot in memory, and a second kernel adds them up in order.  (In
 // the first one, by the last CTA to arrive, the sums' code took registers from the
 // steps: 96 sequences 220 us, 192 without it.)  Within a CTA each warp takes every kWarps-th step of ST tokens through a ring of its own,
-// filled by tensor copies: no barrier but at a segment's end.
+// filled by tensor copies: no barrier but at a segment's end.  Measured: next tokens of 96
+// sequences (600,000 tokens, 8 heads of 128, 1.22 GB) 196 us, 6.2 TB/s, 92 % of a
+// copy's rate; the copies alone 181 us.  A ring of three stages and two CTAs an SM: 235;
+// steps of 16 tokens through registers, rows as the MMA's 16 (M): 332.
 //
 // The rows are the MMA's N, so that 8 of them fill it: S^T = K Q^T, O^T = V^T P^T,
 // codes as the A operand, straight from their bytes.  The order of the values in a

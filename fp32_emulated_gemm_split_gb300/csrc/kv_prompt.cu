@@ -15,9 +15,17 @@
 // (kv_join_kernel).  The CTAs take equal consecutive
 // ranges of all units, of which a causal tile has as many as it needs.
 //
+// Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
+// 128, BF16 (412 GFLOP), 668 us, 616 TFLOP/s: tensor cores active in 29 % of the cycles,
+// exponentials' units in 15 %.  A unit of 256 rows takes 5700 cycles, its MMAs 2048: a group's
+// 3000 cycles of arithmetic, the waits from P to the next S (the products, and S over
+// P's place) and the segments' ends are not hidden by the other group.  Barriers that let
+// the groups compute by turns: 831 us for 709.
+//
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
 // taken in a pass of its own over S (0.5 operations a value); O's reference moves
-// only where p s_v would pass 2^14, so O is rarely scaled.
+// only where p s_v would pass 2^14, so O is rarely scaled.  (1200 to 2500 tokens, window
+// 1000, 12 heads over 4 of 96: 187 us.)
 #include "kv_attention.cuh"
 
 namespace emu {
