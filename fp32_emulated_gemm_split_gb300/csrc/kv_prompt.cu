@@ -13,10 +13,12 @@
 // other), so that one's exponentials run beside the other's products; sums of the same
 // rows are joined at the segment's end, as are those of CTAs that share a segment
 // (kv_join_kernel).  The CTAs take equal consecutive
-// ranges of all units, of which a causal tile has as many as it needs.
+// ranges of all units, of which a causal tile has as many as it needs.  Each role goes from
+// a segment to the next by itself, through rings: the next one's codes and scores are under
+// way while the outputs of the last are written.
 //
 // Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
-// 128, BF16 (412 GFLOP), 668 us, 616 TFLOP/s: tensor cores active in 29 % of the cycles,
+// 128, BF16 (412 GFLOP), 664 us, 620 TFLOP/s: tensor cores active in 29 % of the cycles,
 // exponentials' units in 15 %.  A unit of 256 rows takes 5700 cycles, its MMAs 2048: a group's
 // 3000 cycles of arithmetic, the waits from P to the next S (the products, and S over
 // P's place) and the segments' ends are not hidden by the other group.  Barriers that let
@@ -25,7 +27,7 @@
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
 // taken in a pass of its own over S (0.5 operations a value); O's reference moves
 // only where p s_v would pass 2^14, so O is rarely scaled.  (1200 to 2500 tokens, window
-// 1000, 12 heads over 4 of 96: 187 us.)
+// 1000, 12 heads over 4 of 96: 105 us.)
 #include "kv_attention.cuh"
 
 namespace emu {
@@ -36,7 +38,8 @@ constexpr int kPanel = kTile * 128;                  // 128 rows of 64 FP16 valu
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kCopyWarp = kMmaWarp + 2;    // (an issuer for each group)
 constexpr int kThreads = (kCopyWarp + 2) * 32;        // (the last warp fills the fourth group of warps)
-enum { kSoft, kCode, kMma, kCopy, kIdle };
+enum { kCode, kMma, kCopy };
+constexpr int kSegs = 4;                             // segments whose descriptions are held
 // Registers of a thread: at launch, of the groups that turn scores into weights, of the others.
 constexpr int kLaunchRegs = 128, kSoftRegs = 168, kOtherRegs = 88;
 static_assert(kSoftWarps * kSoftRegs + (kThreads / 32 - kSoftWarps) * kOtherRegs <= kThreads / 32 * kLaunchRegs, "no more than there are");
@@ -45,41 +48,46 @@ constexpr int kHalf = kTile / 2;                     // tokens of a copied piece
 // ------------------------------------------------- tiles of a sequence --
 
 // Tile i of a sequence: its units from first(i) to end(i), in the order of tiles and, within one, heads.
-template <int ROWS>
+// What a segment costs besides (its queries, its outputs, units that some row does not see)
+// counts as SETUP units more, that come first, and of which nothing is done: CTAs with many
+// short tiles took 1.6 times as long as the others without them.
+template <int ROWS, int SETUP>
 struct Tiles {
     static constexpr int kSlope = ROWS / kTile;      // units that a tile `group` tiles on lies further
-    int n, group, pos0, window, count;
+    int n, pos0, window, count;
+    uint32_t group;
     __device__ __forceinline__ Tiles(const AttnParams& p, const Seq& s)
-        : n(s.n), group(p.group), pos0(max(s.len, 0) - s.n), window(p.window),
-          count((int)(((int64_t)s.n * p.group + ROWS - 1) / ROWS)) {}
-    __device__ __forceinline__ int64_t end_token(int64_t i) const {      // behind the last one that a row sees, any tile but the last
-        return (int64_t)pos0 + (ROWS * (i + 1) - 1) / group + 1;
+        : n(s.n), pos0(max(s.len, 0) - s.n), window(p.window), count((int)(((int64_t)s.n * p.group + ROWS - 1) / ROWS)),
+          group(p.group) {}
+    static __device__ __forceinline__ int up(int token) { return (token >> 7) + ((token & 127) != 0); }
+    __device__ __forceinline__ int end_token(uint32_t i) const {         // behind the last one that a row sees, any tile but the last
+        return pos0 + (int)((ROWS * (i + 1) - 1) / group) + 1;
     }
-    __device__ __forceinline__ int64_t first_token(int64_t i) const {    // negative: none before
-        return window ? (int64_t)pos0 + ROWS * i / group - window + 1 : -1;
+    __device__ __forceinline__ int first_token(uint32_t i) const {       // negative: none before
+        return window ? pos0 + (int)(ROWS * i / group) - window + 1 : -1;
     }
-    __device__ __forceinline__ int first(int i) const { return (int)(max(first_token(i), (int64_t)0) / kTile); }
+    __device__ __forceinline__ int first(int i) const { return max(first_token(i), 0) / kTile; }
     __device__ __forceinline__ int end(int i) const {                    // (a tile that sees nothing has a unit: it is written)
-        const int64_t e = i == count - 1 ? (int64_t)pos0 + n : end_token(i);
-        return (int)max((e + kTile - 1) >> 7, (int64_t)1);
+        return max(up(i == count - 1 ? pos0 + n : end_token(i)), 1);
     }
     __device__ __forceinline__ int units(int i) const { return end(i) - first(i); }
+    __device__ __forceinline__ int cost(int i) const { return units(i) + SETUP; }
     // sum of max(low, a + kSlope k) over 0 <= k < c
-    static __device__ __forceinline__ int64_t ramp(int64_t a, int64_t c, int64_t low) {
-        const int64_t flat = min((max(low - a, (int64_t)0) + kSlope - 1) / kSlope, c);
-        return flat * low + (c - flat) * a + kSlope * (c - 1 + flat) * (c - flat) / 2;
+    static __device__ __forceinline__ int64_t ramp(int a, int c, int low) {
+        const int flat = min((max(low - a, 0) + kSlope - 1) / kSlope, c);
+        return (int64_t)flat * low + (int64_t)(c - flat) * a + kSlope * ((int64_t)(c - 1 + flat) * (c - flat)) / 2;
     }
-    // Units of the first m tiles, m < count: a tile `group` tiles on lies ROWS tokens on.
-    __device__ __forceinline__ int64_t before(int64_t m) const {
-        int64_t sum = 0;
-        for (int64_t r = 0; r < min((int64_t)group, m); ++r) {
-            const int64_t c = (m - r + group - 1) / group;
-            sum += ramp((end_token(r) + kTile - 1) >> 7, c, 1);
+    // The costs of the first m tiles, m < count: a tile `group` tiles on lies ROWS tokens on.
+    __device__ __forceinline__ int64_t before(uint32_t m) const {
+        int64_t sum = (int64_t)SETUP * m;
+        for (uint32_t r = 0; r < min(group, m); ++r) {
+            const int c = (int)((m - r + group - 1) / group);
+            sum += ramp(up(end_token(r)), c, 1);
             if (window) sum -= ramp(first_token(r) >> 7, c, 0);
         }
         return sum;
     }
-    __device__ __forceinline__ int64_t all() const { return count ? before(count - 1) + units(count - 1) : 0; }
+    __device__ __forceinline__ int64_t all() const { return count ? before(count - 1) + cost(count - 1) : 0; }
 };
 
 // ------------------------------------------------------- tensor memory --
@@ -159,6 +167,7 @@ struct Plan {
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
     static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
     static constexpr int bytes = tiles + slots * piece;
+    static constexpr int setup = PAIR ? 4 : 3;                   // (17,000 to 20,000 cycles, a unit 5000 to 6000)
 };
 
 __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -174,17 +183,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     constexpr int PIECES = TWO ? 2 : 1;
     static_assert(!(PAIR && TWO), "one piece of each tile");
     using Pl = Plan<T, NG, PAIR>;
-    using Ti = Tiles<Pl::rows>;
+    using Ti = Tiles<Pl::rows, Pl::setup>;
     constexpr int SLOTS = Pl::slots, KS = Pl::k_stages, VS = Pl::v_stages, kStageBytes = NG * kPanel;
     extern __shared__ __align__(1024) uint8_t smem[];
     // q: [tile or piece][64 values], k and v: [stage][64 values] panels; then the ring of codes as they are
     const uint32_t q_at = smem_u32(smem), k_at = q_at + Pl::q_tiles * kStageBytes, v_at = k_at + KS * kStageBytes,
                    raw_at = v_at + VS * kStageBytes;
-    __shared__ __align__(8) uint64_t bars[24 + 2 * SLOTS];
+    __shared__ __align__(8) uint64_t bars[33 + 2 * SLOTS];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, nan_flag;
+    __shared__ int abort_flag;
     __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ Work work, work_next;                 // (the next segment: found while this one runs)
+    // Segments, a ring that the copying warp fills: each role goes from one to the next by itself.  And whether a NaN
+    // was taken out of a segment's values.
+    __shared__ Work works[kSegs];
+    __shared__ int nan_flags[kSegs];
     // of a unit's tiles of 16 tokens: keys, values (eight units: a group may still read a unit's while the copies
     // are four ahead)
     __shared__ float scales[8][2][8];
@@ -192,8 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     __shared__ float q_factor[2][kTile];
     __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
     const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
-                   s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 104,
-                   c_full = k_full + 112, o_done = k_full + 176, raw_full = k_full + 192, raw_free = raw_full + 8 * SLOTS;
+                   s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 112,
+                   c_full = k_full + 120, o_done = k_full + 184, seg_full = k_full + 200, seg_free = seg_full + 8 * kSegs,
+                   raw_full = seg_free + 8 * kSegs, raw_free = raw_full + 8 * SLOTS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D;
     volatile int* const aborted = &abort_flag;
     const float nan = __uint_as_float(0x7FC00000u);
@@ -207,15 +220,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, kTile);
             mbar_init(o_done + 8 * i, 1);
+            mbar_init(q_full + 8 * i, kSoftWarps * 32);
         }
-        mbar_init(q_full, kSoftWarps * 32);
         mbar_init(drained, 2);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(seg_full + 8 * i, 1);
+            mbar_init(seg_free + 8 * i, kCopyWarp);  // (a lane of each warp but the copying one and the last)
+            nan_flags[i] = 0;
+        }
         for (int i = 0; i < 8; ++i) mbar_init(c_full + 8 * i, 8);
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_free + 8 * i, kCodeWarps);
         }
-        abort_flag = nan_flag = 0;
+        abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -253,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     const int64_t ctas = min((int64_t)gridDim.x, all);
     bool ok = true;
 
+    uint32_t last_seg = 0;                           // of thread 0: the segment that it had last
     if (blockIdx.x < ctas) {
         const int64_t begin = all * blockIdx.x / ctas;
         if (sum - mine <= begin && begin < sum) {    // (one thread)
@@ -263,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 if (begin < before + n) break;
                 before += n;
             }
+            Work& work = works[0];
             work.all = all;
             work.ctas = ctas;
             work.at = begin;
@@ -273,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         __syncthreads();
         {
             // the tile of the sequence: every thread tries some, twice where there are many
+            Work& work = works[0];
             const Ti ti(p, seq_of(p, work.seq));
             const int64_t u = (work.at - work.base) / p.heads;
             __shared__ int found;
@@ -290,14 +311,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
             if (tid == 0) {
                 work.begin = work.base + ti.before(lo) * p.heads;            // of the tile's first head
-                const int units = ti.units(lo);
-                work.head = (int)((work.at - work.begin) / units);
-                work.begin += (int64_t)work.head * units;
+                const int cost = ti.cost(lo);
+                work.head = (int)((work.at - work.begin) / cost);
+                work.begin += (int64_t)work.head * cost;
                 work.row0 = lo * Pl::rows;
             }
         }
         uint32_t j = 0, second = 0, pieces = 0;      // units, those of a second tile, copied pieces of this CTA so far
-        uint32_t segments = 0;
+        uint32_t seg = 0;                            // segments so far
         // The rest of a segment's description, from its sequence, tile, head, first unit and the CTA's next unit.
         auto describe = [&](Work& w) {
             const Seq s = seq_of(p, w.seq);
@@ -307,11 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             w.start = s.start;
             w.len = max(s.len, 0);
             w.pos0 = w.len - s.n;
-            w.end = w.begin + units;
+            w.end = w.begin + units + Pl::setup;
+            // from unit a to unit b
+            const int a = max((int)(w.at - w.begin) - Pl::setup, 0), b = max((int)(min(w.stop, w.end) - w.begin) - Pl::setup, 0);
             w.rows = (int)min((int64_t)s.n * p.group - w.row0, (int64_t)Pl::rows);
-            w.token0 = (ti.first(i) + (int)(w.at - w.begin)) * kTile;
-            w.units = (int)(min(w.stop, w.end) - w.at);
-            w.starts = w.at == w.begin;
+            w.token0 = (ti.first(i) + a) * kTile;
+            w.units = b - a;
+            w.starts = a == 0;
             w.whole = w.units == units;
         };
         // The segment behind it: the next head, tile or sequence.
@@ -330,27 +353,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             }
             describe(w);
         };
-        if (tid == 0) describe(work);
+        if (tid == 0) describe(works[0]);
         __syncthreads();
+        // Whether this CTA has a unit of the segment behind w.
+        auto goes_on = [](const Work& w) { return w.end + Pl::setup < w.stop; };
+        // whether a row (from position pos_a to pos_b) does not see some token of a unit
+        auto hides = [&](int tok, int pos_a, int pos_b, int len) {
+            return tok + kTile > pos_a + 1 || tok + kTile > len || (p.window && tok <= pos_b - p.window);
+        };
+        // phases: of unit i's stages of keys and values, and of its scores in group t (of a segment from unit j0 on)
+        auto k_phase = [](uint32_t i) { return i / KS & 1; };
+        auto v_phase = [](uint32_t i) { return i / VS & 1; };
+        auto s_phase = [&](uint32_t i, uint32_t t, uint32_t j0, uint32_t second) {
+            return PAIR ? (t ? second + (i - j0) : i) & 1 : i >> 1 & 1;
+        };
+        // Segment seg's description is there (its warps agree).
+        auto has_segment = [&]() {
+            ok = ok && mbar_wait(seg_full + 8 * (seg % kSegs), seg / kSegs & 1, p.err, kDevErrTimeout) && !*aborted;
+            return ok = __all_sync(0xffffffffu, ok);
+        };
+        // Segment seg is over for this warp; whether another one follows.
+        auto leave_segment = [&](const Work& work) {
+            const bool more = goes_on(work), both = PAIR && work.rows > kTile;
+            if (both) second += work.units;
+            j += work.units;
+            pieces += 4 * work.units;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_free + 8 * (seg % kSegs));
+            ++seg;
+            return more;
+        };
         // One segment, as a warp of this role; whether another one follows.
         auto segment = [&](int role) __attribute__((always_inline)) {
+            if (role != kCopy && !has_segment()) {
+                *aborted = 1;
+                return false;
+            }
+            const Work& work = works[seg % kSegs];
             const int units = work.units, token0 = work.token0, len = work.len, pos0 = work.pos0, head = work.head;
             const int row0 = work.row0, rows = work.rows;
             // tokens that some row of the segment sees
             const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
             const int sees_end = max(0, min(len, pos_last + 1));
             const int sees_begin = p.window ? max(0, pos_first - p.window + 1) : 0;
-            // whether some row (from the first's position to the last's) does not see some token of a unit
-            auto hides = [&](int tok, int pos_a, int pos_b) {
-                return tok + kTile > pos_a + 1 || tok + kTile > len || (p.window && tok <= pos_b - p.window);
-            };
-            auto edge_of = [&](int tok) { return hides(tok, pos_first, pos_last); };
             const uint32_t j0 = j, j1 = j + units;
             const bool both = PAIR && rows > kTile;  // (a second tile)
-            // phases: of unit i's stages of keys and values, and of its scores in group t
-            auto k_phase = [](uint32_t i) { return i / KS & 1; };
-            auto v_phase = [](uint32_t i) { return i / VS & 1; };
-            auto s_phase = [&](uint32_t i, uint32_t t) { return PAIR ? (t ? second + (i - j0) : i) & 1 : i >> 1 & 1; };
 
             if (role == kMma) {
                 // ------------------------------------------------- MMAs
@@ -362,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 constexpr uint32_t kStage = kStageBytes >> 4;        // a stage (a piece of Q) in descriptors
                 const uint32_t s_at = tmem + t * kTile, o_at = tmem + (2 + t) * kTile;
                 const bool idle = PAIR && t && !both;
-                ok = ok && mbar_wait(q_full, segments & 1, p.err, kDevErrTimeout);
+                // (two barriers: the rows may be a segment ahead of a group that had no unit in the one before)
+                ok = ok && mbar_wait(q_full + 8 * (seg & 1), seg >> 1 & 1, p.err, kDevErrTimeout);
+                ok = __all_sync(0xffffffffu, ok);
                 // (MMAs of one warp run in the order of their issue: P is read before the next S is written over it)
                 const uint32_t from = PAIR ? j0 : j0 + ((j0 ^ t) & 1);
                 for (uint32_t i = from; i < j1 && ok; i += PAIR ? 1 : 2) {
@@ -386,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     tc_commit(k_free + 8 * (i % KS), leader);
                     // O += P V
                     ok = mbar_wait(v_full + 8 * (i % VS), v_phase(i), p.err, kDevErrTimeout) &&
-                         (idle || mbar_wait(p_full + 8 * t, s_phase(i, t), p.err, kDevErrTimeout)) && !*aborted;
+                         (idle || mbar_wait(p_full + 8 * t, s_phase(i, t, j0, second), p.err, kDevErrTimeout)) && !*aborted;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -464,10 +513,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         mbar_arrive(c_full + 8 * (i & 7));
                     }
                 }
-                if (lane == 0 && work.end < work.stop) {
-                    Work next = work;
-                    advance(next);
-                    work_next = next;
+                // the next segment: as soon as the one that had its place is over
+                if (ok && goes_on(work)) {
+                    const uint32_t x = seg + 1;
+                    ok = mbar_wait(seg_free + 8 * (x % kSegs), (x / kSegs & 1) ^ 1, p.err, kDevErrTimeout) && !*aborted;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && lane == 0) {
+                        Work next = work;
+                        advance(next);
+                        works[x % kSegs] = next;
+                        nan_flags[x % kSegs] = 0;
+                        mbar_arrive(seg_full + 8 * (x % kSegs));
+                    }
                 }
                 if (!ok) {
                     // no copy may land after this CTA is gone
@@ -534,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                 }
                             }
                         }
-                        if (nans) nan_flag = 1;
+                        if (nans) nan_flags[seg % kSegs] = 1;
                     }
 #pragma unroll
                     for (int n = 0; n < NG * 4; ++n)
@@ -547,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 };
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
                     const int tok = token0 + (int)(i - j0) * kTile;
-                    const bool edge = edge_of(tok);
+                    const bool edge = hides(tok, pos_first, pos_last, len);
 #pragma unroll 1
                     for (int side = 0; side < 2 && ok; ++side) {
                         const uint32_t s = side ? i % VS : i % KS, to = (side ? v_at : k_at) + s * kStageBytes;
@@ -561,19 +618,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     }
                 }
                 if (!ok) *aborted = 1;
-            } else if (role == kSoft) {
-                // --------------------------------------------- scores to weights
-                const int half = warp >> 2, r = tid & (kTile - 1);       // group, row of its tile
-                const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-                const int tile_row = PAIR ? half * kTile : 0;    // the tile's first row of the segment
-                const bool idle = PAIR && half && !both;         // no row in the tile
-                const int row = row0 + min(tile_row + r, rows - 1), token = row / p.group, pos = pos0 + token;
-                const int pos_a = pos0 + (row0 + min(tile_row, rows - 1)) / p.group;
-                const int pos_b = pos0 + (row0 + min(tile_row + kTile, rows) - 1) / p.group;
+            }
+            if (role == kCopy) {                     // (no part in seg_free)
+                const bool more = goes_on(work);
+                pieces += 4 * units;
+                j = j1;
+                ++seg;
+                __syncwarp();
+                return ok && more;
+            }
+            return leave_segment(work) && ok;
+        };
+        // Scores to weights, a thread a row; and around them Q of the next segment and the outputs of this one.
+        auto scores_to_weights = [&]() __attribute__((always_inline)) {
+            const int half = warp >> 2, r = tid & (kTile - 1);           // group, row of its tile
+            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t s_at = (tmem + half * kTile) | lanes, o_at = (tmem + (2 + half) * kTile) | lanes;
+            float m = -INFINITY, l = 0.0f, ref = -INFINITY;
+            bool more = true;                        // segment seg follows; segment seg - 1 waits for its last products
+            for (;;) {
+                row_stat[half][r][0] = m;
+                row_stat[half][r][1] = l;
+                row_stat[half][r][2] = ref;
+                // (behind the barrier all scores of segment seg - 1 have been read, and so has its Q)
+                if (more) ok = has_segment();
+                ok = bar_and(1, kSoftWarps * 32, ok);
+                if (!ok) break;
                 // Q: 16 lanes a row, eight values each, 16 rows at a time (all loads before the first use); a group has its
                 // tile's rows, or half of the one tile's
-                float factor;
-                {
+                if (more) {
+                    const Work& work = works[seg % kSegs];
+                    const int row0 = work.row0, rows = work.rows, head = work.head, tile_row = PAIR ? half * kTile : 0;
                     constexpr int ROWS = PAIR ? 32 : 16, LOADS = 8;      // of a warp, at once (16: 709 -> 735 us)
                     const int r0 = (PAIR ? 0 : half * 64) + (warp & 3) * ROWS, d = (lane & 15) * 8;
                     const uint32_t to = q_at + (PAIR ? half * kStageBytes : 0) + (d / 64) * kPanel;
@@ -620,16 +695,125 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         }
                     }
                     fence_async_smem();
-                    mbar_arrive(q_full);
-                    bar_and(1, kSoftWarps * 32, true);
-                    factor = q_factor[PAIR ? half : 0][r];
+                    mbar_arrive(q_full + 8 * (seg & 1));
                 }
-
-                float m = -INFINITY, l = 0.0f, ref = -INFINITY;
-                const uint32_t s_at = (tmem + half * kTile) | lanes, o_at = (tmem + (2 + half) * kTile) | lanes;
+                if (seg > 0) {
+                    // --------------------------------------------- the end of segment seg - 1
+                    // the last products: of this group's tile, of both groups' units
+                    const Work& work = works[(seg - 1) % kSegs];
+                    const int units = work.units, token0 = work.token0, len = work.len, pos0 = work.pos0, head = work.head;
+                    const int row0 = work.row0, rows = work.rows;
+                    const uint32_t j1 = j, j0 = j - units;
+                    const bool both = PAIR && rows > kTile, idle = PAIR && half && !both, two_units = !PAIR && units > 1;
+                    const int tile_row = PAIR ? half * kTile : 0;
+                    const int row = row0 + min(tile_row + r, rows - 1), token = row / p.group, pos = pos0 + token;
+                    const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
+                    auto done = [&](uint32_t i, uint32_t t) {
+                        return mbar_wait(o_done + 8 * t, s_phase(i, t, j0, second - (both ? units : 0)), p.err, kDevErrTimeout);
+                    };
+                    if (!idle) ok = done(j1 - 1, PAIR ? half : (j1 - 1) & 1) && (!two_units || done(j1 - 2, (j1 - 2) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok && !idle) {
+                        tc_fence_after();
+                        const uint32_t s0 = PAIR ? half : j0 & 1;    // the group that had the first unit
+                        const float m_a = row_stat[s0][r][0], l_a = row_stat[s0][r][1], ref_a = row_stat[s0][r][2];
+                        float m_all = m_a, ref_all = ref_a, l_all = l_a, x_a = 1.0f, x_b = 0.0f;
+                        if (two_units) {
+                            const float m_b = row_stat[s0 ^ 1][r][0], l_b = row_stat[s0 ^ 1][r][1], ref_b = row_stat[s0 ^ 1][r][2];
+                            m_all = fmaxf(m_a, m_b);
+                            ref_all = fmaxf(ref_a, ref_b);
+                            l_all = l_a * weight_of(m_a, l_a, m_all) + l_b * weight_of(m_b, l_b, m_all);
+                            x_a = share_of(ref_a, ref_all);
+                            x_b = share_of(ref_b, ref_all);
+                        }
+                        const bool live = tile_row + r < rows;
+                        float* const slot = p.partial + ((2 * (int64_t)blockIdx.x + work.starts) * p.slot_rows + tile_row + r) * (D + 4);
+                        if (!work.whole && live && (PAIR || half == 0))
+                            *reinterpret_cast<float4*>(slot) = make_float4(m_all, l_all, ref_all, 0.0f);
+                        const bool nan_seen = nan_flags[(seg - 1) % kSegs] != 0;
+                        const float f_all = row_factor(work.bad, m_all, l_all, ref_all);
+                        T* const to = static_cast<T*>(p.out) + (work.start + token) * p.out_t +
+                                      (head * p.group + row - token * p.group) * p.out_h;
+                        // eight values of the row from column c
+                        auto put = [&](int c, float (&y)[8]) {
+                            if (!live) return;
+                            if (nan_seen)
+                                for (int u = 0; u < units; ++u) {
+                                    const int tok = token0 + u * kTile;
+                                    if (!hides(tok, pos_first, pos_last, len)) continue;
+                                    const int lo = max(tok, p.window ? pos - p.window + 1 : 0), hi = min(tok + kTile, min(pos, len - 1) + 1);
+                                    for (int t = max(lo, 0); t < hi; ++t) {
+                                        const int page = p.table[(int64_t)work.seq * p.width + (t >> p.page_log)];
+                                        if (page < 0 || page >= p.pages) continue;
+                                        const uint8_t* v = p.v + (((((int64_t)page * p.heads + head) << p.page_log) +
+                                                                   (t & ((1 << p.page_log) - 1))) * D + c);
+                                        for (int e = 0; e < 8; ++e)
+                                            if ((v[e] & 0x7F) == 0x7F) y[e] = nan;
+                                    }
+                                }
+                            if (work.whole) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] *= f_all;
+                                kv_store8(to + c, p.wide_out, y);
+                            } else {
+                                *reinterpret_cast<float4*>(slot + 4 + c) = make_float4(y[0], y[1], y[2], y[3]);
+                                *reinterpret_cast<float4*>(slot + 8 + c) = make_float4(y[4], y[5], y[6], y[7]);
+                            }
+                        };
+                        if constexpr (PAIR) {
+                            // (the next columns on the way while these are written: 830 us for 700, registers of the units' loop)
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t a[16];
+                                tmem_ld_32x32b_x16((tmem + (2 + s0) * kTile + c) | lanes, a);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float y[8];
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(a[8 * h + e]);
+                                    put(c + 8 * h, y);
+                                }
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+                                uint32_t a[8], b[8];
+                                tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
+                                if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
+                                tmem_ld_wait();
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    y[e] = __uint_as_float(a[e]) * x_a;
+                                    if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
+                                }
+                                put(c, y);
+                            }
+                        }
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(seg_free + 8 * ((seg - 1) % kSegs));
+                }
+                if (!more) break;
+                // Q's factors; and the products of segment seg go over what was read here
+                ok = bar_and(1, kSoftWarps * 32, ok);
+                if (!ok) break;
+                const Work& work = works[seg % kSegs];
+                const int units = work.units, token0 = work.token0, len = work.len, rows = work.rows, row0 = work.row0;
+                const int tile_row = PAIR ? half * kTile : 0;    // the tile's first row of the segment
+                const bool both = PAIR && rows > kTile, idle = PAIR && half && !both;    // a second tile; no row in this one
+                const int pos = work.pos0 + (row0 + min(tile_row + r, rows - 1)) / p.group;
+                const int pos_a = work.pos0 + (row0 + min(tile_row, rows - 1)) / p.group;
+                const int pos_b = work.pos0 + (row0 + min(tile_row + kTile, rows) - 1) / p.group;
+                const uint32_t j0 = j, j1 = j + units;
+                const float factor = q_factor[PAIR ? half : 0][r];
+                m = ref = -INFINITY;
+                l = 0.0f;
                 bool first = true;
                 for (uint32_t i = PAIR ? (idle ? j1 : j0) : j0 + ((j0 ^ half) & 1); i < j1 && ok; i += PAIR ? 1 : 2) {
-                    ok = mbar_wait(s_full + 8 * half, s_phase(i, half), p.err, kDevErrTimeout) &&
+                    ok = mbar_wait(s_full + 8 * half, s_phase(i, half, j0, second), p.err, kDevErrTimeout) &&
                          mbar_wait(c_full + 8 * (i & 7), i >> 3 & 1, p.err, kDevErrTimeout) && !*aborted;
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -637,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     }
                     tc_fence_after();
                     const int tok = token0 + (int)(i - j0) * kTile;
-                    const bool edge = hides(tok, pos_a, pos_b);
+                    const bool edge = hides(tok, pos_a, pos_b, len);
                     const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
                     const float* const ks = scales[i & 7][0];
                     const float* const vs = scales[i & 7][1];
@@ -724,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                         const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
                         if (!first) {
                             // (O is whole once the group's unit before is)
-                            ok = mbar_wait(o_done + 8 * half, s_phase(i, half) ^ 1, p.err, kDevErrTimeout);
+                            ok = mbar_wait(o_done + 8 * half, s_phase(i, half, j0, second) ^ 1, p.err, kDevErrTimeout);
                             if (!__all_sync(0xffffffffu, ok)) {
                                 ok = false;
                                 break;
@@ -787,135 +971,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     tc_fence_before();
                     mbar_arrive(p_full + 8 * half);
                 }
-                if (!ok) *aborted = 1;
-                // --------------------------------------------- the segment's end
-                row_stat[half][r][0] = m;
-                row_stat[half][r][1] = l;
-                row_stat[half][r][2] = ref;
-                // the last products: of this group's tile, of both groups' units
-                const bool two_units = !PAIR && units > 1;
-                if (ok && !idle) {
-                    const uint32_t t = PAIR ? half : (j1 - 1) & 1;
-                    ok = mbar_wait(o_done + 8 * t, s_phase(j1 - 1, t), p.err, kDevErrTimeout);
-                }
-                if (ok && two_units) ok = mbar_wait(o_done + 8 * ((j1 - 2) & 1), s_phase(j1 - 2, (j1 - 2) & 1), p.err, kDevErrTimeout);
-                ok = bar_and(1, kSoftWarps * 32, ok);
-                if (ok && !idle) {
-                    tc_fence_after();
-                    const uint32_t s0 = PAIR ? half : j0 & 1;    // the group that had the first unit
-                    const float m_a = row_stat[s0][r][0], l_a = row_stat[s0][r][1], ref_a = row_stat[s0][r][2];
-                    float m_all = m_a, ref_all = ref_a, l_all = l_a, x_a = 1.0f, x_b = 0.0f;
-                    if (two_units) {
-                        const float m_b = row_stat[s0 ^ 1][r][0], l_b = row_stat[s0 ^ 1][r][1], ref_b = row_stat[s0 ^ 1][r][2];
-                        m_all = fmaxf(m_a, m_b);
-                        ref_all = fmaxf(ref_a, ref_b);
-                        l_all = l_a * weight_of(m_a, l_a, m_all) + l_b * weight_of(m_b, l_b, m_all);
-                        x_a = share_of(ref_a, ref_all);
-                        x_b = share_of(ref_b, ref_all);
-                    }
-                    const bool live = tile_row + r < rows;
-                    float* const slot = p.partial + ((2 * (int64_t)blockIdx.x + work.starts) * p.slot_rows + tile_row + r) * (D + 4);
-                    if (!work.whole && live && (PAIR || half == 0))
-                        *reinterpret_cast<float4*>(slot) = make_float4(m_all, l_all, ref_all, 0.0f);
-                    const bool nan_seen = nan_flag != 0;
-                    const float f_all = row_factor(work.bad, m_all, l_all, ref_all);
-                    T* const to = static_cast<T*>(p.out) + (work.start + token) * p.out_t +
-                                  (head * p.group + row - token * p.group) * p.out_h;
-                    // eight values of the row from column c
-                    auto put = [&](int c, float (&y)[8]) {
-                        if (!live) return;
-                        if (nan_seen)
-                            for (int u = 0; u < units; ++u) {
-                                const int tok = token0 + u * kTile;
-                                if (!edge_of(tok)) continue;
-                                const int lo = max(tok, p.window ? pos - p.window + 1 : 0), hi = min(tok + kTile, min(pos, len - 1) + 1);
-                                for (int t = max(lo, 0); t < hi; ++t) {
-                                    const int page = p.table[(int64_t)work.seq * p.width + (t >> p.page_log)];
-                                    if (page < 0 || page >= p.pages) continue;
-                                    const uint8_t* v = p.v + (((((int64_t)page * p.heads + head) << p.page_log) +
-                                                               (t & ((1 << p.page_log) - 1))) * D + c);
-                                    for (int e = 0; e < 8; ++e)
-                                        if ((v[e] & 0x7F) == 0x7F) y[e] = nan;
-                                }
-                            }
-                        if (work.whole) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] *= f_all;
-                            kv_store8(to + c, p.wide_out, y);
-                        } else {
-                            *reinterpret_cast<float4*>(slot + 4 + c) = make_float4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<float4*>(slot + 8 + c) = make_float4(y[4], y[5], y[6], y[7]);
-                        }
-                    };
-                    if constexpr (PAIR) {
-                        // (the next columns on the way while these are written: 830 us for 700, registers of the units' loop)
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t a[16];
-                            tmem_ld_32x32b_x16((tmem + (2 + s0) * kTile + c) | lanes, a);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float y[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(a[8 * h + e]);
-                                put(c + 8 * h, y);
-                            }
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
-                            uint32_t a[8], b[8];
-                            tmem_ld_32x32b_x8((tmem + (2 + s0) * kTile + c) | lanes, a);
-                            if (two_units) tmem_ld_32x32b_x8((tmem + (2 + (s0 ^ 1)) * kTile + c) | lanes, b);
-                            tmem_ld_wait();
-                            float y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                y[e] = __uint_as_float(a[e]) * x_a;
-                                if (two_units) y[e] = fmaf(__uint_as_float(b[e]), x_b, y[e]);
-                            }
-                            put(c, y);
-                        }
-                    }
-                    tc_fence_before();
-                }
+                ok = __all_sync(0xffffffffu, ok);
+                more = goes_on(work);
+                j = j1;
+                if (both) second += units;
+                ++seg;
             }
-            if (both) second += units;
-            j = j1;
-            pieces += 4 * units;
-            ++segments;
-            if (__syncthreads_or(!ok) || work.end >= work.stop) return false;
-            __syncthreads();                         // (all have looked)
-            if (tid == 0) {
-                work = work_next;
-                nan_flag = 0;
-            }
-            __syncthreads();
-            return true;
+            if (!ok) *aborted = 1;
+            last_seg = seg ? seg - 1 : 0;
         };
         // (a unit's P waits in registers: with 128 for all, spilled, prompts took 700 us)
-        if (warp < kSoftWarps) {
+        if (works[0].units == 0) {                   // (nothing but a segment's setup: the next CTA does it)
+        } else if (warp < kSoftWarps) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftRegs));
-            while (segment(kSoft)) {}
+            scores_to_weights();
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
             if (warp < kMmaWarp) while (segment(kCode)) {}
             else if (warp < kCopyWarp) while (segment(kMma)) {}
-            else if (warp == kCopyWarp) while (segment(kCopy)) {}
-            else while (segment(kIdle)) {}
+            else if (warp == kCopyWarp) {
+                if (lane == 0) mbar_arrive(seg_full);            // (the first segment)
+                while (segment(kCopy)) {}
+            }
         }
         // (tensor memory is freed behind the MMAs issued; they are done unless a wait gave up)
-        if ((warp == kMmaWarp || warp == kMmaWarp + 1) && !ok) {
+        if ((warp == kMmaWarp || warp == kMmaWarp + 1) && (!ok || *aborted)) {
             const uint32_t leader = elect_one();
             tc_commit(drained, leader);
             mbar_wait(drained, 0, p.err, kDevErrTimeout);
         }
     }
     if (tid == 0) {
-        if (blockIdx.x >= ctas) work.units = 0;
-        else if (work.whole || !work.starts) work.units = 0;
-        p.shared[blockIdx.x] = work;
+        Work w = works[last_seg % kSegs];
+        if (blockIdx.x >= ctas || w.whole || !w.starts) w.units = 0;     // (or 0 as it is)
+        p.shared[blockIdx.x] = w;
     }
     tc_fence_before();
     __syncthreads();
