@@ -18,11 +18,11 @@
 // way while the outputs of the last are written.
 //
 // Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
-// 128, BF16 (412 GFLOP), 664 us, 620 TFLOP/s: tensor cores active in 29 % of the cycles,
-// exponentials' units in 15 %.  A unit of 256 rows takes 5700 cycles, its MMAs 2048: a group's
-// 3000 cycles of arithmetic, the waits from P to the next S (the products, and S over
-// P's place) and the segments' ends are not hidden by the other group.  Barriers that let
-// the groups compute by turns: 831 us for 709.
+// 128, BF16 (412 GFLOP), 594 us, 693 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
+// MMAs 2560 (scores of 64 tokens are bound by reading Q again: 512 of them), a group's weights
+// 2500; codes, MMAs and weights wait for one another.  A segment costs 17,000 cycles
+// besides: Q, units that some row does not see, outputs.  Barriers that let the groups compute by
+// turns: 831 us for 709 before.
 //
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
 // taken in a pass of its own over S (0.5 operations a value); O's reference moves
@@ -160,9 +160,13 @@ struct Plan {
     static constexpr bool TWO = sizeof(T) == 4;
     static constexpr int rows = PAIR ? 2 * kTile : kTile;
     static constexpr int q_tiles = PAIR || TWO ? 2 : 1;          // tiles of Q, or pieces
-    // (two stages of V where the groups take units in turn: each issuer then meets every phase of its own.  One of K
-    // and two of V for a pair: 727 us for 709)
-    static constexpr int k_stages = 2, v_stages = PAIR ? 1 : 2;
+    // Two stages of V, so that they are written while products run; where the groups take units in turn two of K as well
+    // (each issuer then meets every phase of its own).  Pairs: 594 us, two of K and one of V 630, two each 607 (three
+    // slots are left for codes).
+    static constexpr int k_stages = PAIR ? 1 : 2, v_stages = 2;
+    // Parts of a unit whose scores and weights go by themselves: the scores of one are under way while the group looks at
+    // the other's.  (16-bit pairs: 664 us, 630 in two; FP32 in two 123 us for 105)
+    static constexpr int parts = PAIR ? 2 : 1;
     static constexpr int piece = kHalf * NG * 64;                // bytes of a piece of codes
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
     static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
@@ -184,12 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     static_assert(!(PAIR && TWO), "one piece of each tile");
     using Pl = Plan<T, NG, PAIR>;
     using Ti = Tiles<Pl::rows, Pl::setup>;
-    constexpr int SLOTS = Pl::slots, KS = Pl::k_stages, VS = Pl::v_stages, kStageBytes = NG * kPanel;
+    constexpr int SLOTS = Pl::slots, PARTS = Pl::parts, kPart = kTile / PARTS, KS = Pl::k_stages, VS = Pl::v_stages, kStageBytes = NG * kPanel;
     extern __shared__ __align__(1024) uint8_t smem[];
     // q: [tile or piece][64 values], k and v: [stage][64 values] panels; then the ring of codes as they are
     const uint32_t q_at = smem_u32(smem), k_at = q_at + Pl::q_tiles * kStageBytes, v_at = k_at + KS * kStageBytes,
                    raw_at = v_at + VS * kStageBytes;
-    __shared__ __align__(8) uint64_t bars[33 + 2 * SLOTS];
+    __shared__ __align__(8) uint64_t bars[39 + 2 * SLOTS];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int64_t warp_sum[kThreads / 32];
@@ -204,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     __shared__ float q_factor[2][kTile];
     __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
     const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
-                   s_full = k_full + 64, p_full = k_full + 80, q_full = k_full + 96, drained = k_full + 112,
-                   c_full = k_full + 120, o_done = k_full + 184, seg_full = k_full + 200, seg_free = seg_full + 8 * kSegs,
+                   s_full = k_full + 64, p_full = k_full + 96, o_done = k_full + 128,      // [group][part]
+                   q_full = k_full + 160, drained = k_full + 176, c_full = k_full + 184, seg_full = k_full + 248,
+                   seg_free = seg_full + 8 * kSegs,
                    raw_full = seg_free + 8 * kSegs, raw_free = raw_full + 8 * SLOTS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D;
     volatile int* const aborted = &abort_flag;
@@ -217,10 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             mbar_init(k_free + 8 * i, PAIR ? 2 : 1);
             mbar_init(v_full + 8 * i, kCodeWarps * 32);
             mbar_init(v_free + 8 * i, PAIR ? 2 : 1);
+            mbar_init(q_full + 8 * i, kSoftWarps * 32);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, kTile);
             mbar_init(o_done + 8 * i, 1);
-            mbar_init(q_full + 8 * i, kSoftWarps * 32);
         }
         mbar_init(drained, 2);
         for (int i = 0; i < kSegs; ++i) {
@@ -357,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         __syncthreads();
         // Whether this CTA has a unit of the segment behind w.
         auto goes_on = [](const Work& w) { return w.end + Pl::setup < w.stop; };
-        // whether a row (from position pos_a to pos_b) does not see some token of a unit
-        auto hides = [&](int tok, int pos_a, int pos_b, int len) {
-            return tok + kTile > pos_a + 1 || tok + kTile > len || (p.window && tok <= pos_b - p.window);
+        // whether a row (from position pos_a to pos_b) does not see some of the tokens
+        auto hides = [&](int tok, int tokens, int pos_a, int pos_b, int len) {
+            return tok + tokens > pos_a + 1 || tok + tokens > len || (p.window && tok <= pos_b - p.window);
         };
         // phases: of unit i's stages of keys and values, and of its scores in group t (of a segment from unit j0 on)
         auto k_phase = [](uint32_t i) { return i / KS & 1; };
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 // ------------------------------------------------- MMAs
                 const uint32_t t = warp - kMmaWarp;  // the group
                 const uint32_t leader = elect_one();
-                const uint32_t idesc_s = make_idesc(0u, kTile, kTile), idesc_o = make_idesc(0u, kTile, D) | kIdescBMn;
+                const uint32_t idesc_s = make_idesc(0u, kTile, kPart), idesc_o = make_idesc(0u, kTile, D) | kIdescBMn;
                 const uint64_t q_desc = make_sw128_kmajor_desc(q_at + (PAIR ? t : 0) * kStageBytes);
                 const uint64_t k_desc = make_sw128_kmajor_desc(k_at), v_desc = make_sw128_mn_desc(v_at, kPanel);
                 constexpr uint32_t kStage = kStageBytes >> 4;        // a stage (a piece of Q) in descriptors
@@ -412,46 +419,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 // (two barriers: the rows may be a segment ahead of a group that had no unit in the one before)
                 ok = ok && mbar_wait(q_full + 8 * (seg & 1), seg >> 1 & 1, p.err, kDevErrTimeout);
                 ok = __all_sync(0xffffffffu, ok);
-                // (MMAs of one warp run in the order of their issue: P is read before the next S is written over it)
-                const uint32_t from = PAIR ? j0 : j0 + ((j0 ^ t) & 1);
-                for (uint32_t i = from; i < j1 && ok; i += PAIR ? 1 : 2) {
-                    // S = Q K^T
-                    ok = ok && mbar_wait(k_full + 8 * (i % KS), k_phase(i), p.err, kDevErrTimeout) && !*aborted;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (!idle) {
-                        const uint64_t b = k_desc + i % KS * kStage;
+                // S = Q K^T, part h of unit i
+                auto scores = [&](uint32_t i, int h) {
+                    const uint64_t b = k_desc + i % KS * kStage + h * (kPart * 128 >> 4);
 #pragma unroll
-                        for (int piece = PIECES - 1; piece >= 0; --piece)
+                    for (int piece = PIECES - 1; piece >= 0; --piece)
 #pragma unroll
-                            for (int k = 0; k < NG * 4; ++k)
-                                if (k < D / 16) {
-                                    const uint32_t step = (k / 4) * (kPanel >> 4) + (k % 4) * 2;
-                                    mma_cta1(s_at, q_desc + piece * kStage + step, b + step, idesc_s, piece < PIECES - 1 || k > 0, leader);
-                                }
-                        tc_commit(s_full + 8 * t, leader);
+                        for (int k = 0; k < NG * 4; ++k)
+                            if (k < D / 16) {
+                                const uint32_t step = (k / 4) * (kPanel >> 4) + (k % 4) * 2;
+                                mma_cta1(s_at + h * kPart, q_desc + piece * kStage + step, b + step, idesc_s,
+                                         piece < PIECES - 1 || k > 0, leader);
+                            }
+                    tc_commit(s_full + 8 * (2 * t + h), leader);
+                };
+                // O += P V
+                auto products = [&](uint32_t i, int h, bool go_on) {
+                    const uint64_t b = v_desc + i % VS * kStage;
+#pragma unroll
+                    for (int x = 0; x < kPart / 16; ++x) {
+                        // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
+                        const int k = h * (kPart / 16) + x;
+                        const uint32_t at = s_at + 32 * (k / 2) + 8 * (k % 2);
+                        if constexpr (TWO) mma_cta1_ta(o_at, at + 16, b + k * (2048 >> 4), idesc_o, x > 0 || go_on, leader);
+                        mma_cta1_ta(o_at, at, b + k * (2048 >> 4), idesc_o, TWO || x > 0 || go_on, leader);
                     }
-                    tc_commit(k_free + 8 * (i % KS), leader);
-                    // O += P V
-                    ok = mbar_wait(v_full + 8 * (i % VS), v_phase(i), p.err, kDevErrTimeout) &&
-                         (idle || mbar_wait(p_full + 8 * t, s_phase(i, t, j0, second), p.err, kDevErrTimeout)) && !*aborted;
+                    tc_commit(o_done + 8 * (2 * t + h), leader);
+                };
+                auto wait = [&](uint32_t bar, uint32_t phase) {
+                    ok = ok && mbar_wait(bar, phase, p.err, kDevErrTimeout) && !*aborted;
                     ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
                     tc_fence_after();
-                    if (!idle) {
-                        const uint64_t b = v_desc + i % VS * kStage;
-                        const bool go_on = i > from;
+                    return ok;
+                };
+                // MMAs of one warp run in the order of their issue, so P is read before the next S is written over it:
+                // part 0 of the next unit is on the way while the group looks at part 1.
+                const uint32_t by = PAIR ? 1 : 2, from = PAIR ? j0 : j0 + ((j0 ^ t) & 1);
+                if (from < j1 && wait(k_full + 8 * (from % KS), k_phase(from))) {
+                    if (!idle)
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k) {
-                            // (2048 bytes of V a step; P's pieces beside one another, 32 tokens at a time)
-                            if constexpr (TWO)
-                                mma_cta1_ta(o_at, s_at + 16 + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, k > 0 || go_on, leader);
-                            mma_cta1_ta(o_at, s_at + 32 * (k / 2) + 8 * (k % 2), b + k * (2048 >> 4), idesc_o, TWO || k > 0 || go_on, leader);
+                        for (int h = 0; h < PARTS; ++h) scores(from, h);
+                    tc_commit(k_free + 8 * (from % KS), leader);
+                }
+                for (uint32_t i = from; i < j1 && ok; i += by) {
+                    const uint32_t next = i + by, phase = s_phase(i, t, j0, second);
+                    if (!wait(v_full + 8 * (i % VS), v_phase(i))) break;
+#pragma unroll
+                    for (int h = 0; h < PARTS; ++h) {
+                        if (!idle) {
+                            if (!wait(p_full + 8 * (2 * t + h), phase)) break;
+                            products(i, h, h > 0 || i > from);
                         }
-                        tc_commit(o_done + 8 * t, leader);
+                        if (h == PARTS - 1) tc_commit(v_free + 8 * (i % VS), leader);
+                        if (next < j1) {
+                            if (h == 0 && !wait(k_full + 8 * (next % KS), k_phase(next))) break;
+                            if (!idle) scores(next, h);
+                            if (h == PARTS - 1) tc_commit(k_free + 8 * (next % KS), leader);
+                        }
                     }
-                    tc_commit(v_free + 8 * (i % VS), leader);
                 }
                 if (!ok) *aborted = 1;
             } else if (role == kCopy) {
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 };
                 for (uint32_t i = j0; i < j1 && ok; ++i) {
                     const int tok = token0 + (int)(i - j0) * kTile;
-                    const bool edge = hides(tok, pos_first, pos_last, len);
+                    const bool edge = hides(tok, kTile, pos_first, pos_last, len);
 #pragma unroll 1
                     for (int side = 0; side < 2 && ok; ++side) {
                         const uint32_t s = side ? i % VS : i % KS, to = (side ? v_at : k_at) + s * kStageBytes;
@@ -709,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                     const int row = row0 + min(tile_row + r, rows - 1), token = row / p.group, pos = pos0 + token;
                     const int pos_first = pos0 + row0 / p.group, pos_last = pos0 + (row0 + rows - 1) / p.group;
                     auto done = [&](uint32_t i, uint32_t t) {
-                        return mbar_wait(o_done + 8 * t, s_phase(i, t, j0, second - (both ? units : 0)), p.err, kDevErrTimeout);
+                        return mbar_wait(o_done + 8 * (2 * t + PARTS - 1), s_phase(i, t, j0, second - (both ? units : 0)), p.err, kDevErrTimeout);
                     };
                     if (!idle) ok = done(j1 - 1, PAIR ? half : (j1 - 1) & 1) && (!two_units || done(j1 - 2, (j1 - 2) & 1));
                     ok = __all_sync(0xffffffffu, ok);
@@ -740,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             if (nan_seen)
                                 for (int u = 0; u < units; ++u) {
                                     const int tok = token0 + u * kTile;
-                                    if (!hides(tok, pos_first, pos_last, len)) continue;
+                                    if (!hides(tok, kTile, pos_first, pos_last, len)) continue;
                                     const int lo = max(tok, p.window ? pos - p.window + 1 : 0), hi = min(tok + kTile, min(pos, len - 1) + 1);
                                     for (int t = max(lo, 0); t < hi; ++t) {
                                         const int page = p.table[(int64_t)work.seq * p.width + (t >> p.page_log)];
@@ -813,163 +838,168 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 l = 0.0f;
                 bool first = true;
                 for (uint32_t i = PAIR ? (idle ? j1 : j0) : j0 + ((j0 ^ half) & 1); i < j1 && ok; i += PAIR ? 1 : 2) {
-                    ok = mbar_wait(s_full + 8 * half, s_phase(i, half, j0, second), p.err, kDevErrTimeout) &&
-                         mbar_wait(c_full + 8 * (i & 7), i >> 3 & 1, p.err, kDevErrTimeout) && !*aborted;
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int tok = token0 + (int)(i - j0) * kTile;
-                    const bool edge = hides(tok, pos_a, pos_b, len);
-                    const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
-                    const float* const ks = scales[i & 7][0];
-                    const float* const vs = scales[i & 7][1];
-                    if constexpr (!TWO) {
-                        // Most units: the maximum and the reference as they are, and P held back until it is known
-                        // that none of it passed FP16's range.
-                        if (!edge && !first) {
-                            uint32_t w[kTile / 2], sc[2][16];
-                            __half2 most = __float2half2_rn(0.0f);
-                            uint64_t sums = 0;
-                            const uint64_t m2 = two(-m);
-                            const float up = exp2_of(m - ref);
-                            tmem_ld_32x32b_x16(s_at, sc[0]);
+                    const uint32_t phase = s_phase(i, half, j0, second);
+#pragma unroll 1
+                    for (int h = 0; h < PARTS; ++h) {
+                        ok = mbar_wait(s_full + 8 * (2 * half + h), phase, p.err, kDevErrTimeout) &&
+                             mbar_wait(c_full + 8 * (i & 7), i >> 3 & 1, p.err, kDevErrTimeout) && !*aborted;
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const int tok = token0 + (int)(i - j0) * kTile + h * kPart;
+                        const uint32_t s_part = s_at + h * kPart;
+                        const bool edge = hides(tok, kPart, pos_a, pos_b, len);
+                        const int last = min(pos, len - 1), from = p.window ? pos - p.window : -1;
+                        const float* const ks = scales[i & 7][0] + h * (kPart / 16);
+                        const float* const vs = scales[i & 7][1] + h * (kPart / 16);
+                        if constexpr (!TWO) {
+                            // Most units: the maximum and the reference as they are, and P held back until it is known
+                            // that none of it passed FP16's range.
+                            if (!edge && !first) {
+                                uint32_t w[kPart / 2], sc[2][16];
+                                __half2 most = __float2half2_rn(0.0f);
+                                uint64_t sums = 0;
+                                const uint64_t m2 = two(-m);
+                                const float up = exp2_of(m - ref);
+                                tmem_ld_32x32b_x16(s_part, sc[0]);
 #pragma unroll
-                            for (int g = 0; g < kTile / 16; ++g) {
+                                for (int g = 0; g < kPart / 16; ++g) {
+                                    tmem_ld_wait();
+                                    if (g + 1 < kPart / 16) tmem_ld_32x32b_x16(s_part + 16 * (g + 1), sc[(g + 1) & 1]);
+                                    const uint64_t k2 = two(factor * ks[g]), f2 = two(vs[g] * up);
+#pragma unroll
+                                    for (int e = 0; e < 16; e += 2) {
+                                        const uint64_t x = fma_f32x2(pack_f32x2(sc[g & 1][e], sc[g & 1][e + 1]), k2, m2);
+                                        const uint64_t pp = pack_f32x2(__float_as_uint(exp2_of(lo_of(x))), __float_as_uint(exp2_of(hi_of(x))));
+                                        sums = add_f32x2(sums, pp);
+                                        const uint64_t ww = mul_f32x2(pp, f2);
+                                        const uint32_t h = half2_bits(lo_of(ww), hi_of(ww));
+                                        most = __hmax2(most, *reinterpret_cast<const __half2*>(&h));
+                                        w[8 * g + e / 2] = h;
+                                    }
+                                }
+                                const float more = lo_of(sums) + hi_of(sums);
+                                const bool fits = !__hisinf(__low2half(most)) && !__hisinf(__high2half(most)) && !(more > 1e37f) &&
+                                                  m > -INFINITY;
+                                if (__all_sync(0xffffffffu, fits)) {
+                                    l += more;
+#pragma unroll
+                                    for (int c = 0; c < kPart / 32; ++c)
+                                        tmem_st_x16(s_part + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * c));
+                                    tmem_st_wait();
+                                    tc_fence_before();
+                                    mbar_arrive(p_full + 8 * (2 * half + h));
+                                    continue;
+                                }
+                            }
+                        }
+                        // the largest score, and the largest with its page's bound
+                        float top = -INFINITY, over = -INFINITY;
+                        uint32_t sc[2][16];              // (16 scores on the way while those before are looked at)
+                        tmem_ld_32x32b_x16(s_part, sc[0]);
+#pragma unroll 1
+                        for (int c = 0; c < kPart; c += 32)
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
                                 tmem_ld_wait();
-                                if (g + 1 < kTile / 16) tmem_ld_32x32b_x16(s_at + 16 * (g + 1), sc[(g + 1) & 1]);
-                                const uint64_t k2 = two(factor * ks[g]), f2 = two(vs[g] * up);
+                                if (g == 0) tmem_ld_32x32b_x16(s_part + c + 16, sc[1]);
+                                else if (c + 32 < kPart) tmem_ld_32x32b_x16(s_part + c + 32, sc[0]);
+                                if (edge) {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        const int t = tok + c + 16 * g + e;
+                                        if (t > last || t <= from) sc[g][e] = 0xFF800000u;
+                                    }
+                                }
+                                float x[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    x[e] = fmaxf(fmaxf(__uint_as_float(sc[g][e]), __uint_as_float(sc[g][4 + e])),
+                                                 fmaxf(__uint_as_float(sc[g][8 + e]), __uint_as_float(sc[g][12 + e])));
+                                float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                                // (what no row sees has scale 0)
+                                if (y > -INFINITY) {
+                                    y *= factor * ks[c / 16 + g];
+                                    top = fmaxf(top, y);
+                                    over = fmaxf(over, y + (float)scale_bound(vs[c / 16 + g]));
+                                }
+                            }
+                        if (top > m) {
+                            l *= exp2_of(m - top);
+                            m = top;
+                        }
+                        // o's reference: p s_v is 2^8 (16-bit rows: 2^4) at its largest (scale_bound is 14 below), and the
+                        // reference moves where it would pass 2^14
+                        const bool move = over > ref;
+                        if (__any_sync(0xffffffffu, move)) {
+                            const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
+                            if (!first) {
+                                // (O is whole once the products of the group's part before are)
+                                ok = mbar_wait(o_done + 8 * (2 * half + (h ^ (PARTS - 1))), phase ^ (h == 0), p.err, kDevErrTimeout);
+                                if (!__all_sync(0xffffffffu, ok)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const float f = move ? exp2_of(ref - now) : 1.0f;
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 8) {
+                                    uint32_t o[8];
+                                    tmem_ld_32x32b_x8(o_at + c, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st_32x32b_x8(o_at + c, o);
+                                }
+                                tmem_st_wait();
+                            }
+                            ref = now;
+                        }
+                        first = false;
+                        const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
+                        uint64_t sums = 0;
+                        tmem_ld_32x32b_x16(s_part, sc[0]);
+#pragma unroll 1
+                        for (int c = 0; c < kPart; c += 32) {
+                            uint32_t w[16], rest[16];
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                tmem_ld_wait();
+                                if (g == 0) tmem_ld_32x32b_x16(s_part + c + 16, sc[1]);
+                                else if (c + 32 < kPart) tmem_ld_32x32b_x16(s_part + c + 32, sc[0]);
+                                const uint64_t k2 = two(factor * ks[c / 16 + g]), m2 = two(-m0), f2 = two(vs[c / 16 + g] * up);
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2) {
-                                    const uint64_t x = fma_f32x2(pack_f32x2(sc[g & 1][e], sc[g & 1][e + 1]), k2, m2);
-                                    const uint64_t pp = pack_f32x2(__float_as_uint(exp2_of(lo_of(x))), __float_as_uint(exp2_of(hi_of(x))));
+                                    const uint64_t x = fma_f32x2(pack_f32x2(sc[g][e], sc[g][e + 1]), k2, m2);
+                                    float p0 = exp2_of(lo_of(x)), p1 = exp2_of(hi_of(x));
+                                    if (edge) {
+                                        const int t0 = tok + c + 16 * g + e;
+                                        if (t0 > last || t0 <= from) p0 = 0.0f;
+                                        if (t0 + 1 > last || t0 + 1 <= from) p1 = 0.0f;
+                                    }
+                                    const uint64_t pp = pack_f32x2(__float_as_uint(p0), __float_as_uint(p1));
                                     sums = add_f32x2(sums, pp);
                                     const uint64_t ww = mul_f32x2(pp, f2);
-                                    const uint32_t h = half2_bits(lo_of(ww), hi_of(ww));
-                                    most = __hmax2(most, *reinterpret_cast<const __half2*>(&h));
-                                    w[8 * g + e / 2] = h;
+                                    float w0 = lo_of(ww), w1 = hi_of(ww);
+                                    if (edge) {          // (a page that is not there has no scale)
+                                        if (p0 == 0.0f) w0 = 0.0f;
+                                        if (p1 == 0.0f) w1 = 0.0f;
+                                    }
+                                    w[8 * g + e / 2] = half2_bits(w0, w1);
+                                    if constexpr (TWO) rest[8 * g + e / 2] = half2_rest(w0, w1, w[8 * g + e / 2]);
                                 }
                             }
-                            const float more = lo_of(sums) + hi_of(sums);
-                            const bool fits = !__hisinf(__low2half(most)) && !__hisinf(__high2half(most)) && !(more > 1e37f) &&
-                                              m > -INFINITY;
-                            if (__all_sync(0xffffffffu, fits)) {
-                                l += more;
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    tmem_st_x16(s_at + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(w + 16 * c));
-                                tmem_st_wait();
-                                tc_fence_before();
-                                mbar_arrive(p_full + 8 * half);
-                                continue;
-                            }
+                            // over the scores just read
+                            tmem_st_x16(s_part + c, w);
+                            if constexpr (TWO) tmem_st_x16(s_part + c + 16, rest);
                         }
+                        l += lo_of(sums) + hi_of(sums);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(p_full + 8 * (2 * half + h));
                     }
-                    // the largest score, and the largest with its page's bound
-                    float top = -INFINITY, over = -INFINITY;
-                    uint32_t sc[2][16];              // (16 scores on the way while those before are looked at)
-                    tmem_ld_32x32b_x16(s_at, sc[0]);
-#pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32)
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            tmem_ld_wait();
-                            if (g == 0) tmem_ld_32x32b_x16(s_at + c + 16, sc[1]);
-                            else if (c + 32 < kTile) tmem_ld_32x32b_x16(s_at + c + 32, sc[0]);
-                            if (edge) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const int t = tok + c + 16 * g + e;
-                                    if (t > last || t <= from) sc[g][e] = 0xFF800000u;
-                                }
-                            }
-                            float x[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[e] = fmaxf(fmaxf(__uint_as_float(sc[g][e]), __uint_as_float(sc[g][4 + e])),
-                                             fmaxf(__uint_as_float(sc[g][8 + e]), __uint_as_float(sc[g][12 + e])));
-                            float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                            // (what no row sees has scale 0)
-                            if (y > -INFINITY) {
-                                y *= factor * ks[c / 16 + g];
-                                top = fmaxf(top, y);
-                                over = fmaxf(over, y + (float)scale_bound(vs[c / 16 + g]));
-                            }
-                        }
-                    if (top > m) {
-                        l *= exp2_of(m - top);
-                        m = top;
-                    }
-                    // o's reference: p s_v is 2^8 (16-bit rows: 2^4) at its largest (scale_bound is 14 below), and the
-                    // reference moves where it would pass 2^14
-                    const bool move = over > ref;
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
-                        if (!first) {
-                            // (O is whole once the group's unit before is)
-                            ok = mbar_wait(o_done + 8 * half, s_phase(i, half, j0, second) ^ 1, p.err, kDevErrTimeout);
-                            if (!__all_sync(0xffffffffu, ok)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const float f = move ? exp2_of(ref - now) : 1.0f;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 8) {
-                                uint32_t o[8];
-                                tmem_ld_32x32b_x8(o_at + c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st_32x32b_x8(o_at + c, o);
-                            }
-                            tmem_st_wait();
-                        }
-                        ref = now;
-                    }
-                    first = false;
-                    const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
-                    uint64_t sums = 0;
-                    tmem_ld_32x32b_x16(s_at, sc[0]);
-#pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
-                        uint32_t w[16], rest[16];
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            tmem_ld_wait();
-                            if (g == 0) tmem_ld_32x32b_x16(s_at + c + 16, sc[1]);
-                            else if (c + 32 < kTile) tmem_ld_32x32b_x16(s_at + c + 32, sc[0]);
-                            const uint64_t k2 = two(factor * ks[c / 16 + g]), m2 = two(-m0), f2 = two(vs[c / 16 + g] * up);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const uint64_t x = fma_f32x2(pack_f32x2(sc[g][e], sc[g][e + 1]), k2, m2);
-                                float p0 = exp2_of(lo_of(x)), p1 = exp2_of(hi_of(x));
-                                if (edge) {
-                                    const int t0 = tok + c + 16 * g + e;
-                                    if (t0 > last || t0 <= from) p0 = 0.0f;
-                                    if (t0 + 1 > last || t0 + 1 <= from) p1 = 0.0f;
-                                }
-                                const uint64_t pp = pack_f32x2(__float_as_uint(p0), __float_as_uint(p1));
-                                sums = add_f32x2(sums, pp);
-                                const uint64_t ww = mul_f32x2(pp, f2);
-                                float w0 = lo_of(ww), w1 = hi_of(ww);
-                                if (edge) {          // (a page that is not there has no scale)
-                                    if (p0 == 0.0f) w0 = 0.0f;
-                                    if (p1 == 0.0f) w1 = 0.0f;
-                                }
-                                w[8 * g + e / 2] = half2_bits(w0, w1);
-                                if constexpr (TWO) rest[8 * g + e / 2] = half2_rest(w0, w1, w[8 * g + e / 2]);
-                            }
-                        }
-                        // over the scores just read
-                        tmem_st_x16(s_at + c, w);
-                        if constexpr (TWO) tmem_st_x16(s_at + c + 16, rest);
-                    }
-                    l += lo_of(sums) + hi_of(sums);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive(p_full + 8 * half);
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 more = goes_on(work);
