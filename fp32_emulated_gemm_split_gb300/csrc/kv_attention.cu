@@ -769,11 +769,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_c
     };
     RowSum s;
     if (parts <= 16) {
-        const int r = blockIdx.y * kJoinWarps + warp;
-        if (r >= w.rows) return;
-        add_row(s, r, 0, 1);
-        if (d0 < D) write_row<T>(p, w, r, d0, s.m, s.l, s.ref, s.v[0]);
-        if (128 + d0 < D) write_row<T>(p, w, r, 128 + d0, s.m, s.l, s.ref, s.v[1]);
+        for (int r = blockIdx.y * kJoinWarps + warp; r < w.rows; r += gridDim.y * kJoinWarps) {
+            add_row(s, r, 0, 1);
+            if (d0 < D) write_row<T>(p, w, r, d0, s.m, s.l, s.ref, s.v[0]);
+            if (128 + d0 < D) write_row<T>(p, w, r, 128 + d0, s.m, s.l, s.ref, s.v[1]);
+        }
         return;
     }
     for (int r = blockIdx.y; r < w.rows; r += gridDim.y) {
@@ -845,7 +845,10 @@ cudaError_t launch_decode(AttnParams p, const emu_kv_cache_t& c, int64_t max_row
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int dtype = sizeof(T) == 4 ? EMU_F32 : std::is_same<T, __half>::value ? EMU_F16 : EMU_BF16;
-    return launch_join(dtype, p, ctas, max_rows < ROWS ? (unsigned)max_rows : ROWS, stream);
+    // Blocks for a segment's rows: eight rows each, or one where so few segments share the CTAs that they have many parts.
+    const unsigned rows = max_rows < ROWS ? (unsigned)max_rows : ROWS;
+    const bool many = (int64_t)p.heads * (p.B < p.T ? p.B : p.T) * 4 < ctas;
+    return launch_join(dtype, p, ctas, many ? rows : (rows + 7) / 8, stream);
 }
 
 template <typename T, int NR>

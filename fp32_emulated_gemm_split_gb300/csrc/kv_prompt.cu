@@ -1064,7 +1064,7 @@ cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
     p.slot_rows = Pl::rows;
     kern<<<(unsigned)sms, kThreads, Pl::bytes, stream>>>(p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, Pl::rows / 8, stream);
+    return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, Pl::rows / 16, stream);
 }
 
 template <typename T, int NG>

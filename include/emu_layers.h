@@ -263,7 +263,7 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  *  starts        B + 1 values, ascending: sequence b has the rows starts[b] ..
  *                starts[b+1] - 1 (none are fine); rows from starts[B] on become zero
  *  lengths       B values
- *  window        0: all tokens before
+ *  window        0, or 2^30 and more: all tokens before
  *  max_new       rows that a sequence has at most, or 0 where the caller does not
  *                know.  It chooses kernels (whose sums are rounded differently), not
  *                what is computed: too small a value is slow, not wrong.
