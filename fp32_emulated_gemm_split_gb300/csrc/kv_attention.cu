@@ -44,7 +44,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKvCtasPerSm = 4;                      // at most
 // Rows of a sequence (16-bit types, heads up to 128) up to which this file's kernel runs, in segments of 16 that
-// each read the cache, all but the first from L2: 24 sequences of 3 to 7 tokens, 8 heads of 128 a key head, 80 us,
+// each read the cache, all but the first from L2: 24 sequences of 3 to 7 tokens, 8 heads of 128 a key head, 75 us,
 // in kv_prompt.cu 106, and in segments of 32 (queries in shared memory, steps of 16 tokens for their registers) 102.
 constexpr int kFewKvRows = 64;
 

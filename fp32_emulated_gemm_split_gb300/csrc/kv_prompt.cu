@@ -18,7 +18,7 @@
 // way while the outputs of the last are written.
 //
 // Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
-// 128, BF16 (412 GFLOP), 594 us, 693 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
+// 128, BF16 (412 GFLOP), 591 us, 697 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
 // MMAs 2560 (scores of 64 tokens are bound by reading Q again: 512 of them), a group's weights
 // 2500; codes, MMAs and weights wait for one another.  A segment costs 17,000 cycles
 // besides: Q, units that some row does not see, outputs.  Barriers that let the groups compute by
@@ -27,7 +27,7 @@
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
 // taken in a pass of its own over S (0.5 operations a value); O's reference moves
 // only where p s_v would pass 2^14, so O is rarely scaled.  (1200 to 2500 tokens, window
-// 1000, 12 heads over 4 of 96: 105 us.)
+// 1000, 12 heads over 4 of 96: 107 us.)
 #include "kv_attention.cuh"
 
 namespace emu {

@@ -325,3 +325,48 @@ def test_stream_and_graph(emu):
     torch.cuda.synchronize()
     other, bound = ref.attention(q, *cache, table, starts, [290, 33], 128 ** -0.5)
     assert ref.within(out, other, bound)
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("most,window", [(100, 0), (30, 0), (30, 70)])
+def test_many_short_segments(emu, type, most, window):
+    """Hundreds of sequences of a tile or two, most of one unit: a CTA goes through many
+    segments, of which many have no second tile."""
+    kept = [(37 * b) % 90 if b % 9 else (211 * b) % 700 for b in range(400)]
+    new = [1 + (53 * b) % most for b in range(400)]
+    _check(emu, _make(kept, new, 8, 2, 64, 16, type), window=window, max_new=100)
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_one_segment_over_all(emu, type):
+    """A few tiles with hundreds of units, and one with fewer than CTAs."""
+    _check(emu, _make([40000, 300], [40, 50], 4, 1, 128, 64, type))
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("n", [1, 200])
+def test_queries_that_are_not_finite(emu, type, n):
+    """They change their own rows only."""
+    import torch
+    q, cache, table, starts, lengths = _make([300, 40], [n, n], 4, 2, 64, 16, type)
+    want, bound = ref.attention(q, *cache, table, starts, lengths, 0.125, 0)
+    at = {(0, 1): math.nan, (n, 0): math.inf, (2 * n - 1, 3): -math.inf}
+    others = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    for (row, head), value in at.items():
+        q[row, head, 5] = value
+        others[row, head] = False
+    out = emu.emu_kv_attention(q, cache, table, _ints(starts), _ints(lengths), scale=0.125, max_new=n)
+    assert torch.isnan(out[0, 1]).all()
+    assert ref.within(out[others], want[others], bound[others])
+    assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("n", [2, 150])
+def test_expanded_queries(emu, type, n):
+    """One head's queries for all heads, one token's for all tokens."""
+    import torch
+    q, cache, table, starts, lengths = _make([70, 20], [n, n], 4, 2, 128, 32, type)
+    for wide in (q[:, :1].expand(-1, 4, -1), q[:1].expand(2 * n, -1, -1)):
+        got = emu.emu_kv_attention(wide, cache, table, _ints(starts), _ints(lengths))
+        assert torch.equal(got, emu.emu_kv_attention(wide.contiguous(), cache, table, _ints(starts), _ints(lengths)))
