@@ -1,6 +1,6 @@
 /*
- * emu_layers.h -- C ABI of libemusgemm: what a transformer block computes
- * beside its attention, on one GB300 GPU (sm_103a).
+ * emu_layers.h -- C ABI of libemusgemm: what a transformer block computes,
+ * on one GB300 GPU (sm_103a).
  *
  *   emu_gated, emu_gated_bwd         gated feed-forward, forward and backward
  *   emu_lora                         a projection with the low-rank adapters
@@ -11,10 +11,10 @@
  *   emu_kv_attention                 which ones a batch's requests get, the
  *                                    store into them and the attention over them
  *
- * The matrix products are emu_sgemm's BF16X9 (emu_sgemm.h): FP32 in and out,
- * at FP32 accuracy.  The conventions of emu_sgemm.h hold: row-major storage,
- * device pointers owned by the caller, work enqueued asynchronously on
- * `stream`, arguments checked on the host before anything is launched,
+ * The matrix products (but emu_kv_attention's, see there) are emu_sgemm's BF16X9
+ * (emu_sgemm.h): FP32 in and out, at FP32 accuracy.  The conventions of
+ * emu_sgemm.h hold: row-major storage, device pointers owned by the caller,
+ * work enqueued asynchronously on `stream`, arguments checked on the host before anything is launched,
  * status codes, the library's workspace (calls on one device share it and
  * must be serialised; a call can be captured in a CUDA graph once a call of
  * the same shape has run outside capture).  Values on the device that have
