@@ -176,8 +176,9 @@ struct Segment {
         uint32_t pb[PIECES][SUB][NR][2];         // P^T: rows of tokens, turned
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            float m0[2], f[SUB][2], fs[SUB][2];
+            float m0[2], f[SUB][2], fs[SUB][2], back[2] = {1.0f, 1.0f};
             uint32_t hidden = 0;
+            bool far = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float m[SUB];
@@ -224,8 +225,20 @@ struct Segment {
                 ref[r][e] = ref_now;
                 m0[e] = top_now == -INFINITY ? 0.0f : top_now;
 #pragma unroll
-                for (int u = 0; u < SUB; ++u)
+                for (int u = 0; u < SUB; ++u) {
                     f[u][e] = top_now == -INFINITY ? 0.0f : v_scale[u] * exp2_of(top_now - ref_now);
+                    far = far || f[u][e] > kFarScale;
+                }
+            }
+            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (top[r][e] > ref[r][e]) {
+                        m0[e] = ref[r][e];
+                        back[e] = exp2_of(ref[r][e] - top[r][e]);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) f[u][e] = v_scale[u];
+                    }
             }
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
@@ -238,7 +251,7 @@ struct Segment {
                         float x = exp2_of(fmaf(sc[u][r][e + 2 * h], fs[u][e], -m0[e]));
                         w2[e] = x * f[u][e];
                         if (EDGE && (hidden >> (4 * u + 2 * h + e) & 1)) x = w2[e] = 0.0f;
-                        total[r][e] += x;
+                        total[r][e] = fmaf(x, back[e], total[r][e]);
                     }
                     const uint32_t hi = half2_bits(w2[0], w2[1]);
                     pb[0][u][r][h] = turned(hi);

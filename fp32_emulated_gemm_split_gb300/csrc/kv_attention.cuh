@@ -68,11 +68,17 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
 }
 
-// A bound of log2 of a page's value scale less 14 (its exponent and one, less 14), and no less than -125, so that
-// 2^(the other way) is finite: what o is held against lies this far from the scores' maximum.
+// A bound of log2 of a page's value scale less 14 (its exponent and one, less 14), and no less than -120, so that
+// 2^(the other way) is finite, and so is the sum of 128 of them: what o is held against lies this far from the
+// scores' maximum.
 __device__ __forceinline__ int scale_bound(float v_scale) {
-    return max((int)((__float_as_uint(v_scale) >> 23) & 0xFF) - 126 - 14, -125);
+    return max((int)((__float_as_uint(v_scale) >> 23) & 0xFF) - 126 - 14, -120);
 }
+
+// A weight p s_v against o's reference is x f, x = 2^(score - m), f = s_v 2^(m - ref).  It is 2^14 at most, but where the
+// row's largest scores are those of pages of a tiny scale (of zeros: 2^-126), m lies up to 120 over ref, and the f of
+// another page is infinite.  From here on x is 2^(score - ref), f s_v, and sums of x count 2^(ref - m) of themselves.
+constexpr float kFarScale = 1e37f;
 
 // A CTA's way through the units, and the segment that it is at (in shared memory: both are
 // looked at between segments only).

@@ -863,12 +863,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                 uint64_t sums = 0;
                                 const uint64_t m2 = two(-m);
                                 const float up = exp2_of(m - ref);
+                                float f_most = 0.0f;
                                 tmem_ld_32x32b_x16(s_part, sc[0]);
 #pragma unroll
                                 for (int g = 0; g < kPart / 16; ++g) {
                                     tmem_ld_wait();
                                     if (g + 1 < kPart / 16) tmem_ld_32x32b_x16(s_part + 16 * (g + 1), sc[(g + 1) & 1]);
-                                    const uint64_t k2 = two(factor * ks[g]), f2 = two(vs[g] * up);
+                                    const float f = vs[g] * up;
+                                    const uint64_t k2 = two(factor * ks[g]), f2 = two(f);
+                                    f_most = fmaxf(f_most, f);
 #pragma unroll
                                     for (int e = 0; e < 16; e += 2) {
                                         const uint64_t x = fma_f32x2(pack_f32x2(sc[g & 1][e], sc[g & 1][e + 1]), k2, m2);
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                                 }
                                 const float more = lo_of(sums) + hi_of(sums);
                                 const bool fits = !__hisinf(__low2half(most)) && !__hisinf(__high2half(most)) && !(more > 1e37f) &&
-                                                  m > -INFINITY;
+                                                  f_most < kFarScale && m > -INFINITY;
                                 if (__all_sync(0xffffffffu, fits)) {
                                     l += more;
 #pragma unroll
@@ -958,7 +961,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             ref = now;
                         }
                         first = false;
-                        const float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref);
+                        float m0 = m == -INFINITY ? 0.0f : m, up = m == -INFINITY ? 0.0f : exp2_of(m - ref), back = 1.0f;
+                        {
+                            float most = 0.0f;
+#pragma unroll
+                            for (int c = 0; c < kPart / 16; ++c) most = fmaxf(most, vs[c]);
+                            if (most * up > kFarScale && m > ref) {
+                                m0 = ref;
+                                up = 1.0f;
+                                back = exp2_of(ref - m);
+                            }
+                        }
                         uint64_t sums = 0;
                         tmem_ld_32x32b_x16(s_part, sc[0]);
 #pragma unroll 1
@@ -995,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             tmem_st_x16(s_part + c, w);
                             if constexpr (TWO) tmem_st_x16(s_part + c + 16, rest);
                         }
-                        l += lo_of(sums) + hi_of(sums);
+                        l = fmaf(lo_of(sums) + hi_of(sums), back, l);
                         tmem_st_wait();
                         tc_fence_before();
                         mbar_arrive(p_full + 8 * (2 * half + h));
