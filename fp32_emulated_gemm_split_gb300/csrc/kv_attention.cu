@@ -932,7 +932,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
     const size_t few = 2 * ctas * 16 * (256 + 4) * sizeof(float), many = 2 * (size_t)d->sms * kKvSlotRows * (128 + 4) * sizeof(float);
     const size_t slots = few > many ? few : many;
-    if (!d->kv_ws && cudaMalloc(&d->kv_ws, slots + ctas * sizeof(Work)) != cudaSuccess) {
+    const size_t moved = 2 * (size_t)d->sms * 128 * 128 * sizeof(float);
+    if (!d->kv_ws && cudaMalloc(&d->kv_ws, slots + moved + ctas * sizeof(Work)) != cudaSuccess) {
         cudaGetLastError();
         d->kv_ws = nullptr;
         return EMU_ERR_ALLOC;
@@ -952,7 +953,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     p.wide = reinterpret_cast<uintptr_t>(p.q) % 16 == 0 && p.q_t * size % 16 == 0 && p.q_h * size % 16 == 0;
     p.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.out_t * size % 16 == 0 && p.out_h * size % 16 == 0;
     p.partial = static_cast<float*>(d->kv_ws);
-    p.shared = reinterpret_cast<Work*>(static_cast<uint8_t*>(d->kv_ws) + slots);
+    p.moved = reinterpret_cast<float4*>(static_cast<uint8_t*>(d->kv_ws) + slots);
+    p.shared = reinterpret_cast<Work*>(static_cast<uint8_t*>(d->kv_ws) + slots + moved);
     p.err = d->err;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t max_rows = (max_new > 0 && max_new < T ? max_new : T) * p.group;

@@ -167,6 +167,12 @@ struct Plan {
     // Parts of a unit whose scores and weights go by themselves: the scores of one are under way while the group looks at
     // the other's.  (16-bit pairs: 664 us, 630 in two; FP32 in two 123 us for 105)
     static constexpr int parts = PAIR ? 2 : 1;
+    // Units of a group that are added up in tensor memory, a power of two.  An MMA rounds toward zero, 2^-25 of the sum lost on
+    // the average as it grows, and a unit is 8 of them, 16 with two pieces: behind so many units O is added to a sum in
+    // memory, to the nearest, where sequences are that long (LONG).  Values of one sign, 400,000 tokens: FP32 9e-7 off (1e-3
+    // with one sum), FP16 3e-5 besides its roundings (2e-3; 6e-5 with 128 units).  Three FP32 prompts of 2000 behind 3000,
+    // 16 heads over 4 of 128: 604 us, 550 with one sum.
+    static constexpr uint32_t chain = TWO ? 4 : 64;
     static constexpr int piece = kHalf * NG * 64;                // bytes of a piece of codes
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
     static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
@@ -181,7 +187,7 @@ __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32
 
 // ------------------------------------------------------------- kernel --
 
-template <typename T, int NG, bool PAIR>
+template <typename T, int NG, bool PAIR, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ AttnParams p) {
     constexpr bool TWO = sizeof(T) == 4;
     constexpr int PIECES = TWO ? 2 : 1;
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
     __shared__ uint32_t present[SLOTS];              // of a piece's tiles of 16 tokens: those that were copied
     __shared__ float q_factor[2][kTile];
     __shared__ float row_stat[2][kTile][3];          // maximum, sum, reference of each group
+    __shared__ float ref_moved[2][kTile];            // what its sums in memory are held against
     const uint32_t k_full = smem_u32(bars), k_free = k_full + 16, v_full = k_full + 32, v_free = k_full + 48,
                    s_full = k_full + 64, p_full = k_full + 96, o_done = k_full + 128,      // [group][part]
                    q_full = k_full + 160, drained = k_full + 176, c_full = k_full + 184, seg_full = k_full + 248,
@@ -463,12 +470,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 }
                 for (uint32_t i = from; i < j1 && ok; i += by) {
                     const uint32_t next = i + by, phase = s_phase(i, t, j0, second);
+                    const bool go_on = LONG ? (i - from) / by % Pl::chain != 0 : i > from;
                     if (!wait(v_full + 8 * (i % VS), v_phase(i))) break;
 #pragma unroll
                     for (int h = 0; h < PARTS; ++h) {
                         if (!idle) {
                             if (!wait(p_full + 8 * (2 * t + h), phase)) break;
-                            products(i, h, h > 0 || i > from);
+                            products(i, h, h > 0 || go_on);
                         }
                         if (h == PARTS - 1) tc_commit(v_free + 8 * (i % VS), leader);
                         if (next < j1) {
@@ -659,6 +667,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
             const int half = warp >> 2, r = tid & (kTile - 1);           // group, row of its tile
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t s_at = (tmem + half * kTile) | lanes, o_at = (tmem + (2 + half) * kTile) | lanes;
+            // O and x times the sums in memory, added up there or, at the end, in O.
+            auto move_sums = [&](bool start, bool end, float x) {
+                float4* const sums = p.moved + (size_t)(blockIdx.x * 2 + half) * (D >> 2) * kTile + r;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    float4 old[4];
+                    tmem_ld_32x32b_x16(o_at + c, o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) old[e] = start ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : sums[(c / 4 + e) * kTile];
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float4 y = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                               __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                        add_to(y, x, old[e]);
+                        if (!end) sums[(c / 4 + e) * kTile] = y;
+                        o[4 * e] = __float_as_uint(y.x);
+                        o[4 * e + 1] = __float_as_uint(y.y);
+                        o[4 * e + 2] = __float_as_uint(y.z);
+                        o[4 * e + 3] = __float_as_uint(y.w);
+                    }
+                    if (end) tmem_st_x16(o_at + c, o);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+            };
             float m = -INFINITY, l = 0.0f, ref = -INFINITY;
             bool more = true;                        // segment seg follows; segment seg - 1 waits for its last products
             for (;;) {
@@ -836,9 +871,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                 const float factor = q_factor[PAIR ? half : 0][r];
                 m = ref = -INFINITY;
                 l = 0.0f;
-                bool first = true;
-                for (uint32_t i = PAIR ? (idle ? j1 : j0) : j0 + ((j0 ^ half) & 1); i < j1 && ok; i += PAIR ? 1 : 2) {
-                    const uint32_t phase = s_phase(i, half, j0, second);
+                bool first = true;                       // O's sum is about to begin
+                const uint32_t by = PAIR ? 1 : 2, i0 = PAIR ? (idle ? j1 : j0) : j0 + ((j0 ^ half) & 1);
+                for (uint32_t i = i0; ok; i += by) {
+                    const uint32_t phase = s_phase(i, half, j0, second), at = (i - i0) / by;
+                    if (LONG && at >= Pl::chain && (at % Pl::chain == 0 || i >= j1)) {
+                        ok = mbar_wait(o_done + 8 * (2 * half + PARTS - 1), phase ^ 1, p.err, kDevErrTimeout) && !*aborted;
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const bool start = at == Pl::chain;
+                        if (i < j1 || !start) move_sums(start, i >= j1, start ? 0.0f : share_of(ref_moved[half][r], ref));
+                        ref_moved[half][r] = ref;
+                        first = true;
+                    }
+                    if (i >= j1) break;
 #pragma unroll 1
                     for (int h = 0; h < PARTS; ++h) {
                         ok = mbar_wait(s_full + 8 * (2 * half + h), phase, p.err, kDevErrTimeout) &&
@@ -1056,10 +1105,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512u));
 }
 
-template <typename T, int NG, bool PAIR>
+template <typename T, int NG, bool PAIR, bool LONG>
 cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
     using Pl = Plan<T, NG, PAIR>;
-    auto kern = kv_prompt_kernel<T, NG, PAIR>;
+    auto kern = kv_prompt_kernel<T, NG, PAIR, LONG>;
     static bool done[kMaxDevices] = {};              // (g_mu is held)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1080,11 +1129,23 @@ cudaError_t launch(AttnParams p, int dtype, int sms, cudaStream_t stream) {
     return e != cudaSuccess ? e : launch_join(dtype, p, (unsigned)sms, Pl::rows / 16, stream);
 }
 
+// Whether a group may have more units of a segment than one sum takes: by what a table's row holds, or a window and the
+// tokens of a segment.  (Without the moves' code 16-bit prompts take 605 us for 630: registers of the units' loop.)
+template <typename Pl>
+bool is_long(const AttnParams& p) {
+    const int64_t kept = (int64_t)p.width << p.page_log, seen = p.window ? (int64_t)p.window + Pl::rows / p.group + 1 : kept;
+    return (kept < seen ? kept : seen) > (int64_t)Pl::chain * kTile;
+}
+
 template <typename T, int NG>
 cudaError_t launch_rows(const AttnParams& p, int dtype, int64_t max_rows, int sms, cudaStream_t stream) {
-    if constexpr (sizeof(T) == 2)
-        if (max_rows > kTile) return launch<T, NG, true>(p, dtype, sms, stream);
-    return launch<T, NG, false>(p, dtype, sms, stream);
+    if constexpr (sizeof(T) == 2) {
+        if (max_rows > kTile)
+            return is_long<Plan<T, NG, true>>(p) ? launch<T, NG, true, true>(p, dtype, sms, stream)
+                                                 : launch<T, NG, true, false>(p, dtype, sms, stream);
+        if (!is_long<Plan<T, NG, false>>(p)) return launch<T, NG, false, false>(p, dtype, sms, stream);
+    }
+    return launch<T, NG, false, true>(p, dtype, sms, stream);
 }
 
 template <typename T>

@@ -9,7 +9,7 @@ import pytest
 import kv_norms as norms
 import kv_ref as ref
 from gpu_util import emu_module
-from test_gpu_kv_attention import TYPES, _error, _ints, _make
+from test_gpu_kv_attention import TYPES, _check, _error, _ints, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,44 @@ def test_zero_values_with_the_largest_scores(emu, type, n, zero_first):
             assert not torch.isnan(out).any(), (scale, gap)
             assert ref.within(out, want, bound + (norms.flushed(made) if gap > 83 else 0.0)), (scale, gap)
     assert _error(emu) == 0
+
+
+# Sums of one sign, segments that one CTA goes through alone.  The products' accumulators round toward zero, half a step (2^-24) of
+# the sum on the average: what an FP32 sum may lose is bounded by its parts of 64 such additions (32 steps, 2^-25 each on the average as
+# it grows), 2e-6 with the rest; in 16 bits by half a step of the type's 11 bits.
+@pytest.mark.parametrize("n,B,most", [(128, 40, 128), (4, 120, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [1000, 8000, 40000])
+def test_long_sums_of_one_sign(emu, n, B, most, D, L):
+    import torch
+    made = norms.one_sign(torch.float32, n, B, L, D, 4)
+    out = _attend(emu, made, max_new=most)
+    rows = [0, n * (B // 2) + n // 2, n * B - 1]
+    assert norms.relative(out[rows], norms.rows_exactly(made, rows)) <= 3e-6
+    assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("n,B,L", [(128, 40, 200000), (300, 20, 200000)])
+def test_long_sums_in_16_bits(emu, n, B, L):
+    """The mean error stays below a quarter of FP16's half step: roundings of weights and outputs average out, what sums
+    lose does not."""
+    import torch
+    made = norms.one_sign(torch.float16, n, B, L, 64, 4)
+    out = _attend(emu, made, max_new=n)
+    rows = [n * b + (n // 12 * b) % n for b in range(0, B, max(1, B // 12))]
+    want = norms.rows_exactly(made, rows)
+    assert abs(float((out[rows].double() / want - 1).mean())) <= 2.0 ** -14
+    assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("D", [16, 48, 96, 128])
+@pytest.mark.parametrize("n,window", [(100, 0), (300, 0), (300, 12000), (129, 5000)])
+def test_sums_in_parts(emu, type, D, n, window):
+    """Segments whose outputs are added up in several parts, with a NaN that some rows see."""
+    import torch
+    q, cache, table, starts, lengths = _make([20000, 5], [n, n], 2, 2, D, 32, type, seed=D)
+    v = cache[1].float()
+    at = lengths[0] - n // 2
+    v[int(table[0, at // 32]), 1, at % 32, 3] = math.nan
+    _check(emu, (q, (cache[0], v.to(ref.F8), *cache[2:]), table, starts, lengths), window=window)
