@@ -48,6 +48,11 @@ constexpr int kKvCtasPerSm = 4;                      // at most
 // in kv_prompt.cu 106, and in segments of 32 (queries in shared memory, steps of 16 tokens for their registers) 102.
 constexpr int kFewKvRows = 64;
 
+// Steps that a warp adds up in an MMA's sums, 16-bit rows: each MMA rounds toward zero, some 2^-24 of the sum lost as it grows.
+// Behind so many the sum goes to one in memory, to the nearest.  (FP32 rows add each step's sums to the nearest.)
+constexpr int kChain = 256;
+constexpr int kMovedQuads = 33;                      // of a lane: o of 16 rows of 256, and its rows' references
+
 // Steps start on multiples of ST tokens; the first one that any row of the sequence sees.
 template <int ST>
 __device__ __forceinline__ int first_token(const AttnParams& p, const Seq& s) {
@@ -123,6 +128,40 @@ struct Segment {
     float top[NR][2], ref[NR][2], total[NR][2];      // running maxima of the scores, what o is held against, sums of p
     uint32_t k_at[NG][2], v_at[Bl::count][4];        // where a lane's codes lie in a stage
     int d_rt, len, window, side;
+
+    // Adds o to this lane's sums in memory (`first`: begins them) and starts anew, or, at the end, the sums to o.
+    __device__ __forceinline__ void move_sums(float4* sums, bool first, bool end) {
+        float4* const held = sums + (kMovedQuads - 1) * 32;      // references
+        float x[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[r][e] = 0.0f;
+        if (!first) {
+            const float4 h = *held;
+            x[0][0] = share_of(h.x, ref[0][0]);
+            x[0][1] = share_of(h.y, ref[0][1]);
+            x[NR - 1][0] = NR > 1 ? share_of(h.z, ref[NR - 1][0]) : x[0][0];
+            x[NR - 1][1] = NR > 1 ? share_of(h.w, ref[NR - 1][1]) : x[0][1];
+        }
+#pragma unroll
+        for (int n = 0; n < Bl::count * 8; ++n)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float4* const at = sums + (n * NR + r) * 32;
+                const float4 old = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
+                float (&y)[4] = o[n][r];
+                y[0] = fmaf(old.x, x[r][0], y[0]);
+                y[1] = fmaf(old.y, x[r][1], y[1]);
+                y[2] = fmaf(old.z, x[r][0], y[2]);
+                y[3] = fmaf(old.w, x[r][1], y[3]);
+                if (!end) {
+                    *at = make_float4(y[0], y[1], y[2], y[3]);
+                    y[0] = y[1] = y[2] = y[3] = 0.0f;
+                }
+            }
+        if (!end) *held = make_float4(ref[0][0], ref[0][1], ref[NR - 1][0], ref[NR - 1][1]);
+    }
 
     // EDGE: some row does not see some token of the step.
     template <bool EDGE>
@@ -591,8 +630,10 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
 #pragma unroll
             for (int k = 0; k < 4; ++k) sg.v_at[bl][k] = swizzled((t + 4 * k) * D + Bl::first(bl, g)) + p.side;
 
+        float4* const sums = p.moved + (size_t)(blockIdx.x * kWarps + warp) * (kMovedQuads * 32) + lane;
         for (int i = 0; i < steps; ++i) {
             const int in_batch = i % BATCH;
+            if (!TWO && i % kChain == 0 && i > 0) sg.move_sums(sums, i == kChain, false);
             if (in_batch == 0 && i > 0) {
                 page_now = page_next;
                 ks_now = ks_next;
@@ -629,6 +670,7 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
             else
                 sg.template step<false>(tok, kt, k_scale, v_scale);
         }
+        if (!TWO && steps > kChain) sg.move_sums(sums, false, true);
 #pragma unroll
         for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -932,7 +974,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
     const size_t ctas = (size_t)d->sms * kKvCtasPerSm;
     const size_t few = 2 * ctas * 16 * (256 + 4) * sizeof(float), many = 2 * (size_t)d->sms * kKvSlotRows * (128 + 4) * sizeof(float);
     const size_t slots = few > many ? few : many;
-    const size_t moved = 2 * (size_t)d->sms * 128 * 128 * sizeof(float);
+    const size_t moved = ctas * kWarps * kMovedQuads * 32 * sizeof(float4);      // (kv_prompt.cu: 2 SMs 128 x 128 values, fewer)
+    static_assert(kKvCtasPerSm * kWarps * kMovedQuads * 32 * sizeof(float4) >= 2 * 128 * 128 * sizeof(float), "sums of both kernels");
     if (!d->kv_ws && cudaMalloc(&d->kv_ws, slots + moved + ctas * sizeof(Work)) != cudaSuccess) {
         cudaGetLastError();
         d->kv_ws = nullptr;

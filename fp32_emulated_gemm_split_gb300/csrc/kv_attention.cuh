@@ -27,7 +27,7 @@ struct AttnParams {
     int depth, side;                                 // stages of a warp's ring, bytes of a stage's keys (or values)
     int copy_tokens;                                 // tokens of one tensor copy
     float* partial;                                  // [2 ctas][slot_rows][D + 4]
-    float4* moved;                                   // kv_prompt.cu: [SMs][2 groups][D / 4][128 rows]
+    float4* moved;                                   // sums of o in memory, kv_prompt.cu: [SMs][2 groups][D / 4][128 rows]
     int slot_rows;
     Work* shared;                             // [ctas]: the segment that a CTA begins and others end (or units 0)
     int* err;

@@ -63,7 +63,7 @@ def test_long_sums_of_one_sign(emu, n, B, most, D, L):
     assert _error(emu) == 0
 
 
-@pytest.mark.parametrize("n,B,L", [(128, 40, 200000), (300, 20, 200000)])
+@pytest.mark.parametrize("n,B,L", [(128, 40, 200000), (300, 20, 200000), (4, 120, 400000)])
 def test_long_sums_in_16_bits(emu, n, B, L):
     """The mean error stays below a quarter of FP16's half step: roundings of weights and outputs average out, what sums
     lose does not."""
@@ -74,6 +74,19 @@ def test_long_sums_in_16_bits(emu, n, B, L):
     want = norms.rows_exactly(made, rows)
     assert abs(float((out[rows].double() / want - 1).mean())) <= 2.0 ** -14
     assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type,most", [("bf16", 2.0 ** -8), ("f16", 2.0 ** -11)])
+@pytest.mark.parametrize("D", [48, 64, 128, 192, 256])
+@pytest.mark.parametrize("n,B", [(2, 160), (12, 120)])
+def test_sums_in_parts_of_few_rows(emu, type, most, D, n, B):
+    """Next tokens and drafts whose warps have hundreds of steps each."""
+    import torch
+    made = norms.one_sign(_type(type), n, B, 70000, D, 4)
+    out = _attend(emu, made, max_new=n)
+    rows = [0, n * (B // 3) + n - 1, n * B - 1]
+    assert norms.relative(out[rows], norms.rows_exactly(made, rows)) <= most
+    assert torch.isfinite(out).all() and _error(emu) == 0
 
 
 @pytest.mark.parametrize("type", TYPES)
