@@ -18,16 +18,15 @@
 // way while the outputs of the last are written.
 //
 // Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
-// 128, BF16 (412 GFLOP), 591 us, 697 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
+// 128, BF16 (412 GFLOP), 592 us, 696 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
 // MMAs 2560 (scores of 64 tokens are bound by reading Q again: 512 of them), a group's weights
 // 2500; codes, MMAs and weights wait for one another.  A segment costs 17,000 cycles
 // besides: Q, units that some row does not see, outputs.  Barriers that let the groups compute by
 // turns: 831 us for 709 before.
 //
 // FP32 rows: two pieces of Q and of P, twice the MMAs.  The scores' maximum is
-// taken in a pass of its own over S (0.5 operations a value); O's reference moves
-// only where p s_v would pass 2^14, so O is rarely scaled.  (1200 to 2500 tokens, window
-// 1000, 12 heads over 4 of 96: 107 us.)
+// taken in a pass of its own over S (0.5 operations a value).  (1200 to 2500 tokens,
+// window 1000, 12 heads over 4 of 96: 110 us.)
 #include "kv_attention.cuh"
 
 namespace emu {
@@ -982,11 +981,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             l *= exp2_of(m - top);
                             m = top;
                         }
-                        // o's reference: p s_v is 2^8 (16-bit rows: 2^4) at its largest (scale_bound is 14 below), and the
-                        // reference moves where it would pass 2^14
+                        // o's reference: p s_v is 2^13 to 2^14 at its largest (scale_bound is 14 below), so that its two pieces end at
+                        // 2^-38 of it.  16-bit rows: 2^7 to 2^8 at first, and the reference moves where it would pass 2^14; O is
+                        // rescaled less often (three prompts of 2000: 594 us; 617 with 2^9 at first, 604 with 2^3).
                         const bool move = over > ref;
                         if (__any_sync(0xffffffffu, move)) {
-                            const float now = move ? over + (TWO ? 6.0f : 10.0f) : ref;
+                            const float now = move ? over + (TWO ? 0.0f : 6.0f) : ref;
                             if (!first) {
                                 // (O is whole once the products of the group's part before are)
                                 ok = mbar_wait(o_done + 8 * (2 * half + (h ^ (PARTS - 1))), phase ^ (h == 0), p.err, kDevErrTimeout);

@@ -100,3 +100,27 @@ def test_sums_in_parts(emu, type, D, n, window):
     at = lengths[0] - n // 2
     v[int(table[0, at // 32]), 1, at % 32, 3] = math.nan
     _check(emu, (q, (cache[0], v.to(ref.F8), *cache[2:]), table, starts, lengths), window=window)
+
+
+@pytest.mark.parametrize("type,own,large", [("f32", norms.TWO_PIECES, 2.0 ** -38), ("bf16", 2.0 ** -8, 2.0 ** -32), ("f16", 2.0 ** -11, 2.0 ** -32)])
+@pytest.mark.parametrize("gap", [0, 7, 11, 14, 18])
+@pytest.mark.parametrize("n", [1, 140])
+def test_weights_beside_a_large_one(emu, type, own, large, gap, n):
+    """Rows whose first token has nearly all the weight, and zero values: the others count as the header says, to a share of
+    themselves or of that one (times a value of the size 100 2^-7, independent in 700 tokens)."""
+    import torch
+    q, cache, table, starts, lengths = _make([700], [n], 4, 2, 64, 32, type, size=(-7, -7))
+    k, v = cache[0].float(), cache[1].float()
+    page = int(table[0, 0])
+    # its score: the queries' first value times its code, 2^-7 and 1/8; no other code there
+    k[..., 0] = 0.0
+    k[page, :, 0, 0] = min(448.0, gap * 32.0)
+    q[..., 0] = gap * 1024.0 / max(float(k[page, 0, 0, 0].to(ref.F8)), 1.0)
+    v[page, :, 0] = 0.0
+    made = (q, (k.to(ref.F8), v.to(ref.F8), *cache[2:]), table, starts, lengths)
+    want = ref.attention(q, *made[1], table, starts, lengths, 0.125)[0]
+    out = _attend(emu, made, scale=0.125, max_new=n)
+    size = 2.0 ** -7 * 100 * math.sqrt(840 * want.numel())
+    least = 2.0 ** -25 * math.sqrt(want.numel()) if type == "f16" else 0.0   # of FP16 outputs
+    assert float((out.double() - want).norm()) <= own * float(want.norm()) + large * size + least
+    assert _error(emu) == 0
