@@ -48,6 +48,19 @@ def test_zero_values_with_the_largest_scores(emu, type, n, zero_first):
     assert _error(emu) == 0
 
 
+@pytest.mark.parametrize("kept,new,Hq,Hk,D", [([20011], [1], 8, 2, 128), ([9000, 10], [3, 4], 4, 1, 64), ([3000, 700], [300, 129], 4, 2, 128),
+                                              ([40000, 300], [40, 50], 4, 1, 128), ([900], [700], 3, 3, 96), ([1500], [40], 16, 1, 256)])
+def test_both_pieces_of_fp32(emu, kept, new, Hq, Hk, D):
+    import torch
+    made = _make(kept, new, Hq, Hk, D, 32, "f32")
+    want = ref.attention(*made[:1], *made[1], *made[2:], D ** -0.5)[0]
+    for most in (max(new), 1):                       # (kernels for many rows, and for few)
+        out = _attend(emu, made, max_new=most)
+        for b in range(len(kept)):
+            rows = slice(made[3][b], made[3][b + 1])
+            assert norms.relative(out[rows], want[rows]) <= norms.TWO_PIECES
+
+
 # Sums of one sign, segments that one CTA goes through alone.  The products' accumulators round toward zero, half a step (2^-24) of
 # the sum on the average: what an FP32 sum may lose is bounded by its parts of 64 such additions (32 steps, 2^-25 each on the average as
 # it grows), 2e-6 with the rest; in 16 bits by half a step of the type's 11 bits.
@@ -124,3 +137,13 @@ def test_weights_beside_a_large_one(emu, type, own, large, gap, n):
     least = 2.0 ** -25 * math.sqrt(want.numel()) if type == "f16" else 0.0   # of FP16 outputs
     assert float((out.double() - want).norm()) <= own * float(want.norm()) + large * size + least
     assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
+def test_same_bits_of_all_types(emu, type):
+    import torch
+    made = _make([5000, 100, 3000, 0], [1, 4, 1, 300], 8, 2, 128, 16, type)
+    for most in (4, None):                           # (kernels for few rows, and for many)
+        first = _attend(emu, made, max_new=most)
+        for _ in range(10):
+            assert torch.equal(_attend(emu, made, max_new=most), first)
