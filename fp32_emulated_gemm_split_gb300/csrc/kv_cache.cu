@@ -425,9 +425,18 @@ emu_status_t emu_kv_tables(int64_t B, const int32_t* kept, const int32_t* fresh,
         return EMU_ERR_INVALID_VALUE;
     if (page < 16 || page > 256 || (page & (page - 1)) != 0 || pages > INT32_MAX / page || width > INT32_MAX / page)
         return EMU_ERR_INVALID_VALUE;
-    if (!starts || !taken_out || taken_out == taken || (n_free > 0 && !free_pages)) return EMU_ERR_INVALID_VALUE;
+    if (!starts || !taken_out || (n_free > 0 && !free_pages)) return EMU_ERR_INVALID_VALUE;
     if (B > 0 && (!kept || !fresh || !lengths || (width > 0 && !table))) return EMU_ERR_INVALID_VALUE;
     if (T > 0 && (!slots || !positions)) return EMU_ERR_INVALID_VALUE;
+    // Every block reads the inputs for itself, and none waits for another: what one writes no other may read.
+    const struct { const int32_t* at; int64_t n; } ranges[] = {{starts, B + 1}, {lengths, B}, {slots, T}, {positions, T},
+        {taken_out, 1}, {table, B * width}, {kept, B}, {fresh, B}, {free_pages, n_free}, {taken, taken ? 1 : 0}};
+    for (int i = 0; i < 6; ++i)                      // (the written ones are first)
+        for (int j = i + 1; j < 10; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(ranges[i].at), b = reinterpret_cast<uintptr_t>(ranges[j].at);
+            if (ranges[i].n && ranges[j].n && a < b + 4 * (uintptr_t)ranges[j].n && b < a + 4 * (uintptr_t)ranges[i].n)
+                return EMU_ERR_INVALID_VALUE;
+        }
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState* d = nullptr;
     const emu_status_t st = current_device(&d);

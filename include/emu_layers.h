@@ -217,7 +217,10 @@ typedef struct {
  *  lengths       B values: kept + fresh
  *  slots         T values: the slot of each row's token, -1 behind the last sequence
  *  positions     T values: its position, 0 behind the last sequence
- *  taken_out     *taken and the pages given (not the same address as taken)
+ *  taken_out     *taken and the pages given
+ *
+ * No output (nor the table) may overlap an input or another output: lengths over kept,
+ * taken_out over taken and the like are refused.
  *
  * B at most 2^20, T at most 2^25 - 1.  Each of these records EMU_ERR_INVALID_VALUE in
  * the device's error word: a negative length, or more tokens than width pages
