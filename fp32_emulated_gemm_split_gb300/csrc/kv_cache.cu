@@ -95,7 +95,13 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TableParam
                 if (b == 0) p.starts[0] = 0;
                 p.starts[b + 1] = end;
                 p.lengths[b] = kept[i] + (end - start);
-                if (a + fresh[i] > p.T) bad = true;
+                if (a + fresh[i] > p.T) {
+                    bad = true;
+                    // (the one that rows run out in: no page is given behind its last row)
+                    if (a <= p.T)
+                        *p.taken_out = (int)min(taken + g + (((int64_t)kept[i] + (p.T - a) + P - 1) >> p.page_log) -
+                                                    (((int64_t)kept[i] + P - 1) >> p.page_log), (int64_t)INT32_MAX);
+                }
             }
             a += fresh[i];
             g += gets[i];
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TableParam
         }
         rows += round_rows;
         given += round_pages;
-        if (r == rounds - 1 && mine && tid == 0) *p.taken_out = (int)min(taken + given, (int64_t)INT32_MAX);
+        if (r == rounds - 1 && mine && tid == 0 && rows <= p.T) *p.taken_out = (int)min(taken + given, (int64_t)INT32_MAX);
         __syncthreads();
     }
     if (p.B == 0 && blockIdx.x == 0 && tid == 0) {

@@ -225,7 +225,7 @@ typedef struct {
  * B at most 2^20, T at most 2^25 - 1.  Each of these records EMU_ERR_INVALID_VALUE in
  * the device's error word: a negative length, or more tokens than width pages
  * hold (that sequence gets no rows, and length 0); more rows than T (those that
- * do not fit are left out, of `lengths` too); free pages that run out or page
+ * do not fit are left out, of `lengths` and of the pages given too); free pages that run out or page
  * numbers outside 0..pages-1 (-1 in the table, slots -1).
  */
 emu_status_t emu_kv_tables(int64_t B, const int32_t* kept, const int32_t* fresh, int64_t pages, int64_t page,
