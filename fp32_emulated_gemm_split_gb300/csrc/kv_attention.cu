@@ -768,8 +768,8 @@ struct RowSum {
     }
 };
 
-// Adds the parts of the segments that CTAs share up in order, and the rows behind the last
-// sequence become zero.  Block (x, y): the segment that CTA x began; where it has few parts
+// Adds the parts of the segments that CTAs share up in order, and the rows before the first and
+// behind the last sequence become zero.  Block (x, y): the segment that CTA x began; where it has few parts
 // (most do: two or three), its rows kJoinWarps y on, a warp each; where it has many, its rows
 // y, y + gridDim.y and so on, the parts dealt to the warps.
 constexpr int kJoinWarps = 8;
@@ -780,12 +780,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = p.D, c0 = blockIdx.x;
     griddep_wait();
     {
-        const int used = p.B > 0 ? min(max(p.starts[p.B], 0), p.T) : 0, values = p.heads * p.group * D;
-        for (int row = used + blockIdx.x + blockIdx.y * gridDim.x; row < p.T; row += gridDim.x * gridDim.y)
+        const int first = p.B > 0 ? min(max(p.starts[0], 0), p.T) : 0;
+        const int used = p.B > 0 ? min(max(p.starts[p.B], first), p.T) - first : 0, values = p.heads * p.group * D;
+        for (int i = blockIdx.x + blockIdx.y * gridDim.x; i < p.T - used; i += gridDim.x * gridDim.y) {
+            const int row = i < first ? i : i + used;
             for (int e = tid; e < values; e += kJoinWarps * 32) {
                 const int h = e / D;
                 static_cast<T*>(p.out)[row * p.out_t + h * p.out_h + (e - h * D)] = kv_from<T>(0.0f);
             }
+        }
     }
     const Work& w = p.shared[c0];
     if (w.units == 0) return;

@@ -260,8 +260,8 @@ def emu_kv_attention(q, cache: KvCache, table, starts, lengths, scale=None, wind
     lengths[b] tokens, over the cache.  scale: D ** -0.5 by default; window: how
     many tokens a row sees at most, itself among them (0: all); max_new: rows
     of a sequence at most, which lets a step of single tokens launch one kernel
-    only.  A row that sees nothing is zero, as are the rows behind the last
-    sequence.  out may be q."""
+    only.  A row that sees nothing is zero, as are the rows before the first
+    and behind the last sequence.  out may be q."""
     if stream is not None:
         return _on(stream, emu_kv_attention, q, cache, table, starts, lengths, scale, window, max_new, out)
     if scale is None:

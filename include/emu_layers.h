@@ -264,7 +264,8 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  *                2^31 - 256.  `dtype`, any strides; out may be q.
  *  table, width  B rows of page numbers, as emu_kv_tables leaves them
  *  starts        B + 1 values, ascending: sequence b has the rows starts[b] ..
- *                starts[b+1] - 1 (none are fine); rows from starts[B] on become zero
+ *                starts[b+1] - 1 (none are fine); rows before starts[0] and from
+ *                starts[B] on become zero
  *  lengths       B values
  *  window        0, or 2^30 and more: all tokens before
  *  max_new       rows that a sequence has at most, or 0 where the caller does not

@@ -140,6 +140,20 @@ def test_weights_beside_a_large_one(emu, type, own, large, gap, n):
 
 
 @pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("n", [1, 100])
+def test_rows_before_the_first_sequence(emu, type, n):
+    """Rows that no sequence has are zero, before the first one as behind the last."""
+    import torch
+    q, cache, table, starts, lengths = _make([50, 9], [n, n], 4, 2, 64, 16, type, behind=7)
+    starts = [s + 4 for s in starts]
+    out = torch.full_like(q, 7.0)
+    _attend(emu, (q, cache, table, starts, lengths), max_new=n, out=out)
+    want, bound = ref.attention(q, *cache, table, starts, lengths, 0.125)
+    assert ref.within(out, want, bound) and not out[:4].any() and not out[2 * n + 4:].any()
+    assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
 def test_same_bits_of_all_types(emu, type):
     import torch
     made = _make([5000, 100, 3000, 0], [1, 4, 1, 300], 8, 2, 128, 16, type)
