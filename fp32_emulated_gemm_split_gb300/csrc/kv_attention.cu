@@ -591,7 +591,7 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
             // 2^(14 - E), top = m 2^E
             const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
             const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-            const float mine_factor = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (p.scale * kLog2e);
+            const float mine_factor = score_factor(top, E, p.scale);
 #pragma unroll
             for (int k = 0; k < NG * 4; ++k)
 #pragma unroll

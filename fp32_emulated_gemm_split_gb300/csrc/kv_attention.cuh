@@ -69,6 +69,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
 }
 
+// What a row's scores are multiplied with, before the keys' scale: `scale` and log2 e, and 2^(E - 14), the inverse of what its
+// queries were. NaN where a query is infinite (top): its scores are infinities or NaN, and no softmax of those is a number.
+__device__ __forceinline__ float score_factor(float top, int E, float scale) {
+    return top <= 3.402823466e38f ? __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (scale * kLog2e)
+                                  : __uint_as_float(0x7FC00000u);
+}
+
 // A bound of log2 of a page's value scale less 14 (its exponent and one, less 14), and no less than -120, so that
 // 2^(the other way) is finite, and so is the sum of 128 of them: what o is held against lies this far from the
 // scores' maximum.

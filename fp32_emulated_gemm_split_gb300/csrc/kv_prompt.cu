@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             const int E = max((int)(__float_as_uint(top) >> 23) - 127, -112);
                             const float up = copysignf(__uint_as_float((uint32_t)(14 - E + 127) << 23), p.scale);
                             if ((lane & 15) == 0)
-                                q_factor[PAIR ? half : 0][rr] = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * (fabsf(p.scale) * kLog2e);
+                                q_factor[PAIR ? half : 0][rr] = score_factor(top, E, fabsf(p.scale));
                             uint32_t hi[4], lo[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {

@@ -275,8 +275,11 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  * Scores and sums are FP32-accurate for FP32 rows, and each weight p times its
  * page's value scale is held to 2^-22 of itself, or to 2^-38 of the row's largest
  * where that is more; for 16-bit rows it is rounded to 11 bits, or to 2^-32 of the
- * row's largest.  Weights below 2^-126 of the row's largest may count as zero.  A row that sees no token is zero.  What a row does not see has no part in it, whatever it holds
- * (NaN among it).  A length that is negative or more than width pages hold, and a
+ * row's largest.  Weights below 2^-126 of the row's largest may count as zero.
+ *
+ * A row that sees no token is zero.  What a row does not see has no part in it,
+ * whatever it holds (NaN among it).  A row whose queries are not finite is NaN, if
+ * it sees a token.  A length that is negative or more than width pages hold, and a
  * page number outside the cache, give NaN in the rows that need them; `starts`
  * out of order leaves the outputs undefined (nothing else is written).  Each
  * records EMU_ERR_INVALID_VALUE.

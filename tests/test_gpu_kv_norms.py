@@ -140,6 +140,30 @@ def test_weights_beside_a_large_one(emu, type, own, large, gap, n):
 
 
 @pytest.mark.parametrize("type", TYPES)
+@pytest.mark.parametrize("n", [1, 40, 140])
+def test_infinite_queries_and_codes_of_one_sign(emu, type, n):
+    """All scores are the same infinity, of which no softmax is a number, and rows that see nothing are zero still."""
+    import torch
+    q, cache, table, starts, lengths = _make([100], [n], 4, 2, 64, 32, type)
+    for sign in (1.0, -1.0):
+        k = cache[0].float()
+        k[..., 5] = sign * k[..., 5].abs().clamp(min=1.0)
+        for value in (math.inf, -math.inf):
+            x = q.clone()
+            x[0, 1, 5] = value
+            made = (x, (k.to(ref.F8), *cache[1:]), table, starts, lengths)
+            out = _attend(emu, made, max_new=n)
+            others = torch.ones(x.shape[:2], dtype=torch.bool, device="cuda")
+            others[0, 1] = False
+            x = torch.where(others[..., None], x, 0.0)
+            want, bound = ref.attention(x, *made[1], table, starts, lengths, 0.125)
+            assert torch.isnan(out[0, 1]).all(), (sign, value)
+            assert ref.within(out[others], want[others], bound[others])
+            assert not _attend(emu, (*made[:4], [0]), max_new=n).any()
+    assert _error(emu) == 0
+
+
+@pytest.mark.parametrize("type", TYPES)
 @pytest.mark.parametrize("n", [1, 100])
 def test_rows_before_the_first_sequence(emu, type, n):
     """Rows that no sequence has are zero, before the first one as behind the last."""
