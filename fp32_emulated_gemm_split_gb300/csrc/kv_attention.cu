@@ -957,7 +957,8 @@ extern "C" emu_status_t emu_kv_attention(int dtype, int64_t T, const emu_heads_t
                                          int64_t max_new, emu_stream_t stream_) {
     constexpr int64_t most = int64_t(1) << 40;
     if (dtype < EMU_F32 || dtype > EMU_F16 || !q || !out || !cache || !kv_cache_ok(*cache)) return EMU_ERR_INVALID_VALUE;
-    if (T < 0 || T > kKvMaxRows || B < 0 || B > 1 << 20 || width < 0 || width > INT32_MAX / cache->page || window < 0 ||
+    // (a tile's end, 128 tokens on, and what rounds up to one stay below 2^31)
+    if (T < 0 || T > kKvMaxRows || B < 0 || B > 1 << 20 || width < 0 || width > (INT32_MAX - 255) / cache->page || window < 0 ||
         max_new < 0 || !(scale - scale == 0.0f))
         return EMU_ERR_INVALID_VALUE;
     if (q->heads < 1 || q->heads > 65536 || q->heads % cache->heads != 0 || out->heads != q->heads)

@@ -262,7 +262,7 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  *  q, out        T rows of the same number of heads, a multiple of cache->heads: head h
  *                reads key head h / (heads / cache->heads); T times that quotient below
  *                2^31 - 256.  `dtype`, any strides; out may be q.
- *  table, width  B rows of page numbers, as emu_kv_tables leaves them
+ *  table, width  B rows of page numbers, as emu_kv_tables leaves them; width * page at most 2^31 - 256
  *  starts        B + 1 values, ascending: sequence b has the rows starts[b] ..
  *                starts[b+1] - 1 (none are fine); rows before starts[0] and from
  *                starts[B] on become zero
