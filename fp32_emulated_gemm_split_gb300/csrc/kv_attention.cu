@@ -50,7 +50,7 @@ constexpr int kFewKvRows = 64;
 
 // Steps that a warp adds up in an MMA's sums, 16-bit rows: each MMA rounds toward zero, some 2^-24 of the sum lost as it grows.
 // Behind so many the sum goes to one in memory, to the nearest.  (FP32 rows add each step's sums to the nearest.)
-constexpr int kChain = 256;
+constexpr int kChain = 256;                          // (whole batches)
 constexpr int kMovedQuads = 33;                      // of a lane: o of 16 rows of 256, and its rows' references
 
 // Steps start on multiples of ST tokens; the first one that any row of the sequence sees.
@@ -217,7 +217,6 @@ struct Segment {
         for (int r = 0; r < NR; ++r) {
             float m0[2], f[SUB][2], fs[SUB][2], back[2] = {1.0f, 1.0f};
             uint32_t hidden = 0;
-            bool far = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float m[SUB];
@@ -264,15 +263,13 @@ struct Segment {
                 ref[r][e] = ref_now;
                 m0[e] = top_now == -INFINITY ? 0.0f : top_now;
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
+                for (int u = 0; u < SUB; ++u)
                     f[u][e] = top_now == -INFINITY ? 0.0f : v_scale[u] * exp2_of(top_now - ref_now);
-                    far = far || f[u][e] > kFarScale;
-                }
             }
-            if (__any_sync(0xffffffffu, far)) {
+            if (v_scale[0] > kFarValue || v_scale[SUB - 1] > kFarValue) {        // (the same for all lanes)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (top[r][e] > ref[r][e]) {
+                    if (fmaxf(f[0][e], f[SUB - 1][e]) > kFarScale && top[r][e] > ref[r][e]) {
                         m0[e] = ref[r][e];
                         back[e] = exp2_of(ref[r][e] - top[r][e]);
 #pragma unroll
@@ -435,6 +432,7 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
     constexpr int ROWS = 8 * NR, SUB = ST / 16;      // rows of a segment; tiles of 16 tokens in a step
     constexpr int UNIT = ST * kWarps;
     constexpr int BATCH = 32 / SUB;                  // steps whose pages the lanes hold, one tile each
+    static_assert(kChain % BATCH == 0, "sums are moved where a batch begins");
     using Bl = Blocks<NG>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps][4];
@@ -633,8 +631,8 @@ kv_decode_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ C
         float4* const sums = p.moved + (size_t)(blockIdx.x * kWarps + warp) * (kMovedQuads * 32) + lane;
         for (int i = 0; i < steps; ++i) {
             const int in_batch = i % BATCH;
-            if (!TWO && i % kChain == 0 && i > 0) sg.move_sums(sums, i == kChain, false);
             if (in_batch == 0 && i > 0) {
+                if (!TWO && i % kChain == 0) sg.move_sums(sums, i == kChain, false);
                 page_now = page_next;
                 ks_now = ks_next;
                 vs_now = vs_next;

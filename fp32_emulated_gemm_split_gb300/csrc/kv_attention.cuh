@@ -86,7 +86,7 @@ __device__ __forceinline__ int scale_bound(float v_scale) {
 // A weight p s_v against o's reference is x f, x = 2^(score - m), f = s_v 2^(m - ref).  It is 2^14 at most, but where the
 // row's largest scores are those of pages of a tiny scale (of zeros: 2^-126), m lies up to 120 over ref, and the f of
 // another page is infinite.  From here on x is 2^(score - ref), f s_v, and sums of x count 2^(ref - m) of themselves.
-constexpr float kFarScale = 1e37f;
+constexpr float kFarScale = 1e37f, kFarValue = 7.0f;     // no f over the first with an s_v up to the second
 
 // A CTA's way through the units, and the segment that it is at (in shared memory: both are
 // looked at between segments only).
