@@ -43,9 +43,13 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKvCtasPerSm = 4;                      // at most
-// Rows of a sequence (16-bit types, heads up to 128) up to which this file's kernel runs, in segments of 16 that
-// each read the cache, all but the first from L2: 24 sequences of 3 to 7 tokens, 8 heads of 128 a key head, 75 us,
-// in kv_prompt.cu 106, and in segments of 32 (queries in shared memory, steps of 16 tokens for their registers) 102.
+// Rows of a sequence (16-bit types, heads up to 128; FP32: 16) up to which this file's kernel runs, in segments of 16 that
+// each read the cache, all but the first from L2.  24 sequences of 3 to 7 tokens, 8 heads of 128 a key head: 75 us, in
+// kv_prompt.cu 106, and in segments of 32 (queries in shared memory, steps of 16 tokens for their registers) 102.  Both
+// kernels where all sequences have so many rows (us, this one's and kv_prompt.cu's): 24 sequences of 300 to 7000 tokens, 4 key
+// heads of 128: 16 rows 38 / 82, 32 rows 62 / 82, 48 rows 91 / 85, 64 rows 119 / 89; 8 of 64: 51 / 108, 93 / 110, 142 / 116,
+// 180 / 120; two of 60,000, 8 of 128: 62 / 158, 103 / 161, 147 / 163, 186 / 165.  FP32: 46 / 95, 79 / 97, 113 / 98, 151 / 98.
+// They meet at 40 to 48 rows in either type where all sequences have as many; drafts of different lengths have fewer.
 constexpr int kFewKvRows = 64;
 
 // Steps that a warp adds up in an MMA's sums, 16-bit rows: each MMA rounds toward zero, some 2^-24 of the sum lost as it grows.

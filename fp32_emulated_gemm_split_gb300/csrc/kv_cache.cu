@@ -493,7 +493,10 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
     p.slots_all = cache->pages * cache->page;
     p.err = d->err;
     p.per_row_inverse = (uint32_t)(((uint64_t(1) << 32) + p.D / 8 - 1) / (p.D / 8));
-    // a warp for each of a few tokens; else a block for each window, up to 32 tokens, of which there are eight or more an SM
+    // A warp for each of a few tokens; else a block for each window, up to 32 tokens, of which there are eight or more an SM.
+    // Blocks are for runs that a warp alone takes long over: 8 heads of 128 in BF16, runs of 100 tokens, 200 rows 4.5 us (a warp
+    // a run 12.3), 4000 rows 9.3 (26.5).  Single tokens are better off with a warp each beyond 32 too: 32 rows 2.9 (2.5), 96
+    // rows 5.7 (2.7), 256 rows 8.3 (3.5), 4096 rows 48 (27); runs of 4: 96 rows 4.3 (2.8), 4096 rows 16.0 (16.9).
     const bool block = T > 32;
     p.window = 1;
     while (block && p.window < 32 && (T + 2 * p.window - 1) / (2 * p.window) * cache->heads * 2 >= (int64_t)d->sms * 8) p.window *= 2;

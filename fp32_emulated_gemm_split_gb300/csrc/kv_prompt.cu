@@ -18,7 +18,7 @@
 // way while the outputs of the last are written.
 //
 // Measured: three prompts of 2000 tokens behind 1500 to 4500 kept, 32 heads over 8 of
-// 128, BF16 (412 GFLOP), 592 us, 696 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
+// 128, BF16 (412 GFLOP), 600 us, 687 TFLOP/s.  A unit of 256 rows takes about 5000 cycles, its
 // MMAs 2560 (scores of 64 tokens are bound by reading Q again: 512 of them), a group's weights
 // 2500; codes, MMAs and weights wait for one another.  A segment costs 17,000 cycles
 // besides: Q, units that some row does not see, outputs.  Barriers that let the groups compute by
@@ -176,7 +176,9 @@ struct Plan {
     static constexpr int tiles = (q_tiles + k_stages + v_stages) * NG * kPanel;
     static constexpr int slots = (216 * 1024 - tiles) / piece < 10 ? (216 * 1024 - tiles) / piece : 10;
     static constexpr int bytes = tiles + slots * piece;
-    static constexpr int setup = PAIR ? 4 : 3;                   // (17,000 to 20,000 cycles, a unit 5000 to 6000)
+    // (17,000 to 20,000 cycles, a unit 5000 to 6000.  Prompts in BF16 and window in FP32: 596 and 115 us; with one unit 625 and
+    // 138, with 8 and 6 units 586 and 120.)
+    static constexpr int setup = PAIR ? 4 : 3;
 };
 
 __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -982,8 +984,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_con
                             m = top;
                         }
                         // o's reference: p s_v is 2^13 to 2^14 at its largest (scale_bound is 14 below), so that its two pieces end at
-                        // 2^-38 of it.  16-bit rows: 2^7 to 2^8 at first, and the reference moves where it would pass 2^14; O is
-                        // rescaled less often (three prompts of 2000: 594 us; 617 with 2^9 at first, 604 with 2^3).
+                        // 2^-38 of it.  16-bit rows: 2^7 to 2^8 at first, and the reference moves where it would pass 2^14, so
+                        // O is rescaled less often (three prompts of 2000: 595 to 611 us over five sets of values, 595 to 606
+                        // with 2^3 at first, 617 with 2^9).
                         const bool move = over > ref;
                         if (__any_sync(0xffffffffu, move)) {
                             const float now = move ? over + (TWO ? 0.0f : 6.0f) : ref;

@@ -259,8 +259,10 @@ def emu_kv_attention(q, cache: KvCache, table, starts, lengths, scale=None, wind
     strides), sequence b's from starts[b] to starts[b + 1], the last of its
     lengths[b] tokens, over the cache.  scale: D ** -0.5 by default; window: how
     many tokens a row sees at most, itself among them (0: all); max_new: rows
-    of a sequence at most, which lets a step of single tokens launch one kernel
-    only.  A row that sees nothing is zero, as are the rows before the first
+    of a sequence at most, None where the caller does not know. It chooses kernels,
+    not what is computed (always two launches): without it a batch of next tokens
+    goes through those for prompts (96 sequences of 600,000 tokens: 630 us for 196).
+    A row that sees nothing is zero, as are the rows before the first
     and behind the last sequence.  out may be q."""
     if stream is not None:
         return _on(stream, emu_kv_attention, q, cache, table, starts, lengths, scale, window, max_new, out)

@@ -270,7 +270,8 @@ emu_status_t emu_kv_store(int dtype, int64_t T, const emu_heads_t* k, const emu_
  *  window        0, or 2^30 and more: all tokens before
  *  max_new       rows that a sequence has at most, or 0 where the caller does not
  *                know.  It chooses kernels (whose sums are rounded differently), not
- *                what is computed: too small a value is slow, not wrong.
+ *                what is computed: too small a value is slow, not wrong, and so is 0 for
+ *                a batch of next tokens, which then takes the prompts' kernels.
  *
  * Scores and sums are FP32-accurate for FP32 rows, and each weight p times its
  * page's value scale is held to 2^-22 of itself, or to 2^-38 of the row's largest
